@@ -148,7 +148,8 @@ def _blocks(x, rows):
     R, K = x.shape[-2:]
     rb, kb = -(-R // rows), -(-K // 128)
     p = torch.nn.functional.pad(x, (0, kb * 128 - K, 0, rb * rows - R)).unflatten(-1, (kb, 128)).unflatten(-3, (rb, rows))
-    s = (p.abs().amax(dim=(-3, -1)) / 448.0).clamp(min=TINY)
+    s = p.abs().amax(dim=(-3, -1))
+    s = (s / torch.full_like(s, 448.0)).clamp(min=TINY)  # by a tensor: by a number torch multiplies with its reciprocal
     q = (p * (1.0 / s).unsqueeze(-2).unsqueeze(-1)).flatten(-2).flatten(-3, -2)[..., :R, :K].to(E4M3)
     return q.contiguous(), s.contiguous()
 
