@@ -323,6 +323,25 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
                                  const uint8_t *decoded_dev, int32_t n_pos, int32_t iteration, int32_t path,
                                  void *y_dev, epoch_stream stream, epoch_iter_stats *stats_dev);
 
+/* The whole layer for a few tokens, outside any block: for each of the n_tok
+ * rows of x_dev [n_tok][H]
+ *   y = sum over the k selected experts w_e E_e(x) + shared experts (+ x if residual)
+ * with the layer's router rule over every expert (no support, no row cache), as
+ * epoch_moe_iter computes it when every position is fresh and every expert
+ * eligible; expert outputs are kept in fp32 up to y. One launch that reads each
+ * selected expert's weights once. A block's plan, cache, stamps and statistics
+ * are neither used nor changed, so it may run inside a block. y_dev must not
+ * overlap x_dev. Like every call on a layer it uses the layer's workspace:
+ * calls on one layer (graph replays among them) must not overlap on the GPU.
+ * Its CTAs wait for one another (a cooperative launch; bounded waits, see
+ * epoch_set_wait_timeout): EPOCH_ECUDA where the device cannot hold one CTA per
+ * SM at once. Zero tokens enqueue nothing.
+ * EPOCH_EINVAL if n_tok is not in [0, min(EPOCH_FEW_MAX, max_positions)], x_dev or
+ * y_dev is NULL/misaligned, or n_tok rows of x, or of the activations (top_k *
+ * inter + n_shared * shared_inter columns each), exceed 2^31 elements. */
+#define EPOCH_FEW_MAX 64
+epoch_status epoch_moe_few(epoch_layer *layer, const void *x_dev, int32_t n_tok, void *y_dev, epoch_stream stream);
+
 /* Ends the block: the plan, cache and stamps become invalid; the next
  * epoch_moe_iter without a new plan runs as a fallback. Host-only, no sync. */
 epoch_status epoch_block_end(epoch_layer *layer);
@@ -331,7 +350,7 @@ epoch_status epoch_block_end(epoch_layer *layer);
  * EPOCH_OK when clear, EPOCH_ETIMEOUT if the timeout bit is set, else EPOCH_EDEVICE. */
 epoch_status epoch_get_status(epoch_layer *layer, epoch_stream stream, uint32_t *word_out);
 
-/* Clears the device error word and resets the gate's grid-barrier counter
+/* Clears the device error word and resets the grid-barrier counters
  * (enqueued on the stream). After a timeout, clear the status before the next
  * call: a call that timed out may leave the barrier part-way. */
 epoch_status epoch_clear_status(epoch_layer *layer, epoch_stream stream);
@@ -400,6 +419,98 @@ epoch_status epoch_plan_support_noalloc(const float *logits_dev, int32_t n_pos, 
                                         double tau, int32_t router, const float *bias_dev, int32_t n_group,
                                         int32_t topk_group, int32_t *support_ids_dev, int32_t *support_len_dev,
                                         epoch_stream stream);
+
+/* ------------------------------------------------------------------ operators beside the layer
+ * What a model runs around an MoE layer and its FP8 form. They need no
+ * epoch_layer, keep nothing between calls, allocate nothing and use no
+ * workspace, so calls on any streams may overlap and be captured into graphs.
+ * Strides are in elements between consecutive rows; rows themselves are
+ * contiguous. Zero rows is a valid call that enqueues nothing. Outputs may
+ * alias inputs only where a function says so. */
+
+/* RMS norm before a block: h = x / sqrt(mean(x^2) + eps) * weight.
+ *  x_dev [n_rows][hidden] of x_dtype (the residual stream), out_dev of
+ *  out_dtype, weight_dev [hidden] of par_dtype; out_dev may be x_dev (same
+ *  dtype and stride). The result is rounded once.
+ * EPOCH_EINVAL: n_rows < 0, hidden not in [1, 2^20], unknown dtype, a NULL
+ * pointer or one not aligned to its element, a stride smaller than hidden (more
+ * than one row), eps negative or not finite. */
+epoch_status epoch_norm_before(const void *x_dev, int64_t x_stride, int32_t x_dtype, const void *weight_dev,
+                               int32_t par_dtype, int32_t n_rows, int32_t hidden, float eps, void *out_dev,
+                               int64_t out_stride, int32_t out_dtype, epoch_stream stream);
+
+/* Norm after a block fused with the block's gate, the residual scale and the
+ * next block's norm:
+ *   z  = block / sqrt(mean(block^2) + eps) * weight   (weight_dev NULL: z = block)
+ *   r' = s * residual + g * z                          -> out_dev, residual_dtype
+ *   h' = r' / sqrt(mean(r'^2) + eps) * next_weight     -> next_out_dev, dtype (next_weight_dev
+ *        NULL: not computed), from r' before its rounding
+ *  block_dev [n_rows][hidden] of dtype; residual_dev, out_dev of
+ *  residual_dtype; per-channel parameters (weight, next_weight, scale, a
+ *  channel gate) of par_dtype.
+ *  s: scale_dev [hidden], or residual_scale where scale_dev is NULL.
+ *  g: gate_kind EPOCH_GATE_NONE 1; EPOCH_GATE_CHANNEL gate_dev [hidden];
+ *  EPOCH_GATE_FULL gate_dev [n_rows][hidden] of dtype; through the logistic
+ *  function first where gate_sigmoid is nonzero.
+ *  out_dev may be residual_dev, next_out_dev may be block_dev (same strides).
+ * EPOCH_EINVAL as epoch_norm_before, for a gate_kind without its gate, and for
+ * exactly one of next_weight_dev and next_out_dev. */
+enum { EPOCH_GATE_NONE = 0, EPOCH_GATE_CHANNEL = 1, EPOCH_GATE_FULL = 2 };
+epoch_status epoch_norm_after(const void *block_dev, int64_t block_stride, int32_t dtype, const void *residual_dev,
+                              int64_t residual_stride, int32_t residual_dtype, const void *weight_dev,
+                              const void *gate_dev, int64_t gate_stride, int32_t gate_kind, int32_t gate_sigmoid,
+                              const void *scale_dev, float residual_scale, const void *next_weight_dev,
+                              int32_t par_dtype, int32_t n_rows, int32_t hidden, float eps, void *out_dev,
+                              int64_t out_stride, void *next_out_dev, int64_t next_stride, epoch_stream stream);
+
+/* Quantisation to e4m3 (8-bit floating point, 4 exponent and 3 mantissa bits)
+ * with one fp32 scale for each 128 consecutive columns of a row:
+ *   s = max(max|v| / 448, 2^-126),  q = e4m3(v * (1 / s))   (round to nearest even)
+ *  v = row i of x_dev ([n_src][cols], dtype), or row rows_dev[i] where rows_dev
+ *  is given (the positions of an expert-sorted worklist); with swiglu nonzero x
+ *  is [n_src][2 cols] and v = silu(x[:, :cols]) * x[:, cols:], in fp32.
+ *  q_dev [n_rows][cols] bytes, scales_dev [n_rows][ceil(cols / 128)], both
+ *  contiguous. A block holding a NaN or an infinity gets a scale that is not
+ *  finite, and so does (NaN) a row whose index is not in [0, n_src), which is
+ *  not read; products with either are NaN.
+ * EPOCH_EINVAL: n_rows or n_src < 0, cols < 1 or > 2^30, rows_dev NULL with n_src !=
+ * n_rows, unknown dtype, a NULL or misaligned pointer, x_stride smaller than a
+ * row, more than 2^31 blocks. */
+epoch_status epoch_fp8_quantize(const void *x_dev, int64_t x_stride, int32_t dtype, const int32_t *rows_dev,
+                                int32_t n_rows, int32_t n_src, int32_t cols, int32_t swiglu, void *q_dev,
+                                float *scales_dev, epoch_stream stream);
+
+/* The same for weight matrices w_dev [n_mats][n][k] (contiguous), with one
+ * scale for each block of 128 rows x 128 columns: q_dev [n_mats][n][k] bytes,
+ * scales_dev [n_mats][ceil(n / 128)][ceil(k / 128)]. n_mats in [0, 65535], n
+ * in [1, 2^22], k in [1, 2^22]. */
+epoch_status epoch_fp8_quantize_weight(const void *w_dev, int32_t dtype, int32_t n_mats, int32_t n, int32_t k,
+                                       void *q_dev, float *scales_dev, epoch_stream stream);
+
+/* Product of e4m3 operands scaled by blocks of 128 (as the two functions above
+ * produce them), accumulated in fp32 and rounded once:
+ *   y[i][j] = sum_b a_scales[i][b] * b_scales[e][j / 128][b] * sum_{k in block b} a[i][k] * b[e][j][k]
+ *  a_dev [m][k] bytes, a_scales_dev [m][ceil(k / 128)]; b_dev [n_groups][n][k],
+ *  b_scales_dev [n_groups][ceil(n / 128)][ceil(k / 128)]; y_dev [m][n] of
+ *  out_dtype (EPOCH_BF16 or EPOCH_F32), rows y_stride apart.
+ *  offsets_dev NULL: dense, n_groups must be 1. Else [n_groups + 1] int32 on the
+ *  device (the offsets of an expert-sorted worklist): rows offsets[e] ..
+ *  offsets[e + 1] - 1 are multiplied by matrix e; rows before offsets[0] or from
+ *  offsets[n_groups] on are not written. Offsets that descend or leave [0, m]
+ *  are read as the nearest ascending values in range.
+ * EPOCH_EINVAL: m < 0, n < 1, k not a positive multiple of 16, n_groups not in
+ * [1, 1024], n_groups * n or n_groups * k beyond int32, unknown out_dtype, a_dev
+ * or b_dev not 16-byte aligned, another pointer NULL or misaligned, y_stride < n.
+ * A bounded device wait that gives up sets the operators' error word. */
+epoch_status epoch_fp8_matmul(const void *a_dev, const float *a_scales_dev, const void *b_dev,
+                              const float *b_scales_dev, const int32_t *offsets_dev, int32_t n_groups, int32_t m,
+                              int32_t n, int32_t k, void *y_dev, int64_t y_stride, int32_t out_dtype,
+                              epoch_stream stream);
+
+/* Sticky error word of the operators beside the layer, one per device, for all
+ * streams: read (synchronises the stream) with the status that epoch_get_status
+ * gives, and cleared when clear is nonzero. Not for stream capture. */
+epoch_status epoch_ops_status(int32_t clear, epoch_stream stream, uint32_t *word_out);
 
 /* Releases host state only (the caller frees the workspace and weights). NULL is ignored. */
 void epoch_layer_destroy(epoch_layer *layer);

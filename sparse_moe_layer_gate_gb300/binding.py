@@ -18,6 +18,8 @@ EPOCH_F32, EPOCH_BF16 = 0, 1
 EPOCH_REFRESH_NEVER = 2**31 - 1
 EPOCH_DEVERR_FLAGS, EPOCH_DEVERR_TIMEOUT, EPOCH_DEVERR_BOUNDS = 1, 2, 4
 EPOCH_PROF_KINDS = 12
+EPOCH_FEW_MAX = 64
+EPOCH_GATE_NONE, EPOCH_GATE_CHANNEL, EPOCH_GATE_FULL = range(3)
 
 
 class epoch_layer_config(C.Structure):
@@ -77,6 +79,7 @@ _SIGS = {
                                  C.c_void_p, C.c_void_p, C.c_void_p]),
     "epoch_moe_iter_path": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
                                       C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "epoch_moe_few": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
     "epoch_block_end": (C.c_int, [C.c_void_p]),
     "epoch_get_status": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint32)]),
     "epoch_clear_status": (C.c_int, [C.c_void_p, C.c_void_p]),
@@ -95,6 +98,19 @@ _SIGS = {
     "epoch_plan_support_noalloc": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_double,
                                              C.c_int32, C.c_void_p, C.c_int32, C.c_int32,
                                              C.c_void_p, C.c_void_p, C.c_void_p]),
+    "epoch_norm_before": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
+                                    C.c_float, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
+    "epoch_norm_after": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
+                                   C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_float, C.c_void_p,
+                                   C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_int64, C.c_void_p]),
+    "epoch_fp8_quantize": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
+                                     C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "epoch_fp8_quantize_weight": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                                            C.c_void_p, C.c_void_p]),
+    "epoch_fp8_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                   C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
+    "epoch_ops_status": (C.c_int, [C.c_int32, C.c_void_p, C.POINTER(C.c_uint32)]),
     "epoch_layer_destroy": (None, [C.c_void_p]),
     "epoch_status_str": (C.c_char_p, [C.c_int]),
 }

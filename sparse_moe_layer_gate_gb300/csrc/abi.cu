@@ -150,6 +150,12 @@ size_t carve(const epoch_layer_config &c, char *base, Work *w) {
   t.ctrl = static_cast<Ctrl *>(take(sizeof(Ctrl)));
   t.stats = static_cast<epoch_iter_stats *>(take(sizeof(epoch_iter_stats)));
   t.err = static_cast<uint32_t *>(take(16));
+  const size_t F = N < kFewTokens ? N : kFewTokens;
+  t.few.logits = static_cast<float *>(take(F * E * 4));
+  t.few.act = take(F * (k * I + nsh * Is) * act);
+  t.few.out = static_cast<float *>(take(F * (k + nsh) * H * 4));
+  t.few.ctr_bytes = (2 + (H + 15) / 16) * sizeof(int32_t);
+  t.few.ctr = static_cast<int32_t *>(take(t.few.ctr_bytes));
   if (w) *w = t;
   return (off + kAlign - 1) & ~(kAlign - 1);
 }
@@ -426,6 +432,18 @@ epoch_status epoch_moe_iter(epoch_layer *L, const void *x, const uint8_t *live, 
   return epoch_moe_iter_path(L, x, live, decoded, n_pos, iteration, 0, y, stream, stats_dev);
 }
 
+epoch_status epoch_moe_few(epoch_layer *L, const void *x, int32_t n_tok, void *y, epoch_stream stream) {
+  if (L == nullptr || n_tok < 0 || n_tok > kFewTokens || n_tok > L->cfg.max_positions) return EPOCH_EINVAL;
+  if (n_tok == 0) return EPOCH_OK;
+  if (!aligned16(x) || !aligned16(y)) return EPOCH_EINVAL;
+  // rows are addressed by 32-bit element offsets
+  const int64_t acts = static_cast<int64_t>(L->dims.k) * L->dims.I + static_cast<int64_t>(L->dims.n_sh) * L->dims.I_s;
+  if (n_tok * acts > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;
+  cudaStream_t s = S(stream);
+  return run(L, K_FEW, s,
+             [&] { return launch_moe_few(L->dims, L->w, L->ws.few, x, y, n_tok, L->bf16, L->ws.err, s); });
+}
+
 epoch_status epoch_block_end(epoch_layer *L) {
   if (L == nullptr) return EPOCH_EINVAL;
   L->planned = false;
@@ -445,9 +463,10 @@ epoch_status epoch_get_status(epoch_layer *L, epoch_stream stream, uint32_t *wor
 
 epoch_status epoch_clear_status(epoch_layer *L, epoch_stream stream) {
   if (L == nullptr) return EPOCH_EINVAL;
-  // the gate's grid barrier too: a call that timed out may leave it part-way
+  // the grid barriers too: a call that timed out may leave them part-way
   return cudaMemsetAsync(L->ws.err, 0, sizeof(uint32_t), S(stream)) == cudaSuccess &&
-                 cudaMemsetAsync(L->ws.gate_arrive, 0, 2 * sizeof(int32_t), S(stream)) == cudaSuccess
+                 cudaMemsetAsync(L->ws.gate_arrive, 0, 2 * sizeof(int32_t), S(stream)) == cudaSuccess &&
+                 cudaMemsetAsync(L->ws.few.ctr, 0, L->ws.few.ctr_bytes, S(stream)) == cudaSuccess
              ? EPOCH_OK
              : EPOCH_ECUDA;
 }

@@ -1,0 +1,671 @@
+// The whole MoE layer for a few tokens in one launch: router, top-k, routed and
+// shared SwiGLU experts, weighted sum (epoch_moe_few).
+//
+//   G = x W_r^T (+ b);  S_t, w_t = the layer's router rule over every expert
+//   y_t = sum_{e in S_t} w_te W_down,e (silu(W_gate,e x_t) * (W_up,e x_t)) + sum_shared (+ x_t)
+//
+// With at most 64 tokens the bytes of the selected experts' weights bound the
+// time, so the kernel is built around reading each of them once, from global
+// memory straight into registers, with loads always in flight. One CTA per SM
+// stays for the whole call; three phases are separated by two grid barriers:
+//
+//   0. router logits, and the shared experts' activations, which need no routing;
+//      -- barrier --  every CTA takes every token's top-k for itself (cheaper
+//      than a third barrier) and sorts the edges by expert in shared memory;
+//   1. activations a = silu(gate) * up of every (token, expert) edge;
+//      -- barrier --  (the first down weights are already in flight)
+//   2. down products, fp32 per edge; the last group of warps to finish a 16-row
+//      tile of H adds its edges up in selection order and writes y.
+//
+// A group of warps works on 16 weight rows and splits K. Thread (g, t) of a warp
+// (g = lane / 4, t = lane % 4) loads 16 consecutive bytes of row g and of row g + 8
+// (64 bytes of a row by four threads): the order of the products along K is
+// free, so these are operand fragments of two m16n8k16 products as they come, and
+// the same bytes of eight tokens' rows are the other operand. In phase 1 rows
+// 0-7 are gate rows and rows 8-15 the up rows of the same eight columns, so one
+// tile of sums holds both halves of the SwiGLU.
+//
+// fp32 layers run the same schedule with FFMA in place of the tensor core.
+#include <atomic>
+#include <climits>
+#include <cstring>
+
+#include "common.cuh"
+#include "layer.h"
+#include "topk.cuh"
+
+namespace epoch {
+
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSplit = 4;    // warps of a group in phases 1 and 2
+constexpr int kSteps = 4;    // K steps (64 bytes of a row) loaded together
+constexpr int kMaxEdges = kFewTokens * 16;
+
+// ------------------------------------------------------------------ element types
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr int step = 32, per = 8;  // columns of a K step, and of a thread in it
+  static constexpr int acc = 4;             // fp32 sums a thread keeps of a 16 x 8 tile while adding along K
+};
+template <> struct Elem<float> {
+  static constexpr int step = 16, per = 4;
+  static constexpr int acc = 16;  // rows g and g + 8 of all eight tokens (this thread's columns only)
+};
+
+__device__ __forceinline__ uint4 load_weights(const void *p, bool ok) {
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+  if (ok)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p));
+  return u;
+}
+// Token rows: x through L1 (no one writes it during the call), activations,
+// which other SMs wrote in this launch, from L2.
+template <bool FRESH> __device__ __forceinline__ uint4 load_tokens(const void *p) {
+  if constexpr (FRESH) return __ldcg(static_cast<const uint4 *>(p));
+  else return __ldg(static_cast<const uint4 *>(p));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Barrier of the `warps` warps of group `id` (hardware barrier id + 1).
+__device__ __forceinline__ void group_sync(int id, int warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
+}
+
+// Grid barrier: every CTA arrives once on *ctr (zero before the launch's first
+// arrival) and waits until all have. False when the bounded wait gives up.
+__device__ bool grid_barrier(int32_t *ctr, uint32_t *err, int64_t timeout_ns) {
+  __shared__ int s_ok;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(ctr, 1);
+    const int32_t want = static_cast<int32_t>(gridDim.x);
+    const volatile int32_t *seen = ctr;
+    s_ok = 1;
+    if (*seen < want) {
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t i = 1; *seen < want; ++i)
+        if ((i & 63u) == 0u && globaltimer_ns() - t0 > static_cast<uint64_t>(timeout_ns)) {
+          set_error(err, EPOCH_DEVERR_TIMEOUT);
+          s_ok = 0;
+          break;
+        }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  return s_ok != 0;
+}
+
+// Sixteen weight rows of one unit, as this thread sees them: its columns of rows
+// g and g + 8 (row index in bounds or not), and its warp's K steps.
+struct WeightRows {
+  const char *p0, *p1;
+  bool ok0, ok1;
+  int step, end, k;  // K steps of this warp, columns of a row
+};
+
+template <typename T>
+__device__ __forceinline__ void load_chunk(const WeightRows &w, int step, uint4 (&a)[kSteps], uint4 (&b)[kSteps]) {
+  const int t = lane_id() & 3;
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const int64_t c = static_cast<int64_t>(step + j) * Elem<T>::step;
+    const bool in = step + j < w.end && c + t * Elem<T>::per < w.k;
+    a[j] = load_weights(w.p0 + c * sizeof(T), in && w.ok0);
+    b[j] = load_weights(w.p1 + c * sizeof(T), in && w.ok1);
+  }
+}
+
+// Adds the products of a loaded chunk with tokens' rows to the sums: rows[i] is
+// where the row of this thread's token of tile i starts in x, negative behind the
+// last token.
+template <typename T, int NT, bool FRESH>
+__device__ __forceinline__ void add_chunk(const WeightRows &w, int step, const uint4 (&a)[kSteps],
+                                          const uint4 (&b)[kSteps], const T *x, const int (&rows)[NT], int tiles,
+                                          float (&acc)[NT][Elem<T>::acc]) {
+  const int lane = lane_id(), t = lane & 3;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= tiles) break;
+      uint4 v[kSteps];
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const int c = (step + j) * Elem<T>::step + t * Elem<T>::per;
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (rows[i] >= 0 && step + j < w.end && c < w.k) v[j] = load_tokens<FRESH>(x + rows[i] + c);
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        mma_bf16(acc[i], a[j].x, b[j].x, a[j].y, b[j].y, v[j].x, v[j].y);
+        mma_bf16(acc[i], a[j].z, b[j].z, a[j].w, b[j].w, v[j].z, v[j].w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= tiles) break;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int row = __shfl_sync(0xffffffffu, rows[i], 4 * n);  // token n of the tile
+        if (row < 0) break;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const int c = (step + j) * Elem<T>::step + t * Elem<T>::per;
+          if (step + j >= w.end || c >= w.k) continue;
+          const uint4 u = load_tokens<FRESH>(x + row + c);
+          const float v0 = __uint_as_float(u.x), v1 = __uint_as_float(u.y), v2 = __uint_as_float(u.z),
+                      v3 = __uint_as_float(u.w);
+          float s = acc[i][n], q = acc[i][8 + n];
+          s = fmaf(__uint_as_float(a[j].x), v0, s);
+          s = fmaf(__uint_as_float(a[j].y), v1, s);
+          s = fmaf(__uint_as_float(a[j].z), v2, s);
+          s = fmaf(__uint_as_float(a[j].w), v3, s);
+          q = fmaf(__uint_as_float(b[j].x), v0, q);
+          q = fmaf(__uint_as_float(b[j].y), v1, q);
+          q = fmaf(__uint_as_float(b[j].z), v2, q);
+          q = fmaf(__uint_as_float(b[j].w), v3, q);
+          acc[i][n] = s;
+          acc[i][8 + n] = q;
+        }
+      }
+    }
+  }
+}
+
+// A warp's sums of tile i to shared memory as [16 rows][8 tokens].
+template <typename T> __device__ __forceinline__ void put_tile(float *d, const float (&acc)[Elem<T>::acc]) {
+  const int lane = lane_id(), g = lane >> 2, t = lane & 3;
+  if constexpr (sizeof(T) == 2) {
+    d[g * 8 + 2 * t] = acc[0];
+    d[g * 8 + 2 * t + 1] = acc[1];
+    d[(g + 8) * 8 + 2 * t] = acc[2];
+    d[(g + 8) * 8 + 2 * t + 1] = acc[3];
+  } else {
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float s = acc[8 * h + n];  // over the four threads of the row
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        if (t == 0) d[(g + 8 * h) * 8 + n] = s;
+      }
+    }
+  }
+}
+
+// Runs the units u = first, first + stride, ... < n of one phase on a group of
+// `warps` warps (this warp is number `w` of group `gid`). A unit with more
+// tokens than NT tiles hold streams its weights once for each 8 NT tokens (the
+// later times from L2). Partial sums meet in `part` ([2][warps][NT][128],
+// alternating halves, so one group barrier each), from which `finish` takes
+// them. The next unit's first weights are in flight before the sums of the
+// present one meet. `ready` runs once, after the first loads are issued: the
+// grid barrier before the phase, if any.
+template <typename T, int NT, bool FRESH, typename Weights, typename Tokens, typename Finish, typename Ready>
+__device__ __forceinline__ bool run_units(int first, int stride, int n, int w, int warps, int gid, float *part,
+                                          const T *x, Weights weights, Tokens tokens, Finish finish, Ready ready) {
+  uint4 a[kSteps], b[kSteps], na[kSteps], nb[kSteps];
+  WeightRows cur, nxt;
+  int u = first, tok0 = 0;
+  if (u < n) {
+    weights(u, w, warps, cur);
+    load_chunk<T>(cur, cur.step, a, b);
+  }
+  if (!ready()) return false;
+  int half = 0;
+  while (u < n) {
+    int rows[NT];
+    const int left = tokens(u, tok0, rows);  // this thread's token rows, and how many tokens there are from tok0 on
+    const int tiles = min((left + 7) >> 3, NT);
+    float acc[NT][Elem<T>::acc];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < Elem<T>::acc; ++j) acc[i][j] = 0.f;
+    const bool last = left <= 8 * NT;
+    const int un = last ? u + stride : u;
+    int step = cur.step;
+    do {
+      const int ns = step + kSteps;
+      if (ns < cur.end) {
+        load_chunk<T>(cur, ns, na, nb);
+      } else if (un < n) {
+        weights(un, w, warps, nxt);
+        load_chunk<T>(nxt, nxt.step, na, nb);
+      }
+      add_chunk<T, NT, FRESH>(cur, step, a, b, x, rows, tiles, acc);
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        a[j] = na[j];
+        b[j] = nb[j];
+      }
+      step = ns;
+    } while (step < cur.end);
+    float *mine = part + (static_cast<size_t>(half) * warps) * (NT * 128);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (i < tiles) put_tile<T>(mine + (w * NT + i) * 128, acc[i]);
+    group_sync(gid, warps);
+    finish(u, tok0, min(left, 8 * NT), last, mine);
+    half ^= 1;
+    cur = nxt;
+    u = un;
+    tok0 = last ? 0 : tok0 + 8 * NT;
+  }
+  return true;
+}
+
+struct FewParams {
+  Dims d;
+  Weights w;
+  FewWork ws;
+  const void *x;
+  void *y;
+  uint32_t *err;
+  int n_tok;
+};
+
+// Routing tables of a CTA, in shared memory.
+struct Routes {
+  int16_t sel[kMaxEdges];   // expert of edge t * k + j
+  float wgt[kMaxEdges];     // its weight
+  int16_t list[kMaxEdges];  // edges by expert
+  int16_t rank[kMaxEdges];
+  int32_t first[1025];      // first entry of each hit expert in list
+  int16_t hit[1024];        // hit experts, ascending
+  int32_t cnt[1024];
+  int32_t n_hit;
+};
+
+// Top-k of token t by one warp, by the layer's router rule over every expert
+// (see epoch_layer_config), from the logits row in global memory. `key` is E
+// words of shared memory of this warp. Lane l owns the consecutive experts
+// [l * per, (l + 1) * per): the lowest lane of equal keys holds the lowest id.
+__device__ void select_token(const FewParams &p, int t, unsigned *key, Routes &r) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const Dims &d = p.d;
+  const int lane = lane_id(), E = d.E, k = d.k;
+  const float *row = p.ws.logits + static_cast<size_t>(t) * E;
+  float top = -INFINITY;
+  for (int e = lane; e < E; e += 32) {
+    const float v = __ldcg(row + e);
+    top = fmaxf(top, v);
+    key[e] = order_key(d.router == 0 ? v : 1.f / (1.f + expf(-v)) + p.w.b_router[e]);
+  }
+  __syncwarp();
+  if (d.router != 0 && d.topk_group < d.n_group) {
+    // groups ranked by the sum of their two best scores; the first topk_group, and further ones while
+    // they hold fewer than k experts, stay
+    const int gs = E / d.n_group;
+    float score = -INFINITY;
+    for (int g = 0; g < d.n_group; ++g) {
+      unsigned k1 = 0u, k2 = 0u;
+      for (int e = lane; e < gs; e += 32) {
+        const unsigned q = key[g * gs + e];
+        if (q > k1) {
+          k2 = k1;
+          k1 = q;
+        } else if (q > k2) {
+          k2 = q;
+        }
+      }
+      const unsigned m1 = __reduce_max_sync(kAll, k1);
+      const int win = __ffs(__ballot_sync(kAll, k1 == m1)) - 1;
+      const unsigned m2 = __reduce_max_sync(kAll, lane == win ? k2 : k1);
+      if (lane == g) score = m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
+    }
+    int rank = 0;
+    for (int i = 0; i < d.n_group; ++i) {
+      const float o = __shfl_sync(kAll, score, i);
+      rank += o > score || (o == score && i < lane);
+    }
+    const unsigned open = __ballot_sync(kAll, lane < d.n_group && (rank < d.topk_group || rank * gs < k));
+    for (int e = lane; e < E; e += 32)
+      if (!((open >> (e / gs)) & 1u)) key[e] = 0u;
+    __syncwarp();
+  }
+  const int per = (E + 31) / 32, lo = lane * per, hi = min(lo + per, E);
+  unsigned best = 0u;
+  int at = lo;
+  for (int e = lo; e < hi; ++e)
+    if (key[e] > best) {
+      best = key[e];
+      at = e;
+    }
+  int sel = 0;
+  float val = -INFINITY;
+  for (int j = 0; j < k; ++j) {
+    const unsigned m = __reduce_max_sync(kAll, best);
+    const int win = __ffs(__ballot_sync(kAll, best == m)) - 1;
+    const int e = __shfl_sync(kAll, at, win);
+    if (lane == j) {
+      sel = e;
+      val = key_value(m);
+    }
+    if (lane == win) {
+      key[at] = 0u;
+      best = 0u;
+      for (int q = lo; q < hi; ++q)
+        if (key[q] > best) {
+          best = key[q];
+          at = q;
+        }
+    }
+  }
+  float num, den = 0.f;
+  if (d.router == 0) {
+    const float ref = d.raw_weights ? 0.f : __shfl_sync(kAll, val, 0);
+    if (d.raw_weights) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      for (int e = lane; e < E; e += 32) den += expf(__ldcg(row + e) - top);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kAll, den, o);
+      num = expf(val - top);
+    } else {
+      num = lane < k ? expf(val - ref) : 0.f;
+    }
+  } else {
+    num = 1.f / (1.f + expf(-__ldcg(row + sel)));
+    if (d.raw_weights) den = 1.f;
+  }
+  if (!d.raw_weights)
+    for (int j = 0; j < k; ++j) den += __shfl_sync(kAll, num, j);
+  if (lane < k) {
+    r.sel[t * k + lane] = static_cast<int16_t>(sel);
+    r.wgt[t * k + lane] = num / den;
+  }
+}
+
+// Edges sorted by expert, from the selections (all threads). The order of an
+// expert's edges does not matter: each is a column of its own everywhere.
+__device__ void build_routes(const FewParams &p, Routes &r) {
+  const int E = p.d.E, edges = p.n_tok * p.d.k;
+  for (int e = threadIdx.x; e < E; e += kThreads) r.cnt[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < edges; i += kThreads) r.rank[i] = static_cast<int16_t>(atomicAdd(&r.cnt[r.sel[i]], 1));
+  __syncthreads();
+  if (warp_id() == 0) {
+    const int lane = lane_id(), per = (E + 31) / 32, lo = lane * per, hi = min(lo + per, E);
+    int n = 0, h = 0;
+    for (int e = lo; e < hi; ++e) {
+      n += r.cnt[e];
+      h += r.cnt[e] > 0;
+    }
+    int sn = n, sh = h;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int yn = __shfl_up_sync(0xffffffffu, sn, o), yh = __shfl_up_sync(0xffffffffu, sh, o);
+      if (lane >= o) {
+        sn += yn;
+        sh += yh;
+      }
+    }
+    if (lane == 31) {
+      r.n_hit = sh;
+      r.first[sh] = sn;
+    }
+    sn -= n;
+    sh -= h;
+    for (int e = lo; e < hi; ++e) {
+      const int c = r.cnt[e];
+      if (c > 0) {
+        r.first[sh] = sn;
+        r.hit[sh++] = static_cast<int16_t>(e);
+      }
+      r.cnt[e] = sn;  // now the expert's first entry
+      sn += c;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < edges; i += kThreads) r.list[r.cnt[r.sel[i]] + r.rank[i]] = static_cast<int16_t>(i);
+  __syncthreads();
+}
+
+template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const __grid_constant__ FewParams p) {
+  extern __shared__ float part[];  // partial sums of the units; the selection's keys between the phases
+  __shared__ Routes r;
+  __shared__ int s_last[kWarps / kSplit];
+  const Dims &d = p.d;
+  const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
+  const int H = d.H, I = d.I, E = d.E, k = d.k, nt = p.n_tok;
+  constexpr int per = Elem<T>::per, step = Elem<T>::step;
+  const T *x = static_cast<const T *>(p.x);
+  T *act = static_cast<T *>(p.ws.act);     // row of edge e at e * I,
+  const int act_sh = p.n_tok * k * I;      // of shared expert s and token t at act_sh + (s * n_tok + t) * I_s
+
+  auto split = [&](WeightRows &o, int cols, int w, int warps) {
+    const int steps = (cols + step - 1) / step;
+    o.k = cols;
+    o.step = steps * w / warps;
+    o.end = steps * (w + 1) / warps;
+  };
+  auto sum = [&](const float *mine, int warps, int tok, int row) {
+    float s = 0.f;
+    const float *q = mine + (tok >> 3) * 128 + row * 8 + (tok & 7);
+    for (int i = 0; i < warps; ++i) s += q[i * NT * 128];
+    return s;
+  };
+
+  // phase 0: router tiles of 8 experts, then shared tiles of 8 activation columns
+  const int n_router = (E + 7) / 8, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[1] = 0;  // no CTA reaches the second barrier before this one passes the first
+  run_units<T, NT, false>(
+      blockIdx.x, gridDim.x, n_router + d.n_sh * sh8, warp, kWarps, 0, part, x,
+      [&](int u, int w, int warps, WeightRows &o) {
+        split(o, H, w, warps);
+        if (u < n_router) {
+          const int e = u * 8 + g;
+          o.ok0 = e < E;
+          o.ok1 = false;
+          o.p0 = o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_router) + static_cast<int64_t>(e) * H + t * per);
+        } else {
+          const int s = (u - n_router) / sh8, c = (u - n_router - s * sh8) * 8 + g;
+          const int64_t at = (static_cast<int64_t>(s) * d.I_s + c) * H + t * per;
+          o.ok0 = o.ok1 = c < d.I_s;
+          o.p0 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.ws_gate) + at);
+          o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.ws_up) + at);
+        }
+      },
+      [&](int, int tok0, int (&rows)[NT]) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) rows[i] = tok0 + 8 * i + g < nt ? (tok0 + 8 * i + g) * H : -1;
+        return nt - tok0;
+      },
+      [&](int u, int tok0, int count, bool, const float *mine) {
+        for (int v = threadIdx.x; v < count * 8; v += kThreads) {
+          const int tok = v >> 3, c = v & 7;
+          if (u < n_router) {
+            const int e = u * 8 + c;
+            if (e < E)
+              p.ws.logits[static_cast<size_t>(tok0 + tok) * E + e] =
+                  sum(mine, kWarps, tok, c) + (d.router == 0 ? p.w.b_router[e] : 0.f);
+          } else {
+            const int s = (u - n_router) / sh8, col = (u - n_router - s * sh8) * 8 + c;
+            if (col < d.I_s)
+              act[act_sh + (s * nt + tok0 + tok) * d.I_s + col] =
+                  from_f32<T>(silu(sum(mine, kWarps, tok, c)) * sum(mine, kWarps, tok, c + 8));
+          }
+        }
+      },
+      [] { return true; });
+  if (!grid_barrier(p.ws.ctr, p.err, d.timeout_ns)) return;
+
+  for (int tok = warp; tok < nt; tok += kWarps) select_token(p, tok, reinterpret_cast<unsigned *>(part) + warp * E, r);
+  __syncthreads();
+  build_routes(p, r);
+
+  const int grp = warp / kSplit, w = warp % kSplit;
+  const int first = grp * gridDim.x + blockIdx.x, stride = gridDim.x * (kWarps / kSplit);  // SMs first
+  float *gpart = part + static_cast<size_t>(grp) * 2 * kSplit * NT * 128;
+  const int gthread = threadIdx.x - grp * kSplit * 32;
+
+  // phase 1: routed activations, 8 columns of an expert a unit
+  const int i8 = (I + 7) / 8;
+  run_units<T, NT, false>(
+      first, stride, r.n_hit * i8, w, kSplit, grp, gpart, x,
+      [&](int u, int wi, int warps, WeightRows &o) {
+        const int h = u / i8, c = (u - h * i8) * 8 + g;
+        const int64_t at = (static_cast<int64_t>(r.hit[h]) * I + c) * H + t * per;
+        split(o, H, wi, warps);
+        o.ok0 = o.ok1 = c < I;
+        o.p0 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_gate) + at);
+        o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_up) + at);
+      },
+      [&](int u, int tok0, int (&rows)[NT]) {
+        const int h = u / i8, f = r.first[h] + tok0, n = r.first[h + 1] - f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) rows[i] = 8 * i + g < n ? r.list[f + 8 * i + g] / k * H : -1;
+        return n;
+      },
+      [&](int u, int tok0, int count, bool, const float *mine) {
+        const int h = u / i8, f = r.first[h] + tok0;
+        for (int v = gthread; v < count * 8; v += kSplit * 32) {
+          const int tok = v >> 3, c = v & 7, col = (u - h * i8) * 8 + c;
+          if (col < I)
+            act[r.list[f + tok] * I + col] = from_f32<T>(silu(sum(mine, kSplit, tok, c)) * sum(mine, kSplit, tok, c + 8));
+        }
+      },
+      [] { return true; });
+
+  // phase 2: 16 rows of H of an expert (routed, then shared) a unit; rows of
+  // the fp32 sums: edge e at row e, shared expert s and token t at n_tok * k + s * n_tok + t
+  const int h16 = (H + 15) / 16, groups = r.n_hit + d.n_sh;
+  run_units<T, NT, true>(
+      first, stride, groups * h16, w, kSplit, grp, gpart, act,
+      [&](int u, int wi, int warps, WeightRows &o) {
+        const int h = u / h16, row = (u - h * h16) * 16 + g;
+        const bool shared = h >= r.n_hit;
+        const int cols = shared ? d.I_s : I;
+        const T *base = static_cast<const T *>(shared ? p.w.ws_down : p.w.w_down);
+        const int64_t at = (static_cast<int64_t>(shared ? h - r.n_hit : r.hit[h]) * H + row) * cols + t * per;
+        split(o, cols, wi, warps);
+        o.ok0 = row < H;
+        o.ok1 = row + 8 < H;
+        o.p0 = reinterpret_cast<const char *>(base + at);
+        o.p1 = reinterpret_cast<const char *>(base + at + static_cast<int64_t>(8) * cols);
+      },
+      [&](int u, int tok0, int (&rows)[NT]) {
+        const int h = u / h16;
+        if (h >= r.n_hit) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            rows[i] = tok0 + 8 * i + g < nt ? act_sh + ((h - r.n_hit) * nt + tok0 + 8 * i + g) * d.I_s : -1;
+          return nt - tok0;
+        }
+        const int f = r.first[h] + tok0, n = r.first[h + 1] - f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) rows[i] = 8 * i + g < n ? r.list[f + 8 * i + g] * I : -1;
+        return n;
+      },
+      [&](int u, int tok0, int count, bool last, const float *mine) {
+        const int h = u / h16, tile = u - h * h16;
+        const bool shared = h >= r.n_hit;
+        for (int v = gthread; v < count * 16; v += kSplit * 32) {
+          const int tok = tok0 + (v >> 4), c = v & 15, col = tile * 16 + c;
+          const int at = shared ? nt * k + (h - r.n_hit) * nt + tok : r.list[r.first[h] + tok];
+          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * H + col, sum(mine, kSplit, v >> 4, c));
+        }
+        if (!last) return;
+        group_sync(grp, kSplit);
+        if (gthread == 0) {
+          __threadfence();
+          const int n = atomicAdd(p.ws.ctr + 2 + tile, 1);
+          s_last[grp] = n == groups - 1;
+          if (n == groups - 1) p.ws.ctr[2 + tile] = 0;  // for the next call
+          __threadfence();
+        }
+        group_sync(grp, kSplit);
+        if (!s_last[grp]) return;
+        for (int v = gthread; v < nt * 16; v += kSplit * 32) {
+          const int tok = v >> 4, col = tile * 16 + (v & 15);
+          if (col >= H) continue;
+          const float *o = p.ws.out + col;
+          float s = 0.f;
+          for (int j = 0; j < k; ++j) s = fmaf(r.wgt[tok * k + j], __ldcg(o + static_cast<size_t>(tok * k + j) * H), s);
+          for (int j = 0; j < d.n_sh; ++j) s += __ldcg(o + static_cast<size_t>(nt * k + j * nt + tok) * H);
+          const size_t at = static_cast<size_t>(tok) * H + col;
+          if (d.residual) s += to_f32(x[at]);
+          static_cast<T *>(p.y)[at] = from_f32<T>(s);
+        }
+      },
+      [&] {
+        if (!grid_barrier(p.ws.ctr + 1, p.err, d.timeout_ns)) return false;
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[0] = 0;  // every CTA has left the first barrier
+        return true;
+      });
+}
+
+template <typename T, int NT> cudaError_t launch(const FewParams &p, cudaStream_t s) {
+  auto *fn = &k_moe_few<T, NT>;
+  static std::atomic<uint64_t> ready{0};  // devices whose copy of the kernel has its shared memory raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  size_t smem = static_cast<size_t>(2) * kWarps * NT * 128 * sizeof(float);
+  const size_t keys = static_cast<size_t>(kWarps) * p.d.E * sizeof(unsigned);
+  if (smem < keys) smem = keys;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load() & bit)) {
+    const int most = 2 * kWarps * NT * 128 * 4 > kWarps * 1024 * 4 ? 2 * kWarps * NT * 128 * 4 : kWarps * 1024 * 4;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) e = prefer_max_shared(fn);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  // Cooperative: the grid's CTAs are resident together or the launch fails, which the grid barriers need.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+// Token tiles a thread's registers hold: up to 32 tokens of bf16 layers (16
+// fp32 sums), 16 of fp32 layers (32 sums).
+cudaError_t by_tokens(const FewParams &p, bool bf16, cudaStream_t s) {
+  if (bf16) {
+    if (p.n_tok <= 8) return launch<__nv_bfloat16, 1>(p, s);
+    if (p.n_tok <= 16) return launch<__nv_bfloat16, 2>(p, s);
+    return launch<__nv_bfloat16, 4>(p, s);
+  }
+  return p.n_tok <= 8 ? launch<float, 1>(p, s) : launch<float, 2>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_few(const Dims &d, const Weights &w, const FewWork &ws, const void *x, void *y, int n_tok,
+                           int bf16, uint32_t *err, cudaStream_t s) {
+  FewParams p;
+  p.d = d;
+  p.w = w;
+  p.ws = ws;
+  p.x = x;
+  p.y = y;
+  p.err = err;
+  p.n_tok = n_tok;
+  return by_tokens(p, bf16 != 0, s);
+}
+
+}  // namespace epoch

@@ -1069,6 +1069,18 @@ bool encode_kmajor_bf16(CUtensorMap *map, const void *base, uint64_t k_elems, ui
   return r == CUDA_SUCCESS;
 }
 
+bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, uint64_t rows, uint32_t box_rows) {
+  if (!g_encode || base == nullptr || rows == 0) return false;
+  cuuint64_t dims[2] = {k_elems, rows};
+  cuuint64_t strides[1] = {k_elems};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Gate launch geometry. CTAs per cluster (H slices): 8 when H / 8 is a whole
 // number of 64-column K blocks, else 4. Positions per cluster tile: as few as
 // let every cluster of the launch be resident at once (the device holds a

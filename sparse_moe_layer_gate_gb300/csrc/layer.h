@@ -25,6 +25,19 @@ struct Ctrl {
   int32_t short_next;   // the support coverage fell short: the next iteration runs full fresh
 };
 
+// Scratch of the few-token call (few.cu), carved from the caller's workspace; a
+// block's state is not touched by it.
+constexpr int kFewTokens = 64;  // tokens of one call, at most
+struct FewWork {
+  float *logits;   // [kFewTokens][E]
+  void *act;       // activations, layer dtype: [n_tok*k][I] of the edges, then [n_sh][n_tok][I_s]
+  float *out;      // [kFewTokens*(k + n_sh)][H] expert outputs
+  int32_t *ctr;    // [0], [1] arrivals at the two grid barriers, then finished expert tiles of each 16 rows
+                   // of H; all but [1] (zeroed by each call) are zero between calls, and after a timeout
+                   // once the status is cleared
+  size_t ctr_bytes;
+};
+
 // Device pointers carved from the caller's workspace.
 struct Work {
   // block-lifetime state
@@ -88,6 +101,7 @@ struct Work {
   Ctrl *ctrl;
   epoch_iter_stats *stats;
   uint32_t *err;
+  FewWork few;
 };
 
 // Per-CTA trace record of a tcgen05 kernel (globaltimer ns): entry, setup done,
@@ -153,7 +167,7 @@ struct AtlasParams {
 
 // Kernel kinds, for profiling and launch counting.
 enum Kind {
-  K_GATE = 0, K_PLAN_TOPK, K_PLAN_SUPPORT, K_ROUTING, K_UP, K_DOWN, K_COMBINE, K_TEST, K_SELECT, K_NUM
+  K_GATE = 0, K_PLAN_TOPK, K_PLAN_SUPPORT, K_ROUTING, K_UP, K_DOWN, K_COMBINE, K_TEST, K_SELECT, K_FEW, K_NUM
 };
 extern const char *const kKindName[K_NUM];
 
@@ -211,6 +225,10 @@ cudaError_t launch_wait_test(uint32_t *err, int64_t timeout_ns, cudaStream_t s);
 cudaError_t launch_up_simt(const Dims &d, const Weights &w, const Work &ws, const void *x, cudaStream_t s);
 cudaError_t launch_down_simt(const Dims &d, const Weights &w, const Work &ws, cudaStream_t s);
 
+// few.cu: the whole layer for n_tok <= kFewTokens tokens in one cooperative launch
+cudaError_t launch_moe_few(const Dims &d, const Weights &w, const FewWork &ws, const void *x, void *y, int n_tok,
+                           int bf16, uint32_t *err, cudaStream_t s);
+
 // gemm_tc.cu (bf16 layers, tcgen05 + TMA)
 // Packs row-major [rows][k] bf16 into swizzled tiles at dst + t * tile_stride + tile_off.
 // Tiles of `pair` consecutive row blocks that share a K block are stored adjacent.
@@ -238,7 +256,56 @@ bool gate_tc_supported(const Dims &d);
 // wave of clusters), which its in-kernel grid barrier before the worklist needs.
 bool gate_builds_worklist(const Dims &d);
 
+// Row-major [rows][k_elems] 8-bit matrix, boxes of 128 (K) x box_rows, 128-byte swizzle.
+bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, uint64_t rows, uint32_t box_rows);
+
 int num_sms();
+
+// ------------------------------------------------------------ operators without a layer
+// block_norm.cu; strides in elements, parameters (weight, channel gate, channel
+// scale, next_weight) fp32 or bf16 together
+struct NormArgs {
+  const void *block, *residual;  // before: residual is the input, block unused
+  const void *weight, *gate, *scale, *next_weight;
+  void *out, *next_out;
+  int64_t block_stride, residual_stride, gate_stride, out_stride, next_stride;
+  int32_t n_rows, hidden;
+  int32_t act_bf16, res_bf16, par_bf16;
+  int32_t gate_kind;     // 0 none, 1 one value a channel, 2 one a row and channel
+  int32_t gate_sigmoid;
+  float residual_scale, eps;
+};
+cudaError_t launch_block_norm(const NormArgs &a, bool after, cudaStream_t s);
+
+// fp8_quant.cu
+struct QuantArgs {
+  const void *x;
+  const int32_t *rows;  // nullable: row i of the output is row rows[i] of x
+  uint8_t *q;
+  float *scales;
+  int64_t x_stride;
+  int64_t n_rows, n_src;
+  int32_t cols;
+  int32_t swiglu;
+};
+cudaError_t launch_fp8_quant(const QuantArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_fp8_quant_weight(const void *w, bool bf16, int64_t mats, int64_t n, int64_t k, uint8_t *q,
+                                    float *scales, cudaStream_t s);
+
+// fp8_gemm.cu
+struct GemmArgs {
+  const void *a, *b;
+  const float *sa, *sb;
+  const int32_t *offsets;  // nullable (dense)
+  void *out;
+  int64_t out_stride;
+  int32_t m, N, K, n_groups;
+  int32_t out_bf16;
+  int32_t wide_out;  // rows of the output start on 16-byte boundaries
+};
+cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s);
+// Device error word of the operators without a layer, on the current device (nullptr: none).
+uint32_t *ops_error_word();
 
 // cudaLaunchKernelEx of `fn`: programmatic (may start before the previous
 // kernel in the stream ends; the kernel calls pdl_wait before touching its

@@ -25,7 +25,7 @@
 namespace epoch {
 
 const char *const kKindName[K_NUM] = {"gate",        "plan_topk", "plan_support", "routing", "experts",
-                                      "expert_down", "combine",   "wait_test",    "select"};
+                                      "expert_down", "combine",   "wait_test",    "select",  "few"};
 
 // ---------------------------------------------------------------- helpers
 

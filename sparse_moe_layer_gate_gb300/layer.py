@@ -126,6 +126,25 @@ class EpochLayer:
                                      int(iteration), y.data_ptr(), _stream(stream), _ptr(stats)), "epoch_moe_iter")
         return y
 
+    def forward_few(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The whole layer for the at most 64 rows of x (also at most
+        max_positions), outside any block: every expert eligible, no row cache
+        (epoch_moe_few). Leaves a block in progress as it is."""
+        self._check_x(x)
+        if y is None:
+            if stream is None:
+                y = torch.empty_like(x)
+            else:
+                with torch.cuda.stream(stream):
+                    y = torch.empty_like(x)
+        else:
+            self._check_x(y)
+            if y.shape != x.shape:
+                raise ValueError("y must have the shape of x")
+        B.check(B.lib().epoch_moe_few(self.handle, x.data_ptr(), x.shape[0], y.data_ptr(), _stream(stream)),
+                "epoch_moe_few")
+        return y
+
     @staticmethod
     def stats_dict(stats: torch.Tensor) -> dict:
         """Host view of a stats tensor that moe_iter filled."""

@@ -1,0 +1,535 @@
+"""Operators beside the layer: norms around a block, e4m3 quantisation and the
+scaled e4m3 product, each against its formula in 64 bits, and their refusals.
+
+Tolerances count roundings: u is half a step of fp32 (2^-24) and _half(t) half a
+step of the result's type, both relative. They are derived at each test."""
+import ctypes as C
+import math
+
+import pytest
+import torch
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+U = 2.0 ** -24
+TINY = 2.0 ** -126
+
+
+def _half(t):
+    return torch.finfo(t).eps / 2
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from sparse_moe_layer_gate_gb300 import builder, ops as o
+    if builder.is_stale():
+        builder.build()
+    return o
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _rnd(g, *shape, std=1.0, dtype=F32):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _rms64(x, w, eps):
+    k = 1.0 / torch.sqrt(x.square().mean(1, keepdim=True) + eps)
+    return k, x * k * w
+
+
+def _within(got, want, bound, what=""):
+    d = (got.double() - want).abs()
+    over = d > bound
+    assert not bool(over.any()), (what, int(over.sum()), float((d / bound.clamp(min=1e-300)).max()))
+
+
+def _norm_units(h):
+    """Roundings of rms's factor: a thread adds at most 32 squares (or h / 512 where the row is longer) one after
+    another, then 5 + 16 sums across threads; half of that through the root, plus root, mean and products."""
+    return (max(32, h / 512) + 21) / 2 + 12
+
+
+# ------------------------------------------------------------------------------------- norm before
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,h", [(1, 1), (1, 2048), (3, 8), (5, 7), (33, 64), (17, 513), (2, 2047), (9, 4096),
+                                 (4, 8200), (2, 16384), (3, 16392), (2, 20001)])
+@pytest.mark.parametrize("xt,ot,pt", [(BF16, BF16, F32), (F32, BF16, BF16), (BF16, F32, BF16), (F32, F32, F32)])
+def test_norm_before(ops, n, h, xt, ot, pt):
+    g = _gen(n * 7919 + h)
+    x, w = _rnd(g, n, h, std=3.0, dtype=xt), (1 + _rnd(g, h, std=0.2)).to(pt)
+    got = ops.norm_before(x, w, eps=1e-5, out_dtype=ot)
+    assert got.dtype == ot and got.shape == (n, h)
+    _, want = _rms64(x.double(), w.double(), float(torch.tensor(1e-5)))
+    _within(got, want, want.abs() * (_norm_units(h) * U + _half(ot) * (ot == BF16)) + 1e-30)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", ["stride", "offset", "alias", "zero_rows", "zeros", "nan_row", "far_rows"])
+def test_norm_before_layouts(ops, case):
+    g = _gen(5)
+    n, h = 6, 256
+    w = 1 + _rnd(g, h, std=0.2)
+    if case == "zero_rows":
+        got = ops.norm_before(torch.empty(0, h, device="cuda", dtype=BF16), w)
+        assert got.shape == (0, h)
+        return
+    x = _rnd(g, n, h, dtype=BF16)
+    want = _rms64(x.double(), w.double(), 1e-6)[1]
+    bound = want.abs() * (_norm_units(h) * U + _half(BF16)) + 1e-30
+    if case == "stride":  # rows apart, on and off 16-byte boundaries
+        for pad in (8, 3):
+            v = torch.full((n, h + pad), 99.0, device="cuda", dtype=BF16)
+            v[:, :h] = x
+            o = torch.full((n, h + pad + 1), -7.0, device="cuda", dtype=BF16)
+            got = ops.norm_before(v[:, :h], w, out=o[:, 1:h + 1])
+            _within(got, want, bound)
+            assert bool((o[:, 0] == -7).all()) and bool((o[:, h + 1:] == -7).all())
+    elif case == "offset":  # a base that is aligned to its element alone
+        v = torch.empty(n * h + 1, device="cuda", dtype=BF16)[1:].view(n, h)
+        v.copy_(x)
+        _within(ops.norm_before(v, w), want, bound)
+    elif case == "alias":
+        v = x.clone()
+        assert ops.norm_before(v, w, out=v) is v
+        _within(v, want, bound)
+    elif case == "zeros":  # a row of zeros is a row of zeros
+        x[2] = 0
+        got = ops.norm_before(x, w)
+        assert bool((got[2] == 0).all()) and bool(got.isfinite().all())
+    elif case == "nan_row":  # a bad row stays alone
+        x[3, 17] = math.nan
+        got = ops.norm_before(x, w)
+        assert bool(got[3].isnan().all())
+        keep = [0, 1, 2, 4, 5]
+        _within(got[keep], want[keep], bound[keep])
+    else:  # rows whose offsets pass 32 bits
+        far = (1 << 31) // 2 + 24
+        base = torch.empty(2 * far + h, device="cuda", dtype=BF16)
+        v = base.as_strided((3, h), (far, 1))
+        v.copy_(x[:3])
+        got = ops.norm_before(v, w, out=v)
+        _within(got, want[:3], bound[:3])
+
+
+# -------------------------------------------------------------------------------------- norm after
+def _after64(b, r, w, gate, sig, scale, nw, eps):
+    """r', h' in 64 bits and the bounds of both in fp32, before their last rounding."""
+    b, r = b.double(), r.double()
+    h = b.shape[1]
+    z = b if w is None else _rms64(b, w.double(), eps)[1]
+    if gate is not None:
+        gate = gate.double()
+        z = z * (torch.sigmoid(gate) if sig else gate)
+    sr = r * (scale.double() if isinstance(scale, torch.Tensor) else scale)
+    out = sr + z
+    size = sr.abs() + z.abs()
+    e_out = size * (_norm_units(h) + 10) * U  # the factor, the gate (exp, sum, quotient), two products and a sum
+    if nw is None:
+        return out, e_out, None, None
+    k, nxt = _rms64(out, nw.double(), eps)
+    rel = e_out.square().mean(1, keepdim=True).sqrt() * k + _norm_units(h) * U
+    return out, e_out, nxt, (e_out + out.abs() * rel) * k * nw.double().abs()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,h", [(1, 1), (1, 2048), (7, 40), (19, 1001), (5, 4096), (3, 8192), (2, 16400), (3, 17001)])
+@pytest.mark.parametrize("at,rt,pt", [(BF16, BF16, F32), (BF16, F32, BF16), (F32, BF16, F32), (F32, F32, BF16)])
+@pytest.mark.parametrize("form", ["plain", "gate", "full", "no_weight"])
+def test_norm_after(ops, n, h, at, rt, pt, form):
+    g = _gen(n * 104729 + h)
+    b, r = _rnd(g, n, h, dtype=at), _rnd(g, n, h, std=2.0, dtype=rt)
+    w, nw = (1 + _rnd(g, h, std=0.2)).to(pt), (1 + _rnd(g, h, std=0.2)).to(pt)
+    gate, sig, scale = None, False, 1.0
+    if form == "gate":
+        gate, scale, nw = _rnd(g, h).to(pt), (1 + _rnd(g, h, std=0.1)).to(pt), None
+    elif form == "full":
+        gate, sig, scale = _rnd(g, n, h, std=3.0, dtype=at), True, 0.75
+    elif form == "no_weight":
+        w, scale = None, -0.5
+    got = ops.norm_after(b, r, w, gate=gate, gate_sigmoid=sig, residual_scale=scale, next_weight=nw, eps=1e-6)
+    out, e_out, nxt, e_nxt = _after64(b, r, w, gate, sig, scale, nw, 1e-6)
+    a = got if nw is None else got[0]
+    assert a.dtype == rt
+    _within(a, out, e_out + out.abs() * _half(rt) * (1 + 2 ** -7) + 1e-30, "r'")
+    if nw is not None:
+        assert got[1].dtype == at
+        _within(got[1], nxt, e_nxt + nxt.abs() * _half(at) * (1 + 2 ** -7) + 1e-30, "h'")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h", [1024, 1023, 16400])
+def test_norm_after_in_place_and_strided(ops, h):
+    g = _gen(11)
+    n = 5
+    b, r = _rnd(g, n, h, dtype=BF16), _rnd(g, n, h, dtype=F32)
+    w, nw = 1 + _rnd(g, h, std=0.1), 1 + _rnd(g, h, std=0.1)
+    want = ops.norm_after(b, r, w, next_weight=nw)
+    bb, rr = b.clone(), r.clone()
+    got = ops.norm_after(bb, rr, w, next_weight=nw, out=rr, next_out=bb)
+    assert got[0] is rr and got[1] is bb
+    assert torch.equal(rr, want[0]) and torch.equal(bb, want[1])
+    wide_b, wide_r = torch.zeros(n, h + 16, device="cuda", dtype=BF16), torch.zeros(n, h + 5, device="cuda")
+    wide_b[:, :h], wide_r[:, :h] = b, r
+    got = ops.norm_after(wide_b[:, :h], wide_r[:, :h], w, next_weight=nw)
+    out, e_out, nxt, e_nxt = _after64(b, r, w, None, False, 1.0, nw, 1e-6)
+    _within(got[0], out, e_out + 1e-30)
+    _within(got[1], nxt, e_nxt + nxt.abs() * _half(BF16) * (1 + 2 ** -7) + 1e-30)
+
+
+# ---------------------------------------------------------------------------------------- quantise
+def _scale32(amax):
+    """max(amax / 448, 2^-126) rounded once to fp32: a quotient of fp32 values taken in 64 bits rounds to the fp32
+    quotient (torch's own division by a number multiplies by its rounded reciprocal)."""
+    return (amax.double() / 448.0).float().clamp(min=TINY)
+
+
+def _quant64(v):
+    """Scales in fp32 as defined, values in 64 bits, blocks of 128 columns."""
+    n, k = v.shape
+    kb = -(-k // 128)
+    p = torch.nn.functional.pad(v, (0, kb * 128 - k)).view(n, kb, 128)
+    return (_scale32(p.abs().amax(2)) if v.dtype == F32 else (p.abs().amax(2) / 448.0).clamp(min=TINY)), p
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("n,k", [(1, 1), (1, 128), (1, 2048), (3, 130), (5, 1001), (64, 512), (333, 264), (2, 4096)])
+def test_fp8_quantize_rows(ops, n, k, dt):
+    x = _rnd(_gen(n + k), n, k, dtype=dt)
+    x[0, : max(1, k // 2)] = 0
+    q, s = ops.fp8_quantize(x)
+    ws, p = _quant64(x.float())  # fp32 and the same two operations: equal bit by bit
+    wq = (p * (1.0 / ws.double()).float().unsqueeze(2)).flatten(1)[:, :k].to(E4M3)
+    assert torch.equal(s, ws)
+    assert torch.equal(q.view(torch.uint8), wq.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_fp8_quantize_gather_strided_and_bad_rows(ops):
+    g = _gen(3)
+    x = _rnd(g, 9, 300, dtype=BF16)
+    wide = torch.zeros(9, 308, device="cuda", dtype=BF16)
+    wide[:, :300] = x
+    rows = torch.tensor([8, 0, 0, 3, 9, -1, 7], device="cuda", dtype=torch.int32)
+    q, s = ops.fp8_quantize(wide[:, :300], rows=rows)
+    good = [0, 1, 2, 3, 6]
+    wq, ws = ops.fp8_quantize(x[rows[good].long()].contiguous())
+    assert torch.equal(q[good].view(torch.uint8), wq.view(torch.uint8)) and torch.equal(s[good], ws)
+    assert bool(s[[4, 5]].isnan().all())
+    e, es = ops.fp8_quantize(x, rows=rows[:0])
+    assert e.shape == (0, 300) and es.shape == (0, 3)
+    e, es = ops.fp8_quantize(x[:0], rows=rows)  # no source row: every index is out of range
+    assert bool(es.isnan().all())
+
+
+@pytest.mark.gpu
+def test_fp8_quantize_special_values(ops):
+    x = torch.zeros(5, 256, device="cuda")
+    x[1, 5], x[2, 200], x[3, 0], x[4, 0] = math.nan, math.inf, 1e-40, 3e38
+    q, s = ops.fp8_quantize(x)
+    assert float(s[0, 0]) == TINY and bool((q[0].float() == 0).all())
+    assert bool(s[1, 0].isnan()) and float(s[1, 1]) == TINY
+    assert bool(s[2, 1].isinf()) and float(s[2, 0]) == TINY
+    assert float(s[3, 0]) == TINY
+    assert float(q[4, 0].float()) == 448.0
+    b, sb = ops.fp8_quantize_weight(torch.ones(64, 256, device="cuda"))
+    y = ops.fp8_matmul(q, s, b, sb)
+    assert bool(y[0].eq(0).all()) and bool(y[1].isnan().all()) and bool(y[2].isnan().all())
+    assert bool(y[3:].isfinite().all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("n,k", [(1, 8), (3, 512), (77, 200), (5, 333)])
+def test_fp8_quantize_swiglu(ops, n, k, dt):
+    x = _rnd(_gen(n * k), n, 2 * k, dtype=dt)
+    q, s = ops.fp8_quantize(x, swiglu=True)
+    v = torch.nn.functional.silu(x[:, :k].double()) * x[:, k:].double()
+    ws, _ = _quant64(v)
+    # exp (2 steps), sum, quotient and product of the SwiGLU, the quotient by 448: 8 roundings
+    _within(s, ws, ws * 8 * U + 1e-300)
+    sk = ws.repeat_interleave(128, 1)[:, :k]
+    # half a step of e4m3 (2^-4 of the value, 2^-10 of the scale below its normal range), and 20 fp32 roundings
+    _within(q.double() * s.double().repeat_interleave(128, 1)[:, :k], v,
+            v.abs() * (2.0 ** -4 + 20 * U) + sk * 2.0 ** -10 * (1 + 20 * U))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("shape", [(1, 1), (128, 128), (130, 300), (2, 256, 144), (3, 5, 1000)])
+def test_fp8_quantize_weight(ops, shape, dt):
+    w = _rnd(_gen(sum(shape)), *shape, dtype=dt)
+    q, s = ops.fp8_quantize_weight(w)
+    n, k = shape[-2:]
+    nb, kb = -(-n // 128), -(-k // 128)
+    p = torch.nn.functional.pad(w.float(), (0, kb * 128 - k, 0, nb * 128 - n)).unflatten(-1, (kb, 128)).unflatten(-3, (nb, 128))
+    ws = _scale32(p.abs().amax(dim=(-3, -1)))
+    assert torch.equal(s, ws)
+    wide = (1.0 / ws.double()).float().repeat_interleave(128, -1).repeat_interleave(128, -2)[..., :n, :k]
+    assert torch.equal(q.view(torch.uint8), (w.float() * wide).to(E4M3).view(torch.uint8))
+
+
+# ----------------------------------------------------------------------------------------- product
+def _operands(ops, g, m, n, k, e):
+    """e4m3 operands with scales of very different sizes from block to block."""
+    a = _rnd(g, m, k) * torch.exp(2 * _rnd(g, m, 1))
+    b = _rnd(g, e, n, k, std=k ** -0.5) * torch.exp(_rnd(g, e, 1, 1))
+    qa, sa = ops.fp8_quantize(a)
+    qb, sb = ops.fp8_quantize_weight(b)
+    sa = sa * torch.exp(_rnd(g, *sa.shape))
+    sb = sb * torch.exp(_rnd(g, *sb.shape))
+    return qa, sa.contiguous(), qb, sb.contiguous()
+
+
+def _product64(qa, sa, qb, sb, offsets):
+    """y in 64 bits, and the same sum over absolute values."""
+    m, k = qa.shape
+    e, n = qb.shape[:2]
+    a = qa.double() * sa.double().repeat_interleave(128, 1)[:, :k]
+    y = torch.full((m, n), math.nan, device="cuda", dtype=torch.float64)
+    s = torch.zeros_like(y)
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        if hi > lo:
+            w = qb[i].double() * sb[i].double().repeat_interleave(128, 1).repeat_interleave(128, 0)[:n, :k]
+            y[lo:hi] = a[lo:hi] @ w.T
+            s[lo:hi] = a[lo:hi].abs() @ w.abs().T
+    return y, s
+
+
+def _product_bound(y, s, k, out):
+    """Products of e4m3 are exact in fp32. A block's 128 are summed by the tensor core (a truncating sum: 2^-23 each),
+    then each block takes a product with the scale, a product of scales and a sum."""
+    kb = -(-k // 128)
+    return s * (128 * 2.0 ** -23 + (kb + 2) * U) + (y.abs() * _half(BF16) * (1 + 2 ** -7) if out == BF16 else 0) + 1e-30
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 4096, 2048), (2, 15, 128), (7, 130, 144), (9, 33, 640), (16, 256, 48),
+                                   (31, 200, 1040), (64, 129, 512), (65, 64, 128), (65, 1, 16), (128, 256, 256),
+                                   (129, 300, 272), (200, 511, 1168), (257, 513, 2064), (1000, 1024, 512)])
+def test_fp8_matmul_dense(ops, m, n, k, out):
+    qa, sa, qb, sb = _operands(ops, _gen(m * n + k), m, n, k, 1)
+    got = ops.fp8_matmul(qa, sa, qb[0], sb[0], out_dtype=out)
+    y, s = _product64(qa, sa, qb, sb, [0, m])
+    assert got.dtype == out
+    _within(got, y, _product_bound(y, s, k, out))
+
+
+GROUPS = {
+    "one_each": [0, 1, 2, 3, 4],
+    "empty_ends": [0, 0, 0, 9, 9],
+    "few": [0, 5, 5, 40, 64],
+    "ragged": [0, 1, 130, 130, 163, 420, 421],
+    "boxes": [0, 32, 97, 161, 290, 546],
+    "late_start": [3, 10, 80, 100],
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("n,k", [(64, 128), (272, 400), (513, 1040)])
+@pytest.mark.parametrize("name", list(GROUPS))
+def test_fp8_matmul_grouped(ops, name, n, k, out):
+    offsets = GROUPS[name]
+    m = offsets[-1] + 6  # rows behind the last group stay as they were
+    e = len(offsets) - 1
+    qa, sa, qb, sb = _operands(ops, _gen(m + n), m, n, k, e)
+    buf = torch.full((m, n), 77.0, device="cuda", dtype=out)
+    got = ops.fp8_matmul(qa, sa, qb, sb, offsets=torch.tensor(offsets, device="cuda", dtype=torch.int32), out=buf)
+    y, s = _product64(qa, sa, qb, sb, offsets)
+    lo, hi = offsets[0], offsets[-1]
+    _within(got[lo:hi], y[lo:hi], _product_bound(y, s, k, out)[lo:hi])
+    assert bool((got[:lo] == 77).all()) and bool((got[hi:] == 77).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [40, 300])
+def test_fp8_matmul_bad_offsets_are_read_in_range(ops, m):
+    g = _gen(m)
+    qa, sa, qb, sb = _operands(ops, g, m, 96, 256, 4)
+    bad = torch.tensor([-5, 20, 10, m + 1000, m - 1], device="cuda", dtype=torch.int32)
+    good = [0, 20, 20, m, m]
+    got = ops.fp8_matmul(qa, sa, qb, sb, offsets=bad, out_dtype=F32)
+    y, s = _product64(qa, sa, qb, sb, good)
+    _within(got, y, _product_bound(y, s, 256, F32))
+    assert ops.status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [5, 200])
+def test_fp8_matmul_strided_output_and_far_rows(ops, m):
+    g = _gen(m)
+    n, k = 72, 256
+    qa, sa, qb, sb = _operands(ops, g, m, n, k, 1)
+    want = ops.fp8_matmul(qa, sa, qb[0], sb[0], out_dtype=F32)
+    for pad in (8, 3):
+        buf = torch.full((m, n + pad), 5.0, device="cuda")
+        got = ops.fp8_matmul(qa, sa, qb[0], sb[0], out=buf[:, :n])
+        assert torch.equal(got, want) and bool((buf[:, n:] == 5).all())
+    stride = (1 << 31) // (m - 1) + 17  # the last rows' offsets pass 32 bits
+    far = torch.empty(stride * (m - 1) + n, device="cuda", dtype=BF16).as_strided((m, n), (stride, 1))
+    got = ops.fp8_matmul(qa, sa, qb[0], sb[0], out=far)
+    assert torch.equal(got.contiguous(), want.to(BF16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 48, 700])
+def test_fp8_matmul_repeats_bit_by_bit(ops, m):
+    """Sums are taken in a fixed order: the same operands give the same bits."""
+    qa, sa, qb, sb = _operands(ops, _gen(m), m, 520, 1024, 3)
+    off = torch.tensor([0, m // 3, m // 2, m], device="cuda", dtype=torch.int32)
+    first = ops.fp8_matmul(qa, sa, qb, sb, offsets=off)
+    for _ in range(3):
+        assert torch.equal(ops.fp8_matmul(qa, sa, qb, sb, offsets=off), first)
+
+
+# ------------------------------------------------------------------------------ streams and graphs
+@pytest.mark.gpu
+def test_ops_on_a_stream_of_their_own_and_in_a_graph(ops):
+    g = _gen(1)
+    h, m = 512, 96
+    x, w = _rnd(g, m, h, dtype=BF16), 1 + _rnd(g, h, std=0.1)
+    wq, ws = ops.fp8_quantize_weight(_rnd(g, 300, h, std=h ** -0.5))
+    ob = torch.empty(m, h, device="cuda", dtype=BF16)
+    oy = torch.empty(m, 300, device="cuda", dtype=BF16)
+    q, s = torch.empty(m, h, device="cuda", dtype=E4M3), torch.empty(m, 4, device="cuda")
+
+    def step(stream=None):
+        ops.norm_before(x, w, out=ob, stream=stream)
+        ops.fp8_quantize(ob, q=q, scales=s, stream=stream)
+        ops.fp8_matmul(q, s, wq, ws, out=oy, stream=stream)
+
+    step()
+    want = oy.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    oy.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    fresh = ops.norm_before(x, w, stream=side)
+    side.synchronize()
+    assert torch.equal(oy, want) and torch.equal(fresh, ob)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x2 = _rnd(g, m, h, dtype=BF16)
+    for src in (x2, x.clone()):
+        x.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = oy.clone()
+        step()
+        assert torch.equal(replayed, oy)
+    assert torch.equal(oy, want)
+
+
+@pytest.mark.gpu
+def test_two_products_at_once(ops):
+    """Calls on two streams share nothing."""
+    g = _gen(9)
+    sets = [_operands(ops, g, m, 512, 1024, 1) for m in (256, 40)]
+    want = [ops.fp8_matmul(a, sa, b[0], sb[0]) for a, sa, b, sb in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, (a, sa, b, sb) in enumerate(sets):
+            got[i].append(ops.fp8_matmul(a, sa, b[0], sb[0], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+# ---------------------------------------------------------------------------------------- refusals
+P = 1 << 20  # a pointer that is never followed: every call below is refused on the host, or has no rows
+
+
+@pytest.fixture(scope="module")
+def lib(ops):
+    from sparse_moe_layer_gate_gb300 import binding
+    return binding.lib()
+
+
+BEFORE = dict(x=P, x_stride=64, x_dtype=1, weight=P, par=0, n=4, h=64, eps=1e-6, out=P, out_stride=64, out_dtype=1, stream=None)
+AFTER = dict(block=P, block_stride=64, dtype=1, res=P, res_stride=64, res_dtype=0, weight=P, gate=None, gate_stride=0,
+             kind=0, sig=0, scale=None, number=1.0, nw=None, par=0, n=4, h=64, eps=1e-6, out=P, out_stride=64, nout=None,
+             nstride=0, stream=None)
+QUANT = dict(x=P, x_stride=256, dtype=1, rows=None, n=4, src=4, cols=256, swiglu=0, q=P, s=P, stream=None)
+WEIGHT = dict(w=P, dtype=1, mats=1, n=128, k=128, q=P, s=P, stream=None)
+MATMUL = dict(a=P, sa=P, b=P, sb=P, offsets=None, groups=1, m=4, n=64, k=128, y=P, stride=64, out=1, stream=None)
+
+
+def _refusals():
+    f = math.inf
+    for kw in (dict(n=-1), dict(h=0), dict(h=(1 << 20) + 1), dict(x_dtype=2), dict(par=-1), dict(out_dtype=5),
+               dict(eps=-1.0), dict(eps=f), dict(eps=math.nan), dict(x=None), dict(weight=None), dict(out=None),
+               dict(x=P + 1), dict(weight=P + 2), dict(x_stride=63), dict(out_stride=0)):
+        yield "epoch_norm_before", BEFORE, kw
+    for kw in (dict(n=-1), dict(h=0), dict(dtype=3), dict(res_dtype=3), dict(par=3), dict(kind=3), dict(kind=-1),
+               dict(kind=1), dict(kind=2), dict(kind=2, gate=P, gate_stride=63), dict(block=None), dict(res=None),
+               dict(out=None), dict(nw=P), dict(nout=P, nstride=64), dict(nw=P, nout=P, nstride=1),
+               dict(block_stride=1), dict(res_stride=1), dict(out_stride=1), dict(res=P + 2), dict(eps=math.nan),
+               dict(scale=P + 1), dict(nw=P + 1, nout=P, nstride=64)):
+        yield "epoch_norm_after", AFTER, kw
+    for kw in (dict(n=-1, src=-1), dict(src=3), dict(cols=0), dict(dtype=7), dict(x=None), dict(x=P + 1), dict(q=None),
+               dict(s=None), dict(s=P + 2), dict(x_stride=255), dict(swiglu=1), dict(rows=P + 2),
+               dict(n=1 << 30, src=1 << 30, cols=512)):
+        yield "epoch_fp8_quantize", QUANT, kw
+    for kw in (dict(dtype=2), dict(mats=-1), dict(mats=65536), dict(n=0), dict(k=0), dict(n=(1 << 22) + 1), dict(w=None),
+               dict(q=None), dict(s=None), dict(w=P + 1)):
+        yield "epoch_fp8_quantize_weight", WEIGHT, kw
+    for kw in (dict(m=-1), dict(n=0), dict(k=0), dict(k=8), dict(k=136), dict(groups=0), dict(groups=2),
+               dict(groups=1025, offsets=P), dict(offsets=P + 2), dict(groups=1024, offsets=P, n=1 << 22), dict(a=None),
+               dict(a=P + 8), dict(b=P + 4), dict(b=None), dict(sa=None), dict(sb=P + 2), dict(y=None), dict(y=P + 1),
+               dict(stride=63), dict(out=2)):
+        yield "epoch_fp8_matmul", MATMUL, kw
+
+
+@pytest.mark.parametrize("name,base,change", list(_refusals()), ids=lambda v: str(v)[:60] if not isinstance(v, dict) else "")
+def test_refused_on_the_host(lib, name, base, change):
+    assert set(change) <= set(base)
+    assert getattr(lib, name)(*{**base, **change}.values()) == 1  # EPOCH_EINVAL, nothing enqueued
+
+
+def test_no_rows_enqueue_nothing(lib):
+    for name, base, kw in (("epoch_norm_before", BEFORE, dict(n=0, x=None, out=None)),
+                           ("epoch_norm_after", AFTER, dict(n=0, block=None, res=None, out=None)),
+                           ("epoch_fp8_quantize", QUANT, dict(n=0, src=0, x=None, q=None, s=None)),
+                           ("epoch_fp8_quantize_weight", WEIGHT, dict(mats=0, w=None)),
+                           ("epoch_fp8_matmul", MATMUL, dict(m=0, a=None, y=None))):
+        assert getattr(lib, name)(*{**base, **kw}.values()) == 0
+
+
+def test_cpu_tensors_are_refused(ops):
+    x = torch.zeros(2, 64)
+    for call in (lambda: ops.norm_before(x, x[0]), lambda: ops.norm_after(x, x, x[0]), lambda: ops.fp8_quantize(x),
+                 lambda: ops.fp8_quantize_weight(x), lambda: ops.fp8_matmul(x.to(E4M3), x, x.to(E4M3), x)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.gpu
+def test_tensors_are_checked(ops):
+    c = dict(device="cuda")
+    x, w = torch.zeros(4, 64, **c), torch.zeros(64, **c)
+    q, s = ops.fp8_quantize(torch.zeros(4, 128, **c))
+    b, sb = ops.fp8_quantize_weight(torch.zeros(64, 128, **c))
+    off = torch.zeros(3, dtype=torch.int32, **c)
+    for call in (lambda: ops.norm_before(x.half(), w), lambda: ops.norm_before(x, w[:63]), lambda: ops.norm_before(x, w.cpu()),
+                 lambda: ops.norm_before(x.T, w[:4]), lambda: ops.norm_before(x, w, out=x[:3]),
+                 lambda: ops.norm_before(x[0].expand(4, 64), w), lambda: ops.norm_before(x, w, eps=-1.0),
+                 lambda: ops.norm_before(x, w, out=x, out_dtype=BF16), lambda: ops.norm_after(x, x[:3], w),
+                 lambda: ops.norm_after(x, x, w, gate=x.to(BF16)), lambda: ops.norm_after(x, x, w, gate_sigmoid=True),
+                 lambda: ops.norm_after(x, x, w, next_weight=w.to(BF16)), lambda: ops.norm_after(x, x, w, next_out=x),
+                 lambda: ops.norm_after(x, x, w, out=x.to(BF16)), lambda: ops.fp8_quantize(x[:, :63], swiglu=True),
+                 lambda: ops.fp8_quantize(x, rows=torch.zeros(2, dtype=torch.int64, **c)),
+                 lambda: ops.fp8_quantize(x, q=torch.zeros(4, 64, **c)), lambda: ops.fp8_quantize_weight(x.T),
+                 lambda: ops.fp8_matmul(q, s, b[:, :64], sb), lambda: ops.fp8_matmul(q, s[:, :0], b, sb),
+                 lambda: ops.fp8_matmul(q, s, b[None], sb[None], offsets=off), lambda: ops.fp8_matmul(q, s, b, sb, offsets=off),
+                 lambda: ops.fp8_matmul(q, s, b, sb, out_dtype=torch.float16)):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
