@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSplit = 4;    // warps of a group in phases 1 and 2
 constexpr int kSteps = 4;    // K steps (64 bytes of a row) loaded together
 constexpr int kMaxEdges = kFewTokens * 16;
 
@@ -78,76 +77,87 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Barrier of the `warps` warps of group `id` (hardware barrier id + 1).
+// Barrier of the `warps` warps of group `id` (hardware barrier id + 1 where there is more than one).
 __device__ __forceinline__ void group_sync(int id, int warps) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
+  if (warps == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
 }
 
-// Grid barrier: every CTA arrives once on *ctr (zero before the launch's first
-// arrival) and waits until all have. False when the bounded wait gives up.
-__device__ bool grid_barrier(int32_t *ctr, uint32_t *err, int64_t timeout_ns) {
-  __shared__ int s_ok;
+// Grid barrier in two halves. Every CTA arrives once on *ctr (zero before the
+// launch's first arrival); the wait ends when all have, or gives up (false).
+// Loads issued between the halves do not hold the arrival back.
+__device__ __forceinline__ void grid_arrive(int32_t *ctr) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(ctr, 1);
+  }
+}
+__device__ bool grid_wait(const int32_t *ctr, uint32_t *err, int64_t timeout_ns) {
+  __shared__ int s_ok;
+  if (threadIdx.x == 0) {
     const int32_t want = static_cast<int32_t>(gridDim.x);
-    const volatile int32_t *seen = ctr;
-    s_ok = 1;
-    if (*seen < want) {
+    auto seen = [&] {
+      int32_t v;
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+      return v;
+    };
+    int ok = 1;
+    if (seen() < want) {
       const uint64_t t0 = globaltimer_ns();
-      for (uint32_t i = 1; *seen < want; ++i)
+      for (uint32_t i = 1; seen() < want; ++i)
         if ((i & 63u) == 0u && globaltimer_ns() - t0 > static_cast<uint64_t>(timeout_ns)) {
           set_error(err, EPOCH_DEVERR_TIMEOUT);
-          s_ok = 0;
+          ok = 0;
           break;
         }
     }
-    __threadfence();
+    s_ok = ok;
   }
   __syncthreads();
   return s_ok != 0;
 }
 
 // Sixteen weight rows of one unit, as this thread sees them: its columns of rows
-// g and g + 8 (row index in bounds or not), and its warp's K steps.
+// g and g + 8 (rows behind the last one read it again: their sums go nowhere),
+// and its warp's K steps, a whole number of chunks.
 struct WeightRows {
   const char *p0, *p1;
-  bool ok0, ok1;
   int step, end, k;  // K steps of this warp, columns of a row
 };
 
+// Whether columns of a K step that a thread holds exist: rows of bf16 layers are
+// a whole number of chunks.
+template <typename T> __device__ __forceinline__ bool in_row(int c, int k) { return sizeof(T) == 2 || c < k; }
+
 template <typename T>
 __device__ __forceinline__ void load_chunk(const WeightRows &w, int step, uint4 (&a)[kSteps], uint4 (&b)[kSteps]) {
-  const int t = lane_id() & 3;
+  const int c0 = step * Elem<T>::step, ct = c0 + (lane_id() & 3) * Elem<T>::per;
+  const char *p0 = w.p0 + static_cast<int64_t>(c0) * sizeof(T), *p1 = w.p1 + static_cast<int64_t>(c0) * sizeof(T);
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
-    const int64_t c = static_cast<int64_t>(step + j) * Elem<T>::step;
-    const bool in = step + j < w.end && c + t * Elem<T>::per < w.k;
-    a[j] = load_weights(w.p0 + c * sizeof(T), in && w.ok0);
-    b[j] = load_weights(w.p1 + c * sizeof(T), in && w.ok1);
+    const bool in = in_row<T>(ct + j * Elem<T>::step, w.k);
+    a[j] = load_weights(p0 + 64 * j, in);
+    b[j] = load_weights(p1 + 64 * j, in);
   }
 }
 
 // Adds the products of a loaded chunk with tokens' rows to the sums: rows[i] is
-// where the row of this thread's token of tile i starts in x, negative behind the
-// last token.
+// where the row of this thread's token of tile i starts in x (tiles behind the
+// last token repeat one: every token is a column of its own).
 template <typename T, int NT, bool FRESH>
-__device__ __forceinline__ void add_chunk(const WeightRows &w, int step, const uint4 (&a)[kSteps],
-                                          const uint4 (&b)[kSteps], const T *x, const int (&rows)[NT], int tiles,
+__device__ __forceinline__ void add_chunk(int step, int k, const uint4 (&a)[kSteps], const uint4 (&b)[kSteps],
+                                          const T *x, const int (&rows)[NT], int tiles,
                                           float (&acc)[NT][Elem<T>::acc]) {
-  const int lane = lane_id(), t = lane & 3;
+  const int c0 = step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if (i >= tiles) break;
+      const T *row = x + rows[i] + c0;
       uint4 v[kSteps];
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const int c = (step + j) * Elem<T>::step + t * Elem<T>::per;
-        v[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (rows[i] >= 0 && step + j < w.end && c < w.k) v[j] = load_tokens<FRESH>(x + rows[i] + c);
-      }
+      for (int j = 0; j < kSteps; ++j) v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
         mma_bf16(acc[i], a[j].x, b[j].x, a[j].y, b[j].y, v[j].x, v[j].y);
@@ -160,16 +170,18 @@ __device__ __forceinline__ void add_chunk(const WeightRows &w, int step, const u
       if (i >= tiles) break;
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        const int row = __shfl_sync(0xffffffffu, rows[i], 4 * n);  // token n of the tile
-        if (row < 0) break;
+        const T *row = x + __shfl_sync(0xffffffffu, rows[i], 4 * n) + c0;  // token n of the tile
+        uint4 v[kSteps];
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-          const int c = (step + j) * Elem<T>::step + t * Elem<T>::per;
-          if (step + j >= w.end || c >= w.k) continue;
-          const uint4 u = load_tokens<FRESH>(x + row + c);
-          const float v0 = __uint_as_float(u.x), v1 = __uint_as_float(u.y), v2 = __uint_as_float(u.z),
-                      v3 = __uint_as_float(u.w);
-          float s = acc[i][n], q = acc[i][8 + n];
+          v[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (in_row<T>(c0 + j * Elem<T>::step, k)) v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
+        }
+        float s = acc[i][n], q = acc[i][8 + n];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const float v0 = __uint_as_float(v[j].x), v1 = __uint_as_float(v[j].y), v2 = __uint_as_float(v[j].z),
+                      v3 = __uint_as_float(v[j].w);
           s = fmaf(__uint_as_float(a[j].x), v0, s);
           s = fmaf(__uint_as_float(a[j].y), v1, s);
           s = fmaf(__uint_as_float(a[j].z), v2, s);
@@ -178,9 +190,9 @@ __device__ __forceinline__ void add_chunk(const WeightRows &w, int step, const u
           q = fmaf(__uint_as_float(b[j].y), v1, q);
           q = fmaf(__uint_as_float(b[j].z), v2, q);
           q = fmaf(__uint_as_float(b[j].w), v3, q);
-          acc[i][n] = s;
-          acc[i][8 + n] = q;
         }
+        acc[i][n] = s;
+        acc[i][8 + n] = q;
       }
     }
   }
@@ -213,18 +225,20 @@ template <typename T> __device__ __forceinline__ void put_tile(float *d, const f
 // tokens than NT tiles hold streams its weights once for each 8 NT tokens (the
 // later times from L2). Partial sums meet in `part` ([2][warps][NT][128],
 // alternating halves, so one group barrier each), from which `finish` takes
-// them. The next unit's first weights are in flight before the sums of the
-// present one meet. `ready` runs once, after the first loads are issued: the
-// grid barrier before the phase, if any.
+// them. Two chunks of weights are always on their way: a chunk's registers are
+// loaded again, with the unit's next columns or the next unit's first, as soon
+// as its products are issued. `ready` runs once, after the first loads are
+// issued: the wait for the grid barrier before the phase, if any.
 template <typename T, int NT, bool FRESH, typename Weights, typename Tokens, typename Finish, typename Ready>
 __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, int warps, int gid, float *part,
                                           const T *x, Weights weights, Tokens tokens, Finish finish, Ready ready) {
-  uint4 a[kSteps], b[kSteps], na[kSteps], nb[kSteps];
-  WeightRows cur, nxt;
+  uint4 a0[kSteps], b0[kSteps], a1[kSteps], b1[kSteps];
+  WeightRows cur;
   int u = first, tok0 = 0;
   if (u < n) {
     weights(u, w, warps, cur);
-    load_chunk<T>(cur, cur.step, a, b);
+    if (cur.step < cur.end) load_chunk<T>(cur, cur.step, a0, b0);
+    if (cur.step + kSteps < cur.end) load_chunk<T>(cur, cur.step + kSteps, a1, b1);
   }
   if (!ready()) return false;
   int half = 0;
@@ -239,23 +253,22 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
       for (int j = 0; j < Elem<T>::acc; ++j) acc[i][j] = 0.f;
     const bool last = left <= 8 * NT;
     const int un = last ? u + stride : u;
+    const int end = cur.end;
     int step = cur.step;
     do {
-      const int ns = step + kSteps;
-      if (ns < cur.end) {
-        load_chunk<T>(cur, ns, na, nb);
-      } else if (un < n) {
-        weights(un, w, warps, nxt);
-        load_chunk<T>(nxt, nxt.step, na, nb);
-      }
-      add_chunk<T, NT, FRESH>(cur, step, a, b, x, rows, tiles, acc);
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        a[j] = na[j];
-        b[j] = nb[j];
-      }
+      int ns = step + 2 * kSteps;  // what the registers hold next
+      const int s1 = step + kSteps, k0 = cur.k;
+      if (step < end) add_chunk<T, NT, FRESH>(step, k0, a0, b0, x, rows, tiles, acc);
       step = ns;
-    } while (step < cur.end);
+      if (ns >= end) {
+        cur.end = 0;  // nothing left to load
+        if (un < n) weights(un, w, warps, cur);
+        ns = cur.step;
+      }
+      if (ns < cur.end) load_chunk<T>(cur, ns, a0, b0);
+      if (s1 < end) add_chunk<T, NT, FRESH>(s1, k0, a1, b1, x, rows, tiles, acc);
+      if (ns + kSteps < cur.end) load_chunk<T>(cur, ns + kSteps, a1, b1);
+    } while (step < end);
     float *mine = part + (static_cast<size_t>(half) * warps) * (NT * 128);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -263,12 +276,15 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
     group_sync(gid, warps);
     finish(u, tok0, min(left, 8 * NT), last, mine);
     half ^= 1;
-    cur = nxt;
     u = un;
     tok0 = last ? 0 : tok0 + 8 * NT;
   }
   return true;
 }
+
+// Warps of a group in phases 1 and 2, for rows of `chunks` chunks: at most four,
+// and no more than leave each of them the two chunks it keeps in flight.
+__device__ __forceinline__ int split_of(int chunks) { return chunks >= 8 ? 4 : chunks >= 4 ? 2 : 1; }
 
 struct FewParams {
   Dims d;
@@ -284,101 +300,116 @@ struct FewParams {
 struct Routes {
   int16_t sel[kMaxEdges];   // expert of edge t * k + j
   float wgt[kMaxEdges];     // its weight
-  int16_t list[kMaxEdges];  // edges by expert
+  int16_t list[kMaxEdges];  // edges by expert,
+  int16_t tok[kMaxEdges];   // and their tokens
   int16_t rank[kMaxEdges];
   int32_t first[1025];      // first entry of each hit expert in list
   int16_t hit[1024];        // hit experts, ascending
   int32_t cnt[1024];
+  int32_t warp_sum[kWarps];
   int32_t n_hit;
 };
 
 // Top-k of token t by one warp, by the layer's router rule over every expert
-// (see epoch_layer_config), from the logits row in global memory. `key` is E
-// words of shared memory of this warp. Lane l owns the consecutive experts
-// [l * per, (l + 1) * per): the lowest lane of equal keys holds the lowest id.
-__device__ void select_token(const FewParams &p, int t, unsigned *key, Routes &r) {
+// (see epoch_layer_config), from the logits row in global memory. Lane l owns the
+// EPL consecutive experts [l * EPL, (l + 1) * EPL): among equal keys the lowest
+// lane holds the lowest id. Each of the k rounds takes the largest of the lanes'
+// best keys. `key` is E words of shared memory of this warp (group rule only).
+template <int EPL> __device__ __noinline__ void select_token(const FewParams &p, int t, unsigned *key_s, Routes &r) {
   constexpr unsigned kAll = 0xffffffffu;
   const Dims &d = p.d;
-  const int lane = lane_id(), E = d.E, k = d.k;
+  const int lane = lane_id(), E = d.E, k = d.k, lo = lane * EPL;
   const float *row = p.ws.logits + static_cast<size_t>(t) * E;
-  float top = -INFINITY;
-  for (int e = lane; e < E; e += 32) {
-    const float v = __ldcg(row + e);
-    top = fmaxf(top, v);
-    key[e] = order_key(d.router == 0 ? v : 1.f / (1.f + expf(-v)) + p.w.b_router[e]);
-  }
-  __syncwarp();
-  if (d.router != 0 && d.topk_group < d.n_group) {
-    // groups ranked by the sum of their two best scores; the first topk_group, and further ones while
-    // they hold fewer than k experts, stay
-    const int gs = E / d.n_group;
-    float score = -INFINITY;
-    for (int g = 0; g < d.n_group; ++g) {
-      unsigned k1 = 0u, k2 = 0u;
-      for (int e = lane; e < gs; e += 32) {
-        const unsigned q = key[g * gs + e];
-        if (q > k1) {
-          k2 = k1;
-          k1 = q;
-        } else if (q > k2) {
-          k2 = q;
+  float v[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) v[j] = lo + j < E ? __ldcg(row + lo + j) : -INFINITY;
+  unsigned key[EPL];  // 0: not eligible, or taken
+  if (d.router == 0) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = lo + j < E ? order_key(v[j]) : 0u;
+  } else {
+    float b[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) b[j] = lo + j < E ? __ldg(p.w.b_router + lo + j) : 0.f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = lo + j < E ? order_key(1.f / (1.f + expf(-v[j])) + b[j]) : 0u;
+    if (d.topk_group < d.n_group) {
+      // groups ranked by the sum of their two best scores; the first topk_group, and further ones while
+      // they hold fewer than k experts, stay
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (lo + j < E) key_s[lo + j] = key[j];
+      __syncwarp();
+      const int gs = E / d.n_group;
+      float score = -INFINITY;
+      for (int g = 0; g < d.n_group; ++g) {
+        unsigned k1 = 0u, k2 = 0u;
+        for (int e = lane; e < gs; e += 32) {
+          const unsigned q = key_s[g * gs + e];
+          if (q > k1) {
+            k2 = k1;
+            k1 = q;
+          } else if (q > k2) {
+            k2 = q;
+          }
         }
+        const unsigned m1 = __reduce_max_sync(kAll, k1);
+        const int win = __ffs(__ballot_sync(kAll, k1 == m1)) - 1;
+        const unsigned m2 = __reduce_max_sync(kAll, lane == win ? k2 : k1);
+        if (lane == g) score = m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
       }
-      const unsigned m1 = __reduce_max_sync(kAll, k1);
-      const int win = __ffs(__ballot_sync(kAll, k1 == m1)) - 1;
-      const unsigned m2 = __reduce_max_sync(kAll, lane == win ? k2 : k1);
-      if (lane == g) score = m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
+      int rank = 0;
+      for (int i = 0; i < d.n_group; ++i) {
+        const float o = __shfl_sync(kAll, score, i);
+        rank += o > score || (o == score && i < lane);
+      }
+      const unsigned open = __ballot_sync(kAll, lane < d.n_group && (rank < d.topk_group || rank * gs < k));
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (lo + j < E && !((open >> ((lo + j) / gs)) & 1u)) key[j] = 0u;
     }
-    int rank = 0;
-    for (int i = 0; i < d.n_group; ++i) {
-      const float o = __shfl_sync(kAll, score, i);
-      rank += o > score || (o == score && i < lane);
-    }
-    const unsigned open = __ballot_sync(kAll, lane < d.n_group && (rank < d.topk_group || rank * gs < k));
-    for (int e = lane; e < E; e += 32)
-      if (!((open >> (e / gs)) & 1u)) key[e] = 0u;
-    __syncwarp();
   }
-  const int per = (E + 31) / 32, lo = lane * per, hi = min(lo + per, E);
-  unsigned best = 0u;
-  int at = lo;
-  for (int e = lo; e < hi; ++e)
-    if (key[e] > best) {
-      best = key[e];
-      at = e;
+  unsigned best = key[0];
+  int at = 0;
+#pragma unroll
+  for (int j = 1; j < EPL; ++j)
+    if (key[j] > best) {
+      best = key[j];
+      at = j;
     }
   int sel = 0;
   float val = -INFINITY;
-  for (int j = 0; j < k; ++j) {
+  for (int i = 0; i < k; ++i) {
     const unsigned m = __reduce_max_sync(kAll, best);
     const int win = __ffs(__ballot_sync(kAll, best == m)) - 1;
-    const int e = __shfl_sync(kAll, at, win);
-    if (lane == j) {
+    const int e = __shfl_sync(kAll, lo + at, win);
+    if (lane == i) {
       sel = e;
       val = key_value(m);
     }
     if (lane == win) {
-      key[at] = 0u;
-      best = 0u;
-      for (int q = lo; q < hi; ++q)
-        if (key[q] > best) {
-          best = key[q];
-          at = q;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (j == at) key[j] = 0u;
+      best = key[0];
+      at = 0;
+#pragma unroll
+      for (int j = 1; j < EPL; ++j)
+        if (key[j] > best) {
+          best = key[j];
+          at = j;
         }
     }
   }
   float num, den = 0.f;
   if (d.router == 0) {
-    const float ref = d.raw_weights ? 0.f : __shfl_sync(kAll, val, 0);
+    const float top = __shfl_sync(kAll, val, 0);  // the row's largest logit: every expert is eligible
+    num = lane < k ? expf(val - top) : 0.f;
     if (d.raw_weights) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      for (int e = lane; e < E; e += 32) den += expf(__ldcg(row + e) - top);
+      for (int j = 0; j < EPL; ++j) den += lo + j < E ? expf(v[j] - top) : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kAll, den, o);
-      num = expf(val - top);
-    } else {
-      num = lane < k ? expf(val - ref) : 0.f;
     }
   } else {
     num = 1.f / (1.f + expf(-__ldcg(row + sel)));
@@ -392,55 +423,62 @@ __device__ void select_token(const FewParams &p, int t, unsigned *key, Routes &r
   }
 }
 
-// Edges sorted by expert, from the selections (all threads). The order of an
-// expert's edges does not matter: each is a column of its own everywhere.
+// Edges sorted by expert, from the selections (all threads; r.cnt is zero). The
+// order of an expert's edges does not matter: each is a column of its own everywhere.
 __device__ void build_routes(const FewParams &p, Routes &r) {
-  const int E = p.d.E, edges = p.n_tok * p.d.k;
-  for (int e = threadIdx.x; e < E; e += kThreads) r.cnt[e] = 0;
-  __syncthreads();
+  const int E = p.d.E, k = p.d.k, edges = p.n_tok * k, lane = lane_id(), warp = warp_id();
   for (int i = threadIdx.x; i < edges; i += kThreads) r.rank[i] = static_cast<int16_t>(atomicAdd(&r.cnt[r.sel[i]], 1));
   __syncthreads();
-  if (warp_id() == 0) {
-    const int lane = lane_id(), per = (E + 31) / 32, lo = lane * per, hi = min(lo + per, E);
-    int n = 0, h = 0;
-    for (int e = lo; e < hi; ++e) {
-      n += r.cnt[e];
-      h += r.cnt[e] > 0;
-    }
-    int sn = n, sh = h;
+  // thread i holds experts 2 i and 2 i + 1; running sums of (hit experts << 16 | edges)
+  static_assert(2 * kThreads >= 1024, "two experts a thread");
+  const int e0 = 2 * threadIdx.x;
+  const int c0 = e0 < E ? r.cnt[e0] : 0, c1 = e0 + 1 < E ? r.cnt[e0 + 1] : 0;
+  const int own = ((c0 > 0) + (c1 > 0)) << 16 | (c0 + c1);
+  int sum = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int yn = __shfl_up_sync(0xffffffffu, sn, o), yh = __shfl_up_sync(0xffffffffu, sh, o);
-      if (lane >= o) {
-        sn += yn;
-        sh += yh;
-      }
-    }
-    if (lane == 31) {
-      r.n_hit = sh;
-      r.first[sh] = sn;
-    }
-    sn -= n;
-    sh -= h;
-    for (int e = lo; e < hi; ++e) {
-      const int c = r.cnt[e];
-      if (c > 0) {
-        r.first[sh] = sn;
-        r.hit[sh++] = static_cast<int16_t>(e);
-      }
-      r.cnt[e] = sn;  // now the expert's first entry
-      sn += c;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) r.warp_sum[warp] = sum;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const int y = r.warp_sum[i];
+    before += i < warp ? y : 0;
+    all += y;
+  }
+  sum += before - own;
+  int hit = sum >> 16, at = sum & 0xFFFF;
+  if (c0 > 0) {
+    r.first[hit] = at;
+    r.hit[hit++] = static_cast<int16_t>(e0);
+    r.cnt[e0] = at;  // now the expert's first entry
+    at += c0;
+  }
+  if (c1 > 0) {
+    r.first[hit] = at;
+    r.hit[hit] = static_cast<int16_t>(e0 + 1);
+    r.cnt[e0 + 1] = at;
+  }
+  if (threadIdx.x == 0) {
+    r.n_hit = all >> 16;
+    r.first[all >> 16] = edges;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < edges; i += kThreads) r.list[r.cnt[r.sel[i]] + r.rank[i]] = static_cast<int16_t>(i);
+  for (int i = threadIdx.x; i < edges; i += kThreads) {
+    const int q = r.cnt[r.sel[i]] + r.rank[i];
+    r.list[q] = static_cast<int16_t>(i);
+    r.tok[q] = static_cast<int16_t>(i / k);
+  }
   __syncthreads();
 }
 
 template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const __grid_constant__ FewParams p) {
   extern __shared__ float part[];  // partial sums of the units; the selection's keys between the phases
   __shared__ Routes r;
-  __shared__ int s_last[kWarps / kSplit];
+  __shared__ int s_last[kWarps];
   const Dims &d = p.d;
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const int H = d.H, I = d.I, E = d.E, k = d.k, nt = p.n_tok;
@@ -450,10 +488,10 @@ template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_m
   const int act_sh = p.n_tok * k * I;      // of shared expert s and token t at act_sh + (s * n_tok + t) * I_s
 
   auto split = [&](WeightRows &o, int cols, int w, int warps) {
-    const int steps = (cols + step - 1) / step;
+    const int chunks = (cols + step * kSteps - 1) / (step * kSteps);
     o.k = cols;
-    o.step = steps * w / warps;
-    o.end = steps * (w + 1) / warps;
+    o.step = chunks * w / warps * kSteps;
+    o.end = chunks * (w + 1) / warps * kSteps;
   };
   auto sum = [&](const float *mine, int warps, int tok, int row) {
     float s = 0.f;
@@ -462,141 +500,156 @@ template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_m
     return s;
   };
 
-  // phase 0: router tiles of 8 experts, then shared tiles of 8 activation columns
-  const int n_router = (E + 7) / 8, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
+  // phase 0: router tiles of 16 experts, then shared tiles of 8 activation columns
+  const int n_router = (E + 15) / 16, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[1] = 0;  // no CTA reaches the second barrier before this one passes the first
+  if (threadIdx.x < 16 && blockIdx.x * 16 + threadIdx.x < E)  // the bias of this CTA's experts, needed at the end of the tile
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.b_router + blockIdx.x * 16 + threadIdx.x));
   run_units<T, NT, false>(
       blockIdx.x, gridDim.x, n_router + d.n_sh * sh8, warp, kWarps, 0, part, x,
-      [&](int u, int w, int warps, WeightRows &o) {
-        split(o, H, w, warps);
+      [&](int u, int wi, int warps, WeightRows &o) {
+        split(o, H, wi, warps);
         if (u < n_router) {
-          const int e = u * 8 + g;
-          o.ok0 = e < E;
-          o.ok1 = false;
-          o.p0 = o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_router) + static_cast<int64_t>(e) * H + t * per);
+          const T *base = static_cast<const T *>(p.w.w_router) + t * per;
+          o.p0 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(u * 16 + g, E - 1)) * H);
+          o.p1 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(u * 16 + g + 8, E - 1)) * H);
         } else {
-          const int s = (u - n_router) / sh8, c = (u - n_router - s * sh8) * 8 + g;
+          const int s = (u - n_router) / sh8, c = min((u - n_router - s * sh8) * 8 + g, d.I_s - 1);
           const int64_t at = (static_cast<int64_t>(s) * d.I_s + c) * H + t * per;
-          o.ok0 = o.ok1 = c < d.I_s;
           o.p0 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.ws_gate) + at);
           o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.ws_up) + at);
         }
       },
       [&](int, int tok0, int (&rows)[NT]) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) rows[i] = tok0 + 8 * i + g < nt ? (tok0 + 8 * i + g) * H : -1;
+        for (int i = 0; i < NT; ++i) rows[i] = min(tok0 + 8 * i + g, nt - 1) * H;
         return nt - tok0;
       },
       [&](int u, int tok0, int count, bool, const float *mine) {
-        for (int v = threadIdx.x; v < count * 8; v += kThreads) {
-          const int tok = v >> 3, c = v & 7;
-          if (u < n_router) {
-            const int e = u * 8 + c;
+        if (u < n_router) {
+          for (int v = threadIdx.x; v < count * 16; v += kThreads) {
+            const int tok = v >> 4, e = u * 16 + (v & 15);
             if (e < E)
               p.ws.logits[static_cast<size_t>(tok0 + tok) * E + e] =
-                  sum(mine, kWarps, tok, c) + (d.router == 0 ? p.w.b_router[e] : 0.f);
-          } else {
-            const int s = (u - n_router) / sh8, col = (u - n_router - s * sh8) * 8 + c;
-            if (col < d.I_s)
-              act[act_sh + (s * nt + tok0 + tok) * d.I_s + col] =
-                  from_f32<T>(silu(sum(mine, kWarps, tok, c)) * sum(mine, kWarps, tok, c + 8));
+                  (d.router == 0 ? __ldg(p.w.b_router + e) : 0.f) + sum(mine, kWarps, tok, v & 15);
           }
+          return;
+        }
+        const int s = (u - n_router) / sh8, col0 = (u - n_router - s * sh8) * 8;
+        for (int v = threadIdx.x; v < count * 8; v += kThreads) {
+          const int tok = v >> 3, c = v & 7;
+          if (col0 + c < d.I_s)
+            act[act_sh + (s * nt + tok0 + tok) * d.I_s + col0 + c] =
+                from_f32<T>(silu(sum(mine, kWarps, tok, c)) * sum(mine, kWarps, tok, c + 8));
         }
       },
       [] { return true; });
-  if (!grid_barrier(p.ws.ctr, p.err, d.timeout_ns)) return;
+  grid_arrive(p.ws.ctr);
+  for (int e = threadIdx.x; e < E; e += kThreads) r.cnt[e] = 0;
+  if (!grid_wait(p.ws.ctr, p.err, d.timeout_ns)) return;
 
-  for (int tok = warp; tok < nt; tok += kWarps) select_token(p, tok, reinterpret_cast<unsigned *>(part) + warp * E, r);
+  for (int tok = warp; tok < nt; tok += kWarps) {
+    unsigned *key = reinterpret_cast<unsigned *>(part) + warp * E;
+    if (E <= 256) select_token<8>(p, tok, key, r);
+    else select_token<32>(p, tok, key, r);
+  }
   __syncthreads();
   build_routes(p, r);
 
-  const int grp = warp / kSplit, w = warp % kSplit;
-  const int first = grp * gridDim.x + blockIdx.x, stride = gridDim.x * (kWarps / kSplit);  // SMs first
-  float *gpart = part + static_cast<size_t>(grp) * 2 * kSplit * NT * 128;
-  const int gthread = threadIdx.x - grp * kSplit * 32;
-
   // phase 1: routed activations, 8 columns of an expert a unit
   const int i8 = (I + 7) / 8;
+  int warps = split_of(H / (step * kSteps)), grp = warp / warps, w = warp % warps;
+  int gthread = threadIdx.x - grp * warps * 32;
   run_units<T, NT, false>(
-      first, stride, r.n_hit * i8, w, kSplit, grp, gpart, x,
-      [&](int u, int wi, int warps, WeightRows &o) {
-        const int h = u / i8, c = (u - h * i8) * 8 + g;
+      grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), r.n_hit * i8, w, warps, grp,
+      part + static_cast<size_t>(grp) * 2 * warps * NT * 128, x,
+      [&](int u, int wi, int ws, WeightRows &o) {
+        const int h = u / i8, c = min((u - h * i8) * 8 + g, I - 1);
         const int64_t at = (static_cast<int64_t>(r.hit[h]) * I + c) * H + t * per;
-        split(o, H, wi, warps);
-        o.ok0 = o.ok1 = c < I;
+        split(o, H, wi, ws);
         o.p0 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_gate) + at);
         o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_up) + at);
       },
       [&](int u, int tok0, int (&rows)[NT]) {
         const int h = u / i8, f = r.first[h] + tok0, n = r.first[h + 1] - f;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) rows[i] = 8 * i + g < n ? r.list[f + 8 * i + g] / k * H : -1;
+        for (int i = 0; i < NT; ++i) rows[i] = r.tok[f + min(8 * i + g, n - 1)] * H;
         return n;
       },
       [&](int u, int tok0, int count, bool, const float *mine) {
         const int h = u / i8, f = r.first[h] + tok0;
-        for (int v = gthread; v < count * 8; v += kSplit * 32) {
+        for (int v = gthread; v < count * 8; v += warps * 32) {
           const int tok = v >> 3, c = v & 7, col = (u - h * i8) * 8 + c;
           if (col < I)
-            act[r.list[f + tok] * I + col] = from_f32<T>(silu(sum(mine, kSplit, tok, c)) * sum(mine, kSplit, tok, c + 8));
+            act[r.list[f + tok] * I + col] = from_f32<T>(silu(sum(mine, warps, tok, c)) * sum(mine, warps, tok, c + 8));
         }
       },
       [] { return true; });
+  grid_arrive(p.ws.ctr + 1);
 
   // phase 2: 16 rows of H of an expert (routed, then shared) a unit; rows of
-  // the fp32 sums: edge e at row e, shared expert s and token t at n_tok * k + s * n_tok + t
-  const int h16 = (H + 15) / 16, groups = r.n_hit + d.n_sh;
+  // the fp32 sums: edge e at row e, shared expert s and token t at n_tok * k + s * n_tok + t.
+  // Groups take neighbouring experts of a row tile one after another and count a tile's experts once for the run.
+  const int h16 = (H + 15) / 16, experts = r.n_hit + d.n_sh;
+  warps = split_of(I / (step * kSteps));
+  grp = warp / warps;
+  w = warp % warps;
+  gthread = threadIdx.x - grp * warps * 32;
+  const int64_t group = grp * gridDim.x + blockIdx.x, n_groups = gridDim.x * (kWarps / warps);
+  const int lo = static_cast<int>(experts * h16 * group / n_groups);
+  const int hi = static_cast<int>(experts * h16 * (group + 1) / n_groups);
   run_units<T, NT, true>(
-      first, stride, groups * h16, w, kSplit, grp, gpart, act,
-      [&](int u, int wi, int warps, WeightRows &o) {
-        const int h = u / h16, row = (u - h * h16) * 16 + g;
+      lo, 1, hi, w, warps, grp, part + static_cast<size_t>(grp) * 2 * warps * NT * 128, act,
+      [&](int u, int wi, int ws, WeightRows &o) {
+        const int tile = u / experts, h = u - tile * experts, row = tile * 16 + g;
         const bool shared = h >= r.n_hit;
         const int cols = shared ? d.I_s : I;
-        const T *base = static_cast<const T *>(shared ? p.w.ws_down : p.w.w_down);
-        const int64_t at = (static_cast<int64_t>(shared ? h - r.n_hit : r.hit[h]) * H + row) * cols + t * per;
-        split(o, cols, wi, warps);
-        o.ok0 = row < H;
-        o.ok1 = row + 8 < H;
-        o.p0 = reinterpret_cast<const char *>(base + at);
-        o.p1 = reinterpret_cast<const char *>(base + at + static_cast<int64_t>(8) * cols);
+        const T *base = static_cast<const T *>(shared ? p.w.ws_down : p.w.w_down) +
+                        static_cast<int64_t>(shared ? h - r.n_hit : r.hit[h]) * H * cols + t * per;
+        split(o, cols, wi, ws);
+        o.p0 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(row, H - 1)) * cols);
+        o.p1 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(row + 8, H - 1)) * cols);
       },
       [&](int u, int tok0, int (&rows)[NT]) {
-        const int h = u / h16;
+        const int h = u % experts;
         if (h >= r.n_hit) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            rows[i] = tok0 + 8 * i + g < nt ? act_sh + ((h - r.n_hit) * nt + tok0 + 8 * i + g) * d.I_s : -1;
+            rows[i] = act_sh + ((h - r.n_hit) * nt + min(tok0 + 8 * i + g, nt - 1)) * d.I_s;
           return nt - tok0;
         }
         const int f = r.first[h] + tok0, n = r.first[h + 1] - f;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) rows[i] = 8 * i + g < n ? r.list[f + 8 * i + g] * I : -1;
+        for (int i = 0; i < NT; ++i) rows[i] = r.list[f + min(8 * i + g, n - 1)] * I;
         return n;
       },
       [&](int u, int tok0, int count, bool last, const float *mine) {
-        const int h = u / h16, tile = u - h * h16;
+        const int tile = u / experts, h = u - tile * experts;
         const bool shared = h >= r.n_hit;
-        for (int v = gthread; v < count * 16; v += kSplit * 32) {
+        for (int v = gthread; v < count * 16; v += warps * 32) {
           const int tok = tok0 + (v >> 4), c = v & 15, col = tile * 16 + c;
           const int at = shared ? nt * k + (h - r.n_hit) * nt + tok : r.list[r.first[h] + tok];
-          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * H + col, sum(mine, kSplit, v >> 4, c));
+          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * H + col, sum(mine, warps, v >> 4, c));
         }
-        if (!last) return;
-        group_sync(grp, kSplit);
+        if (!last || (h < experts - 1 && u < hi - 1)) return;
+        // this group is through with the tile: the group that counts the last expert sums the edges up
+        group_sync(grp, warps);
         if (gthread == 0) {
           __threadfence();
-          const int n = atomicAdd(p.ws.ctr + 2 + tile, 1);
-          s_last[grp] = n == groups - 1;
-          if (n == groups - 1) p.ws.ctr[2 + tile] = 0;  // for the next call
+          const int mine_n = u - max(lo, tile * experts) + 1;
+          const bool all = atomicAdd(p.ws.ctr + 2 + tile, mine_n) + mine_n == experts;
+          s_last[grp] = all;
+          if (all) p.ws.ctr[2 + tile] = 0;  // for the next call
           __threadfence();
         }
-        group_sync(grp, kSplit);
+        group_sync(grp, warps);
         if (!s_last[grp]) return;
-        for (int v = gthread; v < nt * 16; v += kSplit * 32) {
+        for (int v = gthread; v < nt * 16; v += warps * 32) {
           const int tok = v >> 4, col = tile * 16 + (v & 15);
           if (col >= H) continue;
           const float *o = p.ws.out + col;
           float s = 0.f;
+#pragma unroll 4
           for (int j = 0; j < k; ++j) s = fmaf(r.wgt[tok * k + j], __ldcg(o + static_cast<size_t>(tok * k + j) * H), s);
           for (int j = 0; j < d.n_sh; ++j) s += __ldcg(o + static_cast<size_t>(nt * k + j * nt + tok) * H);
           const size_t at = static_cast<size_t>(tok) * H + col;
@@ -605,7 +658,7 @@ template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_m
         }
       },
       [&] {
-        if (!grid_barrier(p.ws.ctr + 1, p.err, d.timeout_ns)) return false;
+        if (!grid_wait(p.ws.ctr + 1, p.err, d.timeout_ns)) return false;
         if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[0] = 0;  // every CTA has left the first barrier
         return true;
       });
@@ -624,7 +677,9 @@ template <typename T, int NT> cudaError_t launch(const FewParams &p, cudaStream_
   if (!(ready.load() & bit)) {
     const int most = 2 * kWarps * NT * 128 * 4 > kWarps * 1024 * 4 ? 2 * kWarps * NT * 128 * 4 : kWarps * 1024 * 4;
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess) e = prefer_max_shared(fn);
+    // tokens' rows are read through L1, which gets what the partial sums leave
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
