@@ -154,8 +154,9 @@ size_t carve(const epoch_layer_config &c, char *base, Work *w) {
   t.few.logits = static_cast<float *>(take(F * E * 4));
   t.few.act = take(F * (k * I + nsh * Is) * act);
   t.few.out = static_cast<float *>(take(F * (k + nsh) * H * 4));
-  t.few.ctr_bytes = (2 + (H + 15) / 16) * sizeof(int32_t);
-  t.few.ctr = static_cast<int32_t *>(take(t.few.ctr_bytes));
+  t.few.sel = static_cast<int16_t *>(take(F * k * 2));
+  t.few.wgt = static_cast<float *>(take(F * k * 4));
+  t.few.ctr = static_cast<int32_t *>(take(4 * sizeof(int32_t)));
   if (w) *w = t;
   return (off + kAlign - 1) & ~(kAlign - 1);
 }
@@ -466,7 +467,7 @@ epoch_status epoch_clear_status(epoch_layer *L, epoch_stream stream) {
   // the grid barriers too: a call that timed out may leave them part-way
   return cudaMemsetAsync(L->ws.err, 0, sizeof(uint32_t), S(stream)) == cudaSuccess &&
                  cudaMemsetAsync(L->ws.gate_arrive, 0, 2 * sizeof(int32_t), S(stream)) == cudaSuccess &&
-                 cudaMemsetAsync(L->ws.few.ctr, 0, L->ws.few.ctr_bytes, S(stream)) == cudaSuccess
+                 cudaMemsetAsync(L->ws.few.ctr, 0, 4 * sizeof(int32_t), S(stream)) == cudaSuccess
              ? EPOCH_OK
              : EPOCH_ECUDA;
 }

@@ -32,10 +32,10 @@ struct FewWork {
   float *logits;   // [kFewTokens][E]
   void *act;       // activations, layer dtype: [n_tok*k][I] of the edges, then [n_sh][n_tok][I_s]
   float *out;      // [kFewTokens*(k + n_sh)][H] expert outputs
-  int32_t *ctr;    // [0], [1] arrivals at the two grid barriers, then finished expert tiles of each 16 rows
-                   // of H; all but [1] (zeroed by each call) are zero between calls, and after a timeout
-                   // once the status is cleared
-  size_t ctr_bytes;
+  int16_t *sel;    // [kFewTokens][k] selections and
+  float *wgt;      // their weights, where the CTAs share the selection out
+  int32_t *ctr;    // [4] arrivals at the grid barriers: zero between calls ([3]: zeroed by each call), and
+                   // after a timeout once the status is cleared
 };
 
 // Device pointers carved from the caller's workspace.
