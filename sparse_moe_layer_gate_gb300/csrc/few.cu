@@ -125,100 +125,100 @@ __device__ bool grid_wait(const int32_t *ctr, uint32_t *err, int64_t timeout_ns)
   return s_ok != 0;
 }
 
-// Sixteen weight rows of one unit, as this thread sees them: its columns of rows
-// g and g + 8 (rows behind the last one read it again: their sums go nowhere),
-// and its warp's K steps, a whole number of chunks.
-struct WeightRows {
+// A unit's share of one warp, as a thread sees it: its columns of weight rows g
+// and g + 8 (rows behind the last one read it again: their sums go nowhere), the
+// row of its token g (behind the last token one repeats: every token is a column
+// of its own), and the warp's K steps, a whole number of chunks.
+struct Share {
   const char *p0, *p1;
-  int step, end, k;  // K steps of this warp, columns of a row
+  int row;           // where the token's row starts
+  int count;         // tokens of the unit, at most 8
+  int step, end, k;  // K steps, columns of a row
+};
+
+template <typename T> struct Chunk {
+  uint4 a[kSteps], b[kSteps];                   // weight rows g and g + 8
+  uint4 v[sizeof(T) == 2 ? kSteps : 1];         // token row g (bf16)
 };
 
 // Whether columns of a K step that a thread holds exist: rows of bf16 layers are
 // a whole number of chunks.
 template <typename T> __device__ __forceinline__ bool in_row(int c, int k) { return sizeof(T) == 2 || c < k; }
 
-template <typename T>
-__device__ __forceinline__ void load_chunk(const WeightRows &w, int step, uint4 (&a)[kSteps], uint4 (&b)[kSteps]) {
+template <typename T> __device__ __forceinline__ void load_rows(const Share &w, int step, Chunk<T> &c) {
   const int c0 = step * Elem<T>::step, ct = c0 + (lane_id() & 3) * Elem<T>::per;
   const char *p0 = w.p0 + static_cast<int64_t>(c0) * sizeof(T), *p1 = w.p1 + static_cast<int64_t>(c0) * sizeof(T);
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     const bool in = in_row<T>(ct + j * Elem<T>::step, w.k);
-    a[j] = load_weights(p0 + 64 * j, in);
-    b[j] = load_weights(p1 + 64 * j, in);
+    c.a[j] = load_weights(p0 + 64 * j, in);
+    c.b[j] = load_weights(p1 + 64 * j, in);
+  }
+}
+template <typename T, bool FRESH>
+__device__ __forceinline__ void load_token(const Share &w, int step, const T *x, Chunk<T> &c) {
+  if constexpr (sizeof(T) == 2) {
+    const T *row = x + w.row + step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) c.v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
   }
 }
 
-// Adds the products of a loaded chunk with tokens' rows to the sums: rows[i] is
-// where the row of this thread's token of tile i starts in x (tiles behind the
-// last token repeat one: every token is a column of its own), of `count` tokens.
-template <typename T, int NT, bool FRESH>
-__device__ __forceinline__ void add_chunk(int step, int k, const uint4 (&a)[kSteps], const uint4 (&b)[kSteps],
-                                          const T *x, const int (&rows)[NT], int count,
-                                          float (&acc)[NT][Elem<T>::acc]) {
-  const int c0 = step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
+// Adds a chunk's products to the sums. The fp32 form reads the tokens' rows here,
+// two tokens' loads on their way together: a thread's sums are of every token.
+template <typename T, bool FRESH>
+__device__ __forceinline__ void add_chunk(const Share &w, int step, const Chunk<T> &c, const T *x,
+                                          float (&acc)[Elem<T>::acc]) {
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if (8 * i >= count) break;
-      const T *row = x + rows[i] + c0;
-      uint4 v[kSteps];
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        mma_bf16(acc[i], a[j].x, b[j].x, a[j].y, b[j].y, v[j].x, v[j].y);
-        mma_bf16(acc[i], a[j].z, b[j].z, a[j].w, b[j].w, v[j].z, v[j].w);
-      }
+    for (int j = 0; j < kSteps; ++j) {
+      mma_bf16(acc, c.a[j].x, c.b[j].x, c.a[j].y, c.b[j].y, c.v[j].x, c.v[j].y);
+      mma_bf16(acc, c.a[j].z, c.b[j].z, c.a[j].w, c.b[j].w, c.v[j].z, c.v[j].w);
     }
   } else {
+    const int c0 = step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int n = 0; n < 8; n += 2) {
+      if (n >= w.count) break;
+      uint4 v[2][kSteps];
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {  // two tokens' loads on their way together
-        if (8 * i + n >= count) break;
-        uint4 v[2][kSteps];
+      for (int m = 0; m < 2; ++m) {
+        const T *row = x + __shfl_sync(0xffffffffu, w.row, 4 * (n + m)) + c0;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const T *row = x + __shfl_sync(0xffffffffu, rows[i], 4 * (n + m)) + c0;  // token n + m of the tile
-#pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            v[m][j] = make_uint4(0u, 0u, 0u, 0u);
-            if (in_row<T>(c0 + j * Elem<T>::step, k)) v[m][j] = load_tokens<FRESH>(row + j * Elem<T>::step);
-          }
+        for (int j = 0; j < kSteps; ++j) {
+          v[m][j] = make_uint4(0u, 0u, 0u, 0u);
+          if (in_row<T>(c0 + j * Elem<T>::step, w.k)) v[m][j] = load_tokens<FRESH>(row + j * Elem<T>::step);
         }
+      }
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float s = acc[i][n + m], q = acc[i][8 + n + m];
+      for (int m = 0; m < 2; ++m) {
+        float s = acc[n + m], q = acc[8 + n + m];
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            const float v0 = __uint_as_float(v[m][j].x), v1 = __uint_as_float(v[m][j].y),
-                        v2 = __uint_as_float(v[m][j].z), v3 = __uint_as_float(v[m][j].w);
-            s = fmaf(__uint_as_float(a[j].x), v0, s);
-            s = fmaf(__uint_as_float(a[j].y), v1, s);
-            s = fmaf(__uint_as_float(a[j].z), v2, s);
-            s = fmaf(__uint_as_float(a[j].w), v3, s);
-            q = fmaf(__uint_as_float(b[j].x), v0, q);
-            q = fmaf(__uint_as_float(b[j].y), v1, q);
-            q = fmaf(__uint_as_float(b[j].z), v2, q);
-            q = fmaf(__uint_as_float(b[j].w), v3, q);
-          }
-          acc[i][n + m] = s;
-          acc[i][8 + n + m] = q;
+        for (int j = 0; j < kSteps; ++j) {
+          const float v0 = __uint_as_float(v[m][j].x), v1 = __uint_as_float(v[m][j].y),
+                      v2 = __uint_as_float(v[m][j].z), v3 = __uint_as_float(v[m][j].w);
+          s = fmaf(__uint_as_float(c.a[j].x), v0, s);
+          s = fmaf(__uint_as_float(c.a[j].y), v1, s);
+          s = fmaf(__uint_as_float(c.a[j].z), v2, s);
+          s = fmaf(__uint_as_float(c.a[j].w), v3, s);
+          q = fmaf(__uint_as_float(c.b[j].x), v0, q);
+          q = fmaf(__uint_as_float(c.b[j].y), v1, q);
+          q = fmaf(__uint_as_float(c.b[j].z), v2, q);
+          q = fmaf(__uint_as_float(c.b[j].w), v3, q);
         }
+        acc[n + m] = s;
+        acc[8 + n + m] = q;
       }
     }
   }
 }
 
-// A warp's sums of tile i to shared memory as [16 rows][8 tokens].
+// A warp's sums to shared memory as [16 rows][8 tokens].
 template <typename T> __device__ __forceinline__ void put_tile(float *d, const float (&acc)[Elem<T>::acc]) {
   const int lane = lane_id(), g = lane >> 2, t = lane & 3;
   if constexpr (sizeof(T) == 2) {
-    d[g * 8 + 2 * t] = acc[0];
-    d[g * 8 + 2 * t + 1] = acc[1];
-    d[(g + 8) * 8 + 2 * t] = acc[2];
-    d[(g + 8) * 8 + 2 * t + 1] = acc[3];
+    *reinterpret_cast<float2 *>(d + g * 8 + 2 * t) = make_float2(acc[0], acc[1]);
+    *reinterpret_cast<float2 *>(d + (g + 8) * 8 + 2 * t) = make_float2(acc[2], acc[3]);
   } else {
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -234,63 +234,61 @@ template <typename T> __device__ __forceinline__ void put_tile(float *d, const f
 }
 
 // Runs the units u = first, first + stride, ... < n of one phase on a group of
-// `warps` warps (this warp is number `w` of group `gid`). A unit with more
-// tokens than NT tiles hold streams its weights once for each 8 NT tokens (the
-// later times from L2). Partial sums meet in `part` ([2][warps][NT][128],
-// alternating halves, so one group barrier each), from which `finish` takes
-// them. Two chunks of weights are always on their way: a chunk's registers are
-// loaded again, with the unit's next columns or the next unit's first, as soon
-// as its products are issued. `ready` runs once, after the first loads are
-// issued: the wait for the grid barrier before the phase, if any.
-template <typename T, int NT, bool FRESH, typename Weights, typename Tokens, typename Finish, typename Ready>
+// `warps` warps (this warp is number `w` of group `gid`). Partial sums meet in
+// `part` ([2][warps][128], alternating halves, so one group barrier a unit),
+// from which `finish` takes them. Two chunks are always on their way: a chunk's
+// registers are loaded again, with the unit's next columns or the next unit's
+// first, as soon as its products are issued. `ready` runs once, after the first
+// weights are asked for and before any token's row: the wait for the grid
+// barrier before the phase, if any.
+template <typename T, bool FRESH, typename Locate, typename Finish, typename Ready>
 __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, int warps, int gid, float *part,
-                                          const T *x, Weights weights, Tokens tokens, Finish finish, Ready ready) {
-  uint4 a0[kSteps], b0[kSteps], a1[kSteps], b1[kSteps];
-  WeightRows cur;
-  int u = first, tok0 = 0;
+                                          const T *x, Locate locate, Finish finish, Ready ready) {
+  Chunk<T> c0, c1;
+  Share cur;
+  int u = first;
   if (u < n) {
-    weights(u, w, warps, cur);
-    if (cur.step < cur.end) load_chunk<T>(cur, cur.step, a0, b0);
-    if (cur.step + kSteps < cur.end) load_chunk<T>(cur, cur.step + kSteps, a1, b1);
+    locate(u, w, warps, cur);
+    if (cur.step < cur.end) load_rows<T>(cur, cur.step, c0);
+    if (cur.step + kSteps < cur.end) load_rows<T>(cur, cur.step + kSteps, c1);
   }
   if (!ready()) return false;
+  if (u < n) {
+    if (cur.step < cur.end) load_token<T, FRESH>(cur, cur.step, x, c0);
+    if (cur.step + kSteps < cur.end) load_token<T, FRESH>(cur, cur.step + kSteps, x, c1);
+  }
   int half = 0;
   while (u < n) {
-    int rows[NT];
-    const int left = tokens(u, tok0, rows);  // this thread's token rows, and how many tokens there are from tok0 on
-    const int count = min(left, 8 * NT);
-    float acc[NT][Elem<T>::acc];
+    float acc[Elem<T>::acc];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < Elem<T>::acc; ++j) acc[i][j] = 0.f;
-    const bool last = left <= 8 * NT;
-    const int un = last ? u + stride : u;
-    const int end = cur.end;
-    int step = cur.step;
+    for (int j = 0; j < Elem<T>::acc; ++j) acc[j] = 0.f;
+    const int un = u + stride;
+    Share now = cur;
     do {
-      int ns = step + 2 * kSteps;  // what the registers hold next
-      const int s1 = step + kSteps, k0 = cur.k;
-      if (step < end) add_chunk<T, NT, FRESH>(step, k0, a0, b0, x, rows, count, acc);
-      step = ns;
-      if (ns >= end) {
+      int ns = now.step + 2 * kSteps;  // what the registers hold next
+      if (now.step < now.end) add_chunk<T, FRESH>(now, now.step, c0, x, acc);
+      if (ns >= now.end) {
         cur.end = 0;  // nothing left to load
-        if (un < n) weights(un, w, warps, cur);
+        if (un < n) locate(un, w, warps, cur);
         ns = cur.step;
       }
-      if (ns < cur.end) load_chunk<T>(cur, ns, a0, b0);
-      if (s1 < end) add_chunk<T, NT, FRESH>(s1, k0, a1, b1, x, rows, count, acc);
-      if (ns + kSteps < cur.end) load_chunk<T>(cur, ns + kSteps, a1, b1);
-    } while (step < end);
-    float *mine = part + (static_cast<size_t>(half) * warps) * (NT * 128);
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-      if (8 * i < count) put_tile<T>(mine + (w * NT + i) * 128, acc[i]);
+      if (ns < cur.end) {
+        load_rows<T>(cur, ns, c0);
+        load_token<T, FRESH>(cur, ns, x, c0);
+      }
+      if (now.step + kSteps < now.end) add_chunk<T, FRESH>(now, now.step + kSteps, c1, x, acc);
+      if (ns + kSteps < cur.end) {
+        load_rows<T>(cur, ns + kSteps, c1);
+        load_token<T, FRESH>(cur, ns + kSteps, x, c1);
+      }
+      now.step += 2 * kSteps;
+    } while (now.step < now.end);
+    float *mine = part + (half * warps) * 128;
+    put_tile<T>(mine + w * 128, acc);
     group_sync(gid, warps);
-    finish(u, tok0, count, last, mine);
+    finish(u, now.count, mine);
     half ^= 1;
     u = un;
-    tok0 = last ? 0 : tok0 + 8 * NT;
   }
   return true;
 }
@@ -309,20 +307,19 @@ struct FewParams {
   int n_tok;
 };
 
-// Routing tables of a CTA, in shared memory.
+// Routing tables of a CTA, in shared memory. A job is at most eight tokens of an
+// expert: its units cost the same whatever the routing, and the weights that the
+// jobs of a busy expert share come from memory once and from L2 the other times.
 struct Routes {
   int16_t sel[kMaxEdges];   // expert of edge t * k + j
   float wgt[kMaxEdges];     // its weight
   int16_t list[kMaxEdges];  // edges by expert,
   int16_t tok[kMaxEdges];   // and their tokens
-  int16_t rank[kMaxEdges];
-  int32_t first[1025];      // first entry of each hit expert in list
-  int16_t hit[1024];        // hit experts
-  int32_t cnt[1024];
+  int16_t job_expert[kMaxEdges], job_first[kMaxEdges], job_n[kMaxEdges];
+  uint32_t mask[1024][2];   // tokens of each expert
+  int16_t first[1024];      // its first entry in list
   int32_t warp_sum[kWarps];
-  int32_t n_hit;
-  int16_t turn[1024];       // order of phase 1: hit experts
-  int16_t deal[1024 + 8];   // order of phase 2 within a row tile: hit expert, or n_hit + shared expert
+  int32_t n_jobs;
 };
 
 // Group rule of the sigmoid router (see warp_group_limit) over the scores c of
@@ -430,9 +427,9 @@ __device__ __noinline__ void select_token(const FewParams &p, int t, uint2 *scra
   const float *row = p.ws.logits + static_cast<size_t>(t) * E;
   float v[EPL], c[EPL];
   bool ok[EPL];
-  if ((E & 3) == 0) {
+  if (EPL % 4 == 0 && (E & 3) == 0) {
 #pragma unroll
-    for (int j = 0; j < EPL; j += 4) {
+    for (int j = 0; j < EPL / 4 * 4; j += 4) {
       const float4 q = lo + j < E ? __ldcg(reinterpret_cast<const float4 *>(row + lo + j))
                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
@@ -479,28 +476,33 @@ __device__ __noinline__ void select_token(const FewParams &p, int t, uint2 *scra
   }
 }
 
-// Edges sorted by expert, from the selections (all threads; r.cnt is zero). The
-// order of an expert's edges does not matter: each is a column of its own everywhere.
+// Edges sorted by expert, then token, and the jobs, from the selections (all
+// threads; r.mask is zero). Every CTA has to come to the same jobs: an edge's place
+// follows from its expert's token mask, which no order of atomics changes.
 __device__ void build_routes(const FewParams &p, Routes &r) {
   const int E = p.d.E, k = p.d.k, edges = p.n_tok * k, lane = lane_id(), warp = warp_id();
   if (p.n_tok == 1) {  // one edge an expert: nothing to sort
-    if (threadIdx.x <= k) r.first[threadIdx.x] = threadIdx.x;
     if (threadIdx.x < k) {
-      r.hit[threadIdx.x] = r.sel[threadIdx.x];
-      r.list[threadIdx.x] = static_cast<int16_t>(threadIdx.x);
+      r.list[threadIdx.x] = r.job_first[threadIdx.x] = static_cast<int16_t>(threadIdx.x);
       r.tok[threadIdx.x] = 0;
+      r.job_expert[threadIdx.x] = r.sel[threadIdx.x];
+      r.job_n[threadIdx.x] = 1;
     }
-    if (threadIdx.x == 0) r.n_hit = k;
+    if (threadIdx.x == 0) r.n_jobs = k;
     __syncthreads();
     return;
   }
-  for (int i = threadIdx.x; i < edges; i += kThreads) r.rank[i] = static_cast<int16_t>(atomicAdd(&r.cnt[r.sel[i]], 1));
+  for (int i = threadIdx.x; i < edges; i += kThreads) {
+    const int t = i / k;
+    atomicOr(&r.mask[r.sel[i]][t >> 5], 1u << (t & 31));
+  }
   __syncthreads();
-  // thread i holds experts 2 i and 2 i + 1; running sums of (hit experts << 16 | edges)
+  // thread i holds experts 2 i and 2 i + 1; running sums of (jobs << 16 | edges)
   static_assert(2 * kThreads >= 1024, "two experts a thread");
   const int e0 = 2 * threadIdx.x;
-  const int c0 = e0 < E ? r.cnt[e0] : 0, c1 = e0 + 1 < E ? r.cnt[e0 + 1] : 0;
-  const int own = ((c0 > 0) + (c1 > 0)) << 16 | (c0 + c1);
+  auto count = [&](int e) { return e < E ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0; };
+  const int c0 = count(e0), c1 = count(e0 + 1);
+  const int own = (((c0 + 7) >> 3) + ((c1 + 7) >> 3)) << 16 | (c0 + c1);
   int sum = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -517,82 +519,41 @@ __device__ void build_routes(const FewParams &p, Routes &r) {
     all += y;
   }
   sum += before - own;
-  int hit = sum >> 16, at = sum & 0xFFFF;
-  if (c0 > 0) {
-    r.first[hit] = at;
-    r.hit[hit++] = static_cast<int16_t>(e0);
-    r.cnt[e0] = at;  // now the expert's first entry
-    at += c0;
+  int job = sum >> 16, at = sum & 0xFFFF;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = j ? c1 : c0;
+    if (c > 0) r.first[e0 + j] = static_cast<int16_t>(at);
+    for (int q = 0; q < c; q += 8) {
+      r.job_expert[job] = static_cast<int16_t>(e0 + j);
+      r.job_first[job] = static_cast<int16_t>(at + q);
+      r.job_n[job++] = static_cast<int16_t>(min(8, c - q));
+    }
+    at += c;
   }
-  if (c1 > 0) {
-    r.first[hit] = at;
-    r.hit[hit] = static_cast<int16_t>(e0 + 1);
-    r.cnt[e0 + 1] = at;
-  }
-  if (threadIdx.x == 0) {
-    r.n_hit = all >> 16;
-    r.first[all >> 16] = edges;
-  }
+  if (threadIdx.x == 0) r.n_jobs = all >> 16;
   __syncthreads();
   for (int i = threadIdx.x; i < edges; i += kThreads) {
-    const int q = r.cnt[r.sel[i]] + r.rank[i];
+    const int t = i / k, e = r.sel[i];
+    const int q = r.first[e] + (t >= 32 ? __popc(r.mask[e][0]) : 0) + __popc(r.mask[e][t >> 5] & ((1u << (t & 31)) - 1u));
     r.list[q] = static_cast<int16_t>(i);
-    r.tok[q] = static_cast<int16_t>(i / k);
+    r.tok[q] = static_cast<int16_t>(t);
   }
   __syncthreads();
 }
 
-// Orders in which the phases take the experts, dearest first where they differ:
-// an expert costs its weights and, per 8 tokens, the tokens' rows and products.
-// Phase 1 deals its units out in turns, so a group gets one of each price.
-// Phase 2 gives a group a run of neighbours in `deal`: the experts, by price,
-// dealt into `columns` columns that stand one after another, so that any run
-// of a column's length holds one of each price too. All threads.
-__device__ void order_by_cost(const FewParams &p, Routes &r, int columns) {
-  const int n_hit = r.n_hit, all = n_hit + p.d.n_sh;
-  auto tiles = [&](int h) { return ((h < n_hit ? r.first[h + 1] - r.first[h] : p.n_tok) + 7) >> 3; };
-  const int q = all / columns, rem = all % columns;
-  int place[3], rank[3];  // up to 1024 + 8 entries
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int h = threadIdx.x + i * kThreads;
-    rank[i] = h;
-    if (h < all && p.n_tok > 8) {
-      const int mine = tiles(h);
-      rank[i] = 0;
-      for (int o = 0; o < all; ++o) {
-        const int other = tiles(o);
-        rank[i] += other > mine || (other == mine && o < h);
-      }
-    }
-    const int c = rank[i] % columns;
-    place[i] = c * q + min(c, rem) + rank[i] / columns;
-    if (h < all) r.deal[place[i]] = static_cast<int16_t>(h);
-  }
-  if (p.n_tok <= 8) {
-    for (int h = threadIdx.x; h < n_hit; h += kThreads) r.turn[h] = static_cast<int16_t>(h);
-  } else {
-    // ranks among the hit experts alone: without the shared ones before them
-    for (int h = threadIdx.x; h < n_hit; h += kThreads) {
-      const int at = rank[h / kThreads] - (((p.n_tok + 7) >> 3) > tiles(h) ? p.d.n_sh : 0);
-      r.turn[at] = static_cast<int16_t>(h);
-    }
-  }
-  __syncthreads();
-}
-
-template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const __grid_constant__ FewParams p) {
-  extern __shared__ float part[];  // partial sums of the units; the selection's scratch between the phases
+template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const __grid_constant__ FewParams p) {
+  __shared__ __align__(16) float part[2 * kWarps * 128];  // partial sums of the units; the selection's scratch between the phases
   __shared__ Routes r;
   const Dims &d = p.d;
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
-  const int H = d.H, I = d.I, E = d.E, k = d.k, nt = p.n_tok;
+  const int H = d.H, I = d.I, E = d.E, k = d.k, nt = p.n_tok, nt8 = (nt + 7) / 8;
   constexpr int per = Elem<T>::per, step = Elem<T>::step;
   const T *x = static_cast<const T *>(p.x);
   T *act = static_cast<T *>(p.ws.act);     // row of edge e at e * I,
   const int act_sh = p.n_tok * k * I;      // of shared expert s and token t at act_sh + (s * n_tok + t) * I_s
 
-  auto split = [&](WeightRows &o, int cols, int w, int warps) {
+  auto split = [&](Share &o, int cols, int w, int warps) {
     const int chunks = (cols + step * kSteps - 1) / (step * kSteps);
     o.k = cols;
     o.step = chunks * w / warps * kSteps;
@@ -600,62 +561,58 @@ template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_m
   };
   auto sum = [&](const float *mine, int warps, int tok, int row) {
     float s = 0.f;
-    const float *q = mine + (tok >> 3) * 128 + row * 8 + (tok & 7);
-    for (int i = 0; i < warps; ++i) s += q[i * NT * 128];
+    const float *q = mine + row * 8 + tok;
+    for (int i = 0; i < warps; ++i) s += q[i * 128];
     return s;
   };
+  auto at_row = [&](const void *base, int64_t row, int64_t cols) {
+    return reinterpret_cast<const char *>(static_cast<const T *>(base) + row * cols + t * per);
+  };
 
-  // phase 0: router tiles of 16 experts, then shared tiles of 8 activation columns
+  // phase 0: router tiles of 16 experts, then shared tiles of 8 activation columns; eight tokens a unit
   const int n_router = (E + 15) / 16, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[3] = 0;  // no CTA reaches the last barrier before this one passes the first
-  if (threadIdx.x < 16 && blockIdx.x * 16 + threadIdx.x < E)  // the bias of this CTA's experts, needed at the end of the tile
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.b_router + blockIdx.x * 16 + threadIdx.x));
-  run_units<T, NT, false>(
-      blockIdx.x, gridDim.x, n_router + d.n_sh * sh8, warp, kWarps, 0, part, x,
-      [&](int u, int wi, int warps, WeightRows &o) {
-        split(o, H, wi, warps);
-        if (u < n_router) {
-          const T *base = static_cast<const T *>(p.w.w_router) + t * per;
-          o.p0 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(u * 16 + g, E - 1)) * H);
-          o.p1 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(u * 16 + g + 8, E - 1)) * H);
+  if (threadIdx.x < 16 && blockIdx.x / nt8 * 16 + threadIdx.x < E)  // the bias of this CTA's experts, needed at the end of the tile
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.b_router + blockIdx.x / nt8 * 16 + threadIdx.x));
+  run_units<T, false>(
+      blockIdx.x, gridDim.x, (n_router + d.n_sh * sh8) * nt8, warp, kWarps, 0, part, x,
+      [&](int u, int wi, int ws, Share &o) {
+        const int v = u / nt8, tok0 = (u - v * nt8) * 8;
+        split(o, H, wi, ws);
+        o.count = min(8, nt - tok0);
+        o.row = min(tok0 + g, nt - 1) * H;
+        if (v < n_router) {
+          o.p0 = at_row(p.w.w_router, min(v * 16 + g, E - 1), H);
+          o.p1 = at_row(p.w.w_router, min(v * 16 + g + 8, E - 1), H);
         } else {
-          const int s = (u - n_router) / sh8, c = min((u - n_router - s * sh8) * 8 + g, d.I_s - 1);
-          const int64_t at = (static_cast<int64_t>(s) * d.I_s + c) * H + t * per;
-          o.p0 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.ws_gate) + at);
-          o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.ws_up) + at);
+          const int s = (v - n_router) / sh8, c = min((v - n_router - s * sh8) * 8 + g, d.I_s - 1);
+          o.p0 = at_row(p.w.ws_gate, static_cast<int64_t>(s) * d.I_s + c, H);
+          o.p1 = at_row(p.w.ws_up, static_cast<int64_t>(s) * d.I_s + c, H);
         }
       },
-      [&](int, int tok0, int (&rows)[NT]) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) rows[i] = min(tok0 + 8 * i + g, nt - 1) * H;
-        return nt - tok0;
-      },
-      [&](int u, int tok0, int count, bool, const float *mine) {
-        if (u < n_router) {
-          for (int v = threadIdx.x; v < count * 16; v += kThreads) {
-            const int tok = v >> 4, e = u * 16 + (v & 15);
-            if (e < E)
-              p.ws.logits[static_cast<size_t>(tok0 + tok) * E + e] =
-                  (d.router == 0 ? __ldg(p.w.b_router + e) : 0.f) + sum(mine, kWarps, tok, v & 15);
-          }
-          return;
-        }
-        const int s = (u - n_router) / sh8, col0 = (u - n_router - s * sh8) * 8;
-        for (int v = threadIdx.x; v < count * 8; v += kThreads) {
-          const int tok = v >> 3, c = v & 7;
-          if (col0 + c < d.I_s)
-            act[act_sh + (s * nt + tok0 + tok) * d.I_s + col0 + c] =
-                from_f32<T>(silu(sum(mine, kWarps, tok, c)) * sum(mine, kWarps, tok, c + 8));
+      [&](int u, int count, const float *mine) {
+        const int v = u / nt8, tok0 = (u - v * nt8) * 8, q = threadIdx.x;
+        if (v < n_router) {
+          const int tok = q >> 4, e = v * 16 + (q & 15);
+          if (tok < count && e < E)
+            p.ws.logits[static_cast<size_t>(tok0 + tok) * E + e] =
+                (d.router == 0 ? __ldg(p.w.b_router + e) : 0.f) + sum(mine, kWarps, tok, q & 15);
+        } else {
+          const int s = (v - n_router) / sh8, tok = q >> 3, col = (v - n_router - s * sh8) * 8 + (q & 7);
+          if (tok < count && col < d.I_s)
+            act[act_sh + (s * nt + tok0 + tok) * d.I_s + col] =
+                from_f32<T>(silu(sum(mine, kWarps, tok, q & 7)) * sum(mine, kWarps, tok, (q & 7) + 8));
         }
       },
       [] { return true; });
   grid_arrive(p.ws.ctr);
-  for (int e = threadIdx.x; e < E; e += kThreads) r.cnt[e] = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) r.mask[e][0] = r.mask[e][1] = 0u;
   if (!grid_wait(p.ws.ctr, p.err, d.timeout_ns)) return;
 
   uint2 *scratch = reinterpret_cast<uint2 *>(part) + warp * 32;
   auto select = [&](int tok, int16_t *sel, float *wgt) {
-    if (E <= 256) select_token<8>(p, tok, scratch, sel, wgt);
+    if (E <= 64) select_token<2>(p, tok, scratch, sel, wgt);
+    else if (E <= 256) select_token<8>(p, tok, scratch, sel, wgt);
     else select_token<32>(p, tok, scratch, sel, wgt);
   };
   if (nt <= kWarps) {
@@ -675,83 +632,67 @@ template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_m
   }
   build_routes(p, r);
 
-  const int h16 = (H + 15) / 16;
-  const int warps2 = split_of(I / (step * kSteps)), n_groups = gridDim.x * (kWarps / warps2);
-  order_by_cost(p, r, max(1, (n_groups + h16 - 1) / h16));
-
-  // phase 1: routed activations, 8 columns of an expert a unit
+  // phase 1: routed activations, 8 columns of a job's expert a unit
   const int i8 = (I + 7) / 8;
   int warps = split_of(H / (step * kSteps)), grp = warp / warps, w = warp % warps;
   int gthread = threadIdx.x - grp * warps * 32;
-  run_units<T, NT, false>(
-      grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), r.n_hit * i8, w, warps, grp,
-      part + static_cast<size_t>(grp) * 2 * warps * NT * 128, x,
-      [&](int u, int wi, int ws, WeightRows &o) {
-        const int at_h = u / i8, h = r.turn[at_h], c = min((u - at_h * i8) * 8 + g, I - 1);
-        const int64_t at = (static_cast<int64_t>(r.hit[h]) * I + c) * H + t * per;
+  run_units<T, false>(
+      grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), r.n_jobs * i8, w, warps, grp,
+      part + grp * 2 * warps * 128, x,
+      [&](int u, int wi, int ws, Share &o) {
+        const int j = u / i8, c = min((u - j * i8) * 8 + g, I - 1);
         split(o, H, wi, ws);
-        o.p0 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_gate) + at);
-        o.p1 = reinterpret_cast<const char *>(static_cast<const T *>(p.w.w_up) + at);
+        o.count = r.job_n[j];
+        o.row = r.tok[r.job_first[j] + min(g, o.count - 1)] * H;
+        o.p0 = at_row(p.w.w_gate, static_cast<int64_t>(r.job_expert[j]) * I + c, H);
+        o.p1 = at_row(p.w.w_up, static_cast<int64_t>(r.job_expert[j]) * I + c, H);
       },
-      [&](int u, int tok0, int (&rows)[NT]) {
-        const int h = r.turn[u / i8], f = r.first[h] + tok0, n = r.first[h + 1] - f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) rows[i] = r.tok[f + min(8 * i + g, n - 1)] * H;
-        return n;
-      },
-      [&](int u, int tok0, int count, bool, const float *mine) {
-        const int at_h = u / i8, f = r.first[r.turn[at_h]] + tok0;
+      [&](int u, int count, const float *mine) {
+        const int j = u / i8;
         for (int v = gthread; v < count * 8; v += warps * 32) {
-          const int tok = v >> 3, c = v & 7, col = (u - at_h * i8) * 8 + c;
+          const int tok = v >> 3, c = v & 7, col = (u - j * i8) * 8 + c;
           if (col < I)
-            act[r.list[f + tok] * I + col] = from_f32<T>(silu(sum(mine, warps, tok, c)) * sum(mine, warps, tok, c + 8));
+            act[r.list[r.job_first[j] + tok] * I + col] =
+                from_f32<T>(silu(sum(mine, warps, tok, c)) * sum(mine, warps, tok, c + 8));
         }
       },
       [] { return true; });
   grid_arrive(p.ws.ctr + 2);
 
-  // phase 2: 16 rows of H of an expert (routed, then shared) a unit; rows of
-  // the fp32 sums: edge e at row e, shared expert s and token t at n_tok * k + s * n_tok + t.
-  const int experts = r.n_hit + d.n_sh;
-  warps = warps2;
+  // phase 2: 16 rows of H of a job's expert (after the routed jobs, eight tokens
+  // of a shared expert each) a unit; rows of the fp32 sums: edge e at row e,
+  // shared expert s and token t at n_tok * k + s * n_tok + t
+  const int h16 = (H + 15) / 16;
+  warps = split_of(I / (step * kSteps));
   grp = warp / warps;
   w = warp % warps;
   gthread = threadIdx.x - grp * warps * 32;
-  const int64_t group = grp * gridDim.x + blockIdx.x;
-  const int lo = static_cast<int>(experts * h16 * group / n_groups);
-  const int hi = static_cast<int>(experts * h16 * (group + 1) / n_groups);
-  run_units<T, NT, true>(
-      lo, 1, hi, w, warps, grp, part + static_cast<size_t>(grp) * 2 * warps * NT * 128, act,
-      [&](int u, int wi, int ws, WeightRows &o) {
-        const int tile = u / experts, h = r.deal[u - tile * experts], row = tile * 16 + g;
-        const bool shared = h >= r.n_hit;
-        const int cols = shared ? d.I_s : I;
-        const T *base = static_cast<const T *>(shared ? p.w.ws_down : p.w.w_down) +
-                        static_cast<int64_t>(shared ? h - r.n_hit : r.hit[h]) * H * cols + t * per;
-        split(o, cols, wi, ws);
-        o.p0 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(row, H - 1)) * cols);
-        o.p1 = reinterpret_cast<const char *>(base + static_cast<int64_t>(min(row + 8, H - 1)) * cols);
-      },
-      [&](int u, int tok0, int (&rows)[NT]) {
-        const int h = r.deal[u % experts];
-        if (h >= r.n_hit) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-            rows[i] = act_sh + ((h - r.n_hit) * nt + min(tok0 + 8 * i + g, nt - 1)) * d.I_s;
-          return nt - tok0;
+  run_units<T, true>(
+      grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), (r.n_jobs + d.n_sh * nt8) * h16, w, warps, grp,
+      part + grp * 2 * warps * 128, act,
+      [&](int u, int wi, int ws, Share &o) {
+        const int j = u / h16, row = (u - j * h16) * 16 + g;
+        if (j < r.n_jobs) {
+          split(o, I, wi, ws);
+          o.count = r.job_n[j];
+          o.row = r.list[r.job_first[j] + min(g, o.count - 1)] * I;
+          o.p0 = at_row(p.w.w_down, static_cast<int64_t>(r.job_expert[j]) * H + min(row, H - 1), I);
+          o.p1 = at_row(p.w.w_down, static_cast<int64_t>(r.job_expert[j]) * H + min(row + 8, H - 1), I);
+        } else {
+          const int s = (j - r.n_jobs) / nt8, tok0 = (j - r.n_jobs - s * nt8) * 8;
+          split(o, d.I_s, wi, ws);
+          o.count = min(8, nt - tok0);
+          o.row = act_sh + (s * nt + min(tok0 + g, nt - 1)) * d.I_s;
+          o.p0 = at_row(p.w.ws_down, static_cast<int64_t>(s) * H + min(row, H - 1), d.I_s);
+          o.p1 = at_row(p.w.ws_down, static_cast<int64_t>(s) * H + min(row + 8, H - 1), d.I_s);
         }
-        const int f = r.first[h] + tok0, n = r.first[h + 1] - f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) rows[i] = r.list[f + min(8 * i + g, n - 1)] * I;
-        return n;
       },
-      [&](int u, int tok0, int count, bool last, const float *mine) {
-        const int tile = u / experts, h = r.deal[u - tile * experts];
-        const bool shared = h >= r.n_hit;
+      [&](int u, int count, const float *mine) {
+        const int j = u / h16, sj = j - r.n_jobs;
         for (int v = gthread; v < count * 16; v += warps * 32) {
-          const int tok = tok0 + (v >> 4), c = v & 15, col = tile * 16 + c;
-          const int at = shared ? nt * k + (h - r.n_hit) * nt + tok : r.list[r.first[h] + tok];
-          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * H + col, sum(mine, warps, v >> 4, c));
+          const int tok = v >> 4, c = v & 15, col = (u - j * h16) * 16 + c;
+          const int at = sj < 0 ? r.list[r.job_first[j] + tok] : nt * k + sj / nt8 * nt + sj % nt8 * 8 + tok;
+          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * H + col, sum(mine, warps, tok, c));
         }
       },
       [&] { return grid_wait(p.ws.ctr + 2, p.err, d.timeout_ns); });
@@ -786,19 +727,16 @@ template <typename T, int NT> __global__ void __launch_bounds__(kThreads, 1) k_m
   }
 }
 
-template <typename T, int NT> cudaError_t launch(const FewParams &p, cudaStream_t s) {
-  auto *fn = &k_moe_few<T, NT>;
-  static std::atomic<uint64_t> ready{0};  // devices whose copy of the kernel has its shared memory raised
+template <typename T> cudaError_t launch(const FewParams &p, cudaStream_t s) {
+  auto *fn = &k_moe_few<T>;
+  static std::atomic<uint64_t> ready{0};  // devices whose copy of the kernel has its carveout set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  constexpr int smem = 2 * kWarps * NT * 128 * sizeof(float);
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    // tokens' rows are read through L1, which gets what the partial sums leave
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1);
+    // tokens' rows are read through L1, which gets what the tables and partial sums leave
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
@@ -809,22 +747,10 @@ template <typename T, int NT> cudaError_t launch(const FewParams &p, cudaStream_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_sms()));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, p);
-}
-
-// Token tiles a thread's registers hold: up to 32 tokens of bf16 layers (16
-// fp32 sums), 16 of fp32 layers (32 sums).
-cudaError_t by_tokens(const FewParams &p, bool bf16, cudaStream_t s) {
-  if (bf16) {
-    if (p.n_tok <= 8) return launch<__nv_bfloat16, 1>(p, s);
-    if (p.n_tok <= 16) return launch<__nv_bfloat16, 2>(p, s);
-    return launch<__nv_bfloat16, 4>(p, s);
-  }
-  return p.n_tok <= 8 ? launch<float, 1>(p, s) : launch<float, 2>(p, s);
 }
 
 }  // namespace
@@ -839,7 +765,7 @@ cudaError_t launch_moe_few(const Dims &d, const Weights &w, const FewWork &ws, c
   p.y = y;
   p.err = err;
   p.n_tok = n_tok;
-  return by_tokens(p, bf16 != 0, s);
+  return bf16 ? launch<__nv_bfloat16>(p, s) : launch<float>(p, s);
 }
 
 }  // namespace epoch
