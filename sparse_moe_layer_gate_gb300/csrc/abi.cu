@@ -152,8 +152,8 @@ size_t carve(const epoch_layer_config &c, char *base, Work *w) {
   t.err = static_cast<uint32_t *>(take(16));
   const size_t F = N < kFewTokens ? N : kFewTokens;
   t.few.logits = static_cast<float *>(take(F * E * 4));
-  t.few.act = take(F * (k * I + nsh * Is) * act);
-  t.few.out = static_cast<float *>(take(F * (k + nsh) * H * 4));
+  t.few.act = take(F * (k * few_row(I) + nsh * few_row(Is)) * act);
+  t.few.out = static_cast<float *>(take(F * (k + nsh) * few_row(H) * 4));
   t.few.sel = static_cast<int16_t *>(take(F * k * 2));
   t.few.wgt = static_cast<float *>(take(F * k * 4));
   t.few.ctr = static_cast<int32_t *>(take(4 * sizeof(int32_t)));
@@ -438,7 +438,7 @@ epoch_status epoch_moe_few(epoch_layer *L, const void *x, int32_t n_tok, void *y
   if (n_tok == 0) return EPOCH_OK;
   if (!aligned16(x) || !aligned16(y)) return EPOCH_EINVAL;
   // rows are addressed by 32-bit element offsets
-  const int64_t acts = static_cast<int64_t>(L->dims.k) * L->dims.I + static_cast<int64_t>(L->dims.n_sh) * L->dims.I_s;
+  const int64_t acts = static_cast<int64_t>(L->dims.k) * few_row(L->dims.I) + static_cast<int64_t>(L->dims.n_sh) * few_row(L->dims.I_s);
   if (n_tok * acts > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;
   cudaStream_t s = S(stream);
   return run(L, K_FEW, s,

@@ -118,7 +118,7 @@ __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-
 // the registers hold, and every pass reads the row again -- from L2 or L1, and
 // only elements that the same thread writes at the end, so out may be r).
 template <typename TA, typename TR, bool AFTER, int E, int VPT>
-__global__ void __launch_bounds__(512) k_block_norm(const NormArgs a, int tpr) {
+__global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const NormArgs a, int tpr) {
   __shared__ float sums[32];
   const int p = threadIdx.x & (tpr - 1);
   const int warps = tpr >> 5, w = p >> 5;

@@ -42,17 +42,18 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSteps = 4;    // K steps (64 bytes of a row) loaded together
 constexpr int kMaxEdges = kFewTokens * 16;
 
 // ------------------------------------------------------------------ element types
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
-  static constexpr int step = 32, per = 8;  // columns of a K step, and of a thread in it
+  static constexpr int step = 32, per = 8;  // columns of a K step (64 bytes of a row), and of a thread in it
+  static constexpr int steps = 4;           // K steps loaded together: a chunk
   static constexpr int acc = 4;             // fp32 sums a thread keeps of a 16 x 8 tile while adding along K
 };
 template <> struct Elem<float> {
   static constexpr int step = 16, per = 4;
+  static constexpr int steps = 2;  // its sums and the tokens' columns need the registers of the other two
   static constexpr int acc = 16;  // rows g and g + 8 of all eight tokens (this thread's columns only)
 };
 
@@ -95,10 +96,7 @@ __device__ __forceinline__ void group_sync(int id, int warps) {
 // Loads issued between the halves do not hold the arrival back.
 __device__ __forceinline__ void grid_arrive(int32_t *ctr) {
   __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(ctr, 1);
-  }
+  if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(ctr) : "memory");
 }
 __device__ bool grid_wait(const int32_t *ctr, uint32_t *err, int64_t timeout_ns) {
   __shared__ int s_ok;
@@ -137,8 +135,9 @@ struct Share {
 };
 
 template <typename T> struct Chunk {
-  uint4 a[kSteps], b[kSteps];                   // weight rows g and g + 8
-  uint4 v[sizeof(T) == 2 ? kSteps : 1];         // token row g (bf16)
+  static constexpr int n = Elem<T>::steps;
+  uint4 a[n], b[n];                   // weight rows g and g + 8
+  uint4 v[sizeof(T) == 2 ? n : 1];              // token row g (bf16)
 };
 
 // Whether columns of a K step that a thread holds exist: rows of bf16 layers are
@@ -149,7 +148,7 @@ template <typename T> __device__ __forceinline__ void load_rows(const Share &w, 
   const int c0 = step * Elem<T>::step, ct = c0 + (lane_id() & 3) * Elem<T>::per;
   const char *p0 = w.p0 + static_cast<int64_t>(c0) * sizeof(T), *p1 = w.p1 + static_cast<int64_t>(c0) * sizeof(T);
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
+  for (int j = 0; j < Elem<T>::steps; ++j) {
     const bool in = in_row<T>(ct + j * Elem<T>::step, w.k);
     c.a[j] = load_weights(p0 + 64 * j, in);
     c.b[j] = load_weights(p1 + 64 * j, in);
@@ -160,41 +159,41 @@ __device__ __forceinline__ void load_token(const Share &w, int step, const T *x,
   if constexpr (sizeof(T) == 2) {
     const T *row = x + w.row + step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) c.v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
+    for (int j = 0; j < Elem<T>::steps; ++j) c.v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
   }
 }
 
 // Adds a chunk's products to the sums. The fp32 form reads the tokens' rows here,
-// two tokens' loads on their way together: a thread's sums are of every token.
+// four tokens' loads on their way together: a thread's sums are of every token.
 template <typename T, bool FRESH>
 __device__ __forceinline__ void add_chunk(const Share &w, int step, const Chunk<T> &c, const T *x,
                                           float (&acc)[Elem<T>::acc]) {
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
+    for (int j = 0; j < Elem<T>::steps; ++j) {
       mma_bf16(acc, c.a[j].x, c.b[j].x, c.a[j].y, c.b[j].y, c.v[j].x, c.v[j].y);
       mma_bf16(acc, c.a[j].z, c.b[j].z, c.a[j].w, c.b[j].w, c.v[j].z, c.v[j].w);
     }
   } else {
     const int c0 = step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
 #pragma unroll
-    for (int n = 0; n < 8; n += 2) {
+    for (int n = 0; n < 8; n += 4) {
       if (n >= w.count) break;
-      uint4 v[2][kSteps];
+      uint4 v[4][Elem<T>::steps];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int m = 0; m < 4; ++m) {
         const T *row = x + __shfl_sync(0xffffffffu, w.row, 4 * (n + m)) + c0;
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
+        for (int j = 0; j < Elem<T>::steps; ++j) {
           v[m][j] = make_uint4(0u, 0u, 0u, 0u);
           if (in_row<T>(c0 + j * Elem<T>::step, w.k)) v[m][j] = load_tokens<FRESH>(row + j * Elem<T>::step);
         }
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int m = 0; m < 4; ++m) {
         float s = acc[n + m], q = acc[8 + n + m];
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
+        for (int j = 0; j < Elem<T>::steps; ++j) {
           const float v0 = __uint_as_float(v[m][j].x), v1 = __uint_as_float(v[m][j].y),
                       v2 = __uint_as_float(v[m][j].z), v3 = __uint_as_float(v[m][j].w);
           s = fmaf(__uint_as_float(c.a[j].x), v0, s);
@@ -250,12 +249,12 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
   if (u < n) {
     locate(u, w, warps, cur);
     if (cur.step < cur.end) load_rows<T>(cur, cur.step, c0);
-    if (cur.step + kSteps < cur.end) load_rows<T>(cur, cur.step + kSteps, c1);
+    if (cur.step + Elem<T>::steps < cur.end) load_rows<T>(cur, cur.step + Elem<T>::steps, c1);
   }
   if (!ready()) return false;
   if (u < n) {
     if (cur.step < cur.end) load_token<T, FRESH>(cur, cur.step, x, c0);
-    if (cur.step + kSteps < cur.end) load_token<T, FRESH>(cur, cur.step + kSteps, x, c1);
+    if (cur.step + Elem<T>::steps < cur.end) load_token<T, FRESH>(cur, cur.step + Elem<T>::steps, x, c1);
   }
   int half = 0;
   while (u < n) {
@@ -265,7 +264,7 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
     const int un = u + stride;
     Share now = cur;
     do {
-      int ns = now.step + 2 * kSteps;  // what the registers hold next
+      int ns = now.step + 2 * Elem<T>::steps;  // what the registers hold next
       if (now.step < now.end) add_chunk<T, FRESH>(now, now.step, c0, x, acc);
       if (ns >= now.end) {
         cur.end = 0;  // nothing left to load
@@ -276,12 +275,12 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
         load_rows<T>(cur, ns, c0);
         load_token<T, FRESH>(cur, ns, x, c0);
       }
-      if (now.step + kSteps < now.end) add_chunk<T, FRESH>(now, now.step + kSteps, c1, x, acc);
-      if (ns + kSteps < cur.end) {
-        load_rows<T>(cur, ns + kSteps, c1);
-        load_token<T, FRESH>(cur, ns + kSteps, x, c1);
+      if (now.step + Elem<T>::steps < now.end) add_chunk<T, FRESH>(now, now.step + Elem<T>::steps, c1, x, acc);
+      if (ns + Elem<T>::steps < cur.end) {
+        load_rows<T>(cur, ns + Elem<T>::steps, c1);
+        load_token<T, FRESH>(cur, ns + Elem<T>::steps, x, c1);
       }
-      now.step += 2 * kSteps;
+      now.step += 2 * Elem<T>::steps;
     } while (now.step < now.end);
     float *mine = part + (half * warps) * 128;
     put_tile<T>(mine + w * 128, acc);
@@ -548,16 +547,19 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   const Dims &d = p.d;
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const int H = d.H, I = d.I, E = d.E, k = d.k, nt = p.n_tok, nt8 = (nt + 7) / 8;
-  constexpr int per = Elem<T>::per, step = Elem<T>::step;
+  constexpr int per = Elem<T>::per, chunk = Elem<T>::step * Elem<T>::steps, steps = Elem<T>::steps;
   const T *x = static_cast<const T *>(p.x);
-  T *act = static_cast<T *>(p.ws.act);     // row of edge e at e * I,
-  const int act_sh = p.n_tok * k * I;      // of shared expert s and token t at act_sh + (s * n_tok + t) * I_s
+  // Scratch rows are whole 32-byte sectors, so that no store touches part of one (which L2 would complete from
+  // memory first: a barrier after such stores costs 3 to 5 us more).
+  const int Ia = few_row(I), Is = few_row(d.I_s), Ho = few_row(H);
+  T *act = static_cast<T *>(p.ws.act);     // row of edge e at e * Ia,
+  const int act_sh = p.n_tok * k * Ia;     // of shared expert s and token t at act_sh + (s * n_tok + t) * Is
 
   auto split = [&](Share &o, int cols, int w, int warps) {
-    const int chunks = (cols + step * kSteps - 1) / (step * kSteps);
+    const int chunks = (cols + chunk - 1) / chunk;
     o.k = cols;
-    o.step = chunks * w / warps * kSteps;
-    o.end = chunks * (w + 1) / warps * kSteps;
+    o.step = chunks * w / warps * steps;
+    o.end = chunks * (w + 1) / warps * steps;
   };
   auto sum = [&](const float *mine, int warps, int tok, int row) {
     float s = 0.f;
@@ -572,6 +574,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   // phase 0: router tiles of 16 experts, then shared tiles of 8 activation columns; eight tokens a unit
   const int n_router = (E + 15) / 16, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[3] = 0;  // no CTA reaches the last barrier before this one passes the first
+  // units store 8 activations of a token: half a sector in bf16, so the sectors have to be in L2
+  const int64_t act_bytes = (static_cast<int64_t>(act_sh) + static_cast<int64_t>(d.n_sh) * nt * Is) * sizeof(T);
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 128; i < act_bytes; i += static_cast<int64_t>(gridDim.x) * kThreads * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(act) + i));
   if (threadIdx.x < 16 && blockIdx.x / nt8 * 16 + threadIdx.x < E)  // the bias of this CTA's experts, needed at the end of the tile
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.b_router + blockIdx.x / nt8 * 16 + threadIdx.x));
   run_units<T, false>(
@@ -600,7 +606,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
         } else {
           const int s = (v - n_router) / sh8, tok = q >> 3, col = (v - n_router - s * sh8) * 8 + (q & 7);
           if (tok < count && col < d.I_s)
-            act[act_sh + (s * nt + tok0 + tok) * d.I_s + col] =
+            act[act_sh + (s * nt + tok0 + tok) * Is + col] =
                 from_f32<T>(silu(sum(mine, kWarps, tok, q & 7)) * sum(mine, kWarps, tok, (q & 7) + 8));
         }
       },
@@ -634,7 +640,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
 
   // phase 1: routed activations, 8 columns of a job's expert a unit
   const int i8 = (I + 7) / 8;
-  int warps = split_of(H / (step * kSteps)), grp = warp / warps, w = warp % warps;
+  int warps = split_of(H / chunk), grp = warp / warps, w = warp % warps;
   int gthread = threadIdx.x - grp * warps * 32;
   run_units<T, false>(
       grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), r.n_jobs * i8, w, warps, grp,
@@ -652,7 +658,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
         for (int v = gthread; v < count * 8; v += warps * 32) {
           const int tok = v >> 3, c = v & 7, col = (u - j * i8) * 8 + c;
           if (col < I)
-            act[r.list[r.job_first[j] + tok] * I + col] =
+            act[r.list[r.job_first[j] + tok] * Ia + col] =
                 from_f32<T>(silu(sum(mine, warps, tok, c)) * sum(mine, warps, tok, c + 8));
         }
       },
@@ -663,7 +669,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   // of a shared expert each) a unit; rows of the fp32 sums: edge e at row e,
   // shared expert s and token t at n_tok * k + s * n_tok + t
   const int h16 = (H + 15) / 16;
-  warps = split_of(I / (step * kSteps));
+  warps = split_of(I / chunk);
   grp = warp / warps;
   w = warp % warps;
   gthread = threadIdx.x - grp * warps * 32;
@@ -675,14 +681,14 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
         if (j < r.n_jobs) {
           split(o, I, wi, ws);
           o.count = r.job_n[j];
-          o.row = r.list[r.job_first[j] + min(g, o.count - 1)] * I;
+          o.row = r.list[r.job_first[j] + min(g, o.count - 1)] * Ia;
           o.p0 = at_row(p.w.w_down, static_cast<int64_t>(r.job_expert[j]) * H + min(row, H - 1), I);
           o.p1 = at_row(p.w.w_down, static_cast<int64_t>(r.job_expert[j]) * H + min(row + 8, H - 1), I);
         } else {
           const int s = (j - r.n_jobs) / nt8, tok0 = (j - r.n_jobs - s * nt8) * 8;
           split(o, d.I_s, wi, ws);
           o.count = min(8, nt - tok0);
-          o.row = act_sh + (s * nt + min(tok0 + g, nt - 1)) * d.I_s;
+          o.row = act_sh + (s * nt + min(tok0 + g, nt - 1)) * Is;
           o.p0 = at_row(p.w.ws_down, static_cast<int64_t>(s) * H + min(row, H - 1), d.I_s);
           o.p1 = at_row(p.w.ws_down, static_cast<int64_t>(s) * H + min(row + 8, H - 1), d.I_s);
         }
@@ -692,7 +698,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
         for (int v = gthread; v < count * 16; v += warps * 32) {
           const int tok = v >> 4, c = v & 15, col = (u - j * h16) * 16 + c;
           const int at = sj < 0 ? r.list[r.job_first[j] + tok] : nt * k + sj / nt8 * nt + sj % nt8 * 8 + tok;
-          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * H + col, sum(mine, warps, tok, c));
+          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * Ho + col, sum(mine, warps, tok, c));
         }
       },
       [&] { return grid_wait(p.ws.ctr + 2, p.err, d.timeout_ns); });
@@ -708,7 +714,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
     auto add = [&](int first, int n, const float *wgt) {  // rows first, first + n_rows.. of the expert outputs
 #pragma unroll 8
       for (int j = 0; j < n; ++j) {
-        const float4 q = __ldcg(reinterpret_cast<const float4 *>(p.ws.out + static_cast<size_t>(first + j * (wgt ? 1 : nt)) * H + col));
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(p.ws.out + static_cast<size_t>(first + j * (wgt ? 1 : nt)) * Ho + col));
         const float f = wgt ? wgt[j] : 1.f;
         s[0] = fmaf(f, q.x, s[0]);
         s[1] = fmaf(f, q.y, s[1]);

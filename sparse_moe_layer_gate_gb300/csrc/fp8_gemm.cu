@@ -31,7 +31,11 @@ namespace {
 constexpr int kBm = 128;
 constexpr int kBk = 128;  // one scale block; 128 bytes: one swizzle row
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+// Three warpgroups: producer and MMA (two of four warps), and the epilogue's two.
+// The launch's 168 registers a thread are handed over: 56 to the first group,
+// 224 to the others, whose sums alone take 128 (56 + 2 * 224 = 3 * 168).
+constexpr int kThreads = 32 * (kEpiWarps + 4);
+constexpr int kRegsFew = 56, kRegsMany = 224;
 constexpr int kMaxGroups = 1024;
 
 struct GemmParams {
@@ -55,6 +59,32 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uin
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+template <int R> __device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R> __device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Two fp32 sums in a register pair; acc += v * s on both at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t &acc, uint64_t v, uint64_t s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+template <int N> __device__ __forceinline__ void add_scaled(uint64_t *acc, const float (&v)[N], uint64_t s) {
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) fma_pair(acc[j], pair(v[2 * j], v[2 * j + 1]), s);
 }
 
 // First rows of the groups, in ascending order and within [0, m] whatever the
@@ -164,8 +194,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   volatile int *abort = &s_abort;
   TileWalk walk(s_start, s_cum, p.g.offsets ? p.g.n_groups : 1, p.nt_n);
 
-  if (warp == kEpiWarps) {  // ------------------------------------------------ producer
-    if (lane == 0) {
+  // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 10, 11: none
+  if (warp >= kEpiWarps) {
+  give_registers<kRegsFew>();
+  if (warp == kEpiWarps && lane == 0) {  // ------------------------------------- producer
+    {
       const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
       // weights of a tile's columns are read once per row tile; with one row tile a group they stream through
       const uint64_t wpol = p.g.offsets ? pass : keep;
@@ -196,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         mbar_wait_bounded(full + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
       }
     }
-  } else if (warp == kEpiWarps + 1) {  // -------------------------------------- MMA
-    if (lane == 0) {
+  } else if (warp == kEpiWarps + 1 && lane == 0) {  // -------------------------- MMA
+    {
       constexpr uint32_t idesc = idesc_e4m3_f32(kBm, BN);
       uint32_t it = 0;
       bool ok = true;
@@ -225,7 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         mbar_wait_bounded(tfull + 8 * (i % G::bufs), (i / G::bufs) & 1u, &done, p.err, p.timeout_ns);
       }
     }
+  }
   } else {  // ------------------------------------------------------------------ epilogue
+    take_registers<kRegsMany>();
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 32, columns kCols half .. + kCols
     uint32_t it = 0;
     bool ok = true;
@@ -238,9 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       const bool any = quarter * 32 < rows && n0 < p.g.N;  // this warp holds a row of the tile
       const float *sa = p.g.sa + static_cast<int64_t>(on ? row : row0) * p.kb_n;
       const float *sb = p.g.sb + (static_cast<int64_t>(e) * p.nb_n + min(n0 / kFp8Block, p.nb_n - 1)) * p.kb_n;
-      float acc[kCols];
+      uint64_t acc[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+      for (int c = 0; c < kCols / 2; ++c) acc[c] = 0ull;
       float s = __ldg(sa) * __ldg(sb);
       for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
         const uint32_t buf = it % G::bufs;
@@ -250,20 +285,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         const int nk = min(kb + 1, p.kb_n - 1);
         const float s_next = __ldg(sa + nk) * __ldg(sb + nk);
         if (any) {
+          // 32 columns are on their way from TMEM while the 32 before them are added
           tc_fence_after();
           const uint32_t src = tmem + buf * BN + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+          const uint64_t s2 = pair(s, s);
+          float v[2][32];
+          tmem_ld32(src, v[0]);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            float v[32];
-            tmem_ld32(src + c, v);
+          for (int c = 0; c < kCols / 32; ++c) {
             tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], s, acc[c + j]);
+            if (c + 1 < kCols / 32) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
+            else tc_fence_before();
+            if (c + 1 == kCols / 32) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(tempty + 8 * buf);
+            }
+            add_scaled(acc + 16 * c, v[c & 1], s2);
           }
-          tc_fence_before();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty + 8 * buf);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty + 8 * buf);
         s = s_next;
       }
       if (ok && on) {
@@ -272,30 +314,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride + n0;
           if (p.g.wide_out && n == kCols) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8) {
+            for (int c = 0; c < kCols / 2; c += 4) {
               uint32_t w[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[c + 2 * j], acc[c + 2 * j + 1]);
+                const float2 f = unpair(acc[c + j]);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
                 w[j] = *reinterpret_cast<const uint32_t *>(&h);
               }
-              *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(dst + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              if (c < n) dst[c] = __float2bfloat16_rn(acc[c]);
+            for (int c = 0; c < kCols / 2; ++c) {
+              const float2 f = unpair(acc[c]);
+              if (2 * c < n) dst[2 * c] = __float2bfloat16_rn(f.x);
+              if (2 * c + 1 < n) dst[2 * c + 1] = __float2bfloat16_rn(f.y);
+            }
           }
         } else {
           float *dst = static_cast<float *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride + n0;
           if (p.g.wide_out && n == kCols) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4)
-              *reinterpret_cast<float4 *>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            for (int c = 0; c < kCols / 2; c += 2) {
+              const float2 f = unpair(acc[c]), h = unpair(acc[c + 1]);
+              *reinterpret_cast<float4 *>(dst + 2 * c) = make_float4(f.x, f.y, h.x, h.y);
+            }
           } else {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              if (c < n) dst[c] = acc[c];
+            for (int c = 0; c < kCols / 2; ++c) {
+              const float2 f = unpair(acc[c]);
+              if (2 * c < n) dst[2 * c] = f.x;
+              if (2 * c + 1 < n) dst[2 * c + 1] = f.y;
+            }
           }
         }
       }

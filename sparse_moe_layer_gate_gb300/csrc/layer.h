@@ -28,10 +28,13 @@ struct Ctrl {
 // Scratch of the few-token call (few.cu), carved from the caller's workspace; a
 // block's state is not touched by it.
 constexpr int kFewTokens = 64;  // tokens of one call, at most
+// Elements between scratch rows of n: a multiple of 16, so rows of either type are whole 32-byte sectors.
+__host__ __device__ inline int few_row(int n) { return (n + 15) / 16 * 16; }
 struct FewWork {
   float *logits;   // [kFewTokens][E]
   void *act;       // activations, layer dtype: [n_tok*k][I] of the edges, then [n_sh][n_tok][I_s]
-  float *out;      // [kFewTokens*(k + n_sh)][H] expert outputs
+                   // (rows few_row apart)
+  float *out;      // [kFewTokens*(k + n_sh)][H] expert outputs (rows few_row apart)
   int16_t *sel;    // [kFewTokens][k] selections and
   float *wgt;      // their weights, where the CTAs share the selection out
   int32_t *ctr;    // [4] arrivals at the grid barriers: zero between calls ([3]: zeroed by each call), and
