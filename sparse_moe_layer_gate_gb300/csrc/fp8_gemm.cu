@@ -31,7 +31,7 @@ namespace {
 constexpr int kBm = 128;
 constexpr int kBk = 128;  // one scale block; 128 bytes: one swizzle row
 constexpr int kEpiWarps = 8;
-// Three warpgroups: producer and MMA (two of four warps), and the epilogue's two.
+// Three warpgroups: producer, MMA and two warps for the scales, and the epilogue's two.
 // The launch's 168 registers a thread are handed over: 56 to the first group,
 // 224 to the others, whose sums alone take 128 (56 + 2 * 224 = 3 * 168).
 constexpr int kThreads = 32 * (kEpiWarps + 4);
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   __shared__ __align__(8) uint64_t bars[2 * G::stages + 2 * G::bufs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ float s_scale[G::bufs][2][kBm];  // a's scale times b's, for each row and epilogue half
   __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
   const int warp = warp_id(), lane = lane_id();
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < G::bufs; ++i) {
-      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tfull + 8 * i, 2);  // the products, and the scales
       mbar_init(tempty + 8 * i, kEpiWarps);
     }
     mbar_fence_init();
@@ -194,11 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   volatile int *abort = &s_abort;
   TileWalk walk(s_start, s_cum, p.g.offsets ? p.g.n_groups : 1, p.nt_n);
 
-  // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 10, 11: none
+  // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 10, 11: scales
   if (warp >= kEpiWarps) {
-  give_registers<kRegsFew>();
-  if (warp == kEpiWarps && lane == 0) {  // ------------------------------------- producer
-    {
+    give_registers<kRegsFew>();
+    if (warp == kEpiWarps && lane == 0) {  // ----------------------------------- producer
       const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
       // weights of a tile's columns are read once per row tile; with one row tile a group they stream through
       const uint64_t wpol = p.g.offsets ? pass : keep;
@@ -228,9 +228,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         int done = 0;
         mbar_wait_bounded(full + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
       }
-    }
-  } else if (warp == kEpiWarps + 1 && lane == 0) {  // -------------------------- MMA
-    {
+    } else if (warp >= kEpiWarps + 2) {  // ------------------------------------- scales, every other K block a warp
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < walk.total; t += gridDim.x) {
+        int e, row0, rows, nt;
+        walk.at(t, &e, &row0, &rows, &nt);
+        const float *sa[4], *sb[2];
+        float fa[4], fb[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sa[i] = p.g.sa + static_cast<int64_t>(row0 + min(32 * i + lane, rows - 1)) * p.kb_n;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          sb[i] = p.g.sb + (static_cast<int64_t>(e) * p.nb_n + min((nt * BN + i * kCols) / kFp8Block, p.nb_n - 1)) * p.kb_n;
+        auto load = [&](int kb) {
+          kb = min(kb, p.kb_n - 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) fa[i] = __ldg(sa[i] + kb);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) fb[i] = __ldg(sb[i] + kb);
+        };
+        const int first = static_cast<int>((it ^ static_cast<uint32_t>(warp)) & 1u);
+        load(first);
+        for (int kb = first; kb < p.kb_n; kb += 2) {
+          const uint32_t i = it + kb, buf = i % G::bufs;
+          ok = mbar_wait_bounded(tempty + 8 * buf, ((i / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s_scale[buf][h][32 * j + lane] = fa[j] * fb[h];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tfull + 8 * buf);
+          load(kb + 2);
+        }
+        it += p.kb_n;
+      }
+    } else if (warp == kEpiWarps + 1 && lane == 0) {  // ------------------------ MMA
       constexpr uint32_t idesc = idesc_e4m3_f32(kBm, BN);
       uint32_t it = 0;
       bool ok = true;
@@ -258,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         mbar_wait_bounded(tfull + 8 * (i % G::bufs), (i / G::bufs) & 1u, &done, p.err, p.timeout_ns);
       }
     }
-  }
   } else {  // ------------------------------------------------------------------ epilogue
     take_registers<kRegsMany>();
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 32, columns kCols half .. + kCols
@@ -271,23 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       const int n0 = nt * BN + half * kCols;
       const bool on = r < rows && n0 < p.g.N;
       const bool any = quarter * 32 < rows && n0 < p.g.N;  // this warp holds a row of the tile
-      const float *sa = p.g.sa + static_cast<int64_t>(on ? row : row0) * p.kb_n;
-      const float *sb = p.g.sb + (static_cast<int64_t>(e) * p.nb_n + min(n0 / kFp8Block, p.nb_n - 1)) * p.kb_n;
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int c = 0; c < kCols / 2; ++c) acc[c] = 0ull;
-      float s = __ldg(sa) * __ldg(sb);
       for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
         const uint32_t buf = it % G::bufs;
         ok = mbar_wait_bounded(tfull + 8 * buf, (it / G::bufs) & 1u, abort, p.err, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int nk = min(kb + 1, p.kb_n - 1);
-        const float s_next = __ldg(sa + nk) * __ldg(sb + nk);
         if (any) {
           // 32 columns are on their way from TMEM while the 32 before them are added
           tc_fence_after();
           const uint32_t src = tmem + buf * BN + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+          const float s = s_scale[buf][half][r];
           const uint64_t s2 = pair(s, s);
           float v[2][32];
           tmem_ld32(src, v[0]);
@@ -306,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           __syncwarp();
           if (lane == 0) mbar_arrive(tempty + 8 * buf);
         }
-        s = s_next;
       }
       if (ok && on) {
         const int n = min(kCols, p.g.N - n0);
