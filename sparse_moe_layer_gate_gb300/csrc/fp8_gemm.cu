@@ -16,7 +16,6 @@
 //
 // Few rows (k_fp8_small): bound by the weights' bytes; sixteen weight rows per
 // CTA go from global memory straight into mma.sync fragments (see below).
-#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -40,7 +39,7 @@ constexpr int kMaxGroups = 1024;
 
 struct GemmParams {
   CUtensorMap a[3];  // boxes of 32, 64, 128 rows
-  CUtensorMap b;     // boxes of BN rows
+  CUtensorMap b;     // boxes of the rows that a CTA loads
   GemmArgs g;
   int kb_n, nb_n, nt_n;  // K blocks, N scale blocks, N tiles
   uint32_t *err;
@@ -51,14 +50,98 @@ struct GemmParams {
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// mbar_wait_bounded for the short waits of this kernel, all on its critical path:
+// the clock is first read after 256 attempts, not after the first.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
+                                         int64_t timeout_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255u) != 0u) continue;
+    if (*abort) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > static_cast<uint64_t>(timeout_ns)) {
+      set_error(err, EPOCH_DEVERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
+                                          int64_t timeout_ns) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort, err, timeout_ns));
+}
+
+// True for one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Forms for two CTAs that work on one tile (a cluster of two; their shared memory
+// and TMEM are laid out alike). TMEM is allocated and freed by a warp of each; the
+// first CTA's MMA thread issues the products of both, and its commit arrives on
+// the barriers of both; copies of both count on the first CTA's barrier.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+template <bool PAIR> __device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    tc_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, uint32_t bar,
+                                         uint64_t policy) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+        : "memory");
+  else
+    tma_load_2d(dst, map, c0, c1, bar, policy);
+}
+// Arrives on a barrier of another CTA of the cluster (or its own; address from
+// mapa_shared), after TMEM reads that have returned: nothing in memory has to be
+// released to the other CTA (a release at cluster scope waits for every access of
+// the warp, which made the whole product twice as slow).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 template <int R> __device__ __forceinline__ void give_registers() {
@@ -85,6 +168,14 @@ __device__ __forceinline__ void fma_pair(uint64_t &acc, uint64_t v, uint64_t s) 
 template <int N> __device__ __forceinline__ void add_scaled(uint64_t *acc, const float (&v)[N], uint64_t s) {
 #pragma unroll
   for (int j = 0; j < N / 2; ++j) fma_pair(acc[j], pair(v[2 * j], v[2 * j + 1]), s);
+}
+
+// A thread's 32 bytes of its own row: a whole sector (16-byte stores of halves of
+// sectors took a fifth of the product's time at 8192 x 4096 x 4096).
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // First rows of the groups, in ascending order and within [0, m] whatever the
@@ -126,11 +217,13 @@ __device__ void group_tiles(const int32_t *offsets, int E, int m, int tile, int 
 }
 
 // The tiles of one role: tile t of the launch is row tile t / nt_n (groups in
-// order) and column tile t % nt_n, so neighbouring CTAs share their rows.
+// order) and column tile t % nt_n, so neighbouring CTAs share their rows. The
+// CTA's rows of the tile are `rows` (0 or less: none) from row0 on.
 struct TileWalk {
   const int *start, *cum;
-  int E, nt_n, e, total;
-  __device__ TileWalk(const int *s, const int *c, int E_, int nt) : start(s), cum(c), E(E_), nt_n(nt), e(0) {
+  int E, nt_n, bm, first, e, total;
+  __device__ TileWalk(const int *s, const int *c, int E_, int nt, int bm_, int rank)
+      : start(s), cum(c), E(E_), nt_n(nt), bm(bm_), first(rank * kBm), e(0) {
     total = cum[E] * nt_n;
   }
   __device__ void at(int t, int *group, int *row0, int *rows, int *nt) {
@@ -138,43 +231,55 @@ struct TileWalk {
     *nt = t - mt * nt_n;
     while (cum[e + 1] <= mt) ++e;
     *group = e;
-    *row0 = start[e] + (mt - cum[e]) * kBm;
+    *row0 = start[e] + (mt - cum[e]) * bm + first;
     *rows = min(kBm, start[e + 1] - *row0);
   }
 };
 
-template <int BN> struct Geo {
-  static constexpr int stage = (kBm + BN) * kBk;
-  static constexpr int stages = BN == 256 ? 4 : 6;
-  static constexpr int bufs = 512 / BN;  // TMEM accumulators
+// Tiles are 256 columns wide. PAIR: two CTAs take 256 rows, each its own 128 rows
+// of a and half of the weights' rows, which the products of both read.
+constexpr int kBn = 256;
+template <bool PAIR> struct Geo {
+  static constexpr int bm = PAIR ? 2 * kBm : kBm;
+  static constexpr int b_rows = PAIR ? kBn / 2 : kBn;
+  static constexpr int stage = (kBm + b_rows) * kBk;
+  static constexpr int stages = PAIR ? 6 : 4;
+  static constexpr int bufs = 2;  // TMEM accumulators
   static constexpr int smem = 1024 + stages * stage;
 };
 
-template <int BN, bool BF16>
+template <bool PAIR, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ GemmParams p) {
-  using G = Geo<BN>;
+  using G = Geo<PAIR>;
+  constexpr int BN = kBn;
   constexpr int kCols = BN / 2;  // columns of an epilogue warpgroup
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * G::stages + 2 * G::bufs];
+  __shared__ __align__(8) uint64_t bars[2 * G::stages + 3 * G::bufs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float s_scale[G::bufs][2][kBm];  // a's scale times b's, for each row and epilogue half
   __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
   const int warp = warp_id(), lane = lane_id();
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cta = PAIR ? blockIdx.x >> 1 : blockIdx.x, ctas = PAIR ? gridDim.x >> 1 : gridDim.x;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_u32(bars), empty = full + 8 * G::stages, tfull = empty + 8 * G::stages,
-                 tempty = tfull + 8 * G::bufs;
+                 tempty = tfull + 8 * G::bufs, sempty = tempty + 8 * G::bufs;
   if (warp == 0) {
-    tmem_alloc(smem_u32(&s_tmem), 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(&s_tmem), 512);
+    } else {
+      tmem_alloc(smem_u32(&s_tmem), 512);
+      tmem_relinquish();
+    }
   } else if (warp == 1) {
     if (p.g.offsets != nullptr) {
-      group_tiles(p.g.offsets, p.g.n_groups, p.g.m, kBm, s_start, s_cum);
+      group_tiles(p.g.offsets, p.g.n_groups, p.g.m, G::bm, s_start, s_cum);
     } else if (lane == 0) {
       s_start[0] = 0;
       s_start[1] = p.g.m;
       s_cum[0] = 0;
-      s_cum[1] = (p.g.m + kBm - 1) / kBm;
+      s_cum[1] = (p.g.m + G::bm - 1) / G::bm;
     }
   } else if (warp == 2 && lane == 0) {
     s_abort = 0;
@@ -184,60 +289,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     }
     for (int i = 0; i < G::bufs; ++i) {
       mbar_init(tfull + 8 * i, 2);  // the products, and the scales
-      mbar_init(tempty + 8 * i, kEpiWarps);
+      mbar_init(tempty + 8 * i, PAIR ? 2 * kEpiWarps : kEpiWarps);  // accumulators read (both CTAs')
+      mbar_init(sempty + 8 * i, kEpiWarps);                         // this CTA's scales read
     }
     mbar_fence_init();
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int *abort = &s_abort;
-  TileWalk walk(s_start, s_cum, p.g.offsets ? p.g.n_groups : 1, p.nt_n);
+  TileWalk walk(s_start, s_cum, p.g.offsets ? p.g.n_groups : 1, p.nt_n, G::bm, rank);
 
   // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 10, 11: scales
   if (warp >= kEpiWarps) {
     give_registers<kRegsFew>();
-    if (warp == kEpiWarps && lane == 0) {  // ----------------------------------- producer
+    if (warp == kEpiWarps) {  // ------------------------------------------------ producer
       const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
       // weights of a tile's columns are read once per row tile; with one row tile a group they stream through
       const uint64_t wpol = p.g.offsets ? pass : keep;
-      uint32_t it = 0;
+      const uint32_t counts = PAIR ? mapa_shared(full, 0) : full;  // the barriers that the copies count on
+      uint32_t it = 0, st = 0, phase = 1;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < walk.total; t += gridDim.x) {
+      for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
-        const int box = rows <= 32 ? 0 : rows <= 64 ? 1 : 2;
-        const CUtensorMap *ma = p.g.offsets ? &p.a[box] : &p.a[2];
-        const uint32_t bytes = ((p.g.offsets ? 32u << box : 128u) + BN) * kBk;
-        const int brow = e * p.g.N + nt * BN;
+        // small groups of single CTAs load the smallest box that holds their rows
+        const int box = PAIR || p.g.offsets == nullptr ? 2 : rows <= 32 ? 0 : rows <= 64 ? 1 : 2;
+        const uint32_t bytes = PAIR ? 2 * G::stage : ((32u << box) + BN) * kBk;
+        const int brow = e * p.g.N + nt * BN + rank * G::b_rows;
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
-          const uint32_t st = it % G::stages, ph = (it / G::stages) & 1u;
-          if (!mbar_wait_bounded(empty + 8 * st, ph ^ 1u, abort, p.err, p.timeout_ns)) {
-            ok = false;
-            break;
+          ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t dst = ring + st * G::stage;
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
+            load_box<PAIR>(dst, &p.a[box], kb * kBk, row0, counts + 8 * st, keep);
+            load_box<PAIR>(dst + kBm * kBk, &p.b, kb * kBk, brow, counts + 8 * st, wpol);
           }
-          const uint32_t dst = ring + st * G::stage;
-          mbar_arrive_expect_tx(full + 8 * st, bytes);
-          tma_load_2d(dst, ma, kb * kBk, row0, full + 8 * st, keep);
-          tma_load_2d(dst + kBm * kBk, &p.b, kb * kBk, brow, full + 8 * st, wpol);
+          __syncwarp();
+          if (++st == G::stages) {
+            st = 0;
+            phase ^= 1u;
+          }
         }
       }
-      // no exit with copies in flight: the last stages' copies have landed before the CTA ends
-      for (uint32_t i = it > G::stages ? it - G::stages : 0; i < it; ++i) {
-        int done = 0;
-        mbar_wait_bounded(full + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
-      }
+      // no exit with copies in flight: the last stages' copies (both CTAs' count here) have landed before the end
+      if (rank == 0)
+        for (uint32_t i = it > G::stages ? it - G::stages : 0; i < it; ++i) {
+          int done = 0;
+          wait_for(full + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
+        }
     } else if (warp >= kEpiWarps + 2) {  // ------------------------------------- scales, every other K block a warp
       uint32_t it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < walk.total; t += gridDim.x) {
+      for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
         const float *sa[4], *sb[2];
         float fa[4], fb[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sa[i] = p.g.sa + static_cast<int64_t>(row0 + min(32 * i + lane, rows - 1)) * p.kb_n;
+        for (int i = 0; i < 4; ++i)  // rows behind the last one read a row that exists
+          sa[i] = p.g.sa + static_cast<int64_t>(min(row0 + 32 * i + lane, p.g.m - 1)) * p.kb_n;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           sb[i] = p.g.sb + (static_cast<int64_t>(e) * p.nb_n + min((nt * BN + i * kCols) / kFp8Block, p.nb_n - 1)) * p.kb_n;
@@ -252,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         load(first);
         for (int kb = first; kb < p.kb_n; kb += 2) {
           const uint32_t i = it + kb, buf = i % G::bufs;
-          ok = mbar_wait_bounded(tempty + 8 * buf, ((i / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = warp_wait(sempty + 8 * buf, ((i / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
           if (!ok) break;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -265,40 +381,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         }
         it += p.kb_n;
       }
-    } else if (warp == kEpiWarps + 1 && lane == 0) {  // ------------------------ MMA
-      constexpr uint32_t idesc = idesc_e4m3_f32(kBm, BN);
-      uint32_t it = 0;
+    } else if (warp == kEpiWarps + 1 && rank == 0) {  // ------------------------ MMA
+      // The warp stays together and one elected lane issues: descriptors and barriers are then uniform values, which
+      // the instructions take as they are. (From a single lane's branch, with the stage by division, a K block took
+      // this warp 920 clocks at 256 x 256, against 512 of products.)
+      constexpr uint32_t idesc = idesc_e4m3_f32(G::bm, BN);
+      uint32_t it = 0, st = 0, phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < walk.total; t += gridDim.x) {
+      for (int t = cta; ok && t < walk.total; t += ctas) {
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
-          const uint32_t st = it % G::stages, buf = it % G::bufs;
-          if (!mbar_wait_bounded(full + 8 * st, (it / G::stages) & 1u, abort, p.err, p.timeout_ns) ||
-              !mbar_wait_bounded(tempty + 8 * buf, ((it / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns)) {
-            ok = false;
-            break;
-          }
+          const uint32_t buf = it % G::bufs;
+          ok = wait_for(full + 8 * st, phase, abort, p.err, p.timeout_ns) &&
+               wait_for(tempty + 8 * buf, ((it / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t src = ring + st * G::stage;
           const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kBk);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBk / 32; ++k)  // 32 columns (32 bytes) per instruction
-            tc_mma_e4m3(tmem + buf * BN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-          tc_commit(empty + 8 * st);
-          tc_commit(tfull + 8 * buf);
+            for (int k = 0; k < kBk / 32; ++k)  // 32 columns (32 bytes) per instruction
+              tc_mma_e4m3<PAIR>(tmem + buf * BN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+            commit<PAIR>(tfull + 8 * buf);
+            commit<PAIR>(empty + 8 * st);
+          }
+          __syncwarp();
+          if (++st == G::stages) {
+            st = 0;
+            phase ^= 1u;
+          }
         }
       }
       // no exit with products in flight: the last accumulators are complete
       for (uint32_t i = it > G::bufs ? it - G::bufs : 0; i < it; ++i) {
         int done = 0;
-        mbar_wait_bounded(tfull + 8 * (i % G::bufs), (i / G::bufs) & 1u, &done, p.err, p.timeout_ns);
+        wait_for(tfull + 8 * (i % G::bufs), (i / G::bufs) & 1u, &done, p.err, p.timeout_ns);
       }
     }
   } else {  // ------------------------------------------------------------------ epilogue
     take_registers<kRegsMany>();
+    const uint32_t read = PAIR ? mapa_shared(tempty, 0) : tempty;  // the barriers that the MMA thread waits on
+    auto release = [&](uint32_t buf) {
+      __syncwarp();
+      if (lane != 0) return;
+      if constexpr (PAIR) arrive_cluster(read + 8 * buf);
+      else mbar_arrive(read + 8 * buf);
+      mbar_arrive(sempty + 8 * buf);
+    };
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 32, columns kCols half .. + kCols
     uint32_t it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < walk.total; t += gridDim.x) {
+    for (int t = cta; ok && t < walk.total; t += ctas) {
       int e, row0, rows, nt;
       walk.at(t, &e, &row0, &rows, &nt);
       const int r = quarter * 32 + lane, row = row0 + r;
@@ -310,31 +443,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       for (int c = 0; c < kCols / 2; ++c) acc[c] = 0ull;
       for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
         const uint32_t buf = it % G::bufs;
-        ok = mbar_wait_bounded(tfull + 8 * buf, (it / G::bufs) & 1u, abort, p.err, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(tfull + 8 * buf, (it / G::bufs) & 1u, abort, p.err, p.timeout_ns);
         if (!ok) break;
         if (any) {
-          // 32 columns are on their way from TMEM while the 32 before them are added
+          // The accumulator is free for the products after the next ones as soon as its last columns are on their
+          // way, so loads go in two rounds of two (a load answers after 200 clocks and more) and the sums follow.
           tc_fence_after();
           const uint32_t src = tmem + buf * BN + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+          float v0[32], v1[32];
+          tmem_ld32(src, v0);
+          tmem_ld32(src + 32, v1);
           const float s = s_scale[buf][half][r];
           const uint64_t s2 = pair(s, s);
-          float v[2][32];
-          tmem_ld32(src, v[0]);
-#pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
-            tmem_ld_wait();
-            if (c + 1 < kCols / 32) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
-            else tc_fence_before();
-            if (c + 1 == kCols / 32) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(tempty + 8 * buf);
-            }
-            add_scaled(acc + 16 * c, v[c & 1], s2);
-          }
+          tmem_ld_wait();
+          add_scaled(acc, v0, s2);
+          tmem_ld32(src + 64, v0);
+          add_scaled(acc + 16, v1, s2);
+          tmem_ld32(src + 96, v1);
+          tmem_ld_wait();
+          tc_fence_before();
+          release(buf);
+          add_scaled(acc + 32, v0, s2);
+          add_scaled(acc + 48, v1, s2);
         } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tempty + 8 * buf);
+          release(buf);
         }
       }
       if (ok && on) {
@@ -343,15 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride + n0;
           if (p.g.wide_out && n == kCols) {
 #pragma unroll
-            for (int c = 0; c < kCols / 2; c += 4) {
-              uint32_t w[4];
+            for (int c = 0; c < kCols / 2; c += 8) {
+              uint32_t w[8];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 const float2 f = unpair(acc[c + j]);
                 const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
                 w[j] = *reinterpret_cast<const uint32_t *>(&h);
               }
-              *reinterpret_cast<uint4 *>(dst + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+              store32(dst + 2 * c, w);
             }
           } else {
 #pragma unroll
@@ -365,9 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           float *dst = static_cast<float *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride + n0;
           if (p.g.wide_out && n == kCols) {
 #pragma unroll
-            for (int c = 0; c < kCols / 2; c += 2) {
-              const float2 f = unpair(acc[c]), h = unpair(acc[c + 1]);
-              *reinterpret_cast<float4 *>(dst + 2 * c) = make_float4(f.x, f.y, h.x, h.y);
+            for (int c = 0; c < kCols / 2; c += 4) {
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = unpair(acc[c + j]);
+                w[2 * j] = __float_as_uint(f.x);
+                w[2 * j + 1] = __float_as_uint(f.y);
+              }
+              store32(dst + 2 * c, w);
             }
           } else {
 #pragma unroll
@@ -383,9 +521,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {  // the other CTA may still reach this one's barriers
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
   }
 }
 
@@ -520,26 +663,47 @@ uint32_t *ops_error_address(int device) {
   return addr[device];
 }
 
-template <int BN, bool BF16> cudaError_t launch_tc(GemmParams &p, cudaStream_t s) {
-  using G = Geo<BN>;
-  auto *fn = &k_fp8_gemm<BN, BF16>;
-  static std::atomic<uint64_t> ready{0};  // devices whose copy of the kernel has its shared memory raised
-  int dev = 0;
+template <bool PAIR, bool BF16> cudaError_t launch_tc(GemmParams &p, cudaStream_t s) {
+  using G = Geo<PAIR>;
+  auto *fn = &k_fp8_gemm<PAIR, BF16>;
+  static std::mutex mu;
+  static int resident[64] = {};  // CTAs that a device holds at once
+  int dev = 0, most = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = G::smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (resident[dev & 63] == 0) {
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
+      if (e != cudaSuccess) return e;
+      int n = num_sms();
+      if (PAIR) {
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / 2 * 2));
+        e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+        if (e != cudaSuccess) return e;
+        n *= 2;
+      }
+      resident[dev & 63] = n;
+    }
+    most = resident[dev & 63];
   }
-  p.nt_n = (p.g.N + BN - 1) / BN;
+  if (most < (PAIR ? 2 : 1)) return cudaErrorNotSupported;
+  p.nt_n = (p.g.N + kBn - 1) / kBn;
   // row tiles: at most one partial tile a group beyond the full ones
-  const int64_t mt = p.g.offsets ? p.g.m / kBm + p.g.n_groups : (p.g.m + kBm - 1) / kBm;
-  const int64_t tiles = mt * p.nt_n;
-  const int grid = static_cast<int>(tiles < num_sms() ? tiles : num_sms());
-  fn<<<grid, kThreads, G::smem, s>>>(p);
-  return cudaGetLastError();
+  const int64_t mt = p.g.offsets ? p.g.m / G::bm + p.g.n_groups : (p.g.m + G::bm - 1) / G::bm;
+  const int64_t ctas = mt * p.nt_n * (PAIR ? 2 : 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 template <int NT> cudaError_t launch_small(const GemmArgs &a, int kb_n, int nb_n, cudaStream_t s) {
@@ -570,19 +734,23 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   GemmParams p;
   memset(&p, 0, sizeof(p));
   p.g = a;
-  p.g.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % (a.out_bf16 ? 8 : 4) == 0;
+  p.g.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && a.out_stride % (a.out_bf16 ? 16 : 8) == 0;
   p.kb_n = kb_n;
   p.nb_n = nb_n;
   p.err = ops_error_word();
   p.timeout_ns = 2000000000ll;
   if (p.err == nullptr || !tma_encode_init()) return cudaErrorInitializationError;
-  const int bn = 256;
   const int64_t E = a.offsets ? a.n_groups : 1;
-  bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, bn);
-  if (ok && a.offsets)
+  // Two CTAs a tile where the groups have rows for it: they read 2/3 of the bytes from L2 that single ones do,
+  // which bounds many rows; groups of fewer rows would leave the second CTA's half of the tile empty.
+  const bool pairs = a.m >= 256 * E;
+  const uint32_t b_rows = pairs ? Geo<true>::b_rows : Geo<false>::b_rows;
+  bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, b_rows);
+  if (ok && !pairs && a.offsets)
     ok = encode_kmajor_8bit(&p.a[0], a.a, a.K, a.m, 32) && encode_kmajor_8bit(&p.a[1], a.a, a.K, a.m, 64);
   if (!ok) return cudaErrorInvalidValue;
-  return a.out_bf16 ? launch_tc<256, true>(p, s) : launch_tc<256, false>(p, s);
+  if (pairs) return a.out_bf16 ? launch_tc<true, true>(p, s) : launch_tc<true, false>(p, s);
+  return a.out_bf16 ? launch_tc<false, true>(p, s) : launch_tc<false, false>(p, s);
 }
 
 }  // namespace epoch
