@@ -40,6 +40,7 @@ constexpr int kMaxGroups = 1024;
 struct GemmParams {
   CUtensorMap a[3];  // boxes of 32, 64, 128 rows
   CUtensorMap b;     // boxes of the rows that a CTA loads
+  CUtensorMap out;   // boxes of 64 columns x 32 rows of a bf16 output (pairs)
   GemmArgs g;
   int kb_n, nb_n, nt_n;  // K blocks, N scale blocks, N tiles
   uint32_t *err;
@@ -243,9 +244,10 @@ template <bool PAIR> struct Geo {
   static constexpr int bm = PAIR ? 2 * kBm : kBm;
   static constexpr int b_rows = PAIR ? kBn / 2 : kBn;
   static constexpr int stage = (kBm + b_rows) * kBk;
-  static constexpr int stages = PAIR ? 6 : 4;
-  static constexpr int bufs = 2;  // TMEM accumulators
-  static constexpr int smem = 1024 + stages * stage;
+  static constexpr int stages = 4;
+  static constexpr int bufs = 2;                                           // TMEM accumulators
+  static constexpr int out_bytes = PAIR ? kBm * kBn * 2 : 0;               // a bf16 tile on its way out
+  static constexpr int smem = 1024 + stages * stage + out_bytes;
 };
 
 template <bool PAIR, bool BF16>
@@ -469,7 +471,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           release(buf);
         }
       }
-      if (ok && on) {
+      // A pair's warp whose 32 rows all exist leaves its part to two bulk stores, which run under the next tile's
+      // products (rows behind a group's last one belong to another tile: such a warp stores row by row).
+      bool stored = false;
+      if constexpr (PAIR && BF16) {
+        if (ok && p.g.bulk_out && rows >= quarter * 32 + 32 && n0 < p.g.N) {
+          stored = true;
+          uint8_t *mine = smem_raw + (ring - smem_u32(smem_raw)) + G::stages * G::stage + warp * 8192;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before has left
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {  // 16 bytes at a time, in the 128-byte swizzle
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpair(acc[4 * c + j]);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+              w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(mine + (c >> 3) * 4096 + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (n0 + 64 * h < p.g.N)
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                 reinterpret_cast<uint64_t>(&p.out)),
+                             "r"(n0 + 64 * h), "r"(row0 + quarter * 32), "r"(smem_u32(mine) + 4096 * h)
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      }
+      if (ok && on && !stored) {
         const int n = min(kCols, p.g.N - n0);
         if constexpr (BF16) {
           __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride + n0;
@@ -518,6 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         }
       }
     }
+  }
+  if constexpr (PAIR && BF16) {  // no exit with stores still reading shared memory
+    if (warp < kEpiWarps && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -748,6 +789,10 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, b_rows);
   if (ok && !pairs && a.offsets)
     ok = encode_kmajor_8bit(&p.a[0], a.a, a.K, a.m, 32) && encode_kmajor_8bit(&p.a[1], a.a, a.K, a.m, 64);
+  if (ok && pairs && a.out_bf16 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.m == 1 || a.out_stride % 8 == 0)) {
+    ok = encode_rows_bf16(&p.out, a.out, a.N, a.m, a.out_stride);
+    p.g.bulk_out = 1;
+  }
   if (!ok) return cudaErrorInvalidValue;
   if (pairs) return a.out_bf16 ? launch_tc<true, true>(p, s) : launch_tc<true, false>(p, s);
   return a.out_bf16 ? launch_tc<false, true>(p, s) : launch_tc<false, false>(p, s);

@@ -261,6 +261,8 @@ bool gate_builds_worklist(const Dims &d);
 
 // Row-major [rows][k_elems] 8-bit matrix, boxes of 128 (K) x box_rows, 128-byte swizzle.
 bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, uint64_t rows, uint32_t box_rows);
+// bf16 output of `rows` rows of `cols` columns, `stride` elements apart: boxes of 64 columns x 32 rows, 128-byte swizzle.
+bool encode_rows_bf16(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, uint64_t stride);
 
 int num_sms();
 
@@ -305,6 +307,7 @@ struct GemmArgs {
   int32_t m, N, K, n_groups;
   int32_t out_bf16;
   int32_t wide_out;  // rows of the output start on 32-byte boundaries
+  int32_t bulk_out;  // the output has a tensor map
 };
 cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s);
 // Device error word of the operators without a layer, on the current device (nullptr: none).
