@@ -35,32 +35,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+__device__ __forceinline__ Vec8<__nv_bfloat16> load_vec(const __nv_bfloat16 *p) {
+  Vec8<__nv_bfloat16> v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Vec8<float> load_vec(const float *p) {
+  Vec8<float> v;
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.a.x), "=f"(v.a.y), "=f"(v.a.z), "=f"(v.a.w)
+               : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.b.x), "=f"(v.b.y), "=f"(v.b.z), "=f"(v.b.w)
+               : "l"(p + 4));
+  return v;
+}
+__device__ __forceinline__ void unpack_vec(const Vec8<__nv_bfloat16> &u, float (&v)[8]) {
+  unpack2(u.a.x, v[0], v[1]);
+  unpack2(u.a.y, v[2], v[3]);
+  unpack2(u.a.z, v[4], v[5]);
+  unpack2(u.a.w, v[6], v[7]);
+}
+__device__ __forceinline__ void unpack_vec(const Vec8<float> &u, float (&v)[8]) {
+  v[0] = u.a.x, v[1] = u.a.y, v[2] = u.a.z, v[3] = u.a.w;
+  v[4] = u.b.x, v[5] = u.b.y, v[6] = u.b.z, v[7] = u.b.w;
+}
+
 // E consecutive elements at p as fp32: E = 8 with 16-byte loads, E = 1 scalar.
 // Streamed: rows are read once and need no place in L1.
-template <int E> __device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float (&v)[E]) {
-  if constexpr (E == 8) {
-    uint4 u;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                 : "l"(p));
-    unpack2(u.x, v[0], v[1]);
-    unpack2(u.y, v[2], v[3]);
-    unpack2(u.z, v[4], v[5]);
-    unpack2(u.w, v[6], v[7]);
-  } else {
-    v[0] = __bfloat162float(*p);
-  }
-}
-template <int E> __device__ __forceinline__ void load_row(const float *p, float (&v)[E]) {
-  if constexpr (E == 8) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
-                   : "l"(p + 4 * h));
-  } else {
-    v[0] = *p;
-  }
+template <int E, typename T> __device__ __forceinline__ void load_row(const T *p, float (&v)[E]) {
+  if constexpr (E == 8) unpack_vec(load_vec(p), v);
+  else v[0] = to_f32(*p);
 }
 template <int E> __device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&v)[E]) {
   if constexpr (E == 8)
@@ -98,16 +105,18 @@ template <int E> __device__ __forceinline__ void load_par(const void *p, int bf1
 }
 
 // Sum of v over the `warps` warps of this thread's row (warp `w` of them;
-// row_sums: their slots in shared memory). Every thread of the CTA calls it.
-__device__ __forceinline__ float row_sum(float v, int warps, int w, float *row_sums) {
+// row_sums: their slots in shared memory, two sets 32 apart that consecutive sums
+// alternate between, so each needs one barrier). Every thread of the CTA calls it.
+__device__ __forceinline__ float row_sum(float v, int warps, int w, float *row_sums, int &turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (warps == 1) return v;
-  if (lane_id() == 0) row_sums[w] = v;
+  float *at = row_sums + 32 * turn;
+  turn ^= 1;
+  if (lane_id() == 0) at[w] = v;
   __syncthreads();
   float s = 0.f;
-  for (int i = 0; i < warps; ++i) s += row_sums[i];
-  __syncthreads();
+  for (int i = 0; i < warps; ++i) s += at[i];
   return s;
 }
 
@@ -118,8 +127,9 @@ __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-
 // the registers hold, and every pass reads the row again -- from L2 or L1, and
 // only elements that the same thread writes at the end, so out may be r).
 template <typename TA, typename TR, bool AFTER, int E, int VPT>
-__global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const NormArgs a, int tpr) {
-  __shared__ float sums[32];
+__global__ void __launch_bounds__(512, E == 8 && VPT <= 2 ? 2 : 1) k_block_norm(const NormArgs a, int tpr) {
+  __shared__ float sums[64];
+  int turn = 0;
   const int p = threadIdx.x & (tpr - 1);
   const int warps = tpr >> 5, w = p >> 5;
   float *row_sums = sums + (threadIdx.x >> 5) - w;
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const
           sq += v * v;
         }
       if constexpr (!AFTER) {
-        const float k = rsqrtf(row_sum(sq, warps, w, row_sums) * inv_h + a.eps);
+        const float k = rsqrtf(row_sum(sq, warps, w, row_sums, turn) * inv_h + a.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int c = E * p + i * step;
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const
         }
       } else {
         float k = 1.f;
-        if (a.weight) k = rsqrtf(row_sum(sq, warps, w, row_sums) * inv_h + a.eps);
+        if (a.weight) k = rsqrtf(row_sum(sq, warps, w, row_sums, turn) * inv_h + a.eps);
         sq = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const
           }
         }
         if (a.next_weight) {
-          k = rsqrtf(row_sum(sq, warps, w, row_sums) * inv_h + a.eps);
+          k = rsqrtf(row_sum(sq, warps, w, row_sums, turn) * inv_h + a.eps);
 #pragma unroll
           for (int i = 0; i < VPT; ++i) {
             const int c = E * p + i * step;
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const
 #pragma unroll
           for (int j = 0; j < E; ++j) sq += v[j] * v[j];
         }
-        k = rsqrtf(row_sum(sq, warps, w, row_sums) * inv_h + a.eps);
+        k = rsqrtf(row_sum(sq, warps, w, row_sums, turn) * inv_h + a.eps);
       }
       if constexpr (!AFTER) {
         for (int c = E * p; on && c < a.hidden; c += step) {
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const
 #pragma unroll
             for (int j = 0; j < E; ++j) sq += o[j] * o[j];
           }
-          k2 = rsqrtf(row_sum(sq, warps, w, row_sums) * inv_h + a.eps);
+          k2 = rsqrtf(row_sum(sq, warps, w, row_sums, turn) * inv_h + a.eps);
         }
         for (int c = E * p; on && c < a.hidden; c += step) {
           load_row<E>(blk + c, b);
@@ -265,6 +275,116 @@ __global__ void __launch_bounds__(512, E * VPT <= 16 ? 2 : 1) k_block_norm(const
       }
     }
   }
+}
+
+// Many rows of at most 4096 columns: a CTA stays, every thread keeps its eight
+// columns' parameters in registers (they cost more loads than the rows
+// themselves: up to four fp32 values a column), and the next row is on its way
+// while this one is summed up.
+// FULL: the gate has a value for each row and column, and is read with the row.
+constexpr int kStayThreads = 512;
+template <typename TA, typename TR, bool AFTER, bool FULL>
+__global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormArgs a, int tpr) {
+  __shared__ float sums[64];
+  int turn = 0;
+  const int c = 8 * (threadIdx.x & (tpr - 1));
+  const int warps = tpr >> 5, w = (threadIdx.x & (tpr - 1)) >> 5;
+  float *row_sums = sums + (threadIdx.x >> 5) - w;
+  const int rpb = blockDim.x / tpr;
+  const float inv_h = 1.0f / static_cast<float>(a.hidden);
+  const bool in = c < a.hidden;
+  float wt[8], sc[8], nw[8], gt[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    wt[j] = gt[j] = 1.f;
+    sc[j] = a.residual_scale;
+    nw[j] = 0.f;
+  }
+  if (in) {
+    if (a.weight) load_par<8>(a.weight, a.par_bf16, c, wt);
+    if constexpr (AFTER) {
+      if (!FULL && a.gate_kind == 1) {
+        load_par<8>(a.gate, a.par_bf16, c, gt);
+        if (a.gate_sigmoid) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gt[j] = sigmoid(gt[j]);
+        }
+      }
+      if (a.scale) load_par<8>(a.scale, a.par_bf16, c, sc);
+      if (a.next_weight) load_par<8>(a.next_weight, a.par_bf16, c, nw);
+    }
+  }
+  Vec8<TR> r_next;
+  Vec8<TA> b_next, g_next;
+  auto fetch = [&](int64_t row) {
+    if (!in || row >= a.n_rows) return;
+    r_next = load_vec(static_cast<const TR *>(a.residual) + row * a.residual_stride + c);
+    if constexpr (AFTER) b_next = load_vec(static_cast<const TA *>(a.block) + row * a.block_stride + c);
+    if constexpr (FULL) g_next = load_vec(static_cast<const TA *>(a.gate) + row * a.gate_stride + c);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
+  const int64_t mine = threadIdx.x / tpr;
+  fetch(static_cast<int64_t>(blockIdx.x) * rpb + mine);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.n_rows; r0 += step) {
+    const int64_t row = r0 + mine;
+    const bool on = in && row < a.n_rows;
+    float r[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = b[j] = 0.f;
+    if (on) {
+      unpack_vec(r_next, r);
+      if constexpr (AFTER) unpack_vec(b_next, b);
+    }
+    float sq = 0.f, k = 1.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq += AFTER ? b[j] * b[j] : r[j] * r[j];
+    if constexpr (AFTER) {
+      if constexpr (FULL) {
+        float g[8];
+        if (on) {
+          unpack_vec(g_next, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b[j] *= a.gate_sigmoid ? sigmoid(g[j]) : g[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[j] *= sc[j];
+        b[j] *= FULL ? wt[j] : wt[j] * gt[j];
+      }
+    }
+    fetch(row + step);
+    if (!AFTER || a.weight) k = rsqrtf(row_sum(sq, warps, w, row_sums, turn) * inv_h + a.eps);
+    if constexpr (!AFTER) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] *= k * wt[j];
+      if (on) store_row<8>(static_cast<TA *>(a.out) + row * a.out_stride + c, r);
+    } else {
+      sq = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[j] = fmaf(b[j], k, r[j]);
+        sq += r[j] * r[j];
+      }
+      if (on) store_row<8>(static_cast<TR *>(a.out) + row * a.out_stride + c, r);
+      if (a.next_weight) {
+        k = rsqrtf(row_sum(on ? sq : 0.f, warps, w, row_sums, turn) * inv_h + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] *= k * nw[j];
+        if (on) store_row<8>(static_cast<TA *>(a.next_out) + row * a.next_stride + c, r);
+      }
+    }
+  }
+}
+
+template <typename TA, typename TR, bool AFTER> cudaError_t launch_stay(const NormArgs &a, int tpr, cudaStream_t s) {
+  const int rpb = kStayThreads / tpr;
+  const int64_t blocks = (a.n_rows + rpb - 1) / rpb;
+  const int64_t most = static_cast<int64_t>(num_sms()) * 2;
+  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER><<<grid, kStayThreads, 0, s>>>(a, tpr);
+  else k_block_norm_stay<TA, TR, AFTER, false><<<grid, kStayThreads, 0, s>>>(a, tpr);
+  return cudaGetLastError();
 }
 
 template <typename TA, typename TR, bool AFTER, int E, int VPT>
@@ -279,6 +399,13 @@ cudaError_t launch(const NormArgs &a, int tpr, cudaStream_t s) {
 
 template <typename TA, typename TR, bool AFTER, int E>
 cudaError_t choose(const NormArgs &a, cudaStream_t s) {
+  if constexpr (E == 8) {
+    // The staying CTAs pay for their parameters once: from four rows a thread on.
+    int wide = 32;
+    while (wide < kStayThreads && wide * 8 < a.hidden) wide *= 2;
+    if (a.hidden <= wide * 8 && a.n_rows >= 4ll * 2 * num_sms() * (kStayThreads / wide))
+      return launch_stay<TA, TR, AFTER>(a, wide, s);
+  }
   // threads of a row: enough for 16 values each; 32 values each from 16 warps on
   const int64_t per = 16;
   int tpr = 32;

@@ -49,66 +49,75 @@ template <bool VEC> __device__ __forceinline__ void load8(const float *p, int n,
   }
 }
 
-// Sixteen threads take one block of a row, eight columns each; a CTA takes
-// sixteen consecutive blocks (rows of the output in order, so a CTA reads 4 KB
-// of consecutive bf16 when the rows are).
-template <typename T, bool SWIGLU, bool VEC>
+// Sixteen threads take a block of a row, eight columns each; a CTA takes U times
+// sixteen consecutive blocks, U of them (their row indices first, then their
+// columns) on their way at once: a block is a chain of two loads, five shuffles and a
+// store. 8192 gathered rows of 2048: 13.9 us with U = 1.
+template <typename T, bool SWIGLU, bool VEC, int U>
 __global__ void __launch_bounds__(kQuantThreads) k_fp8_quant(const QuantArgs a, int kb_n) {
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16);
+  constexpr int kHalves = kQuantThreads / 16;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kHalves * U);
   const int64_t row0 = first / kb_n;
-  const int at = static_cast<int>(first - row0 * kb_n) + (threadIdx.x >> 4);
-  const int64_t row = row0 + at / kb_n;
-  const int kb = at % kb_n;
-  const int c = kb * 128 + (threadIdx.x & 15) * 8;
-  const bool on = row < a.n_rows;
-  const int n = on && c < a.cols ? (a.cols - c < 8 ? a.cols - c : 8) : 0;
-  int64_t src = row;
-  if (a.rows != nullptr && on) src = a.rows[row];
-  const bool bad = src < 0 || src >= a.n_src;  // never read: its scales are NaN
-  float v[8];
+  const unsigned at0 = static_cast<unsigned>(first - row0 * kb_n) + (threadIdx.x >> 4);
+  int64_t src[U];
+  float v[U][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  if (n > 0 && !bad) {
-    const T *p = static_cast<const T *>(a.x) + src * a.x_stride + c;
-    load8<VEC>(p, n, v);
-    if constexpr (SWIGLU) {
-      float u[8];
-      load8<VEC>(p + a.cols, n, u);
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + (at0 + u * kHalves) / static_cast<unsigned>(kb_n);
+    src[u] = row;
+    if (a.rows != nullptr && row < a.n_rows) src[u] = __ldg(a.rows + row);
+  }
+  auto place = [&](int u, int64_t *row, int *kb, int *c, int *n) {
+    const unsigned at = at0 + u * kHalves, r = at / static_cast<unsigned>(kb_n);
+    *row = row0 + r;
+    *kb = static_cast<int>(at - r * kb_n);
+    *c = *kb * 128 + (threadIdx.x & 15) * 8;
+    *n = *row < a.n_rows && *c < a.cols ? min(a.cols - *c, 8) : 0;
+  };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * u[i];
+  for (int u = 0; u < U; ++u) {
+    int64_t row;
+    int kb, c, n;
+    place(u, &row, &kb, &c, &n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+    // an index out of range is never followed: its scales are NaN
+    if (n > 0 && src[u] >= 0 && src[u] < a.n_src) {
+      const T *p = static_cast<const T *>(a.x) + src[u] * a.x_stride + c;
+      load8<VEC>(p, n, v[u]);
+      if constexpr (SWIGLU) {
+        float w[8];
+        load8<VEC>(p + a.cols, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = silu(v[u][i]) * w[i];
+      }
     }
   }
-  unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-    m = b > m ? b : m;
-  }
+  for (int u = 0; u < U; ++u) {
+    int64_t row;
+    int kb, c, n;
+    place(u, &row, &kb, &c, &n);
+    unsigned m = 0;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    const unsigned b = __shfl_xor_sync(0xffffffffu, m, o);
-    m = b > m ? b : m;
-  }
-  float s = fp8_scale(m);
-  if (bad) s = __uint_as_float(0x7FC00000u);
-  if (!on) return;
-  if ((threadIdx.x & 15) == 0) a.scales[row * kb_n + kb] = s;
-  if (n == 0) return;
-  const float inv = 1.0f / s;
-  uint8_t *q = a.q + row * a.cols + c;
-  if (VEC || n == 8) {
-    const uint2 out = make_uint2(fp8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                                 fp8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-    if (VEC) {
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[u][i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = fp8_scale(m);
+    if (src[u] < 0 || src[u] >= a.n_src) s = __uint_as_float(0x7FC00000u);
+    if (row < a.n_rows && (threadIdx.x & 15) == 0) a.scales[row * kb_n + kb] = s;
+    if (n == 0) continue;
+    const float inv = 1.0f / s;
+    uint8_t *q = a.q + row * a.cols + c;
+    const uint2 out = make_uint2(fp8_pack4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv),
+                                 fp8_pack4(v[u][4] * inv, v[u][5] * inv, v[u][6] * inv, v[u][7] * inv));
+    if constexpr (VEC) {
       *reinterpret_cast<uint2 *>(q) = out;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = static_cast<uint8_t>((i < 4 ? out.x : out.y) >> (8 * (i & 3)));
+      for (int i = 0; i < 8; ++i)
+        if (i < n) q[i] = static_cast<uint8_t>((i < 4 ? out.x : out.y) >> (8 * (i & 3)));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) q[i] = static_cast<uint8_t>(fp8_pack4(v[i] * inv, 0.f, 0.f, 0.f) & 0xFFu);
   }
 }
 
@@ -142,19 +151,19 @@ __global__ void __launch_bounds__(256) k_fp8_quant_weight(const T *w, int64_t n,
   }
 }
 
-template <typename T> cudaError_t launch_rows(const QuantArgs &a, bool vec, cudaStream_t s) {
+template <typename T, bool SWIGLU, bool VEC> cudaError_t launch_blocks(const QuantArgs &a, cudaStream_t s) {
   const int kb = (a.cols + 127) / 128;
-  const int64_t per = kQuantThreads / 16;
-  const int64_t grid = (a.n_rows * kb + per - 1) / per;
-  const unsigned g = static_cast<unsigned>(grid);
-  if (a.swiglu) {
-    if (vec) k_fp8_quant<T, true, true><<<g, kQuantThreads, 0, s>>>(a, kb);
-    else k_fp8_quant<T, true, false><<<g, kQuantThreads, 0, s>>>(a, kb);
-  } else {
-    if (vec) k_fp8_quant<T, false, true><<<g, kQuantThreads, 0, s>>>(a, kb);
-    else k_fp8_quant<T, false, false><<<g, kQuantThreads, 0, s>>>(a, kb);
-  }
+  const int64_t blocks = a.n_rows * kb, per = kQuantThreads / 16;
+  // four blocks at once where that still leaves every SM eight CTAs
+  if (blocks >= 4 * per * 8 * num_sms())
+    k_fp8_quant<T, SWIGLU, VEC, 4><<<static_cast<unsigned>((blocks + 4 * per - 1) / (4 * per)), kQuantThreads, 0, s>>>(a, kb);
+  else
+    k_fp8_quant<T, SWIGLU, VEC, 1><<<static_cast<unsigned>((blocks + per - 1) / per), kQuantThreads, 0, s>>>(a, kb);
   return cudaGetLastError();
+}
+template <typename T> cudaError_t launch_rows(const QuantArgs &a, bool vec, cudaStream_t s) {
+  if (a.swiglu) return vec ? launch_blocks<T, true, true>(a, s) : launch_blocks<T, true, false>(a, s);
+  return vec ? launch_blocks<T, false, true>(a, s) : launch_blocks<T, false, false>(a, s);
 }
 
 }  // namespace

@@ -159,6 +159,34 @@ def test_norm_after(ops, n, h, at, rt, pt, form):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,h", [(1300, 4096), (2433, 2048), (5001, 1000), (20000, 64), (9731, 8)])
+@pytest.mark.parametrize("at,rt", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("form", ["before", "channel", "full", "no_weight"])
+def test_norms_of_many_rows(ops, n, h, at, rt, form):
+    g = _gen(n + h)
+    b, r = _rnd(g, n, h, dtype=at), _rnd(g, n, h, std=2.0, dtype=rt)
+    w, nw = 1 + _rnd(g, h, std=0.2), 1 + _rnd(g, h, std=0.2)
+    if form == "before":
+        want = _rms64(r.double(), w.double(), 1e-6)[1]
+        _within(ops.norm_before(r, w, out_dtype=at), want, want.abs() * (_norm_units(h) * U + _half(at)) + 1e-30)
+        return
+    gate, sig, scale = None, False, 1.0
+    if form == "channel":
+        gate, sig, scale = _rnd(g, h), True, 1 + _rnd(g, h, std=0.1)
+    elif form == "full":
+        gate, sig, scale = _rnd(g, n, h, std=3.0, dtype=at), True, 0.75
+    else:
+        w = None
+    got = ops.norm_after(b, r, w, gate=gate, gate_sigmoid=sig, residual_scale=scale, next_weight=nw)
+    out, e_out, nxt, e_nxt = _after64(b, r, w, gate, sig, scale, nw, 1e-6)
+    _within(got[0], out, e_out + out.abs() * _half(rt) * (1 + 2 ** -7) + 1e-30, "r'")
+    _within(got[1], nxt, e_nxt + nxt.abs() * _half(at) * (1 + 2 ** -7) + 1e-30, "h'")
+    alone = ops.norm_after(b, r, w, gate=gate, gate_sigmoid=sig, residual_scale=scale, next_weight=None)
+    assert torch.equal(alone, got[0])
+    assert torch.equal(ops.norm_after(b, r, w, gate=gate, gate_sigmoid=sig, residual_scale=scale, out=r), got[0])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("h", [1024, 1023, 16400])
 def test_norm_after_in_place_and_strided(ops, h):
     g = _gen(11)
@@ -195,7 +223,7 @@ def _quant64(v):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", [BF16, F32])
-@pytest.mark.parametrize("n,k", [(1, 1), (1, 128), (1, 2048), (3, 130), (5, 1001), (64, 512), (333, 264), (2, 4096)])
+@pytest.mark.parametrize("n,k", [(1, 1), (1, 128), (1, 2048), (3, 130), (5, 1001), (64, 512), (333, 264), (2, 4096), (9000, 2048), (20011, 520), (30000, 333)])
 def test_fp8_quantize_rows(ops, n, k, dt):
     x = _rnd(_gen(n + k), n, k, dtype=dt)
     x[0, : max(1, k // 2)] = 0
@@ -310,7 +338,8 @@ def _product_bound(y, s, k, out):
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 4096, 2048), (2, 15, 128), (7, 130, 144), (9, 33, 640), (16, 256, 48),
                                    (31, 200, 1040), (64, 129, 512), (65, 64, 128), (65, 1, 16), (128, 256, 256),
-                                   (129, 300, 272), (200, 511, 1168), (257, 513, 2064), (1000, 1024, 512)])
+                                   (129, 300, 272), (200, 511, 1168), (257, 513, 2064), (1000, 1024, 512), (511, 584, 256),
+                                   (256, 8, 400)])
 def test_fp8_matmul_dense(ops, m, n, k, out):
     qa, sa, qb, sb = _operands(ops, _gen(m * n + k), m, n, k, 1)
     got = ops.fp8_matmul(qa, sa, qb[0], sb[0], out_dtype=out)
@@ -326,6 +355,7 @@ GROUPS = {
     "ragged": [0, 1, 130, 130, 163, 420, 421],
     "boxes": [0, 32, 97, 161, 290, 546],
     "late_start": [3, 10, 80, 100],
+    "wide": [0, 300, 301, 302, 1200],
 }
 
 
