@@ -441,27 +441,31 @@ epoch_status epoch_norm_before(const void *x_dev, int64_t x_stride, int32_t x_dt
 
 /* Norm after a block fused with the block's gate, the residual scale and the
  * next block's norm:
- *   z  = block / sqrt(mean(block^2) + eps) * weight   (weight_dev NULL: z = block)
- *   r' = s * residual + g * z                          -> out_dev, residual_dtype
- *   h' = r' / sqrt(mean(r'^2) + eps) * next_weight     -> next_out_dev, dtype (next_weight_dev
+ *   z  = block / sqrt(mean(block^2) + eps) * weight   (weight NULL: z = block)
+ *   r' = s * residual + g * z                          -> out, residual_dtype
+ *   h' = r' / sqrt(mean(r'^2) + eps) * next_weight     -> next_out, dtype (next_weight
  *        NULL: not computed), from r' before its rounding
- *  block_dev [n_rows][hidden] of dtype; residual_dev, out_dev of
- *  residual_dtype; per-channel parameters (weight, next_weight, scale, a
- *  channel gate) of par_dtype.
- *  s: scale_dev [hidden], or residual_scale where scale_dev is NULL.
- *  g: gate_kind EPOCH_GATE_NONE 1; EPOCH_GATE_CHANNEL gate_dev [hidden];
- *  EPOCH_GATE_FULL gate_dev [n_rows][hidden] of dtype; through the logistic
+ *  block [n_rows][hidden] of dtype; residual, out of residual_dtype; per-channel
+ *  parameters (weight, next_weight, scale, a channel gate) of par_dtype.
+ *  s: scale [hidden], or residual_scale where scale is NULL.
+ *  g: gate_kind EPOCH_GATE_NONE 1; EPOCH_GATE_CHANNEL gate [hidden];
+ *  EPOCH_GATE_FULL gate [n_rows][hidden] of dtype; through the logistic
  *  function first where gate_sigmoid is nonzero.
- *  out_dev may be residual_dev, next_out_dev may be block_dev (same strides).
- * EPOCH_EINVAL as epoch_norm_before, for a gate_kind without its gate, and for
- * exactly one of next_weight_dev and next_out_dev. */
+ *  out may be residual, next_out may be block (same strides).
+ * EPOCH_EINVAL as epoch_norm_before, for a NULL args, a gate_kind without its
+ * gate, and for exactly one of next_weight and next_out. */
 enum { EPOCH_GATE_NONE = 0, EPOCH_GATE_CHANNEL = 1, EPOCH_GATE_FULL = 2 };
-epoch_status epoch_norm_after(const void *block_dev, int64_t block_stride, int32_t dtype, const void *residual_dev,
-                              int64_t residual_stride, int32_t residual_dtype, const void *weight_dev,
-                              const void *gate_dev, int64_t gate_stride, int32_t gate_kind, int32_t gate_sigmoid,
-                              const void *scale_dev, float residual_scale, const void *next_weight_dev,
-                              int32_t par_dtype, int32_t n_rows, int32_t hidden, float eps, void *out_dev,
-                              int64_t out_stride, void *next_out_dev, int64_t next_stride, epoch_stream stream);
+typedef struct {
+  const void *block, *residual;                       /* device, as all pointers here */
+  const void *weight, *gate, *scale, *next_weight;    /* any may be NULL */
+  void *out, *next_out;
+  int64_t block_stride, residual_stride, gate_stride, out_stride, next_stride;
+  int32_t n_rows, hidden;
+  int32_t dtype, residual_dtype, par_dtype;
+  int32_t gate_kind, gate_sigmoid;
+  float residual_scale, eps;
+} epoch_norm_after_args;
+epoch_status epoch_norm_after(const epoch_norm_after_args *args, epoch_stream stream);
 
 /* Quantisation to e4m3 (8-bit floating point, 4 exponent and 3 mantissa bits)
  * with one fp32 scale for each 128 consecutive columns of a row:

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +40,9 @@ class epoch_layer_weights(C.Structure):
                 ("w_up", C.c_void_p), ("w_down", C.c_void_p), ("ws_gate", C.c_void_p),
                 ("ws_up", C.c_void_p), ("ws_down", C.c_void_p)]
 
+
+# epoch_norm_after_args, in the C compiler's layout
+NORM_AFTER_ARGS = struct.Struct("@PPPPPPPPqqqqqiiiiiiiff")
 
 STATS_FIELDS = ("iteration", "n_pos", "n_live", "n_new", "n_miss", "n_stale", "n_forced", "n_reuse",
                 "n_fresh", "n_edges", "n_hit_experts", "support_len", "fallback", "bad_flags",
@@ -100,10 +104,8 @@ _SIGS = {
                                              C.c_void_p, C.c_void_p, C.c_void_p]),
     "epoch_norm_before": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                     C.c_float, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
-    "epoch_norm_after": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
-                                   C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_float, C.c_void_p,
-                                   C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_int64, C.c_void_p,
-                                   C.c_int64, C.c_void_p]),
+    # a packed NORM_AFTER_ARGS
+    "epoch_norm_after": (C.c_int, [C.c_char_p, C.c_void_p]),
     "epoch_fp8_quantize": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                      C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
     "epoch_fp8_quantize_weight": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,

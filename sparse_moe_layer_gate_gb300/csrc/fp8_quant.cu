@@ -19,106 +19,125 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 
-template <bool VEC> __device__ __forceinline__ void load8(const __nv_bfloat16 *p, int n, float (&v)[8]) {
-  if constexpr (VEC) {
-    uint4 u;
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16], unsigned &m) {
+  uint4 u[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                 : "l"(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                 : "=r"(u[h].x), "=r"(u[h].y), "=r"(u[h].z), "=r"(u[h].w)
+                 : "l"(p + 8 * h));
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  uint32_t big = 0;  // largest magnitudes of the low and of the high halves
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+  for (int i = 0; i < 8; ++i) {
+    big = __vmaxu2(big, w[i] & 0x7FFF7FFFu);
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+  m = max(big << 16, big & 0xFFFF0000u);
 }
-template <bool VEC> __device__ __forceinline__ void load8(const float *p, int n, float (&v)[8]) {
-  if constexpr (VEC) {
+__device__ __forceinline__ void load16(const float *p, float (&v)[16], unsigned &m) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
-                   : "l"(p + 4 * h));
-  } else {
+  for (int h = 0; h < 4; ++h)
+    asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
+                 : "l"(p + 4 * h));
+  m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
-  }
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 }
 
-// Sixteen threads take a block of a row, eight columns each; a CTA takes U times
-// sixteen consecutive blocks, U of them (their row indices first, then their
-// columns) on their way at once: a block is a chain of two loads, five shuffles and a
-// store. 8192 gathered rows of 2048: 13.9 us with U = 1.
-template <typename T, bool SWIGLU, bool VEC, int U>
-__global__ void __launch_bounds__(kQuantThreads) k_fp8_quant(const QuantArgs a, int kb_n) {
-  constexpr int kHalves = kQuantThreads / 16;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kHalves * U);
-  const int64_t row0 = first / kb_n;
-  const unsigned at0 = static_cast<unsigned>(first - row0 * kb_n) + (threadIdx.x >> 4);
-  int64_t src[U];
-  float v[U][8];
+// Rows of whole 16-column pieces: eight threads take a block, sixteen columns
+// each, and a CTA a tile of 2^tx blocks of a row x 32 / 2^tx rows, where 2^tx is the
+// largest power of two (up to 32) that divides a row's blocks: places follow by
+// shifts. The instructions of a block bound this kernel (13.9 us at 8192 gathered
+// rows of 2048 with eight columns a thread and places by division).
+template <typename T, bool SWIGLU>
+__global__ void __launch_bounds__(kQuantThreads) k_fp8_quant_wide(const QuantArgs a, int kb_n, int tx) {
+  const unsigned tiles_x = static_cast<unsigned>(kb_n) >> tx;
+  const unsigned ty = blockIdx.x / tiles_x;
+  const int local = threadIdx.x >> 3;
+  const int kb = static_cast<int>((blockIdx.x - ty * tiles_x) << tx) + (local & ((1 << tx) - 1));
+  const int64_t row = static_cast<int64_t>(ty) * (32 >> tx) + (local >> tx);
+  if (row >= a.n_rows) return;  // a block's eight threads leave together
+  const unsigned lanes = 0xFFu << (threadIdx.x & 24);
+  const int c = kb * 128 + (threadIdx.x & 7) * 16;
+  int64_t src = row;
+  if (a.rows != nullptr) src = __ldg(a.rows + row);
+  const bool bad = src < 0 || src >= a.n_src;  // never followed: its scales are NaN
+  const bool in = c < a.cols;
+  float v[16];
+  unsigned m = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t row = row0 + (at0 + u * kHalves) / static_cast<unsigned>(kb_n);
-    src[u] = row;
-    if (a.rows != nullptr && row < a.n_rows) src[u] = __ldg(a.rows + row);
-  }
-  auto place = [&](int u, int64_t *row, int *kb, int *c, int *n) {
-    const unsigned at = at0 + u * kHalves, r = at / static_cast<unsigned>(kb_n);
-    *row = row0 + r;
-    *kb = static_cast<int>(at - r * kb_n);
-    *c = *kb * 128 + (threadIdx.x & 15) * 8;
-    *n = *row < a.n_rows && *c < a.cols ? min(a.cols - *c, 8) : 0;
-  };
+  for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  if (in && !bad) {
+    const T *p = static_cast<const T *>(a.x) + src * a.x_stride + c;
+    load16(p, v, m);
+    if constexpr (SWIGLU) {
+      float u[16];
+      unsigned unused;
+      load16(p + a.cols, u, unused);
+      m = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    int64_t row;
-    int kb, c, n;
-    place(u, &row, &kb, &c, &n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-    // an index out of range is never followed: its scales are NaN
-    if (n > 0 && src[u] >= 0 && src[u] < a.n_src) {
-      const T *p = static_cast<const T *>(a.x) + src[u] * a.x_stride + c;
-      load8<VEC>(p, n, v[u]);
-      if constexpr (SWIGLU) {
-        float w[8];
-        load8<VEC>(p + a.cols, n, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = silu(v[u][i]) * w[i];
+      for (int i = 0; i < 16; ++i) {
+        v[i] = silu(v[i]) * u[i];
+        m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    int64_t row;
-    int kb, c, n;
-    place(u, &row, &kb, &c, &n);
-    unsigned m = 0;
+  for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(lanes, m, o));
+  const float s = bad ? __uint_as_float(0x7FC00000u) : fp8_scale(m);
+  if ((threadIdx.x & 7) == 0) a.scales[row * kb_n + kb] = s;
+  if (!in) return;
+  const float inv = 1.0f / s;
+  uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[u][i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 4; ++i) q[i] = fp8_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+  *reinterpret_cast<uint4 *>(a.q + row * a.cols + c) = make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// Any row: sixteen threads take a block, eight columns each; a CTA takes sixteen
+// consecutive blocks.
+template <typename T, bool SWIGLU>
+__global__ void __launch_bounds__(kQuantThreads) k_fp8_quant(const QuantArgs a, int kb_n) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16);
+  const int64_t row0 = first / kb_n;
+  const unsigned at = static_cast<unsigned>(first - row0 * kb_n) + (threadIdx.x >> 4), r = at / static_cast<unsigned>(kb_n);
+  const int64_t row = row0 + r;
+  const int kb = static_cast<int>(at - r * kb_n), c = kb * 128 + (threadIdx.x & 15) * 8;
+  const bool on = row < a.n_rows;
+  const int n = on && c < a.cols ? min(a.cols - c, 8) : 0;
+  int64_t src = row;
+  if (a.rows != nullptr && on) src = __ldg(a.rows + row);
+  const bool bad = src < 0 || src >= a.n_src;
+  float v[8];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = fp8_scale(m);
-    if (src[u] < 0 || src[u] >= a.n_src) s = __uint_as_float(0x7FC00000u);
-    if (row < a.n_rows && (threadIdx.x & 15) == 0) a.scales[row * kb_n + kb] = s;
-    if (n == 0) continue;
-    const float inv = 1.0f / s;
-    uint8_t *q = a.q + row * a.cols + c;
-    const uint2 out = make_uint2(fp8_pack4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv),
-                                 fp8_pack4(v[u][4] * inv, v[u][5] * inv, v[u][6] * inv, v[u][7] * inv));
-    if constexpr (VEC) {
-      *reinterpret_cast<uint2 *>(q) = out;
-    } else {
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (n > 0 && !bad) {
+    const T *p = static_cast<const T *>(a.x) + src * a.x_stride + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v[i] = to_f32(p[i]);
+    if constexpr (SWIGLU) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n) q[i] = static_cast<uint8_t>((i < 4 ? out.x : out.y) >> (8 * (i & 3)));
+        if (i < n) v[i] = silu(v[i]) * to_f32(p[a.cols + i]);
     }
   }
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!on) return;
+  const float s = bad ? __uint_as_float(0x7FC00000u) : fp8_scale(m);
+  if ((threadIdx.x & 15) == 0) a.scales[row * kb_n + kb] = s;
+  const float inv = 1.0f / s;
+  uint8_t *q = a.q + row * a.cols + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) q[i] = static_cast<uint8_t>(fp8_pack4(v[i] * inv, 0.f, 0.f, 0.f) & 0xFFu);
 }
 
 // One CTA per 128 x 128 block of a weight matrix [n][k]; blockIdx.z: the matrix.
@@ -151,28 +170,29 @@ __global__ void __launch_bounds__(256) k_fp8_quant_weight(const T *w, int64_t n,
   }
 }
 
-template <typename T, bool SWIGLU, bool VEC> cudaError_t launch_blocks(const QuantArgs &a, cudaStream_t s) {
+template <typename T, bool SWIGLU> cudaError_t launch_blocks(const QuantArgs &a, bool wide, cudaStream_t s) {
   const int kb = (a.cols + 127) / 128;
-  const int64_t blocks = a.n_rows * kb, per = kQuantThreads / 16;
-  // four blocks at once where that still leaves every SM eight CTAs
-  if (blocks >= 4 * per * 8 * num_sms())
-    k_fp8_quant<T, SWIGLU, VEC, 4><<<static_cast<unsigned>((blocks + 4 * per - 1) / (4 * per)), kQuantThreads, 0, s>>>(a, kb);
-  else
-    k_fp8_quant<T, SWIGLU, VEC, 1><<<static_cast<unsigned>((blocks + per - 1) / per), kQuantThreads, 0, s>>>(a, kb);
+  if (wide) {
+    int tx = 0;
+    while (tx < 5 && (kb >> tx) % 2 == 0) ++tx;
+    const int64_t rows = 32 >> tx, grid = (a.n_rows + rows - 1) / rows * (kb >> tx);
+    k_fp8_quant_wide<T, SWIGLU><<<static_cast<unsigned>(grid), kQuantThreads, 0, s>>>(a, kb, tx);
+  } else {
+    const int64_t per = kQuantThreads / 16, grid = (a.n_rows * kb + per - 1) / per;
+    k_fp8_quant<T, SWIGLU><<<static_cast<unsigned>(grid), kQuantThreads, 0, s>>>(a, kb);
+  }
   return cudaGetLastError();
-}
-template <typename T> cudaError_t launch_rows(const QuantArgs &a, bool vec, cudaStream_t s) {
-  if (a.swiglu) return vec ? launch_blocks<T, true, true>(a, s) : launch_blocks<T, true, false>(a, s);
-  return vec ? launch_blocks<T, false, true>(a, s) : launch_blocks<T, false, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_quant(const QuantArgs &a, bool bf16, cudaStream_t s) {
-  // eight columns at a time where every block of eight starts on a 16-byte (q: 8-byte) boundary
-  const bool vec = a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.x_stride % 8 == 0 &&
-                   (reinterpret_cast<uintptr_t>(a.q) & 7u) == 0;
-  return bf16 ? launch_rows<__nv_bfloat16>(a, vec, s) : launch_rows<float>(a, vec, s);
+  // sixteen columns at a time where every such piece starts on a 16-byte boundary
+  const int64_t per16 = bf16 ? 8 : 4;
+  const bool wide = a.cols % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
+                    (a.n_src <= 1 || a.x_stride % per16 == 0) && (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0;
+  if (a.swiglu) return bf16 ? launch_blocks<__nv_bfloat16, true>(a, wide, s) : launch_blocks<float, true>(a, wide, s);
+  return bf16 ? launch_blocks<__nv_bfloat16, false>(a, wide, s) : launch_blocks<float, false>(a, wide, s);
 }
 
 cudaError_t launch_fp8_quant_weight(const void *w, bool bf16, int64_t mats, int64_t n, int64_t k, uint8_t *q,

@@ -53,53 +53,49 @@ epoch_status epoch_norm_before(const void *x, int64_t x_stride, int32_t x_dtype,
   return status_of(launch_block_norm(a, false, S(stream)));
 }
 
-epoch_status epoch_norm_after(const void *block, int64_t block_stride, int32_t dtype, const void *residual,
-                              int64_t residual_stride, int32_t residual_dtype, const void *weight, const void *gate,
-                              int64_t gate_stride, int32_t gate_kind, int32_t gate_sigmoid, const void *scale,
-                              float residual_scale, const void *next_weight, int32_t par_dtype, int32_t n_rows,
-                              int32_t hidden, float eps, void *out, int64_t out_stride, void *next_out,
-                              int64_t next_stride, epoch_stream stream) {
-  if (n_rows < 0 || hidden < 1 || hidden > kMaxHidden || !dtype_ok(dtype) || !dtype_ok(residual_dtype) ||
-      !dtype_ok(par_dtype) || !std::isfinite(eps) || eps < 0.f)
+epoch_status epoch_norm_after(const epoch_norm_after_args *p, epoch_stream stream) {
+  if (p == nullptr || p->n_rows < 0 || p->hidden < 1 || p->hidden > kMaxHidden || !dtype_ok(p->dtype) ||
+      !dtype_ok(p->residual_dtype) || !dtype_ok(p->par_dtype) || !std::isfinite(p->eps) || p->eps < 0.f)
     return EPOCH_EINVAL;
-  if (gate_kind < EPOCH_GATE_NONE || gate_kind > EPOCH_GATE_FULL) return EPOCH_EINVAL;
-  if (!of_type_or_null(weight, par_dtype) || !of_type_or_null(scale, par_dtype) ||
-      !of_type_or_null(next_weight, par_dtype))
+  if (p->gate_kind < EPOCH_GATE_NONE || p->gate_kind > EPOCH_GATE_FULL) return EPOCH_EINVAL;
+  if (!of_type_or_null(p->weight, p->par_dtype) || !of_type_or_null(p->scale, p->par_dtype) ||
+      !of_type_or_null(p->next_weight, p->par_dtype))
     return EPOCH_EINVAL;
-  if (gate_kind == EPOCH_GATE_CHANNEL && !of_type(gate, par_dtype)) return EPOCH_EINVAL;
-  if (n_rows == 0) return EPOCH_OK;
-  if ((next_weight == nullptr) != (next_out == nullptr)) return EPOCH_EINVAL;
-  if (!of_type(block, dtype) || !of_type(residual, residual_dtype) || !of_type(out, residual_dtype) ||
-      !of_type_or_null(next_out, dtype))
+  if (p->gate_kind == EPOCH_GATE_CHANNEL && !of_type(p->gate, p->par_dtype)) return EPOCH_EINVAL;
+  const int32_t n = p->n_rows, h = p->hidden;
+  if (n == 0) return EPOCH_OK;
+  if ((p->next_weight == nullptr) != (p->next_out == nullptr)) return EPOCH_EINVAL;
+  if (!of_type(p->block, p->dtype) || !of_type(p->residual, p->residual_dtype) || !of_type(p->out, p->residual_dtype) ||
+      !of_type_or_null(p->next_out, p->dtype))
     return EPOCH_EINVAL;
-  if (gate_kind == EPOCH_GATE_FULL && (!of_type(gate, dtype) || !stride_ok(gate_stride, n_rows, hidden)))
+  if (p->gate_kind == EPOCH_GATE_FULL && (!of_type(p->gate, p->dtype) || !stride_ok(p->gate_stride, n, h)))
     return EPOCH_EINVAL;
-  if (!stride_ok(block_stride, n_rows, hidden) || !stride_ok(residual_stride, n_rows, hidden) ||
-      !stride_ok(out_stride, n_rows, hidden) || (next_out != nullptr && !stride_ok(next_stride, n_rows, hidden)))
+  if (!stride_ok(p->block_stride, n, h) || !stride_ok(p->residual_stride, n, h) || !stride_ok(p->out_stride, n, h) ||
+      (p->next_out != nullptr && !stride_ok(p->next_stride, n, h)))
     return EPOCH_EINVAL;
   NormArgs a = {};
-  a.block = block;
-  a.residual = residual;
-  a.weight = weight;
-  a.gate = gate_kind == EPOCH_GATE_NONE ? nullptr : gate;
-  a.scale = scale;
-  a.next_weight = next_weight;
-  a.out = out;
-  a.next_out = next_out;
-  a.block_stride = block_stride;
-  a.residual_stride = residual_stride;
-  a.gate_stride = gate_stride;
-  a.out_stride = out_stride;
-  a.next_stride = next_stride;
-  a.n_rows = n_rows;
-  a.hidden = hidden;
-  a.act_bf16 = dtype == EPOCH_BF16;
-  a.res_bf16 = residual_dtype == EPOCH_BF16;
-  a.par_bf16 = par_dtype == EPOCH_BF16;
-  a.gate_kind = gate_kind;
-  a.gate_sigmoid = gate_sigmoid ? 1 : 0;
-  a.residual_scale = residual_scale;
-  a.eps = eps;
+  a.block = p->block;
+  a.residual = p->residual;
+  a.weight = p->weight;
+  a.gate = p->gate_kind == EPOCH_GATE_NONE ? nullptr : p->gate;
+  a.scale = p->scale;
+  a.next_weight = p->next_weight;
+  a.out = p->out;
+  a.next_out = p->next_out;
+  a.block_stride = p->block_stride;
+  a.residual_stride = p->residual_stride;
+  a.gate_stride = p->gate_stride;
+  a.out_stride = p->out_stride;
+  a.next_stride = p->next_stride;
+  a.n_rows = n;
+  a.hidden = h;
+  a.act_bf16 = p->dtype == EPOCH_BF16;
+  a.res_bf16 = p->residual_dtype == EPOCH_BF16;
+  a.par_bf16 = p->par_dtype == EPOCH_BF16;
+  a.gate_kind = p->gate_kind;
+  a.gate_sigmoid = p->gate_sigmoid ? 1 : 0;
+  a.residual_scale = p->residual_scale;
+  a.eps = p->eps;
   return status_of(launch_block_norm(a, true, S(stream)));
 }
 

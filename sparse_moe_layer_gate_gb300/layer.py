@@ -141,8 +141,8 @@ class EpochLayer:
             self._check_x(y)
             if y.shape != x.shape:
                 raise ValueError("y must have the shape of x")
-        B.check(B.lib().epoch_moe_few(self.handle, x.data_ptr(), x.shape[0], y.data_ptr(), _stream(stream)),
-                "epoch_moe_few")
+        s = torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else stream.cuda_stream
+        B.check(B.lib().epoch_moe_few(self.handle, x.data_ptr(), x.shape[0], y.data_ptr(), s), "epoch_moe_few")
         return y
 
     @staticmethod

@@ -39,7 +39,7 @@ def _device(t: torch.Tensor, what: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
     return dev
 
@@ -51,26 +51,26 @@ def _code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _rows(t: torch.Tensor, dev: int, n: int, h: int, what: str) -> int:
-    """Elements between the rows of a [n, h] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != h or t.get_device() != dev:
-        raise ValueError(f"{what} must be a [{n}, {h}] tensor on cuda:{dev}")
+def _rows(t: torch.Tensor, dev: int, shape, what: str) -> int:
+    """Elements between the rows of a tensor of that shape (n, h) whose rows are contiguous."""
+    if t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{what} must be a {list(shape)} tensor on cuda:{dev}")
+    n, h = shape
     row, col = t.stride()
-    if (col != 1 and h > 1) or (n > 1 and row < h):
+    if n <= 1:
+        row = h
+    if (col != 1 and h > 1) or row < h:
         raise ValueError(f"rows of {what} must be contiguous and must not overlap")
-    return row if n > 1 else h
+    return row
 
 
-def _vector(t: Optional[torch.Tensor], dev: int, h: int, par: Optional[torch.dtype], what: str):
-    """(pointer, parameter dtype so far) of a [h] parameter; every parameter of a call has one dtype."""
-    if t is None:
-        return None, par
-    if t.dim() != 1 or t.shape[0] != h or t.get_device() != dev or not t.is_contiguous():
+def _vector(t: torch.Tensor, dev: int, h: int, par: Optional[torch.dtype], what: str) -> int:
+    """Pointer of a [h] parameter; every parameter of a call has one dtype (par, where one came before)."""
+    if t.shape != (h,) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [{h}] tensor on cuda:{dev}")
     if par is not None and t.dtype != par:
         raise ValueError(f"{what} has dtype {t.dtype}, the other parameters {par}")
-    _code(t, what)
-    return t.data_ptr(), t.dtype
+    return t.data_ptr()
 
 
 def norm_before(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
@@ -80,18 +80,18 @@ def norm_before(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, out
     x, weight [H] and the result are float32 or bfloat16 each; ``out`` (which
     may be x) or ``out_dtype`` names the result's dtype (default: x's)."""
     dev = _device(x, "x")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [n, H]")
-    n, h = x.shape
-    xs = _rows(x, dev, n, h, "x")
-    w, par = _vector(weight, dev, h, None, "weight")
+    n, h = shape
+    w = _vector(weight, dev, h, None, "weight")
     if out is None:
-        out = _empty((n, h), out_dtype or x.dtype, x.device, stream)
+        out = _empty(shape, out_dtype or x.dtype, x.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    os = _rows(out, dev, n, h, "out")
-    B.check(B.lib().epoch_norm_before(x.data_ptr(), xs, _code(x, "x"), w, _CODE[par], n, h, eps, out.data_ptr(), os,
-                                      _code(out, "out"), _stream(stream, dev)), "epoch_norm_before")
+    B.check(B.lib().epoch_norm_before(x.data_ptr(), _rows(x, dev, shape, "x"), _code(x, "x"), w, _code(weight, "weight"),
+                                      n, h, eps, out.data_ptr(), _rows(out, dev, shape, "out"), _code(out, "out"),
+                                      _stream(stream, dev)), "epoch_norm_before")
     return out
 
 
@@ -110,58 +110,64 @@ def norm_after(block: torch.Tensor, residual: torch.Tensor, weight: Optional[tor
     through the logistic function. ``out`` may be residual, ``next_out`` block.
     Returns r', or (r', h') with next_weight."""
     dev = _device(block, "block")
-    if block.dim() != 2:
+    shape = block.shape
+    if len(shape) != 2:
         raise ValueError("block must be [n, H]")
-    n, h = block.shape
-    bs = _rows(block, dev, n, h, "block")
-    rs = _rows(residual, dev, n, h, "residual")
-    w, par = _vector(weight, dev, h, None, "weight")
-    nw, par = _vector(next_weight, dev, h, par, "next_weight")
-    scale, number = None, 1.0
+    n, h = shape
+    dtype, res_dtype = block.dtype, residual.dtype
+    par, w, nw, scale, number = None, 0, 0, 0, 1.0
+    if weight is not None:
+        w, par = _vector(weight, dev, h, None, "weight"), weight.dtype
+    if next_weight is not None:
+        nw, par = _vector(next_weight, dev, h, par, "next_weight"), next_weight.dtype
     if isinstance(residual_scale, torch.Tensor):
-        scale, par = _vector(residual_scale, dev, h, par, "residual_scale")
+        scale, par = _vector(residual_scale, dev, h, par, "residual_scale"), residual_scale.dtype
     else:
         number = residual_scale
-    kind, gp, gs = B.EPOCH_GATE_NONE, None, 0
+    kind, gp, gs = B.EPOCH_GATE_NONE, 0, 0
     if gate is not None:
         if gate.dim() == 1:
-            kind = B.EPOCH_GATE_CHANNEL
-            gp, par = _vector(gate, dev, h, par, "gate")
+            kind, gp, par = B.EPOCH_GATE_CHANNEL, _vector(gate, dev, h, par, "gate"), gate.dtype
         else:
-            kind, gp, gs = B.EPOCH_GATE_FULL, gate.data_ptr(), _rows(gate, dev, n, h, "gate")
-            if gate.dtype != block.dtype:
-                raise ValueError(f"gate has dtype {gate.dtype}, block {block.dtype}")
+            kind, gp, gs = B.EPOCH_GATE_FULL, gate.data_ptr(), _rows(gate, dev, shape, "gate")
+            if gate.dtype != dtype:
+                raise ValueError(f"gate has dtype {gate.dtype}, block {dtype}")
     elif gate_sigmoid:
         raise ValueError("gate_sigmoid without a gate")
     if out is None:
-        out = _empty((n, h), residual.dtype, block.device, stream)
-    elif out.dtype != residual.dtype:
-        raise ValueError(f"out has dtype {out.dtype}, residual {residual.dtype}")
-    os = _rows(out, dev, n, h, "out")
-    np_, ns = None, 0
+        out = _empty(shape, res_dtype, block.device, stream)
+    elif out.dtype != res_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, residual {res_dtype}")
+    np_, ns = 0, 0
     if next_weight is not None:
         if next_out is None:
-            next_out = _empty((n, h), block.dtype, block.device, stream)
-        elif next_out.dtype != block.dtype:
-            raise ValueError(f"next_out has dtype {next_out.dtype}, block {block.dtype}")
-        np_, ns = next_out.data_ptr(), _rows(next_out, dev, n, h, "next_out")
+            next_out = _empty(shape, dtype, block.device, stream)
+        elif next_out.dtype != dtype:
+            raise ValueError(f"next_out has dtype {next_out.dtype}, block {dtype}")
+        np_, ns = next_out.data_ptr(), _rows(next_out, dev, shape, "next_out")
     elif next_out is not None:
         raise ValueError("next_out without next_weight")
-    B.check(B.lib().epoch_norm_after(block.data_ptr(), bs, _code(block, "block"), residual.data_ptr(), rs,
-                                     _code(residual, "residual"), w, gp, gs, kind, 1 if gate_sigmoid else 0, scale,
-                                     number, nw, _CODE[par] if par is not None else B.EPOCH_F32, n, h, eps,
-                                     out.data_ptr(), os, np_, ns, _stream(stream, dev)), "epoch_norm_after")
+    code = B.EPOCH_F32
+    if par is not None:
+        code = _CODE.get(par)
+        if code is None:
+            raise ValueError(f"parameters must be float32 or bfloat16, not {par}")
+    args = B.NORM_AFTER_ARGS.pack(
+        block.data_ptr(), residual.data_ptr(), w, gp, scale, nw, out.data_ptr(), np_, _rows(block, dev, shape, "block"),
+        _rows(residual, dev, shape, "residual"), gs, _rows(out, dev, shape, "out"), ns, n, h, _code(block, "block"),
+        _code(residual, "residual"), code, kind, 1 if gate_sigmoid else 0, number, eps)
+    B.check(B.lib().epoch_norm_after(args, _stream(stream, dev)), "epoch_norm_after")
     return out if next_weight is None else (out, next_out)
 
 
 def _bytes(t: torch.Tensor, dev: int, shape, what: str) -> int:
-    if t.dtype != _E4M3 or tuple(t.shape) != tuple(shape) or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype != _E4M3 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float8_e4m3fn tensor {list(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
 def _scales(t: torch.Tensor, dev: int, shape, what: str) -> int:
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 tensor {list(shape)} on cuda:{dev}")
     return t.data_ptr()
 
@@ -193,7 +199,7 @@ def fp8_quantize(x: torch.Tensor, *, rows: Optional[torch.Tensor] = None, swiglu
         k //= 2
     rp = _index(rows, dev, "rows")
     n = src if rows is None else rows.shape[0]
-    xs = _rows(x, dev, src, x.shape[1], "x")
+    xs = _rows(x, dev, x.shape, "x")
     kb = -(-k // BLOCK)
     if q is None:
         q = _empty((n, k), _E4M3, x.device, stream)
@@ -249,7 +255,7 @@ def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
         out = _empty((m, n), out_dtype or torch.bfloat16, a.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    ys = _rows(out, dev, m, n, "out")
+    ys = _rows(out, dev, (m, n), "out")
     B.check(B.lib().epoch_fp8_matmul(ap, asp, bp, bsp, op, groups, m, n, k, out.data_ptr(), ys, _code(out, "out"),
                                      _stream(stream, dev)), "epoch_fp8_matmul")
     return out

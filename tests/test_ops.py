@@ -485,9 +485,8 @@ def lib(ops):
 
 
 BEFORE = dict(x=P, x_stride=64, x_dtype=1, weight=P, par=0, n=4, h=64, eps=1e-6, out=P, out_stride=64, out_dtype=1, stream=None)
-AFTER = dict(block=P, block_stride=64, dtype=1, res=P, res_stride=64, res_dtype=0, weight=P, gate=None, gate_stride=0,
-             kind=0, sig=0, scale=None, number=1.0, nw=None, par=0, n=4, h=64, eps=1e-6, out=P, out_stride=64, nout=None,
-             nstride=0, stream=None)
+AFTER = dict(block=P, res=P, weight=P, gate=0, scale=0, nw=0, out=P, nout=0, block_stride=64, res_stride=64, gate_stride=0,
+             out_stride=64, nstride=0, n=4, h=64, dtype=1, res_dtype=0, par=0, kind=0, sig=0, number=1.0, eps=1e-6)
 QUANT = dict(x=P, x_stride=256, dtype=1, rows=None, n=4, src=4, cols=256, swiglu=0, q=P, s=P, stream=None)
 WEIGHT = dict(w=P, dtype=1, mats=1, n=128, k=128, q=P, s=P, stream=None)
 MATMUL = dict(a=P, sa=P, b=P, sb=P, offsets=None, groups=1, m=4, n=64, k=128, y=P, stride=64, out=1, stream=None)
@@ -500,8 +499,8 @@ def _refusals():
                dict(x=P + 1), dict(weight=P + 2), dict(x_stride=63), dict(out_stride=0)):
         yield "epoch_norm_before", BEFORE, kw
     for kw in (dict(n=-1), dict(h=0), dict(dtype=3), dict(res_dtype=3), dict(par=3), dict(kind=3), dict(kind=-1),
-               dict(kind=1), dict(kind=2), dict(kind=2, gate=P, gate_stride=63), dict(block=None), dict(res=None),
-               dict(out=None), dict(nw=P), dict(nout=P, nstride=64), dict(nw=P, nout=P, nstride=1),
+               dict(kind=1), dict(kind=2), dict(kind=2, gate=P, gate_stride=63), dict(block=0), dict(res=0),
+               dict(out=0), dict(nw=P), dict(nout=P, nstride=64), dict(nw=P, nout=P, nstride=1),
                dict(block_stride=1), dict(res_stride=1), dict(out_stride=1), dict(res=P + 2), dict(eps=math.nan),
                dict(scale=P + 1), dict(nw=P + 1, nout=P, nstride=64)):
         yield "epoch_norm_after", AFTER, kw
@@ -522,16 +521,27 @@ def _refusals():
 @pytest.mark.parametrize("name,base,change", list(_refusals()), ids=lambda v: str(v)[:60] if not isinstance(v, dict) else "")
 def test_refused_on_the_host(lib, name, base, change):
     assert set(change) <= set(base)
-    assert getattr(lib, name)(*{**base, **change}.values()) == 1  # EPOCH_EINVAL, nothing enqueued
+    assert _call(lib, name, {**base, **change}) == 1  # EPOCH_EINVAL, nothing enqueued
+
+
+def _call(lib, name, args):
+    if name == "epoch_norm_after":  # takes a struct
+        from sparse_moe_layer_gate_gb300 import binding
+        return lib.epoch_norm_after(binding.NORM_AFTER_ARGS.pack(*args.values()), None)
+    return getattr(lib, name)(*args.values())
+
+
+def test_norm_after_without_arguments(lib):
+    assert lib.epoch_norm_after(None, None) == 1
 
 
 def test_no_rows_enqueue_nothing(lib):
     for name, base, kw in (("epoch_norm_before", BEFORE, dict(n=0, x=None, out=None)),
-                           ("epoch_norm_after", AFTER, dict(n=0, block=None, res=None, out=None)),
+                           ("epoch_norm_after", AFTER, dict(n=0, block=0, res=0, out=0)),
                            ("epoch_fp8_quantize", QUANT, dict(n=0, src=0, x=None, q=None, s=None)),
                            ("epoch_fp8_quantize_weight", WEIGHT, dict(mats=0, w=None)),
                            ("epoch_fp8_matmul", MATMUL, dict(m=0, a=None, y=None))):
-        assert getattr(lib, name)(*{**base, **kw}.values()) == 0
+        assert _call(lib, name, {**base, **kw}) == 0
 
 
 def test_cpu_tensors_are_refused(ops):
