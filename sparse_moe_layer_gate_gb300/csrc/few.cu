@@ -613,14 +613,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
       [] { return true; });
   grid_arrive(p.ws.ctr);
   for (int e = threadIdx.x; e < E; e += kThreads) r.mask[e][0] = r.mask[e][1] = 0u;
-  if (!grid_wait(p.ws.ctr, p.err, d.timeout_ns)) return;
-
   uint2 *scratch = reinterpret_cast<uint2 *>(part) + warp * 32;
   auto select = [&](int tok, int16_t *sel, float *wgt) {
     if (E <= 64) select_token<2>(p, tok, scratch, sel, wgt);
     else if (E <= 256) select_token<8>(p, tok, scratch, sel, wgt);
     else select_token<32>(p, tok, scratch, sel, wgt);
   };
+  // One warp runs the selection on whatever the logits hold by now, so that its code is in the instruction cache
+  // when the barrier opens (its results are written again below).
+  if (warp == 1 && nt <= kWarps) select(0, r.sel, r.wgt);
+  if (!grid_wait(p.ws.ctr, p.err, d.timeout_ns)) return;
+
   if (nt <= kWarps) {
     if (warp < nt) select(warp, r.sel + warp * k, r.wgt + warp * k);
     __syncthreads();
