@@ -27,7 +27,19 @@
 // 0-7 are gate rows and rows 8-15 the up rows of the same eight columns, so one
 // tile of sums holds both halves of the SwiGLU.
 //
+// Sums are split into a fixed number of parts that meet in a fixed order, and a
+// token is a column of its own in every product, so a token's result is the same
+// bits whatever its neighbours and however often it is computed. Rounding: the
+// activations of bf16 layers, which are an operand of the tensor core (as in the
+// iteration path), and y; everything else is fp32.
+//
 // fp32 layers run the same schedule with FFMA in place of the tensor core.
+//
+// Measured (H 2048, 256 experts of 512 columns, 8 and 1 shared a token, bf16;
+// weights from memory): 1 token 20.8 us, of which 7.8 us are phases 1 and 2 and
+// 1.1 us each barrier; 32 tokens (47 experts) 64 us at 4.7 TB/s, phases 1 and 2
+// at 6.3 TB/s. Reading a unit's rows only (no products, no barriers) reaches
+// 6.1 to 6.4 TB/s at 400 MB with these loads.
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -53,8 +65,8 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<float> {
   static constexpr int step = 16, per = 4;
-  static constexpr int steps = 2;  // its sums and the tokens' columns need the registers of the other two
-  static constexpr int acc = 16;  // rows g and g + 8 of all eight tokens (this thread's columns only)
+  static constexpr int steps = 2;           // its sums and the tokens' columns need the registers of the other two
+  static constexpr int acc = 16;            // rows g and g + 8 of all eight tokens (this thread's columns only)
 };
 
 __device__ __forceinline__ uint4 load_weights(const void *p, bool ok) {
@@ -136,8 +148,8 @@ struct Share {
 
 template <typename T> struct Chunk {
   static constexpr int n = Elem<T>::steps;
-  uint4 a[n], b[n];                   // weight rows g and g + 8
-  uint4 v[sizeof(T) == 2 ? n : 1];              // token row g (bf16)
+  uint4 a[n], b[n];                 // weight rows g and g + 8
+  uint4 v[sizeof(T) == 2 ? n : 1];  // token row g (bf16)
 };
 
 // Whether columns of a K step that a thread holds exist: rows of bf16 layers are
@@ -365,7 +377,7 @@ __device__ __forceinline__ void limit_groups(const float (&c)[EPL], bool (&ok)[E
 // them is a bound that the k best keys reach and few others do. Those are
 // compacted into `scratch` (32 entries of this warp) and ranked against each
 // other. All steps but the last are without loops or branches: a selection is
-// a chain of latencies (2100 clocks as k rounds of a warp maximum).
+// a chain of latencies (k rounds of a warp maximum took 2100 clocks for 8 of 256).
 template <int EPL>
 __device__ __forceinline__ void rank_topk(const float (&c)[EPL], const bool (&ok)[EPL], int k, int *rank, int *sel,
                                           float *val, uint2 *scratch) {
@@ -676,7 +688,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   grp = warp / warps;
   w = warp % warps;
   gthread = threadIdx.x - grp * warps * 32;
-  run_units<T, true>(
+  const bool in_time = run_units<T, true>(
       grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), (r.n_jobs + d.n_sh * nt8) * h16, w, warps, grp,
       part + grp * 2 * warps * 128, act,
       [&](int u, int wi, int ws, Share &o) {
@@ -705,6 +717,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
         }
       },
       [&] { return grid_wait(p.ws.ctr + 2, p.err, d.timeout_ns); });
+  if (!in_time) return;
   grid_arrive(p.ws.ctr + 3);
   if (!grid_wait(p.ws.ctr + 3, p.err, d.timeout_ns)) return;
   if (blockIdx.x == 0 && threadIdx.x < 3) p.ws.ctr[threadIdx.x] = 0;  // every CTA has left these barriers

@@ -286,6 +286,46 @@ def test_streams_graphs_and_outputs(Layer):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 20])
+def test_in_place(Layer, dtype, n):
+    lay, _ = make(Layer, 512, 32, 128, 4, dtype, 1, seed=12, residual=True)
+    x = tokens(512, n, dtype)
+    want = lay.forward_few(x)
+    assert lay.forward_few(x, y=x) is x
+    assert torch.equal(x, want)
+
+
+@pytest.mark.gpu
+def test_two_layers_and_two_graphs_of_one_layer(Layer):
+    """Two layers overlap on two streams; two graphs of one layer, replayed one after the other, share its workspace."""
+    a, _ = make(Layer, 512, 32, 128, 4, "bf16", 1, seed=13)
+    b, _ = make(Layer, 1024, 16, 256, 2, "bf16", 0, seed=14)
+    xa, xb = tokens(512, 30, "bf16"), tokens(1024, 5, "bf16")
+    wa, wb = a.forward_few(xa), b.forward_few(xb)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ya, yb = [], []
+    for _ in range(10):
+        ya.append(a.forward_few(xa, stream=sa))
+        yb.append(b.forward_few(xb, stream=sb))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, wa) for y in ya) and all(torch.equal(y, wb) for y in yb)
+    assert a.status() == (0, 0) and b.status() == (0, 0)
+    graphs = []
+    for n in (3, 30):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = a.forward_few(xa[:n])
+        graphs.append((g, y, n))
+    for _ in range(3):
+        for g, y, n in graphs:
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, wa[:n])
+
+
+@pytest.mark.gpu
 def test_a_wait_that_runs_out_is_reported_and_cleared(Layer):
     """A limit of a microsecond lets the grid barriers give up; the call returns, the status says so, and after
     clearing it the layer works as before."""

@@ -457,6 +457,51 @@ def test_ops_on_a_stream_of_their_own_and_in_a_graph(ops):
     assert torch.equal(oy, want)
 
 
+FIRST_CALL = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from sparse_moe_layer_gate_gb300 import ops
+from sparse_moe_layer_gate_gb300.layer import EpochLayer
+m, n, k = {m}, 320, 512
+a = torch.randn(m, k, device="cuda", dtype=torch.bfloat16)
+w = torch.ones(k, device="cuda")
+qb = torch.randn(n, k, device="cuda").to(torch.float8_e4m3fn)
+sb = torch.ones(3, 4, device="cuda")
+d = dict(device="cuda", dtype=torch.bfloat16)
+lay = EpochLayer(hidden=k, n_experts=8, inter=128, top_k=2, max_positions=16, dtype="bf16", tau=1.0, refresh_R=4,
+                 weights=dict(w_router=torch.randn(8, k, **d), b_router=torch.zeros(8, device="cuda"),
+                              w_gate=torch.randn(8, 128, k, **d) / 22, w_up=torch.randn(8, 128, k, **d) / 22,
+                              w_down=torch.randn(8, k, 128, **d) / 11))
+x = torch.randn(3, k, **d)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    h = ops.norm_before(a, w)
+    q, s = ops.fp8_quantize(h)
+    y = ops.fp8_matmul(q, s, qb, sb)
+    f = lay.forward_few(x)
+g.replay()
+torch.cuda.synchronize()
+h2 = ops.norm_before(a, w)
+assert torch.equal(h, h2) and torch.equal(y, ops.fp8_matmul(*ops.fp8_quantize(h2), qb, sb))
+assert torch.equal(f, lay.forward_few(x)) and ops.status() == (0, 0) and lay.status() == (0, 0)
+print("same")
+"""
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [5, 100, 600])
+def test_a_process_whose_first_calls_are_captured(ops, m):
+    """Whatever a call sets up once per process it can set up under capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root, m=m)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 @pytest.mark.gpu
 def test_two_products_at_once(ops):
     """Calls on two streams share nothing."""
