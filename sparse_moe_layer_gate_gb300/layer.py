@@ -145,6 +145,22 @@ class EpochLayer:
         B.check(B.lib().epoch_moe_few(self.handle, x.data_ptr(), x.shape[0], y.data_ptr(), s), "epoch_moe_few")
         return y
 
+    def worklist(self):
+        """(positions, offsets) of the last iteration's expert-sorted worklist, as
+        int32 views of the workspace in stream order: positions [max_positions *
+        top_k], of which the first offsets[-1] are this iteration's, and offsets
+        [n_experts + 1]. What ops.fp8_quantize (rows) and ops.fp8_matmul (offsets)
+        take, so FP8 experts run over the layer's own routing. The next call on the
+        layer overwrites them."""
+        v = B.epoch_debug_view()
+        B.check(B.lib().epoch_debug_pointers(self.handle, C.byref(v)), "epoch_debug_pointers")
+
+        def view(ptr, n):
+            at = ptr - self._ws.data_ptr()
+            return self._ws[at:at + 4 * n].view(torch.int32)
+
+        return view(v.wl_pos, self.max_positions * self.top_k), view(v.offsets, self.n_experts + 1)
+
     @staticmethod
     def stats_dict(stats: torch.Tensor) -> dict:
         """Host view of a stats tensor that moe_iter filled."""
