@@ -179,6 +179,9 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+__device__ __forceinline__ void load_tmem(uint32_t at, float (&v)[32]) { tmem_ld32(at, v); }
+__device__ __forceinline__ void load_tmem(uint32_t at, float (&v)[16]) { tmem_ld16(at, v); }
+
 // First rows of the groups, in ascending order and within [0, m] whatever the
 // caller's offsets hold (start, E + 1 entries), and the number of row tiles
 // before each group (cum, E + 1 entries). One warp; E <= kMaxGroups.
@@ -237,23 +240,23 @@ struct TileWalk {
   }
 };
 
-// Tiles are 256 columns wide. PAIR: two CTAs take 256 rows, each its own 128 rows
-// of a and half of the weights' rows, which the products of both read.
-constexpr int kBn = 256;
-template <bool PAIR> struct Geo {
+// Tiles are BN columns wide. PAIR (BN = 256): two CTAs take 256 rows, each its own
+// 128 rows of a and half of the weights' rows, which the products of both read.
+template <int BN, bool PAIR> struct Geo {
+  static_assert(!PAIR || BN == 256, "pairs work on 256 columns");
   static constexpr int bm = PAIR ? 2 * kBm : kBm;
-  static constexpr int b_rows = PAIR ? kBn / 2 : kBn;
+  static constexpr int b_rows = PAIR ? BN / 2 : BN;
   static constexpr int stage = (kBm + b_rows) * kBk;
-  static constexpr int stages = 4;
-  static constexpr int bufs = 2;                                           // TMEM accumulators
-  static constexpr int out_bytes = PAIR ? kBm * kBn * 2 : 0;               // a bf16 tile on its way out
+  static constexpr int stages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int bufs = BN == 256 ? 2 : 4;                           // TMEM accumulators
+  static constexpr int tmem = bufs * BN;                                   // their columns
+  static constexpr int out_bytes = PAIR ? kBm * BN * 2 : 0;                // a bf16 tile on its way out
   static constexpr int smem = 1024 + stages * stage + out_bytes;
 };
 
-template <bool PAIR, bool BF16>
+template <int BN, bool PAIR, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ GemmParams p) {
-  using G = Geo<PAIR>;
-  constexpr int BN = kBn;
+  using G = Geo<BN, PAIR>;
   constexpr int kCols = BN / 2;  // columns of an epilogue warpgroup
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * G::stages + 3 * G::bufs];
@@ -269,9 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                  tempty = tfull + 8 * G::bufs, sempty = tempty + 8 * G::bufs;
   if (warp == 0) {
     if constexpr (PAIR) {
-      tmem_alloc_pair(smem_u32(&s_tmem), 512);
+      tmem_alloc_pair(smem_u32(&s_tmem), G::tmem);
     } else {
-      tmem_alloc(smem_u32(&s_tmem), 512);
+      tmem_alloc(smem_u32(&s_tmem), G::tmem);
       tmem_relinquish();
     }
   } else if (warp == 1) {
@@ -320,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
-        // small groups of single CTAs load the smallest box that holds their rows
-        const int box = PAIR || p.g.offsets == nullptr ? 2 : rows <= 32 ? 0 : rows <= 64 ? 1 : 2;
+        // single CTAs load the smallest box that holds their rows
+        const int box = PAIR || rows > 64 ? 2 : rows > 32 ? 1 : 0;
         const uint32_t bytes = PAIR ? 2 * G::stage : ((32u << box) + BN) * kBk;
         const int brow = e * p.g.N + nt * BN + rank * G::b_rows;
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
@@ -452,21 +455,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           // way, so loads go in two rounds of two (a load answers after 200 clocks and more) and the sums follow.
           tc_fence_after();
           const uint32_t src = tmem + buf * BN + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
-          float v0[32], v1[32];
-          tmem_ld32(src, v0);
-          tmem_ld32(src + 32, v1);
+          constexpr int kLoad = kCols < 32 ? kCols : 32;
+          float v0[kLoad], v1[kLoad];
+          load_tmem(src, v0);
+          if constexpr (kCols > 32) load_tmem(src + 32, v1);
           const float s = s_scale[buf][half][r];
           const uint64_t s2 = pair(s, s);
           tmem_ld_wait();
-          add_scaled(acc, v0, s2);
-          tmem_ld32(src + 64, v0);
-          add_scaled(acc + 16, v1, s2);
-          tmem_ld32(src + 96, v1);
-          tmem_ld_wait();
+          if constexpr (kCols == 128) {
+            add_scaled(acc, v0, s2);
+            load_tmem(src + 64, v0);
+            add_scaled(acc + 16, v1, s2);
+            load_tmem(src + 96, v1);
+            tmem_ld_wait();
+          }
           tc_fence_before();
           release(buf);
-          add_scaled(acc + 32, v0, s2);
-          add_scaled(acc + 48, v1, s2);
+          add_scaled(acc + (kCols == 128 ? 32 : 0), v0, s2);
+          if constexpr (kCols > 32) add_scaled(acc + (kCols == 128 ? 48 : 16), v1, s2);
         } else {
           release(buf);
         }
@@ -568,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   }
   if (warp == 0) {
     tc_fence_after();
-    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
-    else tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, G::tmem);
+    else tmem_dealloc(tmem, G::tmem);
   }
 }
 
@@ -629,37 +635,47 @@ __global__ void __launch_bounds__(32 * kSmallWarps) k_fp8_small(const GemmArgs a
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    for (int kb = warp; kb < kb_n; kb += kSmallWarps) {
-      uint4 wa[2], wb[2];
+    for (int kb0 = warp; kb0 < kb_n; kb0 += 2 * kSmallWarps) {
+      uint4 wa[2][2], wb[2][2];  // two blocks' weights on their way together
+      float sw[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = kb * kFp8Block + 64 * h;
-        const bool in = k + 16 * t < a.K;
-        wa[h] = load16(w + k, w0 && in);
-        wb[h] = load16(w + k + static_cast<int64_t>(8) * a.K, w1 && in);
-      }
-      const float sw = __ldg(sb + kb);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (i * 8 >= rows) break;
-        const int tok = i * 8 + g;
-        const uint8_t *x = static_cast<const uint8_t *>(a.a) + static_cast<int64_t>(row0 + tok) * a.K + 16 * t;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < 2; ++b) {
+        const int kb = kb0 + b * kSmallWarps;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int k = kb * kFp8Block + 64 * h;
-          uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-          if (tok < rows && k + 16 * t < a.K) xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
-          mma_e4m3(part, wa[h].x, wb[h].x, wa[h].y, wb[h].y, xv.x, xv.y);
-          mma_e4m3(part, wa[h].z, wb[h].z, wa[h].w, wb[h].w, xv.z, xv.w);
+          const bool in = k + 16 * t < a.K;  // false for a block behind the last one
+          wa[b][h] = load16(w + k, w0 && in);
+          wb[b][h] = load16(w + k + static_cast<int64_t>(8) * a.K, w1 && in);
         }
-        const int c0 = i * 8 + 2 * t;
-        const float s0 = c0 < rows ? __ldg(a.sa + static_cast<int64_t>(row0 + c0) * kb_n + kb) * sw : 0.f;
-        const float s1 = c0 + 1 < rows ? __ldg(a.sa + static_cast<int64_t>(row0 + c0 + 1) * kb_n + kb) * sw : 0.f;
-        acc[i][0] = fmaf(part[0], s0, acc[i][0]);
-        acc[i][1] = fmaf(part[1], s1, acc[i][1]);
-        acc[i][2] = fmaf(part[2], s0, acc[i][2]);
-        acc[i][3] = fmaf(part[3], s1, acc[i][3]);
+        sw[b] = kb < kb_n ? __ldg(sb + kb) : 0.f;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int kb = kb0 + b * kSmallWarps;
+        if (kb >= kb_n) break;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          if (i * 8 >= rows) break;
+          const int tok = i * 8 + g;
+          const uint8_t *x = static_cast<const uint8_t *>(a.a) + static_cast<int64_t>(row0 + tok) * a.K + 16 * t;
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = kb * kFp8Block + 64 * h;
+            uint4 xv = make_uint4(0u, 0u, 0u, 0u);
+            if (tok < rows && k + 16 * t < a.K) xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
+            mma_e4m3(part, wa[b][h].x, wb[b][h].x, wa[b][h].y, wb[b][h].y, xv.x, xv.y);
+            mma_e4m3(part, wa[b][h].z, wb[b][h].z, wa[b][h].w, wb[b][h].w, xv.z, xv.w);
+          }
+          const int c0 = i * 8 + 2 * t;
+          const float s0 = c0 < rows ? __ldg(a.sa + static_cast<int64_t>(row0 + c0) * kb_n + kb) * sw[b] : 0.f;
+          const float s1 = c0 + 1 < rows ? __ldg(a.sa + static_cast<int64_t>(row0 + c0 + 1) * kb_n + kb) * sw[b] : 0.f;
+          acc[i][0] = fmaf(part[0], s0, acc[i][0]);
+          acc[i][1] = fmaf(part[1], s1, acc[i][1]);
+          acc[i][2] = fmaf(part[2], s0, acc[i][2]);
+          acc[i][3] = fmaf(part[3], s1, acc[i][3]);
+        }
       }
     }
     // sums of the warps: value v of a token tile is weight row v / 8, token v % 8
@@ -704,9 +720,9 @@ uint32_t *ops_error_address(int device) {
   return addr[device];
 }
 
-template <bool PAIR, bool BF16> cudaError_t launch_tc(GemmParams &p, cudaStream_t s) {
-  using G = Geo<PAIR>;
-  auto *fn = &k_fp8_gemm<PAIR, BF16>;
+template <int BN, bool PAIR, bool BF16> cudaError_t launch_tc(GemmParams &p, cudaStream_t s) {
+  using G = Geo<BN, PAIR>;
+  auto *fn = &k_fp8_gemm<BN, PAIR, BF16>;
   static std::mutex mu;
   static int resident[64] = {};  // CTAs that a device holds at once
   int dev = 0, most = 0;
@@ -739,7 +755,7 @@ template <bool PAIR, bool BF16> cudaError_t launch_tc(GemmParams &p, cudaStream_
     most = resident[dev & 63];
   }
   if (most < (PAIR ? 2 : 1)) return cudaErrorNotSupported;
-  p.nt_n = (p.g.N + kBn - 1) / kBn;
+  p.nt_n = (p.g.N + BN - 1) / BN;
   // row tiles: at most one partial tile a group beyond the full ones
   const int64_t mt = p.g.offsets ? p.g.m / G::bm + p.g.n_groups : (p.g.m + G::bm - 1) / G::bm;
   const int64_t ctas = mt * p.nt_n * (PAIR ? 2 : 1);
@@ -766,7 +782,9 @@ uint32_t *ops_error_word() {
 
 cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   const int kb_n = (a.K + kBk - 1) / kBk, nb_n = (a.N + kFp8Block - 1) / kFp8Block;
-  if (a.m <= kSmallTokens) {
+  // Few rows: the weights' bytes and latency bound the time. Rows of one expert cost mma.sync products (4096 x 4096:
+  // 6.2 us at 8 rows, 8.1 at 16, 14 at 32, where the tiles below take 13), rows of several experts hardly.
+  if (a.m <= (a.offsets ? kSmallTokens : 16)) {
     if (a.m <= 8) return launch_small<1>(a, kb_n, nb_n, s);
     if (a.m <= 16) return launch_small<2>(a, kb_n, nb_n, s);
     if (a.m <= 32) return launch_small<4>(a, kb_n, nb_n, s);
@@ -782,20 +800,40 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   p.timeout_ns = 2000000000ll;
   if (p.err == nullptr || !tma_encode_init()) return cudaErrorInitializationError;
   const int64_t E = a.offsets ? a.n_groups : 1;
-  // Two CTAs a tile where the groups have rows for it: they read 2/3 of the bytes from L2 that single ones do,
-  // which bounds many rows; groups of fewer rows would leave the second CTA's half of the tile empty.
-  const bool pairs = a.m >= 256 * E;
-  const uint32_t b_rows = pairs ? Geo<true>::b_rows : Geo<false>::b_rows;
+  // The tile: the one whose rounds of tiles take the least time, by the clocks that a K block of each took. Pairs
+  // need groups that fill 256 rows.
+  const int sms = num_sms();
+  const int64_t mt = a.m / kBm + (a.offsets ? (E < a.m ? E : a.m) : (a.m % kBm != 0));
+  auto cost = [&](int64_t tiles, int64_t at_once, int64_t clocks) { return (tiles + at_once - 1) / at_once * clocks; };
+  int bn = 256;
+  int64_t best = cost(mt * ((a.N + 255) / 256), sms, 1000);
+  const int64_t narrow[3][2] = {{128, 720}, {64, 650}, {32, 640}};
+  for (const auto &c : narrow) {
+    const int64_t t = cost(mt * ((a.N + c[0] - 1) / c[0]), sms, c[1]);
+    if (t < best) {
+      best = t;
+      bn = static_cast<int>(c[0]);
+    }
+  }
+  bool pairs = false;
+  if (a.m >= 256 * E) {
+    const int64_t tiles = (a.m / 256 + (a.offsets ? E : a.m % 256 != 0)) * ((a.N + 255) / 256);
+    pairs = cost(tiles, sms / 2, 800) <= best;
+  }
+  const uint32_t b_rows = pairs ? Geo<256, true>::b_rows : bn;
   bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, b_rows);
-  if (ok && !pairs && a.offsets)
+  if (ok && !pairs && (a.offsets || a.m % kBm != 0))
     ok = encode_kmajor_8bit(&p.a[0], a.a, a.K, a.m, 32) && encode_kmajor_8bit(&p.a[1], a.a, a.K, a.m, 64);
-  if (ok && pairs && a.out_bf16 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.m == 1 || a.out_stride % 8 == 0)) {
+  if (ok && pairs && a.out_bf16 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % 8 == 0) {
     ok = encode_rows_bf16(&p.out, a.out, a.N, a.m, a.out_stride);
     p.g.bulk_out = 1;
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (pairs) return a.out_bf16 ? launch_tc<true, true>(p, s) : launch_tc<true, false>(p, s);
-  return a.out_bf16 ? launch_tc<false, true>(p, s) : launch_tc<false, false>(p, s);
+  if (pairs) return a.out_bf16 ? launch_tc<256, true, true>(p, s) : launch_tc<256, true, false>(p, s);
+  if (bn == 256) return a.out_bf16 ? launch_tc<256, false, true>(p, s) : launch_tc<256, false, false>(p, s);
+  if (bn == 128) return a.out_bf16 ? launch_tc<128, false, true>(p, s) : launch_tc<128, false, false>(p, s);
+  if (bn == 64) return a.out_bf16 ? launch_tc<64, false, true>(p, s) : launch_tc<64, false, false>(p, s);
+  return a.out_bf16 ? launch_tc<32, false, true>(p, s) : launch_tc<32, false, false>(p, s);
 }
 
 }  // namespace epoch
