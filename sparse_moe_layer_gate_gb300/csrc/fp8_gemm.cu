@@ -89,8 +89,11 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   }
   return true;
 }
+// The whole warp waits; a phase that is complete already (the usual case, and then
+// the loop's overhead is what counts) costs one attempt and a vote.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
                                           int64_t timeout_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_for(bar, parity, abort, err, timeout_ns));
 }
 
@@ -396,10 +399,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       for (int t = cta; ok && t < walk.total; t += ctas) {
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
           const uint32_t buf = it % G::bufs;
-          ok = wait_for(full + 8 * st, phase, abort, p.err, p.timeout_ns) &&
-               wait_for(tempty + 8 * buf, ((it / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          const uint32_t free = ((it / G::bufs) & 1u) ^ 1u;
+          const bool loaded = mbar_try_wait(full + 8 * st, phase), read = mbar_try_wait(tempty + 8 * buf, free);
+          if (!__all_sync(0xffffffffu, loaded && read)) {
+            ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns) &&
+                 warp_wait(tempty + 8 * buf, free, abort, p.err, p.timeout_ns);
+            if (!ok) break;
+          }
           tc_fence_after();
           const uint32_t src = ring + st * G::stage;
           const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kBk);
@@ -448,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       for (int c = 0; c < kCols / 2; ++c) acc[c] = 0ull;
       for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
         const uint32_t buf = it % G::bufs;
-        ok = warp_wait(tfull + 8 * buf, (it / G::bufs) & 1u, abort, p.err, p.timeout_ns);
+        if constexpr (PAIR) ok = warp_wait(tfull + 8 * buf, (it / G::bufs) & 1u, abort, p.err, p.timeout_ns);
+        else ok = __all_sync(0xffffffffu, wait_for(tfull + 8 * buf, (it / G::bufs) & 1u, abort, p.err, p.timeout_ns));
         if (!ok) break;
         if (any) {
           // The accumulator is free for the products after the next ones as soon as its last columns are on their
@@ -807,7 +814,7 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   auto cost = [&](int64_t tiles, int64_t at_once, int64_t clocks) { return (tiles + at_once - 1) / at_once * clocks; };
   int bn = 256;
   int64_t best = cost(mt * ((a.N + 255) / 256), sms, 1000);
-  const int64_t narrow[3][2] = {{128, 720}, {64, 650}, {32, 640}};
+  const int64_t narrow[3][2] = {{128, 720}, {64, 600}, {32, 560}};
   for (const auto &c : narrow) {
     const int64_t t = cost(mt * ((a.N + c[0] - 1) / c[0]), sms, c[1]);
     if (t < best) {
