@@ -329,7 +329,8 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
  * with the layer's router rule over every expert (no support, no row cache), as
  * epoch_moe_iter computes it when every position is fresh and every expert
  * eligible; expert outputs are kept in fp32 up to y. One launch that reads each
- * selected expert's weights once. A block's plan, cache, stamps and statistics
+ * selected expert's weights once, from the caller's own arrays (bf16 layers
+ * keep a packed copy for the iterations; both have to hold the same values). A block's plan, cache, stamps and statistics
  * are neither used nor changed, so it may run inside a block. y_dev may be x_dev,
  * but not otherwise overlap it. Like every call on a layer it uses the layer's workspace:
  * calls on one layer (graph replays among them) must not overlap on the GPU.

@@ -8,7 +8,9 @@
 //
 // Every value is held in fp32 from its load to its store: one rounding per
 // output. Rows are independent and move through registers once (read r, b and a
-// per-element gate, write r' and h'), so the bytes of the rows bound the time.
+// per-element gate, write r' and h'), so the bytes of the rows bound the time: 16384 rows
+// of 4096 (fp32 r, r' and bf16 b, h') take 141 us at 5.7 TB/s; a few rows take the launch
+// and two dependent sums, 2.0 us for norm_before of one row of 2048.
 #include <cmath>
 
 #include "common.cuh"
@@ -122,7 +124,7 @@ __device__ __forceinline__ float row_sum(float v, int warps, int w, float *row_s
 
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
-// A row belongs to `tpr` consecutive threads; thread p of them holds columns
+// A row belongs to `tpr` consecutive threads (whole warps); thread p of them holds columns
 // E * (p + i * tpr) .. + E, i < VPT, in registers (VPT = 0: H is larger than
 // the registers hold, and every pass reads the row again -- from L2 or L1, and
 // only elements that the same thread writes at the end, so out may be r).
@@ -130,7 +132,7 @@ template <typename TA, typename TR, bool AFTER, int E, int VPT>
 __global__ void __launch_bounds__(512, E == 8 && VPT <= 2 ? 2 : 1) k_block_norm(const NormArgs a, int tpr) {
   __shared__ float sums[64];
   int turn = 0;
-  const int p = threadIdx.x & (tpr - 1);
+  const int p = threadIdx.x % tpr;
   const int warps = tpr >> 5, w = p >> 5;
   float *row_sums = sums + (threadIdx.x >> 5) - w;
   const int rpb = blockDim.x / tpr;
@@ -287,8 +289,8 @@ template <typename TA, typename TR, bool AFTER, bool FULL>
 __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormArgs a, int tpr) {
   __shared__ float sums[64];
   int turn = 0;
-  const int c = 8 * (threadIdx.x & (tpr - 1));
-  const int warps = tpr >> 5, w = (threadIdx.x & (tpr - 1)) >> 5;
+  const int p = threadIdx.x % tpr, c = 8 * p;
+  const int warps = tpr >> 5, w = p >> 5;
   float *row_sums = sums + (threadIdx.x >> 5) - w;
   const int rpb = blockDim.x / tpr;
   const float inv_h = 1.0f / static_cast<float>(a.hidden);
@@ -378,19 +380,18 @@ __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormA
 }
 
 template <typename TA, typename TR, bool AFTER> cudaError_t launch_stay(const NormArgs &a, int tpr, cudaStream_t s) {
-  const int rpb = kStayThreads / tpr;
+  const int rpb = kStayThreads / tpr, threads = tpr * rpb;
   const int64_t blocks = (a.n_rows + rpb - 1) / rpb;
   const int64_t most = static_cast<int64_t>(num_sms()) * 2;
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER><<<grid, kStayThreads, 0, s>>>(a, tpr);
-  else k_block_norm_stay<TA, TR, AFTER, false><<<grid, kStayThreads, 0, s>>>(a, tpr);
+  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER><<<grid, threads, 0, s>>>(a, tpr);
+  else k_block_norm_stay<TA, TR, AFTER, false><<<grid, threads, 0, s>>>(a, tpr);
   return cudaGetLastError();
 }
 
 template <typename TA, typename TR, bool AFTER, int E, int VPT>
 cudaError_t launch(const NormArgs &a, int tpr, cudaStream_t s) {
-  const int threads = tpr < 128 ? 128 : tpr;
-  const int rpb = threads / tpr;
+  const int rpb = tpr < 128 ? 128 / tpr : 1, threads = tpr * rpb;
   const int64_t blocks = (a.n_rows + rpb - 1) / rpb;
   const int64_t most = static_cast<int64_t>(num_sms()) * (2048 / threads) * 8;
   k_block_norm<TA, TR, AFTER, E, VPT><<<static_cast<unsigned>(blocks < most ? blocks : most), threads, 0, s>>>(a, tpr);
@@ -400,16 +401,21 @@ cudaError_t launch(const NormArgs &a, int tpr, cudaStream_t s) {
 template <typename TA, typename TR, bool AFTER, int E>
 cudaError_t choose(const NormArgs &a, cudaStream_t s) {
   if constexpr (E == 8) {
-    // The staying CTAs pay for their parameters once: from four rows a thread on.
-    int wide = 32;
-    while (wide < kStayThreads && wide * 8 < a.hidden) wide *= 2;
-    if (a.hidden <= wide * 8 && a.n_rows >= 4ll * 2 * num_sms() * (kStayThreads / wide))
-      return launch_stay<TA, TR, AFTER>(a, wide, s);
+    // The staying CTAs pay for their parameters once, and eight columns a thread are the
+    // shorter way through a row. Between one and three rows for each row's place on the
+    // device their last turn is half empty. norm_after of bf16 z, fp32 r, a gate and h', us
+    // by short CTAs / staying ones (n, the rows for a place):
+    //   H = 2048   304, 1/2: 4.45 / 3.89    608, 1: 5.22 / 5.16   1216, 2: 7.57 / 7.83
+    //             1824, 3: 12.96 / 10.60   2432, 4: 15.39 / 13.16   9728, 16: 47.3 / 42.0
+    //   H = 4096   152, 1/2: 4.53 / 3.90    608, 2: 7.76 / 8.22    912, 3: 13.41 / 11.24
+    const int wide = (a.hidden / 8 + 31) / 32 * 32;
+    if (wide <= kStayThreads) {
+      const int64_t places = 2ll * num_sms() * (kStayThreads / wide);
+      if (a.n_rows <= places || a.n_rows >= 3 * places) return launch_stay<TA, TR, AFTER>(a, wide, s);
+    }
   }
-  // threads of a row: enough for 16 values each; 32 values each from 16 warps on
-  const int64_t per = 16;
-  int tpr = 32;
-  while (tpr < 512 && tpr * per < a.hidden) tpr *= 2;
+  // threads of a row: whole warps, enough for 16 values each; more values from 16 warps on
+  const int want = (a.hidden + 511) / 512 * 32, tpr = want < 512 ? want : 512;
   const int64_t vpt = (a.hidden + static_cast<int64_t>(tpr) * E - 1) / (static_cast<int64_t>(tpr) * E);
   if (vpt * E <= 8) return launch<TA, TR, AFTER, E, 8 / E>(a, tpr, s);
   if (vpt * E <= 16) return launch<TA, TR, AFTER, E, 16 / E>(a, tpr, s);

@@ -304,9 +304,9 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
   return true;
 }
 
-// Warps of a group in phases 1 and 2, for rows of `chunks` chunks: at most four,
-// and no more than leave each of them the two chunks it keeps in flight.
-__device__ __forceinline__ int split_of(int chunks) { return chunks >= 8 ? 4 : chunks >= 4 ? 2 : 1; }
+// Warps of a group in phases 1 and 2, for rows of `bytes` bytes: at most four, and
+// no more than leave each of them 512 bytes of a row (two chunks of bf16, four of fp32).
+__device__ __forceinline__ int split_of(int bytes) { return bytes >= 2048 ? 4 : bytes >= 1024 ? 2 : 1; }
 
 struct FewParams {
   Dims d;
@@ -655,7 +655,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
 
   // phase 1: routed activations, 8 columns of a job's expert a unit
   const int i8 = (I + 7) / 8;
-  int warps = split_of(H / chunk), grp = warp / warps, w = warp % warps;
+  int warps = split_of(H * static_cast<int>(sizeof(T))), grp = warp / warps, w = warp % warps;
   int gthread = threadIdx.x - grp * warps * 32;
   run_units<T, false>(
       grp * gridDim.x + blockIdx.x, gridDim.x * (kWarps / warps), r.n_jobs * i8, w, warps, grp,
@@ -684,7 +684,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   // of a shared expert each) a unit; rows of the fp32 sums: edge e at row e,
   // shared expert s and token t at n_tok * k + s * n_tok + t
   const int h16 = (H + 15) / 16;
-  warps = split_of(I / chunk);
+  warps = split_of(I * static_cast<int>(sizeof(T)));
   grp = warp / warps;
   w = warp % warps;
   gthread = threadIdx.x - grp * warps * 32;
