@@ -279,23 +279,69 @@ __global__ void __launch_bounds__(512, E == 8 && VPT <= 2 ? 2 : 1) k_block_norm(
   }
 }
 
-// Many rows of at most 4096 columns: a CTA stays, every thread keeps its eight
-// columns' parameters in registers (they cost more loads than the rows
-// themselves: up to four fp32 values a column), and the next row is on its way
-// while this one is summed up.
+// Rows of at most 4096 columns: a CTA stays, every thread keeps its eight columns'
+// parameters in registers (they cost more loads than the rows themselves: up to four
+// fp32 values a column), and the next row is on its way while this one is summed up.
+// VEC: the eight columns are neighbours and come in 16-byte loads. Else (rows of an odd
+// length start anywhere) they lie tpr apart, so a warp's scalar loads are neighbours.
 // FULL: the gate has a value for each row and column, and is read with the row.
 constexpr int kStayThreads = 512;
-template <typename TA, typename TR, bool AFTER, bool FULL>
-__global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormArgs a, int tpr) {
+
+template <bool VEC, typename T> struct Row8;
+template <typename T> struct Row8<true, T> {
+  Vec8<T> v;
+  __device__ __forceinline__ void load(const T *row, int c, int, int) { v = load_vec(row + c); }
+  __device__ __forceinline__ void get(int, int, int, float (&o)[8]) const { unpack_vec(v, o); }
+};
+template <typename T> struct Row8<false, T> {
+  T v[8];
+  __device__ __forceinline__ void load(const T *row, int c, int tpr, int hidden) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j * tpr < hidden) v[j] = row[c + j * tpr];
+  }
+  __device__ __forceinline__ void get(int c, int tpr, int hidden, float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = c + j * tpr < hidden ? to_f32(v[j]) : 0.f;
+  }
+};
+
+template <typename TA, typename TR, bool AFTER, bool FULL, bool VEC>
+__global__ void __launch_bounds__(kStayThreads, VEC ? 2 : 1) k_block_norm_stay(const NormArgs a, int tpr) {
   __shared__ float sums[64];
   int turn = 0;
-  const int p = threadIdx.x % tpr, c = 8 * p;
+  const int p = threadIdx.x % tpr, c = VEC ? 8 * p : p;
   const int warps = tpr >> 5, w = p >> 5;
   float *row_sums = sums + (threadIdx.x >> 5) - w;
   const int rpb = blockDim.x / tpr;
   const float inv_h = 1.0f / static_cast<float>(a.hidden);
   const bool in = c < a.hidden;
   float wt[8], sc[8], nw[8], gt[8];
+  auto params = [&](const void *from, float (&o)[8]) {
+    if constexpr (VEC) {
+      load_par<8>(from, a.par_bf16, c, o);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float one[1];
+        if (c + j * tpr < a.hidden) {
+          load_par<1>(from, a.par_bf16, c + j * tpr, one);
+          o[j] = one[0];
+        }
+      }
+    }
+  };
+  auto put = [&](auto *row, const float (&o)[8]) {
+    if constexpr (VEC) {
+      store_row<8>(row + c, o);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float one[1] = {o[j]};
+        if (c + j * tpr < a.hidden) store_row<1>(row + c + j * tpr, one);
+      }
+    }
+  };
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     wt[j] = gt[j] = 1.f;
@@ -303,26 +349,26 @@ __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormA
     nw[j] = 0.f;
   }
   if (in) {
-    if (a.weight) load_par<8>(a.weight, a.par_bf16, c, wt);
+    if (a.weight) params(a.weight, wt);
     if constexpr (AFTER) {
       if (!FULL && a.gate_kind == 1) {
-        load_par<8>(a.gate, a.par_bf16, c, gt);
+        params(a.gate, gt);
         if (a.gate_sigmoid) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) gt[j] = sigmoid(gt[j]);
         }
       }
-      if (a.scale) load_par<8>(a.scale, a.par_bf16, c, sc);
-      if (a.next_weight) load_par<8>(a.next_weight, a.par_bf16, c, nw);
+      if (a.scale) params(a.scale, sc);
+      if (a.next_weight) params(a.next_weight, nw);
     }
   }
-  Vec8<TR> r_next;
-  Vec8<TA> b_next, g_next;
+  Row8<VEC, TR> r_next;
+  Row8<VEC, TA> b_next, g_next;
   auto fetch = [&](int64_t row) {
     if (!in || row >= a.n_rows) return;
-    r_next = load_vec(static_cast<const TR *>(a.residual) + row * a.residual_stride + c);
-    if constexpr (AFTER) b_next = load_vec(static_cast<const TA *>(a.block) + row * a.block_stride + c);
-    if constexpr (FULL) g_next = load_vec(static_cast<const TA *>(a.gate) + row * a.gate_stride + c);
+    r_next.load(static_cast<const TR *>(a.residual) + row * a.residual_stride, c, tpr, a.hidden);
+    if constexpr (AFTER) b_next.load(static_cast<const TA *>(a.block) + row * a.block_stride, c, tpr, a.hidden);
+    if constexpr (FULL) g_next.load(static_cast<const TA *>(a.gate) + row * a.gate_stride, c, tpr, a.hidden);
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
   const int64_t mine = threadIdx.x / tpr;
@@ -334,8 +380,8 @@ __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormA
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[j] = b[j] = 0.f;
     if (on) {
-      unpack_vec(r_next, r);
-      if constexpr (AFTER) unpack_vec(b_next, b);
+      r_next.get(c, tpr, a.hidden, r);
+      if constexpr (AFTER) b_next.get(c, tpr, a.hidden, b);
     }
     float sq = 0.f, k = 1.f;
 #pragma unroll
@@ -344,7 +390,7 @@ __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormA
       if constexpr (FULL) {
         float g[8];
         if (on) {
-          unpack_vec(g_next, g);
+          g_next.get(c, tpr, a.hidden, g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b[j] *= a.gate_sigmoid ? sigmoid(g[j]) : g[j];
         }
@@ -360,7 +406,7 @@ __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormA
     if constexpr (!AFTER) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[j] *= k * wt[j];
-      if (on) store_row<8>(static_cast<TA *>(a.out) + row * a.out_stride + c, r);
+      if (on) put(static_cast<TA *>(a.out) + row * a.out_stride, r);
     } else {
       sq = 0.f;
 #pragma unroll
@@ -368,24 +414,25 @@ __global__ void __launch_bounds__(kStayThreads, 2) k_block_norm_stay(const NormA
         r[j] = fmaf(b[j], k, r[j]);
         sq += r[j] * r[j];
       }
-      if (on) store_row<8>(static_cast<TR *>(a.out) + row * a.out_stride + c, r);
+      if (on) put(static_cast<TR *>(a.out) + row * a.out_stride, r);
       if (a.next_weight) {
         k = rsqrtf(row_sum(on ? sq : 0.f, warps, w, row_sums, turn) * inv_h + a.eps);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] *= k * nw[j];
-        if (on) store_row<8>(static_cast<TA *>(a.next_out) + row * a.next_stride + c, r);
+        if (on) put(static_cast<TA *>(a.next_out) + row * a.next_stride, r);
       }
     }
   }
 }
 
-template <typename TA, typename TR, bool AFTER> cudaError_t launch_stay(const NormArgs &a, int tpr, cudaStream_t s) {
+template <typename TA, typename TR, bool AFTER, bool VEC>
+cudaError_t launch_stay(const NormArgs &a, int tpr, cudaStream_t s) {
   const int rpb = kStayThreads / tpr, threads = tpr * rpb;
   const int64_t blocks = (a.n_rows + rpb - 1) / rpb;
-  const int64_t most = static_cast<int64_t>(num_sms()) * 2;
+  const int64_t most = static_cast<int64_t>(num_sms()) * (VEC ? 2 : 1);
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER><<<grid, threads, 0, s>>>(a, tpr);
-  else k_block_norm_stay<TA, TR, AFTER, false><<<grid, threads, 0, s>>>(a, tpr);
+  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER, VEC><<<grid, threads, 0, s>>>(a, tpr);
+  else k_block_norm_stay<TA, TR, AFTER, false, VEC><<<grid, threads, 0, s>>>(a, tpr);
   return cudaGetLastError();
 }
 
@@ -400,7 +447,7 @@ cudaError_t launch(const NormArgs &a, int tpr, cudaStream_t s) {
 
 template <typename TA, typename TR, bool AFTER, int E>
 cudaError_t choose(const NormArgs &a, cudaStream_t s) {
-  if constexpr (E == 8) {
+  {
     // The staying CTAs pay for their parameters once, and eight columns a thread are the
     // shorter way through a row. Between one and three rows for each row's place on the
     // device their last turn is half empty. norm_after of bf16 z, fp32 r, a gate and h', us
@@ -408,16 +455,19 @@ cudaError_t choose(const NormArgs &a, cudaStream_t s) {
     //   H = 2048   304, 1/2: 4.45 / 3.89    608, 1: 5.22 / 5.16   1216, 2: 7.57 / 7.83
     //             1824, 3: 12.96 / 10.60   2432, 4: 15.39 / 13.16   9728, 16: 47.3 / 42.0
     //   H = 4096   152, 1/2: 4.53 / 3.90    608, 2: 7.76 / 8.22    912, 3: 13.41 / 11.24
-    const int wide = (a.hidden / 8 + 31) / 32 * 32;
+    // Scalar rows stay always: 20000 of 1001 take 175 / 69, 1216 of 2047 27 / 10.
+    const int wide = (a.hidden + 255) / 256 * 32;
     if (wide <= kStayThreads) {
       const int64_t places = 2ll * num_sms() * (kStayThreads / wide);
-      if (a.n_rows <= places || a.n_rows >= 3 * places) return launch_stay<TA, TR, AFTER>(a, wide, s);
+      if (E == 1 || a.n_rows <= places || a.n_rows >= 3 * places)
+        return launch_stay<TA, TR, AFTER, E == 8>(a, wide, s);
     }
   }
   // threads of a row: whole warps, enough for 16 values each; more values from 16 warps on
   const int want = (a.hidden + 511) / 512 * 32, tpr = want < 512 ? want : 512;
   const int64_t vpt = (a.hidden + static_cast<int64_t>(tpr) * E - 1) / (static_cast<int64_t>(tpr) * E);
-  if (vpt * E <= 8) return launch<TA, TR, AFTER, E, 8 / E>(a, tpr, s);
+  if constexpr (E == 8)
+    if (vpt == 1) return launch<TA, TR, AFTER, E, 1>(a, tpr, s);
   if (vpt * E <= 16) return launch<TA, TR, AFTER, E, 16 / E>(a, tpr, s);
   if (vpt * E <= 32) return launch<TA, TR, AFTER, E, 32 / E>(a, tpr, s);
   return launch<TA, TR, AFTER, E, 0>(a, 512, s);
