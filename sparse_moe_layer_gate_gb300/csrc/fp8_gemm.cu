@@ -40,7 +40,7 @@ constexpr int kMaxGroups = 1024;
 struct GemmParams {
   CUtensorMap a[3];  // boxes of 32, 64, 128 rows
   CUtensorMap b;     // boxes of the rows that a CTA loads
-  CUtensorMap out;   // boxes of 64 columns x 32 rows of a bf16 output (pairs)
+  CUtensorMap out;   // boxes of 128 bytes x 32 rows of the output (pairs)
   GemmArgs g;
   int kb_n, nb_n, nt_n;  // K blocks, N scale blocks, N tiles
   uint32_t *err;
@@ -253,7 +253,7 @@ template <int BN, bool PAIR> struct Geo {
   static constexpr int stages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
   static constexpr int bufs = BN == 256 ? 2 : 4;                           // TMEM accumulators
   static constexpr int tmem = bufs * BN;                                   // their columns
-  static constexpr int out_bytes = PAIR ? kBm * BN * 2 : 0;                // a bf16 tile on its way out
+  static constexpr int out_bytes = PAIR ? kBm * BN * 2 : 0;                // 8 KB of the output a warp, on their way
   static constexpr int smem = 1024 + stages * stage + out_bytes;
 };
 
@@ -484,38 +484,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
           release(buf);
         }
       }
-      // A pair's warp whose 32 rows all exist leaves its part to two bulk stores, which run under the next tile's
-      // products (rows behind a group's last one belong to another tile: such a warp stores row by row).
+      // A pair's warp whose 32 rows all exist leaves its part to bulk stores, which run under the next tile's products
+      // (rows behind a group's last one belong to another tile: such a warp stores row by row). They take 128 bytes of
+      // each row at a time, from two places in shared memory in turn.
       bool stored = false;
-      if constexpr (PAIR && BF16) {
+      if constexpr (PAIR) {
         if (ok && p.g.bulk_out && rows >= quarter * 32 + 32 && n0 < p.g.N) {
           stored = true;
-          uint8_t *mine = smem_raw + (ring - smem_u32(smem_raw)) + G::stages * G::stage + warp * 8192;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before has left
-          __syncwarp();
+          // columns of a part, and parts of one commit: a bf16 warp's two fit the two places, four of fp32 take turns
+          constexpr int kPart = BF16 ? 64 : 32, kTogether = BF16 ? 2 : 1;
+          uint8_t *places = smem_raw + (ring - smem_u32(smem_raw)) + G::stages * G::stage + warp * 8192;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {  // 16 bytes at a time, in the 128-byte swizzle
-            uint32_t w[4];
+          for (int h0 = 0; h0 < kCols / kPart; h0 += kTogether) {
+            if (n0 + kPart * h0 >= p.g.N) break;
+            // what was here has left
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(2 / kTogether - 1) : "memory");
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = unpair(acc[4 * c + j]);
-              const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-              w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            for (int h = h0; h < h0 + kTogether; ++h) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {  // 16 bytes at a time, in the 128-byte swizzle
+                uint32_t w[4];
+                if constexpr (BF16) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpair(acc[32 * h + 4 * c + j]);
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&v);
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    const float2 f = unpair(acc[16 * h + 2 * c + j]);
+                    w[2 * j] = __float_as_uint(f.x);
+                    w[2 * j + 1] = __float_as_uint(f.y);
+                  }
+                }
+                *reinterpret_cast<uint4 *>(places + (h & 1) * 4096 + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
-            *reinterpret_cast<uint4 *>(mine + (c >> 3) * 4096 + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (n0 + 64 * h < p.g.N)
-                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                                 reinterpret_cast<uint64_t>(&p.out)),
-                             "r"(n0 + 64 * h), "r"(row0 + quarter * 32), "r"(smem_u32(mine) + 4096 * h)
-                             : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              for (int h = h0; h < h0 + kTogether; ++h)
+                if (n0 + kPart * h < p.g.N)
+                  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                   reinterpret_cast<uint64_t>(&p.out)),
+                               "r"(n0 + kPart * h), "r"(row0 + quarter * 32), "r"(smem_u32(places) + 4096 * (h & 1))
+                               : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
           }
         }
       }
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       }
     }
   }
-  if constexpr (PAIR && BF16) {  // no exit with stores still reading shared memory
+  if constexpr (PAIR) {  // no exit with stores still reading shared memory
     if (warp < kEpiWarps && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
   }
@@ -831,8 +851,8 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, b_rows);
   if (ok && !pairs && (a.offsets || a.m % kBm != 0))
     ok = encode_kmajor_8bit(&p.a[0], a.a, a.K, a.m, 32) && encode_kmajor_8bit(&p.a[1], a.a, a.K, a.m, 64);
-  if (ok && pairs && a.out_bf16 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % 8 == 0) {
-    ok = encode_rows_bf16(&p.out, a.out, a.N, a.m, a.out_stride);
+  if (ok && pairs && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % (a.out_bf16 ? 8 : 4) == 0) {
+    ok = encode_rows(&p.out, a.out, a.out_bf16, a.N, a.m, a.out_stride);
     p.g.bulk_out = 1;
   }
   if (!ok) return cudaErrorInvalidValue;

@@ -1081,14 +1081,14 @@ bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, ui
   return r == CUDA_SUCCESS;
 }
 
-bool encode_rows_bf16(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, uint64_t stride) {
+bool encode_rows(CUtensorMap *map, void *base, bool bf16, uint64_t cols, uint64_t rows, uint64_t stride) {
   if (!g_encode || base == nullptr || rows == 0) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {stride * 2};
-  cuuint32_t box[2] = {64, 32};
+  cuuint64_t strides[1] = {stride * (bf16 ? 2 : 4)};
+  cuuint32_t box[2] = {bf16 ? 64u : 32u, 32};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base,
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

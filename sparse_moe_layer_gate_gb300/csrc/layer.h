@@ -261,8 +261,9 @@ bool gate_builds_worklist(const Dims &d);
 
 // Row-major [rows][k_elems] 8-bit matrix, boxes of 128 (K) x box_rows, 128-byte swizzle.
 bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, uint64_t rows, uint32_t box_rows);
-// bf16 output of `rows` rows of `cols` columns, `stride` elements apart: boxes of 64 columns x 32 rows, 128-byte swizzle.
-bool encode_rows_bf16(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, uint64_t stride);
+// bf16 or fp32 output of `rows` rows of `cols` columns, `stride` elements apart: boxes of 128 bytes x 32 rows, 128-byte
+// swizzle.
+bool encode_rows(CUtensorMap *map, void *base, bool bf16, uint64_t cols, uint64_t rows, uint64_t stride);
 
 int num_sms();
 
