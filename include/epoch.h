@@ -329,11 +329,12 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
  * with the layer's router rule over every expert (no support, no row cache), as
  * epoch_moe_iter computes it when every position is fresh and every expert
  * eligible; expert outputs are kept in fp32 up to y. One launch that reads each
- * selected expert's weights once, from the caller's own arrays (bf16 layers
- * keep a packed copy for the iterations; both have to hold the same values). A block's plan, cache, stamps and statistics
- * are neither used nor changed, so it may run inside a block. y_dev may be x_dev,
- * but not otherwise overlap it. Like every call on a layer it uses the layer's workspace:
- * calls on one layer (graph replays among them) must not overlap on the GPU.
+ * selected expert's weights once, from the caller's own arrays (bf16 layers keep
+ * a packed copy for the iterations; both have to hold the same values). A
+ * block's plan, cache, stamps and statistics are neither used nor changed, so it
+ * may run inside a block. y_dev may be x_dev, but not otherwise overlap it. Like
+ * every call on a layer it uses the layer's workspace: calls on one layer (graph
+ * replays among them) must not overlap on the GPU.
  * Its CTAs wait for one another (a cooperative launch; bounded waits, see
  * epoch_set_wait_timeout): EPOCH_ECUDA where the device cannot hold one CTA per
  * SM at once. Zero tokens enqueue nothing.
@@ -504,8 +505,8 @@ epoch_status epoch_fp8_quantize_weight(const void *w_dev, int32_t dtype, int32_t
  *  offsets[n_groups] on are not written. Offsets that descend or leave [0, m]
  *  are read as the nearest ascending values in range.
  * EPOCH_EINVAL: m < 0, n < 1, k not a positive multiple of 16, n_groups not in
- * [1, 1024], n_groups * n or n_groups * k beyond int32, unknown out_dtype, a_dev
- * or b_dev not 16-byte aligned, another pointer NULL or misaligned, y_stride < n.
+ * [1, 1024], m or n_groups * n above 2^31 - 257, unknown out_dtype, a_dev or b_dev
+ * not 16-byte aligned, another pointer NULL or misaligned, y_stride < n.
  * A bounded device wait that gives up sets the operators' error word. */
 epoch_status epoch_fp8_matmul(const void *a_dev, const float *a_scales_dev, const void *b_dev,
                               const float *b_scales_dev, const int32_t *offsets_dev, int32_t n_groups, int32_t m,

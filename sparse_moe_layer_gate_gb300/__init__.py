@@ -4,8 +4,9 @@ The compute path is the C-ABI library built from ``csrc/`` (see
 ``include/epoch.h``); this package holds its ctypes binding (``binding``), a
 torch-facing wrapper (``layer.EpochLayer``), the operators a model runs around
 the layer (``ops``: norms before and after a block, FP8 products) and the
-in-tree build (``builder.build``). Importing the package does not load the library; the first
-call into it does, and fails loudly if the library has not been built.
+in-tree build (``builder.build``). Importing the package does not load the
+library; the first call into it does, and fails loudly if the library has not
+been built.
 """
 __all__ = ["binding", "builder", "layer", "ops"]
 

@@ -139,9 +139,14 @@ class EpochLayer:
                     y = torch.empty_like(x)
         else:
             self._check_x(y)
-            if y.shape != x.shape:
-                raise ValueError("y must have the shape of x")
-        s = torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else stream.cuda_stream
+            if y.shape != x.shape or y.get_device() != x.get_device():
+                raise ValueError("y must have the shape and the device of x")
+            if 0 < abs(y.data_ptr() - x.data_ptr()) < x.numel() * x.element_size():
+                raise ValueError("y must be x or not overlap it")
+        dev = x.get_device()
+        if dev != self._ws.get_device() or dev != torch._C._cuda_getDevice():
+            raise ValueError(f"x is on cuda:{dev}, which is not the layer's or not the current device")
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
         B.check(B.lib().epoch_moe_few(self.handle, x.data_ptr(), x.shape[0], y.data_ptr(), s), "epoch_moe_few")
         return y
 

@@ -21,6 +21,7 @@ from . import binding as B
 _CODE = {torch.float32: B.EPOCH_F32, torch.bfloat16: B.EPOCH_BF16}
 BLOCK = 128  # columns (and, for weights, rows) that share a scale
 _E4M3 = torch.float8_e4m3fn
+_MOST = 2 ** 31 - 1  # rows and columns are 32-bit in the ABI
 
 
 def _stream(stream, dev: int) -> int:
@@ -56,6 +57,8 @@ def _rows(t: torch.Tensor, dev: int, shape, what: str) -> int:
     if t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{what} must be a {list(shape)} tensor on cuda:{dev}")
     n, h = shape
+    if n > _MOST or h > _MOST:
+        raise ValueError(f"{what} has more than 2^31 - 1 rows or columns")
     row, col = t.stride()
     if n <= 1:
         row = h
@@ -163,6 +166,8 @@ def norm_after(block: torch.Tensor, residual: torch.Tensor, weight: Optional[tor
 def _bytes(t: torch.Tensor, dev: int, shape, what: str) -> int:
     if t.dtype != _E4M3 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float8_e4m3fn tensor {list(shape)} on cuda:{dev}")
+    if shape[-1] > _MOST or shape[-2] > _MOST:
+        raise ValueError(f"{what} has more than 2^31 - 1 rows or columns")
     return t.data_ptr()
 
 
@@ -219,6 +224,8 @@ def fp8_quantize_weight(w: torch.Tensor, *, stream=None) -> Tuple[torch.Tensor, 
     if w.dim() not in (2, 3) or not w.is_contiguous():
         raise ValueError("w must be a contiguous [N, K] or [E, N, K] tensor")
     n, k = w.shape[-2:]
+    if max(w.shape) > _MOST:
+        raise ValueError("w has more than 2^31 - 1 matrices, rows or columns")
     mats = w.shape[0] if w.dim() == 3 else 1
     q = _empty(tuple(w.shape), _E4M3, w.device, stream)
     scales = _empty(tuple(w.shape[:-2]) + (-(-n // BLOCK), -(-k // BLOCK)), torch.float32, w.device, stream)

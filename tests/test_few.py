@@ -361,6 +361,8 @@ def test_refusals(Layer):
             lay.forward_few(bad)
     with pytest.raises(ValueError):
         lay.forward_few(x[:4], y=x[4:7])
+    with pytest.raises(ValueError):  # overlaps x without being x
+        lay.forward_few(x[:4], y=x[3:7])
     h, L = lay.handle, B.lib()
     p = x.data_ptr()
     assert L.epoch_moe_few(None, p, 4, p + 8192, None) == B.EPOCH_EINVAL

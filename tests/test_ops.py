@@ -619,3 +619,13 @@ def test_tensors_are_checked(ops):
                  lambda: ops.fp8_matmul(q, s, b, sb, out_dtype=torch.float16)):
         with pytest.raises((ValueError, RuntimeError)):
             call()
+
+
+@pytest.mark.gpu
+def test_more_rows_than_the_abi_counts_are_refused(ops):
+    n, c = 2 ** 31, dict(device="cuda")
+    one, far = torch.ones(1, **c), torch.empty(n, 1, dtype=BF16, **c)
+    for call in (lambda: ops.norm_before(far, one), lambda: ops.norm_after(far, far, one, out=far),
+                 lambda: ops.fp8_quantize(far.view(1, n)), lambda: ops.fp8_quantize_weight(far)):
+        with pytest.raises(ValueError):
+            call()
