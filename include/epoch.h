@@ -340,7 +340,8 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
  * SM at once. Zero tokens enqueue nothing.
  * EPOCH_EINVAL if n_tok is not in [0, min(EPOCH_FEW_MAX, max_positions)], x_dev or
  * y_dev is NULL/misaligned, or n_tok rows of x, or of the activations (top_k *
- * inter + n_shared * shared_inter columns each), exceed 2^31 elements. */
+ * inter + n_shared * shared_inter columns each, in bf16 layers twice as many),
+ * exceed 2^31 elements. */
 #define EPOCH_FEW_MAX 64
 epoch_status epoch_moe_few(epoch_layer *layer, const void *x_dev, int32_t n_tok, void *y_dev, epoch_stream stream);
 

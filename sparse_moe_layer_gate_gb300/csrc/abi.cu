@@ -152,7 +152,7 @@ size_t carve(const epoch_layer_config &c, char *base, Work *w) {
   t.err = static_cast<uint32_t *>(take(16));
   const size_t F = N < kFewTokens ? N : kFewTokens;
   t.few.logits = static_cast<float *>(take(F * E * 4));
-  t.few.act = take(F * (k * few_row(I) + nsh * few_row(Is)) * act);
+  t.few.act = take(F * (k * few_row(I) + nsh * few_row(Is)) * 4);
   t.few.out = static_cast<float *>(take(F * (k + nsh) * few_row(H) * 4));
   t.few.sel = static_cast<int16_t *>(take(F * k * 2));
   t.few.wgt = static_cast<float *>(take(F * k * 4));
@@ -439,7 +439,7 @@ epoch_status epoch_moe_few(epoch_layer *L, const void *x, int32_t n_tok, void *y
   if (!aligned16(x) || !aligned16(y)) return EPOCH_EINVAL;
   // rows are addressed by 32-bit element offsets
   const int64_t acts = static_cast<int64_t>(L->dims.k) * few_row(L->dims.I) + static_cast<int64_t>(L->dims.n_sh) * few_row(L->dims.I_s);
-  if (n_tok * acts > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;
+  if (n_tok * acts * (L->bf16 ? 2 : 1) > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;
   cudaStream_t s = S(stream);
   return run(L, K_FEW, s,
              [&] { return launch_moe_few(L->dims, L->w, L->ws.few, x, y, n_tok, L->bf16, L->ws.err, s); });

@@ -30,8 +30,8 @@
 // Sums are split into a fixed number of parts that meet in a fixed order, and a
 // token is a column of its own in every product, so a token's result is the same
 // bits whatever its neighbours and however often it is computed. Rounding: the
-// activations of bf16 layers, which are an operand of the tensor core (as in the
-// iteration path), and y; everything else is fp32.
+// activations of bf16 layers, which are an operand of the tensor core, to two bf16
+// values each (16 bits), and y; everything else is fp32.
 //
 // fp32 layers run the same schedule with FFMA in place of the tensor core.
 //
@@ -41,6 +41,7 @@
 // at 6.3 TB/s. Reading a unit's rows only (no products, no barriers) reaches
 // 6.1 to 6.4 TB/s at 400 MB with these loads.
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cstring>
 
@@ -146,45 +147,59 @@ struct Share {
   int step, end, k;  // K steps, columns of a row
 };
 
-template <typename T> struct Chunk {
-  static constexpr int n = Elem<T>::steps;
-  uint4 a[n], b[n];                 // weight rows g and g + 8
-  uint4 v[sizeof(T) == 2 ? n : 1];  // token row g (bf16)
+// FRESH: the tokens' rows are activations, in bf16 layers of two parts each, whose
+// registers leave fewer for the weights on their way.
+template <typename T, bool FRESH> struct Chunk {
+  static constexpr int n = FRESH && sizeof(T) == 2 ? Elem<T>::steps / 2 : Elem<T>::steps;  // K steps
+  uint4 a[n], b[n];                                     // weight rows g and g + 8
+  uint4 v[sizeof(T) == 2 ? (FRESH ? 2 * n : n) : 1];  // token row g (bf16)
 };
 
 // Whether columns of a K step that a thread holds exist: rows of bf16 layers are
 // a whole number of chunks.
 template <typename T> __device__ __forceinline__ bool in_row(int c, int k) { return sizeof(T) == 2 || c < k; }
 
-template <typename T> __device__ __forceinline__ void load_rows(const Share &w, int step, Chunk<T> &c) {
+template <typename T, bool FRESH>
+__device__ __forceinline__ void load_rows(const Share &w, int step, Chunk<T, FRESH> &c) {
   const int c0 = step * Elem<T>::step, ct = c0 + (lane_id() & 3) * Elem<T>::per;
   const char *p0 = w.p0 + static_cast<int64_t>(c0) * sizeof(T), *p1 = w.p1 + static_cast<int64_t>(c0) * sizeof(T);
 #pragma unroll
-  for (int j = 0; j < Elem<T>::steps; ++j) {
+  for (int j = 0; j < c.n; ++j) {
     const bool in = in_row<T>(ct + j * Elem<T>::step, w.k);
     c.a[j] = load_weights(p0 + 64 * j, in);
     c.b[j] = load_weights(p1 + 64 * j, in);
   }
 }
 template <typename T, bool FRESH>
-__device__ __forceinline__ void load_token(const Share &w, int step, const T *x, Chunk<T> &c) {
-  if constexpr (sizeof(T) == 2) {
-    const T *row = x + w.row + step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
+__device__ __forceinline__ void load_token(const Share &w, int step, const T *x, Chunk<T, FRESH> &c) {
+  const int c0 = step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
+  if constexpr (sizeof(T) == 2 && FRESH) {
+    const T *row = x + w.row + 2 * c0;  // eight leading parts, then their eight rests
 #pragma unroll
-    for (int j = 0; j < Elem<T>::steps; ++j) c.v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
+    for (int j = 0; j < c.n; ++j)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(c.v[2 * j].x), "=r"(c.v[2 * j].y), "=r"(c.v[2 * j].z), "=r"(c.v[2 * j].w),
+                     "=r"(c.v[2 * j + 1].x), "=r"(c.v[2 * j + 1].y), "=r"(c.v[2 * j + 1].z), "=r"(c.v[2 * j + 1].w)
+                   : "l"(row + 2 * j * Elem<T>::step)
+                   : "memory");
+  } else if constexpr (sizeof(T) == 2) {
+    const T *row = x + w.row + c0;
+#pragma unroll
+    for (int j = 0; j < c.n; ++j) c.v[j] = load_tokens<FRESH>(row + j * Elem<T>::step);
   }
 }
 
 // Adds a chunk's products to the sums. The fp32 form reads the tokens' rows here,
 // four tokens' loads on their way together: a thread's sums are of every token.
 template <typename T, bool FRESH>
-__device__ __forceinline__ void add_chunk(const Share &w, int step, const Chunk<T> &c, const T *x,
+__device__ __forceinline__ void add_chunk(const Share &w, int step, const Chunk<T, FRESH> &c, const T *x,
                                           float (&acc)[Elem<T>::acc]) {
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int j = 0; j < Elem<T>::steps; ++j) {
-      mma_bf16(acc, c.a[j].x, c.b[j].x, c.a[j].y, c.b[j].y, c.v[j].x, c.v[j].y);
-      mma_bf16(acc, c.a[j].z, c.b[j].z, c.a[j].w, c.b[j].w, c.v[j].z, c.v[j].w);
+    for (int j = 0; j < c.n * (FRESH ? 2 : 1); ++j) {
+      const uint4 &a = c.a[FRESH ? j / 2 : j], &b = c.b[FRESH ? j / 2 : j];
+      mma_bf16(acc, a.x, b.x, a.y, b.y, c.v[j].x, c.v[j].y);
+      mma_bf16(acc, a.z, b.z, a.w, b.w, c.v[j].z, c.v[j].w);
     }
   } else {
     const int c0 = step * Elem<T>::step + (lane_id() & 3) * Elem<T>::per;
@@ -224,6 +239,19 @@ __device__ __forceinline__ void add_chunk(const Share &w, int step, const Chunk<
   }
 }
 
+// Part `part` of column col of an activation row. bf16 keeps eight columns' leading
+// parts and then what is left of each, together 16 bits of a value (activations rounded
+// to one bf16 raised y's error against 64 bits from 0.0017 to 0.0025 of its size);
+// infinities leave nothing. The sixteen parts are one sector.
+__device__ __forceinline__ void put_act(float *row, int col, int, float v) { row[col] = v; }
+__device__ __forceinline__ void put_act(__nv_bfloat16 *row, int col, int part, float v) {
+  if (part) {
+    const float lead = __bfloat162float(__float2bfloat16_rn(v));
+    v = fabsf(lead) <= FLT_MAX ? v - lead : 0.f;
+  }
+  row[(col >> 3) * 16 + part * 8 + (col & 7)] = __float2bfloat16_rn(v);
+}
+
 // A warp's sums to shared memory as [16 rows][8 tokens].
 template <typename T> __device__ __forceinline__ void put_tile(float *d, const float (&acc)[Elem<T>::acc]) {
   const int lane = lane_id(), g = lane >> 2, t = lane & 3;
@@ -255,18 +283,19 @@ template <typename T> __device__ __forceinline__ void put_tile(float *d, const f
 template <typename T, bool FRESH, typename Locate, typename Finish, typename Ready>
 __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, int warps, int gid, float *part,
                                           const T *x, Locate locate, Finish finish, Ready ready) {
-  Chunk<T> c0, c1;
+  Chunk<T, FRESH> c0, c1;
+  constexpr int kSteps = Chunk<T, FRESH>::n;
   Share cur;
   int u = first;
   if (u < n) {
     locate(u, w, warps, cur);
-    if (cur.step < cur.end) load_rows<T>(cur, cur.step, c0);
-    if (cur.step + Elem<T>::steps < cur.end) load_rows<T>(cur, cur.step + Elem<T>::steps, c1);
+    if (cur.step < cur.end) load_rows<T, FRESH>(cur, cur.step, c0);
+    if (cur.step + kSteps < cur.end) load_rows<T, FRESH>(cur, cur.step + kSteps, c1);
   }
   if (!ready()) return false;
   if (u < n) {
     if (cur.step < cur.end) load_token<T, FRESH>(cur, cur.step, x, c0);
-    if (cur.step + Elem<T>::steps < cur.end) load_token<T, FRESH>(cur, cur.step + Elem<T>::steps, x, c1);
+    if (cur.step + kSteps < cur.end) load_token<T, FRESH>(cur, cur.step + kSteps, x, c1);
   }
   int half = 0;
   while (u < n) {
@@ -276,7 +305,7 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
     const int un = u + stride;
     Share now = cur;
     do {
-      int ns = now.step + 2 * Elem<T>::steps;  // what the registers hold next
+      int ns = now.step + 2 * kSteps;  // what the registers hold next
       if (now.step < now.end) add_chunk<T, FRESH>(now, now.step, c0, x, acc);
       if (ns >= now.end) {
         cur.end = 0;  // nothing left to load
@@ -284,15 +313,15 @@ __device__ __forceinline__ bool run_units(int first, int stride, int n, int w, i
         ns = cur.step;
       }
       if (ns < cur.end) {
-        load_rows<T>(cur, ns, c0);
+        load_rows<T, FRESH>(cur, ns, c0);
         load_token<T, FRESH>(cur, ns, x, c0);
       }
-      if (now.step + Elem<T>::steps < now.end) add_chunk<T, FRESH>(now, now.step + Elem<T>::steps, c1, x, acc);
-      if (ns + Elem<T>::steps < cur.end) {
-        load_rows<T>(cur, ns + Elem<T>::steps, c1);
-        load_token<T, FRESH>(cur, ns + Elem<T>::steps, x, c1);
+      if (now.step + kSteps < now.end) add_chunk<T, FRESH>(now, now.step + kSteps, c1, x, acc);
+      if (ns + kSteps < cur.end) {
+        load_rows<T, FRESH>(cur, ns + kSteps, c1);
+        load_token<T, FRESH>(cur, ns + kSteps, x, c1);
       }
-      now.step += 2 * Elem<T>::steps;
+      now.step += 2 * kSteps;
     } while (now.step < now.end);
     float *mine = part + (half * warps) * 128;
     put_tile<T>(mine + w * 128, acc);
@@ -563,7 +592,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   const T *x = static_cast<const T *>(p.x);
   // Scratch rows are whole 32-byte sectors, so that no store touches part of one (which L2 would complete from
   // memory first: a barrier after such stores costs 3 to 5 us more).
-  const int Ia = few_row(I), Is = few_row(d.I_s), Ho = few_row(H);
+  constexpr int parts = sizeof(T) == 2 ? 2 : 1;  // of an activation
+  const int Ia = few_row(I) * parts, Is = few_row(d.I_s) * parts, Ho = few_row(H);
   T *act = static_cast<T *>(p.ws.act);     // row of edge e at e * Ia,
   const int act_sh = p.n_tok * k * Ia;     // of shared expert s and token t at act_sh + (s * n_tok + t) * Is
 
@@ -586,10 +616,6 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   // phase 0: router tiles of 16 experts, then shared tiles of 8 activation columns; eight tokens a unit
   const int n_router = (E + 15) / 16, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[3] = 0;  // no CTA reaches the last barrier before this one passes the first
-  // units store 8 activations of a token: half a sector in bf16, so the sectors have to be in L2
-  const int64_t act_bytes = (static_cast<int64_t>(act_sh) + static_cast<int64_t>(d.n_sh) * nt * Is) * sizeof(T);
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 128; i < act_bytes; i += static_cast<int64_t>(gridDim.x) * kThreads * 128)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(act) + i));
   if (threadIdx.x < 16 && blockIdx.x / nt8 * 16 + threadIdx.x < E)  // the bias of this CTA's experts, needed at the end of the tile
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.b_router + blockIdx.x / nt8 * 16 + threadIdx.x));
   run_units<T, false>(
@@ -616,10 +642,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
             p.ws.logits[static_cast<size_t>(tok0 + tok) * E + e] =
                 (d.router == 0 ? __ldg(p.w.b_router + e) : 0.f) + sum(mine, kWarps, tok, q & 15);
         } else {
-          const int s = (v - n_router) / sh8, tok = q >> 3, col = (v - n_router - s * sh8) * 8 + (q & 7);
-          if (tok < count && col < d.I_s)
-            act[act_sh + (s * nt + tok0 + tok) * Is + col] =
-                from_f32<T>(silu(sum(mine, kWarps, tok, q & 7)) * sum(mine, kWarps, tok, (q & 7) + 8));
+          const int s = (v - n_router) / sh8, tok = q / (8 * parts), col = (v - n_router - s * sh8) * 8 + (q & 7);
+          if (tok < count && col < Is / parts)
+            put_act(act + act_sh + (s * nt + tok0 + tok) * Is, col, q >> 3 & (parts - 1),
+                    silu(sum(mine, kWarps, tok, q & 7)) * sum(mine, kWarps, tok, (q & 7) + 8));
         }
       },
       [] { return true; });
@@ -670,11 +696,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
       },
       [&](int u, int count, const float *mine) {
         const int j = u / i8;
-        for (int v = gthread; v < count * 8; v += warps * 32) {
-          const int tok = v >> 3, c = v & 7, col = (u - j * i8) * 8 + c;
-          if (col < I)
-            act[r.list[r.job_first[j] + tok] * Ia + col] =
-                from_f32<T>(silu(sum(mine, warps, tok, c)) * sum(mine, warps, tok, c + 8));
+        for (int v = gthread; v < count * 8 * parts; v += warps * 32) {
+          const int tok = v / (8 * parts), c = v & 7, col = (u - j * i8) * 8 + c;
+          if (col < Ia / parts)  // the last sector whole: columns behind I hold copies that nobody reads
+            put_act(act + r.list[r.job_first[j] + tok] * Ia, col, v >> 3 & (parts - 1),
+                    silu(sum(mine, warps, tok, c)) * sum(mine, warps, tok, c + 8));
         }
       },
       [] { return true; });
@@ -713,7 +739,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
         for (int v = gthread; v < count * 16; v += warps * 32) {
           const int tok = v >> 4, c = v & 15, col = (u - j * h16) * 16 + c;
           const int at = sj < 0 ? r.list[r.job_first[j] + tok] : nt * k + sj / nt8 * nt + sj % nt8 * 8 + tok;
-          if (col < H) __stcg(p.ws.out + static_cast<size_t>(at) * Ho + col, sum(mine, warps, tok, c));
+          if (col < Ho) __stcg(p.ws.out + static_cast<size_t>(at) * Ho + col, sum(mine, warps, tok, c));
         }
       },
       [&] { return grid_wait(p.ws.ctr + 2, p.err, d.timeout_ns); });

@@ -7,15 +7,22 @@
 // one expert). Products of a K block are summed by the tensor cores; the
 // scaled sums of the blocks are kept in fp32 registers and rounded once.
 //
-// Many rows (k_fp8_gemm): tiles of 128 rows x BN columns. A producer warp
-// streams 128-byte-wide (one K block) operand tiles by TMA through a ring in
-// shared memory, an MMA warp issues tcgen05 products of one K block into one of
-// two TMEM accumulators, and eight epilogue warps read the other accumulator,
-// scale it and add it to their registers: the promotion of one block runs under
-// the products of the next.
+// Many rows (k_fp8_gemm): tiles of 128 rows x 256, 128, 64 or 32 columns, or of
+// 256 x 256 by two CTAs whose tensor cores read both halves of the weights. A
+// producer warp streams 128-byte-wide (one K block) operand tiles by TMA through
+// a ring in shared memory, an MMA warp issues the tcgen05 products of one K block
+// into one of two (narrow tiles: four) TMEM accumulators, and eight epilogue
+// warps read the other, scale it and add it to their registers: the promotion of
+// one block runs under the products of the next. What bounds it: TMEM serves one
+// side at a time, so the reading of an accumulator (256 clocks at 256 columns)
+// adds to its products (512) and a K block of a pair takes about 790 clocks;
+// narrow tiles are taken where a round of wide ones would leave SMs idle.
+// 8192 x 4096 x 4096 to bf16 95 us (2.9 PFLOP/s), to fp32 106 us; 256 experts of
+// 1024 x 2048 with 8192 rows 94 us, where the weights' bytes bound it (6.1 TB/s).
 //
 // Few rows (k_fp8_small): bound by the weights' bytes; sixteen weight rows per
-// CTA go from global memory straight into mma.sync fragments (see below).
+// CTA go from global memory straight into mma.sync fragments (see below). One row
+// by 4096 x 2048: 3.1 us.
 #include <cstring>
 #include <mutex>
 

@@ -32,8 +32,8 @@ constexpr int kFewTokens = 64;  // tokens of one call, at most
 __host__ __device__ inline int few_row(int n) { return (n + 15) / 16 * 16; }
 struct FewWork {
   float *logits;   // [kFewTokens][E]
-  void *act;       // activations, layer dtype: [n_tok*k][I] of the edges, then [n_sh][n_tok][I_s]
-                   // (rows few_row apart)
+  void *act;       // activations, fp32 or two bf16 parts each: [n_tok*k][I] of the edges, then
+                   // [n_sh][n_tok][I_s] (rows few_row apart)
   float *out;      // [kFewTokens*(k + n_sh)][H] expert outputs (rows few_row apart)
   int16_t *sel;    // [kFewTokens][k] selections and
   float *wgt;      // their weights, where the CTAs share the selection out

@@ -141,13 +141,13 @@ class EpochLayer:
             self._check_x(y)
             if y.shape != x.shape or y.get_device() != x.get_device():
                 raise ValueError("y must have the shape and the device of x")
-            if 0 < abs(y.data_ptr() - x.data_ptr()) < x.numel() * x.element_size():
-                raise ValueError("y must be x or not overlap it")
-        dev = x.get_device()
+        dev, px, py = x.get_device(), x.data_ptr(), y.data_ptr()
+        if px != py and abs(px - py) < x.nbytes:
+            raise ValueError("y must be x or not overlap it")
         if dev != self._ws.get_device() or dev != torch._C._cuda_getDevice():
             raise ValueError(f"x is on cuda:{dev}, which is not the layer's or not the current device")
         s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-        B.check(B.lib().epoch_moe_few(self.handle, x.data_ptr(), x.shape[0], y.data_ptr(), s), "epoch_moe_few")
+        B.check(B.lib().epoch_moe_few(self.handle, px, x.shape[0], py, s), "epoch_moe_few")
         return y
 
     def worklist(self):

@@ -88,9 +88,12 @@ def layer64(w, x, c, dtype):
         a, b = v @ g.T, v @ u.T
         da, db = (v.abs() @ g.abs().T) * chain, (v.abs() @ u.abs().T) * chain
         act = torch.nn.functional.silu(a) * b
-        # silu' <= 1.1; exp, sum, quotient, product: 8 roundings; one rounding to the layer's type
-        e_act = 1.1 * da * b.abs() + torch.nn.functional.silu(a).abs() * db + act.abs() * (8 * U + half)
-        inner = (d.shape[1] / 64 + 24) * 2.0 ** -23
+        # silu' <= 1.1; exp, sum, quotient, product: 8 roundings; bf16 layers keep a value in two bf16 parts, so what
+        # is lost is half a step of what the first part leaves, itself at most half a step
+        e_act = 1.1 * da * b.abs() + torch.nn.functional.silu(a).abs() * db + act.abs() * (8 * U + (U if half == U else half * half))
+        # bf16: a warp's part of I (all of it below 512 columns) in products of 16 columns, twice for the two parts
+        cols = d.shape[1]
+        inner = ((cols / 64 if half == U else max(min(cols, 512), cols / 4) / 8) + 24) * 2.0 ** -23
         return act @ d.T, e_act @ d.abs().T + (act.abs() @ d.abs().T) * inner
 
     y, err = torch.zeros_like(xd), torch.zeros_like(xd)

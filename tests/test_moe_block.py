@@ -91,8 +91,9 @@ def test_a_decoders_block(mod, dtype, n):
     y, size, gap = moe64(h.double(), w, k)
     keep = gap > 1e-4  # a selection that no rounding of a logit (2e-5 here) can change
     assert int(keep.sum()) >= 0.9 * n
-    # the activation's rounding on every term, sums of 512 (2^-23 a step of 16 columns, both products) and y's rounding
-    bound = size * (half + 300 * U) + y.abs() * half * (1 + 2 ** -7)
+    # the activation's rounding on every term (bf16: to two parts), sums of 512 (2^-23 a step of 16 columns, both
+    # products, the second of both parts) and y's rounding
+    bound = size * ((half * half if dtype == "bf16" else U) + 300 * U) + y.abs() * half * (1 + 2 ** -7)
     # gate and up sums of an activation: 64 roundings of terms whose sizes add up to at most 16 times the sum's scale
     bound = bound + size * 16 * 64 * U
     assert bool(((b.double() - y).abs() <= bound)[keep].all()), float(((b.double() - y).abs() / bound)[keep].max())
