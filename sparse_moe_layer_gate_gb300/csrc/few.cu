@@ -36,10 +36,15 @@
 // fp32 layers run the same schedule with FFMA in place of the tensor core.
 //
 // Measured (H 2048, 256 experts of 512 columns, 8 and 1 shared a token, bf16;
-// weights from memory): 1 token 20.8 us, of which 7.8 us are phases 1 and 2 and
-// 1.1 us each barrier; 32 tokens (47 experts) 64 us at 4.7 TB/s, phases 1 and 2
-// at 6.3 TB/s. Reading a unit's rows only (no products, no barriers) reaches
-// 6.1 to 6.4 TB/s at 400 MB with these loads.
+// weights from memory): 1 token 21.9 us, of which 8 us are phases 1 and 2 and
+// 1.1 us each barrier; 32 tokens (47 experts) 67 us at 4.5 TB/s, phase 1 at 7
+// and phase 2 at 5.2 TB/s (its activations are twice the bytes of phase 1's
+// tokens). Reading a unit's rows only (no products, no barriers) reaches 6.1 to 6.4
+// TB/s at 400 MB with these loads. Loads leave L1 in the order in which they came,
+// so a hit waits for the misses before it: activations' second parts that were
+// read where they are used cost 75 us in place of 67, and tokens' rows that were asked for one
+// chunk ahead, not two, 71; sharing a group's activations between two tiles of
+// weight rows 68.
 #include <atomic>
 #include <cfloat>
 #include <climits>
