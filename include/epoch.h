@@ -505,9 +505,10 @@ epoch_status epoch_fp8_quantize_weight(const void *w_dev, int32_t dtype, int32_t
  *  offsets[e + 1] - 1 are multiplied by matrix e; rows before offsets[0] or from
  *  offsets[n_groups] on are not written. Offsets that descend or leave [0, m]
  *  are read as the nearest ascending values in range.
- * EPOCH_EINVAL: m < 0, n < 1, k not a positive multiple of 16, n_groups not in
- * [1, 1024], m or n_groups * n above 2^31 - 257, unknown out_dtype, a_dev or b_dev
- * not 16-byte aligned, another pointer NULL or misaligned, y_stride < n.
+ * EPOCH_EINVAL: m < 0, n < 1, k not a positive multiple of 16 or above 2^30,
+ * n_groups not in [1, 1024], m or n_groups * n above 2^31 - 257, unknown
+ * out_dtype, a_dev or b_dev not 16-byte aligned, another pointer NULL or
+ * misaligned, y_stride < n.
  * A bounded device wait that gives up sets the operators' error word. */
 epoch_status epoch_fp8_matmul(const void *a_dev, const float *a_scales_dev, const void *b_dev,
                               const float *b_scales_dev, const int32_t *offsets_dev, int32_t n_groups, int32_t m,

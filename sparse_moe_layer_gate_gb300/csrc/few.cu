@@ -677,7 +677,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
     grid_arrive(p.ws.ctr + 1);
     if (!grid_wait(p.ws.ctr + 1, p.err, d.timeout_ns)) return;
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
-      r.sel[i] = __ldcg(p.ws.sel + i);
+      // in range even where a call that gave up left its barriers half counted
+      r.sel[i] = static_cast<int16_t>(min(max(static_cast<int>(__ldcg(p.ws.sel + i)), 0), E - 1));
       r.wgt[i] = __ldcg(p.ws.wgt + i);
     }
     __syncthreads();

@@ -136,7 +136,7 @@ epoch_status epoch_fp8_quantize_weight(const void *w, int32_t dtype, int32_t n_m
 epoch_status epoch_fp8_matmul(const void *a, const float *a_scales, const void *b, const float *b_scales,
                               const int32_t *offsets, int32_t n_groups, int32_t m, int32_t n, int32_t k, void *y,
                               int64_t y_stride, int32_t out_dtype, epoch_stream stream) {
-  if (m < 0 || n < 1 || k < 16 || k % 16 || n_groups < 1 || n_groups > 1024 || !dtype_ok(out_dtype))
+  if (m < 0 || n < 1 || k < 16 || k % 16 || k > (1 << 30) || n_groups < 1 || n_groups > 1024 || !dtype_ok(out_dtype))
     return EPOCH_EINVAL;
   if (offsets == nullptr ? n_groups != 1 : !on(offsets, 4)) return EPOCH_EINVAL;
   if (static_cast<int64_t>(n_groups) * n > INT32_MAX - 256 || m > INT32_MAX - 256) return EPOCH_EINVAL;

@@ -4,10 +4,10 @@ Norms before and after a block, fused with its gate and residual scale, and
 matrix products in 8-bit floating point (e4m3) with a scale for each block of
 128. Every operator is one launch of the sm_103a library through the C ABI
 (include/epoch.h states the formulas); it allocates its outputs where none are
-given and keeps nothing between calls. All tensors of a call are on the current
-CUDA device. ``stream`` (default: torch's current stream) orders the launch and
-the outputs allocated for it; tensors that another stream produced are the
-caller's to order.
+given and keeps nothing between calls. Results carry no gradient history. All
+tensors of a call are on the current CUDA device. ``stream`` (default: torch's
+current stream) orders the launch and the outputs allocated for it; tensors that
+another stream produced are the caller's to order.
 """
 from __future__ import annotations
 

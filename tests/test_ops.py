@@ -557,7 +557,7 @@ def _refusals():
     for kw in (dict(dtype=2), dict(mats=-1), dict(mats=65536), dict(n=0), dict(k=0), dict(n=(1 << 22) + 1), dict(w=None),
                dict(q=None), dict(s=None), dict(w=P + 1)):
         yield "epoch_fp8_quantize_weight", WEIGHT, kw
-    for kw in (dict(m=-1), dict(n=0), dict(k=0), dict(k=8), dict(k=136), dict(groups=0), dict(groups=2),
+    for kw in (dict(m=-1), dict(n=0), dict(k=0), dict(k=8), dict(k=136), dict(k=(1 << 30) + 16), dict(groups=0), dict(groups=2),
                dict(groups=1025, offsets=P), dict(offsets=P + 2), dict(groups=1024, offsets=P, n=1 << 22), dict(a=None),
                dict(a=P + 8), dict(b=P + 4), dict(b=None), dict(sa=None), dict(sb=P + 2), dict(y=None), dict(y=P + 1),
                dict(stride=63), dict(out=2)):
