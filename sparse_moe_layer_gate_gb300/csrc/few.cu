@@ -36,8 +36,8 @@
 // fp32 layers run the same schedule with FFMA in place of the tensor core.
 //
 // Measured (H 2048, 256 experts of 512 columns, 8 and 1 shared a token, bf16;
-// weights from memory): 1 token 21.9 us, of which 8 us are phases 1 and 2 and
-// 1.1 us each barrier; 32 tokens (47 experts) 67 us at 4.5 TB/s, phase 1 at 7
+// weights from memory): 1 token 21.6 us, of which 8 us are phases 1 and 2 and
+// 1.1 us each barrier; 32 tokens (47 experts) 66 us at 4.6 TB/s, phase 1 at 7
 // and phase 2 at 5.2 TB/s (its activations are twice the bytes of phase 1's
 // tokens). Reading a unit's rows only (no products, no barriers) reaches 6.1 to 6.4
 // TB/s at 400 MB with these loads. Loads leave L1 in the order in which they came,
@@ -621,6 +621,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   // phase 0: router tiles of 16 experts, then shared tiles of 8 activation columns; eight tokens a unit
   const int n_router = (E + 15) / 16, sh8 = d.n_sh ? (d.I_s + 7) / 8 : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.ws.ctr[3] = 0;  // no CTA reaches the last barrier before this one passes the first
+  // the places that activations go to, in L2: stores to lines that are not there cost a block of 32 tokens 1.4 us
+  const int64_t act_bytes = (static_cast<int64_t>(act_sh) + static_cast<int64_t>(d.n_sh) * nt * Is) * sizeof(T);
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 128; i < act_bytes; i += static_cast<int64_t>(gridDim.x) * kThreads * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(act) + i));
   if (threadIdx.x < 16 && blockIdx.x / nt8 * 16 + threadIdx.x < E)  // the bias of this CTA's experts, needed at the end of the tile
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.b_router + blockIdx.x / nt8 * 16 + threadIdx.x));
   run_units<T, false>(
