@@ -38,13 +38,12 @@
 // Measured (H 2048, 256 experts of 512 columns, 8 and 1 shared a token, bf16;
 // weights from memory): 1 token 21.6 us, of which 8 us are phases 1 and 2 and
 // 1.1 us each barrier; 32 tokens (47 experts) 66 us at 4.6 TB/s, phase 1 at 7
-// and phase 2 at 5.2 TB/s (its activations are twice the bytes of phase 1's
-// tokens). Reading a unit's rows only (no products, no barriers) reaches 6.1 to 6.4
-// TB/s at 400 MB with these loads. Loads leave L1 in the order in which they came,
-// so a hit waits for the misses before it: activations' second parts that were
-// read where they are used cost 75 us in place of 67, and tokens' rows that were asked for one
-// chunk ahead, not two, 71; sharing a group's activations between two tiles of
-// weight rows 68.
+// and phase 2 at 5.2 TB/s (its activations are as many bytes as its weights, phase
+// 1's tokens half of them). Reading a unit's rows only (no products, no barriers)
+// reaches 6.1 to 6.4 TB/s at 400 MB with these loads. Other ways for the two parts of
+// the activations, at 32 tokens where this one took 67 us: the second parts read where they
+// are used 75, tokens' rows asked for one chunk ahead and not two 71, two tiles of
+// weight rows for a group's activations 68.
 #include <atomic>
 #include <cfloat>
 #include <climits>

@@ -87,14 +87,15 @@ def norm_before(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, out
     if len(shape) != 2:
         raise ValueError("x must be [n, H]")
     n, h = shape
-    w = _vector(weight, dev, h, None, "weight")
+    w, xs = _vector(weight, dev, h, None, "weight"), _rows(x, dev, shape, "x")
     if out is None:
-        out = _empty(shape, out_dtype or x.dtype, x.device, stream)
+        out, ys = _empty(shape, out_dtype or x.dtype, x.device, stream), h
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    B.check(B.lib().epoch_norm_before(x.data_ptr(), _rows(x, dev, shape, "x"), _code(x, "x"), w, _code(weight, "weight"),
-                                      n, h, eps, out.data_ptr(), _rows(out, dev, shape, "out"), _code(out, "out"),
-                                      _stream(stream, dev)), "epoch_norm_before")
+    else:
+        ys = _rows(out, dev, shape, "out")
+    B.check(B.lib().epoch_norm_before(x.data_ptr(), xs, _code(x, "x"), w, _code(weight, "weight"), n, h, eps,
+                                      out.data_ptr(), ys, _code(out, "out"), _stream(stream, dev)), "epoch_norm_before")
     return out
 
 
@@ -137,17 +138,22 @@ def norm_after(block: torch.Tensor, residual: torch.Tensor, weight: Optional[tor
                 raise ValueError(f"gate has dtype {gate.dtype}, block {dtype}")
     elif gate_sigmoid:
         raise ValueError("gate_sigmoid without a gate")
+    bs, rs = _rows(block, dev, shape, "block"), _rows(residual, dev, shape, "residual")
     if out is None:
-        out = _empty(shape, res_dtype, block.device, stream)
+        out, ys = _empty(shape, res_dtype, block.device, stream), h
     elif out.dtype != res_dtype:
         raise ValueError(f"out has dtype {out.dtype}, residual {res_dtype}")
+    else:
+        ys = _rows(out, dev, shape, "out")
     np_, ns = 0, 0
     if next_weight is not None:
         if next_out is None:
-            next_out = _empty(shape, dtype, block.device, stream)
+            next_out, ns = _empty(shape, dtype, block.device, stream), h
         elif next_out.dtype != dtype:
             raise ValueError(f"next_out has dtype {next_out.dtype}, block {dtype}")
-        np_, ns = next_out.data_ptr(), _rows(next_out, dev, shape, "next_out")
+        else:
+            ns = _rows(next_out, dev, shape, "next_out")
+        np_ = next_out.data_ptr()
     elif next_out is not None:
         raise ValueError("next_out without next_weight")
     code = B.EPOCH_F32
@@ -156,9 +162,8 @@ def norm_after(block: torch.Tensor, residual: torch.Tensor, weight: Optional[tor
         if code is None:
             raise ValueError(f"parameters must be float32 or bfloat16, not {par}")
     args = B.NORM_AFTER_ARGS.pack(
-        block.data_ptr(), residual.data_ptr(), w, gp, scale, nw, out.data_ptr(), np_, _rows(block, dev, shape, "block"),
-        _rows(residual, dev, shape, "residual"), gs, _rows(out, dev, shape, "out"), ns, n, h, _code(block, "block"),
-        _code(residual, "residual"), code, kind, 1 if gate_sigmoid else 0, number, eps)
+        block.data_ptr(), residual.data_ptr(), w, gp, scale, nw, out.data_ptr(), np_, bs, rs, gs, ys, ns, n, h,
+        _code(block, "block"), _code(residual, "residual"), code, kind, 1 if gate_sigmoid else 0, number, eps)
     B.check(B.lib().epoch_norm_after(args, _stream(stream, dev)), "epoch_norm_after")
     return out if next_weight is None else (out, next_out)
 
@@ -206,13 +211,18 @@ def fp8_quantize(x: torch.Tensor, *, rows: Optional[torch.Tensor] = None, swiglu
     n = src if rows is None else rows.shape[0]
     xs = _rows(x, dev, x.shape, "x")
     kb = -(-k // BLOCK)
+    if n > _MOST:
+        raise ValueError("rows has more than 2^31 - 1 entries")
     if q is None:
         q = _empty((n, k), _E4M3, x.device, stream)
+    else:
+        _bytes(q, dev, (n, k), "q")
     if scales is None:
         scales = _empty((n, kb), torch.float32, x.device, stream)
-    B.check(B.lib().epoch_fp8_quantize(x.data_ptr(), xs, _code(x, "x"), rp, n, src, k, 1 if swiglu else 0,
-                                       _bytes(q, dev, (n, k), "q"), _scales(scales, dev, (n, kb), "scales"),
-                                       _stream(stream, dev)), "epoch_fp8_quantize")
+    else:
+        _scales(scales, dev, (n, kb), "scales")
+    B.check(B.lib().epoch_fp8_quantize(x.data_ptr(), xs, _code(x, "x"), rp, n, src, k, 1 if swiglu else 0, q.data_ptr(),
+                                       scales.data_ptr(), _stream(stream, dev)), "epoch_fp8_quantize")
     return q, scales
 
 
@@ -259,10 +269,11 @@ def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     ap, asp = _bytes(a, dev, (m, k), "a"), _scales(a_scales, dev, (m, kb), "a_scales")
     bp, bsp = _bytes(b, dev, lead + (n, k), "b"), _scales(b_scales, dev, lead + (nb, kb), "b_scales")
     if out is None:
-        out = _empty((m, n), out_dtype or torch.bfloat16, a.device, stream)
+        out, ys = _empty((m, n), out_dtype or torch.bfloat16, a.device, stream), n
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    ys = _rows(out, dev, (m, n), "out")
+    else:
+        ys = _rows(out, dev, (m, n), "out")
     B.check(B.lib().epoch_fp8_matmul(ap, asp, bp, bsp, op, groups, m, n, k, out.data_ptr(), ys, _code(out, "out"),
                                      _stream(stream, dev)), "epoch_fp8_matmul")
     return out
