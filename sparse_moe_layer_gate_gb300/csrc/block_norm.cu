@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(512, E == 8 && VPT <= 2 ? 2 : 1) k_block_norm(
 // VEC: the eight columns are neighbours and come in 16-byte loads. Else (rows of an odd
 // length start anywhere) they lie tpr apart, so a warp's scalar loads are neighbours.
 // FULL: the gate has a value for each row and column, and is read with the row.
+// THREADS: scalar rows of up to 8192 columns take a CTA of up to 1024 threads each (vector
+// rows gain nothing from that: 2432 of 8192 took 58 us so, 56 by short CTAs).
 constexpr int kStayThreads = 512;
 
 template <bool VEC, typename T> struct Row8;
@@ -306,8 +308,8 @@ template <typename T> struct Row8<false, T> {
   }
 };
 
-template <typename TA, typename TR, bool AFTER, bool FULL, bool VEC>
-__global__ void __launch_bounds__(kStayThreads, VEC ? 2 : 1) k_block_norm_stay(const NormArgs a, int tpr) {
+template <typename TA, typename TR, bool AFTER, bool FULL, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, VEC && THREADS == kStayThreads ? 2 : 1) k_block_norm_stay(const NormArgs a, int tpr) {
   __shared__ float sums[64];
   int turn = 0;
   const int p = threadIdx.x % tpr, c = VEC ? 8 * p : p;
@@ -425,14 +427,14 @@ __global__ void __launch_bounds__(kStayThreads, VEC ? 2 : 1) k_block_norm_stay(c
   }
 }
 
-template <typename TA, typename TR, bool AFTER, bool VEC>
+template <typename TA, typename TR, bool AFTER, bool VEC, int THREADS>
 cudaError_t launch_stay(const NormArgs &a, int tpr, cudaStream_t s) {
-  const int rpb = kStayThreads / tpr, threads = tpr * rpb;
+  const int rpb = THREADS / tpr, threads = tpr * rpb;
   const int64_t blocks = (a.n_rows + rpb - 1) / rpb;
-  const int64_t most = static_cast<int64_t>(num_sms()) * (VEC ? 2 : 1);
+  const int64_t most = static_cast<int64_t>(num_sms()) * (VEC && THREADS == kStayThreads ? 2 : 1);
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER, VEC><<<grid, threads, 0, s>>>(a, tpr);
-  else k_block_norm_stay<TA, TR, AFTER, false, VEC><<<grid, threads, 0, s>>>(a, tpr);
+  if (AFTER && a.gate_kind == 2) k_block_norm_stay<TA, TR, AFTER, AFTER, VEC, THREADS><<<grid, threads, 0, s>>>(a, tpr);
+  else k_block_norm_stay<TA, TR, AFTER, false, VEC, THREADS><<<grid, threads, 0, s>>>(a, tpr);
   return cudaGetLastError();
 }
 
@@ -455,20 +457,23 @@ cudaError_t choose(const NormArgs &a, cudaStream_t s) {
     //   H = 2048   304, 1/2: 4.45 / 3.89    608, 1: 5.22 / 5.16   1216, 2: 7.57 / 7.83
     //             1824, 3: 12.96 / 10.60   2432, 4: 15.39 / 13.16   9728, 16: 47.3 / 42.0
     //   H = 4096   152, 1/2: 4.53 / 3.90    608, 2: 7.76 / 8.22    912, 3: 13.41 / 11.24
-    // Scalar rows stay always: 20000 of 1001 take 175 / 69, 1216 of 2047 27 / 10.
+    // Scalar rows stay always: 20000 of 1001 take 175 / 69, 1216 of 2047 27 / 10, 2432 of 5761 176 / 104.
     const int wide = (a.hidden + 255) / 256 * 32;
     if (wide <= kStayThreads) {
       const int64_t places = 2ll * num_sms() * (kStayThreads / wide);
       if (E == 1 || a.n_rows <= places || a.n_rows >= 3 * places)
-        return launch_stay<TA, TR, AFTER, E == 8>(a, wide, s);
+        return launch_stay<TA, TR, AFTER, E == 8, kStayThreads>(a, wide, s);
     }
+    if constexpr (E == 1)
+      if (wide <= 2 * kStayThreads) return launch_stay<TA, TR, AFTER, false, 2 * kStayThreads>(a, wide, s);
   }
   // threads of a row: whole warps, enough for 16 values each; more values from 16 warps on
   const int want = (a.hidden + 511) / 512 * 32, tpr = want < 512 ? want : 512;
   const int64_t vpt = (a.hidden + static_cast<int64_t>(tpr) * E - 1) / (static_cast<int64_t>(tpr) * E);
-  if constexpr (E == 8)
+  if constexpr (E == 8) {  // scalar rows of so few columns stay
     if (vpt == 1) return launch<TA, TR, AFTER, E, 1>(a, tpr, s);
-  if (vpt * E <= 16) return launch<TA, TR, AFTER, E, 16 / E>(a, tpr, s);
+    if (vpt == 2) return launch<TA, TR, AFTER, E, 2>(a, tpr, s);
+  }
   if (vpt * E <= 32) return launch<TA, TR, AFTER, E, 32 / E>(a, tpr, s);
   return launch<TA, TR, AFTER, E, 0>(a, 512, s);
 }

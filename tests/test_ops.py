@@ -160,7 +160,7 @@ def test_norm_after(ops, n, h, at, rt, pt, form):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,h", [(1300, 4096), (2433, 2048), (5001, 1000), (20000, 64), (9731, 8), (6011, 1088),
-                                 (2600, 2816), (700, 4632)])
+                                 (2600, 2816), (700, 4632), (1500, 1001), (400, 5761)])
 @pytest.mark.parametrize("at,rt", [(BF16, BF16), (BF16, F32), (F32, F32)])
 @pytest.mark.parametrize("form", ["before", "channel", "full", "no_weight"])
 def test_norms_of_many_rows(ops, n, h, at, rt, form):
