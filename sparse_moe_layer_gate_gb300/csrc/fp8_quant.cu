@@ -98,9 +98,26 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quant_wide(const QuantArg
   *reinterpret_cast<uint4 *>(a.q + row * a.cols + c) = make_uint4(q[0], q[1], q[2], q[3]);
 }
 
+// Eight consecutive elements from a 16-byte boundary on.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
 // Any row: sixteen threads take a block, eight columns each; a CTA takes sixteen
-// consecutive blocks.
-template <typename T, bool SWIGLU>
+// consecutive blocks. VEC: eight columns at a time (8192 rows of 2040, bf16: 20.1 us by
+// single elements, 14.4 so).
+template <typename T, bool SWIGLU, bool VEC>
 __global__ void __launch_bounds__(kQuantThreads) k_fp8_quant(const QuantArgs a, int kb_n) {
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16);
   const int64_t row0 = first / kb_n;
@@ -117,13 +134,23 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quant(const QuantArgs a, 
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
   if (n > 0 && !bad) {
     const T *p = static_cast<const T *>(a.x) + src * a.x_stride + c;
+    if constexpr (VEC) {
+      load8(p, v);
+      if constexpr (SWIGLU) {
+        float u[8];
+        load8(p + a.cols, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) v[i] = to_f32(p[i]);
-    if constexpr (SWIGLU) {
+        for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * u[i];
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n) v[i] = silu(v[i]) * to_f32(p[a.cols + i]);
+        if (i < n) v[i] = to_f32(p[i]);
+      if constexpr (SWIGLU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < n) v[i] = silu(v[i]) * to_f32(p[a.cols + i]);
+      }
     }
   }
   unsigned m = 0;
@@ -136,6 +163,12 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quant(const QuantArgs a, 
   if ((threadIdx.x & 15) == 0) a.scales[row * kb_n + kb] = s;
   const float inv = 1.0f / s;
   uint8_t *q = a.q + row * a.cols + c;
+  if constexpr (VEC) {
+    if (n > 0)
+      *reinterpret_cast<uint2 *>(q) = make_uint2(fp8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                                                 fp8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) q[i] = static_cast<uint8_t>(fp8_pack4(v[i] * inv, 0.f, 0.f, 0.f) & 0xFFu);
@@ -171,16 +204,17 @@ __global__ void __launch_bounds__(256) k_fp8_quant_weight(const T *w, int64_t n,
   }
 }
 
-template <typename T, bool SWIGLU> cudaError_t launch_blocks(const QuantArgs &a, bool wide, cudaStream_t s) {
+template <typename T, bool SWIGLU> cudaError_t launch_blocks(const QuantArgs &a, int per, cudaStream_t s) {
   const int kb = (a.cols + 127) / 128;
-  if (wide) {
+  if (per == 16) {
     int tx = 0;
     while (tx < 5 && (kb >> tx) % 2 == 0) ++tx;
     const int64_t rows = 32 >> tx, grid = (a.n_rows + rows - 1) / rows * (kb >> tx);
     k_fp8_quant_wide<T, SWIGLU><<<static_cast<unsigned>(grid), kQuantThreads, 0, s>>>(a, kb, tx);
   } else {
-    const int64_t per = kQuantThreads / 16, grid = (a.n_rows * kb + per - 1) / per;
-    k_fp8_quant<T, SWIGLU><<<static_cast<unsigned>(grid), kQuantThreads, 0, s>>>(a, kb);
+    const int64_t blocks = kQuantThreads / 16, grid = (a.n_rows * kb + blocks - 1) / blocks;
+    if (per == 8) k_fp8_quant<T, SWIGLU, true><<<static_cast<unsigned>(grid), kQuantThreads, 0, s>>>(a, kb);
+    else k_fp8_quant<T, SWIGLU, false><<<static_cast<unsigned>(grid), kQuantThreads, 0, s>>>(a, kb);
   }
   return cudaGetLastError();
 }
@@ -188,12 +222,13 @@ template <typename T, bool SWIGLU> cudaError_t launch_blocks(const QuantArgs &a,
 }  // namespace
 
 cudaError_t launch_fp8_quant(const QuantArgs &a, bool bf16, cudaStream_t s) {
-  // sixteen columns at a time where every such piece starts on a 16-byte boundary
+  // sixteen or eight columns at a time where every such piece starts on a 16-byte boundary (of q, on one of its size)
   const int64_t per16 = bf16 ? 8 : 4;
-  const bool wide = a.cols % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
-                    (a.n_src <= 1 || a.x_stride % per16 == 0) && (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0;
-  if (a.swiglu) return bf16 ? launch_blocks<__nv_bfloat16, true>(a, wide, s) : launch_blocks<float, true>(a, wide, s);
-  return bf16 ? launch_blocks<__nv_bfloat16, false>(a, wide, s) : launch_blocks<float, false>(a, wide, s);
+  const uintptr_t q = reinterpret_cast<uintptr_t>(a.q);
+  const bool on16 = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && (a.n_src <= 1 || a.x_stride % per16 == 0);
+  const int per = on16 && a.cols % 16 == 0 && (q & 15u) == 0 ? 16 : on16 && a.cols % 8 == 0 && (q & 7u) == 0 ? 8 : 1;
+  if (a.swiglu) return bf16 ? launch_blocks<__nv_bfloat16, true>(a, per, s) : launch_blocks<float, true>(a, per, s);
+  return bf16 ? launch_blocks<__nv_bfloat16, false>(a, per, s) : launch_blocks<float, false>(a, per, s);
 }
 
 cudaError_t launch_fp8_quant_weight(const void *w, bool bf16, int64_t mats, int64_t n, int64_t k, uint8_t *q,
