@@ -170,6 +170,16 @@ def test_routers_and_options(Layer, c, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(60, 4, 2, 6), (140, 4, 1, 3), (1001, 7, 3, 8), (96, 32, 5, 8), (35, 5, 1, 7),
+                                                    (12, 6, 1, 8), (250, 2, 1, 16), (21, 21, 4, 4)])
+def test_groups_of_any_size(Layer, E, n_group, topk_group, k):
+    c = dict(router="sigmoid_group", n_group=n_group, topk_group=topk_group)
+    lay, w = make(Layer, 256, E, 128, k, "bf16", seed=E, bias_scale=0.02, **c)
+    for n in (1, 16, 33):
+        check(lay, w, tokens(256, n, "bf16", seed=n), dict(c, top_k=k), "bf16", least=0.8)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("router", ["softmax", "sigmoid_group"])
 def test_exact_ties_go_to_the_lower_expert(Layer, router):
     """x = 0: every logit is its bias, in groups of four equal values."""
