@@ -504,8 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
 #pragma unroll
           for (int h0 = 0; h0 < kCols / kPart; h0 += kTogether) {
             if (n0 + kPart * h0 >= p.g.N) break;
-            // what was here has left
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(2 / kTogether - 1) : "memory");
+            // What was here has left. A tile begins with the first place whichever the last one ended with (one part or
+            // three of fp32 at the last columns of N: the first), so all of that tile's stores have to have read theirs.
+            if (lane == 0) {
+              if (h0 == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              else asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(2 / kTogether - 1) : "memory");
+            }
             __syncwarp();
 #pragma unroll
             for (int h = h0; h < h0 + kTogether; ++h) {

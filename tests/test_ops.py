@@ -418,6 +418,23 @@ def test_fp8_matmul_repeats_bit_by_bit(ops, m):
         assert torch.equal(ops.fp8_matmul(qa, sa, qb, sb, offsets=off), first)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [4128, 4176, 4256])
+@pytest.mark.parametrize("k", [16, 128, 400])
+def test_fp8_matmul_pairs_whose_last_columns_are_an_odd_number_of_parts(ops, n, k):
+    """fp32 tiles of CTA pairs leave 32 columns at a time from two places in shared memory in turn, and a pair takes
+    several tiles: with one part or three in the last columns, the next tile begins where the last store may still read."""
+    m = 8192
+    qa, sa, qb, sb = _operands(ops, _gen(n + k), m, n, k, 1)
+    y, s = _product64(qa, sa, qb, sb, [0, m])
+    bound = _product_bound(y, s, k, F32)
+    first = ops.fp8_matmul(qa, sa, qb[0], sb[0], out_dtype=F32)
+    _within(first, y, bound)
+    for _ in range(4):
+        assert torch.equal(ops.fp8_matmul(qa, sa, qb[0], sb[0], out_dtype=F32), first)
+    assert ops.status() == (0, 0)
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 @pytest.mark.gpu
 def test_ops_on_a_stream_of_their_own_and_in_a_graph(ops):
