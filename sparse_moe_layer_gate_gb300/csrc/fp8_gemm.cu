@@ -862,7 +862,9 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, b_rows);
   if (ok && !pairs && (a.offsets || a.m % kBm != 0))
     ok = encode_kmajor_8bit(&p.a[0], a.a, a.K, a.m, 32) && encode_kmajor_8bit(&p.a[1], a.a, a.K, a.m, 64);
-  if (ok && pairs && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % (a.out_bf16 ? 8 : 4) == 0) {
+  // Bulk stores end a row on a 16-byte boundary: with another N they write zeros into the columns behind it.
+  const int per16 = a.out_bf16 ? 8 : 4;
+  if (ok && pairs && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % per16 == 0 && a.N % per16 == 0) {
     ok = encode_rows(&p.out, a.out, a.out_bf16, a.N, a.m, a.out_stride);
     p.g.bulk_out = 1;
   }

@@ -308,7 +308,7 @@ struct GemmArgs {
   int32_t m, N, K, n_groups;
   int32_t out_bf16;
   int32_t wide_out;  // rows of the output start on 32-byte boundaries
-  int32_t bulk_out;  // the output has a tensor map
+  int32_t bulk_out;  // the output has a tensor map: its rows start and end on 16-byte boundaries
 };
 cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s);
 // Device error word of the operators without a layer, on the current device (nullptr: none).

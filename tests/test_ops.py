@@ -435,6 +435,19 @@ def test_fp8_matmul_pairs_whose_last_columns_are_an_odd_number_of_parts(ops, n, 
     assert ops.status() == (0, 0)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("out,n", [(BF16, 4097), (BF16, 4100), (BF16, 4104), (F32, 4098), (F32, 4100), (F32, 4199)])
+def test_fp8_matmul_pairs_leave_the_columns_behind_n_alone(ops, out, n):
+    """Rows of a wider buffer that start on 16-byte boundaries and end anywhere."""
+    m, k, stride = 4096, 144, 4208
+    qa, sa, qb, sb = _operands(ops, _gen(n), m, n, k, 1)
+    buf = torch.full((m, stride), 77.0, device="cuda", dtype=out)
+    got = ops.fp8_matmul(qa, sa, qb[0], sb[0], out=buf[:, :n])
+    assert bool((buf[:, n:] == 77).all())
+    y, s = _product64(qa, sa, qb, sb, [0, m])
+    _within(got, y, _product_bound(y, s, k, out))
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 @pytest.mark.gpu
 def test_ops_on_a_stream_of_their_own_and_in_a_graph(ops):
