@@ -515,6 +515,14 @@ epoch_status epoch_fp8_matmul(const void *a_dev, const float *a_scales_dev, cons
                               int32_t n, int32_t k, void *y_dev, int64_t y_stride, int32_t out_dtype,
                               epoch_stream stream);
 
+/* Which kernel epoch_fp8_matmul takes for these sizes (n_groups 0: dense) on a
+ * device of n_sms SMs (0: the current device): 0 the one for few rows, 32, 64, 128
+ * or 256 tiles of 128 rows and that many columns, EPOCH_FP8_PAIRS tiles of 256 x 256 by
+ * pairs of CTAs; -1 for sizes out of range. Host only, for inspection and tests:
+ * results do not depend on the caller knowing it. */
+#define EPOCH_FP8_PAIRS 512
+int32_t epoch_fp8_matmul_kernel(int32_t n_groups, int32_t m, int32_t n, int32_t n_sms);
+
 /* Sticky error word of the operators beside the layer, one per device, for all
  * streams: read (synchronises the stream) with the status that epoch_get_status
  * gives, and cleared when clear is nonzero. Not for stream capture. */

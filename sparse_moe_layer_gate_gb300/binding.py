@@ -20,6 +20,7 @@ EPOCH_REFRESH_NEVER = 2**31 - 1
 EPOCH_DEVERR_FLAGS, EPOCH_DEVERR_TIMEOUT, EPOCH_DEVERR_BOUNDS = 1, 2, 4
 EPOCH_PROF_KINDS = 12
 EPOCH_FEW_MAX = 64
+EPOCH_FP8_PAIRS = 512
 EPOCH_GATE_NONE, EPOCH_GATE_CHANNEL, EPOCH_GATE_FULL = range(3)
 
 
@@ -112,6 +113,7 @@ _SIGS = {
                                             C.c_void_p, C.c_void_p]),
     "epoch_fp8_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
                                    C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
+    "epoch_fp8_matmul_kernel": (C.c_int32, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "epoch_ops_status": (C.c_int, [C.c_int32, C.c_void_p, C.POINTER(C.c_uint32)]),
     "epoch_layer_destroy": (None, [C.c_void_p]),
     "epoch_status_str": (C.c_char_p, [C.c_int]),

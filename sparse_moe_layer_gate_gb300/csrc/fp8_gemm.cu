@@ -818,11 +818,38 @@ uint32_t *ops_error_word() {
   return cudaGetDevice(&dev) == cudaSuccess ? ops_error_address(dev) : nullptr;
 }
 
-cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
-  const int kb_n = (a.K + kBk - 1) / kBk, nb_n = (a.N + kFp8Block - 1) / kFp8Block;
+// The kernel a product takes: 0 the one for few rows, else the columns of a tile of single CTAs, kFp8Pairs tiles of CTA
+// pairs. n_groups 0: dense.
+int fp8_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms) {
   // Few rows: the weights' bytes and latency bound the time. Rows of one expert cost mma.sync products (4096 x 4096:
   // 6.2 us at 8 rows, 8.1 at 16, 14 at 32, where the tiles below take 13), rows of several experts hardly.
-  if (a.m <= (a.offsets ? kSmallTokens : 16)) {
+  if (m <= (n_groups ? kSmallTokens : 16)) return 0;
+  const int64_t E = n_groups ? n_groups : 1;
+  // The tile: the one whose rounds of tiles take the least time, by the clocks that a K block of each took. Pairs
+  // need groups that fill 256 rows.
+  const int64_t mt = m / kBm + (n_groups ? (E < m ? E : m) : (m % kBm != 0));
+  auto cost = [&](int64_t tiles, int64_t at_once, int64_t clocks) { return (tiles + at_once - 1) / at_once * clocks; };
+  int bn = 256;
+  int64_t best = cost(mt * ((N + 255) / 256), sms, 1000);
+  const int64_t narrow[3][2] = {{128, 720}, {64, 600}, {32, 560}};
+  for (const auto &c : narrow) {
+    const int64_t t = cost(mt * ((N + c[0] - 1) / c[0]), sms, c[1]);
+    if (t < best) {
+      best = t;
+      bn = static_cast<int>(c[0]);
+    }
+  }
+  if (m >= 256 * E && sms >= 2) {
+    const int64_t tiles = (m / 256 + (n_groups ? E : m % 256 != 0)) * ((N + 255) / 256);
+    if (cost(tiles, sms / 2, 800) <= best) return kFp8Pairs;
+  }
+  return bn;
+}
+
+cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
+  const int kb_n = (a.K + kBk - 1) / kBk, nb_n = (a.N + kFp8Block - 1) / kFp8Block;
+  const int kernel = fp8_gemm_kernel(a.offsets ? a.n_groups : 0, a.m, a.N, num_sms());
+  if (kernel == 0) {
     if (a.m <= 8) return launch_small<1>(a, kb_n, nb_n, s);
     if (a.m <= 16) return launch_small<2>(a, kb_n, nb_n, s);
     if (a.m <= 32) return launch_small<4>(a, kb_n, nb_n, s);
@@ -838,27 +865,8 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   p.timeout_ns = 2000000000ll;
   if (p.err == nullptr || !tma_encode_init()) return cudaErrorInitializationError;
   const int64_t E = a.offsets ? a.n_groups : 1;
-  // The tile: the one whose rounds of tiles take the least time, by the clocks that a K block of each took. Pairs
-  // need groups that fill 256 rows.
-  const int sms = num_sms();
-  const int64_t mt = a.m / kBm + (a.offsets ? (E < a.m ? E : a.m) : (a.m % kBm != 0));
-  auto cost = [&](int64_t tiles, int64_t at_once, int64_t clocks) { return (tiles + at_once - 1) / at_once * clocks; };
-  int bn = 256;
-  int64_t best = cost(mt * ((a.N + 255) / 256), sms, 1000);
-  const int64_t narrow[3][2] = {{128, 720}, {64, 600}, {32, 560}};
-  for (const auto &c : narrow) {
-    const int64_t t = cost(mt * ((a.N + c[0] - 1) / c[0]), sms, c[1]);
-    if (t < best) {
-      best = t;
-      bn = static_cast<int>(c[0]);
-    }
-  }
-  bool pairs = false;
-  if (a.m >= 256 * E) {
-    const int64_t tiles = (a.m / 256 + (a.offsets ? E : a.m % 256 != 0)) * ((a.N + 255) / 256);
-    pairs = cost(tiles, sms / 2, 800) <= best;
-  }
-  const uint32_t b_rows = pairs ? Geo<256, true>::b_rows : bn;
+  const bool pairs = kernel == kFp8Pairs;
+  const uint32_t b_rows = pairs ? Geo<256, true>::b_rows : kernel;
   bool ok = encode_kmajor_8bit(&p.a[2], a.a, a.K, a.m, 128) && encode_kmajor_8bit(&p.b, a.b, a.K, E * a.N, b_rows);
   if (ok && !pairs && (a.offsets || a.m % kBm != 0))
     ok = encode_kmajor_8bit(&p.a[0], a.a, a.K, a.m, 32) && encode_kmajor_8bit(&p.a[1], a.a, a.K, a.m, 64);
@@ -870,9 +878,9 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   }
   if (!ok) return cudaErrorInvalidValue;
   if (pairs) return a.out_bf16 ? launch_tc<256, true, true>(p, s) : launch_tc<256, true, false>(p, s);
-  if (bn == 256) return a.out_bf16 ? launch_tc<256, false, true>(p, s) : launch_tc<256, false, false>(p, s);
-  if (bn == 128) return a.out_bf16 ? launch_tc<128, false, true>(p, s) : launch_tc<128, false, false>(p, s);
-  if (bn == 64) return a.out_bf16 ? launch_tc<64, false, true>(p, s) : launch_tc<64, false, false>(p, s);
+  if (kernel == 256) return a.out_bf16 ? launch_tc<256, false, true>(p, s) : launch_tc<256, false, false>(p, s);
+  if (kernel == 128) return a.out_bf16 ? launch_tc<128, false, true>(p, s) : launch_tc<128, false, false>(p, s);
+  if (kernel == 64) return a.out_bf16 ? launch_tc<64, false, true>(p, s) : launch_tc<64, false, false>(p, s);
   return a.out_bf16 ? launch_tc<32, false, true>(p, s) : launch_tc<32, false, false>(p, s);
 }
 

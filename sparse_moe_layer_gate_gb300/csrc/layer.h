@@ -311,6 +311,9 @@ struct GemmArgs {
   int32_t bulk_out;  // the output has a tensor map: its rows start and end on 16-byte boundaries
 };
 cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s);
+// The kernel that launch_fp8_gemm takes on a device of `sms` SMs (host only; see epoch_fp8_matmul_kernel).
+constexpr int kFp8Pairs = EPOCH_FP8_PAIRS;
+int fp8_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms);
 // Device error word of the operators without a layer, on the current device (nullptr: none).
 uint32_t *ops_error_word();
 

@@ -160,6 +160,11 @@ epoch_status epoch_fp8_matmul(const void *a, const float *a_scales, const void *
   return status_of(launch_fp8_gemm(g, S(stream)));
 }
 
+int32_t epoch_fp8_matmul_kernel(int32_t n_groups, int32_t m, int32_t n, int32_t n_sms) {
+  if (m < 0 || n < 1 || n_groups < 0 || n_groups > 1024 || n_sms < 0) return -1;
+  return fp8_gemm_kernel(n_groups, m, n, n_sms ? n_sms : num_sms());
+}
+
 epoch_status epoch_ops_status(int32_t clear, epoch_stream stream, uint32_t *word_out) {
   uint32_t *at = ops_error_word();
   uint32_t word = 0;

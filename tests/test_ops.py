@@ -448,6 +448,60 @@ def test_fp8_matmul_pairs_leave_the_columns_behind_n_alone(ops, out, n):
     _within(got, y, _product_bound(y, s, k, out))
 
 
+# Every kernel that a product can take (epoch_fp8_matmul_kernel): kernel, groups (0: dense), m, n, k. Pairs: several tiles
+# each, last pairs of which one CTA has no row, edges of N inside and outside a CTA's half, K tails, ragged and empty
+# groups. From 32 groups on a lane holds several offsets.
+KERNELS = [(0, 0, 13, 520, 272), (0, 33, 60, 40, 400), (0, 1024, 64, 40, 144), (32, 0, 129, 511, 272), (32, 6, 421, 272, 400),
+           (64, 0, 500, 2000, 400), (128, 0, 500, 2600, 1168), (128, 0, 1000, 2000, 16), (256, 0, 800, 5000, 400),
+           (256, 40, 3000, 2100, 272), (256, 200, 2000, 1500, 144), (256, 1024, 5000, 136, 48), (256, 64, 1500, 520, 1040),
+           (512, 0, 8191, 4100, 272), (512, 0, 4097, 4104, 16), (512, 0, 8065, 4191, 144), (512, 0, 1290, 5000, 1168),
+           (512, 0, 4500, 2300, 2064), (512, 0, 6216, 1600, 400), (512, 5, 6000, 4104, 272), (512, 3, 2500, 6001, 128),
+           (512, 7, 9001, 4096, 400)]
+
+
+def test_every_kernel_of_the_product_has_a_shape_below(lib):
+    for kernel, e, m, n, _ in KERNELS:
+        assert lib.epoch_fp8_matmul_kernel(e, m, n, 152) == kernel, (e, m, n)
+    assert {c[0] for c in KERNELS} == {0, 32, 64, 128, 256, 512}
+    for bad in ((-1, 4, 4, 152), (1025, 4, 4, 152), (0, -1, 4, 152), (0, 4, 0, 152), (0, 4, 4, -1)):
+        assert lib.epoch_fp8_matmul_kernel(*bad) == -1
+    for sms in (1, 2, 3):  # small devices have a kernel for every size too
+        assert all(lib.epoch_fp8_matmul_kernel(e, m, n, sms) in (0, 32, 64, 128, 256, 512) for _, e, m, n, _ in KERNELS)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("apart", ["whole", "wide", "odd"])
+@pytest.mark.parametrize("case", KERNELS, ids=str)
+def test_fp8_matmul_by_every_kernel(ops, lib, case, apart, out):
+    """Rows of the output that follow one another, lie apart on 32-byte boundaries (the stores of wide pieces), or start
+    anywhere (single elements); columns and rows that are not the product's stay as they were."""
+    kernel, e, m, n, k = case
+    assert lib.epoch_fp8_matmul_kernel(e, m, n, 0) == kernel
+    g = _gen(m + n + k)
+    qa, sa, qb, sb = _operands(ops, g, m, n, k, max(e, 1))
+    if e:  # ragged groups, some of them empty, three rows before the first and five behind the last
+        cuts = torch.randint(3, m - 4, (e + 1,), generator=torch.Generator().manual_seed(m)).sort().values
+        cuts[0], cuts[-1] = 3, m - 5
+        cuts[e // 2] = cuts[e // 2 + 1] if e > 1 else cuts[0]
+        offsets = cuts.sort().values.tolist()
+        off = torch.tensor(offsets, device="cuda", dtype=torch.int32)
+        args = (qa, sa, qb, sb)
+    else:
+        offsets, off, args = [0, m], None, (qa, sa, qb[0], sb[0])
+    first, stride = {"whole": (0, n), "wide": (0, n + 16 + -n % 16), "odd": (1, n + 2 + n % 2)}[apart]
+    buf = torch.full((m, stride), 77.0, device="cuda", dtype=out)
+    got = ops.fp8_matmul(*args, offsets=off, out=buf[:, first:first + n])
+    y, s = _product64(qa, sa, qb, sb, offsets)
+    lo, hi = offsets[0], offsets[-1]
+    _within(got[lo:hi], y[lo:hi], _product_bound(y, s, k, out)[lo:hi])
+    assert bool((buf[:lo] == 77).all()) and bool((buf[hi:] == 77).all())
+    assert bool((buf[:, :first] == 77).all()) and bool((buf[:, first + n:] == 77).all())
+    again = ops.fp8_matmul(*args, offsets=off, out_dtype=out)  # rows that follow one another: other stores, the same sums
+    assert torch.equal(again[lo:hi], got[lo:hi])
+    assert ops.status() == (0, 0)
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 @pytest.mark.gpu
 def test_ops_on_a_stream_of_their_own_and_in_a_graph(ops):
