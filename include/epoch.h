@@ -395,6 +395,13 @@ epoch_status epoch_reset_profile(epoch_layer *layer);
  * EPOCH_DEVERR_TIMEOUT and return. Exercises the timeout path without a hang. */
 epoch_status epoch_test_wait_timeout(epoch_layer *layer, int64_t timeout_ns, epoch_stream stream);
 
+/* Test hook: epoch_moe_few with a grid barrier (0 to 3; 1 is used by more than 16
+ * tokens only) that waits for one CTA more than there are: every CTA's wait there
+ * runs out after the layer's limit, EPOCH_DEVERR_TIMEOUT is set and the kernel
+ * returns; y_dev may be left unwritten. Clear the status before the next call. */
+epoch_status epoch_test_few_timeout(epoch_layer *layer, const void *x_dev, int32_t n_tok, void *y_dev, int32_t barrier,
+                                    epoch_stream stream);
+
 /* Block planner for callers that cannot allocate device memory (graph capture
  * into a fixed pool, allocator-free runtimes with a pre-planned arena, serving
  * loops that forbid cudaMalloc between requests); it needs no epoch_layer.

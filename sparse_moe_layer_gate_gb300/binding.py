@@ -115,6 +115,7 @@ _SIGS = {
                                    C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
     "epoch_fp8_matmul_kernel": (C.c_int32, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "epoch_ops_status": (C.c_int, [C.c_int32, C.c_void_p, C.POINTER(C.c_uint32)]),
+    "epoch_test_few_timeout": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p]),
     "epoch_layer_destroy": (None, [C.c_void_p]),
     "epoch_status_str": (C.c_char_p, [C.c_int]),
 }

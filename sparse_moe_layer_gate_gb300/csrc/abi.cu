@@ -250,6 +250,18 @@ epoch_status run_planner(epoch_layer *L, const Dims &d, int clear_state, int32_t
              [&] { return launch_plan_support(d, L->ws, T, all, clear_state, ids_out, len_out, tau, s); });
 }
 
+epoch_status run_few(epoch_layer *L, const void *x, int32_t n_tok, void *y, int hold, epoch_stream stream) {
+  if (L == nullptr || n_tok < 0 || n_tok > kFewTokens || n_tok > L->cfg.max_positions) return EPOCH_EINVAL;
+  if (n_tok == 0) return EPOCH_OK;
+  if (!aligned16(x) || !aligned16(y)) return EPOCH_EINVAL;
+  // rows are addressed by 32-bit element offsets
+  const int64_t acts = static_cast<int64_t>(L->dims.k) * few_row(L->dims.I) + static_cast<int64_t>(L->dims.n_sh) * few_row(L->dims.I_s);
+  if (n_tok * acts * (L->bf16 ? 2 : 1) > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;
+  cudaStream_t s = S(stream);
+  return run(L, K_FEW, s,
+             [&] { return launch_moe_few(L->dims, L->w, L->ws.few, x, y, n_tok, L->bf16, hold, L->ws.err, s); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -434,15 +446,7 @@ epoch_status epoch_moe_iter(epoch_layer *L, const void *x, const uint8_t *live, 
 }
 
 epoch_status epoch_moe_few(epoch_layer *L, const void *x, int32_t n_tok, void *y, epoch_stream stream) {
-  if (L == nullptr || n_tok < 0 || n_tok > kFewTokens || n_tok > L->cfg.max_positions) return EPOCH_EINVAL;
-  if (n_tok == 0) return EPOCH_OK;
-  if (!aligned16(x) || !aligned16(y)) return EPOCH_EINVAL;
-  // rows are addressed by 32-bit element offsets
-  const int64_t acts = static_cast<int64_t>(L->dims.k) * few_row(L->dims.I) + static_cast<int64_t>(L->dims.n_sh) * few_row(L->dims.I_s);
-  if (n_tok * acts * (L->bf16 ? 2 : 1) > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;
-  cudaStream_t s = S(stream);
-  return run(L, K_FEW, s,
-             [&] { return launch_moe_few(L->dims, L->w, L->ws.few, x, y, n_tok, L->bf16, L->ws.err, s); });
+  return run_few(L, x, n_tok, y, -1, stream);
 }
 
 epoch_status epoch_block_end(epoch_layer *L) {
@@ -582,6 +586,13 @@ epoch_status epoch_reset_profile(epoch_layer *L) {
 epoch_status epoch_test_wait_timeout(epoch_layer *L, int64_t timeout_ns, epoch_stream stream) {
   if (L == nullptr || timeout_ns < 1000 || timeout_ns > 5000000000ll) return EPOCH_EINVAL;
   return run(L, K_TEST, S(stream), [&] { return launch_wait_test(L->ws.err, timeout_ns, S(stream)); });
+}
+
+epoch_status epoch_test_few_timeout(epoch_layer *L, const void *x, int32_t n_tok, void *y, int32_t barrier,
+                                    epoch_stream stream) {
+  // barrier 1 is that of the shared selection, which only more than 16 tokens have
+  if (barrier < 0 || barrier > 3 || n_tok < 1 || (barrier == 1 && n_tok <= 16)) return EPOCH_EINVAL;
+  return run_few(L, x, n_tok, y, barrier, stream);
 }
 
 void epoch_layer_destroy(epoch_layer *L) {

@@ -109,16 +109,16 @@ __device__ __forceinline__ void group_sync(int id, int warps) {
 }
 
 // Grid barrier in two halves. Every CTA arrives once on *ctr (zero before the
-// launch's first arrival); the wait ends when all have, or gives up (false).
-// Loads issued between the halves do not hold the arrival back.
+// launch's first arrival); the wait ends when `want` have (the grid, but for the test of
+// a wait that runs out), or gives up (false). Loads issued between the halves do not
+// hold the arrival back.
 __device__ __forceinline__ void grid_arrive(int32_t *ctr) {
   __syncthreads();
   if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(ctr) : "memory");
 }
-__device__ bool grid_wait(const int32_t *ctr, uint32_t *err, int64_t timeout_ns) {
+__device__ bool grid_wait(const int32_t *ctr, int32_t want, uint32_t *err, int64_t timeout_ns) {
   __shared__ int s_ok;
   if (threadIdx.x == 0) {
-    const int32_t want = static_cast<int32_t>(gridDim.x);
     auto seen = [&] {
       int32_t v;
       asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
@@ -128,7 +128,7 @@ __device__ bool grid_wait(const int32_t *ctr, uint32_t *err, int64_t timeout_ns)
     if (seen() < want) {
       const uint64_t t0 = globaltimer_ns();
       for (uint32_t i = 1; seen() < want; ++i)
-        if ((i & 63u) == 0u && globaltimer_ns() - t0 > static_cast<uint64_t>(timeout_ns)) {
+        if ((i & 7u) == 0u && globaltimer_ns() - t0 > static_cast<uint64_t>(timeout_ns)) {
           set_error(err, EPOCH_DEVERR_TIMEOUT);
           ok = 0;
           break;
@@ -349,6 +349,7 @@ struct FewParams {
   void *y;
   uint32_t *err;
   int n_tok;
+  int hold;  // grid barrier that waits for one CTA more than there are (a test's), or -1
 };
 
 // Routing tables of a CTA, in shared memory. A job is at most eight tokens of an
@@ -634,6 +635,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   T *act = static_cast<T *>(p.ws.act);     // row of edge e at e * Ia,
   const int act_sh = p.n_tok * k * Ia;     // of shared expert s and token t at act_sh + (s * n_tok + t) * Is
 
+  auto wait = [&](int b) {
+    return grid_wait(p.ws.ctr + b, static_cast<int32_t>(gridDim.x) + (p.hold == b), p.err, d.timeout_ns);
+  };
   auto split = [&](Share &o, int cols, int w, int warps) {
     const int chunks = (cols + chunk - 1) / chunk;
     o.k = cols;
@@ -701,7 +705,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
   // One warp runs the selection on whatever the logits hold by now, so that its code is in the instruction cache
   // when the barrier opens (its results are written again below).
   if (warp == 1 && nt <= kWarps) select(0, r.sel, r.wgt);
-  if (!grid_wait(p.ws.ctr, p.err, d.timeout_ns)) return;
+  if (!wait(0)) return;
 
   if (nt <= kWarps) {
     if (warp < nt) select(warp, r.sel + warp * k, r.wgt + warp * k);
@@ -711,7 +715,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
     const int tok = blockIdx.x + warp * gridDim.x;
     if (tok < nt) select(tok, p.ws.sel + tok * k, p.ws.wgt + tok * k);
     grid_arrive(p.ws.ctr + 1);
-    if (!grid_wait(p.ws.ctr + 1, p.err, d.timeout_ns)) return;
+    if (!wait(1)) return;
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
       // in range even where a call that gave up left its barriers half counted
       r.sel[i] = static_cast<int16_t>(min(max(static_cast<int>(__ldcg(p.ws.sel + i)), 0), E - 1));
@@ -784,10 +788,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) k_moe_few(c
           if (col < Ho) __stcg(p.ws.out + static_cast<size_t>(at) * Ho + col, sum(mine, warps, tok, c));
         }
       },
-      [&] { return grid_wait(p.ws.ctr + 2, p.err, d.timeout_ns); });
+      [&] { return wait(2); });
   if (!in_time) return;
   grid_arrive(p.ws.ctr + 3);
-  if (!grid_wait(p.ws.ctr + 3, p.err, d.timeout_ns)) return;
+  if (!wait(3)) return;
   if (blockIdx.x == 0 && threadIdx.x < 3) p.ws.ctr[threadIdx.x] = 0;  // every CTA has left these barriers
 
   // y, four columns a thread, edges in selection order
@@ -846,7 +850,7 @@ template <typename T> cudaError_t launch(const FewParams &p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_moe_few(const Dims &d, const Weights &w, const FewWork &ws, const void *x, void *y, int n_tok,
-                           int bf16, uint32_t *err, cudaStream_t s) {
+                           int bf16, int hold, uint32_t *err, cudaStream_t s) {
   FewParams p;
   p.d = d;
   p.w = w;
@@ -855,6 +859,7 @@ cudaError_t launch_moe_few(const Dims &d, const Weights &w, const FewWork &ws, c
   p.y = y;
   p.err = err;
   p.n_tok = n_tok;
+  p.hold = hold;
   return bf16 ? launch<__nv_bfloat16>(p, s) : launch<float>(p, s);
 }
 

@@ -228,9 +228,10 @@ cudaError_t launch_wait_test(uint32_t *err, int64_t timeout_ns, cudaStream_t s);
 cudaError_t launch_up_simt(const Dims &d, const Weights &w, const Work &ws, const void *x, cudaStream_t s);
 cudaError_t launch_down_simt(const Dims &d, const Weights &w, const Work &ws, cudaStream_t s);
 
-// few.cu: the whole layer for n_tok <= kFewTokens tokens in one cooperative launch
+// few.cu: the whole layer for n_tok <= kFewTokens tokens in one cooperative launch. hold: the grid barrier (0 to 3)
+// whose wait has to run out, for tests, or -1.
 cudaError_t launch_moe_few(const Dims &d, const Weights &w, const FewWork &ws, const void *x, void *y, int n_tok,
-                           int bf16, uint32_t *err, cudaStream_t s);
+                           int bf16, int hold, uint32_t *err, cudaStream_t s);
 
 // gemm_tc.cu (bf16 layers, tcgen05 + TMA)
 // Packs row-major [rows][k] bf16 into swizzled tiles at dst + t * tile_stride + tile_off.

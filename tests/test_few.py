@@ -359,6 +359,31 @@ def test_a_wait_that_runs_out_is_reported_and_cleared(Layer):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,barriers", [(1, (0, 2, 3)), (16, (0, 2, 3)), (40, (0, 1, 2, 3))])
+def test_every_barriers_wait_can_run_out(Layer, dtype, n, barriers):
+    """A barrier that waits for an arrival that never comes gives up after the limit: the call returns, the status
+    says so, and after clearing it the layer gives the same bits as before."""
+    from sparse_moe_layer_gate_gb300 import binding as B
+    lay, _ = make(Layer, 512, 32, 128, 4, dtype, 1, seed=15)
+    x = tokens(512, n, dtype)
+    want, y = lay.forward_few(x), torch.empty_like(x)
+    assert lay.status() == (0, 0)
+    stream = torch.cuda.current_stream().cuda_stream
+    lay.set_wait_timeout(1_000_000)
+    for b in barriers:
+        assert B.lib().epoch_test_few_timeout(lay.handle, x.data_ptr(), n, y.data_ptr(), b, stream) == B.EPOCH_OK
+        assert lay.status() == (4, 2)  # EPOCH_ETIMEOUT, EPOCH_DEVERR_TIMEOUT
+        assert lay.status() == (4, 2)  # until it is cleared
+        lay.clear_status()
+        assert torch.equal(lay.forward_few(x), want)
+        assert lay.status() == (0, 0)
+    for b in (-1, 4) + (() if n > 16 else (1,)):
+        assert B.lib().epoch_test_few_timeout(lay.handle, x.data_ptr(), n, y.data_ptr(), b, stream) == B.EPOCH_EINVAL
+    assert B.lib().epoch_test_few_timeout(None, x.data_ptr(), n, y.data_ptr(), 0, stream) == B.EPOCH_EINVAL
+
+
+@pytest.mark.gpu
 def test_refusals(Layer):
     lay, _ = make(Layer, 256, 16, 128, 2, "bf16", max_positions=20)
     x = tokens(256, 64, "bf16")
