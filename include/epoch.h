@@ -516,7 +516,8 @@ epoch_status epoch_fp8_quantize_weight(const void *w_dev, int32_t dtype, int32_t
  * n_groups not in [1, 1024], m or n_groups * n above 2^31 - 257, unknown
  * out_dtype, a_dev or b_dev not 16-byte aligned, another pointer NULL or
  * misaligned, y_stride < n.
- * A bounded device wait that gives up sets the operators' error word. */
+ * A device wait that makes no progress for 2 s gives up, sets the operators' error
+ * word and lets the kernel return. */
 epoch_status epoch_fp8_matmul(const void *a_dev, const float *a_scales_dev, const void *b_dev,
                               const float *b_scales_dev, const int32_t *offsets_dev, int32_t n_groups, int32_t m,
                               int32_t n, int32_t k, void *y_dev, int64_t y_stride, int32_t out_dtype,
@@ -529,6 +530,15 @@ epoch_status epoch_fp8_matmul(const void *a_dev, const float *a_scales_dev, cons
  * results do not depend on the caller knowing it. */
 #define EPOCH_FP8_PAIRS 512
 int32_t epoch_fp8_matmul_kernel(int32_t n_groups, int32_t m, int32_t n, int32_t n_sms);
+
+/* Test hook: epoch_fp8_matmul by its tiles' kernel whose operand copies count 16
+ * bytes that never come: every wait runs out after timeout_ns (1000 to 5e9), the
+ * timeout bit of the operators' error word is set, the kernel returns and y_dev is not
+ * written. EPOCH_EINVAL also for a product of few rows, whose kernel has no waits. */
+epoch_status epoch_test_fp8_timeout(const void *a_dev, const float *a_scales_dev, const void *b_dev,
+                                    const float *b_scales_dev, const int32_t *offsets_dev, int32_t n_groups, int32_t m,
+                                    int32_t n, int32_t k, void *y_dev, int64_t y_stride, int32_t out_dtype,
+                                    int64_t timeout_ns, epoch_stream stream);
 
 /* Sticky error word of the operators beside the layer, one per device, for all
  * streams: read (synchronises the stream) with the status that epoch_get_status

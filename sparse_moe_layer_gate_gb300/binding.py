@@ -113,6 +113,9 @@ _SIGS = {
                                             C.c_void_p, C.c_void_p]),
     "epoch_fp8_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
                                    C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
+    "epoch_test_fp8_timeout": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32,
+                                         C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_int64,
+                                         C.c_void_p]),
     "epoch_fp8_matmul_kernel": (C.c_int32, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "epoch_ops_status": (C.c_int, [C.c_int32, C.c_void_p, C.POINTER(C.c_uint32)]),
     "epoch_test_few_timeout": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p]),

@@ -52,6 +52,7 @@ struct GemmParams {
   int kb_n, nb_n, nt_n;  // K blocks, N scale blocks, N tiles
   uint32_t *err;
   int64_t timeout_ns;
+  uint32_t hold;  // bytes that a stage waits for beyond its copies': 0, but for the test of waits that run out
 };
 
 // Shape N x M of kind::f8f6f4 with e4m3 operands, fp32 accumulator, both K-major.
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         walk.at(t, &e, &row0, &rows, &nt);
         // single CTAs load the smallest box that holds their rows
         const int box = PAIR || rows > 64 ? 2 : rows > 32 ? 1 : 0;
-        const uint32_t bytes = PAIR ? 2 * G::stage : ((32u << box) + BN) * kBk;
+        const uint32_t bytes = (PAIR ? 2 * G::stage : ((32u << box) + BN) * kBk) + p.hold;
         const int brow = e * p.g.N + nt * BN + rank * G::b_rows;
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
           ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
@@ -846,7 +847,7 @@ int fp8_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms) {
   return bn;
 }
 
-cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
+cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s, int64_t timeout_ns, uint32_t hold) {
   const int kb_n = (a.K + kBk - 1) / kBk, nb_n = (a.N + kFp8Block - 1) / kFp8Block;
   const int kernel = fp8_gemm_kernel(a.offsets ? a.n_groups : 0, a.m, a.N, num_sms());
   if (kernel == 0) {
@@ -862,7 +863,8 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s) {
   p.kb_n = kb_n;
   p.nb_n = nb_n;
   p.err = ops_error_word();
-  p.timeout_ns = 2000000000ll;
+  p.timeout_ns = timeout_ns;
+  p.hold = hold;
   if (p.err == nullptr || !tma_encode_init()) return cudaErrorInitializationError;
   const int64_t E = a.offsets ? a.n_groups : 1;
   const bool pairs = kernel == kFp8Pairs;

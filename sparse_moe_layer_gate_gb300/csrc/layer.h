@@ -311,7 +311,9 @@ struct GemmArgs {
   int32_t wide_out;  // rows of the output start on 32-byte boundaries
   int32_t bulk_out;  // the output has a tensor map: its rows start and end on 16-byte boundaries
 };
-cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s);
+// hold: bytes that never come, so that the waits run out (a test's; kernels of few rows have none).
+constexpr int64_t kFp8TimeoutNs = 2000000000ll;
+cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s, int64_t timeout_ns = kFp8TimeoutNs, uint32_t hold = 0);
 // The kernel that launch_fp8_gemm takes on a device of `sms` SMs (host only; see epoch_fp8_matmul_kernel).
 constexpr int kFp8Pairs = EPOCH_FP8_PAIRS;
 int fp8_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms);

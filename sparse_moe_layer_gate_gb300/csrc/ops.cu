@@ -23,6 +23,34 @@ epoch_status status_of(cudaError_t e) { return e == cudaSuccess ? EPOCH_OK : EPO
 
 constexpr int32_t kMaxHidden = 1 << 20;
 
+// Checks the arguments of a product and puts them together (m > 0).
+epoch_status product(const void *a, const float *a_scales, const void *b, const float *b_scales, const int32_t *offsets,
+                     int32_t n_groups, int32_t m, int32_t n, int32_t k, void *y, int64_t y_stride, int32_t out_dtype,
+                     GemmArgs *g) {
+  if (m < 0 || n < 1 || k < 16 || k % 16 || k > (1 << 30) || n_groups < 1 || n_groups > 1024 || !dtype_ok(out_dtype))
+    return EPOCH_EINVAL;
+  if (offsets == nullptr ? n_groups != 1 : !on(offsets, 4)) return EPOCH_EINVAL;
+  if (static_cast<int64_t>(n_groups) * n > INT32_MAX - 256 || m > INT32_MAX - 256) return EPOCH_EINVAL;
+  if (m == 0) return EPOCH_OK;
+  if (!on(a, 16) || !on(b, 16) || !on(a_scales, 4) || !on(b_scales, 4) || !of_type(y, out_dtype) ||
+      !stride_ok(y_stride, m, n))
+    return EPOCH_EINVAL;
+  *g = GemmArgs{};
+  g->a = a;
+  g->b = b;
+  g->sa = a_scales;
+  g->sb = b_scales;
+  g->offsets = offsets;
+  g->out = y;
+  g->out_stride = y_stride;
+  g->m = m;
+  g->N = n;
+  g->K = k;
+  g->n_groups = n_groups;
+  g->out_bf16 = out_dtype == EPOCH_BF16;
+  return EPOCH_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -136,28 +164,22 @@ epoch_status epoch_fp8_quantize_weight(const void *w, int32_t dtype, int32_t n_m
 epoch_status epoch_fp8_matmul(const void *a, const float *a_scales, const void *b, const float *b_scales,
                               const int32_t *offsets, int32_t n_groups, int32_t m, int32_t n, int32_t k, void *y,
                               int64_t y_stride, int32_t out_dtype, epoch_stream stream) {
-  if (m < 0 || n < 1 || k < 16 || k % 16 || k > (1 << 30) || n_groups < 1 || n_groups > 1024 || !dtype_ok(out_dtype))
-    return EPOCH_EINVAL;
-  if (offsets == nullptr ? n_groups != 1 : !on(offsets, 4)) return EPOCH_EINVAL;
-  if (static_cast<int64_t>(n_groups) * n > INT32_MAX - 256 || m > INT32_MAX - 256) return EPOCH_EINVAL;
-  if (m == 0) return EPOCH_OK;
-  if (!on(a, 16) || !on(b, 16) || !on(a_scales, 4) || !on(b_scales, 4) || !of_type(y, out_dtype) ||
-      !stride_ok(y_stride, m, n))
-    return EPOCH_EINVAL;
-  GemmArgs g = {};
-  g.a = a;
-  g.b = b;
-  g.sa = a_scales;
-  g.sb = b_scales;
-  g.offsets = offsets;
-  g.out = y;
-  g.out_stride = y_stride;
-  g.m = m;
-  g.N = n;
-  g.K = k;
-  g.n_groups = n_groups;
-  g.out_bf16 = out_dtype == EPOCH_BF16;
+  GemmArgs g;
+  const epoch_status st = product(a, a_scales, b, b_scales, offsets, n_groups, m, n, k, y, y_stride, out_dtype, &g);
+  if (st != EPOCH_OK || m == 0) return st;
   return status_of(launch_fp8_gemm(g, S(stream)));
+}
+
+epoch_status epoch_test_fp8_timeout(const void *a, const float *a_scales, const void *b, const float *b_scales,
+                                    const int32_t *offsets, int32_t n_groups, int32_t m, int32_t n, int32_t k, void *y,
+                                    int64_t y_stride, int32_t out_dtype, int64_t timeout_ns, epoch_stream stream) {
+  GemmArgs g;
+  const epoch_status st = product(a, a_scales, b, b_scales, offsets, n_groups, m, n, k, y, y_stride, out_dtype, &g);
+  if (st != EPOCH_OK) return st;
+  if (timeout_ns < 1000 || timeout_ns > 5000000000ll || m == 0 ||
+      fp8_gemm_kernel(offsets ? n_groups : 0, m, n, num_sms()) == 0)
+    return EPOCH_EINVAL;
+  return status_of(launch_fp8_gemm(g, S(stream), timeout_ns, 16));
 }
 
 int32_t epoch_fp8_matmul_kernel(int32_t n_groups, int32_t m, int32_t n, int32_t n_sms) {

@@ -502,6 +502,35 @@ def test_fp8_matmul_by_every_kernel(ops, lib, case, apart, out):
     assert ops.status() == (0, 0)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("case", [(32, 0, 129, 511, 272), (32, 6, 421, 272, 400), (64, 0, 500, 2000, 400), (128, 0, 500, 2600, 1168),
+                                  (256, 40, 3000, 2100, 1040), (512, 0, 4500, 2300, 2064), (512, 3, 2500, 6000, 128)], ids=str)
+def test_fp8_matmul_waits_that_run_out(ops, lib, case, out):
+    """Operands that never come whole: the call returns after its limit, writes nothing, says so until it is asked to
+    clear that, and the next product is as before."""
+    kernel, e, m, n, k = case
+    assert lib.epoch_fp8_matmul_kernel(e, m, n, 0) == kernel
+    qa, sa, qb, sb = _operands(ops, _gen(m), m, n, k, max(e, 1))
+    off = torch.arange(e + 1, device="cuda", dtype=torch.int32) * (m // e) if e else None
+    args = (qa, sa, qb, sb) if e else (qa, sa, qb[0], sb[0])
+    want = torch.zeros(m, n, device="cuda", dtype=out)
+    ops.fp8_matmul(*args, offsets=off, out=want)
+    y = torch.full((m, n), 77.0, device="cuda", dtype=out)
+    raw = (qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), off.data_ptr() if e else None, max(e, 1), m, n, k,
+           y.data_ptr(), n, 1 if out == BF16 else 0)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.epoch_test_fp8_timeout(*raw, 1_000_000, stream) == 0
+    assert ops.status() == (4, 2)  # EPOCH_ETIMEOUT, EPOCH_DEVERR_TIMEOUT
+    assert ops.status(clear=True) == (4, 2) and ops.status() == (0, 0)
+    assert bool((y == 77).all())
+    got = torch.zeros(m, n, device="cuda", dtype=out)
+    assert torch.equal(ops.fp8_matmul(*args, offsets=off, out=got), want) and ops.status() == (0, 0)
+    assert lib.epoch_test_fp8_timeout(*raw, 999, stream) == 1  # EPOCH_EINVAL
+    few = raw[:6] + (min(16, m),) + raw[7:] if not e else raw[:6] + (60,) + raw[7:]
+    assert lib.epoch_test_fp8_timeout(*few, 1_000_000, stream) == 1
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 @pytest.mark.gpu
 def test_ops_on_a_stream_of_their_own_and_in_a_graph(ops):
