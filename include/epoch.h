@@ -339,7 +339,7 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
  * epoch_set_wait_timeout): EPOCH_ECUDA where the device cannot hold one CTA per
  * SM at once. Zero tokens enqueue nothing.
  * EPOCH_EINVAL if n_tok is not in [0, min(EPOCH_FEW_MAX, max_positions)], x_dev or
- * y_dev is NULL/misaligned, or n_tok rows of x, or of the activations (top_k *
+ * y_dev is NULL/misaligned, they overlap without being one, or n_tok rows of x, or of the activations (top_k *
  * inter + n_shared * shared_inter columns each, in bf16 layers twice as many),
  * exceed 2^31 elements. */
 #define EPOCH_FEW_MAX 64
@@ -435,8 +435,9 @@ epoch_status epoch_plan_support_noalloc(const float *logits_dev, int32_t n_pos, 
  * epoch_layer, keep nothing between calls, allocate nothing and use no
  * workspace, so calls on any streams may overlap and be captured into graphs.
  * Strides are in elements between consecutive rows; rows themselves are
- * contiguous. Zero rows is a valid call that enqueues nothing. Outputs may
- * alias inputs only where a function says so. */
+ * contiguous. Zero rows is a valid call that enqueues nothing. An output that
+ * shares a byte with an input or another output is refused (EPOCH_EINVAL), but where a
+ * function says otherwise; rows of one buffer in turn, or its columns side by side, share none. */
 
 /* RMS norm before a block: h = x / sqrt(mean(x^2) + eps) * weight.
  *  x_dev [n_rows][hidden] of x_dtype (the residual stream), out_dev of
@@ -461,7 +462,8 @@ epoch_status epoch_norm_before(const void *x_dev, int64_t x_stride, int32_t x_dt
  *  g: gate_kind EPOCH_GATE_NONE 1; EPOCH_GATE_CHANNEL gate [hidden];
  *  EPOCH_GATE_FULL gate [n_rows][hidden] of dtype; through the logistic
  *  function first where gate_sigmoid is nonzero.
- *  out may be residual, next_out may be block (same strides).
+ *  out and next_out may each be a row input (block, residual, a full gate) of the
+ *  same dtype and stride.
  * EPOCH_EINVAL as epoch_norm_before, for a NULL args, a gate_kind without its
  * gate, and for exactly one of next_weight and next_out. */
 enum { EPOCH_GATE_NONE = 0, EPOCH_GATE_CHANNEL = 1, EPOCH_GATE_FULL = 2 };

@@ -254,6 +254,9 @@ epoch_status run_few(epoch_layer *L, const void *x, int32_t n_tok, void *y, int 
   if (L == nullptr || n_tok < 0 || n_tok > kFewTokens || n_tok > L->cfg.max_positions) return EPOCH_EINVAL;
   if (n_tok == 0) return EPOCH_OK;
   if (!aligned16(x) || !aligned16(y)) return EPOCH_EINVAL;
+  const int64_t apart = static_cast<const char *>(y) - static_cast<const char *>(x);
+  const int64_t bytes = static_cast<int64_t>(n_tok) * L->dims.H * (L->bf16 ? 2 : 4);
+  if (apart != 0 && apart < bytes && -apart < bytes) return EPOCH_EINVAL;
   // rows are addressed by 32-bit element offsets
   const int64_t acts = static_cast<int64_t>(L->dims.k) * few_row(L->dims.I) + static_cast<int64_t>(L->dims.n_sh) * few_row(L->dims.I_s);
   if (n_tok * acts * (L->bf16 ? 2 : 1) > INT32_MAX || static_cast<int64_t>(n_tok) * L->dims.H > INT32_MAX) return EPOCH_EINVAL;

@@ -19,6 +19,36 @@ bool of_type_or_null(const void *p, int32_t d) { return p == nullptr || of_type(
 bool stride_ok(int64_t stride, int32_t n_rows, int64_t width) {
   return n_rows <= 1 || (stride >= width && stride <= (INT64_MAX >> 4) / n_rows);
 }
+
+// Bytes of an argument: `rows` runs of `width`, `stride` apart (none where the pointer is null).
+struct Rows {
+  const char *at;
+  int64_t rows, width, stride;
+  Rows(const void *p, int64_t n, int64_t w, int64_t s, size_t size)
+      : at(static_cast<const char *>(p)), rows(p ? n : 0), width(w * static_cast<int64_t>(size)),
+        stride(n > 1 ? s * static_cast<int64_t>(size) : width) {}
+  Rows(const void *p, int64_t n, size_t size) : Rows(p, 1, n, n, size) {}
+  const char *end() const { return at + (rows - 1) * stride + width; }
+  // the other's bytes row by row, so its type too
+  bool same(const Rows &o) const { return at == o.at && rows == o.rows && width == o.width && stride == o.stride; }
+};
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && a < 0); }
+// Whether two arguments share a byte: columns of one buffer side by side, or rows of it in turn, do not.
+bool overlap(const Rows &a, const Rows &b) {
+  if (a.rows == 0 || b.rows == 0 || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.rows > b.rows) return overlap(b, a);
+  const int64_t d = b.at - a.at;  // row j of b starts at d + j * b.stride from a's first
+  auto meets = [&](int64_t start) {  // a's row there: rows j that end behind its start and start before its end
+    const int64_t lo = floor_div(start - d - b.width, b.stride) + 1, hi = floor_div(start + a.width - d - 1, b.stride);
+    return (lo > 0 ? lo : 0) <= (hi < b.rows - 1 ? hi : b.rows - 1);
+  };
+  // Equal strides: with as many rows or fewer, a row of a meets one of b where the first or the last one does.
+  if (a.stride == b.stride) return meets(0) || meets((a.rows - 1) * a.stride);
+  for (int64_t i = 0; i < a.rows; ++i)
+    if (meets(i * a.stride)) return true;
+  return false;
+}
+
 epoch_status status_of(cudaError_t e) { return e == cudaSuccess ? EPOCH_OK : EPOCH_ECUDA; }
 
 constexpr int32_t kMaxHidden = 1 << 20;
@@ -34,6 +64,12 @@ epoch_status product(const void *a, const float *a_scales, const void *b, const 
   if (m == 0) return EPOCH_OK;
   if (!on(a, 16) || !on(b, 16) || !on(a_scales, 4) || !on(b_scales, 4) || !of_type(y, out_dtype) ||
       !stride_ok(y_stride, m, n))
+    return EPOCH_EINVAL;
+  const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128, rows = m;
+  const Rows result(y, m, n, y_stride, size_of(out_dtype));
+  if (overlap(result, Rows(a, rows * k, 1)) || overlap(result, Rows(a_scales, rows * kb, 4)) ||
+      overlap(result, Rows(b, static_cast<int64_t>(n_groups) * n * k, 1)) ||
+      overlap(result, Rows(b_scales, n_groups * nb * kb, 4)) || overlap(result, Rows(offsets, n_groups + 1, 4)))
     return EPOCH_EINVAL;
   *g = GemmArgs{};
   g->a = a;
@@ -65,6 +101,9 @@ epoch_status epoch_norm_before(const void *x, int64_t x_stride, int32_t x_dtype,
   if (n_rows == 0) return EPOCH_OK;
   if (!of_type(x, x_dtype) || !of_type(out, out_dtype) || !stride_ok(x_stride, n_rows, hidden) ||
       !stride_ok(out_stride, n_rows, hidden))
+    return EPOCH_EINVAL;
+  const Rows in(x, n_rows, hidden, x_stride, size_of(x_dtype)), result(out, n_rows, hidden, out_stride, size_of(out_dtype));
+  if ((overlap(result, in) && !result.same(in)) || overlap(result, Rows(weight, hidden, size_of(par_dtype))))
     return EPOCH_EINVAL;
   NormArgs a = {};
   a.residual = x;
@@ -101,6 +140,20 @@ epoch_status epoch_norm_after(const epoch_norm_after_args *p, epoch_stream strea
   if (!stride_ok(p->block_stride, n, h) || !stride_ok(p->residual_stride, n, h) || !stride_ok(p->out_stride, n, h) ||
       (p->next_out != nullptr && !stride_ok(p->next_stride, n, h)))
     return EPOCH_EINVAL;
+  // An output may be an input of its type and rows: a thread reads its elements of a row before it writes them.
+  const size_t sa = size_of(p->dtype), sr = size_of(p->residual_dtype), sp = size_of(p->par_dtype);
+  const bool full = p->gate_kind == EPOCH_GATE_FULL;
+  const Rows block(p->block, n, h, p->block_stride, sa), residual(p->residual, n, h, p->residual_stride, sr);
+  const Rows gate(full ? p->gate : nullptr, n, h, p->gate_stride, sa);
+  const Rows outs[2] = {Rows(p->out, n, h, p->out_stride, sr), Rows(p->next_out, n, h, p->next_stride, sa)};
+  const void *params[4] = {p->weight, p->scale, p->next_weight, p->gate_kind == EPOCH_GATE_CHANNEL ? p->gate : nullptr};
+  if (overlap(outs[0], outs[1])) return EPOCH_EINVAL;
+  for (const Rows &o : outs) {
+    for (const Rows *in : {&block, &residual, &gate})
+      if (overlap(o, *in) && !o.same(*in)) return EPOCH_EINVAL;
+    for (const void *q : params)
+      if (overlap(o, Rows(q, h, sp))) return EPOCH_EINVAL;
+  }
   NormArgs a = {};
   a.block = p->block;
   a.residual = p->residual;
@@ -138,6 +191,12 @@ epoch_status epoch_fp8_quantize(const void *x, int64_t x_stride, int32_t dtype, 
   if ((n_src > 0 && !of_type(x, dtype)) || (rows != nullptr && !on(rows, 4)) || q == nullptr || !on(scales, 4) ||
       !stride_ok(x_stride, n_src, static_cast<int64_t>(cols) * (swiglu ? 2 : 1)))
     return EPOCH_EINVAL;
+  const int64_t wide = static_cast<int64_t>(cols) * (swiglu ? 2 : 1);
+  const Rows in(n_src ? x : nullptr, n_src, wide, x_stride, size_of(dtype)), index(rows, n_rows, 4);
+  const Rows values(q, static_cast<int64_t>(n_rows) * cols, 1), factors(scales, blocks, 4);
+  if (overlap(values, in) || overlap(factors, in) || overlap(values, index) || overlap(factors, index) ||
+      overlap(values, factors))
+    return EPOCH_EINVAL;
   QuantArgs a = {};
   a.x = x;
   a.rows = rows;
@@ -157,6 +216,10 @@ epoch_status epoch_fp8_quantize_weight(const void *w, int32_t dtype, int32_t n_m
     return EPOCH_EINVAL;
   if (n_mats == 0) return EPOCH_OK;
   if (!of_type(w, dtype) || q == nullptr || !on(scales, 4)) return EPOCH_EINVAL;
+  const int64_t count = static_cast<int64_t>(n_mats) * n * k;
+  const Rows in(w, count, size_of(dtype)), values(q, count, 1);
+  const Rows factors(scales, static_cast<int64_t>(n_mats) * ((n + 127) / 128) * ((k + 127) / 128), 4);
+  if (overlap(values, in) || overlap(factors, in) || overlap(values, factors)) return EPOCH_EINVAL;
   return status_of(launch_fp8_quant_weight(w, dtype == EPOCH_BF16, n_mats, n, k, static_cast<uint8_t *>(q), scales,
                                            S(stream)));
 }

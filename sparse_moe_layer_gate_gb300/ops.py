@@ -5,7 +5,8 @@ matrix products in 8-bit floating point (e4m3) with a scale for each block of
 128. Every operator is one launch of the sm_103a library through the C ABI
 (include/epoch.h states the formulas); it allocates its outputs where none are
 given and keeps nothing between calls. Results carry no gradient history. All
-tensors of a call are on the current CUDA device. ``stream`` (default: torch's
+tensors of a call are on the current CUDA device, and an output that overlaps an
+input is refused but where a function allows it. ``stream`` (default: torch's
 current stream) orders the launch and the outputs allocated for it; tensors that
 another stream produced are the caller's to order.
 """
@@ -111,7 +112,8 @@ def norm_after(block: torch.Tensor, residual: torch.Tensor, weight: Optional[tor
     [n, H] of another or the same; weight, next_weight, a per-channel gate and a
     tensor ``residual_scale`` are [H] of one dtype (float32 or bfloat16 each).
     weight None leaves the block's output as it is; gate_sigmoid puts the gate
-    through the logistic function. ``out`` may be residual, ``next_out`` block.
+    through the logistic function. ``out`` and ``next_out`` may each be block,
+    residual or a per-element gate of their dtype and strides.
     Returns r', or (r', h') with next_weight."""
     dev = _device(block, "block")
     shape = block.shape

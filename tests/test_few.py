@@ -408,6 +408,20 @@ def test_refusals(Layer):
         assert L.epoch_moe_few(h, args[0], args[1], args[2], None) == B.EPOCH_EINVAL
 
 
+@pytest.mark.gpu
+def test_a_y_that_overlaps_x_is_refused_by_the_abi(Layer):
+    from sparse_moe_layer_gate_gb300 import binding as B
+    lay, _ = make(Layer, 256, 16, 128, 2, "bf16")
+    buf = torch.zeros(20, 256, device="cuda", dtype=torch.bfloat16)
+    p, row = buf.data_ptr(), 512
+    for x, y in ((p, p + row), (p + 16, p), (p, p + 4 * row - 16), (p + 3 * row, p)):
+        assert B.lib().epoch_moe_few(lay.handle, x, 4, y, None) == B.EPOCH_EINVAL
+    for x, y in ((p, p), (p, p + 4 * row), (p + 4 * row, p)):
+        assert B.lib().epoch_moe_few(lay.handle, x, 4, y, None) == B.EPOCH_OK
+    torch.cuda.synchronize()
+    assert lay.status() == (0, 0)
+
+
 def test_a_null_layer_is_refused_on_the_host():
     from sparse_moe_layer_gate_gb300 import binding as B, builder
     if builder.is_stale():

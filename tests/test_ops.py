@@ -683,6 +683,100 @@ def test_refused_on_the_host(lib, name, base, change):
     assert _call(lib, name, {**base, **change}) == 1  # EPOCH_EINVAL, nothing enqueued
 
 
+POINTERS = {"x", "weight", "out", "block", "res", "gate", "scale", "nw", "nout", "rows", "q", "s", "w", "a", "sa", "b", "sb",
+            "offsets", "y"}
+
+
+def _apart(base):
+    """The arguments with every pointer in a place of its own."""
+    return {name: (P * (16 + 16 * i) if v == P else v) for i, (name, v) in enumerate(base.items())}
+
+
+@pytest.mark.parametrize("name,base,change", list(_refusals()), ids=lambda v: str(v)[:60] if not isinstance(v, dict) else "")
+def test_refused_on_the_host_without_any_overlap(lib, name, base, change):
+    """The same refusals, each for its own reason: no two pointers are one."""
+    own = {k: P * 1024 + v if k in POINTERS and v is not None and v >= P else v for k, v in change.items()}
+    assert _call(lib, name, {**_apart(base), **own}) == 1
+
+
+def _overlaps():
+    b = _apart(BEFORE)
+    x, w = b["x"], b["weight"]
+    for kw in (dict(out=x + 2), dict(out=x - 2), dict(out=x + 128), dict(out=x + 3 * 128 + 126), dict(out=x - 3 * 128),
+               dict(out=x, out_dtype=0), dict(out=x, out_stride=65), dict(out=x + 64, out_stride=64), dict(out=w + 4 * 63),
+               dict(out=w - 3 * 128), dict(x_stride=96, out_stride=96, out=x + 2 * 32 + 62), dict(x_stride=96, out_stride=96, out=x - 2),
+               dict(x_stride=640, out_stride=320, out=x + 640 * 2 * 3 - 640 - 126), dict(n=1, x_stride=0, out_stride=0, out=x + 126)):
+        yield "epoch_norm_before", b, kw
+    b = {**_apart(AFTER), "nstride": 64}
+    blk, res, w, out = b["block"], b["res"], b["weight"], b["out"]
+    far = P * 4096
+    for kw in (dict(out=blk), dict(out=res + 4), dict(out=res, out_stride=66), dict(out=w + 252), dict(nw=far, nout=out),
+               dict(nw=far, nout=out + 4 * 64 * 3), dict(nw=far, nout=res), dict(nw=far, nout=blk + 128), dict(nw=far, nout=far + 4),
+               dict(kind=1, gate=out + 4), dict(kind=2, gate=out, gate_stride=64), dict(scale=out), dict(nw=far, nout=w)):
+        yield "epoch_norm_after", b, kw
+    b = _apart(QUANT)
+    x, q, s = b["x"], b["q"], b["s"]
+    for kw in (dict(q=x), dict(q=x + 4 * 512 - 1), dict(s=x + 4), dict(s=q), dict(s=q + 4 * 255), dict(rows=q + 4), dict(rows=s + 4 * 7),
+               dict(swiglu=1, x_stride=512, q=x + 4 * 1024 - 1), dict(q=x + 512, x_stride=512)):
+        yield "epoch_fp8_quantize", b, kw
+    b = _apart(WEIGHT)
+    for kw in (dict(q=b["w"]), dict(q=b["w"] + 2 * 128 * 128 - 1), dict(s=b["w"] + 4), dict(s=b["q"] + 4)):
+        yield "epoch_fp8_quantize_weight", b, kw
+    b = _apart(MATMUL)
+    for kw in (dict(y=b["a"] + 2), dict(y=b["a"] + 4 * 128 - 2), dict(y=b["b"] + 64 * 128 - 2), dict(y=b["sa"]), dict(y=b["sb"]),
+               dict(y=b["a"] - 4 * 128 + 2), dict(offsets=b["y"] + 4)):
+        yield "epoch_fp8_matmul", b, kw
+
+
+@pytest.mark.parametrize("name,base,change", list(_overlaps()), ids=lambda v: str(v)[:60] if not isinstance(v, dict) else "")
+def test_outputs_that_overlap_are_refused(lib, name, base, change):
+    assert set(change) <= set(base)
+    assert _call(lib, name, {**base, **change}) == 1  # EPOCH_EINVAL, nothing enqueued
+
+
+@pytest.mark.gpu
+def test_rows_in_turn_and_columns_side_by_side_do_not_overlap(ops):
+    g = _gen(21)
+    n, h = 12, 64
+    w = 1 + _rnd(g, h, std=0.1)
+    x = _rnd(g, n, h)
+    # rows that start off a 16-byte boundary add their squares in another order: the formula's bound, not equal bits
+    want = _rms64(x.double(), w.double(), 1e-6)[1]
+    bound = want.abs() * _norm_units(h) * U + 1e-30
+    for layout in (lambda b: (b[:n, :h], b[:n, h:2 * h]), lambda b: (b[:n, 1:h + 1], b[:n, h + 1:2 * h + 1]),
+                   lambda b: (b[0:2 * n:2, :h], b[1:2 * n:2, :h]), lambda b: (b[0:4 * n:4, :h], b[1:2 * n:2, :h]),
+                   lambda b: (b[1:2 * n:2, 9:h + 9], b[0:4 * n:4, 9:h + 9]), lambda b: (b[n:2 * n, :h], b[:n, :h])):
+        buf = torch.full((4 * n, 3 * h), 5.0, device="cuda")
+        src, dst = layout(buf)
+        src.copy_(x)
+        assert ops.norm_before(src, w, out=dst) is dst
+        assert torch.equal(src, x)
+        _within(dst, want, bound)
+        assert int((buf != 5).sum()) == 2 * n * h
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,h", [(3, 64), (3, 1001), (700, 4632), (2, 17001)])
+def test_norm_after_into_any_row_input(ops, n, h):
+    g = _gen(22)
+    w, nw = 1 + _rnd(g, h, std=0.1), 1 + _rnd(g, h, std=0.1)
+    rows = [_rnd(g, n, h) for _ in range(3)]  # block, residual, gate
+
+    def call(t, out=None, next_out=None):
+        return ops.norm_after(t[0], t[1], w, gate=t[2], gate_sigmoid=True, next_weight=nw, out=out, next_out=next_out)
+
+    want = call(rows)
+    for i in range(3):
+        for j in range(3):
+            if i == j:
+                continue
+            t = [r.clone() for r in rows]
+            got = call(t, t[i], t[j])
+            assert got[0] is t[i] and got[1] is t[j]
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert torch.equal(t[3 - i - j], rows[3 - i - j])
+
+
 def _call(lib, name, args):
     if name == "epoch_norm_after":  # takes a struct
         from sparse_moe_layer_gate_gb300 import binding
