@@ -207,6 +207,37 @@ def test_norm_after_in_place_and_strided(ops, h):
     _within(got[1], nxt, e_nxt + nxt.abs() * _half(BF16) * (1 + 2 ** -7) + 1e-30)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,h", [(5, 64), (700, 4632), (5, 1001), (1300, 2048), (3, 16400), (2, 17001), (6, 5761)])
+@pytest.mark.parametrize("at,rt", [(BF16, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("kind", ["full", "full_sigmoid", "channel", "channel_sigmoid"])
+@pytest.mark.parametrize("pad", [16, 3])
+def test_norm_after_every_row_tensor_strided(ops, n, h, at, rt, kind, pad):
+    """Block, residual, a gate for each element and both outputs in rows of their own distances, with the gate as it is
+    and through the logistic function; what lies between the rows stays as it was."""
+    g = _gen(n + h + pad)
+    b, r, gate = _rnd(g, n, h, dtype=at), _rnd(g, n, h, std=2.0, dtype=rt), _rnd(g, n, h, std=3.0, dtype=at)
+    w, nw, scale = 1 + _rnd(g, h, std=0.2), 1 + _rnd(g, h, std=0.2), 1 + _rnd(g, h, std=0.1)
+    if kind.startswith("channel"):
+        gate = _rnd(g, h)
+
+    def apart(dtype, extra, src=None):
+        v = torch.full((n, h + extra), 77.0, device="cuda", dtype=dtype)
+        if src is not None:
+            v[:, :h] = src
+        return v
+
+    vb, vr, vo, vn = apart(at, pad, b), apart(rt, 2 * pad, r), apart(rt, 3 * pad), apart(at, 4 * pad)
+    vg = gate if gate.dim() == 1 else apart(at, 5 * pad, gate)[:, :h]
+    sig = kind.endswith("sigmoid")
+    got = ops.norm_after(vb[:, :h], vr[:, :h], w, gate=vg, gate_sigmoid=sig, residual_scale=scale, next_weight=nw, out=vo[:, :h],
+                         next_out=vn[:, :h])
+    out, e_out, nxt, e_nxt = _after64(b, r, w, gate, sig, scale, nw, 1e-6)
+    _within(got[0], out, e_out + out.abs() * _half(rt) * (rt == BF16) * (1 + 2 ** -7) + 1e-30, "r'")
+    _within(got[1], nxt, e_nxt + nxt.abs() * _half(at) * (1 + 2 ** -7) + 1e-30, "h'")
+    assert bool((vo[:, h:] == 77).all()) and bool((vn[:, h:] == 77).all())
+
+
 # ---------------------------------------------------------------------------------------- quantise
 def _scale32(amax):
     """max(amax / 448, 2^-126) rounded once to fp32: a quotient of fp32 values taken in 64 bits rounds to the fp32
@@ -529,6 +560,42 @@ def test_fp8_matmul_waits_that_run_out(ops, lib, case, out):
     assert lib.epoch_test_fp8_timeout(*raw, 999, stream) == 1  # EPOCH_EINVAL
     few = raw[:6] + (min(16, m),) + raw[7:] if not e else raw[:6] + (60,) + raw[7:]
     assert lib.epoch_test_fp8_timeout(*few, 1_000_000, stream) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [20, 700])
+def test_weights_whose_offsets_pass_32_bits(ops, m):
+    """The last of 40 matrices of 8192 x 8192 begins behind 2^31 bytes, and its rows in bf16 behind 2^32."""
+    e, n, k = 40, 8192, 8192
+    g = _gen(m)
+    w = torch.zeros(e, n, k, device="cuda", dtype=BF16)
+    last = _rnd(g, n, k, std=k ** -0.5)
+    w[-1] = last
+    qb, sb = ops.fp8_quantize_weight(w)
+    wq, ws = ops.fp8_quantize_weight(w[-1].contiguous())
+    assert torch.equal(qb[-1].view(torch.uint8), wq.view(torch.uint8)) and torch.equal(sb[-1], ws)
+    del w
+    qa, sa = ops.fp8_quantize(_rnd(g, m, k))
+    off = torch.zeros(e + 1, device="cuda", dtype=torch.int32)
+    off[-1] = m
+    got = ops.fp8_matmul(qa, sa, qb, sb, offsets=off, out_dtype=F32)
+    y, s = _product64(qa, sa, wq[None], ws[None], [0, m])
+    _within(got, y, _product_bound(y, s, k, F32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [1024, 1000, 1001])
+def test_fp8_quantize_rows_whose_offsets_pass_32_bits(ops, k):
+    g = _gen(k)
+    n, far = 3, (1 << 31) // 2 + 24
+    x = _rnd(g, n, k, dtype=BF16)
+    v = torch.empty(far * (n - 1) + k, device="cuda", dtype=BF16).as_strided((n, k), (far, 1))
+    v.copy_(x)
+    for rows in (None, torch.tensor([2, 0, 2, 1], device="cuda", dtype=torch.int32)):
+        src = x if rows is None else x[rows.long()].contiguous()
+        q, s = ops.fp8_quantize(v, rows=rows)
+        wq, ws = ops.fp8_quantize(src)
+        assert torch.equal(q.view(torch.uint8), wq.view(torch.uint8)) and torch.equal(s, ws)
 
 
 # ------------------------------------------------------------------------------ streams and graphs
