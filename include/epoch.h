@@ -329,7 +329,8 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
  * with the layer's router rule over every expert (no support, no row cache), as
  * epoch_moe_iter computes it when every position is fresh and every expert
  * eligible; expert outputs are kept in fp32 up to y. One launch that reads each
- * selected expert's weights once, from the caller's own arrays (bf16 layers keep
+ * selected expert's weights from memory once (and again from L2 for every eight
+ * further tokens of the expert), out of the caller's own arrays (bf16 layers keep
  * a packed copy for the iterations; both have to hold the same values). A
  * block's plan, cache, stamps and statistics are neither used nor changed, so it
  * may run inside a block. y_dev may be x_dev, but not otherwise overlap it. Like
@@ -339,9 +340,9 @@ epoch_status epoch_moe_iter_path(epoch_layer *layer, const void *x_dev, const ui
  * epoch_set_wait_timeout): EPOCH_ECUDA where the device cannot hold one CTA per
  * SM at once. Zero tokens enqueue nothing.
  * EPOCH_EINVAL if n_tok is not in [0, min(EPOCH_FEW_MAX, max_positions)], x_dev or
- * y_dev is NULL/misaligned, they overlap without being one, or n_tok rows of x, or of the activations (top_k *
- * inter + n_shared * shared_inter columns each, in bf16 layers twice as many),
- * exceed 2^31 elements. */
+ * y_dev is NULL/misaligned, they overlap without being one, or n_tok rows of x, or
+ * of the activations (top_k * inter + n_shared * shared_inter columns each, in bf16
+ * layers twice as many), exceed 2^31 elements. */
 #define EPOCH_FEW_MAX 64
 epoch_status epoch_moe_few(epoch_layer *layer, const void *x_dev, int32_t n_tok, void *y_dev, epoch_stream stream);
 

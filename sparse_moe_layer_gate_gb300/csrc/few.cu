@@ -5,8 +5,10 @@
 //   y_t = sum_{e in S_t} w_te W_down,e (silu(W_gate,e x_t) * (W_up,e x_t)) + sum_shared (+ x_t)
 //
 // With at most 64 tokens the bytes of the selected experts' weights bound the
-// time, so the kernel is built around reading each of them once, from global
-// memory straight into registers, with loads always in flight. One CTA per SM
+// time, so the kernel is built around reading each of them from memory once,
+// straight into registers, with loads always in flight. (Eight tokens share a
+// reading; an expert of more has its rows read again from L2 for every eight: 43
+// tokens on 12 experts take 2.8 times their floor, a block on 47 experts 1.5 times.) One CTA per SM
 // stays for the whole call; its phases are separated by grid barriers:
 //
 //   0. router logits, and the shared experts' activations, which need no routing;

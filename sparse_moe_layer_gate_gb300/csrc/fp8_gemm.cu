@@ -17,8 +17,9 @@
 // side at a time, so the reading of an accumulator (256 clocks at 256 columns)
 // adds to its products (512) and a K block of a pair takes about 790 clocks;
 // narrow tiles are taken where a round of wide ones would leave SMs idle.
-// 8192 x 4096 x 4096 to bf16 95 us (2.9 PFLOP/s), to fp32 106 us; 256 experts of
-// 1024 x 2048 with 8192 rows 94 us, where the weights' bytes bound it (6.1 TB/s).
+// 8192 x 4096 x 4096 to bf16 95 us (2.9 PFLOP/s), to fp32 104 us; 256 experts of
+// 1024 x 2048 with 8192 rows 93 us, where the weights' bytes bound it (6.1 TB/s). K is
+// not split: 17 to 128 rows by 4096 x 4096 take 11 us, since 128 CTAs walk all of K.
 //
 // Few rows (k_fp8_small): bound by the weights' bytes; sixteen weight rows per
 // CTA go from global memory straight into mma.sync fragments (see below). One row

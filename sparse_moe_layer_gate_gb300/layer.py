@@ -155,8 +155,10 @@ class EpochLayer:
         int32 views of the workspace in stream order: positions [max_positions *
         top_k], of which the first offsets[-1] are this iteration's, and offsets
         [n_experts + 1]. What ops.fp8_quantize (rows) and ops.fp8_matmul (offsets)
-        take, so FP8 experts run over the layer's own routing. The next call on the
-        layer overwrites them."""
+        take, so FP8 experts run over the layer's own routing. Only moe_iter fills
+        them (and has run its own experts then); positions behind offsets[-1] are
+        zero or an earlier iteration's, and the routing weights are not among them.
+        The next moe_iter on the layer overwrites them."""
         v = B.epoch_debug_view()
         B.check(B.lib().epoch_debug_pointers(self.handle, C.byref(v)), "epoch_debug_pointers")
 
