@@ -164,21 +164,12 @@ def _packed(code):
     return code[..., 0::2] | (code[..., 1::2] << 4)
 
 
-def _row_scales(s, form):
-    """[n, K / block] -> [ceil(K / 256), n, scales of 256 columns]: what the products read of a tile's rows is contiguous."""
+def _laid(s, form):
+    """[.., n, K / block] -> [.., ceil(K / 256), n, scales of 256 columns]: what the products read of a tile's rows is contiguous."""
     per = 256 // BLOCK[form]
-    kb = -(-s.shape[1] // per)
-    return torch.nn.functional.pad(s.view(torch.uint8), (0, kb * per - s.shape[1])).view(-1, kb, per).transpose(0, 1).contiguous().view(s.dtype)
-
-
-def _weight_scales(s, form):
-    """[E, N, K / block] -> [E, ceil(N / 128), ceil(K / 256), 4 or 2, 32, 4, 4]: element [.., g, l, c, j] belongs to row
-    32 c + l of 128 and to scale 4 g + j of 256 columns."""
-    E, N, kn = s.shape
-    per = 256 // BLOCK[form]
-    nb, kb = -(-N // 128), -(-kn // per)
-    p = torch.nn.functional.pad(s.view(torch.uint8), (0, kb * per - kn, 0, nb * 128 - N))
-    return p.view(E, nb, 4, 32, kb, per // 4, 4).permute(0, 1, 4, 5, 3, 2, 6).contiguous().view(s.dtype)
+    kb = -(-s.shape[-1] // per)
+    p = torch.nn.functional.pad(s.view(torch.uint8), (0, kb * per - s.shape[-1]))
+    return p.unflatten(-1, (kb, per)).transpose(-2, -3).contiguous().view(s.dtype)
 
 
 def _routing(sel, E):
@@ -236,7 +227,7 @@ def prepare(case, seed):
             t = torch.exp2(torch.ceil(torch.log2(w.abs().amax((1, 2)) / (6 * 448)))) if c["form"] == "nvfp4" else torch.ones(E, device=DEV)
             w /= t.view(-1, 1, 1)
             b, sb = _fp4(w, c["form"])
-            s |= {"a": _packed(a), "sa": _row_scales(sa, c["form"]), "b": _packed(b), "sb": _weight_scales(sb, c["form"]), "scale": t}
+            s |= {"a": _packed(a), "sa": _laid(sa, c["form"]), "b": _packed(b), "sb": _laid(sb, c["form"]), "scale": t}
     return s
 
 
@@ -301,7 +292,7 @@ def _quant_plain(s):
     if c["way"] == "swiglu":
         x = _swiglu(x)
     code, scale = _fp4(x / c["tscale"], c["form"])
-    return _values(code, scale, c["tscale"]).to(BF16), _row_scales(scale, c["form"])
+    return _values(code, scale, c["tscale"]).to(BF16), _laid(scale, c["form"])
 
 
 def _values(code, scale, tscale):
@@ -310,18 +301,11 @@ def _values(code, scale, tscale):
     return (v.unflatten(-1, (scale.shape[-1], -1)) * (scale.float() * tscale).unsqueeze(-1)).flatten(-2)
 
 
-def _opened(q, scale, K, weight):
-    """Values of packed codes: scales in the layout of rows or of weights."""
-    code = torch.stack([q & 15, q >> 4], -1).flatten(-2)
-    n = code.shape[-2]
-    raw = scale.view(torch.uint8)
-    if weight:
-        E, nb, kb = raw.shape[:3]
-        rows = raw.permute(0, 1, 5, 4, 2, 3, 6).reshape(E, nb * 128, -1)[:, :n]
-    else:
-        rows = raw.transpose(0, 1).reshape(n, -1)
+def _opened(q, scale, K):
+    """Values of packed codes [.., n, K / 2]."""
+    rows = scale.view(torch.uint8).transpose(-2, -3).flatten(-2)
     block = 16 if scale.dtype == E4M3 else 32
-    return _values(code, rows[..., :K // block].contiguous().view(scale.dtype), 1.0)
+    return _values(torch.stack([q & 15, q >> 4], -1).flatten(-2), rows[..., :K // block].contiguous().view(scale.dtype), 1.0)
 
 
 def _grouped_plain(a, b, s, scale=None):
@@ -347,7 +331,7 @@ def run(state):
             x = s["x"] if s["rows"] is None else s["x"][s["rows"].long()]
             return _grouped_plain(x.float(), s["w"].float(), s)
         if c["op"] == "fp4":
-            return _grouped_plain(_opened(s["a"], s["sa"], c["K"], False), _opened(s["b"], s["sb"], c["K"], True), s, s["scale"])
+            return _grouped_plain(_opened(s["a"], s["sa"], c["K"]), _opened(s["b"], s["sb"], c["K"]), s, s["scale"])
         return {"route": _route_plain, "combine": _combine_plain, "quant": _quant_plain}[c["op"]](s)
     from sparse_moe_layer_gate_gb300 import ops
     if c["op"] == "route":
@@ -421,16 +405,9 @@ def exact(case, seed):
         if c["op"] == "group":
             y[lo:hi] = x[lo:hi] @ s["w"][e].double().T
         else:
-            y[lo:hi] = _fp4_exact(s["a"][lo:hi], s["sa"][:, lo:hi], c["K"]) @ _fp4_exact(s["b"][e], _rows_of(s["sb"][e], c["N"]), c["K"]).T
+            y[lo:hi] = _fp4_exact(s["a"][lo:hi], s["sa"][:, lo:hi], c["K"]) @ _fp4_exact(s["b"][e], s["sb"][e], c["K"]).T
             y[lo:hi] *= s["scale"][e].double()
     return silu(y) if c["swiglu"] else y
-
-
-def _rows_of(scales, N):
-    """A matrix's scales [nb, kb, g, 32, 4, 4] as [kb, N, 4 g]."""
-    nb, kb, g = scales.shape[:3]
-    t = scales.view(torch.uint8).permute(1, 0, 4, 3, 2, 5).reshape(kb, nb * 128, g * 4)[:, :N]
-    return t.contiguous().view(scales.dtype)
 
 
 def _fp4_exact(q, scales, K):
