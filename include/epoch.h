@@ -434,7 +434,8 @@ epoch_status epoch_plan_support_noalloc(const float *logits_dev, int32_t n_pos, 
 /* ------------------------------------------------------------------ operators beside the layer
  * What a model runs around an MoE layer and its FP8 form. They need no
  * epoch_layer, keep nothing between calls, allocate nothing and use no
- * workspace, so calls on any streams may overlap and be captured into graphs.
+ * workspace (but epoch_route, whose caller gives one), so calls on any streams may
+ * overlap and be captured into graphs.
  * Strides are in elements between consecutive rows; rows themselves are
  * contiguous. Zero rows is a valid call that enqueues nothing. An output that
  * shares a byte with an input or another output is refused (EPOCH_EINVAL), but where a
@@ -542,6 +543,149 @@ epoch_status epoch_test_fp8_timeout(const void *a_dev, const float *a_scales_dev
                                     const float *b_scales_dev, const int32_t *offsets_dev, int32_t n_groups, int32_t m,
                                     int32_t n, int32_t k, void *y_dev, int64_t y_stride, int32_t out_dtype,
                                     int64_t timeout_ns, epoch_stream stream);
+
+/* ------------------------------------------------------------------ the experts by themselves
+ * A router with the products of its experts, for a layer that is run in parts:
+ *   epoch_route -> (epoch_fp4_quantize ->) epoch_expert_matmul -> epoch_combine
+ * Conventions as for the operators above. */
+
+/* Router: from logits to each position's experts and weights and to the
+ * expert-sorted worklist, without running an expert.
+ *  logits [n_tok][n_experts] of dtype, rows logits_stride apart.
+ *  EPOCH_ROUTER_SOFTMAX: the top_k largest logits (bias must be NULL: it is part of
+ *    the logits), equal ones by lower id; weights are a softmax over them, or with
+ *    raw_weights their probabilities among all n_experts.
+ *  EPOCH_ROUTER_SIGMOID_GROUP: the top_k largest sigmoid(logit) + bias (NULL: 0)
+ *    under the group rule of epoch_layer_config, in exact arithmetic; weights are the
+ *    selected sigmoids over their sum, or with raw_weights the sigmoids.
+ *  live [n_tok] (NULL: all): a position with 0 is routed to no expert.
+ *  eligible [n_experts] (NULL: all): an expert with 0 is never selected; nor is one
+ *    whose logit is -inf. A NaN ranks below every number and makes all of its
+ *    position's weights NaN.
+ *  sel, weights, slots [n_tok][top_k]: experts in order of selection, weights, and each
+ *    edge's row of the worklist; -1, 0 and -1 where fewer than top_k can be selected.
+ *  positions [n_tok * top_k]: the worklist, expert-major, positions ascending; -1
+ *    behind its offsets[n_experts] rows. offsets [n_experts + 1].
+ *  workspace: epoch_route_workspace_bytes bytes (4-byte aligned; may be NULL where that is
+ *    0); calls that may overlap need one each.
+ * EPOCH_EINVAL: n_tok < 0, n_experts not in [1, 1024], top_k not in [1, min(16,
+ * n_experts)], n_tok * top_k above 2^31 - 257, n_group not in [1, 32] or no divisor of
+ * n_experts, topk_group not in [1, n_group] (softmax: both are ignored), a NULL or
+ * misaligned pointer, logits_stride < n_experts, too small a workspace, outputs that
+ * overlap. */
+typedef struct {
+  const void *logits;                /* device, as all pointers here */
+  const float *bias;
+  const uint8_t *live, *eligible;
+  int32_t *sel;
+  float *weights;
+  int32_t *positions, *offsets, *slots;
+  void *workspace;
+  uint64_t workspace_bytes;
+  int64_t logits_stride;
+  int32_t n_tok, n_experts, top_k;
+  int32_t dtype, router, n_group, topk_group, raw_weights;
+} epoch_route_args;
+/* For the current device (0 on invalid sizes, which epoch_route refuses). */
+size_t epoch_route_workspace_bytes(int32_t n_tok, int32_t n_experts);
+epoch_status epoch_route(const epoch_route_args *args, epoch_stream stream);
+
+/* Weighted sum of each position's edges:
+ *   y[t] = sum_j weights[t][j] * edges[slots[t][j]] (+ shared[t]) (+ residual[t])
+ * in fp32, j ascending, rounded once.
+ *  edges [n_edges][hidden], shared (NULL: none) [n_tok][hidden] of dtype, residual (NULL:
+ *  none) of residual_dtype, out of out_dtype; slots, weights [n_tok][k] as epoch_route gives
+ *  them: a negative slot adds nothing, one not below n_edges makes the row NaN and is
+ *  not followed. out may be shared or residual of its dtype and stride.
+ * EPOCH_EINVAL: n_tok or n_edges < 0, hidden not in [1, 2^20], k not in [1, 64], unknown
+ * dtype, a NULL or misaligned pointer, a stride smaller than hidden, more than 2^38
+ * elements, an output that overlaps. */
+typedef struct {
+  const void *edges, *shared, *residual;
+  const int32_t *slots;
+  const float *weights;
+  void *out;
+  int64_t edges_stride, shared_stride, residual_stride, out_stride;
+  int32_t n_tok, n_edges, hidden, k;
+  int32_t dtype, residual_dtype, out_dtype;
+} epoch_combine_args;
+epoch_status epoch_combine(const epoch_combine_args *args, epoch_stream stream);
+
+/* 4-bit floating point (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two values a
+ * byte, the even column in the low half) with a scale for each block of columns:
+ *  EPOCH_FP4_NVFP4: blocks of 16, v' = v * (1 / tensor_scale) in fp32,
+ *    s = e4m3(min(max|v'| / 6, 448)), at least 2^-9;  q = e2m1(v' / s)
+ *  EPOCH_FP4_MXFP4: blocks of 32, s = 2^(floor(log2 max|v|) - 2), at least 2^-127, as e8m0
+ *    (the exponent plus 127); q = e2m1(v / s); tensor_scale must be 1
+ * Both roundings are to nearest even of the exact quotients; beyond 6, q is 6. The value
+ * that a code stands for is q * s (* tensor_scale). A block that holds a NaN or an
+ * infinity has a NaN scale (0x7F, 0xFF), and so does every block of a row whose index
+ * is not in [0, n_src), which is not read; products with them are NaN.
+ *  x_dev, rows_dev, n_src, swiglu as for epoch_fp8_quantize.
+ *  q_dev [n_rows][cols / 2] bytes; scales_dev [ceil(cols / 256)][n_rows][16 or 8] bytes: the
+ *  scales of 256 columns of a row together, zeros behind the last column. Both contiguous,
+ *  16-byte aligned.
+ * EPOCH_EINVAL as epoch_fp8_quantize, and for cols not a multiple of 32, an unknown format,
+ * a tensor_scale that is not positive and finite with a finite reciprocal, or not 1 with mxfp4. */
+enum { EPOCH_FP4_NVFP4 = 0, EPOCH_FP4_MXFP4 = 1 };
+epoch_status epoch_fp4_quantize(const void *x_dev, int64_t x_stride, int32_t dtype, const int32_t *rows_dev,
+                                int32_t n_rows, int32_t n_src, int32_t cols, int32_t swiglu, int32_t format,
+                                float tensor_scale, void *q_dev, void *scales_dev, epoch_stream stream);
+
+/* The same for weight matrices w_dev [n_mats][n][k] (contiguous): q_dev [n_mats][n][k / 2],
+ * scales_dev [n_mats][ceil(k / 256)][n][16 or 8], and tensor_scales_dev [n_mats] float: nvfp4:
+ * the least power of two t >= 2^-126 with max|w| <= 2688 t (1 for a matrix of zeros or with a NaN or
+ * infinity), mxfp4: 1. k a multiple of 32; n_mats in [0, 65535], n and k in [1, 2^22]. */
+epoch_status epoch_fp4_quantize_weight(const void *w_dev, int32_t dtype, int32_t n_mats, int32_t n, int32_t k,
+                                       int32_t format, void *q_dev, void *scales_dev, float *tensor_scales_dev,
+                                       epoch_stream stream);
+
+/* The values that codes stand for, times scale and, where it is given, group_scale_dev [n_mats]:
+ * out_dev [n_mats * n] rows of k values of out_dtype, out_stride apart, from q_dev [n_mats][n][k / 2]
+ * and scales_dev [n_mats][ceil(k / 256)][n][16 or 8] (rows as epoch_fp4_quantize gives them: n_mats 1).
+ * Rounded once. EPOCH_EINVAL as above. */
+epoch_status epoch_fp4_dequantize(const void *q_dev, const void *scales_dev, int32_t format, int32_t n_mats, int32_t n,
+                                  int32_t k, float scale, const float *group_scale_dev, void *out_dev,
+                                  int64_t out_stride, int32_t out_dtype, epoch_stream stream);
+
+/* Products of experts, dense or grouped by expert, accumulated in fp32 and rounded once:
+ *   y[i][j] = f * sum_c a[r_i][c] * b[e][j][c],   f = scale * group_scale[e] (NULL: scale)
+ *  and with swiglu, n being even, y [m][n / 2] = silu(y[i][j]) * y[i][n / 2 + j].
+ *  kind: EPOCH_EXPERT_F32, EPOCH_EXPERT_BF16: a [n_src][k], b [n_groups][n][k] of that type;
+ *  EPOCH_EXPERT_NVFP4, EPOCH_EXPERT_MXFP4: 4-bit operands with scales as the functions above
+ *  make them (their tensor scales are the caller's to put into the factors).
+ *  offsets as for epoch_fp8_matmul (NULL: dense, n_groups 1).
+ *  rows (NULL: r_i = i, n_src = m): r_i = rows[i], the positions of a worklist; a row whose
+ *  index is not in [0, n_src) is not read, and its result is NaN. F32 and BF16 only.
+ *  a_stride: elements between rows of a (F32, BF16; 4-bit rows are contiguous).
+ * EPOCH_EINVAL: m < 0, n < 1, k < 1 or above 2^30, k not a multiple of 4 (F32), 8 (BF16) or 32
+ * (4-bit), n_groups not in [1, 1024], m, n_src or n_groups * n above 2^31 - 257, an unknown kind or
+ * out_dtype, swiglu with an odd n, rows with 4-bit operands, a, b or scales not 16-byte aligned, an
+ * a_stride that is smaller than k or no multiple of 16 bytes, another pointer NULL or misaligned,
+ * y_stride smaller than a row, y overlapping an input, scale not finite.
+ * A device wait that makes no progress for 2 s gives up, sets the operators' error word
+ * and lets the kernel return. */
+enum { EPOCH_EXPERT_F32 = 0, EPOCH_EXPERT_BF16 = 1, EPOCH_EXPERT_NVFP4 = 2, EPOCH_EXPERT_MXFP4 = 3 };
+typedef struct {
+  const void *a, *b, *a_scales, *b_scales;
+  const int32_t *offsets, *rows;
+  const float *group_scale;
+  void *y;
+  int64_t a_stride, y_stride;
+  float scale;
+  int32_t n_groups, m, n_src, n, k;
+  int32_t kind, swiglu, out_dtype;
+} epoch_expert_args;
+epoch_status epoch_expert_matmul(const epoch_expert_args *args, epoch_stream stream);
+
+/* Which kernel epoch_expert_matmul takes for these sizes, as epoch_fp8_matmul_kernel says it:
+ * tiles of 32, 64, 128 or 256 columns, or EPOCH_FP8_PAIRS (the fp32 kernel: 0); -1 for sizes out of
+ * range. Host only. */
+int32_t epoch_expert_matmul_kernel(int32_t kind, int32_t n_groups, int32_t m, int32_t n, int32_t k, int32_t n_sms);
+
+/* Test hook: epoch_expert_matmul whose operand copies count 16 bytes that never come, as
+ * epoch_test_fp8_timeout. EPOCH_EINVAL also for EPOCH_EXPERT_F32, whose kernel has no waits. */
+epoch_status epoch_test_expert_timeout(const epoch_expert_args *args, int64_t timeout_ns, epoch_stream stream);
 
 /* Sticky error word of the operators beside the layer, one per device, for all
  * streams: read (synchronises the stream) with the status that epoch_get_status

@@ -21,6 +21,9 @@ EPOCH_DEVERR_FLAGS, EPOCH_DEVERR_TIMEOUT, EPOCH_DEVERR_BOUNDS = 1, 2, 4
 EPOCH_PROF_KINDS = 12
 EPOCH_FEW_MAX = 64
 EPOCH_FP8_PAIRS = 512
+EPOCH_ROUTER_SOFTMAX, EPOCH_ROUTER_SIGMOID_GROUP = 0, 1
+EPOCH_FP4_NVFP4, EPOCH_FP4_MXFP4 = 0, 1
+EPOCH_EXPERT_F32, EPOCH_EXPERT_BF16, EPOCH_EXPERT_NVFP4, EPOCH_EXPERT_MXFP4 = range(4)
 EPOCH_GATE_NONE, EPOCH_GATE_CHANNEL, EPOCH_GATE_FULL = range(3)
 
 
@@ -44,6 +47,10 @@ class epoch_layer_weights(C.Structure):
 
 # epoch_norm_after_args, in the C compiler's layout
 NORM_AFTER_ARGS = struct.Struct("@PPPPPPPPqqqqqiiiiiiiff")
+# epoch_route_args, epoch_combine_args and epoch_expert_args, likewise
+ROUTE_ARGS = struct.Struct("@PPPPPPPPPPQqiiiiiiii")
+COMBINE_ARGS = struct.Struct("@PPPPPPqqqqiiiiiii")
+EXPERT_ARGS = struct.Struct("@PPPPPPPPqqfiiiiiiii")
 
 STATS_FIELDS = ("iteration", "n_pos", "n_live", "n_new", "n_miss", "n_stale", "n_forced", "n_reuse",
                 "n_fresh", "n_edges", "n_hit_experts", "support_len", "fallback", "bad_flags",
@@ -117,6 +124,18 @@ _SIGS = {
                                          C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_int64,
                                          C.c_void_p]),
     "epoch_fp8_matmul_kernel": (C.c_int32, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
+    "epoch_route_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32]),
+    "epoch_route": (C.c_int, [C.c_char_p, C.c_void_p]),  # a packed ROUTE_ARGS
+    "epoch_combine": (C.c_int, [C.c_char_p, C.c_void_p]),  # a packed COMBINE_ARGS
+    "epoch_fp4_quantize": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
+                                     C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "epoch_fp4_quantize_weight": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                                            C.c_void_p, C.c_void_p, C.c_void_p]),
+    "epoch_fp4_dequantize": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_float,
+                                       C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
+    "epoch_expert_matmul": (C.c_int, [C.c_char_p, C.c_void_p]),  # a packed EXPERT_ARGS
+    "epoch_expert_matmul_kernel": (C.c_int32, [C.c_int32] * 6),
+    "epoch_test_expert_timeout": (C.c_int, [C.c_char_p, C.c_int64, C.c_void_p]),
     "epoch_ops_status": (C.c_int, [C.c_int32, C.c_void_p, C.POINTER(C.c_uint32)]),
     "epoch_test_few_timeout": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p]),
     "epoch_layer_destroy": (None, [C.c_void_p]),

@@ -1,0 +1,613 @@
+// Matrix products of the routed experts, dense or grouped by expert, on bf16 rows or on
+// 4-bit (e2m1) operands with a scale for each 16 or 32 columns:
+//
+//   y[i, n] = s_e * sum_k a[i, k] * w[e, n, k],   offsets[e] <= i < offsets[e + 1]
+//
+// and, with swiglu, z[i, n] = silu(y[i, n]) * y[i, N / 2 + n]. Row i of a bf16 product may be row
+// rows[i] of x (a worklist's positions). Sums are the tensor cores' fp32 accumulators; the factors
+// s_e and the SwiGLU are applied to them in fp32 and the result is rounded once.
+//
+// Tiles of 128 rows x 256, 128, 64 or 32 columns, or of 256 x 256 by two CTAs whose tensor cores
+// read both halves of the weights. A producer warp streams 128-byte-wide operand tiles (64 bf16 or
+// 256 e2m1 columns) by TMA through a ring in shared memory, gathered rows four at a time; an MMA
+// warp issues the tcgen05 products into TMEM; eight epilogue warps take a finished accumulator into
+// registers, free it, and store under the next tile's products. With swiglu a tile's columns are
+// half gate and half up rows of the weights, so that both halves of an output meet in one thread.
+//
+// 4-bit operands: the tensor core multiplies by both scales itself and reads them from TMEM, where
+// 32 rows x 4 scales take a column of 32 lanes. Scales lie in memory by blocks of 256 columns,
+// [K / 256][rows][16 or 8], so that the rows of a tile are one run wherever it starts. Three warps
+// bring them into shared memory in the order of TMEM (lane l of row group c), from which the MMA
+// thread copies them ahead of the products that use them.
+#include <cstring>
+#include <mutex>
+
+#include "common.cuh"
+#include "layer.h"
+#include "tiles.cuh"
+
+namespace epoch {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kRow = 128;  // bytes of an operand row of a stage: one swizzle row
+
+struct ExpertParams {
+  CUtensorMap a[3];  // boxes of 32, 64, 128 rows; gathered: a[0] with boxes of one row
+  CUtensorMap b;     // boxes of half a tile's columns (pairs: 128)
+  ExpertGemmArgs g;
+  int kb_n, nt_n;    // K blocks, tiles along N
+  int out_n;         // columns of the output
+  int wide;          // output rows start on 32-byte boundaries
+  int reuse;         // weights are read by several row tiles
+  uint32_t *err;
+  int64_t timeout_ns;
+  uint32_t hold;  // bytes that a stage waits for beyond its copies': 0, but for the test of waits that run out
+};
+
+// Tiles are BN columns wide. FP4 0: bf16; 4 or 2: e2m1 with 16 or 8 scales a row in 256 columns, in so many chunks
+// of 4 scales.
+template <int FP4, int BN, bool PAIR> struct Tile {
+  static_assert(!PAIR || BN == 256, "pairs work on 256 columns");
+  static constexpr int bm = PAIR ? 2 * kBm : kBm;
+  static constexpr int b_rows = PAIR ? BN / 2 : BN;
+  static constexpr int box_b = BN == 256 ? 128 : BN / 2;  // rows of a copy of weights
+  static constexpr int operands = (kBm + b_rows) * kRow;
+  static constexpr int groups_b = BN == 256 ? 2 : 1;      // 128-row groups of the weights' scales
+  static constexpr int scale_bytes = (1 + groups_b) * FP4 * 512;
+  static constexpr int stage = operands + scale_bytes;
+  static constexpr int fit = 220 * 1024 / stage;
+  static constexpr int stages = fit < 8 ? fit : 8;
+  // TMEM: accumulators, then four places for the scales of a stage (the copies and the products of one thread
+  // complete in order; four let a copy be well ahead of them)
+  static constexpr int bufs = FP4 && BN == 256 ? 1 : 2;
+  static constexpr int cols_b = BN == 256 ? 8 : 4;        // TMEM columns of a chunk of the weights' scales
+  static constexpr int place = FP4 * (4 + cols_b);
+  static constexpr int need = bufs * BN + 4 * place;
+  static constexpr int tmem = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+  static constexpr int smem = 1024 + stages * stage;
+  // warpgroups: the epilogue's two, producer and MMA, and one for the scales
+  static constexpr int threads = 32 * (kEpiWarps + (FP4 ? 8 : 4));
+  static constexpr int regs_launch = FP4 ? 128 : 168, regs_few = FP4 ? 88 : 72, regs_many = FP4 ? 168 : 216;
+};
+
+// Shape M x N, fp32 accumulator, both operands K-major.
+template <int FP4> __host__ __device__ constexpr uint32_t idesc_of(int M, int N) {
+  if (FP4 == 0) return idesc_bf16_f32(M, N);
+  return (1u << 7) | (1u << 10)                       // A and B: e2m1
+         | (static_cast<uint32_t>(N >> 3) << 17) | (FP4 == 2 ? 1u << 23 : 0u)  // scales: e8m0, else e4m3
+         | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int FP4, bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                    uint32_t accumulate) {
+#define EPOCH_MMA_SCALED(GROUP, VEC)                                                             \
+  asm volatile(                                                                                  \
+      "{\n\t.reg .pred p;\n\t"                                                                   \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                \
+      "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), \
+      "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                            \
+      : "memory")
+  if constexpr (FP4 == 0) {
+    if constexpr (PAIR)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "setp.ne.b32 p, %4, 0;\n\t"
+          "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+          "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+          : "memory");
+    else
+      tc_mma_bf16(d, ad, bd, idesc, accumulate);
+  } else if constexpr (FP4 == 4) {
+    if constexpr (PAIR) EPOCH_MMA_SCALED("2", "4X");
+    else EPOCH_MMA_SCALED("1", "4X");
+  } else {
+    if constexpr (PAIR) EPOCH_MMA_SCALED("2", "2X");
+    else EPOCH_MMA_SCALED("1", "2X");
+  }
+#undef EPOCH_MMA_SCALED
+}
+
+// 32 rows of 16 bytes from shared memory to a run of four TMEM columns, in all four quarters of the lanes (of both
+// CTAs' TMEM, each from its own shared memory).
+template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+                        (static_cast<uint64_t>(1) << 46);  // no swizzle, groups of eight rows 128 bytes apart
+  if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Four rows of a matrix, one operand row each.
+template <bool PAIR>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int32_t c0, const int (&r)[4],
+                                          uint32_t bar, uint64_t policy) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// An arrival that releases this thread's writes to the cluster, and a wait that acquires them.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+template <int Q> __device__ __forceinline__ void load_cols(uint32_t at, float (&v)[Q]) {
+  if constexpr (Q == 8) tmem_ld8(at, v);
+  else if constexpr (Q == 16) tmem_ld16(at, v);
+  else if constexpr (Q == 32) tmem_ld32(at, v);
+  else {
+    tmem_ld32(at, reinterpret_cast<float (&)[32]>(v[0]));
+    tmem_ld32(at + 32, reinterpret_cast<float (&)[32]>(v[32]));
+  }
+}
+
+// Q consecutive values of an output row from column n0 on, `n` of which exist.
+template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, int n, const float (&v)[Q], bool bf16, bool wide) {
+  if (bf16) {
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(row) + n0;
+    if (wide && n >= Q) {
+      uint32_t w[Q / 2];
+#pragma unroll
+      for (int j = 0; j < Q / 2; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+      if constexpr (Q >= 16) {
+#pragma unroll
+        for (int j = 0; j < Q / 2; j += 8) store32(dst + 2 * j, reinterpret_cast<const uint32_t (&)[8]>(w[j]));
+      } else {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < Q; ++j)
+        if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
+    }
+  } else {
+    float *dst = static_cast<float *>(row) + n0;
+    if (wide && n >= Q) {
+#pragma unroll
+      for (int j = 0; j < Q; j += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[j + i]);
+        store32(dst + j, w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < Q; ++j)
+        if (j < n) dst[j] = v[j];
+    }
+  }
+}
+
+template <int FP4, int BN, bool PAIR>
+__global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm(const __grid_constant__ ExpertParams p) {
+  using G = Tile<FP4, BN, PAIR>;
+  constexpr int Q = BN / 4;                                        // columns of one of a thread's two runs
+  constexpr int kFull = 1 + (FP4 ? (1 + G::groups_b) * (PAIR ? 2 : 1) : 0);  // arrivals that fill a stage
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * G::stages + 2 * G::bufs];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
+  const int warp = warp_id(), lane = lane_id();
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cta = PAIR ? blockIdx.x >> 1 : blockIdx.x, ctas = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *const ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+  const uint32_t full = smem_u32(bars), empty = full + 8 * G::stages, tfull = empty + 8 * G::stages,
+                 tempty = tfull + 8 * G::bufs;
+  if (warp == 0) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(&s_tmem), G::tmem);
+    } else {
+      tmem_alloc(smem_u32(&s_tmem), G::tmem);
+      tmem_relinquish();
+    }
+  } else if (warp == 1) {
+    if (p.g.offsets != nullptr) {
+      group_tiles(p.g.offsets, p.g.n_groups, p.g.m, G::bm, s_start, s_cum);
+    } else if (lane == 0) {
+      s_start[0] = 0;
+      s_start[1] = p.g.m;
+      s_cum[0] = 0;
+      s_cum[1] = (p.g.m + G::bm - 1) / G::bm;
+    }
+  } else if (warp == 2 && lane == 0) {
+    s_abort = 0;
+    for (int i = 0; i < G::stages; ++i) {
+      mbar_init(full + 8 * i, kFull);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < G::bufs; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, PAIR ? 2 * kEpiWarps : kEpiWarps);  // accumulators read (both CTAs')
+    }
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int *abort = &s_abort;
+  TileWalk walk(s_start, s_cum, p.g.offsets ? p.g.n_groups : 1, p.nt_n, G::bm, rank);
+  const int half_n = p.g.N / 2;
+
+  // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 12 .. 15: scales
+  if (warp >= kEpiWarps) {
+    give_registers<G::regs_few>();
+    if (warp == kEpiWarps) {  // ------------------------------------------------ producer
+      const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
+      const uint64_t wpol = p.reuse ? keep : pass;
+      const uint32_t counts = PAIR ? mapa_shared(full, 0) : full;  // the barriers that the copies count on
+      constexpr int kCols = FP4 ? kRow : kRow / 2;                 // tensor map elements of an operand row
+      uint32_t it = 0, st = 0, phase = 1;
+      bool ok = true;
+      for (int t = cta; ok && t < walk.total; t += ctas) {
+        int e, row0, rows, nt;
+        walk.at(t, &e, &row0, &rows, &nt);
+        int idx[4] = {-1, -1, -1, -1};  // out of range: read as zeros (and the result is NaN)
+        int quads = 32;
+        if (p.g.rows != nullptr) {
+          if (!PAIR) quads = (rows + 3) / 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (4 * lane + j < rows) {
+              const int r = __ldg(p.g.rows + row0 + 4 * lane + j);
+              if (r >= 0 && r < p.g.n_src) idx[j] = r;
+            }
+        }
+        // single CTAs load the smallest box that holds their rows
+        const int box = PAIR || rows > 64 ? 2 : rows > 32 ? 1 : 0;
+        const uint32_t a_bytes = p.g.rows != nullptr ? quads * 4 * kRow : PAIR ? kBm * kRow : (32u << box) * kRow;
+        const uint32_t bytes = (PAIR ? 2 : 1) * (a_bytes + G::b_rows * kRow) + p.hold;
+        int b0, b1;  // first rows of the two copies of weights
+        if (p.g.swiglu) {
+          b0 = e * p.g.N + nt * (BN / 2);
+          b1 = b0 + half_n;
+          if (PAIR && rank) b0 = b1;
+        } else {
+          b0 = e * p.g.N + nt * BN + rank * G::b_rows;
+          b1 = b0 + G::box_b;
+        }
+        for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
+          ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
+          if (!ok) break;
+          const uint32_t dst = ring + st * G::stage, bar = counts + 8 * st;
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
+            if (p.g.rows == nullptr) load_box<PAIR>(dst, &p.a[box], kb * kCols, row0, bar, keep);
+            load_box<PAIR>(dst + kBm * kRow, &p.b, kb * kCols, b0, bar, wpol);
+            if constexpr (!PAIR) load_box<PAIR>(dst + kBm * kRow + G::box_b * kRow, &p.b, kb * kCols, b1, bar, wpol);
+          }
+          __syncwarp();
+          if (p.g.rows != nullptr && lane < quads) load_rows<PAIR>(dst + lane * 4 * kRow, &p.a[0], kb * kCols, idx, bar, keep);
+          __syncwarp();
+          if (++st == G::stages) {
+            st = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // no exit with copies in flight: the last stages' copies (both CTAs' count here) have landed before the end
+      if (rank == 0)
+        for (uint32_t i = it > G::stages ? it - G::stages : 0; i < it; ++i) {
+          int done = 0;
+          wait_for(full + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
+        }
+    } else if (FP4 && warp >= kEpiWarps + 4 && warp <= kEpiWarps + 4 + G::groups_b) {  // scales, a group of 128 rows a warp
+      constexpr int kPer = FP4 * 4;  // scales of a row in a stage
+      const int group = warp - kEpiWarps - 4;  // 0: a's rows; 1, 2: the weights'
+      const uint32_t filled = PAIR ? mapa_shared(full, 0) : full;
+      uint32_t st = 0, phase = 1;
+      bool ok = true;
+      for (int t = cta; ok && t < walk.total; t += ctas) {
+        int e, row0, rows, nt;
+        walk.at(t, &e, &row0, &rows, &nt);
+        const uint8_t *src[4];
+        int64_t step;  // bytes between K blocks
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // rows that do not exist read one that does
+          const int r = 32 * c + lane;
+          if (group == 0) {
+            src[c] = p.g.sa + static_cast<int64_t>(min(row0 + r, p.g.m - 1)) * kPer;
+          } else {
+            const int j = min((group - 1) * 128 + r, BN - 1);
+            const int n = !p.g.swiglu ? nt * BN + j : j < BN / 2 ? nt * (BN / 2) + j : half_n + nt * (BN / 2) + j - BN / 2;
+            src[c] = p.g.sb + (static_cast<int64_t>(e) * p.kb_n * p.g.N + min(n, p.g.N - 1)) * kPer;
+          }
+        }
+        step = static_cast<int64_t>(group == 0 ? p.g.m : p.g.N) * kPer;
+        uint32_t v[4][FP4 ? FP4 : 1];
+        auto load = [&](int kb) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint8_t *at = src[c] + min(kb, p.kb_n - 1) * step;
+            if constexpr (FP4 == 4) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4 *>(at));
+              v[c][0] = u.x, v[c][1] = u.y, v[c][2] = u.z, v[c][3] = u.w;
+            } else if constexpr (FP4 == 2) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2 *>(at));
+              v[c][0] = u.x, v[c][1] = u.y;
+            }
+          }
+        };
+        load(0);
+        for (int kb = 0; kb < p.kb_n; ++kb) {
+          ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
+          if (!ok) break;
+          uint8_t *dst = ring_ptr + st * G::stage + G::operands + group * FP4 * 512 + lane * 16;
+#pragma unroll
+          for (int k = 0; k < FP4; ++k)
+            *reinterpret_cast<uint4 *>(dst + k * 512) = make_uint4(v[0][k], v[1][k], v[2][k], v[3][k]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR) arrive_release_cluster(filled + 8 * st);
+            else mbar_arrive(filled + 8 * st);
+          }
+          load(kb + 1);
+          if (++st == G::stages) {
+            st = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    } else if (warp == kEpiWarps + 1 && rank == 0) {  // ------------------------ MMA
+      // The warp stays together and one elected lane issues, so that descriptors and barriers are uniform values.
+      constexpr uint32_t idesc = idesc_of<FP4>(G::bm, BN);
+      uint32_t it = 0, st = 0, phase = 0, tile = 0;
+      bool ok = true;
+      for (int t = cta; ok && t < walk.total; t += ctas, ++tile) {
+        const uint32_t buf = tile % G::bufs;
+        ok = warp_wait(tempty + 8 * buf, ((tile / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
+        if (!ok) break;
+        for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
+          ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
+          if (!ok) break;
+          if constexpr (PAIR && FP4 != 0) acquire_cluster();
+          tc_fence_after();
+          const uint32_t src = ring + st * G::stage;
+          const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kRow);
+          const uint32_t sa = tmem + G::bufs * BN + (it & 3u) * G::place, sb = sa + 4 * FP4;
+          if (elect_one()) {
+            if constexpr (FP4 != 0) {
+#pragma unroll
+              for (int k = 0; k < FP4; ++k) {
+                copy_scales<PAIR>(sa + 4 * k, src + G::operands + k * 512);
+#pragma unroll
+                for (int g = 0; g < G::groups_b; ++g)
+                  copy_scales<PAIR>(sb + G::cols_b * k + 4 * g, src + G::operands + ((1 + g) * FP4 + k) * 512);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 32 bytes of columns an instruction
+              // two products share a chunk of e8m0 scales: the second takes its upper half
+              const int chunk = FP4 == 2 ? k / 2 : k;
+              const uint32_t id = FP4 == 2 && (k & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
+              mma<FP4, PAIR>(tmem + buf * BN, ad + 2 * k, bd + 2 * k, id, sa + 4 * chunk, sb + G::cols_b * chunk,
+                             kb > 0 || k > 0);
+            }
+            commit<PAIR>(empty + 8 * st);
+            if (kb == p.kb_n - 1) commit<PAIR>(tfull + 8 * buf);
+          }
+          __syncwarp();
+          if (++st == G::stages) {
+            st = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // no exit with products in flight: the last stages have been read
+      for (uint32_t i = it > G::stages ? it - G::stages : 0; i < it; ++i) {
+        int done = 0;
+        wait_for(empty + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
+      }
+    }
+  } else {  // ------------------------------------------------------------------ epilogue
+    take_registers<G::regs_many>();
+    const uint32_t read = PAIR ? mapa_shared(tempty, 0) : tempty;  // the barriers that the MMA thread waits on
+    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 32, half of the columns
+    const bool swiglu = p.g.swiglu != 0, bf16 = p.g.out_bf16 != 0, wide = p.wide != 0;
+    const int c0 = swiglu ? half * Q : half * 2 * Q, c1 = swiglu ? BN / 2 + half * Q : c0 + Q;
+    const size_t size = bf16 ? 2 : 4;
+    uint32_t tile = 0;
+    for (int t = cta; t < walk.total; t += ctas, ++tile) {
+      int e, row0, rows, nt;
+      walk.at(t, &e, &row0, &rows, &nt);
+      const uint32_t buf = tile % G::bufs;
+      const int row = row0 + quarter * 32 + lane;
+      const bool on = quarter * 32 + lane < rows;
+      const int n0 = (swiglu ? nt * (BN / 2) : nt * BN) + c0;  // output column of the first run
+      float s = p.g.scale;
+      if (p.g.group_scale != nullptr) s *= __ldg(p.g.group_scale + e);
+      if (on && p.g.rows != nullptr) {
+        const int r = __ldg(p.g.rows + row);
+        if (r < 0 || r >= p.g.n_src) s = __uint_as_float(0x7FC00000u);
+      }
+      const bool ok = __all_sync(0xffffffffu, wait_for(tfull + 8 * buf, (tile / G::bufs) & 1u, abort, p.err, p.timeout_ns));
+      if (!ok) break;
+      tc_fence_after();
+      float v0[Q], v1[Q];
+      const bool any = quarter * 32 < rows && n0 < p.out_n;  // this warp holds an element of the tile
+      if (any) {
+        const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+        load_cols<Q>(src + c0, v0);
+        load_cols<Q>(src + c1, v1);
+        tmem_ld_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) arrive_cluster(read + 8 * buf);
+        else mbar_arrive(read + 8 * buf);
+      }
+      if (!any || !on) continue;
+      void *dst = static_cast<uint8_t *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride * size;
+      if (swiglu) {
+        if (bf16) {
+#pragma unroll
+          for (int j = 0; j < Q; ++j) v0[j] = silu_fast(v0[j] * s) * (v1[j] * s);
+        } else {
+#pragma unroll
+          for (int j = 0; j < Q; ++j) v0[j] = silu(v0[j] * s) * (v1[j] * s);
+        }
+        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, wide);
+      } else {
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          v0[j] *= s;
+          v1[j] *= s;
+        }
+        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, wide);
+        if (n0 + Q < p.out_n) store_cols<Q>(dst, n0 + Q, p.out_n - n0 - Q, v1, bf16, wide);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {  // the other CTA may still reach this one's barriers
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp == 0) {
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, G::tmem);
+    else tmem_dealloc(tmem, G::tmem);
+  }
+}
+
+template <int FP4, int BN, bool PAIR> cudaError_t launch_tile(ExpertParams &p, cudaStream_t s) {
+  using G = Tile<FP4, BN, PAIR>;
+  auto *fn = &k_expert_gemm<FP4, BN, PAIR>;
+  static std::mutex mu;
+  static int resident[64] = {};  // CTAs that a device holds at once; -1: the kernel cannot run there
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(G::threads);
+  cfg.dynamicSmemBytes = G::smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (resident[dev] == 0) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, fn);
+      if (e != cudaSuccess) return e;
+      // the warpgroups hand registers over within what the launch holds
+      if (fa.numRegs < G::regs_launch) return cudaErrorInvalidConfiguration;
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
+      if (e != cudaSuccess) return e;
+      int n = num_sms();
+      if (PAIR) {
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / 2 * 2));
+        e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+        if (e != cudaSuccess) return e;
+        n *= 2;
+      }
+      resident[dev] = n;
+    }
+    most = resident[dev];
+  }
+  if (most < (PAIR ? 2 : 1)) return cudaErrorNotSupported;
+  p.nt_n = (p.g.N + BN - 1) / BN;
+  // row tiles: at most one partial tile a group beyond the full ones
+  const int64_t mt = p.g.offsets ? p.g.m / G::bm + (p.g.n_groups < p.g.m ? p.g.n_groups : p.g.m) : (p.g.m + G::bm - 1) / G::bm;
+  const int64_t ctas = mt * p.nt_n * (PAIR ? 2 : 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <int FP4> cudaError_t launch_kind(ExpertParams &p, int kernel, cudaStream_t s) {
+  if (kernel == kExpertPairs) return launch_tile<FP4, 256, true>(p, s);
+  if (kernel == 256) return launch_tile<FP4, 256, false>(p, s);
+  if (kernel == 128) return launch_tile<FP4, 128, false>(p, s);
+  if (kernel == 64) return launch_tile<FP4, 64, false>(p, s);
+  return launch_tile<FP4, 32, false>(p, s);
+}
+
+}  // namespace
+
+// The tiles a product takes: the columns of a tile of single CTAs, kExpertPairs tiles of CTA pairs. n_groups 0: dense.
+int expert_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms) {
+  const int64_t E = n_groups ? n_groups : 1;
+  // The tile whose rounds of tiles take the least time. Pairs need groups that fill 256 rows.
+  const int64_t mt = m / kBm + (n_groups ? (E < m ? E : m) : (m % kBm != 0));
+  auto cost = [&](int64_t tiles, int64_t at_once, int64_t clocks) { return (tiles + at_once - 1) / at_once * clocks; };
+  int bn = 256;
+  int64_t best = cost(mt * ((N + 255) / 256), sms, 1000);
+  const int64_t narrow[3][2] = {{128, 720}, {64, 600}, {32, 560}};
+  for (const auto &c : narrow) {
+    const int64_t t = cost(mt * ((N + c[0] - 1) / c[0]), sms, c[1]);
+    if (t < best) {
+      best = t;
+      bn = static_cast<int>(c[0]);
+    }
+  }
+  if (m >= 256 * E && sms >= 2) {
+    const int64_t tiles = (m / 256 + (n_groups ? E : m % 256 != 0)) * ((N + 255) / 256);
+    if (cost(tiles, sms / 2, 1000) <= best) return kExpertPairs;
+  }
+  return bn;
+}
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t timeout_ns, uint32_t hold) {
+  const int kernel = expert_gemm_kernel(a.offsets ? a.n_groups : 0, a.m, a.N, num_sms());
+  ExpertParams p;
+  memset(&p, 0, sizeof(p));
+  p.g = a;
+  const bool fp4 = a.kind != EPOCH_EXPERT_BF16;
+  p.kb_n = (a.K + (fp4 ? 255 : 63)) / (fp4 ? 256 : 64);
+  p.out_n = a.swiglu ? a.N / 2 : a.N;
+  p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && a.out_stride % (a.out_bf16 ? 16 : 8) == 0;
+  const int64_t E = a.offsets ? a.n_groups : 1;
+  p.reuse = a.m > kBm * E;
+  p.err = ops_error_word();
+  p.timeout_ns = timeout_ns;
+  p.hold = hold;
+  if (p.err == nullptr || !tma_encode_init()) return cudaErrorInitializationError;
+  const uint64_t k_row = fp4 ? a.K / 2 : a.K, src_rows = a.rows ? a.n_src : a.m;
+  const uint32_t b_box = kernel == kExpertPairs || kernel == 256 ? 128 : kernel / 2;
+  bool ok = encode_operand(&p.b, a.b, !fp4, k_row, E * a.N, k_row, b_box);
+  if (a.rows) {
+    // nothing to gather from: every index is out of range, of any tensor
+    const bool none = a.n_src == 0;
+    ok = ok && encode_operand(&p.a[0], none ? a.b : a.a, !fp4, k_row, none ? 1 : src_rows, a.a_stride, 1);
+  } else {
+    ok = ok && encode_operand(&p.a[2], a.a, !fp4, k_row, src_rows, a.a_stride, 128);
+    if (kernel != kExpertPairs && (a.offsets || a.m % kBm != 0))
+      ok = ok && encode_operand(&p.a[0], a.a, !fp4, k_row, src_rows, a.a_stride, 32) &&
+           encode_operand(&p.a[1], a.a, !fp4, k_row, src_rows, a.a_stride, 64);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  if (a.kind == EPOCH_EXPERT_BF16) return launch_kind<0>(p, kernel, s);
+  return a.kind == EPOCH_EXPERT_NVFP4 ? launch_kind<4>(p, kernel, s) : launch_kind<2>(p, kernel, s);
+}
+
+}  // namespace epoch

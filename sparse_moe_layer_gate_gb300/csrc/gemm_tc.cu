@@ -1081,6 +1081,20 @@ bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, ui
   return r == CUDA_SUCCESS;
 }
 
+bool encode_operand(CUtensorMap *map, const void *base, bool bf16, uint64_t k_elems, uint64_t rows, uint64_t stride,
+                    uint32_t box_rows) {
+  if (!g_encode || base == nullptr || rows == 0) return false;
+  cuuint64_t dims[2] = {k_elems, rows};
+  cuuint64_t strides[1] = {stride * (bf16 ? 2 : 1)};
+  cuuint32_t box[2] = {bf16 ? 64u : 128u, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool encode_rows(CUtensorMap *map, void *base, bool bf16, uint64_t cols, uint64_t rows, uint64_t stride) {
   if (!g_encode || base == nullptr || rows == 0) return false;
   cuuint64_t dims[2] = {cols, rows};

@@ -262,6 +262,9 @@ bool gate_builds_worklist(const Dims &d);
 
 // Row-major [rows][k_elems] 8-bit matrix, boxes of 128 (K) x box_rows, 128-byte swizzle.
 bool encode_kmajor_8bit(CUtensorMap *map, const void *base, uint64_t k_elems, uint64_t rows, uint32_t box_rows);
+// Row-major bf16 or 8-bit matrix, rows `stride` elements apart: boxes of 128 bytes (K) x box_rows, 128-byte swizzle.
+bool encode_operand(CUtensorMap *map, const void *base, bool bf16, uint64_t k_elems, uint64_t rows, uint64_t stride,
+                    uint32_t box_rows);
 // bf16 or fp32 output of `rows` rows of `cols` columns, `stride` elements apart: boxes of 128 bytes x 32 rows, 128-byte
 // swizzle.
 bool encode_rows(CUtensorMap *map, void *base, bool bf16, uint64_t cols, uint64_t rows, uint64_t stride);
@@ -317,6 +320,95 @@ cudaError_t launch_fp8_gemm(const GemmArgs &a, cudaStream_t s, int64_t timeout_n
 // The kernel that launch_fp8_gemm takes on a device of `sms` SMs (host only; see epoch_fp8_matmul_kernel).
 constexpr int kFp8Pairs = EPOCH_FP8_PAIRS;
 int fp8_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms);
+// router.cu
+struct RouteArgs {
+  const void *logits;       // [n_tok][n_experts], rows logits_stride apart
+  const float *bias;        // nullable
+  const uint8_t *live;      // nullable: [n_tok]
+  const uint8_t *eligible;  // nullable: [n_experts]
+  int32_t *sel;             // [n_tok][top_k]
+  float *weights;
+  int32_t *positions;       // [n_tok * top_k]
+  int32_t *offsets;         // [n_experts + 1]
+  int32_t *slots;           // [n_tok][top_k]
+  int32_t *counts;          // workspace: edges of each CTA's positions and expert
+  int64_t logits_stride;
+  int32_t n_tok, n_experts, top_k;
+  int32_t bf16, sigmoid, n_group, topk_group, raw_weights;
+  int32_t vec;  // rows of logits start on 16-byte boundaries
+};
+size_t router_workspace(int64_t n_tok, int n_experts);
+cudaError_t launch_router(RouteArgs a, cudaStream_t s);
+
+// combine.cu
+struct CombineArgs {
+  const void *edges, *shared, *residual;  // shared, residual nullable
+  const int32_t *slots;
+  const float *weights;
+  void *out;
+  int64_t edges_stride, shared_stride, residual_stride, out_stride;
+  int64_t n_tok, n_edges;
+  int32_t hidden, k;
+  int32_t residual_bf16, out_bf16;
+};
+cudaError_t launch_combine_edges(const CombineArgs &a, bool bf16, cudaStream_t s);
+
+// fp4_quant.cu
+struct Fp4QuantArgs {
+  const void *x;
+  const int32_t *rows;   // nullable: row i of the output is row rows[i] of x
+  const uint32_t *amax;  // weights: largest |x| of each matrix (bit patterns), from which its tensor scale follows
+  uint8_t *q, *scales;
+  int64_t x_stride;
+  int64_t n_rows, n_src;
+  int64_t mat_rows;      // weights: rows of a matrix
+  int32_t cols;
+  int32_t swiglu;
+  float inv_scale;       // 1 / tensor scale
+};
+struct Fp4DequantArgs {
+  const uint8_t *q, *scales;
+  const float *group_scale;  // nullable: a factor for each matrix
+  void *out;
+  int64_t n_rows, mat_rows, out_stride;
+  int32_t cols;
+  int32_t wide;  // output rows start on 16-byte boundaries
+  float scale;
+};
+cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, bool bf16, bool nv, cudaStream_t s);
+cudaError_t launch_fp4_quant_weight(Fp4QuantArgs a, int n_mats, bool bf16, bool nv, float *tensor_scales, cudaStream_t s);
+cudaError_t launch_fp4_dequant(Fp4DequantArgs a, bool bf16, bool nv, cudaStream_t s);
+#ifdef __CUDACC__
+// The least power of two t >= 2^-126 with |x| / t <= 6 * 448 for every |x| up to the one with bit pattern `amax`
+// (2688 = 1.3125 * 2^11); 1 for a matrix of zeros or one that holds a NaN or an infinity.
+__device__ __forceinline__ float fp4_tensor_scale(uint32_t amax) {
+  if (amax == 0u || amax >= 0x7F800000u) return 1.0f;
+  const int e = static_cast<int>(amax >> 23) - 11 + ((amax & 0x7FFFFFu) > 0x280000u);  // biased by 127
+  return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
+}
+#endif
+
+// expert_gemm.cu
+struct ExpertGemmArgs {
+  const void *a, *b;       // rows (bf16, or packed e2m1), weights [n_groups][N][K]
+  const uint8_t *sa, *sb;  // scales of 4-bit operands
+  const int32_t *offsets;  // nullable (dense)
+  const int32_t *rows;     // nullable: row i of the product is row rows[i] of a (bf16)
+  const float *group_scale;  // nullable: a factor for each group
+  void *out;
+  int64_t a_stride, out_stride;  // elements (packed e2m1: bytes)
+  float scale;
+  int32_t m, n_src, N, K, n_groups;
+  int32_t kind;  // EPOCH_EXPERT_*
+  int32_t swiglu, out_bf16;
+};
+constexpr int kExpertPairs = EPOCH_FP8_PAIRS;
+cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t timeout_ns = kFp8TimeoutNs,
+                               uint32_t hold = 0);
+// expert_simt.cu (fp32 rows)
+cudaError_t launch_expert_simt(const ExpertGemmArgs &a, cudaStream_t s);
+int expert_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms);
+
 // Device error word of the operators without a layer, on the current device (nullptr: none).
 uint32_t *ops_error_word();
 

@@ -87,6 +87,84 @@ epoch_status product(const void *a, const float *a_scales, const void *b, const 
   return EPOCH_OK;
 }
 
+// Bytes that no output may share: whether any two of them do, or one shares some with an input.
+template <int N, int M> bool clash(const Rows (&outs)[N], const Rows (&ins)[M]) {
+  for (int i = 0; i < N; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+    for (const Rows &in : ins)
+      if (overlap(outs[i], in)) return true;
+  }
+  return false;
+}
+
+bool fp4_format(int32_t f) { return f == EPOCH_FP4_NVFP4 || f == EPOCH_FP4_MXFP4; }
+int64_t fp4_scale_bytes(int32_t format, int64_t rows, int64_t cols) {
+  return (cols + 255) / 256 * rows * (format == EPOCH_FP4_NVFP4 ? 16 : 8);
+}
+
+// Checks the arguments of a product of experts and puts them together (m > 0).
+epoch_status expert_product(const epoch_expert_args *p, ExpertGemmArgs *g) {
+  if (p == nullptr || p->kind < EPOCH_EXPERT_F32 || p->kind > EPOCH_EXPERT_MXFP4 || !dtype_ok(p->out_dtype))
+    return EPOCH_EINVAL;
+  const bool fp4 = p->kind >= EPOCH_EXPERT_NVFP4;
+  const int32_t unit = fp4 ? 32 : p->kind == EPOCH_EXPERT_BF16 ? 8 : 4;
+  if (p->m < 0 || p->n < 1 || p->k < unit || p->k % unit || p->k > (1 << 30) || p->n_groups < 1 || p->n_groups > 1024 ||
+      p->n_src < 0 || !std::isfinite(p->scale))
+    return EPOCH_EINVAL;
+  if ((p->swiglu && p->n % 2) || (fp4 && p->rows != nullptr) || (p->rows == nullptr && p->n_src != p->m))
+    return EPOCH_EINVAL;
+  if (p->offsets == nullptr ? p->n_groups != 1 : !on(p->offsets, 4)) return EPOCH_EINVAL;
+  const int64_t weights = static_cast<int64_t>(p->n_groups) * p->n;
+  if (weights > INT32_MAX - 256 || p->m > INT32_MAX - 256 || p->n_src > INT32_MAX - 256) return EPOCH_EINVAL;
+  if (p->m == 0) return EPOCH_OK;
+  const size_t in_size = p->kind == EPOCH_EXPERT_F32 ? 4 : 2;
+  const int64_t out_n = p->swiglu ? p->n / 2 : p->n, k_row = fp4 ? p->k / 2 : p->k;
+  if ((p->n_src > 0 && !on(p->a, 16)) || !on(p->b, 16) || !of_type(p->y, p->out_dtype) || !stride_ok(p->y_stride, p->m, out_n) ||
+      (p->rows != nullptr && !on(p->rows, 4)) || (p->group_scale != nullptr && !on(p->group_scale, 4)))
+    return EPOCH_EINVAL;
+  if (fp4 && (!on(p->a_scales, 16) || !on(p->b_scales, 16))) return EPOCH_EINVAL;
+  int64_t a_stride = k_row;
+  if (!fp4 && p->n_src > 1) {
+    a_stride = p->a_stride;
+    if (!stride_ok(a_stride, p->n_src, p->k) || a_stride * static_cast<int64_t>(in_size) % 16 ||
+        a_stride >= (1ll << 40) / static_cast<int64_t>(in_size))
+      return EPOCH_EINVAL;
+  }
+  const int32_t format = p->kind == EPOCH_EXPERT_NVFP4 ? EPOCH_FP4_NVFP4 : EPOCH_FP4_MXFP4;
+  const size_t size = fp4 ? 1 : in_size;
+  const Rows outs[1] = {Rows(p->y, p->m, out_n, p->y_stride, size_of(p->out_dtype))};
+  const Rows ins[7] = {Rows(p->n_src ? p->a : nullptr, p->n_src, k_row, a_stride, size),
+                       Rows(p->b, weights * k_row, size),
+                       Rows(p->offsets, p->n_groups + 1, 4),
+                       Rows(p->rows, p->m, 4),
+                       Rows(p->group_scale, p->n_groups, 4),
+                       Rows(fp4 ? p->a_scales : nullptr, fp4_scale_bytes(format, p->m, p->k), 1),
+                       Rows(fp4 ? p->b_scales : nullptr, fp4_scale_bytes(format, weights, p->k), 1)};
+  if (clash(outs, ins)) return EPOCH_EINVAL;
+  *g = ExpertGemmArgs{};
+  g->a = p->a;
+  g->b = p->b;
+  g->sa = static_cast<const uint8_t *>(p->a_scales);
+  g->sb = static_cast<const uint8_t *>(p->b_scales);
+  g->offsets = p->offsets;
+  g->rows = p->rows;
+  g->group_scale = p->group_scale;
+  g->out = p->y;
+  g->a_stride = a_stride;
+  g->out_stride = p->y_stride;
+  g->scale = p->scale;
+  g->m = p->m;
+  g->n_src = p->n_src;
+  g->N = p->n;
+  g->K = p->k;
+  g->n_groups = p->n_groups;
+  g->kind = p->kind;
+  g->swiglu = p->swiglu ? 1 : 0;
+  g->out_bf16 = p->out_dtype == EPOCH_BF16;
+  return EPOCH_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -248,6 +326,208 @@ epoch_status epoch_test_fp8_timeout(const void *a, const float *a_scales, const 
 int32_t epoch_fp8_matmul_kernel(int32_t n_groups, int32_t m, int32_t n, int32_t n_sms) {
   if (m < 0 || n < 1 || n_groups < 0 || n_groups > 1024 || n_sms < 0) return -1;
   return fp8_gemm_kernel(n_groups, m, n, n_sms ? n_sms : num_sms());
+}
+
+size_t epoch_route_workspace_bytes(int32_t n_tok, int32_t n_experts) {
+  if (n_tok < 1 || n_experts < 1 || n_experts > 1024) return 0;
+  return router_workspace(n_tok, n_experts);
+}
+
+epoch_status epoch_route(const epoch_route_args *p, epoch_stream stream) {
+  if (p == nullptr || p->n_tok < 0 || p->n_experts < 1 || p->n_experts > 1024 || p->top_k < 1 || p->top_k > 16 ||
+      p->top_k > p->n_experts || !dtype_ok(p->dtype) ||
+      (p->router != EPOCH_ROUTER_SOFTMAX && p->router != EPOCH_ROUTER_SIGMOID_GROUP))
+    return EPOCH_EINVAL;
+  const int64_t edges = static_cast<int64_t>(p->n_tok) * p->top_k;
+  if (edges > INT32_MAX - 256) return EPOCH_EINVAL;
+  const bool sigmoid = p->router == EPOCH_ROUTER_SIGMOID_GROUP;
+  if (!sigmoid && p->bias != nullptr) return EPOCH_EINVAL;
+  if (sigmoid && (p->n_group < 1 || p->n_group > 32 || p->n_experts % p->n_group || p->topk_group < 1 ||
+                  p->topk_group > p->n_group || (p->bias != nullptr && !on(p->bias, 4))))
+    return EPOCH_EINVAL;
+  if (!on(p->offsets, 4)) return EPOCH_EINVAL;
+  if (p->n_tok == 0) {  // an empty worklist
+    return status_of(cudaMemsetAsync(p->offsets, 0, sizeof(int32_t) * (p->n_experts + 1), S(stream)));
+  }
+  if (!of_type(p->logits, p->dtype) || !stride_ok(p->logits_stride, p->n_tok, p->n_experts) || !on(p->sel, 4) ||
+      !on(p->weights, 4) || !on(p->positions, 4) || !on(p->slots, 4))
+    return EPOCH_EINVAL;
+  const size_t need = router_workspace(p->n_tok, p->n_experts);
+  if (need > 0 && (!on(p->workspace, 4) || p->workspace_bytes < need)) return EPOCH_EINVAL;
+  const Rows outs[6] = {Rows(p->sel, edges, 4),   Rows(p->weights, edges, 4),
+                        Rows(p->positions, edges, 4), Rows(p->slots, edges, 4),
+                        Rows(p->offsets, p->n_experts + 1, 4), Rows(need ? p->workspace : nullptr, static_cast<int64_t>(need), 1)};
+  const Rows ins[4] = {Rows(p->logits, p->n_tok, p->n_experts, p->logits_stride, size_of(p->dtype)),
+                       Rows(p->bias, p->n_experts, 4), Rows(p->live, p->n_tok, 1), Rows(p->eligible, p->n_experts, 1)};
+  if (clash(outs, ins)) return EPOCH_EINVAL;
+  RouteArgs a = {};
+  a.logits = p->logits;
+  a.bias = p->bias;
+  a.live = p->live;
+  a.eligible = p->eligible;
+  a.sel = p->sel;
+  a.weights = p->weights;
+  a.positions = p->positions;
+  a.offsets = p->offsets;
+  a.slots = p->slots;
+  a.counts = static_cast<int32_t *>(p->workspace);
+  a.logits_stride = p->logits_stride;
+  a.n_tok = p->n_tok;
+  a.n_experts = p->n_experts;
+  a.top_k = p->top_k;
+  a.bf16 = p->dtype == EPOCH_BF16;
+  a.sigmoid = sigmoid;
+  a.n_group = sigmoid ? p->n_group : 1;
+  a.topk_group = sigmoid ? p->topk_group : 1;
+  a.raw_weights = p->raw_weights ? 1 : 0;
+  return status_of(launch_router(a, S(stream)));
+}
+
+epoch_status epoch_combine(const epoch_combine_args *p, epoch_stream stream) {
+  if (p == nullptr || p->n_tok < 0 || p->n_edges < 0 || p->hidden < 1 || p->hidden > kMaxHidden || p->k < 1 || p->k > 64 ||
+      !dtype_ok(p->dtype) || !dtype_ok(p->residual_dtype) || !dtype_ok(p->out_dtype))
+    return EPOCH_EINVAL;
+  const int64_t n = p->n_tok, h = p->hidden;
+  if (n * h > (1ll << 38)) return EPOCH_EINVAL;
+  if (n == 0) return EPOCH_OK;
+  if ((p->n_edges > 0 && !of_type(p->edges, p->dtype)) || !of_type_or_null(p->shared, p->dtype) ||
+      !of_type_or_null(p->residual, p->residual_dtype) || !of_type(p->out, p->out_dtype) || !on(p->slots, 4) || !on(p->weights, 4))
+    return EPOCH_EINVAL;
+  if (!stride_ok(p->edges_stride, p->n_edges, h) || (p->shared && !stride_ok(p->shared_stride, p->n_tok, h)) ||
+      (p->residual && !stride_ok(p->residual_stride, p->n_tok, h)) || !stride_ok(p->out_stride, p->n_tok, h))
+    return EPOCH_EINVAL;
+  const size_t sd = size_of(p->dtype), sr = size_of(p->residual_dtype);
+  const Rows out(p->out, n, h, p->out_stride, size_of(p->out_dtype));
+  const Rows outs[1] = {out};
+  const Rows ins[3] = {Rows(p->n_edges ? p->edges : nullptr, p->n_edges, h, p->edges_stride, sd), Rows(p->slots, n * p->k, 4),
+                       Rows(p->weights, n * p->k, 4)};
+  if (clash(outs, ins)) return EPOCH_EINVAL;
+  // A thread reads its elements of these before it writes them.
+  for (const Rows &in : {Rows(p->shared, n, h, p->shared_stride, sd), Rows(p->residual, n, h, p->residual_stride, sr)})
+    if (overlap(out, in) && !out.same(in)) return EPOCH_EINVAL;
+  CombineArgs a = {};
+  a.edges = p->edges;
+  a.shared = p->shared;
+  a.residual = p->residual;
+  a.slots = p->slots;
+  a.weights = p->weights;
+  a.out = p->out;
+  a.edges_stride = p->edges_stride;
+  a.shared_stride = p->shared_stride;
+  a.residual_stride = p->residual_stride;
+  a.out_stride = p->out_stride;
+  a.n_tok = n;
+  a.n_edges = p->n_edges;
+  a.hidden = p->hidden;
+  a.k = p->k;
+  a.residual_bf16 = p->residual_dtype == EPOCH_BF16;
+  a.out_bf16 = p->out_dtype == EPOCH_BF16;
+  return status_of(launch_combine_edges(a, p->dtype == EPOCH_BF16, S(stream)));
+}
+
+epoch_status epoch_fp4_quantize(const void *x, int64_t x_stride, int32_t dtype, const int32_t *rows, int32_t n_rows,
+                                int32_t n_src, int32_t cols, int32_t swiglu, int32_t format, float tensor_scale, void *q,
+                                void *scales, epoch_stream stream) {
+  if (n_rows < 0 || n_src < 0 || cols < 32 || cols % 32 || cols > (1 << 30) || !dtype_ok(dtype) || !fp4_format(format))
+    return EPOCH_EINVAL;
+  const float inv = 1.0f / tensor_scale;
+  if (!(tensor_scale > 0.f) || !std::isfinite(tensor_scale) || !std::isfinite(inv) || inv == 0.f ||
+      (format == EPOCH_FP4_MXFP4 && tensor_scale != 1.0f))
+    return EPOCH_EINVAL;
+  if (n_rows == 0) return EPOCH_OK;
+  if (rows == nullptr && n_src != n_rows) return EPOCH_EINVAL;
+  if (static_cast<int64_t>(n_rows) * ((cols + 255) / 256) > INT32_MAX) return EPOCH_EINVAL;
+  const int64_t wide = static_cast<int64_t>(cols) * (swiglu ? 2 : 1);
+  if ((n_src > 0 && !of_type(x, dtype)) || (rows != nullptr && !on(rows, 4)) || !on(q, 16) || !on(scales, 16) ||
+      !stride_ok(x_stride, n_src, wide))
+    return EPOCH_EINVAL;
+  const Rows outs[2] = {Rows(q, static_cast<int64_t>(n_rows) * cols / 2, 1), Rows(scales, fp4_scale_bytes(format, n_rows, cols), 1)};
+  const Rows ins[2] = {Rows(n_src ? x : nullptr, n_src, wide, x_stride, size_of(dtype)), Rows(rows, n_rows, 4)};
+  if (clash(outs, ins)) return EPOCH_EINVAL;
+  Fp4QuantArgs a = {};
+  a.x = x;
+  a.rows = rows;
+  a.q = static_cast<uint8_t *>(q);
+  a.scales = static_cast<uint8_t *>(scales);
+  a.x_stride = x_stride;
+  a.n_rows = n_rows;
+  a.n_src = n_src;
+  a.cols = cols;
+  a.swiglu = swiglu ? 1 : 0;
+  a.inv_scale = inv;
+  return status_of(launch_fp4_quant(a, dtype == EPOCH_BF16, format == EPOCH_FP4_NVFP4, S(stream)));
+}
+
+epoch_status epoch_fp4_quantize_weight(const void *w, int32_t dtype, int32_t n_mats, int32_t n, int32_t k, int32_t format,
+                                       void *q, void *scales, float *tensor_scales, epoch_stream stream) {
+  if (!dtype_ok(dtype) || !fp4_format(format) || n_mats < 0 || n_mats > 65535 || n < 1 || n > (1 << 22) || k < 32 || k % 32 ||
+      k > (1 << 22))
+    return EPOCH_EINVAL;
+  if (n_mats == 0) return EPOCH_OK;
+  const int64_t rows = static_cast<int64_t>(n_mats) * n;
+  if (rows * ((k + 255) / 256) > INT32_MAX) return EPOCH_EINVAL;
+  if (!of_type(w, dtype) || !on(q, 16) || !on(scales, 16) || !on(tensor_scales, 4)) return EPOCH_EINVAL;
+  const Rows outs[3] = {Rows(q, rows * k / 2, 1), Rows(scales, fp4_scale_bytes(format, rows, k), 1), Rows(tensor_scales, n_mats, 4)};
+  const Rows ins[1] = {Rows(w, rows * k, size_of(dtype))};
+  if (clash(outs, ins)) return EPOCH_EINVAL;
+  Fp4QuantArgs a = {};
+  a.x = w;
+  a.q = static_cast<uint8_t *>(q);
+  a.scales = static_cast<uint8_t *>(scales);
+  a.x_stride = k;
+  a.n_rows = a.n_src = rows;
+  a.mat_rows = n;
+  a.cols = k;
+  a.inv_scale = 1.0f;
+  return status_of(launch_fp4_quant_weight(a, n_mats, dtype == EPOCH_BF16, format == EPOCH_FP4_NVFP4, tensor_scales, S(stream)));
+}
+
+epoch_status epoch_fp4_dequantize(const void *q, const void *scales, int32_t format, int32_t n_mats, int32_t n, int32_t k,
+                                  float scale, const float *group_scale, void *out, int64_t out_stride, int32_t out_dtype,
+                                  epoch_stream stream) {
+  if (!dtype_ok(out_dtype) || !fp4_format(format) || n_mats < 0 || n < 0 || k < 32 || k % 32 || k > (1 << 30) || !std::isfinite(scale))
+    return EPOCH_EINVAL;
+  const int64_t rows = static_cast<int64_t>(n_mats) * n;
+  if (rows == 0) return EPOCH_OK;
+  if (rows > INT32_MAX || rows * ((k + 255) / 256) > INT32_MAX) return EPOCH_EINVAL;
+  if (!on(q, 16) || !on(scales, 16) || (group_scale != nullptr && !on(group_scale, 4)) || !of_type(out, out_dtype) ||
+      !stride_ok(out_stride, static_cast<int32_t>(rows), k))
+    return EPOCH_EINVAL;
+  const Rows outs[1] = {Rows(out, rows, k, out_stride, size_of(out_dtype))};
+  const Rows ins[3] = {Rows(q, rows * k / 2, 1), Rows(scales, fp4_scale_bytes(format, rows, k), 1), Rows(group_scale, n_mats, 4)};
+  if (clash(outs, ins)) return EPOCH_EINVAL;
+  Fp4DequantArgs a = {};
+  a.q = static_cast<const uint8_t *>(q);
+  a.scales = static_cast<const uint8_t *>(scales);
+  a.group_scale = group_scale;
+  a.out = out;
+  a.n_rows = rows;
+  a.mat_rows = n;
+  a.out_stride = out_stride;
+  a.cols = k;
+  a.scale = scale;
+  return status_of(launch_fp4_dequant(a, out_dtype == EPOCH_BF16, format == EPOCH_FP4_NVFP4, S(stream)));
+}
+
+epoch_status epoch_expert_matmul(const epoch_expert_args *p, epoch_stream stream) {
+  ExpertGemmArgs g;
+  const epoch_status st = expert_product(p, &g);
+  if (st != EPOCH_OK || p->m == 0) return st;
+  return status_of(g.kind == EPOCH_EXPERT_F32 ? launch_expert_simt(g, S(stream)) : launch_expert_gemm(g, S(stream)));
+}
+
+epoch_status epoch_test_expert_timeout(const epoch_expert_args *p, int64_t timeout_ns, epoch_stream stream) {
+  ExpertGemmArgs g;
+  const epoch_status st = expert_product(p, &g);
+  if (st != EPOCH_OK) return st;
+  if (timeout_ns < 1000 || timeout_ns > 5000000000ll || p->m == 0 || g.kind == EPOCH_EXPERT_F32) return EPOCH_EINVAL;
+  return status_of(launch_expert_gemm(g, S(stream), timeout_ns, 16));
+}
+
+int32_t epoch_expert_matmul_kernel(int32_t kind, int32_t n_groups, int32_t m, int32_t n, int32_t k, int32_t n_sms) {
+  if (kind < EPOCH_EXPERT_F32 || kind > EPOCH_EXPERT_MXFP4 || m < 0 || n < 1 || k < 1 || n_groups < 0 || n_groups > 1024 || n_sms < 0)
+    return -1;
+  return kind == EPOCH_EXPERT_F32 ? 0 : expert_gemm_kernel(n_groups, m, n, n_sms ? n_sms : num_sms());
 }
 
 epoch_status epoch_ops_status(int32_t clear, epoch_stream stream, uint32_t *word_out) {

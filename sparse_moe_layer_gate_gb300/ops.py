@@ -1,10 +1,12 @@
 """Torch-facing operators beside the MoE layer (marshalling only).
 
-Norms before and after a block, fused with its gate and residual scale, and
-matrix products in 8-bit floating point (e4m3) with a scale for each block of
-128. Every operator is one launch of the sm_103a library through the C ABI
-(include/epoch.h states the formulas); it allocates its outputs where none are
-given and keeps nothing between calls. Results carry no gradient history. All
+Norms before and after a block, fused with its gate and residual scale; matrix
+products in 8-bit floating point (e4m3) with a scale for each block of 128; and a
+layer's experts by themselves: the router, products grouped by expert on float32,
+bfloat16 or 4-bit (e2m1) operands, and the sum of a position's edges. Every operator
+is a launch of the sm_103a library (the router of many positions two, the 4-bit
+quantiser of weights up to three) through the C ABI (include/epoch.h states the
+formulas); it allocates its outputs where none are given and keeps nothing between calls. Results carry no gradient history. All
 tensors of a call are on the current CUDA device, and an output that overlaps an
 input is refused but where a function allows it. ``stream`` (default: torch's
 current stream) orders the launch and the outputs allocated for it; tensors that
@@ -13,7 +15,7 @@ another stream produced are the caller's to order.
 from __future__ import annotations
 
 import ctypes as C
-from typing import Optional, Tuple, Union
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -279,6 +281,316 @@ def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     B.check(B.lib().epoch_fp8_matmul(ap, asp, bp, bsp, op, groups, m, n, k, out.data_ptr(), ys, _code(out, "out"),
                                      _stream(stream, dev)), "epoch_fp8_matmul")
     return out
+
+
+class Routing(NamedTuple):
+    """What ``route`` gives: experts [T, k] int32 in order of selection (-1: none), their weights [T, k] float32, the
+    expert-sorted worklist's positions [T * k] int32 (-1 behind offsets[-1]) and offsets [E + 1] int32, and each
+    selection's row of the worklist [T, k] int32 (-1: none)."""
+    sel: torch.Tensor
+    weights: torch.Tensor
+    positions: torch.Tensor
+    offsets: torch.Tensor
+    slots: torch.Tensor
+
+
+_ROUTERS = {"softmax": B.EPOCH_ROUTER_SOFTMAX, "sigmoid_group": B.EPOCH_ROUTER_SIGMOID_GROUP}
+
+
+def _of(t: torch.Tensor, dev: int, dtype, shape, what: str) -> int:
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _flags(t: Optional[torch.Tensor], dev: int, n: int, what: str) -> int:
+    if t is None:
+        return 0
+    if t.dtype not in (torch.uint8, torch.bool):
+        raise ValueError(f"{what} must be uint8 or bool, not {t.dtype}")
+    return _of(t, dev, t.dtype, (n,), what)
+
+
+def route(logits: torch.Tensor, top_k: int, *, router: str = "softmax", bias: Optional[torch.Tensor] = None,
+          n_group: int = 1, topk_group: int = 1, raw_weights: bool = False, live: Optional[torch.Tensor] = None,
+          eligible: Optional[torch.Tensor] = None, out: Optional[Routing] = None, stream=None) -> Routing:
+    """Routes positions from their router logits [T, E] (float32 or bfloat16) without running an expert: what
+    grouped_matmul, fp8_quantize, fp4_quantize (positions as ``rows``), the grouped products (offsets) and combine
+    (slots, weights) take.
+
+    router "softmax" selects the largest logits (any bias included in them), "sigmoid_group" the largest sigmoid +
+    bias [E] float32 under the layer's group rule; equal ones by lower id. raw_weights keeps the router's own scores
+    (softmax: probabilities among all E) instead of weights that sum to 1. live [T] and eligible [E] (uint8 or bool)
+    leave out positions and experts, as does a logit of -inf; a NaN logit makes its position's weights NaN."""
+    dev = _device(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    n, e = logits.shape
+    kind = _ROUTERS.get(router)
+    if kind is None:
+        raise ValueError(f"router must be one of {sorted(_ROUTERS)}, not {router!r}")
+    if not 1 <= top_k <= min(16, e):
+        raise ValueError(f"top_k must be in [1, {min(16, e)}], not {top_k}")
+    ls = _rows(logits, dev, logits.shape, "logits")
+    code = _code(logits, "logits")
+    bp = 0
+    if bias is not None:
+        if kind == B.EPOCH_ROUTER_SOFTMAX:
+            raise ValueError("a softmax router's bias is part of its logits")
+        bp = _of(bias, dev, torch.float32, (e,), "bias")
+    lp, ep = _flags(live, dev, n, "live"), _flags(eligible, dev, e, "eligible")
+    if n * top_k > _MOST - 256:
+        raise ValueError("more than 2^31 - 257 edges")
+    if out is None:
+        i32 = torch.int32
+        out = Routing(_empty((n, top_k), i32, logits.device, stream), _empty((n, top_k), torch.float32, logits.device, stream),
+                      _empty((n * top_k,), i32, logits.device, stream), _empty((e + 1,), i32, logits.device, stream),
+                      _empty((n, top_k), i32, logits.device, stream))
+    else:
+        for t, d, shape, what in ((out.sel, torch.int32, (n, top_k), "out.sel"), (out.weights, torch.float32, (n, top_k), "out.weights"),
+                                  (out.positions, torch.int32, (n * top_k,), "out.positions"),
+                                  (out.offsets, torch.int32, (e + 1,), "out.offsets"), (out.slots, torch.int32, (n, top_k), "out.slots")):
+            _of(t, dev, d, shape, what)
+    need = B.lib().epoch_route_workspace_bytes(n, e)
+    ws = _empty((need,), torch.uint8, logits.device, stream) if need else None
+    args = B.ROUTE_ARGS.pack(logits.data_ptr(), bp, lp, ep, out.sel.data_ptr(), out.weights.data_ptr(), out.positions.data_ptr(),
+                             out.offsets.data_ptr(), out.slots.data_ptr(), ws.data_ptr() if need else 0, need, ls, n, e, top_k,
+                             code, kind, n_group, topk_group, 1 if raw_weights else 0)
+    B.check(B.lib().epoch_route(args, _stream(stream, dev)), "epoch_route")
+    return out
+
+
+def combine(edges: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, shared: Optional[torch.Tensor] = None,
+            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] * edges[slots[t, j]] (+ shared[t]) (+ residual[t]), summed in float32.
+
+    edges [n, H] and shared [T, H] (the shared experts' output) are of one dtype, residual [T, H] and the result (default:
+    residual's dtype, else edges') of another or the same; slots [T, k] int32 and weights [T, k] float32 as ``route``
+    gives them. A negative slot adds nothing, one past the last edge makes its row NaN. ``out`` may be shared or
+    residual of its dtype and strides."""
+    dev = _device(edges, "edges")
+    if edges.dim() != 2 or slots.dim() != 2:
+        raise ValueError("edges must be [n, H], slots [T, k]")
+    m, h = edges.shape
+    n, k = slots.shape
+    shape = (n, h)
+    if n > _MOST or not 1 <= k <= 64:
+        raise ValueError("slots must have at most 2^31 - 1 rows and 1 to 64 columns")
+    sp, wp = _of(slots, dev, torch.int32, (n, k), "slots"), _of(weights, dev, torch.float32, (n, k), "weights")
+    es = _rows(edges, dev, edges.shape, "edges")
+    hp = hs = rp = rs = 0
+    if shared is not None:
+        hp, hs = shared.data_ptr(), _rows(shared, dev, shape, "shared")
+        if shared.dtype != edges.dtype:
+            raise ValueError(f"shared has dtype {shared.dtype}, edges {edges.dtype}")
+    code = res = _code(edges, "edges")
+    if residual is not None:
+        rp, rs, res = residual.data_ptr(), _rows(residual, dev, shape, "residual"), _code(residual, "residual")
+    if out is None:
+        dtype = out_dtype or (edges.dtype if residual is None else residual.dtype)
+        out, ys = _empty(shape, dtype, edges.device, stream), h
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    else:
+        ys = _rows(out, dev, shape, "out")
+    args = B.COMBINE_ARGS.pack(edges.data_ptr(), hp, rp, sp, wp, out.data_ptr(), es, hs, rs, ys, n, m, h, k, code, res,
+                               _code(out, "out"))
+    B.check(B.lib().epoch_combine(args, _stream(stream, dev)), "epoch_combine")
+    return out
+
+
+def _expert(kind, x, w, sa, sb, offsets, rows, scale, swiglu, out, out_dtype, m, n_src, k, x_stride, dev, stream):
+    """The product of experts, its operands checked: offsets, factors, output and the call."""
+    if w.dim() != (2 if offsets is None else 3):
+        raise ValueError("weights must be [N, K], or [E, N, K] with offsets")
+    n = w.shape[-2]
+    groups = 1 if offsets is None else w.shape[0]
+    op = _index(offsets, dev, "offsets") or 0
+    if offsets is not None and offsets.shape[0] != groups + 1:
+        raise ValueError(f"offsets must have {groups + 1} entries")
+    if swiglu and n % 2:
+        raise ValueError("swiglu needs an even number of rows of weights")
+    width = n // 2 if swiglu else n
+    number, fp = 1.0, 0
+    if isinstance(scale, torch.Tensor):
+        fp = _of(scale, dev, torch.float32, (groups,), "scale")
+    else:
+        number = scale
+    if out is None:
+        out, ys = _empty((m, width), out_dtype or (torch.float32 if kind == B.EPOCH_EXPERT_F32 else torch.bfloat16), x.device,
+                         stream), width
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    else:
+        ys = _rows(out, dev, (m, width), "out")
+    args = B.EXPERT_ARGS.pack(x.data_ptr(), w.data_ptr(), sa, sb, op, rows, fp, out.data_ptr(), x_stride, ys, number, groups, m,
+                              n_src, n, k, kind, 1 if swiglu else 0, _code(out, "out"))
+    B.check(B.lib().epoch_expert_matmul(args, _stream(stream, dev)), "epoch_expert_matmul")
+    return out
+
+
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor], *, rows: Optional[torch.Tensor] = None,
+                   swiglu: bool = False, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                   stream=None) -> torch.Tensor:
+    """Rows of x [m, K] times their expert's weights: rows offsets[e] .. offsets[e + 1] - 1 by w[e] (w [E, N, K], offsets
+    [E + 1] int32 on the device, as a worklist has them; None: every row by w [N, K]).
+
+    x and w are float32 or bfloat16 together; rows of x start on 16-byte boundaries. rows (int32, [m]) gathers: row i
+    of the product is row rows[i] of x, as the positions of a worklist; an index out of range gives a row of NaN.
+    swiglu: w's rows are gate | up and the result is silu(y[:, :N / 2]) * y[:, N / 2:]. Accumulated in float32 and
+    rounded once (default: x's dtype); rows outside the offsets keep what ``out`` holds (a fresh result leaves them
+    undefined)."""
+    dev = _device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [m, K]")
+    src, k = x.shape
+    code = _code(x, "x")
+    if w.dtype != x.dtype or w.get_device() != dev or not w.is_contiguous() or w.shape[-1] != k or max(w.shape) > _MOST:
+        raise ValueError(f"w must be a contiguous {x.dtype} tensor [(E,) N, {k}] on cuda:{dev}")
+    xs = _rows(x, dev, x.shape, "x")
+    rp = _index(rows, dev, "rows") or 0
+    m = src if rows is None else rows.shape[0]
+    if m > _MOST:
+        raise ValueError("rows has more than 2^31 - 1 entries")
+    if out is None and out_dtype is None:
+        out_dtype = x.dtype
+    return _expert(B.EPOCH_EXPERT_BF16 if code == B.EPOCH_BF16 else B.EPOCH_EXPERT_F32, x, w, 0, 0, offsets, rp, 1.0, swiglu, out,
+                   out_dtype, m, src, k, xs, dev, stream)
+
+
+# format: (code, columns that share a scale, the scales' dtype, the product's kind)
+_FP4 = {"nvfp4": (B.EPOCH_FP4_NVFP4, 16, torch.float8_e4m3fn, B.EPOCH_EXPERT_NVFP4),
+        "mxfp4": (B.EPOCH_FP4_MXFP4, 32, torch.float8_e8m0fnu, B.EPOCH_EXPERT_MXFP4)}
+_FP4_OF = {v[2]: v for v in _FP4.values()}
+
+
+def _fp4(form: str):
+    f = _FP4.get(form)
+    if f is None:
+        raise ValueError(f"form must be one of {sorted(_FP4)}, not {form!r}")
+    return f
+
+
+def _fp4_operand(q: torch.Tensor, scales: torch.Tensor, dev: int, what: str):
+    """(pointers of values and scales, K, the format) of a packed operand [.., n, K / 2]."""
+    f = _FP4_OF.get(scales.dtype)
+    if f is None:
+        raise ValueError(f"{what}_scales must be float8_e4m3fn (nvfp4) or float8_e8m0fnu (mxfp4), not {scales.dtype}")
+    if q.dim() < 2 or max(q.shape) > _MOST // 2:
+        raise ValueError(f"{what} must be [.., n, K / 2] of at most 2^30 rows and columns")
+    k = 2 * q.shape[-1]
+    lead, n = tuple(q.shape[:-2]), q.shape[-2]
+    return (_of(q, dev, torch.uint8, tuple(q.shape), what),
+            _of(scales, dev, f[2], lead + (-(-k // 256), n, 256 // f[1]), what + "_scales"), k, f)
+
+
+def fp4_quantize(x: torch.Tensor, *, form: str = "nvfp4", rows: Optional[torch.Tensor] = None, swiglu: bool = False,
+                 tensor_scale: float = 1.0, q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(q, scales): the rows of x [n, K] (float32 or bfloat16) in e2m1, q [n, K / 2] uint8 with the even column in a
+    byte's low half, and scales [ceil(K / 256), n, 256 / block].
+
+    form "nvfp4": blocks of 16 columns with float8_e4m3fn scales of x / tensor_scale; "mxfp4": blocks of 32 with
+    float8_e8m0fnu scales (powers of two). A value is q * scale (* tensor_scale, which the product's ``scale`` has
+    to bring back); a tensor_scale that is a power of two rounds nothing. rows and swiglu as for fp8_quantize. K must
+    be a multiple of 32."""
+    dev = _device(x, "x")
+    code, block, dtype, _ = _fp4(form)
+    if x.dim() != 2:
+        raise ValueError("x must be [n, K]" if not swiglu else "x must be [n, 2 K]")
+    src, k = x.shape
+    if swiglu:
+        if k % 2:
+            raise ValueError("swiglu needs an even number of columns")
+        k //= 2
+    rp = _index(rows, dev, "rows")
+    n = src if rows is None else rows.shape[0]
+    xs = _rows(x, dev, x.shape, "x")
+    if n > _MOST:
+        raise ValueError("rows has more than 2^31 - 1 entries")
+    if q is None:
+        q = _empty((n, k // 2), torch.uint8, x.device, stream)
+    else:
+        _of(q, dev, torch.uint8, (n, k // 2), "q")
+    shape = (-(-k // 256), n, 256 // block)
+    if scales is None:
+        scales = _empty(shape, dtype, x.device, stream)
+    else:
+        _of(scales, dev, dtype, shape, "scales")
+    B.check(B.lib().epoch_fp4_quantize(x.data_ptr(), xs, _code(x, "x"), rp, n, src, k, 1 if swiglu else 0, code, tensor_scale,
+                                       q.data_ptr(), scales.data_ptr(), _stream(stream, dev)), "epoch_fp4_quantize")
+    return q, scales
+
+
+def fp4_quantize_weight(w: torch.Tensor, *, form: str = "nvfp4", stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(q, scales, tensor_scales) of a weight matrix [N, K] or a stack of them [E, N, K] (float32 or bfloat16,
+    contiguous): q [(E,) N, K / 2], scales [(E,) ceil(K / 256), N, 256 / block] and a factor for each matrix, [E] float32
+    ([1] for one): nvfp4: the power of two that keeps the blocks' scales within e4m3, mxfp4: 1. Together with an
+    activation's tensor_scale they are fp4_matmul's ``scale``."""
+    dev = _device(w, "w")
+    code, block, dtype, _ = _fp4(form)
+    if w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError("w must be a contiguous [N, K] or [E, N, K] tensor")
+    n, k = w.shape[-2:]
+    if max(w.shape) > _MOST:
+        raise ValueError("w has more than 2^31 - 1 matrices, rows or columns")
+    lead = tuple(w.shape[:-2])
+    mats = w.shape[0] if w.dim() == 3 else 1
+    q = _empty(lead + (n, k // 2), torch.uint8, w.device, stream)
+    scales = _empty(lead + (-(-k // 256), n, 256 // block), dtype, w.device, stream)
+    factors = _empty((mats,), torch.float32, w.device, stream)
+    B.check(B.lib().epoch_fp4_quantize_weight(w.data_ptr(), _code(w, "w"), mats, n, k, code, q.data_ptr(), scales.data_ptr(),
+                                              factors.data_ptr(), _stream(stream, dev)), "epoch_fp4_quantize_weight")
+    return q, scales, factors
+
+
+def fp4_dequantize(q: torch.Tensor, scales: torch.Tensor, *, tensor_scale: Union[float, torch.Tensor] = 1.0,
+                   out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """The values [.., n, K] that rows or a stack of weights in e2m1 stand for, times tensor_scale (a number, or a
+    factor for each matrix of the stack, [E] float32), bfloat16 (default) or float32."""
+    dev = _device(q, "q")
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [n, K / 2] or [E, n, K / 2]")
+    qp, sp, k, f = _fp4_operand(q, scales, dev, "q")
+    mats, n = (q.shape[0] if q.dim() == 3 else 1), q.shape[-2]
+    number, fp = 1.0, None
+    if isinstance(tensor_scale, torch.Tensor):
+        fp = _of(tensor_scale, dev, torch.float32, (mats,), "tensor_scale")
+    else:
+        number = tensor_scale
+    shape = tuple(q.shape[:-1]) + (k,)
+    if out is None:
+        out, ys = _empty(shape, out_dtype or torch.bfloat16, q.device, stream), k
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    elif q.dim() == 2:
+        ys = _rows(out, dev, shape, "out")
+    else:
+        _of(out, dev, out.dtype, shape, "out")
+        ys = k
+    B.check(B.lib().epoch_fp4_dequantize(qp, sp, f[0], mats, n, k, number, fp, out.data_ptr(), ys, _code(out, "out"),
+                                         _stream(stream, dev)), "epoch_fp4_dequantize")
+    return out
+
+
+def fp4_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor, *,
+               offsets: Optional[torch.Tensor] = None, scale: Union[float, torch.Tensor] = 1.0, swiglu: bool = False,
+               out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """Product of e2m1 rows a [m, K / 2] with e2m1 weights of the same format, both with their scales as fp4_quantize
+    and fp4_quantize_weight give them.
+
+    Dense: b [N, K / 2], y = scale * a b^T. Grouped (``offsets``): b [E, N, K / 2], as grouped_matmul. scale: a number,
+    or a factor for each matrix of b ([E] float32; dense [1]). swiglu as for grouped_matmul. The result is bfloat16
+    (default) or float32, accumulated in float32 and rounded once."""
+    dev = _device(a, "a")
+    if a.dim() != 2:
+        raise ValueError("a must be [m, K / 2]")
+    ap, asp, k, f = _fp4_operand(a, a_scales, dev, "a")
+    _, bsp, kb, fb = _fp4_operand(b, b_scales, dev, "b")
+    if kb != k or fb is not f:
+        raise ValueError("a and b must have the same K and the same format")
+    return _expert(f[3], a, b, asp, bsp, offsets, 0, scale, swiglu, out, out_dtype, a.shape[0], a.shape[0], k, k // 2, dev, stream)
 
 
 def status(clear: bool = False, stream=None):
