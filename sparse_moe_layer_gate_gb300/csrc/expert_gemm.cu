@@ -9,14 +9,14 @@
 //
 // Tiles of 128 rows x 256, 128, 64 or 32 columns, or of 256 x 256 by two CTAs whose tensor cores
 // read both halves of the weights. A producer warp streams 128-byte-wide operand tiles (64 bf16 or
-// 256 e2m1 columns) by TMA through a ring in shared memory, gathered rows four at a time; an MMA
+// 256 e2m1 columns) by TMA through a ring in shared memory, two more warps the gathered rows; an MMA
 // warp issues the tcgen05 products into TMEM; eight epilogue warps take a finished accumulator into
 // registers, free it, and store under the next tile's products. With swiglu a tile's columns are
 // half gate and half up rows of the weights, so that both halves of an output meet in one thread.
 //
 // 4-bit operands: the tensor core multiplies by both scales itself and reads them from TMEM, where
 // 32 rows x 4 scales take a column of 32 lanes. Scales lie in memory by blocks of 256 columns,
-// [K / 256][rows][16 or 8], so that the rows of a tile are one run wherever it starts. Three warps
+// [K / 256][rows][16 or 8], so that the rows of a tile are one run wherever it starts. Up to three warps
 // bring them into shared memory in the order of TMEM (lane l of row group c), from which the MMA
 // thread copies them ahead of the products that use them.
 #include <cstring>
@@ -34,13 +34,14 @@ constexpr int kEpiWarps = 8;
 constexpr int kRow = 128;  // bytes of an operand row of a stage: one swizzle row
 
 struct ExpertParams {
-  CUtensorMap a[3];  // boxes of 32, 64, 128 rows; gathered: a[0] with boxes of one row
+  CUtensorMap a[3];  // boxes of 32, 64, 128 rows
   CUtensorMap b;     // boxes of half a tile's columns (pairs: 128)
   ExpertGemmArgs g;
   int kb_n, nt_n;    // K blocks, tiles along N
   int out_n;         // columns of the output
   int wide;          // output rows start on 32-byte boundaries
   int reuse;         // weights are read by several row tiles
+  int acc_kb;        // K blocks that an accumulator sums before it is added to the fp32 sums in registers
   uint32_t *err;
   int64_t timeout_ns;
   uint32_t hold;  // bytes that a stage waits for beyond its copies': 0, but for the test of waits that run out
@@ -119,29 +120,26 @@ template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t taddr,
   else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// Four rows of a matrix, one operand row each.
-template <bool PAIR>
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int32_t c0, const int (&r)[4],
-                                          uint32_t bar, uint64_t policy) {
-  if constexpr (PAIR)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "l"(policy)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "l"(policy)
-        : "memory");
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// An arrival that releases this thread's writes to the cluster, and a wait that acquires them.
+// An arrival that releases what happened before it to the cluster, and an attempt at a wait that acquires it.
 __device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 template <int Q> __device__ __forceinline__ void load_cols(uint32_t at, float (&v)[Q]) {
   if constexpr (Q == 8) tmem_ld8(at, v);
@@ -197,9 +195,8 @@ template <int FP4, int BN, bool PAIR>
 __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm(const __grid_constant__ ExpertParams p) {
   using G = Tile<FP4, BN, PAIR>;
   constexpr int Q = BN / 4;                                        // columns of one of a thread's two runs
-  constexpr int kFull = 1 + (FP4 ? (1 + G::groups_b) * (PAIR ? 2 : 1) : 0);  // arrivals that fill a stage
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * G::stages + 2 * G::bufs];
+  __shared__ __align__(8) uint64_t bars[3 * G::stages + 2 * G::bufs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
@@ -209,7 +206,9 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *const ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
   const uint32_t full = smem_u32(bars), empty = full + 8 * G::stages, tfull = empty + 8 * G::stages,
-                 tempty = tfull + 8 * G::bufs;
+                 tempty = tfull + 8 * G::bufs, ready = tempty + 8 * G::bufs;
+  const bool gather = FP4 == 0 && p.g.rows != nullptr;
+  const int helpers = FP4 ? 1 + G::groups_b : gather ? 2 : 0;  // warps that write a stage beside the copies
   if (warp == 0) {
     if constexpr (PAIR) {
       tmem_alloc_pair(smem_u32(&s_tmem), G::tmem);
@@ -229,8 +228,10 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
   } else if (warp == 2 && lane == 0) {
     s_abort = 0;
     for (int i = 0; i < G::stages; ++i) {
-      mbar_init(full + 8 * i, kFull);
+      // the copies' bytes, this CTA's helpers, and for the second CTA's one warp that waits for them
+      mbar_init(full + 8 * i, 1 + helpers + (PAIR && helpers ? 1 : 0));
       mbar_init(empty + 8 * i, 1);
+      mbar_init(ready + 8 * i, helpers ? helpers : 1);
     }
     for (int i = 0; i < G::bufs; ++i) {
       mbar_init(tfull + 8 * i, 1);
@@ -263,20 +264,9 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
       for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
-        int idx[4] = {-1, -1, -1, -1};  // out of range: read as zeros (and the result is NaN)
-        int quads = 32;
-        if (p.g.rows != nullptr) {
-          if (!PAIR) quads = (rows + 3) / 4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (4 * lane + j < rows) {
-              const int r = __ldg(p.g.rows + row0 + 4 * lane + j);
-              if (r >= 0 && r < p.g.n_src) idx[j] = r;
-            }
-        }
         // single CTAs load the smallest box that holds their rows
         const int box = PAIR || rows > 64 ? 2 : rows > 32 ? 1 : 0;
-        const uint32_t a_bytes = p.g.rows != nullptr ? quads * 4 * kRow : PAIR ? kBm * kRow : (32u << box) * kRow;
+        const uint32_t a_bytes = gather ? 0u : PAIR ? kBm * kRow : (32u << box) * kRow;
         const uint32_t bytes = (PAIR ? 2 : 1) * (a_bytes + G::b_rows * kRow) + p.hold;
         int b0, b1;  // first rows of the two copies of weights
         if (p.g.swiglu) {
@@ -293,12 +283,10 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
           const uint32_t dst = ring + st * G::stage, bar = counts + 8 * st;
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
-            if (p.g.rows == nullptr) load_box<PAIR>(dst, &p.a[box], kb * kCols, row0, bar, keep);
+            if (!gather) load_box<PAIR>(dst, &p.a[box], kb * kCols, row0, bar, keep);
             load_box<PAIR>(dst + kBm * kRow, &p.b, kb * kCols, b0, bar, wpol);
             if constexpr (!PAIR) load_box<PAIR>(dst + kBm * kRow + G::box_b * kRow, &p.b, kb * kCols, b1, bar, wpol);
           }
-          __syncwarp();
-          if (p.g.rows != nullptr && lane < quads) load_rows<PAIR>(dst + lane * 4 * kRow, &p.a[0], kb * kCols, idx, bar, keep);
           __syncwarp();
           if (++st == G::stages) {
             st = 0;
@@ -312,17 +300,17 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
           int done = 0;
           wait_for(full + 8 * (i % G::stages), (i / G::stages) & 1u, &done, p.err, p.timeout_ns);
         }
-    } else if (FP4 && warp >= kEpiWarps + 4 && warp <= kEpiWarps + 4 + G::groups_b) {  // scales, a group of 128 rows a warp
-      constexpr int kPer = FP4 * 4;  // scales of a row in a stage
+    } else if (FP4 != 0 && warp >= kEpiWarps + 4 && warp < kEpiWarps + 4 + helpers) {  // scales, a group of 128 rows a warp
+      constexpr int kPer = FP4 * 4;            // scales of a row in a stage
+      constexpr int kAhead = 3;                // stages whose scales are on their way
       const int group = warp - kEpiWarps - 4;  // 0: a's rows; 1, 2: the weights'
-      const uint32_t filled = PAIR ? mapa_shared(full, 0) : full;
+      const uint32_t filled = PAIR && rank ? ready : full;
       uint32_t st = 0, phase = 1;
       bool ok = true;
       for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
         const uint8_t *src[4];
-        int64_t step;  // bytes between K blocks
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // rows that do not exist read one that does
           const int r = 32 * c + lane;
@@ -334,55 +322,138 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
             src[c] = p.g.sb + (static_cast<int64_t>(e) * p.kb_n * p.g.N + min(n, p.g.N - 1)) * kPer;
           }
         }
-        step = static_cast<int64_t>(group == 0 ? p.g.m : p.g.N) * kPer;
-        uint32_t v[4][FP4 ? FP4 : 1];
-        auto load = [&](int kb) {
+        const int64_t step = static_cast<int64_t>(group == 0 ? p.g.m : p.g.N) * kPer;  // bytes between K blocks
+        uint32_t v[kAhead][4][FP4 ? FP4 : 1];
+        auto load = [&](int kb, uint32_t (&u)[4][FP4 ? FP4 : 1]) {
+          if (kb >= p.kb_n) return;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint8_t *at = src[c] + min(kb, p.kb_n - 1) * step;
+            const uint8_t *at = src[c] + kb * step;
             if constexpr (FP4 == 4) {
-              const uint4 u = __ldg(reinterpret_cast<const uint4 *>(at));
-              v[c][0] = u.x, v[c][1] = u.y, v[c][2] = u.z, v[c][3] = u.w;
+              const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at));
+              u[c][0] = x.x, u[c][1] = x.y, u[c][2] = x.z, u[c][3] = x.w;
             } else if constexpr (FP4 == 2) {
-              const uint2 u = __ldg(reinterpret_cast<const uint2 *>(at));
-              v[c][0] = u.x, v[c][1] = u.y;
+              const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at));
+              u[c][0] = x.x, u[c][1] = x.y;
             }
           }
         };
-        load(0);
-        for (int kb = 0; kb < p.kb_n; ++kb) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(i, v[i]);
+        for (int kb0 = 0; ok && kb0 < p.kb_n; kb0 += kAhead) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            if (kb0 + i >= p.kb_n) break;
+            ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
+            if (!ok) break;
+            uint8_t *dst = ring_ptr + st * G::stage + G::operands + group * FP4 * 512 + lane * 16;
+#pragma unroll
+            for (int k = 0; k < FP4; ++k)
+              *reinterpret_cast<uint4 *>(dst + k * 512) = make_uint4(v[i][0][k], v[i][1][k], v[i][2][k], v[i][3][k]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(filled + 8 * st);
+            load(kb0 + i + kAhead, v[i]);
+            if (++st == G::stages) {
+              st = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+      }
+    } else if (FP4 == 0 && gather && warp >= kEpiWarps + 2) {  // gathered rows, every other four of them a warp
+      // Eight lanes copy an operand row in the 128-byte swizzle. (Copies of four rows an instruction by TMA took 80
+      // clocks each, which bound tiles of many rows at 0.5 PFLOP/s.)
+      constexpr int kLag = 2;  // stages between a copy and its arrival
+      const int w = warp - kEpiWarps - 2, chunk = lane & 7;
+      const uint32_t filled = PAIR && rank ? ready : full;
+      uint32_t it = 0, st = 0, phase = 1;
+      bool ok = true;
+      auto arrive = [&](uint32_t i) {  // this warp's copies of stage i have landed
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(filled + 8 * (i % G::stages));
+      };
+      for (int t = cta; ok && t < walk.total; t += ctas) {
+        int e, row0, rows, nt;
+        walk.at(t, &e, &row0, &rows, &nt);
+        int idx[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = 4 * (2 * i + w) + (lane >> 3);
+          idx[i] = r < rows ? __ldg(p.g.rows + row0 + r) : -1;
+        }
+        for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
           ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
           if (!ok) break;
-          uint8_t *dst = ring_ptr + st * G::stage + G::operands + group * FP4 * 512 + lane * 16;
+          const int k = kb * 64 + 8 * chunk;
+          const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.g.a) + k;
+          const uint32_t dst = ring + st * G::stage;
 #pragma unroll
-          for (int k = 0; k < FP4; ++k)
-            *reinterpret_cast<uint4 *>(dst + k * 512) = make_uint4(v[0][k], v[1][k], v[2][k], v[3][k]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR) arrive_release_cluster(filled + 8 * st);
-            else mbar_arrive(filled + 8 * st);
+          for (int i = 0; i < 16; ++i) {
+            const int r4 = 4 * (2 * i + w), r = r4 + (lane >> 3);
+            if (r4 >= rows) break;
+            const bool there = idx[i] >= 0 && idx[i] < p.g.n_src && k < p.g.K;  // else zeros
+            copy16(dst + r * kRow + ((chunk ^ (r & 7)) << 4), there ? static_cast<const void *>(src + idx[i] * p.g.a_stride) : p.g.b,
+                   there);
           }
-          load(kb + 1);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (it >= kLag) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+            arrive(it - kLag);
+          }
           if (++st == G::stages) {
             st = 0;
             phase ^= 1u;
           }
         }
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (ok)
+        for (uint32_t i = it > kLag ? it - kLag : 0; i < it; ++i) arrive(i);
+    } else if (PAIR && warp == kEpiWarps + 1 && rank == 1) {  // ---------------- the second CTA's helpers, to the first
+      // One warp without accesses of its own releases them to the cluster: a release waits for every access of its warp.
+      if (helpers) {
+        const uint32_t filled = mapa_shared(full, 0);
+        uint32_t st = 0, phase = 0;
+        bool ok = true;
+        for (int t = cta; ok && t < walk.total; t += ctas)
+          for (int kb = 0; kb < p.kb_n; ++kb) {
+            ok = warp_wait(ready + 8 * st, phase, abort, p.err, p.timeout_ns);
+            if (!ok) break;
+            if (lane == 0) arrive_release_cluster(filled + 8 * st);
+            __syncwarp();
+            if (++st == G::stages) {
+              st = 0;
+              phase ^= 1u;
+            }
+          }
+      }
     } else if (warp == kEpiWarps + 1 && rank == 0) {  // ------------------------ MMA
       // The warp stays together and one elected lane issues, so that descriptors and barriers are uniform values.
       constexpr uint32_t idesc = idesc_of<FP4>(G::bm, BN);
-      uint32_t it = 0, st = 0, phase = 0, tile = 0;
+      uint32_t it = 0, st = 0, phase = 0, seq = 0;  // seq: accumulators begun
       bool ok = true;
-      for (int t = cta; ok && t < walk.total; t += ctas, ++tile) {
-        const uint32_t buf = tile % G::bufs;
-        ok = warp_wait(tempty + 8 * buf, ((tile / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
-        if (!ok) break;
-        for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
-          ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
-          if (!ok) break;
-          if constexpr (PAIR && FP4 != 0) acquire_cluster();
+      for (int t = cta; ok && t < walk.total; t += ctas) {
+        for (int kb = 0, part = 0; kb < p.kb_n; ++kb, ++it) {
+          const uint32_t buf = seq % G::bufs;
+          if (part == 0) {
+            ok = warp_wait(tempty + 8 * buf, ((seq / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
+            if (!ok) break;
+          }
+          if constexpr (PAIR) {
+            // the second CTA's helpers wrote its shared memory
+            if (!__all_sync(0xffffffffu, try_wait_cluster(full + 8 * st, phase))) {
+              ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
+              if (!ok) break;
+              // complete by now: this attempt acquires
+              ok = __all_sync(0xffffffffu, try_wait_cluster(full + 8 * st, phase) || try_wait_cluster(full + 8 * st, phase));
+              if (!ok) break;
+            }
+          } else {
+            ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
+            if (!ok) break;
+          }
           tc_fence_after();
           const uint32_t src = ring + st * G::stage;
           const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kRow);
@@ -403,12 +474,14 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
               const int chunk = FP4 == 2 ? k / 2 : k;
               const uint32_t id = FP4 == 2 && (k & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
               mma<FP4, PAIR>(tmem + buf * BN, ad + 2 * k, bd + 2 * k, id, sa + 4 * chunk, sb + G::cols_b * chunk,
-                             kb > 0 || k > 0);
+                             part > 0 || k > 0);
             }
             commit<PAIR>(empty + 8 * st);
-            if (kb == p.kb_n - 1) commit<PAIR>(tfull + 8 * buf);
+            if (part == p.acc_kb - 1 || kb == p.kb_n - 1) commit<PAIR>(tfull + 8 * buf);
           }
           __syncwarp();
+          if (++part == p.acc_kb) part = 0;
+          if (part == 0 || kb == p.kb_n - 1) ++seq;
           if (++st == G::stages) {
             st = 0;
             phase ^= 1u;
@@ -428,11 +501,12 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
     const bool swiglu = p.g.swiglu != 0, bf16 = p.g.out_bf16 != 0, wide = p.wide != 0;
     const int c0 = swiglu ? half * Q : half * 2 * Q, c1 = swiglu ? BN / 2 + half * Q : c0 + Q;
     const size_t size = bf16 ? 2 : 4;
-    uint32_t tile = 0;
-    for (int t = cta; t < walk.total; t += ctas, ++tile) {
+    constexpr int kPiece = Q < 32 ? Q : 32;
+    uint32_t seq = 0;
+    bool ok = true;
+    for (int t = cta; ok && t < walk.total; t += ctas) {
       int e, row0, rows, nt;
       walk.at(t, &e, &row0, &rows, &nt);
-      const uint32_t buf = tile % G::bufs;
       const int row = row0 + quarter * 32 + lane;
       const bool on = quarter * 32 + lane < rows;
       const int n0 = (swiglu ? nt * (BN / 2) : nt * BN) + c0;  // output column of the first run
@@ -442,23 +516,42 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
         const int r = __ldg(p.g.rows + row);
         if (r < 0 || r >= p.g.n_src) s = __uint_as_float(0x7FC00000u);
       }
-      const bool ok = __all_sync(0xffffffffu, wait_for(tfull + 8 * buf, (tile / G::bufs) & 1u, abort, p.err, p.timeout_ns));
-      if (!ok) break;
-      tc_fence_after();
       float v0[Q], v1[Q];
       const bool any = quarter * 32 < rows && n0 < p.out_n;  // this warp holds an element of the tile
-      if (any) {
-        const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-        load_cols<Q>(src + c0, v0);
-        load_cols<Q>(src + c1, v1);
-        tmem_ld_wait();
+      for (int kb = 0; kb < p.kb_n; kb += p.acc_kb, ++seq) {
+        const uint32_t buf = seq % G::bufs;
+        ok = __all_sync(0xffffffffu, wait_for(tfull + 8 * buf, (seq / G::bufs) & 1u, abort, p.err, p.timeout_ns));
+        if (!ok) break;
+        tc_fence_after();
+        if (any) {
+          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+          if (FP4 != 0 || kb == 0) {
+            load_cols<Q>(src + c0, v0);
+            load_cols<Q>(src + c1, v1);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < Q; j += kPiece) {
+              float w[kPiece];
+              load_cols<kPiece>(src + c0 + j, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kPiece; ++i) v0[j + i] += w[i];
+              load_cols<kPiece>(src + c1 + j, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kPiece; ++i) v1[j + i] += w[i];
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) arrive_cluster(read + 8 * buf);
+          else mbar_arrive(read + 8 * buf);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) arrive_cluster(read + 8 * buf);
-        else mbar_arrive(read + 8 * buf);
-      }
+      if (!ok) break;
       if (!any || !on) continue;
       void *dst = static_cast<uint8_t *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride * size;
       if (swiglu) {
@@ -588,22 +681,21 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t 
   p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && a.out_stride % (a.out_bf16 ? 16 : 8) == 0;
   const int64_t E = a.offsets ? a.n_groups : 1;
   p.reuse = a.m > kBm * E;
+  // The tensor core's sums drift by their truncation: over 1024 columns to 1e-6 of an fp32 result, four times what sums
+  // in fp32 are off by. So fp32 results of bf16 products add up accumulators of 256 columns.
+  p.acc_kb = fp4 || a.out_bf16 ? p.kb_n : 4;
   p.err = ops_error_word();
   p.timeout_ns = timeout_ns;
   p.hold = hold;
   if (p.err == nullptr || !tma_encode_init()) return cudaErrorInitializationError;
-  const uint64_t k_row = fp4 ? a.K / 2 : a.K, src_rows = a.rows ? a.n_src : a.m;
+  const uint64_t k_row = fp4 ? a.K / 2 : a.K;
   const uint32_t b_box = kernel == kExpertPairs || kernel == 256 ? 128 : kernel / 2;
   bool ok = encode_operand(&p.b, a.b, !fp4, k_row, E * a.N, k_row, b_box);
-  if (a.rows) {
-    // nothing to gather from: every index is out of range, of any tensor
-    const bool none = a.n_src == 0;
-    ok = ok && encode_operand(&p.a[0], none ? a.b : a.a, !fp4, k_row, none ? 1 : src_rows, a.a_stride, 1);
-  } else {
-    ok = ok && encode_operand(&p.a[2], a.a, !fp4, k_row, src_rows, a.a_stride, 128);
+  if (a.rows == nullptr) {
+    ok = ok && encode_operand(&p.a[2], a.a, !fp4, k_row, a.m, a.a_stride, 128);
     if (kernel != kExpertPairs && (a.offsets || a.m % kBm != 0))
-      ok = ok && encode_operand(&p.a[0], a.a, !fp4, k_row, src_rows, a.a_stride, 32) &&
-           encode_operand(&p.a[1], a.a, !fp4, k_row, src_rows, a.a_stride, 64);
+      ok = ok && encode_operand(&p.a[0], a.a, !fp4, k_row, a.m, a.a_stride, 32) &&
+           encode_operand(&p.a[1], a.a, !fp4, k_row, a.m, a.a_stride, 64);
   }
   if (!ok) return cudaErrorInvalidValue;
   if (a.kind == EPOCH_EXPERT_BF16) return launch_kind<0>(p, kernel, s);

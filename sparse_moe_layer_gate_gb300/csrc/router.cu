@@ -1,17 +1,17 @@
 // A router by itself: from logits to each position's experts and weights and to the worklist that the
 // products grouped by expert take (expert-major, positions ascending), without running any expert.
 //
-// One warp a position: the lanes hold consecutive experts' logits, and the k best are ranked in
-// registers (topk.cuh). Positions of a CTA are marked in a word of bits for each expert, so that an
+// One warp a position: the lanes hold consecutive experts' logits, and the k best are found by rounds
+// of a warp maximum. Positions of a CTA are marked in a word of bits for each expert, so that an
 // edge's place among the CTA's is a population count, whatever order the warps come in. A second
-// kernel adds what earlier CTAs and lower experts hold: every CTA reads all CTAs' counts (64 KB at
+// kernel adds what earlier CTAs and lower experts hold: every CTA reads all CTAs' counts (128 KB at
 // 16384 positions and 256 experts) rather than wait for one that adds them up. Up to 128 positions
 // one CTA does both. What bounds it: latency up to some thousand positions, then the instructions of
-// the ranking (some 350 a position and warp), not the logits' bytes.
+// the ranking, not the logits' bytes.
 //
 // The sigmoid router's order is that of sigmoid(G) + bias in exact arithmetic. It is decided in fp32
-// where neighbours are further apart than fp32's roundings can move them, and once more in 64 bits
-// for the positions where they are not (about 2 in 1000 with 256 experts).
+// where neighbours are further apart than fp32's roundings can move them; for the positions where they
+// are not (2 in 1000 with 256 experts) the entries near the border are ranked once more in 64 bits.
 #include "common.cuh"
 #include "layer.h"
 #include "topk.cuh"
@@ -56,165 +56,284 @@ template <int EPL> __device__ __forceinline__ void row_logits(const void *row, b
   for (int c = 0; c < EPL; ++c) v[c] = e0 + c < E ? logit(row, bf16, e0 + c) : -INFINITY;
 }
 
-__device__ __forceinline__ double shfl_double(double v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
-
-// Largest (value, lowest id) of the warp; id < 0: nothing.
-__device__ __forceinline__ void warp_best(double &v, int &id) {
+// The k best of the warp's entries, lane l owning the EPL consecutive ids from l * EPL on: key 0 is no entry, equal
+// keys go by lower id. Lane j < k gets entry j (id -1: there is none). `scratch`: 32 entries of the warp's own.
+//
+// The k-th best of the lanes' best keys bounds the k best entries from below: only entries at or above it are ranked
+// against one another, one a lane. Each of both rankings is k rounds of a warp maximum, some 15 instructions in all a
+// round, where comparing every pair of lanes took 200.
+template <int EPL>
+__device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2 *scratch, int *id, unsigned *val) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = lane_id();
+  unsigned left = key[0], bound = 0u;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double w = __shfl_xor_sync(0xffffffffu, v, o);
-    const int j = __shfl_xor_sync(0xffffffffu, id, o);
-    if (j >= 0 && (id < 0 || w > v || (w == v && j < id))) v = w, id = j;
+  for (int c = 1; c < EPL; ++c) left = max(left, key[c]);
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    bound = __reduce_max_sync(kAll, left);
+    if (bound == 0u) break;  // fewer than k lanes hold an entry: all entries count
+    const unsigned hold = __ballot_sync(kAll, left == bound);
+    if (lane == __ffs(hold) - 1) left = 0u;
   }
+  int n = 0;
+#pragma unroll
+  for (int c = 0; c < EPL; ++c) n += key[c] >= bound && key[c] != 0u;
+  int sum = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, sum, o);
+    if (lane >= o) sum += y;
+  }
+  const int total = __shfl_sync(kAll, sum, 31);
+  *id = -1;
+  *val = 0u;
+  if (total > 32) {  // many equal keys, or k lanes with several of the best
+    float v;
+    warp_topk_rounds<EPL>(key, k, id, &v);
+    if (*id >= 0) *val = order_key(v);
+    return;
+  }
+  int at = sum - n;
+#pragma unroll
+  for (int c = 0; c < EPL; ++c)
+    if (key[c] >= bound && key[c] != 0u) scratch[at++] = make_uint2(key[c], static_cast<unsigned>(lane * EPL + c));
+  __syncwarp();
+  const uint2 mine = lane < total ? scratch[lane] : make_uint2(0u, 0u);  // ascending ids
+  __syncwarp();
+  left = mine.x;
+  int rank = 32;
+  const int rounds = min(k, total);
+#pragma unroll 1
+  for (int j = 0; j < rounds; ++j) {
+    const unsigned m = __reduce_max_sync(kAll, left);
+    const unsigned hold = __ballot_sync(kAll, left == m);
+    if (lane == __ffs(hold) - 1) {
+      left = 0u;
+      rank = j;
+    }
+  }
+  if (rank < 32) scratch[rank] = mine;
+  __syncwarp();
+  if (lane < rounds) {
+    *id = static_cast<int>(scratch[lane].y);
+    *val = scratch[lane].x;
+  }
+  __syncwarp();
 }
 
-// The selection of one position by sigmoid(G) + bias in 64 bits: lane j < k gets expert j, or -1.
-template <int EPL>
-__device__ __noinline__ int select_exact(const float *g, const bool *can, const RouteArgs &a) {
-  const int lane = lane_id(), E = a.n_experts, gs = E / a.n_group;
-  double c[EPL];
-  bool ok[EPL];
+// Selection score of an expert in 64 bits, and its place in an order of integers (0: none; a NaN ranks with -inf).
+__device__ __forceinline__ double score_exact(const RouteArgs &a, float g, int e) {
+  return 1.0 / (1.0 + exp(-static_cast<double>(g))) + (a.bias != nullptr ? static_cast<double>(__ldg(a.bias + e)) : 0.0);
+}
+__device__ __forceinline__ unsigned long long order_exact(double v) {
+  if (v != v) v = -INFINITY;
+  const long long b = __double_as_longlong(v + 0.0);
+  return static_cast<unsigned long long>(b < 0 ? ~b : b | static_cast<long long>(1ull << 63));
+}
+// Largest of the warp's keys (0: none) and the lowest lane that holds it.
+__device__ __forceinline__ unsigned long long warp_best(unsigned long long v, int *lane) {
+  const unsigned hi = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(v >> 32));
+  const unsigned lo = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(v >> 32) == hi ? static_cast<unsigned>(v) : 0u);
+  const unsigned long long best = (static_cast<unsigned long long>(hi) << 32) | lo;
+  *lane = __ffs(__ballot_sync(0xffffffffu, v == best)) - 1;
+  return best;
+}
+
+// Candidates of one position, at most one a lane in ascending id, ranked in 64 bits: lane j < k gets the id of rank j.
+__device__ __noinline__ int rank_exact(const RouteArgs &a, const void *row, int e, int k) {
+  unsigned long long left = e >= 0 ? order_exact(score_exact(a, logit(row, a.bf16 != 0, e), e)) : 0ull;
+  int sel = -1;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    int win;
+    const unsigned long long best = warp_best(left, &win);
+    const int id = __shfl_sync(0xffffffffu, e, win);
+    if (best == 0ull) break;
+    if (lane_id() == j) sel = id;
+    if (lane_id() == win) left = 0ull;
+  }
+  return sel;
+}
+
+// The whole selection of one position in 64 bits, where groups' scores are too near or too many experts are: lane j < k
+// gets expert j, or -1. `can` has a bit for each of the lane's EPL experts. Rare, and slow.
+template <int EPL> __device__ __noinline__ int select_exact(const RouteArgs &a, const void *row, unsigned can) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = lane_id(), gs = a.n_experts / a.n_group;
+  unsigned long long key[EPL];
 #pragma unroll 1
   for (int q = 0; q < EPL; ++q) {
     const int e = lane * EPL + q;
-    ok[q] = can[q];
-    c[q] = 1.0 / (1.0 + exp(-static_cast<double>(g[q]))) + (a.bias != nullptr && e < E ? static_cast<double>(__ldg(a.bias + e)) : 0.0);
-    if (c[q] != c[q]) c[q] = -INFINITY;  // a NaN ranks with -inf
+    key[q] = (can >> q) & 1u ? order_exact(score_exact(a, logit(row, a.bf16 != 0, e), e)) : 0ull;
   }
   if (a.topk_group < a.n_group) {
     double score = 0.0;  // lane i: group i's
     int held = 0;
 #pragma unroll 1
     for (int i = 0; i < a.n_group; ++i) {
-      double sum = 0.0;
-      int first = -1, n = 0;
+      unsigned long long k1 = 0ull, k2 = 0ull;
+      int n = 0;
 #pragma unroll 1
-      for (int q = 0; q < EPL; ++q) n += ok[q] && (lane * EPL + q) / gs == i;
-      n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
-#pragma unroll 1
-      for (int r = 0; r < 2; ++r) {
-        double v = -INFINITY;
-        int id = -1;
-#pragma unroll 1
-        for (int q = 0; q < EPL; ++q) {
-          const int e = lane * EPL + q;
-          if (ok[q] && e / gs == i && e != first && (id < 0 || c[q] > v)) v = c[q], id = e;
-        }
-        warp_best(v, id);
-        if (id >= 0) sum += v;
-        first = id;
+      for (int q = 0; q < EPL; ++q) {
+        const unsigned long long v = (lane * EPL + q) / gs == i ? key[q] : 0ull;
+        n += v != 0ull;
+        if (v > k1) k2 = k1, k1 = v;
+        else if (v > k2) k2 = v;
       }
-      if (lane == i) score = sum, held = n;
+      n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
+      int win, unused;
+      const unsigned long long m1 = warp_best(k1, &win), m2 = warp_best(lane == win ? k2 : k1, &unused);
+      auto value = [](unsigned long long v) {
+        const long long b = static_cast<long long>(v);
+        return v ? __longlong_as_double(b < 0 ? b & 0x7FFFFFFFFFFFFFFFll : ~b) : 0.0;
+      };
+      if (lane == i) score = value(m1) + value(m2), held = n;
     }
     int rank = 0, before = 0;
 #pragma unroll 1
     for (int i = 0; i < a.n_group; ++i) {
-      const double s = shfl_double(score, i);
-      const int h = __shfl_sync(0xffffffffu, held, i);
+      const double s = __shfl_sync(kAll, score, i);
+      const int h = __shfl_sync(kAll, held, i);
       if (h > 0 && (s > score || (s == score && i < lane))) ++rank, before += h;
     }
-    const unsigned chosen = __ballot_sync(0xffffffffu, lane < a.n_group && held > 0 && (rank < a.topk_group || before < a.top_k));
+    const unsigned chosen = __ballot_sync(kAll, lane < a.n_group && held > 0 && (rank < a.topk_group || before < a.top_k));
 #pragma unroll 1
-    for (int q = 0; q < EPL; ++q) {
-      const int i = (lane * EPL + q) / gs;
-      if (ok[q] && !((chosen >> (i & 31)) & 1u)) ok[q] = false;
-    }
+    for (int q = 0; q < EPL; ++q)
+      if (!((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) key[q] = 0ull;
   }
   int sel = -1;
 #pragma unroll 1
   for (int j = 0; j < a.top_k; ++j) {
-    double v = -INFINITY;
-    int id = -1;
+    unsigned long long v = 0ull;
+    int at = 0;
 #pragma unroll 1
     for (int q = 0; q < EPL; ++q)
-      if (ok[q] && (id < 0 || c[q] > v)) v = c[q], id = lane * EPL + q;
-    warp_best(v, id);
+      if (key[q] > v) v = key[q], at = q;
+    int win;
+    const unsigned long long best = warp_best(v, &win);
+    const int id = __shfl_sync(kAll, lane * EPL + at, win);
+    if (best == 0ull) break;
     if (lane == j) sel = id;
-#pragma unroll 1
-    for (int q = 0; q < EPL; ++q)
-      if (lane * EPL + q == id) ok[q] = false;
+    if (lane == win) key[at] = 0ull;
   }
   return sel;
 }
 
-// Whether two selection scores are apart whatever fp32 made of them: sigmoid is off by at most 4 steps of 2^-23 (expf
-// 2, a sum and a quotient), the sum with the bias by half a step of the result; a group's score is the sum of two.
-__device__ __forceinline__ bool apart(float a, float b) {
-  return fabsf(a - b) > 4e-6f + 8e-7f * fmaxf(fabsf(a), fabsf(b));
-}
+// sigmoid in fp32 for the selection, off by less than 4e-7: the exponential's 2 + 1.2 |g| steps of 2^-23 reach the
+// result by s (1 - s) of them (less than one step), the sum's and the quotient's 2 steps and a half by s.
+__device__ __forceinline__ float sigmoid_near(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// Whether two selection scores are apart whatever fp32 made of them: sigmoid as above, the sum with the bias half a
+// step of the result. Groups' scores are sums of two: twice that.
+__device__ __forceinline__ float reach(float a, float b) { return 1.2e-6f + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)); }
+__device__ __forceinline__ bool apart(float a, float b) { return fabsf(a - b) > reach(a, b); }
+__device__ __forceinline__ bool groups_apart(float a, float b) { return fabsf(a - b) > 2.0f * reach(a, b); }
 
-// The groups that a position may search (clears ok outside them); false where fp32 cannot tell.
-template <int EPL>
-__device__ __forceinline__ bool limit_groups(const float (&c)[EPL], bool (&ok)[EPL], const RouteArgs &a) {
+// The groups that a position may search (clears keys outside them); false where fp32 cannot tell. Where a lane's
+// experts are of one group and a group is 2^i lanes, its lanes merge their two best; else every group is looked for
+// in all lanes.
+template <int EPL> __device__ __forceinline__ bool limit_groups(unsigned (&key)[EPL], const RouteArgs &a) {
   constexpr unsigned kAll = 0xffffffffu;
-  const int lane = lane_id(), gs = a.n_experts / a.n_group;
+  const int lane = lane_id(), gs = a.n_experts / a.n_group, span = gs / EPL;  // span: lanes of a group
+  const bool aligned = gs % EPL == 0 && (span & (span - 1)) == 0;
   float score = -INFINITY;  // lane i: group i's
   int held = 0;
-  for (int i = 0; i < a.n_group; ++i) {
-    unsigned k1 = 0u, k2 = 0u;
-    int n = 0;
-    const int lo = i * gs - lane * EPL, hi = lo + gs;  // the group's entries of this lane
+  if (aligned) {
+    unsigned k1 = 0u, k2 = 0u, n = 0u;
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
-      const unsigned key = ok[q] && q >= lo && q < hi ? order_key(c[q]) : 0u;
-      n += key != 0u;
-      k2 = max(k2, min(k1, key));
-      k1 = max(k1, key);
+      n += key[q] != 0u;
+      k2 = max(k2, min(k1, key[q]));
+      k1 = max(k1, key[q]);
     }
-    const unsigned m1 = __reduce_max_sync(kAll, k1);
-    const unsigned hold = __ballot_sync(kAll, k1 == m1 && k1 != 0u);
-    const unsigned m2 = __reduce_max_sync(kAll, hold && lane == __ffs(hold) - 1 ? k2 : k1);
-    n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
-    if (lane == i) {
-      held = n;
-      score = m1 == 0u ? -INFINITY : m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
+    for (int o = 1; o < span; o <<= 1) {
+      const unsigned o1 = __shfl_xor_sync(kAll, k1, o), o2 = __shfl_xor_sync(kAll, k2, o);
+      n += __shfl_xor_sync(kAll, n, o);
+      k2 = max(max(k2, o2), min(k1, o1));
+      k1 = max(k1, o1);
+    }
+    const float mine = k1 == 0u ? -INFINITY : k2 == 0u ? key_value(k1) : key_value(k1) + key_value(k2);
+    const int from = lane < a.n_group ? lane * span : 0;
+    score = __shfl_sync(kAll, mine, from);
+    held = static_cast<int>(__shfl_sync(kAll, n, from));
+  } else {
+    for (int i = 0; i < a.n_group; ++i) {
+      unsigned k1 = 0u, k2 = 0u;
+      int n = 0;
+      const int lo = i * gs - lane * EPL, hi = lo + gs;  // the group's entries of this lane
+#pragma unroll
+      for (int q = 0; q < EPL; ++q) {
+        const unsigned v = q >= lo && q < hi ? key[q] : 0u;
+        n += v != 0u;
+        k2 = max(k2, min(k1, v));
+        k1 = max(k1, v);
+      }
+      const unsigned m1 = __reduce_max_sync(kAll, k1);
+      const unsigned hold = __ballot_sync(kAll, k1 == m1);
+      const unsigned m2 = __reduce_max_sync(kAll, lane == __ffs(hold) - 1 ? k2 : k1);
+      n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
+      if (lane == i) {
+        held = n;
+        score = m1 == 0u ? -INFINITY : m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
+      }
     }
   }
   const bool there = lane < a.n_group && held > 0;
   int rank = 0, before = 0;
+#pragma unroll 4
   for (int i = 0; i < a.n_group; ++i) {
     const float s = __shfl_sync(kAll, score, i);
     const int h = __shfl_sync(kAll, held, i);
     if (h > 0 && (s > score || (s == score && i < lane))) ++rank, before += h;
   }
   const unsigned chosen = __ballot_sync(kAll, there && (rank < a.topk_group || before < a.top_k));
-  // A chosen and an unchosen group must be apart; where more than topk_group are taken, their order counts too.
-  bool sure = __popc(chosen) <= a.topk_group;
-  for (int i = 0; i < a.n_group; ++i) {
-    const float s = __shfl_sync(kAll, score, i);
-    const int h = __shfl_sync(kAll, held, i);
-    const bool other = there && h > 0 && (((chosen >> i) ^ (chosen >> lane)) & 1u);
-    sure = sure && !(other && !apart(s, score));
-  }
+  const unsigned others = __ballot_sync(kAll, there) & ~chosen;
+  // A chosen and an unchosen group must be apart: the least chosen and the best other. Where more than topk_group are
+  // taken, their order counts too.
+  const unsigned low = __reduce_min_sync(kAll, (chosen >> lane) & 1u ? order_key(score) : 0xffffffffu);
+  const unsigned high = __reduce_max_sync(kAll, (others >> lane) & 1u ? order_key(score) : 0u);
+  const bool sure = __popc(chosen) <= a.topk_group && (others == 0u || groups_apart(key_value(low), key_value(high)));
+  if (aligned) {
+    // lanes behind the last group hold no entry
+    if (!((chosen >> ((lane / span) & 31)) & 1u))
 #pragma unroll
-  for (int q = 0; q < EPL; ++q)
-    if (ok[q] && !((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) ok[q] = false;
-  return __all_sync(kAll, sure);
+      for (int q = 0; q < EPL; ++q) key[q] = 0u;
+  } else {
+#pragma unroll
+    for (int q = 0; q < EPL; ++q)
+      if (!((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) key[q] = 0u;
+  }
+  return sure;
 }
 
-// One position by one warp: lane j < top_k gets its expert (-1: none) and weight.
+// One position by one warp: lane j < top_k gets its expert (-1: none) and weight. `eligible` has a bit for each of the
+// lane's experts.
 template <int EPL>
-__device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool vec, const bool (&eligible)[EPL], uint2 *scratch,
+__device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool vec, unsigned eligible, uint2 *scratch,
                                           int *sel_out, float *w_out) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = lane_id(), k = a.top_k;
   float v[EPL];
-  bool ok[EPL];
+  unsigned key[EPL], can = eligible;
   const bool bf16 = a.bf16 != 0;
   const void *row = static_cast<const uint8_t *>(a.logits) + t * a.logits_stride * (bf16 ? 2 : 4);
   row_logits<EPL>(row, bf16, a.n_experts, vec, v);
   bool nan = false;
 #pragma unroll
   for (int c = 0; c < EPL; ++c) {
-    ok[c] = eligible[c] && v[c] != -INFINITY;
+    if (v[c] == -INFINITY) can &= ~(1u << c);
     nan = nan || v[c] != v[c];
   }
   int sel;
-  float val, w;
+  unsigned val;
+  float w;
   if (!a.sigmoid) {
-    warp_topk<EPL>(v, ok, k, &sel, &val, scratch);
-    const bool on = lane < k && sel >= 0;
-    float top, sum;
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) key[c] = (can >> c) & 1u ? order_key(v[c]) : 0u;
+    best_of<EPL>(key, k, scratch, &sel, &val);
+    const bool on = sel >= 0;
+    const float g = key_value(val);
+    float top = key_value(__shfl_sync(kAll, val, 0)), sum;
     if (a.raw_weights) {  // probabilities over all experts, eligible or not
       float m = v[0];
 #pragma unroll
@@ -224,69 +343,73 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool ve
 #pragma unroll
       for (int c = 0; c < EPL; ++c) sum += lane * EPL + c < a.n_experts ? expf(v[c] - top) : 0.f;
     } else {
-      top = __shfl_sync(kAll, val, 0);
-      sum = on ? expf(val - top) : 0.f;
+      sum = on ? expf(g - top) : 0.f;
     }
-    w = on ? expf(val - top) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    w = on ? w / sum : 0.f;
+    w = on ? expf(g - top) / sum : 0.f;
   } else {
-    float c[EPL];
-    bool open[EPL];
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
       const int e = lane * EPL + q;
-      c[q] = 1.0f / (1.0f + expf(-v[q])) + (a.bias != nullptr && e < a.n_experts ? __ldg(a.bias + e) : 0.f);
-      open[q] = ok[q];
+      v[q] = sigmoid_near(v[q]) + (a.bias != nullptr && e < a.n_experts ? __ldg(a.bias + e) : 0.f);
+      key[q] = (can >> q) & 1u ? order_key(v[q]) : 0u;
     }
-    bool sure = true;
-    if (a.topk_group < a.n_group) sure = limit_groups<EPL>(c, open, a);
+    bool sure = a.topk_group >= a.n_group || limit_groups<EPL>(key, a);
     if (sure) {
       // one more than asked for, so that the last border is seen too
-      warp_topk<EPL>(c, open, k + 1, &sel, &val, scratch);
-      const float next = __shfl_down_sync(kAll, val, 1);
+      best_of<EPL>(key, k + 1, scratch, &sel, &val);
+      const float at = key_value(val), next = __shfl_down_sync(kAll, at, 1);
       const int after = __shfl_down_sync(kAll, sel, 1);
-      bool far = true, tied = false;
-      if (lane < k && sel >= 0 && after >= 0 && !apart(val, next)) {
-        // equal logits and equal biases are equal scores, in the order of their ids
-        const float b0 = a.bias ? __ldg(a.bias + sel) : 0.f, b1 = a.bias ? __ldg(a.bias + after) : 0.f;
-        far = tied = logit(row, bf16, sel) == logit(row, bf16, after) && b0 == b1;
-      }
-      if (__ballot_sync(kAll, tied) >> (k - 1) & 1u) {
-        // a tie at the last border: nothing else may be near it, or it could belong before both
-        const int at = __shfl_sync(kAll, sel, k - 1);
-        const float edge = __shfl_sync(kAll, val, k - 1), g = logit(row, bf16, at), b = a.bias ? __ldg(a.bias + at) : 0.f;
+      if (__any_sync(kAll, lane < k && after >= 0 && !apart(at, next))) {
+        // Every entry that could be among the k: those not surely below the k-th, in 64 bits.
+        const float edge = __shfl_sync(kAll, at, k - 1);
+        const bool all = __shfl_sync(kAll, sel, k - 1) < 0;
+        unsigned near = 0u;
 #pragma unroll
-        for (int q = 0; q < EPL; ++q) {
-          const int e = lane * EPL + q;
-          if (open[q] && !apart(c[q], edge)) far = far && v[q] == g && (a.bias == nullptr || __ldg(a.bias + e) == b);
+        for (int q = 0; q < EPL; ++q)
+          if (key[q] != 0u && (all || !(v[q] < edge && apart(v[q], edge)))) near |= 1u << q;
+        int n = __popc(near), sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kAll, sum, o);
+          if (lane >= o) sum += y;
+        }
+        const int total = __shfl_sync(kAll, sum, 31);
+        sure = total <= 32;
+        if (sure) {
+          int to = sum - n;
+#pragma unroll
+          for (int q = 0; q < EPL; ++q)
+            if ((near >> q) & 1u) scratch[to++].y = static_cast<unsigned>(lane * EPL + q);
+          __syncwarp();
+          const int e = lane < total ? static_cast<int>(scratch[lane].y) : -1;
+          __syncwarp();
+          sel = rank_exact(a, row, e, k);
         }
       }
-      sure = __all_sync(kAll, far);
     }
-    if (!sure) sel = select_exact<EPL>(v, ok, a);
-    const bool on = lane < k && sel >= 0;
-    const float g = on ? logit(row, bf16, sel) : 0.f;
-    w = on ? 1.0f / (1.0f + expf(-g)) : 0.f;
+    if (!sure) sel = select_exact<EPL>(a, row, can);
+    if (lane >= k) sel = -1;
+    const float g = sel >= 0 ? logit(row, bf16, sel) : 0.f;
+    w = sel >= 0 ? 1.0f / (1.0f + expf(-g)) : 0.f;
     if (!a.raw_weights) {
       float sum = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      w = on ? w / sum : 0.f;
+      w = sel >= 0 ? w / sum : 0.f;
     }
   }
   if (__any_sync(kAll, nan) && sel >= 0) w = __uint_as_float(0x7FC00000u);  // a NaN among a position's logits spoils its weights
-  *sel_out = lane < k ? sel : -1;
+  *sel_out = sel;
   *w_out = w;
 }
 
 // First entries of the experts (offsets, E + 1 values in shared memory) from their totals; all threads of the CTA.
-template <int THREADS> __device__ __forceinline__ void scan_totals(const int *total, int E, int *offsets, int *s_warp) {
-  const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
-  constexpr int kWarps = THREADS / 32;
+__device__ __forceinline__ void scan_totals(const int *total, int E, int *offsets, int *s_warp) {
+  const int tid = threadIdx.x, lane = lane_id(), warp = warp_id(), warps = blockDim.x >> 5;
   int carry = 0;
-  for (int base = 0; base < E; base += THREADS) {
+  for (int base = 0; base < E; base += blockDim.x) {
     const int e = base + tid, n = e < E ? total[e] : 0;
     int sum = n;
 #pragma unroll
@@ -296,13 +419,15 @@ template <int THREADS> __device__ __forceinline__ void scan_totals(const int *to
     }
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    int add = carry;
-    for (int w = 0; w < kWarps; ++w) {
-      const int s = s_warp[w];
-      if (w < warp) add += s;
-      carry += s;
+    int all = lane < warps ? s_warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += y;
     }
-    if (e < E) offsets[e] = add + sum - n;
+    const int below = __shfl_sync(0xffffffffu, all, warp > 0 ? warp - 1 : 0);
+    if (e < E) offsets[e] = carry + (warp > 0 ? below : 0) + sum - n;
+    carry += __shfl_sync(0xffffffffu, all, 31);
     __syncthreads();
   }
   if (tid == 0) offsets[E] = carry;
@@ -313,24 +438,23 @@ template <int THREADS> __device__ __forceinline__ void scan_totals(const int *to
 // CTA of a grid (with one pass) finishes the worklist too.
 template <int EPL, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, int passes, int pass) {
-  constexpr int kWarps = THREADS / 32, kRows = kPass / kWarps;  // positions of a warp in a full pass
+  constexpr int kRows = kPass / (THREADS / 32);  // most positions of a warp in a pass
   constexpr int kE = EPL * 32;
   __shared__ uint32_t s_bits[kPass / 32][kE];
-  __shared__ int s_count[kE], s_off[kE + 1], s_warp[kWarps];
-  __shared__ uint2 s_scratch[kWarps][32];
-  const int tid = threadIdx.x, lane = lane_id(), warp = warp_id(), E = a.n_experts, k = a.top_k;
-  const int words = pass / 32;
+  __shared__ int s_count[kE], s_off[kE + 1], s_warp[32];
+  __shared__ uint2 s_scratch[THREADS / 32][32];
+  const int tid = threadIdx.x, threads = blockDim.x, lane = lane_id(), warp = warp_id(), warps = threads >> 5;
+  const int E = a.n_experts, k = a.top_k, words = pass / 32;
   const bool vec = a.vec != 0, one = gridDim.x == 1 && passes == 1;
-  for (int i = tid; i < kE; i += THREADS) {
+  for (int i = tid; i < E; i += threads) {
     s_count[i] = 0;
-#pragma unroll
-    for (int w = 0; w < kPass / 32; ++w) s_bits[w][i] = 0u;
+    for (int w = 0; w < words; ++w) s_bits[w][i] = 0u;
   }
-  bool eligible[EPL];
+  unsigned eligible = 0u;
 #pragma unroll
   for (int c = 0; c < EPL; ++c) {
     const int e = lane * EPL + c;
-    eligible[c] = e < E && (a.eligible == nullptr || __ldg(a.eligible + e) != 0);
+    if (e < E && (a.eligible == nullptr || __ldg(a.eligible + e) != 0)) eligible |= 1u << c;
   }
   const int64_t first = static_cast<int64_t>(blockIdx.x) * passes * pass;
   pdl_trigger();
@@ -338,38 +462,57 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
     const int64_t t0 = first + static_cast<int64_t>(p) * pass;
     if (t0 >= a.n_tok) break;
     __syncthreads();  // the words are clear
+    const int rows = static_cast<int>(min(static_cast<int64_t>(pass), a.n_tok - t0));
     int sel[kRows];
 #pragma unroll
+    for (int i = 0; i < kRows; ++i) sel[i] = -1;
+#pragma unroll 1
     for (int i = 0; i < kRows; ++i) {
-      const int r = i * kWarps + warp;
+      const int r = i * warps + warp;
+      if (r >= rows) break;
       const int64_t t = t0 + r;
-      sel[i] = -1;
-      if (r >= pass || t >= a.n_tok) continue;
+      int e = -1;
       float w = 0.f;
-      if (a.live == nullptr || __ldg(a.live + t) != 0) route_row<EPL>(a, t, vec, eligible, s_scratch[warp], &sel[i], &w);
+      if (a.live == nullptr || __ldg(a.live + t) != 0) route_row<EPL>(a, t, vec, eligible, s_scratch[warp], &e, &w);
       if (lane < k) {
-        a.sel[t * k + lane] = sel[i];
+        a.sel[t * k + lane] = e;
         a.weights[t * k + lane] = w;
-        if (sel[i] >= 0) atomicOr(&s_bits[r >> 5][sel[i]], 1u << (r & 31));
+        if (e >= 0) atomicOr(&s_bits[r >> 5][e], 1u << (r & 31));
       }
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+        if (q == i) sel[q] = e;
     }
     __syncthreads();
-    int place[kRows];
+    if (one) {  // totals, then places in the whole worklist
+      for (int i = tid; i < E; i += threads) {
+        int n = 0;
+        for (int w = 0; w < words; ++w) n += __popc(s_bits[w][i]);
+        s_count[i] = n;
+      }
+      __syncthreads();
+      scan_totals(s_count, E, s_off, s_warp);
+      for (int i = tid; i <= E; i += threads) a.offsets[i] = s_off[i];
+      for (int64_t i = s_off[E] + tid; i < static_cast<int64_t>(a.n_tok) * k; i += threads) a.positions[i] = -1;
+    }
+    const int *base = one ? s_off : s_count;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = i * kWarps + warp;
+      const int r = i * warps + warp;
+      if (r >= rows || lane >= k) continue;
       const int64_t t = t0 + r;
-      place[i] = -1;
-      if (r >= pass || t >= a.n_tok || lane >= k) continue;
+      int place = -1;
       if (sel[i] >= 0) {
-        place[i] = s_count[sel[i]];
-        for (int w = 0; w < (r >> 5); ++w) place[i] += __popc(s_bits[w][sel[i]]);
-        place[i] += __popc(s_bits[r >> 5][sel[i]] & ((1u << (r & 31)) - 1u));
+        place = base[sel[i]];
+        for (int w = 0; w < (r >> 5); ++w) place += __popc(s_bits[w][sel[i]]);
+        place += __popc(s_bits[r >> 5][sel[i]] & ((1u << (r & 31)) - 1u));
+        if (one) a.positions[place] = static_cast<int>(t);
       }
-      if (!one) a.slots[t * k + lane] = place[i];
+      a.slots[t * k + lane] = place;
     }
+    if (one) return;
     __syncthreads();
-    for (int i = tid; i < E; i += THREADS) {
+    for (int i = tid; i < E; i += threads) {
       int n = s_count[i];
       for (int w = 0; w < words; ++w) {
         n += __popc(s_bits[w][i]);
@@ -377,27 +520,9 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       }
       s_count[i] = n;
     }
-    if (one) {
-      __syncthreads();
-      scan_totals<THREADS>(s_count, E, s_off, s_warp);
-      for (int i = tid; i <= E; i += THREADS) a.offsets[i] = s_off[i];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = i * kWarps + warp;
-        const int64_t t = t0 + r;
-        if (r >= pass || t >= a.n_tok || lane >= k) continue;
-        const int slot = sel[i] >= 0 ? s_off[sel[i]] + place[i] : -1;
-        a.slots[t * k + lane] = slot;
-        if (slot >= 0) a.positions[slot] = static_cast<int>(t);
-      }
-      for (int64_t i = s_off[E] + tid; i < static_cast<int64_t>(a.n_tok) * k; i += THREADS) a.positions[i] = -1;
-    }
   }
-  if (!one) {
-    __syncthreads();
-    for (int i = tid; i < E; i += THREADS)
-      a.counts[static_cast<int64_t>(blockIdx.x) * E + i] = s_count[i];
-  }
+  __syncthreads();
+  for (int i = tid; i < E; i += threads) a.counts[static_cast<int64_t>(blockIdx.x) * E + i] = s_count[i];
 }
 
 // Places: what lower experts and earlier CTAs hold is added to every edge's place.
@@ -428,7 +553,7 @@ __global__ void __launch_bounds__(THREADS) k_router_place(const RouteArgs a, int
     }
   }
   __syncthreads();
-  scan_totals<THREADS>(s_total, E, s_off, s_warp);
+  scan_totals(s_total, E, s_off, s_warp);
   if (mine == 0)
     for (int i = tid; i <= E; i += THREADS) a.offsets[i] = s_off[i];
   for (int i = tid; i < E; i += THREADS) s_before[i] += s_off[i];
@@ -463,7 +588,9 @@ Split split_of(int64_t n, int sms) {
 
 template <int EPL> cudaError_t launch_select(const RouteArgs &a, const Split &sp, cudaStream_t s) {
   constexpr int kThreads = EPL <= 8 ? 1024 : 512;
-  k_router_select<EPL, kThreads><<<sp.ctas, kThreads, 0, s>>>(a, sp.passes, sp.pass);
+  // a few positions: as many warps as they need, and at least eight for the experts' totals
+  const int rows = a.n_tok < sp.pass ? a.n_tok : sp.pass, threads = 32 * rows < 256 ? 256 : 32 * rows;
+  k_router_select<EPL, kThreads><<<sp.ctas, threads < kThreads ? threads : kThreads, 0, s>>>(a, sp.passes, sp.pass);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (sp.ctas == 1 && sp.passes == 1)) return e;
   RouteArgs b = a;
