@@ -120,25 +120,9 @@ template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t taddr,
   else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// 16 bytes from global to shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
-// An arrival that releases what happened before it to the cluster, and an attempt at a wait that acquires it.
-__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+// 16 bytes from global to shared memory, of which `size` are read (the others are zeros).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 
 template <int Q> __device__ __forceinline__ void load_cols(uint32_t at, float (&v)[Q]) {
@@ -350,7 +334,6 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
 #pragma unroll
             for (int k = 0; k < FP4; ++k)
               *reinterpret_cast<uint4 *>(dst + k * 512) = make_uint4(v[i][0][k], v[i][1][k], v[i][2][k], v[i][3][k]);
-            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(filled + 8 * st);
             load(kb0 + i + kAhead, v[i]);
@@ -366,37 +349,36 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
       // clocks each, which bound tiles of many rows at 0.5 PFLOP/s.)
       constexpr int kLag = 2;  // stages between a copy and its arrival
       const int w = warp - kEpiWarps - 2, chunk = lane & 7;
+      // without a row of x every index is out of range: a row of the weights stands in
+      const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.g.n_src > 0 ? p.g.a : p.g.b);
       const uint32_t filled = PAIR && rank ? ready : full;
       uint32_t it = 0, st = 0, phase = 1;
       bool ok = true;
       auto arrive = [&](uint32_t i) {  // this warp's copies of stage i have landed
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(filled + 8 * (i % G::stages));
       };
       for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
-        int idx[16];
+        const __nv_bfloat16 *src[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = 4 * (2 * i + w) + (lane >> 3);
-          idx[i] = r < rows ? __ldg(p.g.rows + row0 + r) : -1;
+          int from = r < rows ? __ldg(p.g.rows + row0 + r) : 0;
+          if (from < 0 || from >= p.g.n_src) from = 0;  // never followed; whatever is read instead, the result is NaN
+          src[i] = base + from * p.g.a_stride + 8 * chunk;
         }
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
           ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
           if (!ok) break;
-          const int k = kb * 64 + 8 * chunk;
-          const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.g.a) + k;
-          const uint32_t dst = ring + st * G::stage;
+          const int size = kb * 64 + 8 * chunk < p.g.K ? 16 : 0;  // zeros behind the last column
+          // rows 8 i + 4 w + lane / 8: the chunk's place in the swizzle is the same in all of them
+          const int r0 = 4 * w + (lane >> 3);
+          const uint32_t dst = ring + st * G::stage + r0 * kRow + ((chunk ^ r0) << 4);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r4 = 4 * (2 * i + w), r = r4 + (lane >> 3);
-            if (r4 >= rows) break;
-            const bool there = idx[i] >= 0 && idx[i] < p.g.n_src && k < p.g.K;  // else zeros
-            copy16(dst + r * kRow + ((chunk ^ (r & 7)) << 4), there ? static_cast<const void *>(src + idx[i] * p.g.a_stride) : p.g.b,
-                   there);
-          }
+          for (int i = 0; i < 16; ++i)
+            if (8 * i < rows) copy16(dst + 8 * i * kRow, src[i] + (size ? kb * 64 : 0), size);
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (it >= kLag) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
@@ -412,7 +394,8 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
       if (ok)
         for (uint32_t i = it > kLag ? it - kLag : 0; i < it; ++i) arrive(i);
     } else if (PAIR && warp == kEpiWarps + 1 && rank == 1) {  // ---------------- the second CTA's helpers, to the first
-      // One warp without accesses of its own releases them to the cluster: a release waits for every access of its warp.
+      // The fence between the helpers' writes and the tensor core's reads waits for every access of its warp, the helpers'
+      // loads ahead among them, so it is a warp without accesses that makes it, here as in the first CTA.
       if (helpers) {
         const uint32_t filled = mapa_shared(full, 0);
         uint32_t st = 0, phase = 0;
@@ -421,7 +404,8 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
           for (int kb = 0; kb < p.kb_n; ++kb) {
             ok = warp_wait(ready + 8 * st, phase, abort, p.err, p.timeout_ns);
             if (!ok) break;
-            if (lane == 0) arrive_release_cluster(filled + 8 * st);
+            fence_proxy_async_smem();
+            if (lane == 0) arrive_cluster(filled + 8 * st);
             __syncwarp();
             if (++st == G::stages) {
               st = 0;
@@ -441,19 +425,9 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
             ok = warp_wait(tempty + 8 * buf, ((seq / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
             if (!ok) break;
           }
-          if constexpr (PAIR) {
-            // the second CTA's helpers wrote its shared memory
-            if (!__all_sync(0xffffffffu, try_wait_cluster(full + 8 * st, phase))) {
-              ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
-              if (!ok) break;
-              // complete by now: this attempt acquires
-              ok = __all_sync(0xffffffffu, try_wait_cluster(full + 8 * st, phase) || try_wait_cluster(full + 8 * st, phase));
-              if (!ok) break;
-            }
-          } else {
-            ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
-            if (!ok) break;
-          }
+          ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
+          if (!ok) break;
+          if (helpers) fence_proxy_async_smem();
           tc_fence_after();
           const uint32_t src = ring + st * G::stage;
           const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kRow);
