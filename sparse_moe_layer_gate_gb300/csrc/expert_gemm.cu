@@ -9,7 +9,7 @@
 //
 // Tiles of 128 rows x 256, 128, 64 or 32 columns, or of 256 x 256 by two CTAs whose tensor cores
 // read both halves of the weights. A producer warp streams 128-byte-wide operand tiles (64 bf16 or
-// 256 e2m1 columns) by TMA through a ring in shared memory, two more warps the gathered rows; an MMA
+// 256 e2m1 columns) by TMA through a ring in shared memory, four more warps the gathered rows; an MMA
 // warp issues the tcgen05 products into TMEM; eight epilogue warps take a finished accumulator into
 // registers, free it, and store under the next tile's products. With swiglu a tile's columns are
 // half gate and half up rows of the weights, so that both halves of an output meet in one thread.
@@ -31,6 +31,11 @@ namespace epoch {
 namespace {
 
 constexpr int kEpiWarps = 8;
+// Four warpgroups: the epilogue's two, one for producer and MMA, and the helpers (4-bit operands: scales; gathered rows).
+// The launch's 128 registers a thread are handed over: 88 to the last two, 168 to the epilogue's, whose values alone
+// take 128 (2 * 88 + 2 * 168 = 4 * 128).
+constexpr int kThreads = 32 * (kEpiWarps + 8);
+constexpr int kRegsLaunch = 128, kRegsFew = 88, kRegsMany = 168;
 constexpr int kRow = 128;  // bytes of an operand row of a stage: one swizzle row
 
 struct ExpertParams {
@@ -68,9 +73,6 @@ template <int FP4, int BN, bool PAIR> struct Tile {
   static constexpr int need = bufs * BN + 4 * place;
   static constexpr int tmem = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
   static constexpr int smem = 1024 + stages * stage;
-  // warpgroups: the epilogue's two, producer and MMA, and one for the scales
-  static constexpr int threads = 32 * (kEpiWarps + (FP4 ? 8 : 4));
-  static constexpr int regs_launch = FP4 ? 128 : 168, regs_few = FP4 ? 88 : 72, regs_many = FP4 ? 168 : 216;
 };
 
 // Shape M x N, fp32 accumulator, both operands K-major.
@@ -176,7 +178,7 @@ template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, i
 }
 
 template <int FP4, int BN, bool PAIR>
-__global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm(const __grid_constant__ ExpertParams p) {
+__global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_constant__ ExpertParams p) {
   using G = Tile<FP4, BN, PAIR>;
   constexpr int Q = BN / 4;                                        // columns of one of a thread's two runs
   extern __shared__ uint8_t smem_raw[];
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
   const uint32_t full = smem_u32(bars), empty = full + 8 * G::stages, tfull = empty + 8 * G::stages,
                  tempty = tfull + 8 * G::bufs, ready = tempty + 8 * G::bufs;
   const bool gather = FP4 == 0 && p.g.rows != nullptr;
-  const int helpers = FP4 ? 1 + G::groups_b : gather ? 2 : 0;  // warps that write a stage beside the copies
+  const int helpers = FP4 ? 1 + G::groups_b : gather ? 4 : 0;  // warps that write a stage beside the copies
   if (warp == 0) {
     if constexpr (PAIR) {
       tmem_alloc_pair(smem_u32(&s_tmem), G::tmem);
@@ -235,9 +237,9 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
   TileWalk walk(s_start, s_cum, p.g.offsets ? p.g.n_groups : 1, p.nt_n, G::bm, rank);
   const int half_n = p.g.N / 2;
 
-  // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 12 .. 15: scales
+  // warps 0 .. 7: epilogue; 8: producer; 9: MMA; 12 .. 15: helpers
   if (warp >= kEpiWarps) {
-    give_registers<G::regs_few>();
+    give_registers<kRegsFew>();
     if (warp == kEpiWarps) {  // ------------------------------------------------ producer
       const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
       const uint64_t wpol = p.reuse ? keep : pass;
@@ -344,11 +346,11 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
           }
         }
       }
-    } else if (FP4 == 0 && gather && warp >= kEpiWarps + 2) {  // gathered rows, every other four of them a warp
+    } else if (FP4 == 0 && gather && warp >= kEpiWarps + 4) {  // gathered rows, every fourth four of them a warp
       // Eight lanes copy an operand row in the 128-byte swizzle. (Copies of four rows an instruction by TMA took 80
       // clocks each, which bound tiles of many rows at 0.5 PFLOP/s.)
       constexpr int kLag = 2;  // stages between a copy and its arrival
-      const int w = warp - kEpiWarps - 2, chunk = lane & 7;
+      const int w = warp - kEpiWarps - 4, chunk = lane & 7;
       // without a row of x every index is out of range: a row of the weights stands in
       const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.g.n_src > 0 ? p.g.a : p.g.b);
       const uint32_t filled = PAIR && rank ? ready : full;
@@ -361,10 +363,10 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
       for (int t = cta; ok && t < walk.total; t += ctas) {
         int e, row0, rows, nt;
         walk.at(t, &e, &row0, &rows, &nt);
-        const __nv_bfloat16 *src[16];
+        const __nv_bfloat16 *src[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = 4 * (2 * i + w) + (lane >> 3);
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * (4 * i + w) + (lane >> 3);
           int from = r < rows ? __ldg(p.g.rows + row0 + r) : 0;
           if (from < 0 || from >= p.g.n_src) from = 0;  // never followed; whatever is read instead, the result is NaN
           src[i] = base + from * p.g.a_stride + 8 * chunk;
@@ -373,12 +375,12 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
           ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
           if (!ok) break;
           const int size = kb * 64 + 8 * chunk < p.g.K ? 16 : 0;  // zeros behind the last column
-          // rows 8 i + 4 w + lane / 8: the chunk's place in the swizzle is the same in all of them
+          // rows 16 i + 4 w + lane / 8: the chunk's place in the swizzle is the same in all of them
           const int r0 = 4 * w + (lane >> 3);
-          const uint32_t dst = ring + st * G::stage + r0 * kRow + ((chunk ^ r0) << 4);
+          const uint32_t dst = ring + st * G::stage + r0 * kRow + ((chunk ^ (r0 & 7)) << 4);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (8 * i < rows) copy16(dst + 8 * i * kRow, src[i] + (size ? kb * 64 : 0), size);
+          for (int i = 0; i < 8; ++i)
+            if (16 * i < rows) copy16(dst + 16 * i * kRow, src[i] + (size ? kb * 64 : 0), size);
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (it >= kLag) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(Tile<FP4, BN, PAIR>::threads, 1) k_expert_gemm
       }
     }
   } else {  // ------------------------------------------------------------------ epilogue
-    take_registers<G::regs_many>();
+    take_registers<kRegsMany>();
     const uint32_t read = PAIR ? mapa_shared(tempty, 0) : tempty;  // the barriers that the MMA thread waits on
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 32, half of the columns
     const bool swiglu = p.g.swiglu != 0, bf16 = p.g.out_bf16 != 0, wide = p.wide != 0;
@@ -576,7 +578,7 @@ template <int FP4, int BN, bool PAIR> cudaError_t launch_tile(ExpertParams &p, c
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(G::threads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = G::smem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -588,7 +590,7 @@ template <int FP4, int BN, bool PAIR> cudaError_t launch_tile(ExpertParams &p, c
       e = cudaFuncGetAttributes(&fa, fn);
       if (e != cudaSuccess) return e;
       // the warpgroups hand registers over within what the launch holds
-      if (fa.numRegs < G::regs_launch) return cudaErrorInvalidConfiguration;
+      if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
       e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
       if (e != cudaSuccess) return e;
       int n = num_sms();

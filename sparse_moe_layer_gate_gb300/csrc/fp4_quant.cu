@@ -11,6 +11,10 @@
 // by the remainder's sign. A block that holds a NaN or an infinity gets a NaN scale, so that every
 // product with it is NaN. Scales lie by blocks of 256 columns, [ceil(K / 256)][rows][16 or 8], with
 // zeros behind the last column.
+#include <cmath>
+
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "layer.h"
 
@@ -20,8 +24,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sixteen consecutive elements from a 16-byte boundary on.
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
+// Sixteen consecutive elements from a 16-byte boundary on, and the bits of their largest magnitude.
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16], unsigned &m) {
   uint4 u[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -29,23 +33,34 @@ __device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
                  : "=r"(u[h].x), "=r"(u[h].y), "=r"(u[h].z), "=r"(u[h].w)
                  : "l"(p + 8 * h));
   const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  uint32_t big = 0;  // largest magnitudes of the low and of the high halves
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    big = __vmaxu2(big, w[i] & 0x7FFF7FFFu);
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+  m = max(big << 16, big & 0xFFFF0000u);
 }
-__device__ __forceinline__ void load16(const float *p, float (&v)[16]) {
+__device__ __forceinline__ unsigned largest(const float (&v)[16]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+__device__ __forceinline__ void load16(const float *p, float (&v)[16], unsigned &m) {
 #pragma unroll
   for (int h = 0; h < 4; ++h)
     asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
                  : "l"(p + 4 * h));
+  m = largest(v);
 }
 // The same at any alignment.
-template <typename T> __device__ __forceinline__ void load16_any(const T *p, float (&v)[16]) {
+template <typename T> __device__ __forceinline__ void load16_any(const T *p, float (&v)[16], unsigned &m) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = to_f32(p[i]);
+  m = largest(v);
 }
 
 // Eight values to e2m1 (round to nearest even, out of range to the largest), the first in the lowest four bits.
@@ -78,11 +93,10 @@ __device__ __forceinline__ uint32_t nv_scale(float m, float *s) {
   return b;
 }
 
-// Codes of v / s. Quotients are taken to twelve bits, which leaves every border between codes (three bits) as it is
-// and, where v has eight bits (EXACT false), keeps all others on their side of it: v and a border times s differ by
-// 2^-8 or more of them. EXACT: a quotient that landed on a border moves off it by the sign of its remainder.
-template <bool EXACT> __device__ __forceinline__ void nv_codes(const float (&v)[16], float s, uint32_t (&q)[2]) {
-  const float inv = 1.0f / s;
+// Codes of v / s, inv = 1 / s. Quotients are taken to twelve bits, which leaves every border between codes (three bits)
+// as it is and, where v has eight bits (EXACT false), keeps all others on their side of it: v and a border times s
+// differ by 2^-8 or more of them. EXACT: a quotient that landed on a border moves off it by the sign of its remainder.
+template <bool EXACT> __device__ __forceinline__ void nv_codes(const float (&v)[16], float s, float inv, uint32_t (&q)[2]) {
   float t[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -99,14 +113,13 @@ template <bool EXACT> __device__ __forceinline__ void nv_codes(const float (&v)[
 }
 
 // Sixteen columns a thread; sixteen threads take a block of 256 columns of a row and a CTA sixteen
-// such blocks in order. ALIGNED: pieces start on 16-byte boundaries.
-template <typename T, bool NV, bool SWIGLU, bool ALIGNED>
+// such blocks in order. ALIGNED: pieces start on 16-byte boundaries. EXACT: see nv_codes (else the tensor scale is a
+// power of two and goes into the factor of the quotients).
+template <typename T, bool NV, bool SWIGLU, bool ALIGNED, bool EXACT>
 __global__ void __launch_bounds__(kThreads) k_fp4_quant(const Fp4QuantArgs a, unsigned kb_n) {
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / 16);
-  const int64_t row0 = first / kb_n;
-  const unsigned at = static_cast<unsigned>(first - row0 * kb_n) + (threadIdx.x >> 4), r = at / kb_n;
-  const int64_t row = row0 + r;
-  const unsigned kb = at - r * kb_n, piece = threadIdx.x & 15u;
+  const unsigned at = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);  // blocks of 256 columns: less than 2^31 + 16
+  const int64_t row = at / kb_n;
+  const unsigned kb = at - static_cast<unsigned>(row) * kb_n, piece = threadIdx.x & 15u;
   const int c = static_cast<int>(kb * 256 + piece * 16);
   const bool on = row < a.n_rows, in = on && c < a.cols;
   int64_t src = row, mat = 0;
@@ -117,33 +130,36 @@ __global__ void __launch_bounds__(kThreads) k_fp4_quant(const Fp4QuantArgs a, un
   for (int i = 0; i < 16; ++i) v[i] = 0.f;
   float inv = a.inv_scale;
   if (a.amax != nullptr && on) {
-    mat = row / a.mat_rows;
+    mat = static_cast<unsigned>(row) / static_cast<unsigned>(a.mat_rows);
     inv = 1.0f / fp4_tensor_scale(a.amax[mat]);
   }
+  unsigned m = 0;
   if (in && !bad) {
     const T *p = static_cast<const T *>(a.x) + src * a.x_stride + c;
-    if constexpr (ALIGNED) load16(p, v);
-    else load16_any(p, v);
+    if constexpr (ALIGNED) load16(p, v, m);
+    else load16_any(p, v, m);
     if constexpr (SWIGLU) {
       float u[16];
-      if constexpr (ALIGNED) load16(p + a.cols, u);
-      else load16_any(p + a.cols, u);
+      unsigned unused;
+      if constexpr (ALIGNED) load16(p + a.cols, u, unused);
+      else load16_any(p + a.cols, u, unused);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = silu(v[i]) * u[i];
+      m = largest(v);
     }
-  }
-  unsigned m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if constexpr (NV) v[i] *= inv;
-    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   }
   uint32_t q[2], code;
   if constexpr (NV) {
     float s;
-    code = nv_scale(__uint_as_float(m < 0x7F800000u ? m : 0u), &s);
-    if (m >= 0x7F800000u || bad) code = 0x7Fu;
-    nv_codes<sizeof(T) == 4 || SWIGLU>(v, s, q);
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] *= inv;
+      m = largest(v);
+    }
+    const bool spoilt = m >= 0x7F800000u;
+    code = nv_scale(spoilt ? 0.f : EXACT ? __uint_as_float(m) : __uint_as_float(m) * inv, &s);
+    if (spoilt || bad) code = 0x7Fu;
+    nv_codes<EXACT>(v, s, EXACT ? 1.0f / s : 1.0f / s * inv, q);
   } else {
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     // floor(log2 m) - 2, biased by 127: the exponent field less two, for subnormal m the least
@@ -173,10 +189,10 @@ template <typename T, bool ALIGNED> __global__ void __launch_bounds__(kThreads) 
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 16; i < count;
        i += static_cast<int64_t>(gridDim.x) * kThreads * 16) {
     float v[16];
-    if constexpr (ALIGNED) load16(p + i, v);
-    else load16_any(p + i, v);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    unsigned here;
+    if constexpr (ALIGNED) load16(p + i, v, here);
+    else load16_any(p + i, v, here);
+    m = max(m, here);
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane_id() == 0) s_max[warp_id()] = m;
@@ -195,14 +211,12 @@ __global__ void k_fp4_tensor_scales(uint32_t *amax, int n, int nv) {
 // Sixteen columns a thread, in the order of k_fp4_quant.
 template <typename T, bool NV>
 __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a, unsigned kb_n) {
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / 16);
-  const int64_t row0 = first / kb_n;
-  const unsigned at = static_cast<unsigned>(first - row0 * kb_n) + (threadIdx.x >> 4), r = at / kb_n;
-  const int64_t row = row0 + r;
-  const unsigned kb = at - r * kb_n, piece = threadIdx.x & 15u;
+  const unsigned at = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);  // blocks of 256 columns: less than 2^31 + 16
+  const int64_t row = at / kb_n;
+  const unsigned kb = at - static_cast<unsigned>(row) * kb_n, piece = threadIdx.x & 15u;
   const int c = static_cast<int>(kb * 256 + piece * 16);
   if (row >= a.n_rows || c >= a.cols) return;
-  const int64_t mat = row / a.mat_rows, i = row - mat * a.mat_rows;
+  const int64_t mat = static_cast<unsigned>(row) / static_cast<unsigned>(a.mat_rows), i = row - mat * a.mat_rows;
   constexpr int kPer = NV ? 16 : 8;
   const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.q + (row * a.cols + c) / 2));
   const uint32_t b = __ldg(a.scales + ((mat * kb_n + kb) * a.mat_rows + i) * kPer + (NV ? piece : piece >> 1));
@@ -218,11 +232,22 @@ __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a
   s *= a.group_scale ? a.scale * __ldg(a.group_scale + mat) : a.scale;
   float v[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t n = ((j < 8 ? q.x : q.y) >> (4 * (j & 7))) & 15u, e = (n >> 1) & 3u, f = n & 1u;
-    // e2m1: bias 1; e = 0: f / 2
-    const float x = e ? __uint_as_float(((e + 126u) << 23) | (f << 22)) : 0.5f * static_cast<float>(f);
-    v[j] = (n & 8u ? -x : x) * s;
+  for (int h = 0; h < 2; ++h) {
+    uint32_t p[4];  // pairs in fp16, which holds e2m1's values
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(h ? q.y : q.x));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[j]));
+      v[8 * h + 2 * j] = f.x * s;
+      v[8 * h + 2 * j + 1] = f.y * s;
+    }
   }
   T *out = static_cast<T *>(a.out) + row * a.out_stride + c;
   if (a.wide) {
@@ -246,15 +271,26 @@ __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a
   }
 }
 
-template <typename T, bool NV, bool SWIGLU> cudaError_t launch_one(const Fp4QuantArgs &a, bool aligned, cudaStream_t s) {
+template <typename T, bool NV, bool SWIGLU, bool EXACT> cudaError_t launch_one(const Fp4QuantArgs &a, bool aligned, cudaStream_t s) {
   const int64_t kb = (a.cols + 255) / 256, grid = (a.n_rows * kb + kThreads / 16 - 1) / (kThreads / 16);
-  if (aligned) k_fp4_quant<T, NV, SWIGLU, true><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(kb));
-  else k_fp4_quant<T, NV, SWIGLU, false><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(kb));
+  const unsigned g = static_cast<unsigned>(grid), k = static_cast<unsigned>(kb);
+  if (aligned) k_fp4_quant<T, NV, SWIGLU, true, EXACT><<<g, kThreads, 0, s>>>(a, k);
+  else k_fp4_quant<T, NV, SWIGLU, false, EXACT><<<g, kThreads, 0, s>>>(a, k);
   return cudaGetLastError();
 }
+// Whether dividing by t only moves exponents (and the quotient's factor 1 / s / t stays in range).
+bool power_of_two(float inv) {
+  int e;
+  return std::frexp(inv, &e) == 0.5f && e > -100 && e < 100;
+}
 template <typename T> cudaError_t launch_type(const Fp4QuantArgs &a, bool nv, bool aligned, cudaStream_t s) {
-  if (a.swiglu) return nv ? launch_one<T, true, true>(a, aligned, s) : launch_one<T, false, true>(a, aligned, s);
-  return nv ? launch_one<T, true, false>(a, aligned, s) : launch_one<T, false, false>(a, aligned, s);
+  if (!nv) return a.swiglu ? launch_one<T, false, true, true>(a, aligned, s) : launch_one<T, false, false, true>(a, aligned, s);
+  if (a.swiglu) return launch_one<T, true, true, true>(a, aligned, s);
+  if constexpr (sizeof(T) == 2) {
+    // (a matrix's own scale may be any power of two)
+    if (a.amax == nullptr && power_of_two(a.inv_scale)) return launch_one<T, true, false, false>(a, aligned, s);
+  }
+  return launch_one<T, true, false, true>(a, aligned, s);
 }
 
 }  // namespace

@@ -56,29 +56,36 @@ template <int EPL> __device__ __forceinline__ void row_logits(const void *row, b
   for (int c = 0; c < EPL; ++c) v[c] = e0 + c < E ? logit(row, bf16, e0 + c) : -INFINITY;
 }
 
+// Unsigned key with the order of a number: -0 as +0, above the keys of -inf and of negative NaNs (at most kLowest) and
+// below those of positive NaNs (above kHighest).
+constexpr unsigned kLowest = 0x007FFFFFu, kHighest = 0xFF800000u;  // of -inf and of inf
+__device__ __forceinline__ unsigned number_key(float v) {
+  const int b = __float_as_int(v + 0.0f);
+  return static_cast<unsigned>(b ^ ((b >> 31) | static_cast<int>(0x80000000u)));
+}
+
 // The k best of the warp's entries, lane l owning the EPL consecutive ids from l * EPL on: key 0 is no entry, equal
 // keys go by lower id. Lane j < k gets entry j (id -1: there is none). `scratch`: 32 entries of the warp's own.
 //
-// The k-th best of the lanes' best keys bounds the k best entries from below: only entries at or above it are ranked
-// against one another, one a lane. Each of both rankings is k rounds of a warp maximum, some 15 instructions in all a
-// round, where comparing every pair of lanes took 200.
+// The k-th best of the lanes' best keys (of their different values: a bound that may be lower, not higher) bounds the
+// k best entries from below: only entries at or above it, some ten, are ranked against one another, one a lane.
 template <int EPL>
 __device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2 *scratch, int *id, unsigned *val) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = lane_id();
-  unsigned left = key[0], bound = 0u;
+  unsigned left = key[0], bound = 1u;
 #pragma unroll
   for (int c = 1; c < EPL; ++c) left = max(left, key[c]);
-#pragma unroll 1
+#pragma unroll 4
   for (int j = 0; j < k; ++j) {
-    bound = __reduce_max_sync(kAll, left);
-    if (bound == 0u) break;  // fewer than k lanes hold an entry: all entries count
-    const unsigned hold = __ballot_sync(kAll, left == bound);
-    if (lane == __ffs(hold) - 1) left = 0u;
+    const unsigned m = __reduce_max_sync(kAll, left);
+    bound = max(m, 1u);  // 0: fewer than k different lane bests, all entries count
+    if (left == m) left = 0u;
   }
-  int n = 0;
+  unsigned pass = 0u;
 #pragma unroll
-  for (int c = 0; c < EPL; ++c) n += key[c] >= bound && key[c] != 0u;
+  for (int c = 0; c < EPL; ++c) pass |= key[c] >= bound ? 1u << c : 0u;
+  const int n = __popc(pass);
   int sum = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -94,28 +101,22 @@ __device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2
     if (*id >= 0) *val = order_key(v);
     return;
   }
-  int at = sum - n;
+  uint2 *to = scratch + (sum - n);
 #pragma unroll
   for (int c = 0; c < EPL; ++c)
-    if (key[c] >= bound && key[c] != 0u) scratch[at++] = make_uint2(key[c], static_cast<unsigned>(lane * EPL + c));
+    if ((pass >> c) & 1u) *to++ = make_uint2(key[c], static_cast<unsigned>(lane * EPL + c));
   __syncwarp();
-  const uint2 mine = lane < total ? scratch[lane] : make_uint2(0u, 0u);  // ascending ids
-  __syncwarp();
-  left = mine.x;
-  int rank = 32;
-  const int rounds = min(k, total);
-#pragma unroll 1
-  for (int j = 0; j < rounds; ++j) {
-    const unsigned m = __reduce_max_sync(kAll, left);
-    const unsigned hold = __ballot_sync(kAll, left == m);
-    if (lane == __ffs(hold) - 1) {
-      left = 0u;
-      rank = j;
-    }
+  const uint2 mine = scratch[lane < total ? lane : 0];  // ascending ids
+  int rank = 0;
+#pragma unroll 4
+  for (int i = 0; i < total; ++i) {
+    const unsigned o = scratch[i].x;
+    rank += o > mine.x || (o == mine.x && i < lane);
   }
-  if (rank < 32) scratch[rank] = mine;
   __syncwarp();
-  if (lane < rounds) {
+  if (lane < total) scratch[rank] = mine;
+  __syncwarp();
+  if (lane < min(k, total)) {
     *id = static_cast<int>(scratch[lane].y);
     *val = scratch[lane].x;
   }
@@ -307,10 +308,10 @@ template <int EPL> __device__ __forceinline__ bool limit_groups(unsigned (&key)[
 }
 
 // One position by one warp: lane j < top_k gets its expert (-1: none) and weight. `eligible` has a bit for each of the
-// lane's experts.
+// lane's experts, bias their biases.
 template <int EPL>
-__device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool vec, unsigned eligible, uint2 *scratch,
-                                          int *sel_out, float *w_out) {
+__device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool vec, unsigned eligible, const float (&bias)[EPL],
+                                          uint2 *scratch, int *sel_out, float *w_out) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = lane_id(), k = a.top_k;
   float v[EPL];
@@ -318,18 +319,32 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool ve
   const bool bf16 = a.bf16 != 0;
   const void *row = static_cast<const uint8_t *>(a.logits) + t * a.logits_stride * (bf16 ? 2 : 4);
   row_logits<EPL>(row, bf16, a.n_experts, vec, v);
-  bool nan = false;
+  unsigned low = 0xffffffffu, high = 0u;
 #pragma unroll
   for (int c = 0; c < EPL; ++c) {
-    if (v[c] == -INFINITY) can &= ~(1u << c);
-    nan = nan || v[c] != v[c];
+    key[c] = number_key(v[c]);
+    low = min(low, key[c]);
+    high = max(high, key[c]);
+  }
+  // -inf (behind the last expert too), NaN and masks are rare in a lane of whole experts
+  bool nan = false;
+  if (!__all_sync(kAll, low > kLowest && high <= kHighest && eligible == (EPL == 32 ? 0xffffffffu : (1u << (EPL & 31)) - 1u))) {
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) {
+      if (key[c] < kLowest || key[c] > kHighest) {  // a NaN ranks with -inf, but can be selected
+        nan = true;
+        key[c] = kLowest;
+      } else if (key[c] == kLowest) {
+        can &= ~(1u << c);
+      }
+      if (!((can >> c) & 1u)) key[c] = 0u;
+    }
+    nan = __any_sync(kAll, nan);
   }
   int sel;
   unsigned val;
   float w;
   if (!a.sigmoid) {
-#pragma unroll
-    for (int c = 0; c < EPL; ++c) key[c] = (can >> c) & 1u ? order_key(v[c]) : 0u;
     best_of<EPL>(key, k, scratch, &sel, &val);
     const bool on = sel >= 0;
     const float g = key_value(val);
@@ -351,9 +366,9 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool ve
   } else {
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
-      const int e = lane * EPL + q;
-      v[q] = sigmoid_near(v[q]) + (a.bias != nullptr && e < a.n_experts ? __ldg(a.bias + e) : 0.f);
-      key[q] = (can >> q) & 1u ? order_key(v[q]) : 0u;
+      v[q] = sigmoid_near(v[q]) + bias[q];
+      const unsigned place = number_key(v[q]);
+      key[q] = key[q] == 0u ? 0u : place < kLowest || place > kHighest ? kLowest : place;
     }
     bool sure = a.topk_group >= a.n_group || limit_groups<EPL>(key, a);
     if (sure) {
@@ -400,7 +415,7 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool ve
       w = sel >= 0 ? w / sum : 0.f;
     }
   }
-  if (__any_sync(kAll, nan) && sel >= 0) w = __uint_as_float(0x7FC00000u);  // a NaN among a position's logits spoils its weights
+  if (nan && sel >= 0) w = __uint_as_float(0x7FC00000u);  // a NaN among a position's logits spoils its weights
   *sel_out = sel;
   *w_out = w;
 }
@@ -451,10 +466,12 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
     for (int w = 0; w < words; ++w) s_bits[w][i] = 0u;
   }
   unsigned eligible = 0u;
+  float bias[EPL];
 #pragma unroll
   for (int c = 0; c < EPL; ++c) {
     const int e = lane * EPL + c;
     if (e < E && (a.eligible == nullptr || __ldg(a.eligible + e) != 0)) eligible |= 1u << c;
+    bias[c] = e < E && a.bias != nullptr ? __ldg(a.bias + e) : 0.f;
   }
   const int64_t first = static_cast<int64_t>(blockIdx.x) * passes * pass;
   pdl_trigger();
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       const int64_t t = t0 + r;
       int e = -1;
       float w = 0.f;
-      if (a.live == nullptr || __ldg(a.live + t) != 0) route_row<EPL>(a, t, vec, eligible, s_scratch[warp], &e, &w);
+      if (a.live == nullptr || __ldg(a.live + t) != 0) route_row<EPL>(a, t, vec, eligible, bias, s_scratch[warp], &e, &w);
       if (lane < k) {
         a.sel[t * k + lane] = e;
         a.weights[t * k + lane] = w;
