@@ -26,34 +26,43 @@ constexpr int kPass = 128;  // most positions of a CTA's pass
 __device__ __forceinline__ float logit(const void *row, bool bf16, int e) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]) : __ldg(static_cast<const float *>(row) + e);
 }
-// logits of a lane's EPL consecutive experts; -inf behind the last. vec: rows start on 16-byte boundaries.
-template <int EPL> __device__ __forceinline__ void row_logits(const void *row, bool bf16, int E, bool vec, float (&v)[EPL]) {
+// A lane's EPL consecutive logits as they lie in memory, so that a row's loads can be on their way while the row before
+// is ranked: fp32 bits, or with whole vectors of bf16 pairs in the first half. vec: rows start on 16-byte boundaries.
+template <int EPL> struct Raw {
+  uint32_t w[EPL];
+};
+template <int EPL> __device__ __forceinline__ bool whole(bool vec, int E) { return EPL % 8 == 0 && vec && lane_id() * EPL + EPL <= E; }
+template <int EPL> __device__ __forceinline__ void load_raw(const void *row, bool bf16, int E, bool vec, Raw<EPL> &r) {
   const int e0 = lane_id() * EPL;
   if constexpr (EPL % 8 == 0) {
-    if (vec && e0 + EPL <= E) {
+    if (whole<EPL>(vec, E)) {
       if (bf16) {
 #pragma unroll
         for (int q = 0; q < EPL / 8; ++q) {
           const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(row) + e0) + q);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[8 * q + 2 * i] = __uint_as_float(w[i] << 16);
-            v[8 * q + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-          }
+          r.w[4 * q] = u.x, r.w[4 * q + 1] = u.y, r.w[4 * q + 2] = u.z, r.w[4 * q + 3] = u.w;
         }
       } else {
 #pragma unroll
         for (int q = 0; q < EPL / 4; ++q) {
-          const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e0) + q);
-          v[4 * q] = a.x, v[4 * q + 1] = a.y, v[4 * q + 2] = a.z, v[4 * q + 3] = a.w;
+          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(row) + e0) + q);
+          r.w[4 * q] = u.x, r.w[4 * q + 1] = u.y, r.w[4 * q + 2] = u.z, r.w[4 * q + 3] = u.w;
         }
       }
       return;
     }
   }
 #pragma unroll
-  for (int c = 0; c < EPL; ++c) v[c] = e0 + c < E ? logit(row, bf16, e0 + c) : -INFINITY;
+  for (int c = 0; c < EPL; ++c) r.w[c] = e0 + c < E ? __float_as_uint(logit(row, bf16, e0 + c)) : 0xFF800000u;  // -inf behind the last
+}
+template <int EPL> __device__ __forceinline__ void open_raw(const Raw<EPL> &r, bool bf16, int E, bool vec, float (&v)[EPL]) {
+  if (bf16 && whole<EPL>(vec, E)) {
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) v[c] = __uint_as_float(c & 1 ? r.w[c / 2] & 0xFFFF0000u : r.w[c / 2] << 16);
+  } else {
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) v[c] = __uint_as_float(r.w[c]);
+  }
 }
 
 // Unsigned key with the order of a number: -0 as +0, above the keys of -inf and of negative NaNs (at most kLowest) and
@@ -65,22 +74,28 @@ __device__ __forceinline__ unsigned number_key(float v) {
 }
 
 // The k best of the warp's entries, lane l owning the EPL consecutive ids from l * EPL on: key 0 is no entry, equal
-// keys go by lower id. Lane j < k gets entry j (id -1: there is none). `scratch`: 32 entries of the warp's own.
+// keys go by lower id. Entry j < k ends up in scratch[j] (.x the key, .y the id; 0 and -1 where there is none).
+// `scratch`: 32 entries of the warp's own.
 //
-// The k-th best of the lanes' best keys (of their different values: a bound that may be lower, not higher) bounds the
-// k best entries from below: only entries at or above it, some ten, are ranked against one another, one a lane.
+// The k-th of the best keys of half lanes (of their different values: a bound that may be lower, not higher) bounds the
+// k best entries from below: only entries at or above it, some ten, are ranked against one another, one a lane. (By whole
+// lanes' bests half of the experts in half of the lanes, as the group rule leaves them, let twice as many through.)
 template <int EPL>
-__device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2 *scratch, int *id, unsigned *val) {
+__device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2 *scratch) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = lane_id();
-  unsigned left = key[0], bound = 1u;
+  unsigned lo = 0u, hi = 0u, bound = 1u;  // bests of the lane's two halves
 #pragma unroll
-  for (int c = 1; c < EPL; ++c) left = max(left, key[c]);
+  for (int c = 0; c < EPL / 2; ++c) {
+    lo = max(lo, key[c]);
+    hi = max(hi, key[EPL / 2 + c]);
+  }
 #pragma unroll 4
   for (int j = 0; j < k; ++j) {
-    const unsigned m = __reduce_max_sync(kAll, left);
-    bound = max(m, 1u);  // 0: fewer than k different lane bests, all entries count
-    if (left == m) left = 0u;
+    const unsigned m = __reduce_max_sync(kAll, max(lo, hi));
+    bound = max(m, 1u);  // 0: fewer than k different bests, all entries count
+    if (lo == m) lo = 0u;
+    if (hi == m) hi = 0u;
   }
   unsigned pass = 0u;
 #pragma unroll
@@ -93,12 +108,12 @@ __device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2
     if (lane >= o) sum += y;
   }
   const int total = __shfl_sync(kAll, sum, 31);
-  *id = -1;
-  *val = 0u;
-  if (total > 32) {  // many equal keys, or k lanes with several of the best
+  if (__any_sync(kAll, total > 32)) {  // many equal keys, or k lanes with several of the best
+    int id = -1;
     float v;
-    warp_topk_rounds<EPL>(key, k, id, &v);
-    if (*id >= 0) *val = order_key(v);
+    warp_topk_rounds<EPL>(key, k, &id, &v);
+    scratch[lane] = make_uint2(id >= 0 ? order_key(v) : 0u, static_cast<unsigned>(id));
+    __syncwarp();
     return;
   }
   uint2 *to = scratch + (sum - n);
@@ -115,11 +130,7 @@ __device__ __forceinline__ void best_of(const unsigned (&key)[EPL], int k, uint2
   }
   __syncwarp();
   if (lane < total) scratch[rank] = mine;
-  __syncwarp();
-  if (lane < min(k, total)) {
-    *id = static_cast<int>(scratch[lane].y);
-    *val = scratch[lane].x;
-  }
+  else scratch[lane] = make_uint2(0u, 0xffffffffu);
   __syncwarp();
 }
 
@@ -131,6 +142,10 @@ __device__ __forceinline__ unsigned long long order_exact(double v) {
   if (v != v) v = -INFINITY;
   const long long b = __double_as_longlong(v + 0.0);
   return static_cast<unsigned long long>(b < 0 ? ~b : b | static_cast<long long>(1ull << 63));
+}
+__device__ __forceinline__ double value_exact(unsigned long long key) {  // 0 for none
+  const long long b = static_cast<long long>(key);
+  return key ? __longlong_as_double(b < 0 ? b & 0x7FFFFFFFFFFFFFFFll : ~b) : 0.0;
 }
 // Largest of the warp's keys (0: none) and the lowest lane that holds it.
 __device__ __forceinline__ unsigned long long warp_best(unsigned long long v, int *lane) {
@@ -185,11 +200,7 @@ template <int EPL> __device__ __noinline__ int select_exact(const RouteArgs &a, 
       n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
       int win, unused;
       const unsigned long long m1 = warp_best(k1, &win), m2 = warp_best(lane == win ? k2 : k1, &unused);
-      auto value = [](unsigned long long v) {
-        const long long b = static_cast<long long>(v);
-        return v ? __longlong_as_double(b < 0 ? b & 0x7FFFFFFFFFFFFFFFll : ~b) : 0.0;
-      };
-      if (lane == i) score = value(m1) + value(m2), held = n;
+      if (lane == i) score = value_exact(m1) + value_exact(m2), held = n;
     }
     int rank = 0, before = 0;
 #pragma unroll 1
@@ -222,61 +233,136 @@ template <int EPL> __device__ __noinline__ int select_exact(const RouteArgs &a, 
 }
 
 // sigmoid in fp32 for the selection, off by less than 4e-7: the exponential's 2 + 1.2 |g| steps of 2^-23 reach the
-// result by s (1 - s) of them (less than one step), the sum's and the quotient's 2 steps and a half by s.
-__device__ __forceinline__ float sigmoid_near(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// result by s (1 - s) of them (less than one step), the sum's and the reciprocal's 2 steps and a half by s.
+__device__ __forceinline__ float sigmoid_near(float g) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return s;
+}
 // Whether two selection scores are apart whatever fp32 made of them: sigmoid as above, the sum with the bias half a
 // step of the result. Groups' scores are sums of two: twice that.
 __device__ __forceinline__ float reach(float a, float b) { return 1.2e-6f + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)); }
 __device__ __forceinline__ bool apart(float a, float b) { return fabsf(a - b) > reach(a, b); }
 __device__ __forceinline__ bool groups_apart(float a, float b) { return fabsf(a - b) > 2.0f * reach(a, b); }
 
-// The groups that a position may search (clears keys outside them); false where fp32 cannot tell. Where a lane's
-// experts are of one group and a group is 2^i lanes, its lanes merge their two best; else every group is looked for
-// in all lanes.
-template <int EPL> __device__ __forceinline__ bool limit_groups(unsigned (&key)[EPL], const RouteArgs &a) {
+// Ids of the entries that lanes have marked (bits of their EPL), in ascending order one a lane from scratch on; how many
+// there are, of which at most 32 fit.
+template <int EPL> __device__ __forceinline__ int gather_marked(unsigned marked, uint2 *scratch) {
+  const int lane = lane_id(), n = __popc(marked);
+  int sum = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, sum, 31);
+  __syncwarp();
+  if (__all_sync(0xffffffffu, total <= 32)) {
+    int to = sum - n;
+#pragma unroll
+    for (int q = 0; q < EPL; ++q)
+      if ((marked >> q) & 1u) scratch[to++].y = static_cast<unsigned>(lane * EPL + q);
+  }
+  __syncwarp();
+  return total;
+}
+
+// The topk_group best groups (a bit each) by the entries that could be one of their two best, at most one a lane, in 64
+// bits. Every expert is an entry.
+__device__ __noinline__ unsigned groups_exact(const RouteArgs &a, const void *row, int e, int gs) {
+  const int lane = lane_id(), mine = e >= 0 ? e / gs : -1;
+  const unsigned long long key = e >= 0 ? order_exact(score_exact(a, logit(row, a.bf16 != 0, e), e)) : 0ull;
+  unsigned long long score = 0ull;  // lane i: group i's, as a key
+#pragma unroll 1
+  for (int i = 0; i < a.n_group; ++i) {
+    const unsigned long long v = mine == i ? key : 0ull;
+    int win, unused;
+    const unsigned long long m1 = warp_best(v, &win), m2 = warp_best(lane == win ? 0ull : v, &unused);
+    if (lane == i) score = order_exact(value_exact(m1) + value_exact(m2));
+  }
+  unsigned chosen = 0u;
+#pragma unroll 1
+  for (int i = 0; i < a.topk_group; ++i) {
+    int win;
+    warp_best(score, &win);  // the lowest of equal ones
+    chosen |= 1u << win;
+    if (lane == win) score = 0ull;
+  }
+  return chosen;
+}
+
+// limit_groups for a position whose every expert is an entry: a group is 2^i lanes (`span`), whose two best are merged.
+template <int EPL>
+__device__ __forceinline__ bool limit_groups_fast(unsigned (&key)[EPL], const RouteArgs &a, int span, const void *row, uint2 *scratch) {
   constexpr unsigned kAll = 0xffffffffu;
-  const int lane = lane_id(), gs = a.n_experts / a.n_group, span = gs / EPL;  // span: lanes of a group
-  const bool aligned = gs % EPL == 0 && (span & (span - 1)) == 0;
-  float score = -INFINITY;  // lane i: group i's
-  int held = 0;
-  if (aligned) {
-    unsigned k1 = 0u, k2 = 0u, n = 0u;
+  const int lane = lane_id(), shift = 31 - __clz(span);
+  unsigned k1 = key[0], k2 = 0u;
+#pragma unroll
+  for (int q = 1; q < EPL; ++q) {
+    k2 = max(k2, min(k1, key[q]));
+    k1 = max(k1, key[q]);
+  }
+  for (int o = 1; o < span; o <<= 1) {
+    const unsigned o1 = __shfl_xor_sync(kAll, k1, o), o2 = __shfl_xor_sync(kAll, k2, o);
+    k2 = max(max(k2, o2), min(k1, o1));
+    k1 = max(k1, o1);
+  }
+  const float second = key_value(k2);
+  const unsigned mine = number_key(key_value(k1) + second);
+  // rounds of the best group left; equal ones go together (and are then too near, or all chosen)
+  unsigned left = mine, bound = 0u;
+#pragma unroll 4
+  for (int i = 0; i < a.topk_group; ++i) {
+    bound = __reduce_max_sync(kAll, left);
+    if (left == bound) left = 0u;
+  }
+  bool in = mine >= bound;
+  const unsigned high = __reduce_max_sync(kAll, left);
+  if (!__all_sync(kAll, __popc(__ballot_sync(kAll, in)) == a.topk_group << shift &&
+                            (high == 0u || groups_apart(key_value(bound), key_value(high))))) {
+    unsigned near = 0u;
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
-      n += key[q] != 0u;
-      k2 = max(k2, min(k1, key[q]));
-      k1 = max(k1, key[q]);
+      const float v = key_value(key[q]);
+      if (!(v < second && apart(v, second))) near |= 1u << q;
     }
-    for (int o = 1; o < span; o <<= 1) {
-      const unsigned o1 = __shfl_xor_sync(kAll, k1, o), o2 = __shfl_xor_sync(kAll, k2, o);
-      n += __shfl_xor_sync(kAll, n, o);
-      k2 = max(max(k2, o2), min(k1, o1));
-      k1 = max(k1, o1);
-    }
-    const float mine = k1 == 0u ? -INFINITY : k2 == 0u ? key_value(k1) : key_value(k1) + key_value(k2);
-    const int from = lane < a.n_group ? lane * span : 0;
-    score = __shfl_sync(kAll, mine, from);
-    held = static_cast<int>(__shfl_sync(kAll, n, from));
-  } else {
-    for (int i = 0; i < a.n_group; ++i) {
-      unsigned k1 = 0u, k2 = 0u;
-      int n = 0;
-      const int lo = i * gs - lane * EPL, hi = lo + gs;  // the group's entries of this lane
+    const int total = gather_marked<EPL>(near, scratch);
+    if (__any_sync(kAll, total > 32)) return false;
+    const unsigned chosen = groups_exact(a, row, lane < total ? static_cast<int>(scratch[lane].y) : -1, EPL << shift);
+    __syncwarp();
+    in = (chosen >> (lane >> shift)) & 1u;
+  }
+  if (!in)
 #pragma unroll
-      for (int q = 0; q < EPL; ++q) {
-        const unsigned v = q >= lo && q < hi ? key[q] : 0u;
-        n += v != 0u;
-        k2 = max(k2, min(k1, v));
-        k1 = max(k1, v);
-      }
-      const unsigned m1 = __reduce_max_sync(kAll, k1);
-      const unsigned hold = __ballot_sync(kAll, k1 == m1);
-      const unsigned m2 = __reduce_max_sync(kAll, lane == __ffs(hold) - 1 ? k2 : k1);
-      n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
-      if (lane == i) {
-        held = n;
-        score = m1 == 0u ? -INFINITY : m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
-      }
+    for (int q = 0; q < EPL; ++q) key[q] = 0u;
+  return true;
+}
+
+// The groups that a position may search (clears keys outside them); false where fp32 cannot tell.
+template <int EPL> __device__ __noinline__ bool limit_groups(unsigned *key, const RouteArgs &a) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = lane_id(), gs = a.n_experts / a.n_group;
+  float score = -INFINITY;  // lane i: group i's
+  int held = 0;
+  for (int i = 0; i < a.n_group; ++i) {
+    unsigned k1 = 0u, k2 = 0u;
+    int n = 0;
+    const int lo = i * gs - lane * EPL, hi = lo + gs;  // the group's entries of this lane
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) {
+      const unsigned v = q >= lo && q < hi ? key[q] : 0u;
+      n += v != 0u;
+      k2 = max(k2, min(k1, v));
+      k1 = max(k1, v);
+    }
+    const unsigned m1 = __reduce_max_sync(kAll, k1);
+    const unsigned hold = __ballot_sync(kAll, k1 == m1);
+    const unsigned m2 = __reduce_max_sync(kAll, lane == __ffs(hold) - 1 ? k2 : k1);
+    n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
+    if (lane == i) {
+      held = n;
+      score = m1 == 0u ? -INFINITY : m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
     }
   }
   const bool there = lane < a.n_group && held > 0;
@@ -294,31 +380,22 @@ template <int EPL> __device__ __forceinline__ bool limit_groups(unsigned (&key)[
   const unsigned low = __reduce_min_sync(kAll, (chosen >> lane) & 1u ? order_key(score) : 0xffffffffu);
   const unsigned high = __reduce_max_sync(kAll, (others >> lane) & 1u ? order_key(score) : 0u);
   const bool sure = __popc(chosen) <= a.topk_group && (others == 0u || groups_apart(key_value(low), key_value(high)));
-  if (aligned) {
-    // lanes behind the last group hold no entry
-    if (!((chosen >> ((lane / span) & 31)) & 1u))
 #pragma unroll
-      for (int q = 0; q < EPL; ++q) key[q] = 0u;
-  } else {
-#pragma unroll
-    for (int q = 0; q < EPL; ++q)
-      if (!((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) key[q] = 0u;
-  }
+  for (int q = 0; q < EPL; ++q)
+    if (!((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) key[q] = 0u;
   return sure;
 }
 
-// One position by one warp: lane j < top_k gets its expert (-1: none) and weight. `eligible` has a bit for each of the
-// lane's experts, bias their biases.
+// One position by one warp: selection j goes to id[j] (-1: none) and, with the softmax router, its logit to val[j]; stat
+// gets what its weights need besides: the softmax's largest logit and, where they are raw, its sum over all experts;
+// else 0, or NaN where a logit is (which spoils the weights). `eligible` has a bit for each of the lane's experts,
+// bias their biases (up to eight).
 template <int EPL>
-__device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool vec, unsigned eligible, const float (&bias)[EPL],
-                                          uint2 *scratch, int *sel_out, float *w_out) {
+__device__ __forceinline__ void route_row(const RouteArgs &a, const void *row, float (&v)[EPL], unsigned eligible,
+                                          const float (&bias)[EPL], uint2 *scratch, int16_t *id, float *val, float2 *stat) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = lane_id(), k = a.top_k;
-  float v[EPL];
   unsigned key[EPL], can = eligible;
-  const bool bf16 = a.bf16 != 0;
-  const void *row = static_cast<const uint8_t *>(a.logits) + t * a.logits_stride * (bf16 ? 2 : 4);
-  row_logits<EPL>(row, bf16, a.n_experts, vec, v);
   unsigned low = 0xffffffffu, high = 0u;
 #pragma unroll
   for (int c = 0; c < EPL; ++c) {
@@ -327,8 +404,10 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool ve
     high = max(high, key[c]);
   }
   // -inf (behind the last expert too), NaN and masks are rare in a lane of whole experts
-  bool nan = false;
-  if (!__all_sync(kAll, low > kLowest && high <= kHighest && eligible == (EPL == 32 ? 0xffffffffu : (1u << (EPL & 31)) - 1u))) {
+  float spoilt = 0.f;
+  const bool clean = __all_sync(kAll, low > kLowest && high <= kHighest && eligible == (EPL == 32 ? 0xffffffffu : (1u << (EPL & 31)) - 1u));
+  if (!clean) {
+    bool nan = false;
 #pragma unroll
     for (int c = 0; c < EPL; ++c) {
       if (key[c] < kLowest || key[c] > kHighest) {  // a NaN ranks with -inf, but can be selected
@@ -339,85 +418,73 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t t, bool ve
       }
       if (!((can >> c) & 1u)) key[c] = 0u;
     }
-    nan = __any_sync(kAll, nan);
+    if (__any_sync(kAll, nan)) spoilt = __uint_as_float(0x7FC00000u);
   }
-  int sel;
-  unsigned val;
-  float w;
   if (!a.sigmoid) {
-    best_of<EPL>(key, k, scratch, &sel, &val);
-    const bool on = sel >= 0;
-    const float g = key_value(val);
-    float top = key_value(__shfl_sync(kAll, val, 0)), sum;
+    best_of<EPL>(key, k, scratch);
+    if (lane < k) {
+      const uint2 e = scratch[lane];
+      id[lane] = static_cast<int16_t>(e.y);
+      val[lane] = key_value(e.x);
+    }
+    float top = key_value(scratch[0].x), sum = spoilt;
     if (a.raw_weights) {  // probabilities over all experts, eligible or not
       float m = v[0];
 #pragma unroll
       for (int c = 1; c < EPL; ++c) m = fmaxf(m, v[c]);
       top = key_value(__reduce_max_sync(kAll, order_key(m)));
-      sum = 0.f;
 #pragma unroll
       for (int c = 0; c < EPL; ++c) sum += lane * EPL + c < a.n_experts ? expf(v[c] - top) : 0.f;
-    } else {
-      sum = on ? expf(g - top) : 0.f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    w = on ? expf(g - top) / sum : 0.f;
-  } else {
-#pragma unroll
-    for (int q = 0; q < EPL; ++q) {
-      v[q] = sigmoid_near(v[q]) + bias[q];
-      const unsigned place = number_key(v[q]);
-      key[q] = key[q] == 0u ? 0u : place < kLowest || place > kHighest ? kLowest : place;
-    }
-    bool sure = a.topk_group >= a.n_group || limit_groups<EPL>(key, a);
-    if (sure) {
-      // one more than asked for, so that the last border is seen too
-      best_of<EPL>(key, k + 1, scratch, &sel, &val);
-      const float at = key_value(val), next = __shfl_down_sync(kAll, at, 1);
-      const int after = __shfl_down_sync(kAll, sel, 1);
-      if (__any_sync(kAll, lane < k && after >= 0 && !apart(at, next))) {
-        // Every entry that could be among the k: those not surely below the k-th, in 64 bits.
-        const float edge = __shfl_sync(kAll, at, k - 1);
-        const bool all = __shfl_sync(kAll, sel, k - 1) < 0;
-        unsigned near = 0u;
-#pragma unroll
-        for (int q = 0; q < EPL; ++q)
-          if (key[q] != 0u && (all || !(v[q] < edge && apart(v[q], edge)))) near |= 1u << q;
-        int n = __popc(near), sum = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kAll, sum, o);
-          if (lane >= o) sum += y;
-        }
-        const int total = __shfl_sync(kAll, sum, 31);
-        sure = total <= 32;
-        if (sure) {
-          int to = sum - n;
-#pragma unroll
-          for (int q = 0; q < EPL; ++q)
-            if ((near >> q) & 1u) scratch[to++].y = static_cast<unsigned>(lane * EPL + q);
-          __syncwarp();
-          const int e = lane < total ? static_cast<int>(scratch[lane].y) : -1;
-          __syncwarp();
-          sel = rank_exact(a, row, e, k);
-        }
-      }
-    }
-    if (!sure) sel = select_exact<EPL>(a, row, can);
-    if (lane >= k) sel = -1;
-    const float g = sel >= 0 ? logit(row, bf16, sel) : 0.f;
-    w = sel >= 0 ? 1.0f / (1.0f + expf(-g)) : 0.f;
-    if (!a.raw_weights) {
-      float sum = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      w = sel >= 0 ? w / sum : 0.f;
+    }
+    if (lane == 0) *stat = make_float2(top, sum);
+    __syncwarp();
+    return;
+  }
+  unsigned most = 0u;
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) {
+    const int e = lane * EPL + q;
+    v[q] = sigmoid_near(v[q]) + (EPL <= 8 ? bias[q] : a.bias != nullptr && e < a.n_experts ? __ldg(a.bias + e) : 0.f);
+    const unsigned place = number_key(v[q]);
+    key[q] = key[q] == 0u ? 0u : place;
+    most = max(most, place - kLowest - 1u);
+  }
+  // NaN and -inf of a logit or a bias rank lowest
+  const bool numbers = __all_sync(kAll, most < kHighest - kLowest);
+  if (!numbers)
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) key[q] = key[q] == 0u ? 0u : key[q] < kLowest || key[q] > kHighest ? kLowest : key[q];
+  int sel = -1;
+  bool sure = true;
+  if (a.topk_group < a.n_group) {
+    const int gs = a.n_experts / a.n_group, span = gs / EPL;
+    if (clean && numbers && gs % EPL == 0 && (span & (span - 1)) == 0 && a.topk_group * gs >= k) sure = limit_groups_fast<EPL>(key, a, span, row, scratch);
+    else sure = limit_groups<EPL>(key, a);
+  }
+  if (__all_sync(kAll, sure)) {
+    // one more than asked for, so that the last border is seen too
+    best_of<EPL>(key, k + 1, scratch);
+    const uint2 mine = scratch[min(lane, k)], after = scratch[min(lane + 1, k)];
+    sel = static_cast<int>(mine.y);
+    if (__any_sync(kAll, lane < k && after.x != 0u && !apart(key_value(mine.x), key_value(after.x)))) {
+      // Every entry that could be among the k: those not surely below the k-th, in 64 bits.
+      const uint2 kth = scratch[k - 1];
+      const float edge = key_value(kth.x);
+      unsigned near = 0u;
+#pragma unroll
+      for (int q = 0; q < EPL; ++q)
+        if (key[q] != 0u && (kth.x == 0u || !(v[q] < edge && apart(v[q], edge)))) near |= 1u << q;
+      const int total = gather_marked<EPL>(near, scratch);
+      sure = total <= 32;
+      if (__all_sync(kAll, sure)) sel = rank_exact(a, row, lane < total ? static_cast<int>(scratch[lane].y) : -1, k);
     }
   }
-  if (nan && sel >= 0) w = __uint_as_float(0x7FC00000u);  // a NaN among a position's logits spoils its weights
-  *sel_out = sel;
-  *w_out = w;
+  if (!__all_sync(kAll, sure)) sel = select_exact<EPL>(a, row, can);
+  if (lane < k) id[lane] = static_cast<int16_t>(sel);
+  if (lane == 0) *stat = make_float2(0.f, spoilt);
+  __syncwarp();
 }
 
 // First entries of the experts (offsets, E + 1 values in shared memory) from their totals; all threads of the CTA.
@@ -450,17 +517,35 @@ __device__ __forceinline__ void scan_totals(const int *total, int E, int *offset
 }
 
 // Selection, weights and, in slots, each edge's place among its CTA's edges of the expert; the CTA's counts. The only
-// CTA of a grid (with one pass) finishes the worklist too.
+// CTA of a grid (with one pass) finishes the worklist too. Selecting takes a warp a position; what follows takes a
+// thread an edge.
 template <int EPL, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, int passes, int pass) {
-  constexpr int kRows = kPass / (THREADS / 32);  // most positions of a warp in a pass
   constexpr int kE = EPL * 32;
+  constexpr bool kAhead = EPL <= 8;  // the next position's logits are on their way (wider lanes have no registers for it)
   __shared__ uint32_t s_bits[kPass / 32][kE];
   __shared__ int s_count[kE], s_off[kE + 1], s_warp[32];
   __shared__ uint2 s_scratch[THREADS / 32][32];
-  const int tid = threadIdx.x, threads = blockDim.x, lane = lane_id(), warp = warp_id(), warps = threads >> 5;
-  const int E = a.n_experts, k = a.top_k, words = pass / 32;
-  const bool vec = a.vec != 0, one = gridDim.x == 1 && passes == 1;
+  __shared__ float s_val[kPass * 16];
+  __shared__ int16_t s_id[kPass * 16];
+  __shared__ float2 s_stat[kPass];
+  // (The warp's number by a shuffle: the compiler then knows that the warp takes every branch on it together. Where it
+  // does not, each warp maximum becomes a loop.)
+  const int tid = threadIdx.x, threads = blockDim.x, lane = lane_id(), warp = __shfl_sync(0xffffffffu, warp_id(), 0), warps = threads >> 5;
+  const int E = a.n_experts, k = a.top_k, words = (pass + 31) / 32;
+  const unsigned by_k = (65536u + k - 1) / k;  // i / k = i * by_k >> 16 for i < 2048
+  const bool vec = a.vec != 0, bf16 = a.bf16 != 0, one = gridDim.x == 1 && passes == 1;
+  const int64_t row_bytes = a.logits_stride * (bf16 ? 2 : 4);
+  const uint8_t *logits = static_cast<const uint8_t *>(a.logits);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * passes * pass;
+  Raw<EPL> raw;
+  bool live = true;
+  auto fetch = [&](int64_t t, int64_t end) {
+    if (t >= end) return;
+    live = a.live == nullptr || __ldg(a.live + t) != 0;
+    load_raw<EPL>(logits + t * row_bytes, bf16, E, vec, raw);
+  };
+  if (kAhead) fetch(first + warp, min(first + pass, static_cast<int64_t>(a.n_tok)));
   for (int i = tid; i < E; i += threads) {
     s_count[i] = 0;
     for (int w = 0; w < words; ++w) s_bits[w][i] = 0u;
@@ -471,37 +556,38 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
   for (int c = 0; c < EPL; ++c) {
     const int e = lane * EPL + c;
     if (e < E && (a.eligible == nullptr || __ldg(a.eligible + e) != 0)) eligible |= 1u << c;
-    bias[c] = e < E && a.bias != nullptr ? __ldg(a.bias + e) : 0.f;
+    bias[c] = kAhead && e < E && a.bias != nullptr ? __ldg(a.bias + e) : 0.f;
   }
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * passes * pass;
   pdl_trigger();
   for (int p = 0; p < passes; ++p) {
     const int64_t t0 = first + static_cast<int64_t>(p) * pass;
     if (t0 >= a.n_tok) break;
-    __syncthreads();  // the words are clear
-    const int rows = static_cast<int>(min(static_cast<int64_t>(pass), a.n_tok - t0));
-    int sel[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) sel[i] = -1;
-#pragma unroll 1
-    for (int i = 0; i < kRows; ++i) {
-      const int r = i * warps + warp;
-      if (r >= rows) break;
-      const int64_t t = t0 + r;
-      int e = -1;
-      float w = 0.f;
-      if (a.live == nullptr || __ldg(a.live + t) != 0) route_row<EPL>(a, t, vec, eligible, bias, s_scratch[warp], &e, &w);
-      if (lane < k) {
-        a.sel[t * k + lane] = e;
-        a.weights[t * k + lane] = w;
-        if (e >= 0) atomicOr(&s_bits[r >> 5][e], 1u << (r & 31));
+    const int rows = static_cast<int>(min(static_cast<int64_t>(pass), a.n_tok - t0)), edges = rows * k;
+    for (int r = warp; r < rows; r += warps) {
+      if (!kAhead || (p > 0 && r == warp)) fetch(t0 + r, t0 + rows);
+      float v[EPL];
+      open_raw<EPL>(raw, bf16, E, vec, v);
+      const bool on = __any_sync(0xffffffffu, live);
+      if (kAhead) fetch(t0 + r + warps, t0 + rows);
+      if (on) {
+        route_row<EPL>(a, logits + (t0 + r) * row_bytes, v, eligible, bias, s_scratch[warp], s_id + r * k, s_val + r * k, s_stat + r);
+      } else if (lane < k) {
+        s_id[r * k + lane] = -1;
       }
-#pragma unroll
-      for (int q = 0; q < kRows; ++q)
-        if (q == i) sel[q] = e;
     }
     __syncthreads();
-    if (one) {  // totals, then places in the whole worklist
+    // the weights' terms, a thread an edge; the selections as bits
+    for (int i = tid; i < edges; i += threads) {
+      const int r = static_cast<int>(i * by_k >> 16), e = s_id[i];
+      float x = 0.f;
+      if (e >= 0) {
+        atomicOr(&s_bits[r >> 5][e], 1u << (r & 31));
+        x = a.sigmoid ? 1.0f / (1.0f + expf(-logit(logits + (t0 + r) * row_bytes, bf16, e))) : expf(s_val[i] - s_stat[r].x);
+      }
+      s_val[i] = x;
+    }
+    __syncthreads();
+    if (one) {  // totals, and with them the first places
       for (int i = tid; i < E; i += threads) {
         int n = 0;
         for (int w = 0; w < words; ++w) n += __popc(s_bits[w][i]);
@@ -513,19 +599,24 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       for (int64_t i = s_off[E] + tid; i < static_cast<int64_t>(a.n_tok) * k; i += threads) a.positions[i] = -1;
     }
     const int *base = one ? s_off : s_count;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int r = i * warps + warp;
-      if (r >= rows || lane >= k) continue;
-      const int64_t t = t0 + r;
+    for (int i = tid; i < edges; i += threads) {
+      const int r = static_cast<int>(i * by_k >> 16), e = s_id[i];
+      const int64_t at = t0 * k + i;
       int place = -1;
-      if (sel[i] >= 0) {
-        place = base[sel[i]];
-        for (int w = 0; w < (r >> 5); ++w) place += __popc(s_bits[w][sel[i]]);
-        place += __popc(s_bits[r >> 5][sel[i]] & ((1u << (r & 31)) - 1u));
-        if (one) a.positions[place] = static_cast<int>(t);
+      float w = 0.f;
+      if (e >= 0) {
+        float sum = s_stat[r].y;
+        if (!a.raw_weights)
+          for (int j = 0; j < k; ++j) sum += s_val[r * k + j];
+        w = a.raw_weights && a.sigmoid ? s_val[i] + sum : s_val[i] / sum;
+        place = base[e];
+        for (int q = 0; q < (r >> 5); ++q) place += __popc(s_bits[q][e]);
+        place += __popc(s_bits[r >> 5][e] & ((1u << (r & 31)) - 1u));
+        if (one) a.positions[place] = static_cast<int>(t0 + r);
       }
-      a.slots[t * k + lane] = place;
+      a.sel[at] = e;
+      a.weights[at] = w;
+      a.slots[at] = place;
     }
     if (one) return;
     __syncthreads();
@@ -537,8 +628,8 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       }
       s_count[i] = n;
     }
+    __syncthreads();
   }
-  __syncthreads();
   for (int i = tid; i < E; i += threads) a.counts[static_cast<int64_t>(blockIdx.x) * E + i] = s_count[i];
 }
 

@@ -698,3 +698,19 @@ def test_fp4_offsets_pass_32_bits(ops, form):
     vb = ops.fp4_dequantize(*one[:2], tensor_scale=one[2], out_dtype=F32).double()
     y, size = product64(va, vb[None], [0, m])
     _within(got, y, product_bound(y, size, k / 64 + 16, F32, False))
+
+
+# -------------------------------------------------------------------------------------------- router
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,groups,top", [(256, 8, 4), (64, 4, 2), (512, 16, 3), (96, 6, 2)])
+def test_route_groups_that_fp32_cannot_tell_apart(ops, E, groups, top):
+    """Groups whose two best add up to the same but for a step or two of a logit."""
+    g = _gen(E)
+    T, k, size = 150, 8, E // groups
+    x = _rnd(g, T, E) - 3
+    best = 1 + torch.rand(T, 1, 2, generator=g, device="cuda")
+    steps = torch.randint(-2, 3, (T, groups, 2), generator=g, device="cuda", dtype=I32)
+    x.view(T, groups, size)[:, :, [1, size - 1]] = (best.expand(T, groups, 2).contiguous().view(torch.int32) + steps).view(F32)
+    for bias in (None, torch.zeros(E, device="cuda")):
+        check_route(ops.route(x, k, router="sigmoid_group", bias=bias, n_group=groups, topk_group=top),
+                    route64(x, k, True, bias=bias, n_group=groups, topk_group=top))
