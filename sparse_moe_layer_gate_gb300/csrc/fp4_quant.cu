@@ -6,9 +6,9 @@
 //          2^-9 (the smallest e4m3 value: a block of zeros divides by it), q = e2m1(v' / s)
 //   mxfp4: blocks of 32, s = 2^(floor(log2 max|v|) - 2) within e8m0's range, q = e2m1(v / s)
 //
-// Both roundings are to nearest even of the exact quotients: s has four bits, so a border between
-// two codes times s is exact in fp32, and a quotient that fp32 cannot tell from a border is decided
-// by the remainder's sign. A block that holds a NaN or an infinity gets a NaN scale, so that every
+// Both roundings are to nearest even of the exact quotients: a border between two codes times s, or
+// between two scales times 6, is exact in fp32, and a quotient next to a border is decided by the
+// remainder's sign. A block that holds a NaN or an infinity gets a NaN scale, so that every
 // product with it is NaN. Scales lie by blocks of 256 columns, [ceil(K / 256)][rows][16 or 8], with
 // zeros behind the last column.
 #include <cmath>
@@ -24,43 +24,63 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sixteen consecutive elements from a 16-byte boundary on, and the bits of their largest magnitude.
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16], unsigned &m) {
-  uint4 u[2];
+// N words from global memory, in the widest accesses that `align` bytes allow (elements of T at the least). Accesses of
+// 32 bytes take whole sectors however far apart the lanes' are.
+template <typename T, int N> __device__ __forceinline__ void load_words(const T *p, int align, uint32_t (&w)[N]) {
+  const char *at = reinterpret_cast<const char *>(p);
+  if (N % 8 == 0 && align >= 32) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(u[h].x), "=r"(u[h].y), "=r"(u[h].z), "=r"(u[h].w)
-                 : "l"(p + 8 * h));
-  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-  uint32_t big = 0;  // largest magnitudes of the low and of the high halves
+    for (int h = 0; h + 8 <= N; h += 8)
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[h]), "=r"(w[h + 1]), "=r"(w[h + 2]), "=r"(w[h + 3]), "=r"(w[h + 4]), "=r"(w[h + 5]), "=r"(w[h + 6]),
+                     "=r"(w[h + 7])
+                   : "l"(at + 4 * h));
+  } else if (align >= 16) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    big = __vmaxu2(big, w[i] & 0x7FFF7FFFu);
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int h = 0; h < N; h += 4)
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[h]), "=r"(w[h + 1]), "=r"(w[h + 2]), "=r"(w[h + 3])
+                   : "l"(at + 4 * h));
+  } else if constexpr (sizeof(T) == 2) {
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(q + 2 * i) | (static_cast<uint32_t>(__ldg(q + 2 * i + 1)) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
   }
-  m = max(big << 16, big & 0xFFFF0000u);
 }
-__device__ __forceinline__ unsigned largest(const float (&v)[16]) {
+template <int N> __device__ __forceinline__ void store_words(void *p, int align, const uint32_t (&w)[N]) {
+  char *at = static_cast<char *>(p);
+  if (N % 8 == 0 && align >= 32) {
+#pragma unroll
+    for (int h = 0; h + 8 <= N; h += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + 4 * h), "r"(w[h]), "r"(w[h + 1]),
+                   "r"(w[h + 2]), "r"(w[h + 3]), "r"(w[h + 4]), "r"(w[h + 5]), "r"(w[h + 6]), "r"(w[h + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int h = 0; h < N; h += 4) *reinterpret_cast<uint4 *>(at + 4 * h) = make_uint4(w[h], w[h + 1], w[h + 2], w[h + 3]);
+  }
+}
+// Words of T as values.
+template <typename T, int N> __device__ __forceinline__ void open_words(const uint32_t (&w)[N], float *v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+// Bits of the largest magnitude of N values.
+template <int N> __device__ __forceinline__ unsigned largest(const float *v) {
   unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   return m;
-}
-__device__ __forceinline__ void load16(const float *p, float (&v)[16], unsigned &m) {
-#pragma unroll
-  for (int h = 0; h < 4; ++h)
-    asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
-                 : "l"(p + 4 * h));
-  m = largest(v);
-}
-// The same at any alignment.
-template <typename T> __device__ __forceinline__ void load16_any(const T *p, float (&v)[16], unsigned &m) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = to_f32(p[i]);
-  m = largest(v);
 }
 
 // Eight values to e2m1 (round to nearest even, out of range to the largest), the first in the lowest four bits.
@@ -77,122 +97,157 @@ __device__ __forceinline__ uint32_t pack8(const float *v) {
   return r;
 }
 
-// e4m3 of m / 6 (m finite, >= 0), rounded once and kept within [2^-9, 448]. The quotient in fp32 may round onto a
-// border between two e4m3 values; the remainder tells on which side of it m / 6 lies.
-__device__ __forceinline__ uint32_t nv_scale(float m, float *s) {
-  float q = m / 6.0f;
-  const float rest = fmaf(-6.0f, q, m);
-  if (rest > 0.f) q = __uint_as_float(__float_as_uint(q) | 1u);
-  else if (rest < 0.f && (__float_as_uint(q) & 1u) == 0u) q = __uint_as_float(__float_as_uint(q) - 1u);
+// Quotients decide between neighbours of few bits: codes meet at three bits, scales at five. They are taken to twelve
+// bits, by factors that are off by a few steps of 2^-23, so that an exact quotient on a border is found there. A
+// quotient that was near a border and not on it moves off it by the sign of its remainder (`rest`, exact).
+__device__ __forceinline__ uint32_t to_twelve(float q) { return (__float_as_uint(q) + 0x800u) & 0xFFFFF000u; }
+__device__ __forceinline__ float off_border(uint32_t b, float rest) {
+  const float at = __uint_as_float(b);
+  // away from zero where the dividend is beyond the border, towards it where it is short of it
+  if (rest != 0.f && at != 0.f) b = (rest > 0.f) == (at > 0.f) ? b + 1u : b - 1u;
+  return __uint_as_float(b);
+}
+
+__device__ __forceinline__ float open_e4m3(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+  return __low2float(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// e4m3 of m / 6 (finite, >= 0), rounded once and kept within [2^-9, 448].
+__device__ __forceinline__ uint32_t nv_scale(float m) {
+  const uint32_t b = to_twelve(m * (1.0f / 6.0f));
+  const float q = off_border(b, fmaf(-6.0f, __uint_as_float(b), m));
   uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(q));
-  uint32_t b = two & 0xFFu;
-  if (b == 0u) b = 1u;
-  const uint32_t e = b >> 3, f = b & 7u;  // e4m3: bias 7; e = 0: f * 2^-9
-  *s = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : static_cast<float>(f) * 0x1p-9f;
-  return b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(fmaxf(q, 0x1p-9f)));
+  return two;
 }
 
-// Codes of v / s, inv = 1 / s. Quotients are taken to twelve bits, which leaves every border between codes (three bits)
-// as it is and, where v has eight bits (EXACT false), keeps all others on their side of it: v and a border times s
-// differ by 2^-8 or more of them. EXACT: a quotient that landed on a border moves off it by the sign of its remainder.
-template <bool EXACT> __device__ __forceinline__ void nv_codes(const float (&v)[16], float s, float inv, uint32_t (&q)[2]) {
-  float t[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint32_t b = (__float_as_uint(v[i] * inv) + 0x800u) & 0xFFFFF000u;
-    if constexpr (EXACT) {
-      const float at = __uint_as_float(b), rest = fmaf(-at, s, v[i]);
-      // away from zero where v is beyond at * s, towards it where it is short of it
-      if (rest != 0.f && at != 0.f) b = (rest > 0.f) == (at > 0.f) ? b + 1u : b - 1u;
-    }
-    t[i] = __uint_as_float(b);
+__device__ __forceinline__ float reciprocal_near(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Where a thread works: C columns of the blocks of 256 columns of rows, which threads take in order.
+template <int C> struct Piece {
+  unsigned row, kb;
+  int part, c;
+  __device__ explicit Piece(unsigned kb_n) {
+    const unsigned at = blockIdx.x * (kThreads * C / 256) + threadIdx.x / (256 / C);  // less than 2^31 + 32
+    row = at / kb_n;
+    kb = at - row * kb_n;
+    part = threadIdx.x & (256 / C - 1);
+    c = static_cast<int>(kb * 256) + part * C;
   }
-  q[0] = pack8(t);
-  q[1] = pack8(t + 8);
-}
+};
 
-// Sixteen columns a thread; sixteen threads take a block of 256 columns of a row and a CTA sixteen
-// such blocks in order. ALIGNED: pieces start on 16-byte boundaries. EXACT: see nv_codes (else the tensor scale is a
-// power of two and goes into the factor of the quotients).
-template <typename T, bool NV, bool SWIGLU, bool ALIGNED, bool EXACT>
-__global__ void __launch_bounds__(kThreads) k_fp4_quant(const Fp4QuantArgs a, unsigned kb_n) {
-  const unsigned at = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);  // blocks of 256 columns: less than 2^31 + 16
-  const int64_t row = at / kb_n;
-  const unsigned kb = at - static_cast<unsigned>(row) * kb_n, piece = threadIdx.x & 15u;
-  const int c = static_cast<int>(kb * 256 + piece * 16);
-  const bool on = row < a.n_rows, in = on && c < a.cols;
-  int64_t src = row, mat = 0;
-  if (a.rows != nullptr && on) src = __ldg(a.rows + row);
+// C: 32 columns a thread where there are many (the work for a scale and for addresses is then shared by most), 8 where
+// there are few (four times the threads). EXACT false: the elements have eight bits, so a quotient that is not on a
+// border differs from it by 2^-8 of it or more, and the tensor scale is a power of two, which goes into the factor of
+// the quotients.
+template <typename T, bool NV, bool SWIGLU, bool EXACT, int C>
+__global__ void __launch_bounds__(kThreads) k_fp4_quant(const Fp4QuantArgs a, unsigned kb_n, int align) {
+  constexpr int kB = NV && C == 32 ? 2 : 1, kPer = C / kB;  // blocks of a thread and their columns here
+  constexpr int kWords = C * static_cast<int>(sizeof(T)) / 4;
+  const Piece<C> p(kb_n);
+  const bool row_there = p.row < a.n_rows, in = row_there && p.c < a.cols;
+  int64_t src = p.row;
+  unsigned mat = 0;
+  if (a.rows != nullptr && row_there) src = __ldg(a.rows + p.row);
   const bool bad = src < 0 || src >= a.n_src;  // never followed: its scales are NaN
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  float inv = a.inv_scale;
-  if (a.amax != nullptr && on) {
-    mat = static_cast<unsigned>(row) / static_cast<unsigned>(a.mat_rows);
+  float v[C], inv = a.inv_scale;
+  if (a.amax != nullptr && row_there) {
+    mat = p.row / static_cast<unsigned>(a.mat_rows);
     inv = 1.0f / fp4_tensor_scale(a.amax[mat]);
   }
-  unsigned m = 0;
-  if (in && !bad) {
-    const T *p = static_cast<const T *>(a.x) + src * a.x_stride + c;
-    if constexpr (ALIGNED) load16(p, v, m);
-    else load16_any(p, v, m);
-    if constexpr (SWIGLU) {
-      float u[16];
-      unsigned unused;
-      if constexpr (ALIGNED) load16(p + a.cols, u, unused);
-      else load16_any(p + a.cols, u, unused);
+  uint32_t w[kWords];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = silu(v[i]) * u[i];
-      m = largest(v);
-    }
-  }
-  uint32_t q[2], code;
-  if constexpr (NV) {
-    float s;
-    if constexpr (EXACT) {
+  for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  const T *x = static_cast<const T *>(a.x) + src * a.x_stride + p.c;
+  if (in && !bad) load_words(x, align, w);
+  if constexpr (SWIGLU) {
+    uint32_t y[kWords];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= inv;
-      m = largest(v);
-    }
-    const bool spoilt = m >= 0x7F800000u;
-    code = nv_scale(spoilt ? 0.f : EXACT ? __uint_as_float(m) : __uint_as_float(m) * inv, &s);
-    if (spoilt || bad) code = 0x7Fu;
-    nv_codes<EXACT>(v, s, EXACT ? 1.0f / s : 1.0f / s * inv, q);
+    for (int i = 0; i < kWords; ++i) y[i] = 0u;
+    if (in && !bad) load_words(x + a.cols, align, y);
+    float u[C];
+    open_words<T>(w, v);
+    open_words<T>(y, u);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = silu(v[i]) * u[i];
   } else {
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    // floor(log2 m) - 2, biased by 127: the exponent field less two, for subnormal m the least
-    const int e = max(static_cast<int>(m >> 23) - 2, 0);
-    code = m >= 0x7F800000u || bad ? 0xFFu : static_cast<uint32_t>(e);
-    const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), normal for e <= 253
+    open_words<T>(w, v);
+  }
+  if constexpr (NV && EXACT) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= up;
-    q[0] = pack8(v);
-    q[1] = pack8(v + 8);
+    for (int i = 0; i < C; ++i) v[i] *= inv;
   }
-  if (!on) return;
+  unsigned m[kB];
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    if constexpr (sizeof(T) == 2 && !SWIGLU && !(NV && EXACT)) {
+      uint32_t big = 0;  // largest magnitudes of the low and of the high halves
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) big = __vmaxu2(big, w[b * kPer / 2 + i] & 0x7FFF7FFFu);
+      m[b] = max(big << 16, big & 0xFFFF0000u);
+    } else {
+      m[b] = largest<kPer>(v + b * kPer);
+    }
+    if constexpr (C == 8) {  // a block is two threads', or four
+      m[b] = max(m[b], __shfl_xor_sync(0xffffffffu, m[b], 1));
+      if constexpr (!NV) m[b] = max(m[b], __shfl_xor_sync(0xffffffffu, m[b], 2));
+    }
+  }
+  if (!row_there) return;
+  const int64_t rows = a.amax ? a.mat_rows : a.n_rows, block = (static_cast<int64_t>(mat) * kb_n + p.kb) * rows + (p.row - mat * rows);
+  uint32_t code = 0u;
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    const bool spoilt = m[b] >= 0x7F800000u || bad;
+    float *y = v + b * kPer;
+    if constexpr (NV) {
+      const float f = EXACT ? 1.0f : inv;
+      const uint32_t c = nv_scale(spoilt ? 0.f : __uint_as_float(m[b]) * f);
+      const float s = open_e4m3(c), r = reciprocal_near(s) * f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t t = to_twelve(y[i] * r);
+        y[i] = EXACT ? off_border(t, fmaf(-__uint_as_float(t), s, y[i])) : __uint_as_float(t);
+      }
+      code |= (spoilt ? 0x7Fu : c) << (8 * b);
+    } else {
+      // floor(log2 m) - 2, biased by 127: the exponent field less two, for subnormal m the least
+      const int e = max(static_cast<int>(m[b] >> 23) - 2, 0);
+      const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), normal for e <= 253
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) y[i] *= scale;
+      code = spoilt ? 0xFFu : e;
+    }
+  }
   if (!in) code = 0u;
-  constexpr int kPer = NV ? 16 : 8;
-  if (NV || (piece & 1u) == 0u) {
-    const int64_t rows = a.amax ? a.mat_rows : a.n_rows, i = a.amax ? row - mat * rows : row;
-    a.scales[((mat * kb_n + kb) * rows + i) * kPer + (NV ? piece : piece >> 1)] = static_cast<uint8_t>(code);
-  }
-  if (in) *reinterpret_cast<uint2 *>(a.q + (row * a.cols + c) / 2) = make_uint2(q[0], q[1]);
+  if constexpr (C == 32 && NV) reinterpret_cast<uint16_t *>(a.scales)[block * 8 + p.part] = static_cast<uint16_t>(code);
+  else if constexpr (C == 32) a.scales[block * 8 + p.part] = static_cast<uint8_t>(code);
+  else if constexpr (NV) { if ((p.part & 1) == 0) a.scales[block * 16 + (p.part >> 1)] = static_cast<uint8_t>(code); }
+  else { if ((p.part & 3) == 0) a.scales[block * 8 + (p.part >> 2)] = static_cast<uint8_t>(code); }
+  if (!in) return;
+  uint8_t *q = a.q + (static_cast<int64_t>(p.row) * a.cols + p.c) / 2;
+  if constexpr (C == 32) *reinterpret_cast<uint4 *>(q) = make_uint4(pack8(v), pack8(v + 8), pack8(v + 16), pack8(v + 24));
+  else *reinterpret_cast<uint32_t *>(q) = pack8(v);
 }
 
 // Largest |x| of each matrix, as bit patterns (a NaN's are above infinity's).
-template <typename T, bool ALIGNED> __global__ void __launch_bounds__(kThreads) k_fp4_amax(const T *w, int64_t count, uint32_t *amax) {
+template <typename T> __global__ void __launch_bounds__(kThreads) k_fp4_amax(const T *w, int64_t count, uint32_t *amax, int align) {
   __shared__ uint32_t s_max[kThreads / 32];
   const T *p = w + static_cast<int64_t>(blockIdx.y) * count;
   uint32_t m = 0;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 16; i < count;
-       i += static_cast<int64_t>(gridDim.x) * kThreads * 16) {
-    float v[16];
-    unsigned here;
-    if constexpr (ALIGNED) load16(p + i, v, here);
-    else load16_any(p + i, v, here);
-    m = max(m, here);
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 8; i < count;
+       i += static_cast<int64_t>(gridDim.x) * kThreads * 8) {
+    uint32_t w[2 * sizeof(T)];
+    float v[8];
+    load_words(p + i, align, w);
+    open_words<T>(w, v);
+    m = max(m, largest<8>(v));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane_id() == 0) s_max[warp_id()] = m;
@@ -208,74 +263,94 @@ __global__ void k_fp4_tensor_scales(uint32_t *amax, int n, int nv) {
   if (i < n) reinterpret_cast<float *>(amax)[i] = nv ? fp4_tensor_scale(amax[i]) : 1.0f;
 }
 
-// Sixteen columns a thread, in the order of k_fp4_quant.
-template <typename T, bool NV>
+// In the order of k_fp4_quant.
+template <typename T, bool NV, int C>
 __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a, unsigned kb_n) {
-  const unsigned at = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);  // blocks of 256 columns: less than 2^31 + 16
-  const int64_t row = at / kb_n;
-  const unsigned kb = at - static_cast<unsigned>(row) * kb_n, piece = threadIdx.x & 15u;
-  const int c = static_cast<int>(kb * 256 + piece * 16);
-  if (row >= a.n_rows || c >= a.cols) return;
-  const int64_t mat = static_cast<unsigned>(row) / static_cast<unsigned>(a.mat_rows), i = row - mat * a.mat_rows;
-  constexpr int kPer = NV ? 16 : 8;
-  const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.q + (row * a.cols + c) / 2));
-  const uint32_t b = __ldg(a.scales + ((mat * kb_n + kb) * a.mat_rows + i) * kPer + (NV ? piece : piece >> 1));
-  float s;
-  if constexpr (NV) {
-    const uint32_t e = (b >> 3) & 15u, f = b & 7u;
-    s = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : static_cast<float>(f) * 0x1p-9f;
-    if ((b & 0x7Fu) == 0x7Fu) s = __uint_as_float(0x7FC00000u);
-    if (b & 0x80u) s = -s;
+  constexpr int kCodes = C / 8, kWords = C * static_cast<int>(sizeof(T)) / 4;
+  const Piece<C> p(kb_n);
+  if (p.row >= a.n_rows || p.c >= a.cols) return;
+  const unsigned mat = p.row / static_cast<unsigned>(a.mat_rows);
+  const int64_t block = (static_cast<int64_t>(mat) * kb_n + p.kb) * a.mat_rows + (p.row - mat * a.mat_rows);
+  const uint8_t *at = a.q + (static_cast<int64_t>(p.row) * a.cols + p.c) / 2;
+  uint32_t q[kCodes], code;
+  if constexpr (C == 32) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(at));
+    q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
+    code = NV ? __ldg(reinterpret_cast<const uint16_t *>(a.scales) + block * 8 + p.part) : __ldg(a.scales + block * 8 + p.part);
   } else {
-    s = b == 0xFFu ? __uint_as_float(0x7FC00000u) : b ? __uint_as_float(b << 23) : 0x1p-127f;
+    q[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+    code = __ldg(a.scales + block * (NV ? 16 : 8) + (p.part >> (NV ? 1 : 2)));
   }
-  s *= a.group_scale ? a.scale * __ldg(a.group_scale + mat) : a.scale;
-  float v[16];
+  const float f = a.group_scale ? a.scale * __ldg(a.group_scale + mat) : a.scale;
+  float s[2];
+  if constexpr (NV) {
+    s[0] = open_e4m3(code) * f;
+    s[1] = open_e4m3(code >> 8) * f;
+  } else {
+    s[0] = s[1] = (code == 0xFFu ? __uint_as_float(0x7FC00000u) : code ? __uint_as_float(code << 23) : 0x1p-127f) * f;
+  }
+  uint32_t o[kWords];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t p[4];  // pairs in fp16, which holds e2m1's values
+  for (int h = 0; h < kCodes; ++h) {
+    uint32_t d[4];  // pairs in fp16, which holds e2m1's values
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "mov.b32 {a, b, c, d}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
         "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
         "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
         "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
-        : "r"(h ? q.y : q.x));
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(q[h]));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[j]));
-      v[8 * h + 2 * j] = f.x * s;
-      v[8 * h + 2 * j + 1] = f.y * s;
+      const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&d[j]));
+      const float y0 = x.x * s[h / 2], y1 = x.y * s[h / 2];
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
+        o[4 * h + j] = *reinterpret_cast<const uint32_t *>(&t);
+      } else {
+        o[8 * h + 2 * j] = __float_as_uint(y0);
+        o[8 * h + 2 * j + 1] = __float_as_uint(y1);
+      }
     }
   }
-  T *out = static_cast<T *>(a.out) + row * a.out_stride + c;
-  if (a.wide) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[8];
+  T *out = static_cast<T *>(a.out) + static_cast<int64_t>(p.row) * a.out_stride + p.c;
+  if (a.align >= 16) {
+    store_words(out, a.align, o);
+  } else if constexpr (sizeof(T) == 2) {
+    uint16_t *e = reinterpret_cast<uint16_t *>(out);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-      reinterpret_cast<uint4 *>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4 *>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        reinterpret_cast<float4 *>(out)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    for (int i = 0; i < kWords; ++i) {
+      e[2 * i] = static_cast<uint16_t>(o[i]);
+      e[2 * i + 1] = static_cast<uint16_t>(o[i] >> 16);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) out[j] = from_f32<T>(v[j]);
+    for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(out)[i] = o[i];
   }
 }
 
-template <typename T, bool NV, bool SWIGLU, bool EXACT> cudaError_t launch_one(const Fp4QuantArgs &a, bool aligned, cudaStream_t s) {
-  const int64_t kb = (a.cols + 255) / 256, grid = (a.n_rows * kb + kThreads / 16 - 1) / (kThreads / 16);
-  const unsigned g = static_cast<unsigned>(grid), k = static_cast<unsigned>(kb);
-  if (aligned) k_fp4_quant<T, NV, SWIGLU, true, EXACT><<<g, kThreads, 0, s>>>(a, k);
-  else k_fp4_quant<T, NV, SWIGLU, false, EXACT><<<g, kThreads, 0, s>>>(a, k);
+// Whether threads of 32 columns still fill the device (several warps a scheduler).
+bool many(int64_t blocks) { return blocks >= 64ll * num_sms(); }
+unsigned ctas(int64_t blocks, int c) { return static_cast<unsigned>((blocks + kThreads * c / 256 - 1) / (kThreads * c / 256)); }
+// Bytes on which every row and piece starts: 32, 16 or less.
+int align_of(const void *p, int64_t rows, int64_t stride, int size) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(stride * size) : 0u);
+  return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
+}
+
+template <typename T, bool NV, bool SWIGLU, bool EXACT> cudaError_t launch_one(const Fp4QuantArgs &a, int align, cudaStream_t s) {
+  const int64_t kb = (a.cols + 255) / 256, blocks = a.n_rows * kb;
+  const unsigned k = static_cast<unsigned>(kb);
+  if (many(blocks)) k_fp4_quant<T, NV, SWIGLU, EXACT, 32><<<ctas(blocks, 32), kThreads, 0, s>>>(a, k, align);
+  else k_fp4_quant<T, NV, SWIGLU, EXACT, 8><<<ctas(blocks, 8), kThreads, 0, s>>>(a, k, align);
+  return cudaGetLastError();
+}
+template <typename T, bool NV> cudaError_t launch_back(const Fp4DequantArgs &a, cudaStream_t s) {
+  const int64_t kb = (a.cols + 255) / 256, blocks = a.n_rows * kb;
+  const unsigned k = static_cast<unsigned>(kb);
+  if (many(blocks)) k_fp4_dequant<T, NV, 32><<<ctas(blocks, 32), kThreads, 0, s>>>(a, k);
+  else k_fp4_dequant<T, NV, 8><<<ctas(blocks, 8), kThreads, 0, s>>>(a, k);
   return cudaGetLastError();
 }
 // Whether dividing by t only moves exponents (and the quotient's factor 1 / s / t stays in range).
@@ -283,22 +358,22 @@ bool power_of_two(float inv) {
   int e;
   return std::frexp(inv, &e) == 0.5f && e > -100 && e < 100;
 }
-template <typename T> cudaError_t launch_type(const Fp4QuantArgs &a, bool nv, bool aligned, cudaStream_t s) {
-  if (!nv) return a.swiglu ? launch_one<T, false, true, true>(a, aligned, s) : launch_one<T, false, false, true>(a, aligned, s);
-  if (a.swiglu) return launch_one<T, true, true, true>(a, aligned, s);
+template <typename T> cudaError_t launch_type(const Fp4QuantArgs &a, bool nv, int align, cudaStream_t s) {
+  if (!nv) return a.swiglu ? launch_one<T, false, true, true>(a, align, s) : launch_one<T, false, false, true>(a, align, s);
+  if (a.swiglu) return launch_one<T, true, true, true>(a, align, s);
   if constexpr (sizeof(T) == 2) {
     // (a matrix's own scale may be any power of two)
-    if (a.amax == nullptr && power_of_two(a.inv_scale)) return launch_one<T, true, false, false>(a, aligned, s);
+    if (a.amax == nullptr && power_of_two(a.inv_scale)) return launch_one<T, true, false, false>(a, align, s);
   }
-  return launch_one<T, true, false, true>(a, aligned, s);
+  return launch_one<T, true, false, true>(a, align, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, bool bf16, bool nv, cudaStream_t s) {
-  // every piece of sixteen columns on a 16-byte boundary
-  const bool aligned = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && (a.n_src <= 1 || a.x_stride % (bf16 ? 8 : 4) == 0);
-  return bf16 ? launch_type<__nv_bfloat16>(a, nv, aligned, s) : launch_type<float>(a, nv, aligned, s);
+  // (the up half of a SwiGLU starts a.cols elements on, a multiple of 64 bytes)
+  const int align = align_of(a.x, a.n_src, a.x_stride, bf16 ? 2 : 4);
+  return bf16 ? launch_type<__nv_bfloat16>(a, nv, align, s) : launch_type<float>(a, nv, align, s);
 }
 
 cudaError_t launch_fp4_quant_weight(Fp4QuantArgs a, int n_mats, bool bf16, bool nv, float *tensor_scales, cudaStream_t s) {
@@ -308,17 +383,10 @@ cudaError_t launch_fp4_quant_weight(Fp4QuantArgs a, int n_mats, bool bf16, bool 
   const int64_t count = a.mat_rows * a.cols;  // a multiple of 32
   if (nv) {
     const bool aligned = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0;
-    const int64_t want = (count / 16 + kThreads - 1) / kThreads, most = (8 * num_sms() + n_mats - 1) / n_mats;
+    const int64_t want = (count / 8 + kThreads - 1) / kThreads, most = (8 * num_sms() + n_mats - 1) / n_mats;
     const dim3 grid(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(n_mats));
-    if (bf16) {
-      const auto *w = static_cast<const __nv_bfloat16 *>(a.x);
-      if (aligned) k_fp4_amax<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(w, count, amax);
-      else k_fp4_amax<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(w, count, amax);
-    } else {
-      const auto *w = static_cast<const float *>(a.x);
-      if (aligned) k_fp4_amax<float, true><<<grid, kThreads, 0, s>>>(w, count, amax);
-      else k_fp4_amax<float, false><<<grid, kThreads, 0, s>>>(w, count, amax);
-    }
+    if (bf16) k_fp4_amax<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16 *>(a.x), count, amax, aligned ? 16 : 0);
+    else k_fp4_amax<<<grid, kThreads, 0, s>>>(static_cast<const float *>(a.x), count, amax, aligned ? 16 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -330,17 +398,9 @@ cudaError_t launch_fp4_quant_weight(Fp4QuantArgs a, int n_mats, bool bf16, bool 
 }
 
 cudaError_t launch_fp4_dequant(Fp4DequantArgs a, bool bf16, bool nv, cudaStream_t s) {
-  const int64_t kb = (a.cols + 255) / 256, grid = (a.n_rows * kb + kThreads / 16 - 1) / (kThreads / 16);
-  a.wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.n_rows <= 1 || a.out_stride % (bf16 ? 8 : 4) == 0);
-  const unsigned g = static_cast<unsigned>(grid), k = static_cast<unsigned>(kb);
-  if (bf16) {
-    if (nv) k_fp4_dequant<__nv_bfloat16, true><<<g, kThreads, 0, s>>>(a, k);
-    else k_fp4_dequant<__nv_bfloat16, false><<<g, kThreads, 0, s>>>(a, k);
-  } else {
-    if (nv) k_fp4_dequant<float, true><<<g, kThreads, 0, s>>>(a, k);
-    else k_fp4_dequant<float, false><<<g, kThreads, 0, s>>>(a, k);
-  }
-  return cudaGetLastError();
+  a.align = align_of(a.out, a.n_rows, a.out_stride, bf16 ? 2 : 4);
+  if (bf16) return nv ? launch_back<__nv_bfloat16, true>(a, s) : launch_back<__nv_bfloat16, false>(a, s);
+  return nv ? launch_back<float, true>(a, s) : launch_back<float, false>(a, s);
 }
 
 }  // namespace epoch

@@ -372,7 +372,7 @@ struct Fp4DequantArgs {
   void *out;
   int64_t n_rows, mat_rows, out_stride;
   int32_t cols;
-  int32_t wide;  // output rows start on 16-byte boundaries
+  int32_t align;  // bytes on which output rows start
   float scale;
 };
 cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, bool bf16, bool nv, cudaStream_t s);
