@@ -41,10 +41,12 @@ constexpr int kRow = 128;  // bytes of an operand row of a stage: one swizzle ro
 struct ExpertParams {
   CUtensorMap a[3];  // boxes of 32, 64, 128 rows
   CUtensorMap b;     // boxes of half a tile's columns (pairs: 128)
+  CUtensorMap out;   // boxes of 128 bytes x 32 rows of the output (pairs)
   ExpertGemmArgs g;
   int kb_n, nt_n;    // K blocks, tiles along N
   int out_n;         // columns of the output
   int wide;          // output rows start on 32-byte boundaries
+  int bulk;          // the output has a tensor map: its rows start and end on 16-byte boundaries
   int reuse;         // weights are read by several row tiles
   int acc_kb;        // K blocks that an accumulator sums before it is added to the fp32 sums in registers
   uint32_t *err;
@@ -63,7 +65,8 @@ template <int FP4, int BN, bool PAIR> struct Tile {
   static constexpr int groups_b = BN == 256 ? 2 : 1;      // 128-row groups of the weights' scales
   static constexpr int scale_bytes = (1 + groups_b) * FP4 * 512;
   static constexpr int stage = operands + scale_bytes;
-  static constexpr int fit = 220 * 1024 / stage;
+  static constexpr int places = PAIR ? kEpiWarps * 8192 : 0;  // two places of 32 rows x 128 bytes of the output a warp
+  static constexpr int fit = (220 * 1024 - places) / stage;
   static constexpr int stages = fit < 8 ? fit : 8;
   // TMEM: accumulators, then four places for the scales of a stage (the copies and the products of one thread
   // complete in order; four let a copy be well ahead of them)
@@ -72,7 +75,7 @@ template <int FP4, int BN, bool PAIR> struct Tile {
   static constexpr int place = FP4 * (4 + cols_b);
   static constexpr int need = bufs * BN + 4 * place;
   static constexpr int tmem = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
-  static constexpr int smem = 1024 + stages * stage;
+  static constexpr int smem = 1024 + stages * stage + places;
 };
 
 // Shape M x N, fp32 accumulator, both operands K-major.
@@ -173,6 +176,46 @@ template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, i
 #pragma unroll
       for (int j = 0; j < Q; ++j)
         if (j < n) dst[j] = v[j];
+    }
+  }
+}
+
+// 64 columns of 32 rows, a row a lane, by bulk stores from the warp's two places in shared memory in turn: they run under
+// the next tile's products, and leave the load and store units to the helpers. (Rows' own stores of 32 bytes took a
+// fifth of the 4-bit product's time at 8192 x 4096 x 4096: the scales' loads waited behind them.)
+__device__ __forceinline__ void bulk_run(const CUtensorMap *map, uint8_t *places, uint32_t &turn, int n0, int row, int out_n,
+                                         const float (&v)[64], bool bf16) {
+  const int lane = lane_id(), per = bf16 ? 64 : 32;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if ((bf16 && h == 1) || n0 + per * h >= out_n) break;
+    uint8_t *place = places + (turn & 1u) * 4096;
+    ++turn;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // what was here has left
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {  // 16 bytes at a time, in the 128-byte swizzle
+      uint32_t w[4];
+      if (bf16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
+          w[j] = *reinterpret_cast<const uint32_t *>(&t);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(v[32 * h + 4 * c + j]);
+      }
+      *reinterpret_cast<uint4 *>(place + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(n0 + per * h), "r"(row), "r"(smem_u32(place))
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
 }
@@ -478,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
     const int c0 = swiglu ? half * Q : half * 2 * Q, c1 = swiglu ? BN / 2 + half * Q : c0 + Q;
     const size_t size = bf16 ? 2 : 4;
     constexpr int kPiece = Q < 32 ? Q : 32;
-    uint32_t seq = 0;
+    uint32_t seq = 0, turn = 0;
+    uint8_t *const places = ring_ptr + G::stages * G::stage + warp * 8192;
     bool ok = true;
     for (int t = cta; ok && t < walk.total; t += ctas) {
       int e, row0, rows, nt;
@@ -528,7 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
         }
       }
       if (!ok) break;
-      if (!any || !on) continue;
+      if (!any) continue;
+      // A warp whose 32 rows all exist; rows behind a group's last one belong to another tile.
+      const bool bulk = PAIR && p.bulk && rows >= quarter * 32 + 32;
+      if (!bulk && !on) continue;
       void *dst = static_cast<uint8_t *>(p.g.out) + static_cast<int64_t>(row) * p.g.out_stride * size;
       if (swiglu) {
         if (bf16) {
@@ -538,6 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
 #pragma unroll
           for (int j = 0; j < Q; ++j) v0[j] = silu(v0[j] * s) * (v1[j] * s);
         }
+        if constexpr (PAIR) {
+          if (bulk) {
+            bulk_run(&p.out, places, turn, n0, row0 + quarter * 32, p.out_n, v0, bf16);
+            continue;
+          }
+        }
         store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, wide);
       } else {
 #pragma unroll
@@ -545,10 +598,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
           v0[j] *= s;
           v1[j] *= s;
         }
+        if constexpr (PAIR) {
+          if (bulk) {
+            bulk_run(&p.out, places, turn, n0, row0 + quarter * 32, p.out_n, v0, bf16);
+            bulk_run(&p.out, places, turn, n0 + Q, row0 + quarter * 32, p.out_n, v1, bf16);
+            continue;
+          }
+        }
         store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, wide);
         if (n0 + Q < p.out_n) store_cols<Q>(dst, n0 + Q, p.out_n - n0 - Q, v1, bf16, wide);
       }
     }
+  }
+  if constexpr (PAIR) {  // no exit with stores still reading shared memory
+    if (warp < kEpiWarps && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
   __syncwarp();
   tc_fence_before();
@@ -668,10 +731,18 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t 
   const uint32_t b_box = kernel == kExpertPairs || kernel == 256 ? 128 : kernel / 2;
   bool ok = encode_operand(&p.b, a.b, !fp4, k_row, E * a.N, k_row, b_box);
   if (a.rows == nullptr) {
-    ok = ok && encode_operand(&p.a[2], a.a, !fp4, k_row, a.m, a.a_stride, 128);
-    if (kernel != kExpertPairs && (a.offsets || a.m % kBm != 0))
-      ok = ok && encode_operand(&p.a[0], a.a, !fp4, k_row, a.m, a.a_stride, 32) &&
-           encode_operand(&p.a[1], a.a, !fp4, k_row, a.m, a.a_stride, 64);
+    // the boxes that some tile's rows may ask for
+    const bool pairs = kernel == kExpertPairs, partial = a.offsets != nullptr || a.m % kBm != 0;
+    if (pairs || a.m > 64) ok = ok && encode_operand(&p.a[2], a.a, !fp4, k_row, a.m, a.a_stride, 128);
+    if (!pairs && partial && a.m > 32) ok = ok && encode_operand(&p.a[1], a.a, !fp4, k_row, a.m, a.a_stride, 64);
+    if (!pairs && partial) ok = ok && encode_operand(&p.a[0], a.a, !fp4, k_row, a.m, a.a_stride, 32);
+  }
+  // Bulk stores end a row on a 16-byte boundary: with another width they would write zeros into the columns behind it.
+  const int per16 = a.out_bf16 ? 8 : 4;
+  if (ok && kernel == kExpertPairs && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_stride % per16 == 0 &&
+      p.out_n % per16 == 0) {
+    ok = encode_rows(&p.out, a.out, a.out_bf16, p.out_n, a.m, a.out_stride);
+    p.bulk = 1;
   }
   if (!ok) return cudaErrorInvalidValue;
   if (a.kind == EPOCH_EXPERT_BF16) return launch_kind<0>(p, kernel, s);

@@ -342,10 +342,10 @@ def route(logits: torch.Tensor, top_k: int, *, router: str = "softmax", bias: Op
     if n * top_k > _MOST - 256:
         raise ValueError("more than 2^31 - 257 edges")
     if out is None:
-        i32 = torch.int32
-        out = Routing(_empty((n, top_k), i32, logits.device, stream), _empty((n, top_k), torch.float32, logits.device, stream),
-                      _empty((n * top_k,), i32, logits.device, stream), _empty((e + 1,), i32, logits.device, stream),
-                      _empty((n, top_k), i32, logits.device, stream))
+        at = logits.device
+        sel, slots, positions = _empty((3, n, top_k), torch.int32, at, stream).unbind(0)  # one allocation: it is what costs
+        out = Routing(sel, _empty((n, top_k), torch.float32, at, stream), positions.view(-1),
+                      _empty((e + 1,), torch.int32, at, stream), slots)
     else:
         for t, d, shape, what in ((out.sel, torch.int32, (n, top_k), "out.sel"), (out.weights, torch.float32, (n, top_k), "out.weights"),
                                   (out.positions, torch.int32, (n * top_k,), "out.positions"),
@@ -400,18 +400,25 @@ def combine(edges: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, 
     return out
 
 
-def _expert(kind, x, w, sa, sb, offsets, rows, scale, swiglu, out, out_dtype, m, n_src, k, x_stride, dev, stream):
+def _expert(kind, x, xp, w, wp, sa, sb, offsets, rows, scale, swiglu, out, out_dtype, m, n_src, k, x_stride, dev, stream):
     """The product of experts, its operands checked: offsets, factors, output and the call."""
-    if w.dim() != (2 if offsets is None else 3):
-        raise ValueError("weights must be [N, K], or [E, N, K] with offsets")
-    n = w.shape[-2]
-    groups = 1 if offsets is None else w.shape[0]
-    op = _index(offsets, dev, "offsets") or 0
-    if offsets is not None and offsets.shape[0] != groups + 1:
-        raise ValueError(f"offsets must have {groups + 1} entries")
-    if swiglu and n % 2:
-        raise ValueError("swiglu needs an even number of rows of weights")
-    width = n // 2 if swiglu else n
+    shape = w.shape
+    if offsets is None:
+        groups, op = 1, 0
+        if len(shape) != 2:
+            raise ValueError("weights must be [N, K], or [E, N, K] with offsets")
+    else:
+        groups, op = shape[0], _index(offsets, dev, "offsets")
+        if len(shape) != 3:
+            raise ValueError("weights must be [N, K], or [E, N, K] with offsets")
+        if offsets.shape[0] != groups + 1:
+            raise ValueError(f"offsets must have {groups + 1} entries")
+    n = shape[-2]
+    width = n
+    if swiglu:
+        if n % 2:
+            raise ValueError("swiglu needs an even number of rows of weights")
+        width = n // 2
     number, fp = 1.0, 0
     if isinstance(scale, torch.Tensor):
         fp = _of(scale, dev, torch.float32, (groups,), "scale")
@@ -424,8 +431,8 @@ def _expert(kind, x, w, sa, sb, offsets, rows, scale, swiglu, out, out_dtype, m,
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
     else:
         ys = _rows(out, dev, (m, width), "out")
-    args = B.EXPERT_ARGS.pack(x.data_ptr(), w.data_ptr(), sa, sb, op, rows, fp, out.data_ptr(), x_stride, ys, number, groups, m,
-                              n_src, n, k, kind, 1 if swiglu else 0, _code(out, "out"))
+    args = B.EXPERT_ARGS.pack(xp, wp, sa, sb, op, rows, fp, out.data_ptr(), x_stride, ys, number, groups, m, n_src, n, k, kind,
+                              1 if swiglu else 0, _code(out, "out"))
     B.check(B.lib().epoch_expert_matmul(args, _stream(stream, dev)), "epoch_expert_matmul")
     return out
 
@@ -455,8 +462,8 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
         raise ValueError("rows has more than 2^31 - 1 entries")
     if out is None and out_dtype is None:
         out_dtype = x.dtype
-    return _expert(B.EPOCH_EXPERT_BF16 if code == B.EPOCH_BF16 else B.EPOCH_EXPERT_F32, x, w, 0, 0, offsets, rp, 1.0, swiglu, out,
-                   out_dtype, m, src, k, xs, dev, stream)
+    return _expert(B.EPOCH_EXPERT_BF16 if code == B.EPOCH_BF16 else B.EPOCH_EXPERT_F32, x, x.data_ptr(), w, w.data_ptr(), 0, 0,
+                   offsets, rp, 1.0, swiglu, out, out_dtype, m, src, k, xs, dev, stream)
 
 
 # format: (code, columns that share a scale, the scales' dtype, the product's kind)
@@ -473,16 +480,23 @@ def _fp4(form: str):
 
 
 def _fp4_operand(q: torch.Tensor, scales: torch.Tensor, dev: int, what: str):
-    """(pointers of values and scales, K, the format) of a packed operand [.., n, K / 2]."""
+    """(pointers of values and scales, K, the format) of a packed operand [n, K / 2] or [E, n, K / 2]."""
     f = _FP4_OF.get(scales.dtype)
     if f is None:
         raise ValueError(f"{what}_scales must be float8_e4m3fn (nvfp4) or float8_e8m0fnu (mxfp4), not {scales.dtype}")
-    if q.dim() < 2 or max(q.shape) > _MOST // 2:
-        raise ValueError(f"{what} must be [.., n, K / 2] of at most 2^30 rows and columns")
-    k = 2 * q.shape[-1]
-    lead, n = tuple(q.shape[:-2]), q.shape[-2]
-    return (_of(q, dev, torch.uint8, tuple(q.shape), what),
-            _of(scales, dev, f[2], lead + (-(-k // 256), n, 256 // f[1]), what + "_scales"), k, f)
+    shape = q.shape
+    dims = len(shape)
+    if dims not in (2, 3) or q.dtype != torch.uint8 or q.get_device() != dev or not q.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous uint8 tensor [(E,) n, K / 2] on cuda:{dev}")
+    n, half = shape[-2], shape[-1]
+    if half > _MOST // 2 or n > _MOST or shape[0] > _MOST:
+        raise ValueError(f"{what} has more than 2^31 - 1 matrices, rows or columns")
+    want = (-(-half // 128), n, 256 // f[1])
+    if dims == 3:
+        want = (shape[0], *want)
+    if scales.shape != want or scales.get_device() != dev or not scales.is_contiguous():
+        raise ValueError(f"{what}_scales must be a contiguous tensor {list(want)} on cuda:{dev}")
+    return q.data_ptr(), scales.data_ptr(), 2 * half, f
 
 
 def fp4_quantize(x: torch.Tensor, *, form: str = "nvfp4", rows: Optional[torch.Tensor] = None, swiglu: bool = False,
@@ -587,10 +601,11 @@ def fp4_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     if a.dim() != 2:
         raise ValueError("a must be [m, K / 2]")
     ap, asp, k, f = _fp4_operand(a, a_scales, dev, "a")
-    _, bsp, kb, fb = _fp4_operand(b, b_scales, dev, "b")
+    bp, bsp, kb, fb = _fp4_operand(b, b_scales, dev, "b")
     if kb != k or fb is not f:
         raise ValueError("a and b must have the same K and the same format")
-    return _expert(f[3], a, b, asp, bsp, offsets, 0, scale, swiglu, out, out_dtype, a.shape[0], a.shape[0], k, k // 2, dev, stream)
+    m = a.shape[0]
+    return _expert(f[3], a, ap, b, bp, asp, bsp, offsets, 0, scale, swiglu, out, out_dtype, m, m, k, k // 2, dev, stream)
 
 
 def status(clear: bool = False, stream=None):
