@@ -331,61 +331,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
         }
     } else if (FP4 != 0 && warp >= kEpiWarps + 4 && warp < kEpiWarps + 4 + helpers) {  // scales, a group of 128 rows a warp
       constexpr int kPer = FP4 * 4;            // scales of a row in a stage
-      constexpr int kAhead = 3;                // stages whose scales are on their way
-      const int group = warp - kEpiWarps - 4;  // 0: a's rows; 1, 2: the weights'
+      constexpr int kAhead = FP4 == 4 ? 3 : 5;  // stages whose scales are on their way, the next tile's among them
+      const int group = warp - kEpiWarps - 4;   // 0: a's rows; 1, 2: the weights'
       const uint32_t filled = PAIR && rank ? ready : full;
-      uint32_t st = 0, phase = 1;
-      bool ok = true;
-      for (int t = cta; ok && t < walk.total; t += ctas) {
-        int e, row0, rows, nt;
-        walk.at(t, &e, &row0, &rows, &nt);
-        const uint8_t *src[4];
+      const int steps = walk.total > cta ? (walk.total - cta + ctas - 1) / ctas * p.kb_n : 0;
+      const int64_t step = static_cast<int64_t>(group == 0 ? p.g.m : p.g.N) * kPer;  // bytes between K blocks
+      const uint8_t *src[4];
+      int fetch_t = cta, fetch_kb = 0;  // what is loaded next
+      uint32_t v[kAhead][4][FP4 ? FP4 : 1];
+      auto load = [&](uint32_t (&u)[4][FP4 ? FP4 : 1]) {
+        if (fetch_t >= walk.total) return;
+        if (fetch_kb == 0) {
+          int e, row0, rows, nt;
+          walk.at(fetch_t, &e, &row0, &rows, &nt);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // rows that do not exist read one that does
-          const int r = 32 * c + lane;
-          if (group == 0) {
-            src[c] = p.g.sa + static_cast<int64_t>(min(row0 + r, p.g.m - 1)) * kPer;
-          } else {
-            const int j = min((group - 1) * 128 + r, BN - 1);
-            const int n = !p.g.swiglu ? nt * BN + j : j < BN / 2 ? nt * (BN / 2) + j : half_n + nt * (BN / 2) + j - BN / 2;
-            src[c] = p.g.sb + (static_cast<int64_t>(e) * p.kb_n * p.g.N + min(n, p.g.N - 1)) * kPer;
+          for (int c = 0; c < 4; ++c) {  // rows that do not exist read one that does
+            const int r = 32 * c + lane;
+            if (group == 0) {
+              src[c] = p.g.sa + static_cast<int64_t>(min(row0 + r, p.g.m - 1)) * kPer;
+            } else {
+              const int j = min((group - 1) * 128 + r, BN - 1);
+              const int n = !p.g.swiglu ? nt * BN + j : j < BN / 2 ? nt * (BN / 2) + j : half_n + nt * (BN / 2) + j - BN / 2;
+              src[c] = p.g.sb + (static_cast<int64_t>(e) * p.kb_n * p.g.N + min(n, p.g.N - 1)) * kPer;
+            }
           }
         }
-        const int64_t step = static_cast<int64_t>(group == 0 ? p.g.m : p.g.N) * kPer;  // bytes between K blocks
-        uint32_t v[kAhead][4][FP4 ? FP4 : 1];
-        auto load = [&](int kb, uint32_t (&u)[4][FP4 ? FP4 : 1]) {
-          if (kb >= p.kb_n) return;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint8_t *at = src[c] + kb * step;
-            if constexpr (FP4 == 4) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at));
-              u[c][0] = x.x, u[c][1] = x.y, u[c][2] = x.z, u[c][3] = x.w;
-            } else if constexpr (FP4 == 2) {
-              const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at));
-              u[c][0] = x.x, u[c][1] = x.y;
-            }
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (FP4 == 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src[c]));
+            u[c][0] = x.x, u[c][1] = x.y, u[c][2] = x.z, u[c][3] = x.w;
+          } else if constexpr (FP4 == 2) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src[c]));
+            u[c][0] = x.x, u[c][1] = x.y;
           }
-        };
+          src[c] += step;
+        }
+        if (++fetch_kb == p.kb_n) {
+          fetch_kb = 0;
+          fetch_t += ctas;
+        }
+      };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(i, v[i]);
-        for (int kb0 = 0; ok && kb0 < p.kb_n; kb0 += kAhead) {
+      for (int i = 0; i < kAhead; ++i) load(v[i]);
+      uint32_t st = 0, phase = 1;
+      bool ok = true;
+      for (int n = 0; ok && n < steps; n += kAhead) {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            if (kb0 + i >= p.kb_n) break;
-            ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
-            if (!ok) break;
-            uint8_t *dst = ring_ptr + st * G::stage + G::operands + group * FP4 * 512 + lane * 16;
+        for (int i = 0; i < kAhead; ++i) {
+          if (n + i >= steps) break;
+          ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
+          if (!ok) break;
+          uint8_t *dst = ring_ptr + st * G::stage + G::operands + group * FP4 * 512 + lane * 16;
 #pragma unroll
-            for (int k = 0; k < FP4; ++k)
-              *reinterpret_cast<uint4 *>(dst + k * 512) = make_uint4(v[i][0][k], v[i][1][k], v[i][2][k], v[i][3][k]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(filled + 8 * st);
-            load(kb0 + i + kAhead, v[i]);
-            if (++st == G::stages) {
-              st = 0;
-              phase ^= 1u;
-            }
+          for (int k = 0; k < FP4; ++k)
+            *reinterpret_cast<uint4 *>(dst + k * 512) = make_uint4(v[i][0][k], v[i][1][k], v[i][2][k], v[i][3][k]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(filled + 8 * st);
+          load(v[i]);
+          if (++st == G::stages) {
+            st = 0;
+            phase ^= 1u;
           }
         }
       }
@@ -403,17 +409,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(filled + 8 * (i % G::stages));
       };
-      for (int t = cta; ok && t < walk.total; t += ctas) {
-        int e, row0, rows, nt;
-        walk.at(t, &e, &row0, &rows, &nt);
-        const __nv_bfloat16 *src[8];
+      int from[8], rows = 0, next_rows = 0;  // the next tile's rows of x are read while this one's are copied
+      auto look = [&](int t) {
+        if (t >= walk.total) return;
+        int e, row0, nt;
+        walk.at(t, &e, &row0, &next_rows, &nt);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * (4 * i + w) + (lane >> 3);
-          int from = r < rows ? __ldg(p.g.rows + row0 + r) : 0;
-          if (from < 0 || from >= p.g.n_src) from = 0;  // never followed; whatever is read instead, the result is NaN
-          src[i] = base + from * p.g.a_stride + 8 * chunk;
+          from[i] = r < next_rows ? __ldg(p.g.rows + row0 + r) : 0;
         }
+      };
+      look(cta);
+      for (int t = cta; ok && t < walk.total; t += ctas) {
+        const __nv_bfloat16 *src[8];
+        rows = next_rows;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // an index out of range is never followed; whatever is read instead, the result is NaN
+          const int x = from[i] < 0 || from[i] >= p.g.n_src ? 0 : from[i];
+          src[i] = base + x * p.g.a_stride + 8 * chunk;
+        }
+        look(t + ctas);
         for (int kb = 0; kb < p.kb_n; ++kb, ++it) {
           ok = warp_wait(empty + 8 * st, phase, abort, p.err, p.timeout_ns);
           if (!ok) break;
