@@ -45,7 +45,7 @@ struct ExpertParams {
   ExpertGemmArgs g;
   int kb_n, nt_n;    // K blocks, tiles along N
   int out_n;         // columns of the output
-  int wide;          // output rows start on 32-byte boundaries
+  int align;         // bytes on which output rows start: 32, 16 or less
   int bulk;          // the output has a tensor map: its rows start and end on 16-byte boundaries
   int reuse;         // weights are read by several row tiles
   int acc_kb;        // K blocks that an accumulator sums before it is added to the fp32 sums in registers
@@ -140,42 +140,57 @@ template <int Q> __device__ __forceinline__ void load_cols(uint32_t at, float (&
   }
 }
 
-// Q consecutive values of an output row from column n0 on, `n` of which exist.
-template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, int n, const float (&v)[Q], bool bf16, bool wide) {
+// Q consecutive values of an output row from column n0 on, `n` of which exist, in accesses of `align` bytes: 32 (whole
+// sectors), 16 or the elements.
+template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, int n, const float (&v)[Q], bool bf16, int align) {
+  constexpr int kRun = Q < 16 ? Q : 16;
   if (bf16) {
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(row) + n0;
-    if (wide && n >= Q) {
-      uint32_t w[Q / 2];
 #pragma unroll
-      for (int j = 0; j < Q / 2; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t *>(&h);
+    for (int j = 0; j < Q; j += kRun) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < kRun / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
       }
-      if constexpr (Q >= 16) {
-#pragma unroll
-        for (int j = 0; j < Q / 2; j += 8) store32(dst + 2 * j, reinterpret_cast<const uint32_t (&)[8]>(w[j]));
-      } else {
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (kRun == 16 && align >= 32 && j + 16 <= n) {
+        store32(dst + j, w);
+        continue;
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < Q; ++j)
-        if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
+      for (int c = 0; c < kRun; c += 8) {
+        if (align >= 16 && j + c + 8 <= n) {
+          *reinterpret_cast<uint4 *>(dst + j + c) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (j + c + i < n)
+              reinterpret_cast<uint16_t *>(dst)[j + c + i] = static_cast<uint16_t>(i & 1 ? w[(c + i) / 2] >> 16 : w[(c + i) / 2]);
+        }
+      }
     }
   } else {
     float *dst = static_cast<float *>(row) + n0;
-    if (wide && n >= Q) {
 #pragma unroll
-      for (int j = 0; j < Q; j += 8) {
+    for (int j = 0; j < Q; j += 8) {
+      if (align >= 32 && j + 8 <= n) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[j + i]);
         store32(dst + j, w);
+        continue;
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < Q; ++j)
-        if (j < n) dst[j] = v[j];
+      for (int c = j; c < j + 8; c += 4) {
+        if (align >= 16 && c + 4 <= n) {
+          *reinterpret_cast<float4 *>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        } else {
+#pragma unroll
+          for (int i = c; i < c + 4; ++i)
+            if (i < n) dst[i] = v[i];
+        }
+      }
     }
   }
 }
@@ -476,52 +491,66 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
           }
       }
     } else if (warp == kEpiWarps + 1 && rank == 0) {  // ------------------------ MMA
-      // The warp stays together and one elected lane issues, so that descriptors and barriers are uniform values.
+      // The warp stays together and one elected lane issues, so that descriptors and barriers are uniform values. Two
+      // stages a turn: a turn costs this warp some 300 clocks beside its products' 512 a stage (waits that are over,
+      // fences, the election), which bound small tiles.
       constexpr uint32_t idesc = idesc_of<FP4>(G::bm, BN);
+      constexpr bool kTwo = G::stages >= 6;
       uint32_t it = 0, st = 0, phase = 0, seq = 0;  // seq: accumulators begun
       bool ok = true;
       for (int t = cta; ok && t < walk.total; t += ctas) {
-        for (int kb = 0, part = 0; kb < p.kb_n; ++kb, ++it) {
+        for (int kb = 0, part = 0; kb < p.kb_n;) {
           const uint32_t buf = seq % G::bufs;
-          if (part == 0) {
-            ok = warp_wait(tempty + 8 * buf, ((seq / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns);
+          // (accumulators of fewer K blocks take an even number of them)
+          const int two = kTwo && kb + 1 < p.kb_n;
+          const uint32_t st1 = st + 1 == G::stages ? 0 : st + 1, phase1 = st1 ? phase : phase ^ 1u;
+          const bool r0 = mbar_try_wait(full + 8 * st, phase), r1 = !two || mbar_try_wait(full + 8 * st1, phase1);
+          const bool r2 = part > 0 || mbar_try_wait(tempty + 8 * buf, ((seq / G::bufs) & 1u) ^ 1u);
+          if (!__all_sync(0xffffffffu, r0 && r1 && r2)) {
+            ok = (part > 0 || warp_wait(tempty + 8 * buf, ((seq / G::bufs) & 1u) ^ 1u, abort, p.err, p.timeout_ns)) &&
+                 warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns) &&
+                 (!two || warp_wait(full + 8 * st1, phase1, abort, p.err, p.timeout_ns));
             if (!ok) break;
           }
-          ok = warp_wait(full + 8 * st, phase, abort, p.err, p.timeout_ns);
-          if (!ok) break;
           if (helpers) fence_proxy_async_smem();
           tc_fence_after();
-          const uint32_t src = ring + st * G::stage;
-          const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kRow);
-          const uint32_t sa = tmem + G::bufs * BN + (it & 3u) * G::place, sb = sa + 4 * FP4;
+          const bool last = part + 1 + two == p.acc_kb || kb + 1 + two == p.kb_n;
           if (elect_one()) {
-            if constexpr (FP4 != 0) {
 #pragma unroll
-              for (int k = 0; k < FP4; ++k) {
-                copy_scales<PAIR>(sa + 4 * k, src + G::operands + k * 512);
+            for (int i = 0; i < 2; ++i) {
+              if (i == 1 && !two) break;
+              const uint32_t src = ring + (i ? st1 : st) * G::stage;
+              const uint64_t ad = sw128_kmajor_desc(src), bd = sw128_kmajor_desc(src + kBm * kRow);
+              const uint32_t sa = tmem + G::bufs * BN + ((it + i) & 3u) * G::place, sb = sa + 4 * FP4;
+              if constexpr (FP4 != 0) {
 #pragma unroll
-                for (int g = 0; g < G::groups_b; ++g)
-                  copy_scales<PAIR>(sb + G::cols_b * k + 4 * g, src + G::operands + ((1 + g) * FP4 + k) * 512);
+                for (int k = 0; k < FP4; ++k) {
+                  copy_scales<PAIR>(sa + 4 * k, src + G::operands + k * 512);
+#pragma unroll
+                  for (int g = 0; g < G::groups_b; ++g)
+                    copy_scales<PAIR>(sb + G::cols_b * k + 4 * g, src + G::operands + ((1 + g) * FP4 + k) * 512);
+                }
               }
-            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // 32 bytes of columns an instruction
-              // two products share a chunk of e8m0 scales: the second takes its upper half
-              const int chunk = FP4 == 2 ? k / 2 : k;
-              const uint32_t id = FP4 == 2 && (k & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
-              mma<FP4, PAIR>(tmem + buf * BN, ad + 2 * k, bd + 2 * k, id, sa + 4 * chunk, sb + G::cols_b * chunk,
-                             part > 0 || k > 0);
+              for (int k = 0; k < 4; ++k) {  // 32 bytes of columns an instruction
+                // two products share a chunk of e8m0 scales: the second takes its upper half
+                const int chunk = FP4 == 2 ? k / 2 : k;
+                const uint32_t id = FP4 == 2 && (k & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
+                mma<FP4, PAIR>(tmem + buf * BN, ad + 2 * k, bd + 2 * k, id, sa + 4 * chunk, sb + G::cols_b * chunk,
+                               part > 0 || i > 0 || k > 0);
+              }
+              commit<PAIR>(empty + 8 * (i ? st1 : st));
             }
-            commit<PAIR>(empty + 8 * st);
-            if (part == p.acc_kb - 1 || kb == p.kb_n - 1) commit<PAIR>(tfull + 8 * buf);
+            if (last) commit<PAIR>(tfull + 8 * buf);
           }
           __syncwarp();
-          if (++part == p.acc_kb) part = 0;
-          if (part == 0 || kb == p.kb_n - 1) ++seq;
-          if (++st == G::stages) {
-            st = 0;
-            phase ^= 1u;
-          }
+          kb += 1 + two;
+          it += 1 + two;
+          part = last ? 0 : part + 1 + two;
+          seq += last;
+          const uint32_t next = st + 1 + two;
+          st = next < G::stages ? next : next - G::stages;
+          if (next >= G::stages) phase ^= 1u;
         }
       }
       // no exit with products in flight: the last stages have been read
@@ -534,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
     take_registers<kRegsMany>();
     const uint32_t read = PAIR ? mapa_shared(tempty, 0) : tempty;  // the barriers that the MMA thread waits on
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 32, half of the columns
-    const bool swiglu = p.g.swiglu != 0, bf16 = p.g.out_bf16 != 0, wide = p.wide != 0;
+    const bool swiglu = p.g.swiglu != 0, bf16 = p.g.out_bf16 != 0;
     const int c0 = swiglu ? half * Q : half * 2 * Q, c1 = swiglu ? BN / 2 + half * Q : c0 + Q;
     const size_t size = bf16 ? 2 : 4;
     constexpr int kPiece = Q < 32 ? Q : 32;
@@ -608,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
             continue;
           }
         }
-        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, wide);
+        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, p.align);
       } else {
 #pragma unroll
         for (int j = 0; j < Q; ++j) {
@@ -622,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
             continue;
           }
         }
-        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, wide);
-        if (n0 + Q < p.out_n) store_cols<Q>(dst, n0 + Q, p.out_n - n0 - Q, v1, bf16, wide);
+        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, p.align);
+        if (n0 + Q < p.out_n) store_cols<Q>(dst, n0 + Q, p.out_n - n0 - Q, v1, bf16, p.align);
       }
     }
   }
@@ -704,37 +733,41 @@ template <int FP4> cudaError_t launch_kind(ExpertParams &p, int kernel, cudaStre
 }  // namespace
 
 // The tiles a product takes: the columns of a tile of single CTAs, kExpertPairs tiles of CTA pairs. n_groups 0: dense.
-int expert_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms) {
-  const int64_t E = n_groups ? n_groups : 1;
-  // The tile whose rounds of tiles take the least time. Pairs need groups that fill 256 rows.
-  const int64_t mt = m / kBm + (n_groups ? (E < m ? E : m) : (m % kBm != 0));
-  auto cost = [&](int64_t tiles, int64_t at_once, int64_t clocks) { return (tiles + at_once - 1) / at_once * clocks; };
+// The one whose rounds of tiles take the least time, by the nanoseconds that a K block of each took with many tiles
+// (64 groups, 32768 rows by 2048 x 2048). Wide tiles are bound by what an SM takes in from L2 (about 50 bytes a clock),
+// narrow ones by the MMA warp's turns. A group is expected to end in the middle of a tile.
+int expert_gemm_kernel(bool fp4, int n_groups, int64_t m, int64_t N, int sms) {
+  const int64_t E = n_groups ? (n_groups < m ? n_groups : m) : 1;
+  auto tiles = [&](int64_t rows) {
+    const int64_t t = n_groups ? m / rows + E / 2 : (m + rows - 1) / rows;
+    return t > E ? t : E;
+  };
+  static const int64_t kCost[5][3] = {{256, 420, 790}, {128, 250, 555}, {64, 197, 430}, {32, 190, 390}, {kExpertPairs, 420, 600}};
   int bn = 256;
-  int64_t best = cost(mt * ((N + 255) / 256), sms, 1000);
-  const int64_t narrow[3][2] = {{128, 720}, {64, 600}, {32, 560}};
-  for (const auto &c : narrow) {
-    const int64_t t = cost(mt * ((N + c[0] - 1) / c[0]), sms, c[1]);
+  int64_t best = INT64_MAX;
+  for (const auto &c : kCost) {
+    const bool pairs = c[0] == kExpertPairs;
+    if (pairs && sms < 2) continue;
+    const int64_t n = tiles(pairs ? 256 : kBm) * ((N + (pairs ? 256 : c[0]) - 1) / (pairs ? 256 : c[0])), at_once = pairs ? sms / 2 : sms;
+    const int64_t t = (n + at_once - 1) / at_once * c[fp4 ? 2 : 1];
     if (t < best) {
       best = t;
       bn = static_cast<int>(c[0]);
     }
   }
-  if (m >= 256 * E && sms >= 2) {
-    const int64_t tiles = (m / 256 + (n_groups ? E : m % 256 != 0)) * ((N + 255) / 256);
-    if (cost(tiles, sms / 2, 1000) <= best) return kExpertPairs;
-  }
   return bn;
 }
 
 cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t timeout_ns, uint32_t hold) {
-  const int kernel = expert_gemm_kernel(a.offsets ? a.n_groups : 0, a.m, a.N, num_sms());
+  const bool fp4 = a.kind != EPOCH_EXPERT_BF16;
+  const int kernel = expert_gemm_kernel(fp4, a.offsets ? a.n_groups : 0, a.m, a.N, num_sms());
   ExpertParams p;
   memset(&p, 0, sizeof(p));
   p.g = a;
-  const bool fp4 = a.kind != EPOCH_EXPERT_BF16;
   p.kb_n = (a.K + (fp4 ? 255 : 63)) / (fp4 ? 256 : 64);
   p.out_n = a.swiglu ? a.N / 2 : a.N;
-  p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && a.out_stride % (a.out_bf16 ? 16 : 8) == 0;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.m > 1 ? a.out_stride * (a.out_bf16 ? 2 : 4) : 0);
+  p.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
   const int64_t E = a.offsets ? a.n_groups : 1;
   p.reuse = a.m > kBm * E;
   // The tensor core's sums drift by their truncation: over 1024 columns to 1e-6 of an fp32 result, four times what sums

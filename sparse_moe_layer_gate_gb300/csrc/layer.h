@@ -407,7 +407,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t 
                                uint32_t hold = 0);
 // expert_simt.cu (fp32 rows)
 cudaError_t launch_expert_simt(const ExpertGemmArgs &a, cudaStream_t s);
-int expert_gemm_kernel(int n_groups, int64_t m, int64_t N, int sms);
+int expert_gemm_kernel(bool fp4, int n_groups, int64_t m, int64_t N, int sms);
 
 // Device error word of the operators without a layer, on the current device (nullptr: none).
 uint32_t *ops_error_word();

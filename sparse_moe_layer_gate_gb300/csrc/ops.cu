@@ -527,7 +527,7 @@ epoch_status epoch_test_expert_timeout(const epoch_expert_args *p, int64_t timeo
 int32_t epoch_expert_matmul_kernel(int32_t kind, int32_t n_groups, int32_t m, int32_t n, int32_t k, int32_t n_sms) {
   if (kind < EPOCH_EXPERT_F32 || kind > EPOCH_EXPERT_MXFP4 || m < 0 || n < 1 || k < 1 || n_groups < 0 || n_groups > 1024 || n_sms < 0)
     return -1;
-  return kind == EPOCH_EXPERT_F32 ? 0 : expert_gemm_kernel(n_groups, m, n, n_sms ? n_sms : num_sms());
+  return kind == EPOCH_EXPERT_F32 ? 0 : expert_gemm_kernel(kind != EPOCH_EXPERT_BF16, n_groups, m, n, n_sms ? n_sms : num_sms());
 }
 
 epoch_status epoch_ops_status(int32_t clear, epoch_stream stream, uint32_t *word_out) {
