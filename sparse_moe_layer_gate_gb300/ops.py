@@ -341,21 +341,23 @@ def route(logits: torch.Tensor, top_k: int, *, router: str = "softmax", bias: Op
     lp, ep = _flags(live, dev, n, "live"), _flags(eligible, dev, e, "eligible")
     if n * top_k > _MOST - 256:
         raise ValueError("more than 2^31 - 257 edges")
+    i32, at = torch.int32, logits.device
     if out is None:
-        at = logits.device
-        sel, slots, positions = _empty((3, n, top_k), torch.int32, at, stream).unbind(0)  # one allocation: it is what costs
-        out = Routing(sel, _empty((n, top_k), torch.float32, at, stream), positions.view(-1),
-                      _empty((e + 1,), torch.int32, at, stream), slots)
+        out = Routing(_empty((n, top_k), i32, at, stream), _empty((n, top_k), torch.float32, at, stream),
+                      _empty((n * top_k,), i32, at, stream), _empty((e + 1,), i32, at, stream), _empty((n, top_k), i32, at, stream))
     else:
-        for t, d, shape, what in ((out.sel, torch.int32, (n, top_k), "out.sel"), (out.weights, torch.float32, (n, top_k), "out.weights"),
-                                  (out.positions, torch.int32, (n * top_k,), "out.positions"),
-                                  (out.offsets, torch.int32, (e + 1,), "out.offsets"), (out.slots, torch.int32, (n, top_k), "out.slots")):
+        for t, d, shape, what in ((out.sel, i32, (n, top_k), "out.sel"), (out.weights, torch.float32, (n, top_k), "out.weights"),
+                                  (out.positions, i32, (n * top_k,), "out.positions"), (out.offsets, i32, (e + 1,), "out.offsets"),
+                                  (out.slots, i32, (n, top_k), "out.slots")):
             _of(t, dev, d, shape, what)
-    need = B.lib().epoch_route_workspace_bytes(n, e)
-    ws = _empty((need,), torch.uint8, logits.device, stream) if need else None
-    args = B.ROUTE_ARGS.pack(logits.data_ptr(), bp, lp, ep, out.sel.data_ptr(), out.weights.data_ptr(), out.positions.data_ptr(),
-                             out.offsets.data_ptr(), out.slots.data_ptr(), ws.data_ptr() if need else 0, need, ls, n, e, top_k,
-                             code, kind, n_group, topk_group, 1 if raw_weights else 0)
+    lib, ws = B.lib(), 0
+    need = lib.epoch_route_workspace_bytes(n, e)
+    if need:
+        work = _empty((need,), torch.uint8, at, stream)
+        ws = work.data_ptr()
+    sel, weights, positions, offsets, slots = out
+    args = B.ROUTE_ARGS.pack(logits.data_ptr(), bp, lp, ep, sel.data_ptr(), weights.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
+                             slots.data_ptr(), ws, need, ls, n, e, top_k, code, kind, n_group, topk_group, 1 if raw_weights else 0)
     B.check(B.lib().epoch_route(args, _stream(stream, dev)), "epoch_route")
     return out
 

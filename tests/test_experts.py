@@ -331,7 +331,8 @@ def product_bound(y, size, steps, ot, swiglu):
 
 
 GROUPED = [(1, 1, 1, 8), (1, 8, 64, 64), (3, 2, 40, 72), (17, 5, 130, 200), (64, 64, 32, 128), (100, 3, 256, 512), (129, 1, 257, 1000),
-           (200, 130, 96, 256), (300, 4, 520, 264), (1000, 3, 768, 192), (2050, 2, 1024, 128), (700, 1, 2000, 64)]
+           (200, 130, 96, 256), (300, 4, 520, 264), (1000, 3, 768, 192), (2050, 2, 1024, 128), (700, 1, 2000, 64),
+           (1000, 1, 4096, 64), (900, 2, 4000, 192), (1100, 1, 4096, 136)]
 
 
 @pytest.mark.gpu
@@ -626,7 +627,8 @@ def fp4_operand(g, form, *shape, std=1.0):
 
 
 FP4 = [(1, 1, 1, 32), (1, 8, 64, 256), (3, 2, 40, 96), (17, 5, 130, 288), (64, 64, 32, 512), (100, 3, 256, 1024), (129, 1, 257, 800),
-       (200, 130, 96, 256), (300, 4, 520, 512), (1000, 3, 768, 320), (2050, 2, 1024, 256), (700, 1, 2000, 64), (600, 1, 4096, 768)]
+       (200, 130, 96, 256), (300, 4, 520, 512), (1000, 3, 768, 320), (2050, 2, 1024, 256), (700, 1, 2000, 64), (600, 1, 4096, 768),
+       (700, 64, 1024, 256)]
 
 
 @pytest.mark.gpu
@@ -714,3 +716,332 @@ def test_route_groups_that_fp32_cannot_tell_apart(ops, E, groups, top):
     for bias in (None, torch.zeros(E, device="cuda")):
         check_route(ops.route(x, k, router="sigmoid_group", bias=bias, n_group=groups, topk_group=top),
                     route64(x, k, True, bias=bias, n_group=groups, topk_group=top))
+
+
+# ------------------------------------------------------------------------------ streams and graphs
+def _steps(ops, seed, T=40):
+    """A run of every operator on buffers of its own: (the buffers that new inputs go to, the call, its outputs)."""
+    g = _gen(seed)
+    H, E, I, k = 256, 8, 128, 3
+    x, logits = _rnd(g, T, H, dtype=BF16), _rnd(g, T, E)
+    w13, w2 = _rnd(g, E, 2 * I, H, std=H ** -0.5, dtype=BF16), _rnd(g, E, H, I, std=I ** -0.5, dtype=BF16)
+    q13, s13, t13 = ops.fp4_quantize_weight(w13)
+    q2, s2, t2 = ops.fp4_quantize_weight(w2, form="mxfp4")
+
+    def call(stream=None):
+        r = ops.route(logits, k, stream=stream)
+        a = ops.grouped_matmul(x, w13, r.offsets, rows=r.positions, swiglu=True, stream=stream)
+        o = ops.grouped_matmul(a, w2, r.offsets, stream=stream)
+        y = ops.combine(o, r.slots, r.weights, residual=x, stream=stream)
+        q, s = ops.fp4_quantize(x, rows=r.positions, stream=stream)
+        gu = ops.fp4_matmul(q, s, q13, s13, offsets=r.offsets, scale=t13, stream=stream)
+        q, s = ops.fp4_quantize(gu, form="mxfp4", swiglu=True, stream=stream)
+        o4 = ops.fp4_matmul(q, s, q2, s2, offsets=r.offsets, scale=t2, out_dtype=F32, stream=stream)
+        v = ops.fp4_dequantize(q, s, stream=stream)
+        y4 = ops.combine(o4, r.slots, r.weights, out_dtype=BF16, stream=stream)
+        return (*r, a, o, y, v, y4)
+
+    return (x, logits), call
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_operators_on_a_stream_of_their_own_and_in_a_graph(ops, T):
+    inputs, call = _steps(ops, T, T)
+    want = call()
+    assert all(bool(t.float().isfinite().all()) for t in want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(side)
+    side.synchronize()
+    assert _same(got, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    g = _gen(99)
+    old = [t.clone() for t in inputs]
+    for turn in range(3):
+        for t, o in zip(inputs, old):
+            t.copy_(o if turn == 2 else _rnd(g, *t.shape, dtype=t.dtype))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in out]
+        assert _same(replayed, call())
+    assert _same(replayed, want)
+
+
+@pytest.mark.gpu
+def test_runs_on_two_streams_at_once_and_two_graphs(ops):
+    sets = [_steps(ops, s, T)[1] for s, T in ((1, 200), (2, 33))]
+    want = [c() for c in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, c in enumerate(sets):
+            got[i].append(c(streams[i]))
+    torch.cuda.synchronize()
+    assert all(_same(o, want[i]) for i in range(2) for o in got[i])
+    graphs, outs = [], []
+    for c in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(c())
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(_same(outs[i], want[i]) for i in range(2))
+    assert ops.status() == (0, 0)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+sys.path.insert(0, {root!r} + "/tests")
+import torch
+from sparse_moe_layer_gate_gb300 import ops
+T, H, E, I, k = {T}, 256, 8, 128, 3
+d = dict(device="cuda", dtype=torch.bfloat16)
+x, logits = torch.randn(T, H, **d), torch.randn(T, E, device="cuda")
+w = torch.randn(E, 2 * I, H, **d) / 16
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+def call():
+    qw, sw, tw = ops.fp4_quantize_weight(w)
+    r = ops.route(logits, k)
+    a = ops.grouped_matmul(x, w, r.offsets, rows=r.positions)
+    q, s = ops.fp4_quantize(x, rows=r.positions)
+    f = ops.fp4_matmul(q, s, qw, sw, offsets=r.offsets, scale=tw)
+    return (*r, a, f, ops.combine(a, r.slots, r.weights), ops.fp4_dequantize(q, s), ops.grouped_matmul(x.float(), w.float(), r.offsets, rows=r.positions))
+with torch.cuda.graph(g):
+    out = call()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, call())) and ops.status() == (0, 0)
+print("same")
+"""
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 100, 2000])
+def test_a_process_whose_first_calls_are_captured(ops, T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root, T=T)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+WIDTHS = [32, 64, 128, 256, 512]  # columns of a tile; 512: pairs
+
+
+def test_every_kernel_of_the_products_is_reached(lib):
+    """The sizes above take each width of tiles, and pairs, on a device of 152 SMs."""
+    for kind, sizes in ((1, GROUPED), (2, FP4), (3, FP4)):
+        assert {lib.epoch_expert_matmul_kernel(kind, e, m, n, k, 152) for m, e, n, k in sizes} == set(WIDTHS), kind
+    assert lib.epoch_expert_matmul_kernel(0, 2, 10, 64, 64, 152) == 0
+
+
+def _taking(lib, kind, kernel):
+    """Rows, groups and columns that take the kernel here."""
+    for m, e in ((40, 1), (130, 1), (300, 1), (700, 1), (1100, 1), (1500, 1), (3000, 1), (700, 64)):
+        for n in (64, 256, 512, 1024, 2048, 4096):
+            if lib.epoch_expert_matmul_kernel(kind, e, m, n, 1024, 0) == kernel:
+                return m, e, n
+    raise AssertionError((kind, kernel))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["bf16", "bf16_gather", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("kernel", WIDTHS)
+def test_waits_that_run_out(ops, lib, form, kernel):
+    """Operand copies that count bytes that never come: the status, an untouched output, and the same bits afterwards."""
+    from sparse_moe_layer_gate_gb300 import binding as B
+    kind = {"nvfp4": B.EPOCH_EXPERT_NVFP4, "mxfp4": B.EPOCH_EXPERT_MXFP4}.get(form, B.EPOCH_EXPERT_BF16)
+    m, e, n = _taking(lib, kind, kernel)
+    k, g = 1024, _gen(kernel)
+    off = (torch.arange(e + 1, device="cuda") * m // e).to(I32)
+    y = torch.full((m, n), -3.0, device="cuda", dtype=BF16)
+    rows = torch.arange(m, device="cuda", dtype=I32) if form == "bf16_gather" else None
+    if kind == B.EPOCH_EXPERT_BF16:
+        x, w = _rnd(g, m, k, dtype=BF16), _rnd(g, e, n, k, std=k ** -0.5, dtype=BF16)
+        sx = sw = None
+        want = ops.grouped_matmul(x, w, off, rows=rows)
+    else:
+        x, sx = ops.fp4_quantize(_rnd(g, m, k), form=form)
+        w, sw, _ = ops.fp4_quantize_weight(_rnd(g, e, n, k), form=form)
+        want = ops.fp4_matmul(x, sx, w, sw, offsets=off)
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    args = B.EXPERT_ARGS.pack(ptr(x), ptr(w), ptr(sx), ptr(sw), ptr(off), ptr(rows), 0, ptr(y), k, n, 1.0, e, m, m, n, k, kind,
+                              0, B.EPOCH_BF16)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert ops.status() == (0, 0)
+    assert B.lib().epoch_test_expert_timeout(args, 2_000_000, stream) == 0
+    code, word = ops.status(clear=True)
+    assert code == B.EPOCH_ETIMEOUT and word == B.EPOCH_DEVERR_TIMEOUT
+    assert bool((y == -3).all())
+    assert B.lib().epoch_expert_matmul(args, stream) == 0
+    assert torch.equal(y, want) and ops.status() == (0, 0)
+    assert B.lib().epoch_test_expert_timeout(args, 999, stream) == 1  # EPOCH_EINVAL
+
+
+# ---------------------------------------------------------------------------------------- refusals
+P = 1 << 20  # a pointer that is never followed: every call below is refused on the host, or has no rows
+
+
+@pytest.fixture(scope="module")
+def lib(ops):
+    from sparse_moe_layer_gate_gb300 import binding
+    return binding.lib()
+
+
+ROUTE = dict(logits=P, bias=0, live=0, eligible=0, sel=P, weights=P, positions=P, offsets=P, slots=P, ws=0, bytes=0, stride=64,
+             n=4, experts=64, k=4, dtype=0, router=0, groups=1, top=1, raw=0)
+COMBINE = dict(edges=P, shared=0, residual=0, slots=P, weights=P, out=P, es=64, ss=64, rs=64, os=64, n=4, edges_n=16, h=64, k=4,
+               dtype=1, rd=0, od=1)
+FQUANT = dict(x=P, x_stride=256, dtype=1, rows=None, n=4, src=4, cols=256, swiglu=0, form=0, t=1.0, q=P, s=P, stream=None)
+FWEIGHT = dict(w=P, dtype=1, mats=1, n=128, k=128, form=0, q=P, s=P, t=P, stream=None)
+FBACK = dict(q=P, s=P, form=0, mats=1, n=8, k=128, scale=1.0, factors=None, out=P, stride=128, dtype=1, stream=None)
+EXPERT = dict(a=P, b=P, sa=0, sb=0, offsets=0, rows=0, factors=0, y=P, a_stride=128, stride=64, scale=1.0, groups=1, m=4, src=4, n=64,
+              k=128, kind=1, swiglu=0, out=1)
+EXPERT4 = dict(EXPERT, sa=P, sb=P, kind=2)
+
+
+def _call(lib, name, args):
+    from sparse_moe_layer_gate_gb300 import binding as B
+    packed = {"epoch_route": B.ROUTE_ARGS, "epoch_combine": B.COMBINE_ARGS, "epoch_expert_matmul": B.EXPERT_ARGS}
+    if name in packed:
+        return getattr(lib, name)(packed[name].pack(*args.values()), None)
+    return getattr(lib, name)(*args.values())
+
+
+def _apart(base):
+    """The arguments with every pointer in a place of its own."""
+    return {name: (P * (16 + 16 * i) if v == P else v) for i, (name, v) in enumerate(base.items())}
+
+
+def _refusals():
+    f, far = math.inf, P * 4096
+    b = _apart(ROUTE)
+    for kw in (dict(n=-1), dict(experts=0), dict(experts=1025, stride=1025), dict(k=0), dict(k=17), dict(experts=3, k=4), dict(dtype=2),
+               dict(router=2), dict(bias=far), dict(n=(1 << 30), k=4), dict(logits=0), dict(logits=far + 2), dict(stride=63),
+               dict(sel=0), dict(weights=far + 2), dict(positions=0), dict(offsets=0), dict(offsets=far + 1), dict(slots=0),
+               dict(router=1, groups=0), dict(router=1, groups=33, experts=66, stride=66), dict(router=1, groups=5),
+               dict(router=1, groups=4, top=0), dict(router=1, groups=4, top=5), dict(router=1, bias=far + 2),
+               dict(n=4000), dict(n=4000, ws=far, bytes=16), dict(n=4000, ws=far + 2, bytes=1 << 20),
+               # outputs that overlap
+               dict(sel=b["weights"]), dict(slots=b["positions"] + 60), dict(offsets=b["sel"] + 60), dict(weights=b["logits"] + 4),
+               dict(live=b["sel"] + 63), dict(eligible=b["offsets"]), dict(router=1, bias=b["slots"])):
+        yield "epoch_route", b, kw
+    b = _apart(COMBINE)
+    for kw in (dict(n=-1), dict(edges_n=-1), dict(h=0), dict(h=(1 << 20) + 1), dict(k=0), dict(k=65), dict(dtype=2), dict(rd=2),
+               dict(od=-1), dict(edges=0), dict(edges=far + 1), dict(slots=0), dict(weights=far + 2), dict(out=0), dict(es=63),
+               dict(os=1), dict(residual=far, rs=3), dict(shared=far, ss=63), dict(n=1 << 30, h=1 << 20, es=1 << 20, os=1 << 20),
+               dict(out=b["edges"] + 64), dict(out=b["slots"] + 2), dict(out=b["weights"]), dict(residual=b["out"]),
+               dict(shared=b["out"] + 2), dict(shared=b["out"], ss=65)):
+        yield "epoch_combine", b, kw
+    b = _apart(FQUANT)
+    for kw in (dict(n=-1, src=-1), dict(src=3), dict(cols=0), dict(cols=48), dict(cols=(1 << 30) + 32), dict(dtype=7), dict(form=2),
+               dict(t=0.0), dict(t=-1.0), dict(t=f), dict(t=math.nan), dict(t=1e-45), dict(form=1, t=2.0), dict(x=None),
+               dict(x=far + 1), dict(q=None), dict(q=far + 8), dict(s=None), dict(s=far + 4), dict(x_stride=255), dict(swiglu=1),
+               dict(rows=far + 2), dict(n=1 << 30, src=1 << 30, cols=512, x_stride=512),
+               dict(q=b["x"]), dict(s=b["x"] + 16), dict(q=b["s"]), dict(rows=b["q"] + 4), dict(rows=b["s"])):
+        yield "epoch_fp4_quantize", b, kw
+    b = _apart(FWEIGHT)
+    for kw in (dict(dtype=2), dict(form=-1), dict(mats=-1), dict(mats=65536), dict(n=0), dict(k=0), dict(k=40), dict(n=(1 << 22) + 1),
+               dict(w=None), dict(q=None), dict(s=None), dict(t=None), dict(t=far + 2), dict(q=b["w"]), dict(s=b["q"]), dict(t=b["s"])):
+        yield "epoch_fp4_quantize_weight", b, kw
+    b = _apart(FBACK)
+    for kw in (dict(dtype=2), dict(form=2), dict(mats=-1), dict(n=-1), dict(k=16), dict(k=33), dict(scale=f), dict(q=None), dict(q=far + 8),
+               dict(s=None), dict(s=far + 8), dict(factors=far + 2), dict(out=None), dict(out=far + 1), dict(stride=127), dict(out=b["q"]),
+               dict(out=b["s"]), dict(factors=b["out"])):
+        yield "epoch_fp4_dequantize", b, kw
+    for base in (EXPERT, EXPERT4):
+        b = _apart(base)
+        for kw in (dict(m=-1, src=-1), dict(n=0), dict(k=0), dict(k=4), dict(k=(1 << 30) + 32), dict(groups=0), dict(groups=2),
+                   dict(groups=1025, offsets=far), dict(offsets=far + 2), dict(groups=1024, offsets=far, n=1 << 22), dict(kind=4),
+                   dict(kind=-1), dict(a=0), dict(a=far + 8), dict(b=far + 4), dict(b=0), dict(y=0), dict(y=far + 1), dict(stride=63),
+                   dict(out=2), dict(scale=f), dict(scale=math.nan), dict(swiglu=1, n=63), dict(factors=far + 2), dict(src=5),
+                   dict(src=-1, rows=far), dict(y=b["a"] + 4), dict(y=b["b"] + 64), dict(offsets=b["y"]), dict(factors=b["y"] + 4)):
+            yield "epoch_expert_matmul", b, kw
+    b = _apart(EXPERT)
+    for kw in (dict(a_stride=127), dict(a_stride=132), dict(k=12, a_stride=16), dict(rows=far + 2), dict(rows=b["y"]),
+               dict(kind=0, a_stride=130), dict(kind=0, k=6, a_stride=8), dict(kind=0, a=far + 4)):
+        yield "epoch_expert_matmul", b, kw
+    b = _apart(EXPERT4)
+    for kw in (dict(rows=far), dict(k=48), dict(sa=0), dict(sb=far + 8), dict(y=b["sa"]), dict(y=b["sb"])):
+        yield "epoch_expert_matmul", b, kw
+
+
+@pytest.mark.parametrize("name,base,change", list(_refusals()), ids=lambda v: str(v)[:60] if not isinstance(v, dict) else "")
+def test_refused_on_the_host(lib, name, base, change):
+    assert set(change) <= set(base)
+    assert _call(lib, name, {**base, **change}) == 1  # EPOCH_EINVAL, nothing enqueued
+
+
+def test_without_arguments(lib):
+    for name in ("epoch_route", "epoch_combine", "epoch_expert_matmul"):
+        assert getattr(lib, name)(None, None) == 1
+    assert lib.epoch_test_expert_timeout(None, 1000, None) == 1
+    assert lib.epoch_route_workspace_bytes(0, 64) == 0 and lib.epoch_route_workspace_bytes(100, 2000) == 0
+    assert lib.epoch_expert_matmul_kernel(9, 0, 1, 1, 8, 152) == -1
+
+
+def test_no_rows_enqueue_nothing(lib):
+    for name, base, kw in (("epoch_combine", COMBINE, dict(n=0, edges=0, out=0)),
+                           ("epoch_fp4_quantize", FQUANT, dict(n=0, src=0, x=None, q=None, s=None)),
+                           ("epoch_fp4_quantize_weight", FWEIGHT, dict(mats=0, w=None)),
+                           ("epoch_fp4_dequantize", FBACK, dict(n=0, q=None, out=None)),
+                           ("epoch_expert_matmul", EXPERT, dict(m=0, src=0, a=0, y=0)),
+                           ("epoch_expert_matmul", EXPERT4, dict(m=0, src=0, a=0, y=0))):
+        assert _call(lib, name, {**base, **kw}) == 0
+
+
+def test_cpu_tensors_are_refused(ops):
+    x, q = torch.zeros(2, 64), torch.zeros(2, 32, dtype=U8)
+    s, i = torch.zeros(1, 2, 16).to(E4M3), torch.zeros(2, 1, dtype=I32)
+    for call in (lambda: ops.route(x, 2), lambda: ops.combine(x, i, x[:, :1]), lambda: ops.grouped_matmul(x, x, None),
+                 lambda: ops.fp4_quantize(x), lambda: ops.fp4_quantize_weight(x), lambda: ops.fp4_dequantize(q, s),
+                 lambda: ops.fp4_matmul(q, s, q, s)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.gpu
+def test_tensors_are_checked(ops):
+    c = dict(device="cuda")
+    x, w = torch.zeros(4, 64, **c), torch.zeros(64, **c)
+    i = torch.zeros(4, 2, dtype=I32, **c)
+    q, s = ops.fp4_quantize(x)
+    qm, sm = ops.fp4_quantize(x, form="mxfp4")
+    off = torch.zeros(3, dtype=I32, **c)
+    r = ops.route(x, 2)
+    for call in (lambda: ops.route(x.half(), 2), lambda: ops.route(x[0], 2), lambda: ops.route(x, 0), lambda: ops.route(x, 17),
+                 lambda: ops.route(x, 2, router="top"), lambda: ops.route(x, 2, bias=w), lambda: ops.route(x.T, 2),
+                 lambda: ops.route(x, 2, router="sigmoid_group", bias=w.to(BF16)), lambda: ops.route(x, 2, router="sigmoid_group", n_group=5),
+                 lambda: ops.route(x, 2, live=w[:4]), lambda: ops.route(x, 2, live=w[:3].bool()), lambda: ops.route(x, 2, eligible=w[:4].bool()),
+                 lambda: ops.route(x, 2, out=r._replace(slots=r.slots[:3])), lambda: ops.route(x, 2, out=r._replace(sel=r.slots)),
+                 lambda: ops.combine(x, i.long(), x[:, :2].contiguous()), lambda: ops.combine(x, i, x[:, :2]),
+                 lambda: ops.combine(x, i, x[:, :2].contiguous(), residual=x[:3]), lambda: ops.combine(x, i, x[:, :2].contiguous(), out=x),
+                 lambda: ops.combine(x, i, x[:, :2].contiguous(), shared=x.to(BF16)), lambda: ops.combine(x.half(), i, x[:, :2].contiguous()),
+                 lambda: ops.grouped_matmul(x, x.to(BF16), None), lambda: ops.grouped_matmul(x, x[:, :32], None),
+                 lambda: ops.grouped_matmul(x, x[None], off), lambda: ops.grouped_matmul(x, x, off), lambda: ops.grouped_matmul(x, x[None], None),
+                 lambda: ops.grouped_matmul(x.half(), x.half(), None), lambda: ops.grouped_matmul(x[:, 1:61], x[:, :60].contiguous(), None),
+                 lambda: ops.grouped_matmul(x, x[:3].contiguous(), None, swiglu=True), lambda: ops.grouped_matmul(x, x, None, rows=off.long()),
+                 lambda: ops.grouped_matmul(x, x, None, out=x), lambda: ops.grouped_matmul(x, x, None, out_dtype=torch.float16),
+                 lambda: ops.fp4_quantize(x, form="fp4"), lambda: ops.fp4_quantize(x[:, :48]), lambda: ops.fp4_quantize(x[:, :63], swiglu=True),
+                 lambda: ops.fp4_quantize(x, q=x), lambda: ops.fp4_quantize(x, scales=sm), lambda: ops.fp4_quantize(x, form="mxfp4", tensor_scale=0.5),
+                 lambda: ops.fp4_quantize_weight(x.T), lambda: ops.fp4_dequantize(q, sm[:, :3]), lambda: ops.fp4_dequantize(q, s.view(U8)),
+                 lambda: ops.fp4_dequantize(q, s, tensor_scale=w[:2]), lambda: ops.fp4_matmul(q, s, qm, sm), lambda: ops.fp4_matmul(q, s, q[:, :16], s),
+                 lambda: ops.fp4_matmul(q, s, q[None], s[None]), lambda: ops.fp4_matmul(q, s, q, s, scale=w[:2]),
+                 lambda: ops.fp4_matmul(q, s, q, s, out_dtype=torch.float16), lambda: ops.fp4_matmul(x, s, q, s)):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
