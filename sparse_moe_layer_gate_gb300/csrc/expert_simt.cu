@@ -2,10 +2,14 @@
 // fp32 operands, and TF32's ten bits would lose what an fp32 layer keeps). The formula is that of
 // expert_gemm.cu; sums are fp32, in ascending k.
 //
-// Tiles of 128 or 32 rows x 128 columns, sixteen columns of K at a time through two places in shared
-// memory, each thread 8 (2) x 8 sums as pairs for the packed fp32 multiply-add. With swiglu a tile's
-// columns are 64 gate and 64 up rows of the weights: a thread's columns 4 and 4 of them. Short tiles
-// where groups have few rows. Bound by the FFMA pipes at many rows.
+// Many rows (k_expert_simt): tiles of 128 rows x 128 columns, sixteen columns of K at a time through two
+// places in shared memory, each thread 8 x 8 sums as pairs for the packed fp32 multiply-add. With swiglu a
+// tile's columns are 64 gate and 64 up rows of the weights: a thread's columns 4 and 4 of them. Bound by
+// the FFMA pipes (8192 x 2048 x 2048 over 8 experts 1.44 ms, 48 TFLOP/s).
+//
+// Few rows (k_expert_stream): bound by the weights' bytes and by latency. A warp takes four rows of weights
+// (two gate and two up) and eight tokens: its lanes share K out, each keeps all 32 sums, and the sums meet
+// by exchanges that halve them at every step.
 #include "common.cuh"
 #include "layer.h"
 #include "tiles.cuh"
@@ -30,34 +34,35 @@ __device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
 
-template <int ROWS> __global__ void __launch_bounds__(kThreads) k_expert_simt(const ExpertGemmArgs a, int nt_n) {
-  constexpr int TM = ROWS / 16;                      // rows of a thread
-  constexpr int LA = ROWS * kDepth / 4 / kThreads;   // float4 loads of a thread for the rows (ROWS 32: half the threads)
+constexpr int kRows = 128;
+__global__ void __launch_bounds__(kThreads) k_expert_simt(const ExpertGemmArgs a, int nt_n) {
+  constexpr int TM = kRows / 16;                     // rows of a thread
+  constexpr int LA = kRows * kDepth / 4 / kThreads;  // float4 loads of a thread for the rows
   constexpr int LB = kCols * kDepth / 4 / kThreads;
-  __shared__ __align__(16) float s_a[2][kDepth][ROWS + kPad], s_b[2][kDepth][kCols + kPad];
+  __shared__ __align__(16) float s_a[2][kDepth][kRows + kPad], s_b[2][kDepth][kCols + kPad];
   __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (a.offsets != nullptr) {
-    if (warp_id() == 0) group_tiles(a.offsets, a.n_groups, a.m, ROWS, s_start, s_cum);
+    if (warp_id() == 0) group_tiles(a.offsets, a.n_groups, a.m, kRows, s_start, s_cum);
   } else if (tid == 0) {
     s_start[0] = 0;
     s_start[1] = a.m;
     s_cum[0] = 0;
-    s_cum[1] = (a.m + ROWS - 1) / ROWS;
+    s_cum[1] = (a.m + kRows - 1) / kRows;
   }
   __syncthreads();
-  TileWalk walk(s_start, s_cum, a.offsets ? a.n_groups : 1, nt_n, ROWS, 0);
+  TileWalk walk(s_start, s_cum, a.offsets ? a.n_groups : 1, nt_n, kRows, 0);
   const int half_n = a.N / 2, out_n = a.swiglu ? half_n : a.N;
   const float *x = static_cast<const float *>(a.a), *w = static_cast<const float *>(a.b);
   for (int t = blockIdx.x; t < walk.total; t += gridDim.x) {
     int e, row0, rows, nt;
     walk.at(t, &e, &row0, &rows, &nt);
-    rows = min(rows, ROWS);
+    rows = min(rows, kRows);
     // where this thread's pieces come from: rows and weights that do not exist are zeros
-    const float *pa[LA > 0 ? LA : 1], *pb[LB];
+    const float *pa[LA], *pb[LB];
     const int kq = (tid & 3) * 4;  // columns of K
 #pragma unroll
-    for (int i = 0; i < (LA > 0 ? LA : 1); ++i) {
+    for (int i = 0; i < LA; ++i) {
       const int r = (tid >> 2) + 64 * i;
       pa[i] = nullptr;
       if (r < rows) {
@@ -73,11 +78,11 @@ template <int ROWS> __global__ void __launch_bounds__(kThreads) k_expert_simt(co
       const bool there = a.swiglu ? nt * 64 + (j & 63) < half_n : n < a.N;
       pb[i] = there ? w + (static_cast<int64_t>(e) * a.N + n) * a.K + kq : nullptr;
     }
-    float4 ra[LA > 0 ? LA : 1], rb[LB];
+    float4 ra[LA], rb[LB];
     auto load = [&](int k0) {
       const bool in = k0 + kq < a.K;
 #pragma unroll
-      for (int i = 0; i < (LA > 0 ? LA : 1); ++i)
+      for (int i = 0; i < LA; ++i)
         ra[i] = in && pa[i] ? __ldg(reinterpret_cast<const float4 *>(pa[i] + k0)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < LB; ++i)
@@ -85,11 +90,9 @@ template <int ROWS> __global__ void __launch_bounds__(kThreads) k_expert_simt(co
     };
     auto put = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < (LA > 0 ? LA : 1); ++i) {
+      for (int i = 0; i < LA; ++i) {
         const int r = (tid >> 2) + 64 * i;
-        if (ROWS >= 64 || r < ROWS) {
-          s_a[s][kq][r] = ra[i].x, s_a[s][kq + 1][r] = ra[i].y, s_a[s][kq + 2][r] = ra[i].z, s_a[s][kq + 3][r] = ra[i].w;
-        }
+        s_a[s][kq][r] = ra[i].x, s_a[s][kq + 1][r] = ra[i].y, s_a[s][kq + 2][r] = ra[i].z, s_a[s][kq + 3][r] = ra[i].w;
       }
 #pragma unroll
       for (int i = 0; i < LB; ++i) {
@@ -162,20 +165,136 @@ template <int ROWS> __global__ void __launch_bounds__(kThreads) k_expert_simt(co
   }
 }
 
-template <int ROWS> cudaError_t launch_rows(const ExpertGemmArgs &a, cudaStream_t s) {
-  const int nt = (a.N + kCols - 1) / kCols;  // with swiglu 64 columns of each half
-  const int64_t groups = a.n_groups < a.m ? a.n_groups : a.m;
-  const int64_t tiles = (a.offsets ? a.m / ROWS + groups : (a.m + ROWS - 1) / ROWS) * nt;
-  const int64_t most = 4ll * num_sms();
-  k_expert_simt<ROWS><<<static_cast<unsigned>(tiles < most ? tiles : most), kThreads, 0, s>>>(a, nt);
-  return cudaGetLastError();
+constexpr int kTokens = 8;  // rows of a warp's unit
+
+// The sums of 2^n values that every lane holds a part of: lane l ends with value l >> (5 - n) of them, by exchanges in
+// which each lane passes half of its values on.
+template <int N> __device__ __forceinline__ float meet(float (&v)[N]) {
+  const int lane = lane_id();
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, o /= 2) {
+    const bool high = lane & o;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float send = high ? v[j] : v[j + n], keep = high ? v[j + n] : v[j];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+// One unit with at most R tokens.
+template <int R>
+__device__ __forceinline__ void stream_unit(const ExpertGemmArgs &a, int e, int row0, int rows, int nt) {
+  const int lane = lane_id(), warp = warp_id(), half_n = a.N / 2, out_n = a.swiglu ? half_n : a.N;
+  const float *x = static_cast<const float *>(a.n_src > 0 ? a.a : a.b);
+  const float *px[R], *pw[4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    int64_t src = row0 + min(r, rows - 1);  // (rows that do not exist repeat one that does)
+    if (a.rows != nullptr) src = __ldg(a.rows + src);
+    if (src < 0 || src >= a.n_src) src = 0;  // never followed; the result is NaN
+    px[r] = x + src * a.a_stride;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = a.swiglu ? (i & 2 ? half_n : 0) + min(nt * 16 + warp * 2 + (i & 1), half_n - 1) : min(nt * 32 + warp * 4 + i, a.N - 1);
+    pw[i] = static_cast<const float *>(a.b) + (static_cast<int64_t>(e) * a.N + n) * a.K;
+  }
+  uint64_t acc[4][R];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[i][r] = 0ull;
+#pragma unroll 2
+  for (int k = lane * 4; k < a.K; k += 128) {
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[i].x), "=f"(w[i].y), "=f"(w[i].z), "=f"(w[i].w) : "l"(pw[i] + k));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(px[r] + k));
+      const uint64_t lo = pack2(v.x, v.y), hi = pack2(v.z, v.w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        fma2(acc[i][r], pack2(w[i].x, w[i].y), lo);
+        fma2(acc[i][r], pack2(w[i].z, w[i].w), hi);
+      }
+    }
+  }
+  float v[4 * R];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float2 f = unpack2(acc[i][r]);
+      v[i * R + r] = f.x + f.y;
+    }
+  float y = meet(v);
+  constexpr int kSame = 32 / (4 * R);  // lanes with the same value
+  const int at = lane / kSame, i = at / R, r = at % R;
+  float f = a.scale;
+  if (a.group_scale != nullptr) f *= __ldg(a.group_scale + e);
+  if (a.rows != nullptr && r < rows) {
+    const int src = __ldg(a.rows + row0 + r);
+    if (src < 0 || src >= a.n_src) f = __uint_as_float(0x7FC00000u);
+  }
+  y *= f;
+  int n = nt * 32 + warp * 4 + i;
+  if (a.swiglu) {
+    const float up = __shfl_xor_sync(0xffffffffu, y, 16);  // rows 2 and 3 are the up rows of 0 and 1
+    y = silu(y) * up;
+    n = i < 2 ? nt * 16 + warp * 2 + i : out_n;
+  }
+  if (lane % kSame != 0 || r >= rows || n >= out_n) return;
+  const int64_t to = static_cast<int64_t>(row0 + r) * a.out_stride + n;
+  if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.out)[to] = __float2bfloat16_rn(y);
+  else static_cast<float *>(a.out)[to] = y;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) k_expert_stream(const ExpertGemmArgs a, int nt_n) {
+  __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
+  if (a.offsets != nullptr) {
+    if (warp_id() == 0) group_tiles(a.offsets, a.n_groups, a.m, kTokens, s_start, s_cum);
+  } else if (threadIdx.x == 0) {
+    s_start[0] = 0;
+    s_start[1] = a.m;
+    s_cum[0] = 0;
+    s_cum[1] = (a.m + kTokens - 1) / kTokens;
+  }
+  __syncthreads();
+  TileWalk walk(s_start, s_cum, a.offsets ? a.n_groups : 1, nt_n, kTokens, 0);
+  for (int t = blockIdx.x; t < walk.total; t += gridDim.x) {
+    int e, row0, rows, nt;
+    walk.at(t, &e, &row0, &rows, &nt);
+    rows = min(rows, kTokens);
+    if (rows == 1) stream_unit<1>(a, e, row0, rows, nt);
+    else if (rows == 2) stream_unit<2>(a, e, row0, rows, nt);
+    else if (rows <= 4) stream_unit<4>(a, e, row0, rows, nt);
+    else stream_unit<8>(a, e, row0, rows, nt);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_expert_simt(const ExpertGemmArgs &a, cudaStream_t s) {
-  const int64_t groups = a.offsets ? a.n_groups : 1;
-  return a.m <= 64 * groups ? launch_rows<32>(a, s) : launch_rows<128>(a, s);
+  const int64_t groups = a.offsets ? (a.n_groups < a.m ? a.n_groups : a.m) : 1;
+  const int64_t nt = (a.N + kCols - 1) / kCols;  // with swiglu 64 columns of each half
+  const int64_t tiles = (a.offsets ? a.m / kRows + groups : (a.m + kRows - 1) / kRows) * nt;
+  // Tall tiles where groups fill most of them and the device has work for all.
+  if (a.m > 32 * groups && tiles >= num_sms() / 4) {
+    const int64_t most = 4ll * num_sms();
+    k_expert_simt<<<static_cast<unsigned>(tiles < most ? tiles : most), kThreads, 0, s>>>(a, static_cast<int>(nt));
+  } else {
+    const int64_t nb = (a.N + 31) / 32, units = (a.offsets ? a.m / kTokens + groups : (a.m + kTokens - 1) / kTokens) * nb;
+    const int64_t most = 8ll * num_sms();
+    k_expert_stream<<<static_cast<unsigned>(units < most ? units : most), kThreads, 0, s>>>(a, static_cast<int>(nb));
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace epoch
