@@ -739,7 +739,7 @@ template <int FP4> cudaError_t launch_kind(ExpertParams &p, int kernel, cudaStre
 int expert_gemm_kernel(bool fp4, int n_groups, int64_t m, int64_t N, int sms) {
   const int64_t E = n_groups ? (n_groups < m ? n_groups : m) : 1;
   auto tiles = [&](int64_t rows) {
-    const int64_t t = n_groups ? m / rows + (E + 1) / 2 : (m + rows - 1) / rows;
+    const int64_t t = E > 1 ? m / rows + (E + 1) / 2 : (m + rows - 1) / rows;
     return t > E ? t : E;
   };
   static const int64_t kCost[5][3] = {{256, 420, 790}, {128, 250, 555}, {64, 197, 430}, {32, 190, 390}, {kExpertPairs, 405, 600}};
