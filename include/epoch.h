@@ -679,8 +679,8 @@ typedef struct {
 epoch_status epoch_expert_matmul(const epoch_expert_args *args, epoch_stream stream);
 
 /* Which kernel epoch_expert_matmul takes for these sizes, as epoch_fp8_matmul_kernel says it:
- * tiles of 32, 64, 128 or 256 columns, or EPOCH_FP8_PAIRS (the fp32 kernel: 0); -1 for sizes out of
- * range. Host only. */
+ * 0 the kernel for few rows and the fp32 kernels, else tiles of 32, 64, 128 or 256 columns, or EPOCH_FP8_PAIRS; -1 for
+ * sizes out of range. Host only. */
 int32_t epoch_expert_matmul_kernel(int32_t kind, int32_t n_groups, int32_t m, int32_t n, int32_t k, int32_t n_sms);
 
 /* Test hook: epoch_expert_matmul whose operand copies count 16 bytes that never come, as

@@ -18,7 +18,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libepoch.so")
 SOURCES = ["abi.cu", "route.cu", "gemm_simt.cu", "gemm_tc.cu", "plan_noalloc.cu",
            "ops.cu", "block_norm.cu", "fp8_quant.cu", "fp8_gemm.cu", "few.cu",
-           "router.cu", "combine.cu", "fp4_quant.cu", "expert_gemm.cu", "expert_simt.cu"]
+           "router.cu", "combine.cu", "fp4_quant.cu", "expert_gemm.cu", "expert_simt.cu", "expert_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -407,6 +407,9 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t 
                                uint32_t hold = 0);
 // expert_simt.cu (fp32 rows)
 cudaError_t launch_expert_simt(const ExpertGemmArgs &a, cudaStream_t s);
+// expert_few.cu (bf16 and 4-bit rows, few of them)
+bool expert_few(bool fp4, int n_groups, int64_t m, int64_t N, int sms);
+cudaError_t launch_expert_few(const ExpertGemmArgs &a, cudaStream_t s);
 int expert_gemm_kernel(bool fp4, int n_groups, int64_t m, int64_t N, int sms);
 
 // Device error word of the operators without a layer, on the current device (nullptr: none).

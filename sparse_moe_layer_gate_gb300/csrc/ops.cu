@@ -513,7 +513,9 @@ epoch_status epoch_expert_matmul(const epoch_expert_args *p, epoch_stream stream
   ExpertGemmArgs g;
   const epoch_status st = expert_product(p, &g);
   if (st != EPOCH_OK || p->m == 0) return st;
-  return status_of(g.kind == EPOCH_EXPERT_F32 ? launch_expert_simt(g, S(stream)) : launch_expert_gemm(g, S(stream)));
+  if (g.kind == EPOCH_EXPERT_F32) return status_of(launch_expert_simt(g, S(stream)));
+  const bool few = expert_few(g.kind != EPOCH_EXPERT_BF16, g.offsets ? g.n_groups : 0, g.m, g.N, num_sms());
+  return status_of(few ? launch_expert_few(g, S(stream)) : launch_expert_gemm(g, S(stream)));
 }
 
 epoch_status epoch_test_expert_timeout(const epoch_expert_args *p, int64_t timeout_ns, epoch_stream stream) {
@@ -527,7 +529,9 @@ epoch_status epoch_test_expert_timeout(const epoch_expert_args *p, int64_t timeo
 int32_t epoch_expert_matmul_kernel(int32_t kind, int32_t n_groups, int32_t m, int32_t n, int32_t k, int32_t n_sms) {
   if (kind < EPOCH_EXPERT_F32 || kind > EPOCH_EXPERT_MXFP4 || m < 0 || n < 1 || k < 1 || n_groups < 0 || n_groups > 1024 || n_sms < 0)
     return -1;
-  return kind == EPOCH_EXPERT_F32 ? 0 : expert_gemm_kernel(kind != EPOCH_EXPERT_BF16, n_groups, m, n, n_sms ? n_sms : num_sms());
+  const int sms = n_sms ? n_sms : num_sms();
+  const bool fp4 = kind != EPOCH_EXPERT_BF16;
+  return kind == EPOCH_EXPERT_F32 || expert_few(fp4, n_groups, m, n, sms) ? 0 : expert_gemm_kernel(fp4, n_groups, m, n, sms);
 }
 
 epoch_status epoch_ops_status(int32_t clear, epoch_stream stream, uint32_t *word_out) {

@@ -110,10 +110,12 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
 __device__ inline void group_tiles(const int32_t *offsets, int E, int m, int tile, int *start, int *cum) {
   const int lane = lane_id(), per = (E + 32) / 32;  // entries of offsets [0, E] per lane
   const int lo = lane * per, hi = min(lo + per, E + 1);
+#pragma unroll 4
+  for (int i = lane; i <= E; i += 32) start[i] = min(max(__ldg(offsets + i), 0), m);
+  __syncwarp();
   int mx = 0;
   for (int i = lo; i < hi; ++i) {
-    const int o = min(max(__ldg(offsets + i), 0), m);
-    mx = max(mx, o);
+    mx = max(mx, start[i]);
     start[i] = mx;
   }
   int pre = mx;  // largest entry up to this lane's
@@ -155,7 +157,15 @@ struct TileWalk {
   __device__ void at(int t, int *group, int *row0, int *rows, int *nt) {
     const int mt = t / nt_n;
     *nt = t - mt * nt_n;
-    while (cum[e + 1] <= mt) ++e;
+    // the last group that starts at or before the tile: steps that double, then halve (a launch of few tiles may skip
+    // hundreds of empty groups)
+    if (cum[e + 1] <= mt) {
+      int lo = e + 1, step = 1;
+      for (; lo + step < E && cum[lo + step] <= mt; step *= 2) lo += step;
+      for (; step > 0; step /= 2)
+        if (lo + step < E && cum[lo + step] <= mt) lo += step;
+      e = lo;
+    }
     *group = e;
     *row0 = start[e] + (mt - cum[e]) * bm + first;
     *rows = min(kBm, start[e + 1] - *row0);

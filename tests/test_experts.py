@@ -332,7 +332,8 @@ def product_bound(y, size, steps, ot, swiglu):
 
 GROUPED = [(1, 1, 1, 8), (1, 8, 64, 64), (3, 2, 40, 72), (17, 5, 130, 200), (64, 64, 32, 128), (100, 3, 256, 512), (129, 1, 257, 1000),
            (200, 130, 96, 256), (300, 4, 520, 264), (1000, 3, 768, 192), (2050, 2, 1024, 128), (700, 1, 2000, 64),
-           (1000, 1, 4096, 64), (900, 2, 4000, 192), (1100, 1, 4096, 136)]
+           (1000, 1, 4096, 64), (900, 2, 4000, 192), (1100, 1, 4096, 136),
+           (5, 1, 4900, 72), (40, 1, 2600, 200), (60, 3, 1700, 136), (11, 2, 100, 4104), (16, 1, 2048, 2048)]
 
 
 @pytest.mark.gpu
@@ -628,7 +629,7 @@ def fp4_operand(g, form, *shape, std=1.0):
 
 FP4 = [(1, 1, 1, 32), (1, 8, 64, 256), (3, 2, 40, 96), (17, 5, 130, 288), (64, 64, 32, 512), (100, 3, 256, 1024), (129, 1, 257, 800),
        (200, 130, 96, 256), (300, 4, 520, 512), (1000, 3, 768, 320), (2050, 2, 1024, 256), (700, 1, 2000, 64), (600, 1, 4096, 768),
-       (700, 64, 1024, 256)]
+       (700, 64, 1024, 256), (5, 1, 4900, 96), (40, 1, 300, 288), (13, 2, 100, 8224), (16, 1, 2048, 2048), (2, 500, 48, 544)]
 
 
 @pytest.mark.gpu
@@ -652,6 +653,34 @@ def test_fp4_matmul(ops, m, e, n, k, form, swiglu, ot):
         assert torch.equal(ops.fp4_matmul(a, sa, b[0], sb[0], scale=scale, swiglu=swiglu, out_dtype=ot), got)
         one = ops.fp4_matmul(a, sa, b[0], sb[0], scale=float(scale[0]), swiglu=swiglu, out_dtype=ot)
         assert torch.equal(one, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 12, 300])  # few rows, and tiles
+@pytest.mark.parametrize("form", ["nvfp4", "mxfp4"])
+def test_fp4_matmul_scales_of_their_whole_range(ops, m, form):
+    """Every finite scale of nvfp4, zero and subnormal ones among them; every one of mxfp4, 2^-127 and 2^127, in pairs whose
+    products stay fp32's."""
+    n, k = 136, 32 * 255
+    g, (block, dtype) = _gen(m), FORMS[form]
+    a, _, va = fp4_operand(g, form, m, k)
+    b, _, vb = fp4_operand(g, form, 1, n, k)
+    grid = torch.tensor(GRID + [-x for x in GRID], device="cuda", dtype=F64)
+    lay = lambda byte: torch.nn.functional.pad(byte.to(U8), (0, -(-k // 256) * 256 // block - k // block)).unflatten(  # noqa: E731
+        -1, (-1, 256 // block)).transpose(-2, -3).contiguous().view(dtype)
+    value = lambda q: grid[torch.stack([q & 15, q >> 4], -1).flatten(-2).long()]  # noqa: E731
+    if form == "nvfp4":
+        ba, bb = (torch.randint(0, 0x7F, (r, k // block), generator=g, device="cuda") for r in (m, n))
+        fa, fb = (t.to(U8).view(E4M3).double() for t in (ba, bb))
+    else:
+        ba = torch.randperm(255, generator=g, device="cuda").expand(m, -1)
+        bb = (254 - ba[:1] + torch.randint(-1, 2, (n, 255), generator=g, device="cuda")).clamp(0, 254)
+        fa, fb = (torch.exp2(t.double() - 127) for t in (ba, bb))
+    va, vb = value(a) * fa.repeat_interleave(block, -1), value(b[0]) * fb.repeat_interleave(block, -1)
+    off = torch.tensor([0, m], device="cuda", dtype=I32)
+    y, size = product64(va, vb[None], off)
+    got = ops.fp4_matmul(a, lay(ba), b[0], lay(bb), out_dtype=F32)
+    _within(got, y, product_bound(y, size, k / 64 + 16, F32, False))
 
 
 @pytest.mark.gpu
@@ -844,9 +873,9 @@ WIDTHS = [32, 64, 128, 256, 512]  # columns of a tile; 512: pairs
 
 
 def test_every_kernel_of_the_products_is_reached(lib):
-    """The sizes above take each width of tiles, and pairs, on a device of 152 SMs."""
+    """The sizes above take each width of tiles, pairs, and the kernel for few rows (0), on a device of 152 SMs."""
     for kind, sizes in ((1, GROUPED), (2, FP4), (3, FP4)):
-        assert {lib.epoch_expert_matmul_kernel(kind, e, m, n, k, 152) for m, e, n, k in sizes} == set(WIDTHS), kind
+        assert {lib.epoch_expert_matmul_kernel(kind, e, m, n, k, 152) for m, e, n, k in sizes} == {0, *WIDTHS}, kind
     assert lib.epoch_expert_matmul_kernel(0, 2, 10, 64, 64, 152) == 0
 
 
