@@ -157,14 +157,11 @@ struct TileWalk {
   __device__ void at(int t, int *group, int *row0, int *rows, int *nt) {
     const int mt = t / nt_n;
     *nt = t - mt * nt_n;
-    // the last group that starts at or before the tile: steps that double, then halve (a launch of few tiles may skip
-    // hundreds of empty groups)
-    if (cum[e + 1] <= mt) {
-      int lo = e + 1, step = 1;
-      for (; lo + step < E && cum[lo + step] <= mt; step *= 2) lo += step;
-      for (; step > 0; step /= 2)
-        if (lo + step < E && cum[lo + step] <= mt) lo += step;
-      e = lo;
+    // the last group that starts at or before the tile, by halves (hundreds between two tiles may be empty)
+    for (int hi = cum[e + 1] <= mt ? E - 1 : e; e < hi;) {
+      const int mid = (e + hi + 1) / 2;
+      if (cum[mid] <= mt) e = mid;
+      else hi = mid - 1;
     }
     *group = e;
     *row0 = start[e] + (mt - cum[e]) * bm + first;
