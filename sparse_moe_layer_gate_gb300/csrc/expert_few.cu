@@ -85,7 +85,7 @@ template <int FP4> struct Piece {
   uint32_t s[2];
 };
 // Piece `it` of a row at p, its scales at s (a block's apart by s_block bytes).
-template <int FP4, bool ONCE> __device__ __forceinline__ void load_piece(Piece<FP4> &r, const uint8_t *p, const uint8_t *s, int64_t s_block, int it, int q, int bytes) {
+template <int FP4, bool ONCE> __device__ __forceinline__ void load_piece(Piece<FP4> &r, const uint8_t *p, const uint8_t *s, int64_t s_block, int it, int q, int64_t bytes) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t at = static_cast<int64_t>(it) * 128 + 64 * h + 16 * q;
@@ -111,7 +111,8 @@ template <int FP4, bool TALL>
 __device__ __forceinline__ void few_unit(const ExpertGemmArgs &a, int kb_n, int e, int row0, int rows, int nt, float (*s_part)[256]) {
   constexpr int kAhead = FP4 ? 2 : 4;  // pieces on their way
   const int lane = lane_id(), warp = warp_id(), g = lane >> 2, q = lane & 3;
-  const int half_n = a.N / 2, bytes = FP4 ? a.K / 2 : 2 * a.K;
+  const int half_n = a.N / 2;
+  const int64_t bytes = FP4 ? a.K / 2 : 2ll * a.K;  // of a row: up to 2^31
   const int64_t row_bytes = FP4 ? a.K / 2 : 2 * a.a_stride;
   const uint8_t *base = static_cast<const uint8_t *>(a.n_src > 0 ? a.a : a.b), *px[2], *psx[2], *pw[2], *psw[2];
 #pragma unroll
@@ -126,7 +127,7 @@ __device__ __forceinline__ void few_unit(const ExpertGemmArgs &a, int kb_n, int 
     psw[i] = a.sb + (static_cast<int64_t>(e) * kb_n * a.N + n) * (4 * FP4);
   }
   const int64_t sx_block = static_cast<int64_t>(a.m) * (4 * FP4), sw_block = static_cast<int64_t>(a.N) * (4 * FP4);
-  const int pieces = (bytes + 127) / 128;
+  const int pieces = static_cast<int>((bytes + 127) / 128);
   float sum[2][4] = {};
   for (int it0 = warp; it0 < pieces; it0 += kWarps * kAhead) {
     Piece<FP4> w[kAhead][2];
@@ -234,8 +235,8 @@ template <int FP4> __global__ void __launch_bounds__(kThreads, 2) k_expert_few(c
 }  // namespace
 
 // n_groups 0: dense. Units that are all on the device at once: a second round costs more than the tiles' way through K
-// (one row of 16384 x 2048: bf16 18.6 us, tiles 16.4; nvfp4 13.1 and 7.6). Each unit of 4-bit operands opens its rows again,
-// so more than one unit of rows is left to the tiles (64 of 2048 x 8192: nvfp4 18.5 and 13.0, mxfp4 27.1 and 11.7).
+// (one row of 16384 x 2048: bf16 18.6 us, tiles 16.2; nvfp4 11.0 and 7.6). Each unit of 4-bit operands opens its rows again,
+// so more than one unit of rows is left to the tiles (64 of 2048 x 8192: nvfp4 19.1 and 13.0, mxfp4 27.4 and 11.7).
 bool expert_few(bool fp4, int n_groups, int64_t m, int64_t N, int sms) {
   const int64_t groups = n_groups < m ? n_groups : m;
   const int64_t units = (groups > 1 ? m / kTokens + groups : (m + kTokens - 1) / kTokens) * ((N + 15) / 16);

@@ -100,7 +100,8 @@ def check_route(r, want, what=""):
 
 
 ROUTE_SIZES = [(1, 256, 8), (1, 1, 1), (2, 2, 2), (5, 37, 3), (31, 64, 4), (32, 65, 8), (33, 256, 8), (64, 256, 16), (65, 8, 8),
-               (127, 128, 1), (128, 257, 7), (129, 256, 8), (1000, 64, 6), (700, 1024, 16), (5000, 48, 2)]
+               (127, 128, 1), (128, 257, 7), (129, 256, 8), (1000, 64, 6), (700, 1024, 16), (5000, 48, 2),
+               (19457, 16, 3), (45000, 33, 4)]
 
 
 @pytest.mark.gpu
@@ -356,6 +357,20 @@ def test_grouped_matmul(ops, m, e, n, k, form, dt, ot):
     assert ops.status() == (0, 0)
     if e == 1:
         assert torch.equal(ops.grouped_matmul(x, w[0], None, rows=rows, swiglu=swiglu, out_dtype=ot), got)
+
+
+@pytest.mark.gpu
+def test_grouped_matmul_longest_rows(ops):
+    """Rows of 2^31 bytes: every place that is not zero counts, behind the last 32-bit offset too."""
+    k = 1 << 30
+    x, w = torch.zeros(1, k, device="cuda", dtype=BF16), torch.zeros(2, k, device="cuda", dtype=BF16)
+    for i, at in enumerate((0, 7, k // 2 - 1, k // 2, k - 8, k - 1)):
+        x[0, at] = 1.0
+        w[0, at] = 2.0 ** i
+        w[1, at] = -(2.0 ** (5 - i))
+    got = ops.grouped_matmul(x, w, None, out_dtype=F32)
+    assert got.tolist() == [[63.0, -63.0]]
+    assert ops.status() == (0, 0)
 
 
 @pytest.mark.gpu
