@@ -4,10 +4,11 @@
 // One warp a position: the lanes hold consecutive experts' logits, and the k best are found by rounds
 // of a warp maximum. Positions of a CTA are marked in a word of bits for each expert, so that an
 // edge's place among the CTA's is a population count, whatever order the warps come in. A second
-// kernel adds what earlier CTAs and lower experts hold: every CTA reads all CTAs' counts (128 KB at
+// kernel adds what earlier CTAs and lower experts hold: every CTA reads all CTAs' counts (40 KB at
 // 16384 positions and 256 experts) rather than wait for one that adds them up. Up to 32 positions
 // one CTA does both. What bounds it: latency up to some thousand positions, then the instructions of
-// the ranking, not the logits' bytes.
+// the ranking (650 a position of 256 experts by softmax, 1050 by sigmoid under the group rule), not the logits' bytes:
+// 16384 positions take 20.5 and 31.6 us, their bytes 2.8; one position takes 5.5.
 //
 // The sigmoid router's order is that of sigmoid(G) + bias in exact arithmetic. It is decided in fp32
 // where neighbours are further apart than fp32's roundings can move them; for the positions where they
@@ -516,6 +517,11 @@ __device__ __forceinline__ void scan_totals(const int *total, int E, int *offset
   __syncthreads();
 }
 
+// Counts of CTAs of one pass lie by expert, a byte each, in rows of whole vectors.
+__host__ __device__ constexpr int byte_row(int ctas) { return (ctas + 15) & ~15; }
+// The first n bytes of a word.
+__device__ __forceinline__ uint32_t low_bytes(int n) { return n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u; }
+
 // Selection, weights and, in slots, each edge's place among its CTA's edges of the expert; the CTA's counts. The only
 // CTA of a grid (with one pass) finishes the worklist too. Selecting takes a warp a position; what follows takes a
 // thread an edge.
@@ -630,7 +636,12 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
     }
     __syncthreads();
   }
-  for (int i = tid; i < E; i += threads) a.counts[static_cast<int64_t>(blockIdx.x) * E + i] = s_count[i];
+  if (passes == 1) {  // at most 128: a byte
+    uint8_t *at = reinterpret_cast<uint8_t *>(a.counts) + blockIdx.x;
+    for (int i = tid; i < E; i += threads) at[static_cast<int64_t>(i) * byte_row(gridDim.x)] = static_cast<uint8_t>(s_count[i]);
+  } else {
+    for (int i = tid; i < E; i += threads) a.counts[static_cast<int64_t>(blockIdx.x) * E + i] = s_count[i];
+  }
 }
 
 // Places: what lower experts and earlier CTAs hold is added to every edge's place.
@@ -644,20 +655,36 @@ __global__ void __launch_bounds__(THREADS) k_router_place(const RouteArgs a, int
   // threads of one expert share the CTAs out
   const int per = max(1, THREADS / E), ctas = gridDim.x, mine = blockIdx.x;
   for (int i = tid; i < E * per; i += THREADS) {
-    const int e = i % E, part = i / E;
-    int total = 0, before = 0;
+    int e;
+    unsigned total = 0u, before = 0u;
+    if (passes == 1) {
+      const int row = byte_row(ctas);
+      e = i / per;
+      for (int b = 16 * (i % per); b < ctas; b += 16 * per) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.counts) + static_cast<int64_t>(e) * row + b));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          total = __dp4a(w[q] & low_bytes(ctas - b - 4 * q), 0x01010101u, total);
+          before = __dp4a(w[q] & low_bytes(mine - b - 4 * q), 0x01010101u, before);
+        }
+      }
+    } else {
+      e = i % E;
+      const int part = i / E;
 #pragma unroll 8
-    for (int b = part; b < ctas; b += per) {
-      const int n = __ldcg(a.counts + static_cast<int64_t>(b) * E + e);
-      total += n;
-      before += b < mine ? n : 0;
+      for (int b = part; b < ctas; b += per) {
+        const unsigned n = __ldcg(a.counts + static_cast<int64_t>(b) * E + e);
+        total += n;
+        before += b < mine ? n : 0u;
+      }
     }
     if (per == 1) {
-      s_total[e] = total;
-      s_before[e] = before;
+      s_total[e] = static_cast<int>(total);
+      s_before[e] = static_cast<int>(before);
     } else {
-      atomicAdd(&s_total[e], total);
-      atomicAdd(&s_before[e], before);
+      atomicAdd(&s_total[e], static_cast<int>(total));
+      atomicAdd(&s_before[e], static_cast<int>(before));
     }
   }
   __syncthreads();
@@ -711,13 +738,15 @@ template <int EPL> cudaError_t launch_select(const RouteArgs &a, const Split &sp
 
 size_t router_workspace(int64_t n_tok, int n_experts) {
   const Split sp = split_of(n_tok, num_sms());
-  return sp.ctas == 1 && sp.passes == 1 ? 0 : static_cast<size_t>(sp.ctas) * n_experts * sizeof(int32_t);
+  if (sp.passes > 1) return static_cast<size_t>(sp.ctas) * n_experts * sizeof(int32_t);
+  return sp.ctas == 1 ? 0 : static_cast<size_t>(byte_row(sp.ctas)) * n_experts + 12;  // from a 4-byte boundary to one of 16
 }
 
 cudaError_t launch_router(RouteArgs a, cudaStream_t s) {
   const int per16 = a.bf16 ? 8 : 4;
   a.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && (a.n_tok <= 1 || a.logits_stride % per16 == 0);
   const Split sp = split_of(a.n_tok, num_sms());
+  if (sp.passes == 1) a.counts = reinterpret_cast<int32_t *>((reinterpret_cast<uintptr_t>(a.counts) + 15) & ~static_cast<uintptr_t>(15));
   if (a.n_experts <= 64) return launch_select<2>(a, sp, s);
   if (a.n_experts <= 256) return launch_select<8>(a, sp, s);
   return launch_select<32>(a, sp, s);
