@@ -683,7 +683,7 @@ epoch_status epoch_expert_matmul(const epoch_expert_args *args, epoch_stream str
  * sizes out of range. Host only. */
 int32_t epoch_expert_matmul_kernel(int32_t kind, int32_t n_groups, int32_t m, int32_t n, int32_t k, int32_t n_sms);
 
-/* Test hook: epoch_expert_matmul whose operand copies count 16 bytes that never come, as
+/* Test hook: epoch_expert_matmul by its tiles' kernel whose operand copies count 16 bytes that never come, as
  * epoch_test_fp8_timeout. EPOCH_EINVAL also for EPOCH_EXPERT_F32, whose kernel has no waits. */
 epoch_status epoch_test_expert_timeout(const epoch_expert_args *args, int64_t timeout_ns, epoch_stream stream);
 

@@ -3,7 +3,8 @@
 The compute path is the C-ABI library built from ``csrc/`` (see
 ``include/epoch.h``); this package holds its ctypes binding (``binding``), a
 torch-facing wrapper (``layer.EpochLayer``), the operators a model runs around
-the layer (``ops``: norms before and after a block, FP8 products) and the
+the layer or in its place (``ops``: norms before and after a block, FP8
+products, the router, the experts' products and their sum by themselves) and the
 in-tree build (``builder.build``). Importing the package does not load the
 library; the first call into it does, and fails loudly if the library has not
 been built.
