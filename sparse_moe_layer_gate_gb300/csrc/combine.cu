@@ -6,7 +6,8 @@
 // experts); one past the last edge makes the row NaN. Bound by the edges' bytes: a thread takes up to eight
 // columns, by vectors as wide as the rows' alignment allows, with the edges' loads of four j together on
 // their way; slots and weights are read once for all of its columns (8192 positions of 8 edges by 4096
-// columns in bf16: 100 us, 6.0 TB/s).
+// columns in bf16: 100 us, 6.0 TB/s). bf16 rows off 16-byte boundaries come by aligned vectors too, which
+// are shifted (2000 positions of 8 edges by 2779 columns: 23.7 us; by elements 69).
 #include "common.cuh"
 #include "layer.h"
 
@@ -135,6 +136,117 @@ template <typename T, int C> __global__ void __launch_bounds__(kThreads, 4) k_co
   }
 }
 
+// Eight values of a bf16 row from column c0 on (from -7 on; c0 < hidden), whatever 2-byte boundary they start on: the two
+// aligned vectors that hold them, shifted. A vector without a column of the row is not read; of the others only lie
+// columns of the row in use. (No vector crosses into a page that the row has no part of.)
+__device__ __forceinline__ void load_shifted(const __nv_bfloat16 *row, int c0, int hidden, uint32_t (&w)[8], int *off) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c0);
+  const uint4 *from = reinterpret_cast<const uint4 *>(at & ~static_cast<uintptr_t>(15));
+  *off = static_cast<int>(at & 15u) / 2;
+  const int first = c0 - *off;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 0u;
+  if (first + 8 > 0) asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(from));
+  if (*off > 0 && first + 8 < hidden)
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(from + 1));
+}
+__device__ __forceinline__ void shift(uint32_t (&w)[8], int off, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 4 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 2 ? w[i + 1] : w[i];
+  const unsigned pick = off & 1 ? 0x5432u : 0x3210u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = __byte_perm(w[i], w[i + 1], pick);
+    v[2 * i] = __uint_as_float(u << 16);
+    v[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
+  }
+}
+
+// bf16 edges whose rows start or end off 16-byte boundaries: a thread takes the eight columns of 16 or 32 aligned bytes of the
+// output row, so that lanes' stores are whole vectors too.
+__global__ void __launch_bounds__(kThreads, 4) k_combine_shifted(const CombineArgs a, unsigned lanes) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t t = i / lanes;
+  if (t >= a.n_tok) return;
+  const uintptr_t out = reinterpret_cast<uintptr_t>(a.out) + t * a.out_stride * (a.out_bf16 ? 2 : 4);
+  const int c0 = static_cast<int>(i - t * lanes) * 8 - static_cast<int>(out & 15u) / (a.out_bf16 ? 2 : 4);
+  if (c0 >= a.hidden) return;
+  const int32_t *slots = a.slots + t * a.k;
+  const float *weights = a.weights + t * a.k;
+  const __nv_bfloat16 *edges = static_cast<const __nv_bfloat16 *>(a.edges);
+  float y[8] = {};
+  bool bad = false;
+  constexpr int kTogether = 4;
+  for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+    uint32_t x[kTogether][8];
+    float w[kTogether];
+    int off[kTogether];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const int slot = j0 + j < a.k ? __ldg(slots + j0 + j) : -1;
+      const bool in = slot >= 0 && slot < a.n_edges;
+      bad = bad || slot >= a.n_edges;
+      w[j] = 0.f;
+      off[j] = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[j][q] = 0u;
+      if (in) {
+        w[j] = __ldg(weights + j0 + j);
+        load_shifted(edges + slot * a.edges_stride, c0, a.hidden, x[j], &off[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      float v[8];
+      shift(x[j], off[j], v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = fmaf(w[j], v[q], y[q]);
+    }
+  }
+  auto add = [&](const void *base, bool bf16, int64_t at) {
+    float v[8];
+    if (bf16) {
+      uint32_t x[8];
+      int off;
+      load_shifted(static_cast<const __nv_bfloat16 *>(base) + at, c0, a.hidden, x, &off);
+      shift(x, off, v);
+    } else {
+      const float *row = static_cast<const float *>(base) + at;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = c0 + q >= 0 && c0 + q < a.hidden ? row[c0 + q] : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] += v[q];
+  };
+  if (a.shared) add(a.shared, true, t * a.shared_stride);
+  if (a.residual) add(a.residual, a.residual_bf16, t * a.residual_stride);
+  if (bad)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(0x7FC00000u);
+  const bool whole = c0 >= 0 && c0 + 8 <= a.hidden;
+  if (a.out_bf16) {
+    __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(out) + c0;
+    if (whole) {
+      store_c<8>(to, y);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c0 + q >= 0 && c0 + q < a.hidden) to[q] = __float2bfloat16_rn(y[q]);
+    }
+  } else {
+    float *to = reinterpret_cast<float *>(out) + c0;
+    if (whole) {
+      store_c<8>(to, y);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c0 + q >= 0 && c0 + q < a.hidden) to[q] = y[q];
+    }
+  }
+}
+
 template <typename T, int C> cudaError_t launch_columns(const CombineArgs &a, cudaStream_t s) {
   const int64_t lanes = (a.hidden + 7) / 8, grid = (a.n_tok * lanes + kThreads - 1) / kThreads;
   k_combine_edges<T, C><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(lanes));
@@ -162,7 +274,11 @@ cudaError_t launch_combine_edges(const CombineArgs &a, bool bf16, cudaStream_t s
   fits(a.shared, a.n_tok, a.shared_stride, bf16 ? 2 : 4);
   fits(a.residual, a.n_tok, a.residual_stride, a.residual_bf16 ? 2 : 4);
   fits(a.out, a.n_tok, a.out_stride, a.out_bf16 ? 2 : 4);
-  return bf16 ? launch_type<__nv_bfloat16>(a, c, s) : launch_type<float>(a, c, s);
+  if (!bf16) return launch_type<float>(a, c, s);
+  if (c == 8) return launch_columns<__nv_bfloat16, 8>(a, s);
+  const int64_t lanes = (a.hidden + 14) / 8, grid = (a.n_tok * lanes + kThreads - 1) / kThreads;
+  k_combine_shifted<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(lanes));
+  return cudaGetLastError();
 }
 
 }  // namespace epoch

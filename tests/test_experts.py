@@ -280,6 +280,37 @@ def test_combine_layouts(ops):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [1, 6, 16, 77, 1032])
+@pytest.mark.parametrize("rt,ot", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_combine_rows_from_any_boundary(ops, H, rt, ot):
+    """Rows of each tensor that start on every 2-byte (4-byte) boundary, with NaN beside them; results stay in their row."""
+    g = _gen(H)
+    T, k, n = 9, 5, 40
+
+    def rows(count, dtype, first, pad):
+        flat = torch.full((first + count * (H + pad) + 1,), math.nan, device="cuda", dtype=dtype)
+        view = flat[first:first + count * (H + pad)].view(count, H + pad)[:, :H]
+        return flat, view.copy_(_rnd(g, count, H, dtype=dtype))
+
+    slots = torch.randint(-1, n, (T, k), generator=g, device="cuda", dtype=I32)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    for first in range(8):
+        for pad in (first, 3 - first % 3):
+            _, edges = rows(n, BF16, first, pad)
+            _, shared = rows(T, BF16, (3 * first + 1) % 8, pad)
+            _, res = rows(T, rt, (first + 5) % 8, pad + 1)
+            flat, out = rows(T, ot, 7 - first, pad + 2)
+            y, size = combine64(edges, slots, w, shared, res)
+            bound = size * (k + 3) * U + y.abs() * _half(ot) * (ot == BF16) * (1 + 2 ** -7) + 1e-38
+            assert ops.combine(edges, slots, w, shared=shared, residual=res, out=out) is out
+            _within(out, y, bound)
+            assert int(flat.isnan().sum()) == flat.numel() - T * H
+            if ot == BF16:  # in place on the shared experts' output
+                assert ops.combine(edges, slots, w, shared=shared, residual=res, out=shared) is shared
+                assert torch.equal(shared, out)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("H", [1024, 1001])
 def test_combine_offsets_pass_32_bits(ops, H):
     far = (1 << 31) // 2 + 24
