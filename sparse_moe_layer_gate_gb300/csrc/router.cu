@@ -8,7 +8,9 @@
 // 16384 positions and 256 experts) rather than wait for one that adds them up. Up to 32 positions
 // one CTA does both. What bounds it: latency up to some thousand positions, then the instructions of
 // the ranking (650 a position of 256 experts by softmax, 1050 by sigmoid under the group rule), not the logits' bytes:
-// 16384 positions take 20.5 and 31.6 us, their bytes 2.8; one position takes 5.5.
+// 16384 positions take 20.5 and 31.6 us, their bytes 2.8; one position takes 5.5. A lane holds 2, 4, 8, 16 or 32
+// experts, the fewest that reach all of them: what it does for each is most of the work (8192 positions of 512 experts,
+// sigmoid in two groups: 27 us with 16 a lane, 84 with 32; of 128 experts 18 with four, 29 with eight).
 //
 // The sigmoid router's order is that of sigmoid(G) + bias in exact arithmetic. It is decided in fp32
 // where neighbours are further apart than fp32's roundings can move them; for the positions where they
@@ -32,12 +34,15 @@ __device__ __forceinline__ float logit(const void *row, bool bf16, int e) {
 template <int EPL> struct Raw {
   uint32_t w[EPL];
 };
-template <int EPL> __device__ __forceinline__ bool whole(bool vec, int E) { return EPL % 8 == 0 && vec && lane_id() * EPL + EPL <= E; }
+template <int EPL> __device__ __forceinline__ bool whole(bool vec, int E) { return EPL % 4 == 0 && vec && lane_id() * EPL + EPL <= E; }
 template <int EPL> __device__ __forceinline__ void load_raw(const void *row, bool bf16, int E, bool vec, Raw<EPL> &r) {
   const int e0 = lane_id() * EPL;
-  if constexpr (EPL % 8 == 0) {
+  if constexpr (EPL % 4 == 0) {
     if (whole<EPL>(vec, E)) {
-      if (bf16) {
+      if (bf16 && EPL == 4) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(row) + e0));
+        r.w[0] = u.x, r.w[1] = u.y;
+      } else if (bf16) {
 #pragma unroll
         for (int q = 0; q < EPL / 8; ++q) {
           const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(row) + e0) + q);
@@ -390,7 +395,7 @@ template <int EPL> __device__ __noinline__ bool limit_groups(unsigned *key, cons
 // One position by one warp: selection j goes to id[j] (-1: none) and, with the softmax router, its logit to val[j]; stat
 // gets what its weights need besides: the softmax's largest logit and, where they are raw, its sum over all experts;
 // else 0, or NaN where a logit is (which spoils the weights). `eligible` has a bit for each of the lane's experts,
-// bias their biases (up to eight).
+// bias their biases (up to sixteen).
 template <int EPL>
 __device__ __forceinline__ void route_row(const RouteArgs &a, const void *row, float (&v)[EPL], unsigned eligible,
                                           const float (&bias)[EPL], uint2 *scratch, int16_t *id, float *val, float2 *stat) {
@@ -447,7 +452,7 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, const void *row, f
 #pragma unroll
   for (int q = 0; q < EPL; ++q) {
     const int e = lane * EPL + q;
-    v[q] = sigmoid_near(v[q]) + (EPL <= 8 ? bias[q] : a.bias != nullptr && e < a.n_experts ? __ldg(a.bias + e) : 0.f);
+    v[q] = sigmoid_near(v[q]) + (EPL <= 16 ? bias[q] : a.bias != nullptr && e < a.n_experts ? __ldg(a.bias + e) : 0.f);
     const unsigned place = number_key(v[q]);
     key[q] = key[q] == 0u ? 0u : place;
     most = max(most, place - kLowest - 1u);
@@ -528,7 +533,7 @@ __device__ __forceinline__ uint32_t low_bytes(int n) { return n >= 4 ? 0xFFFFFFF
 template <int EPL, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, int passes, int pass) {
   constexpr int kE = EPL * 32;
-  constexpr bool kAhead = EPL <= 8;  // the next position's logits are on their way (wider lanes have no registers for it)
+  constexpr bool kAhead = EPL <= 16;  // the next position's logits are on their way (wider lanes have no registers for it)
   __shared__ uint32_t s_bits[kPass / 32][kE];
   __shared__ int s_count[kE], s_off[kE + 1], s_warp[32];
   __shared__ uint2 s_scratch[THREADS / 32][32];
@@ -748,7 +753,9 @@ cudaError_t launch_router(RouteArgs a, cudaStream_t s) {
   const Split sp = split_of(a.n_tok, num_sms());
   if (sp.passes == 1) a.counts = reinterpret_cast<int32_t *>((reinterpret_cast<uintptr_t>(a.counts) + 15) & ~static_cast<uintptr_t>(15));
   if (a.n_experts <= 64) return launch_select<2>(a, sp, s);
+  if (a.n_experts <= 128) return launch_select<4>(a, sp, s);
   if (a.n_experts <= 256) return launch_select<8>(a, sp, s);
+  if (a.n_experts <= 512) return launch_select<16>(a, sp, s);
   return launch_select<32>(a, sp, s);
 }
 

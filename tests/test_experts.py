@@ -101,7 +101,7 @@ def check_route(r, want, what=""):
 
 ROUTE_SIZES = [(1, 256, 8), (1, 1, 1), (2, 2, 2), (5, 37, 3), (31, 64, 4), (32, 65, 8), (33, 256, 8), (64, 256, 16), (65, 8, 8),
                (127, 128, 1), (128, 257, 7), (129, 256, 8), (1000, 64, 6), (700, 1024, 16), (5000, 48, 2),
-               (19457, 16, 3), (45000, 33, 4)]
+               (19457, 16, 3), (45000, 33, 4), (300, 512, 8), (40, 400, 16), (500, 100, 5)]
 
 
 @pytest.mark.gpu
@@ -114,7 +114,7 @@ def test_route_softmax(ops, T, E, k, dtype, raw):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,E,k,groups,top", [(1, 256, 8, 8, 4), (1, 4, 4, 4, 1), (7, 24, 5, 6, 2), (33, 256, 8, 1, 1), (130, 64, 16, 32, 3),
+@pytest.mark.parametrize("T,E,k,groups,top", [(1, 256, 8, 8, 4), (1, 4, 4, 4, 1), (7, 24, 5, 6, 2), (90, 512, 8, 16, 4), (90, 128, 8, 8, 3), (64, 320, 9, 5, 2), (33, 256, 8, 1, 1), (130, 64, 16, 32, 3),
                                               (200, 1024, 8, 32, 4), (1500, 256, 8, 8, 4), (300, 512, 16, 16, 1), (40, 30, 16, 2, 1)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("form", ["bias", "no_bias", "raw", "masks"])
@@ -130,7 +130,7 @@ def test_route_sigmoid_groups(ops, T, E, k, groups, top, dtype, form):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("E,groups", [(64, 1), (256, 8), (300, 1)])
+@pytest.mark.parametrize("E,groups", [(64, 1), (256, 8), (300, 1), (128, 4), (512, 8)])
 def test_route_scores_that_fp32_cannot_tell_apart(ops, E, groups):
     """Logits a step or two apart, where sigmoid + bias round to the same fp32 value or to the wrong order: the order
     is that of exact arithmetic."""
