@@ -145,10 +145,88 @@ template <int Q> __device__ __forceinline__ void load_cols(uint32_t at, float (&
   }
 }
 
+// The words of a row that starts on no 16-byte boundary, `n` elements of SIZE bytes from `dst` on: up to the next boundary in
+// pieces, then whole vectors of what is left, shifted, and pieces at the end. (A lane has a row: element stores write 32
+// sectors an instruction.)
+template <int SIZE, int W> __device__ __forceinline__ void store_shifted(uint8_t *dst, int n, uint32_t (&w)[W]) {
+  constexpr int kPer = 16 / SIZE;  // elements of a vector
+  const int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(dst) & 15u)) & 15u) / SIZE;
+  if (n > W * 4 / SIZE) n = W * 4 / SIZE;
+  if (n < head) {
+#pragma unroll
+    for (int i = 0; i < kPer - 1; ++i)
+      if (i < n) {
+        if constexpr (SIZE == 2) reinterpret_cast<uint16_t *>(dst)[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+        else reinterpret_cast<uint32_t *>(dst)[i] = w[i];
+      }
+    return;
+  }
+  if constexpr (SIZE == 2) {
+    const bool odd = head & 1;
+    if (odd) *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(w[0]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __byte_perm(w[i], i + 1 < W ? w[i + 1] : 0u, odd ? 0x5432u : 0x3210u);
+    if (odd) dst += 2;
+  }
+  const bool one = head & (4 / SIZE), two = head & (8 / SIZE);  // words before the boundary
+  if (one) *reinterpret_cast<uint32_t *>(dst) = w[0];
+#pragma unroll
+  for (int i = 0; i + 1 < W; ++i) w[i] = one ? w[i + 1] : w[i];
+  if (one) dst += 4;
+  if (two) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+#pragma unroll
+  for (int i = 0; i + 2 < W; ++i) w[i] = two ? w[i + 2] : w[i];
+  if (two) dst += 8;
+  n -= head;
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const int left = n - i * kPer;
+    uint8_t *to = dst + 16 * i;
+    const uint32_t *u = w + 4 * i;
+    if (left >= kPer) {
+      *reinterpret_cast<uint4 *>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else if (left > 0) {
+      const bool b8 = left & (8 / SIZE), b4 = left & (4 / SIZE);
+      const uint32_t x = b8 ? u[2] : u[0], y = b8 ? u[3] : u[1];
+      if (b8) *reinterpret_cast<uint2 *>(to) = make_uint2(u[0], u[1]);
+      if (b8) to += 8;
+      if (b4) *reinterpret_cast<uint32_t *>(to) = x;
+      if constexpr (SIZE == 2) {
+        if (b4) to += 4;
+        if (left & 1) *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(b4 ? y : x);
+      }
+    }
+  }
+}
+
 // Q consecutive values of an output row from column n0 on, `n` of which exist, in accesses of `align` bytes: 32 (whole
-// sectors), 16 or the elements.
-template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, int n, const float (&v)[Q], bool bf16, int align) {
+// sectors) or 16; less: shifted to 16.
+template <int Q, int WORDS> __device__ __forceinline__ void store_cols(void *row, int n0, int n, const float (&v)[Q], bool bf16, int align) {
   constexpr int kRun = Q < 16 ? Q : 16;
+  if (align < 16) {  // WORDS at a time: all of a run's would not fit into the registers
+    constexpr int kHalves = Q < 2 * WORDS ? Q : 2 * WORDS, kWords = Q < WORDS ? Q : WORDS;
+    if (bf16) {
+#pragma unroll
+      for (int j = 0; j < Q; j += kHalves) {
+        uint32_t w[kHalves / 2];
+#pragma unroll
+        for (int i = 0; i < kHalves / 2; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        if (j < n) store_shifted<2>(static_cast<uint8_t *>(row) + 2 * (n0 + j), n - j, w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < Q; j += kWords) {
+        uint32_t w[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = __float_as_uint(v[j + i]);
+        if (j < n) store_shifted<4>(static_cast<uint8_t *>(row) + 4 * (n0 + j), n - j, w);
+      }
+    }
+    return;
+  }
   if (bf16) {
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(row) + n0;
 #pragma unroll
@@ -165,7 +243,7 @@ template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, i
       }
 #pragma unroll
       for (int c = 0; c < kRun; c += 8) {
-        if (align >= 16 && j + c + 8 <= n) {
+        if (j + c + 8 <= n) {
           *reinterpret_cast<uint4 *>(dst + j + c) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
         } else {
 #pragma unroll
@@ -188,7 +266,7 @@ template <int Q> __device__ __forceinline__ void store_cols(void *row, int n0, i
       }
 #pragma unroll
       for (int c = j; c < j + 8; c += 4) {
-        if (align >= 16 && c + 4 <= n) {
+        if (c + 4 <= n) {
           *reinterpret_cast<float4 *>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         } else {
 #pragma unroll
@@ -642,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
             continue;
           }
         }
-        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, p.align);
+        store_cols<Q, PAIR ? 8 : 16>(dst, n0, p.out_n - n0, v0, bf16, p.align);
       } else {
 #pragma unroll
         for (int j = 0; j < Q; ++j) {
@@ -656,8 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
             continue;
           }
         }
-        store_cols<Q>(dst, n0, p.out_n - n0, v0, bf16, p.align);
-        if (n0 + Q < p.out_n) store_cols<Q>(dst, n0 + Q, p.out_n - n0 - Q, v1, bf16, p.align);
+        store_cols<Q, PAIR ? 8 : 16>(dst, n0, p.out_n - n0, v0, bf16, p.align);
+        if (n0 + Q < p.out_n) store_cols<Q, PAIR ? 8 : 16>(dst, n0 + Q, p.out_n - n0 - Q, v1, bf16, p.align);
       }
     }
   }

@@ -15,6 +15,8 @@
 // The sigmoid router's order is that of sigmoid(G) + bias in exact arithmetic. It is decided in fp32
 // where neighbours are further apart than fp32's roundings can move them; for the positions where they
 // are not (2 in 1000 with 256 experts) the entries near the border are ranked once more in 64 bits.
+#include <climits>
+
 #include "common.cuh"
 #include "layer.h"
 #include "topk.cuh"
@@ -373,19 +375,25 @@ template <int EPL> __device__ __noinline__ bool limit_groups(unsigned *key, cons
   }
   const bool there = lane < a.n_group && held > 0;
   int rank = 0, before = 0;
+  bool close = false;  // to the score of any other group
 #pragma unroll 4
   for (int i = 0; i < a.n_group; ++i) {
     const float s = __shfl_sync(kAll, score, i);
     const int h = __shfl_sync(kAll, held, i);
     if (h > 0 && (s > score || (s == score && i < lane))) ++rank, before += h;
+    close = close || (h > 0 && i != lane && !groups_apart(s, score));
   }
   const unsigned chosen = __ballot_sync(kAll, there && (rank < a.topk_group || before < a.top_k));
   const unsigned others = __ballot_sync(kAll, there) & ~chosen;
   // A chosen and an unchosen group must be apart: the least chosen and the best other. Where more than topk_group are
-  // taken, their order counts too.
+  // taken, because those hold fewer than k, so many groups are chosen whatever their order only if all hold as many;
+  // else their order counts too.
   const unsigned low = __reduce_min_sync(kAll, (chosen >> lane) & 1u ? order_key(score) : 0xffffffffu);
   const unsigned high = __reduce_max_sync(kAll, (others >> lane) & 1u ? order_key(score) : 0u);
-  const bool sure = __popc(chosen) <= a.topk_group && (others == 0u || groups_apart(key_value(low), key_value(high)));
+  const bool alike = __reduce_max_sync(kAll, there ? held : 0) == __reduce_min_sync(kAll, there ? held : INT_MAX);
+  const bool sure = __popc(chosen) <= a.topk_group || alike
+                        ? others == 0u || groups_apart(key_value(low), key_value(high))
+                        : !__any_sync(kAll, ((chosen >> lane) & 1u) && close);
 #pragma unroll
   for (int q = 0; q < EPL; ++q)
     if (!((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) key[q] = 0u;

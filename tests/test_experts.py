@@ -391,6 +391,32 @@ def test_grouped_matmul(ops, m, e, n, k, form, dt, ot):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,e,n", [(400, 2, 75), (1000, 3, 334), (700, 1, 2001), (1000, 3, 767), (1000, 1, 4095), (1100, 1, 4093), (700, 64, 1021)])
+@pytest.mark.parametrize("ot", [BF16, F32])
+@pytest.mark.parametrize("form", ["bf16", "nvfp4"])
+def test_products_outputs_from_any_boundary(ops, m, e, n, ot, form):
+    """Output rows that start on every boundary of their type have the bits of aligned ones, and their neighbours stay."""
+    k, g = 64, _gen(m)
+    off = _offsets(np.random.RandomState(n), e, m)
+    x, w = _rnd(g, m, k, dtype=BF16), _rnd(g, e, n, k, dtype=BF16)
+    if form == "nvfp4":
+        (x, sx), (w, sw, _) = ops.fp4_quantize(x), ops.fp4_quantize_weight(w)
+
+    def run(out):
+        if form == "bf16":
+            return ops.grouped_matmul(x, w, off, out=out)
+        return ops.fp4_matmul(x, sx, w, sw, offsets=off, out=out)
+
+    want = run(torch.empty(m, (n + 15) // 16 * 16, device="cuda", dtype=ot)[:, :n])
+    for first in range(8):
+        for pad in (0, first + 1, 8):
+            flat = torch.full((first + m * (n + pad) + 3,), -7.0, device="cuda", dtype=ot)
+            out = run(flat[first:first + m * (n + pad)].view(m, n + pad)[:, :n])
+            assert torch.equal(out, want)
+            assert int((flat == -7).sum()) - int((want == -7).sum()) == flat.numel() - m * n
+
+
+@pytest.mark.gpu
 def test_grouped_matmul_longest_rows(ops):
     """Rows of 2^31 bytes: every place that is not zero counts, behind the last 32-bit offset too."""
     k = 1 << 30
@@ -791,6 +817,24 @@ def test_route_groups_that_fp32_cannot_tell_apart(ops, E, groups, top):
     for bias in (None, torch.zeros(E, device="cuda")):
         check_route(ops.route(x, k, router="sigmoid_group", bias=bias, n_group=groups, topk_group=top),
                     route64(x, k, True, bias=bias, n_group=groups, topk_group=top))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,groups,top", [(24, 8, 1), (60, 10, 1), (96, 32, 2), (256, 32, 0)])
+def test_route_more_groups_than_asked_for(ops, E, groups, top):
+    """Groups that hold fewer than k: more of them are searched, best first, and so on their order it depends which, where
+    some hold less than others (masks)."""
+    g = _gen(E)
+    T, k, size, top = 150, 8, E // groups, max(top, 1)
+    x = _rnd(g, T, E) - 3
+    best = 1 + torch.rand(T, 1, 2, generator=g, device="cuda")
+    steps = torch.randint(-2, 3, (T, groups, 2), generator=g, device="cuda", dtype=I32)
+    x.view(T, groups, size)[:, :, [1, size - 1]] = (best.expand(T, groups, 2).contiguous().view(torch.int32) + steps).view(F32)
+    x[::2] = _rnd(g, T // 2, E)
+    for kk in (k, min(16, E)):
+        for eligible in (None, torch.rand(E, generator=g, device="cuda") < 0.7):
+            check_route(ops.route(x, kk, router="sigmoid_group", n_group=groups, topk_group=top, eligible=eligible),
+                        route64(x, kk, True, n_group=groups, topk_group=top, eligible=eligible))
 
 
 # ------------------------------------------------------------------------------ streams and graphs
