@@ -2,8 +2,8 @@
 // fp32 operands, and TF32's ten bits would lose what an fp32 layer keeps). The formula is that of
 // expert_gemm.cu; sums are fp32, in ascending k.
 //
-// Many rows (k_expert_simt): tiles of 128 rows x 128 columns, sixteen columns of K at a time through two
-// places in shared memory, each thread 8 x 8 sums as pairs for the packed fp32 multiply-add. With swiglu a
+// Many rows (k_expert_simt): tiles of 128 or 64 rows x 128 columns, sixteen columns of K at a time through two
+// places in shared memory, each thread 8 or 4 x 8 sums as pairs for the packed fp32 multiply-add. With swiglu a
 // tile's columns are 64 gate and 64 up rows of the weights: a thread's columns 4 and 4 of them. Bound by
 // the FFMA pipes (8192 x 2048 x 2048 over 8 experts 1.44 ms, 48 TFLOP/s).
 //
@@ -34,30 +34,29 @@ __device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
 
-constexpr int kRows = 128;
-__global__ void __launch_bounds__(kThreads) k_expert_simt(const ExpertGemmArgs a, int nt_n) {
-  constexpr int TM = kRows / 16;                     // rows of a thread
-  constexpr int LA = kRows * kDepth / 4 / kThreads;  // float4 loads of a thread for the rows
+template <int ROWS> __global__ void __launch_bounds__(kThreads) k_expert_simt(const ExpertGemmArgs a, int nt_n) {
+  constexpr int TM = ROWS / 16;                     // rows of a thread
+  constexpr int LA = ROWS * kDepth / 4 / kThreads;  // float4 loads of a thread for the rows
   constexpr int LB = kCols * kDepth / 4 / kThreads;
-  __shared__ __align__(16) float s_a[2][kDepth][kRows + kPad], s_b[2][kDepth][kCols + kPad];
+  __shared__ __align__(16) float s_a[2][kDepth][ROWS + kPad], s_b[2][kDepth][kCols + kPad];
   __shared__ int s_start[kMaxGroups + 1], s_cum[kMaxGroups + 1];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (a.offsets != nullptr) {
-    if (warp_id() == 0) group_tiles(a.offsets, a.n_groups, a.m, kRows, s_start, s_cum);
+    if (warp_id() == 0) group_tiles(a.offsets, a.n_groups, a.m, ROWS, s_start, s_cum);
   } else if (tid == 0) {
     s_start[0] = 0;
     s_start[1] = a.m;
     s_cum[0] = 0;
-    s_cum[1] = (a.m + kRows - 1) / kRows;
+    s_cum[1] = (a.m + ROWS - 1) / ROWS;
   }
   __syncthreads();
-  TileWalk walk(s_start, s_cum, a.offsets ? a.n_groups : 1, nt_n, kRows, 0);
+  TileWalk walk(s_start, s_cum, a.offsets ? a.n_groups : 1, nt_n, ROWS, 0);
   const int half_n = a.N / 2, out_n = a.swiglu ? half_n : a.N;
   const float *x = static_cast<const float *>(a.a), *w = static_cast<const float *>(a.b);
   for (int t = blockIdx.x; t < walk.total; t += gridDim.x) {
     int e, row0, rows, nt;
     walk.at(t, &e, &row0, &rows, &nt);
-    rows = min(rows, kRows);
+    rows = min(rows, ROWS);
     // where this thread's pieces come from: rows and weights that do not exist are zeros
     const float *pa[LA], *pb[LB];
     const int kq = (tid & 3) * 4;  // columns of K
@@ -282,18 +281,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_expert_stream(const ExpertGemmA
 }  // namespace
 
 cudaError_t launch_expert_simt(const ExpertGemmArgs &a, cudaStream_t s) {
-  const int64_t groups = a.offsets ? (a.n_groups < a.m ? a.n_groups : a.m) : 1;
+  const int64_t groups = a.offsets ? (a.n_groups < a.m ? a.n_groups : a.m) : 1, sms = num_sms();
   const int64_t nt = (a.N + kCols - 1) / kCols;  // with swiglu 64 columns of each half
-  const int64_t tiles = (a.offsets ? a.m / kRows + groups : (a.m + kRows - 1) / kRows) * nt;
-  // Tall tiles where groups fill most of them and the device has work for all.
-  if (a.m > 32 * groups && tiles >= num_sms() / 4) {
-    const int64_t most = 4ll * num_sms();
-    k_expert_simt<<<static_cast<unsigned>(tiles < most ? tiles : most), kThreads, 0, s>>>(a, static_cast<int>(nt));
-  } else {
-    const int64_t nb = (a.N + 31) / 32, units = (a.offsets ? a.m / kTokens + groups : (a.m + kTokens - 1) / kTokens) * nb;
-    const int64_t most = 8ll * num_sms();
-    k_expert_stream<<<static_cast<unsigned>(units < most ? units : most), kThreads, 0, s>>>(a, static_cast<int>(nb));
-  }
+  const int64_t nb = (a.N + 31) / 32;
+  auto tiles = [&](int64_t rows) { return groups > 1 ? a.m / rows + groups : (a.m + rows - 1) / rows; };
+  // The least of three estimates in nanoseconds. A step of 16 columns takes a tile of 64 rows 1000 (loads, and few CTAs)
+  // or, with many, its SM 880 a tile; one of 128 rows 1700 or 1640; a unit of the streaming kernel some 6 and 0.0225 a column.
+  // (us by streaming, 64 and 128 rows: 1024 x 512 x 512 39, 35, 57; 1315 rows over 17 experts of 152 x 352 18, 26, 40;
+  // 2048 over 64 of 512 x 256 59, 33, 53; 8192 over 8 of 2048 x 2048 5197, 1573, 1437.)
+  const double steps = (a.K + kDepth - 1) / kDepth;
+  auto time_of = [&](int64_t rows, double one, double each) {
+    const double many = each * static_cast<double>(tiles(rows) * nt) / static_cast<double>(sms);
+    return 2000.0 + steps * (many > one ? many : one);
+  };
+  const double low = time_of(64, 1000.0, 880.0), tall = time_of(128, 1700.0, 1640.0);
+  const double stream = 6000.0 + static_cast<double>(tiles(kTokens) * nb) * (6.0 + 0.0225 * a.K);
+  auto grid = [&](int64_t n, int64_t most) { return static_cast<unsigned>(n < most ? n : most); };
+  if (stream <= low && stream <= tall) k_expert_stream<<<grid(tiles(kTokens) * nb, 8 * sms), kThreads, 0, s>>>(a, static_cast<int>(nb));
+  else if (low <= tall) k_expert_simt<64><<<grid(tiles(64) * nt, 4 * sms), kThreads, 0, s>>>(a, static_cast<int>(nt));
+  else k_expert_simt<128><<<grid(tiles(128) * nt, 4 * sms), kThreads, 0, s>>>(a, static_cast<int>(nt));
   return cudaGetLastError();
 }
 

@@ -365,7 +365,7 @@ def product_bound(y, size, steps, ot, swiglu):
 GROUPED = [(1, 1, 1, 8), (1, 8, 64, 64), (3, 2, 40, 72), (17, 5, 130, 200), (64, 64, 32, 128), (100, 3, 256, 512), (129, 1, 257, 1000),
            (200, 130, 96, 256), (300, 4, 520, 264), (1000, 3, 768, 192), (2050, 2, 1024, 128), (700, 1, 2000, 64),
            (1000, 1, 4096, 64), (900, 2, 4000, 192), (1100, 1, 4096, 136),
-           (5, 1, 4900, 72), (40, 1, 2600, 200), (60, 3, 1700, 136), (11, 2, 100, 4104), (16, 1, 2048, 2048)]
+           (5, 1, 4900, 72), (40, 1, 2600, 200), (60, 3, 1700, 136), (11, 2, 100, 4104), (16, 1, 2048, 2048), (1200, 3, 600, 512), (2100, 2, 1030, 264)]
 
 
 @pytest.mark.gpu
