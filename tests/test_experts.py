@@ -678,6 +678,32 @@ def test_fp4_quantize_weight(ops, form, dt, shape):
         assert torch.equal((v if e else v[None])[i], ops.fp4_dequantize(qs[i], ss[i], tensor_scale=float(t[i]), out_dtype=F32))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_fp4_quantize_swiglu_of_any_gate(ops, dt):
+    """Gates where the sigmoid is 1, a step from 1, subnormal or nothing, beside ordinary ones: a block of one value is off
+    by half a step of e2m1 (an eighth), or by the smallest scale's."""
+    gates = [1e-30, -1e-30, 3e-39, -0.0, 0.0, 0.7, -3.0, 17.0, 60.0, -60.0, -80.0, -87.0, -88.5, 90.0, 3e38, 1e30]
+    x = torch.empty(len(gates) + 1, 2 * 64, device="cuda", dtype=dt)
+    x[:, 64:] = 1.5
+    x[:, :64] = torch.tensor(gates + [1.0], device="cuda")[:, None]
+    x[-1, 3:40:8] = torch.tensor([-100.0, 1e-35, 0.0, 70.0, -69.5], device="cuda").to(dt)  # in one thread with ordinary ones
+    q, s = ops.fp4_quantize(x, form="mxfp4", swiglu=True)
+    got = ops.fp4_dequantize(q, s, out_dtype=F32).double()
+    g64 = x[:, :64].double()
+    v = 1.5 * g64 * torch.sigmoid(g64)
+    top = v[-1].view(2, 32).abs().amax(1).repeat_interleave(32)  # the last row: by its blocks' scales
+    # a value above 4 s is off by s at most (5 to 4 or 6), in a block whose largest lies from 4 s to 8 s (then 7.99 to 6)
+    over = v.abs() > torch.finfo(F32).max  # 1.5 * 3e38 is infinite in fp32, and so its block NaN
+    assert int(over.sum()) == 64 and bool(got[over].isnan().all())
+    assert bool(((got - v)[:-1].abs() <= v[:-1].abs() / 4 + 2.0 ** -127)[~over[:-1]].all())
+    assert bool(((got - v)[-1].abs() <= top / 4 + 2.0 ** -127).all())
+    x[:, 5] = math.inf
+    q, s = ops.fp4_quantize(x, form="mxfp4", swiglu=True)
+    back = ops.fp4_dequantize(q, s)
+    assert bool(back[:, :32].isnan().all()) and bool(back[:, 32:][~over[:, 32:]].isfinite().all())
+
+
 # -------------------------------------------------------------------------------------- 4-bit products
 def fp4_operand(g, form, *shape, std=1.0):
     """(q, scales, values in 64 bits), made here: any code, scales of several octaves."""
