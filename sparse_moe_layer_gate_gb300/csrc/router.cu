@@ -249,10 +249,12 @@ __device__ __forceinline__ float sigmoid_near(float g) {
   return s;
 }
 // Whether two selection scores are apart whatever fp32 made of them: sigmoid as above, the sum with the bias half a
-// step of the result. Groups' scores are sums of two: twice that.
-__device__ __forceinline__ float reach(float a, float b) { return 1.2e-6f + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)); }
-__device__ __forceinline__ bool apart(float a, float b) { return fabsf(a - b) > reach(a, b); }
-__device__ __forceinline__ bool groups_apart(float a, float b) { return fabsf(a - b) > 2.0f * reach(a, b); }
+// step of the result.
+__device__ __forceinline__ bool apart(float a, float b) { return fabsf(a - b) > 1.2e-6f + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)); }
+// How far fp32 may have put a group's score from that of its two best, a + b: two sigmoids, 8e-7, and half a step of each
+// term, of their sum and of the ends of score -+ group_reach, each at most 2^-24 (|a| + |b|). The terms' sizes count and
+// not the sum's, which is small where the biases cancel.
+__device__ __forceinline__ float group_reach(float a, float b) { return 1.2e-6f + 2.5e-7f * (fabsf(a) + fabsf(b)); }
 
 // Ids of the entries that lanes have marked (bits of their EPL), in ascending order one a lane from scratch on; how many
 // there are, of which at most 32 fit.
@@ -316,8 +318,8 @@ __device__ __forceinline__ bool limit_groups_fast(unsigned (&key)[EPL], const Ro
     k2 = max(max(k2, o2), min(k1, o1));
     k1 = max(k1, o1);
   }
-  const float second = key_value(k2);
-  const unsigned mine = number_key(key_value(k1) + second);
+  const float first = key_value(k1), second = key_value(k2), score = first + second, off = group_reach(first, second);
+  const unsigned mine = number_key(score);
   // rounds of the best group left; equal ones go together (and are then too near, or all chosen)
   unsigned left = mine, bound = 0u;
 #pragma unroll 4
@@ -326,9 +328,10 @@ __device__ __forceinline__ bool limit_groups_fast(unsigned (&key)[EPL], const Ro
     if (left == bound) left = 0u;
   }
   bool in = mine >= bound;
-  const unsigned high = __reduce_max_sync(kAll, left);
-  if (!__all_sync(kAll, __popc(__ballot_sync(kAll, in)) == a.topk_group << shift &&
-                            (high == 0u || groups_apart(key_value(bound), key_value(high))))) {
+  // the least that a chosen group's score can be and the most of another's (an infinite one leaves no certainty: NaN is least)
+  const unsigned low = __reduce_min_sync(kAll, in ? order_key(score - off) : 0xffffffffu);
+  const unsigned high = __reduce_max_sync(kAll, in ? 0u : order_key(score + off));
+  if (!__all_sync(kAll, __popc(__ballot_sync(kAll, in)) == a.topk_group << shift && low > high)) {
     unsigned near = 0u;
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
@@ -351,7 +354,7 @@ __device__ __forceinline__ bool limit_groups_fast(unsigned (&key)[EPL], const Ro
 template <int EPL> __device__ __noinline__ bool limit_groups(unsigned *key, const RouteArgs &a) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = lane_id(), gs = a.n_experts / a.n_group;
-  float score = -INFINITY;  // lane i: group i's
+  float score = -INFINITY, off = 0.f;  // lane i: group i's, and how far it may be off
   int held = 0;
   for (int i = 0; i < a.n_group; ++i) {
     unsigned k1 = 0u, k2 = 0u;
@@ -369,31 +372,38 @@ template <int EPL> __device__ __noinline__ bool limit_groups(unsigned *key, cons
     const unsigned m2 = __reduce_max_sync(kAll, lane == __ffs(hold) - 1 ? k2 : k1);
     n = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
     if (lane == i) {
+      const float first = key_value(m1), second = m2 == 0u ? 0.f : key_value(m2);
       held = n;
-      score = m1 == 0u ? -INFINITY : m2 == 0u ? key_value(m1) : key_value(m1) + key_value(m2);
+      score = m1 == 0u ? -INFINITY : first + second;
+      off = group_reach(first, second);
     }
   }
   const bool there = lane < a.n_group && held > 0;
   int rank = 0, before = 0;
-  bool close = false;  // to the score of any other group
 #pragma unroll 4
   for (int i = 0; i < a.n_group; ++i) {
     const float s = __shfl_sync(kAll, score, i);
     const int h = __shfl_sync(kAll, held, i);
     if (h > 0 && (s > score || (s == score && i < lane))) ++rank, before += h;
-    close = close || (h > 0 && i != lane && !groups_apart(s, score));
   }
   const unsigned chosen = __ballot_sync(kAll, there && (rank < a.topk_group || before < a.top_k));
   const unsigned others = __ballot_sync(kAll, there) & ~chosen;
   // A chosen and an unchosen group must be apart: the least chosen and the best other. Where more than topk_group are
   // taken, because those hold fewer than k, so many groups are chosen whatever their order only if all hold as many;
   // else their order counts too.
-  const unsigned low = __reduce_min_sync(kAll, (chosen >> lane) & 1u ? order_key(score) : 0xffffffffu);
-  const unsigned high = __reduce_max_sync(kAll, (others >> lane) & 1u ? order_key(score) : 0u);
+  const unsigned low = __reduce_min_sync(kAll, (chosen >> lane) & 1u ? order_key(score - off) : 0xffffffffu);
+  const unsigned high = __reduce_max_sync(kAll, (others >> lane) & 1u ? order_key(score + off) : 0u);
   const bool alike = __reduce_max_sync(kAll, there ? held : 0) == __reduce_min_sync(kAll, there ? held : INT_MAX);
-  const bool sure = __popc(chosen) <= a.topk_group || alike
-                        ? others == 0u || groups_apart(key_value(low), key_value(high))
-                        : !__any_sync(kAll, ((chosen >> lane) & 1u) && close);
+  bool sure = low > high;  // (without others high is 0)
+  if (__any_sync(kAll, __popc(chosen) > a.topk_group && !alike)) {
+    bool close = false;  // to the score of any other group
+    for (int i = 0; i < a.n_group; ++i) {
+      const float s = __shfl_sync(kAll, score, i), o = __shfl_sync(kAll, off, i);
+      const int h = __shfl_sync(kAll, held, i);
+      close = close || (h > 0 && i != lane && !(fabsf(s - score) > o + off));
+    }
+    sure = !__any_sync(kAll, ((chosen >> lane) & 1u) && close);
+  }
 #pragma unroll
   for (int q = 0; q < EPL; ++q)
     if (!((chosen >> (((lane * EPL + q) / gs) & 31)) & 1u)) key[q] = 0u;
