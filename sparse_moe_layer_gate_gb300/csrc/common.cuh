@@ -29,6 +29,15 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
+// A router's sigmoid(g) for weights. Below kLowLogit fp32 rounds 1 + exp(g) to 1 and the sigmoid is exp(g), which leaves
+// fp32's normal range from -87 on (as 1 / (1 + exp(-g)) it is 0 from -89 on). Weights are quotients by a sum of sigmoids:
+// where `most`, the largest logit of the sum, is that low too, the result is sigmoid(g) / sigmoid(most).
+constexpr float kLowLogit = -17.f;
+__device__ __forceinline__ float sigmoid_over(float g, float most) {
+  if (g < kLowLogit) return expf(most < kLowLogit ? g - most : g);
+  return 1.0f / (1.0f + expf(-g));
+}
+
 // ------------------------------------------------------------------ error word
 __device__ __forceinline__ void set_error(uint32_t *err, uint32_t bits) { atomicOr(err, bits); }
 

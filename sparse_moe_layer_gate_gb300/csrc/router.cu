@@ -256,6 +256,18 @@ __device__ __forceinline__ bool apart(float a, float b) { return fabsf(a - b) > 
 // not the sum's, which is small where the biases cancel.
 __device__ __forceinline__ float group_reach(float a, float b) { return 1.2e-6f + 2.5e-7f * (fabsf(a) + fabsf(b)); }
 
+// Logits up to here have a score of 0 in 64 bits too (exp(-g) overflows): their order is that of the ids, and the weights of
+// a position that selects no other are 0 / 0.
+constexpr float kNoScore = -709.7827f;
+
+// The largest of a position's selected logits.
+__device__ __noinline__ float most_selected(const void *row, bool bf16, const int16_t *id, int k) {
+  float most = -INFINITY;
+  for (int j = 0; j < k; ++j)
+    if (id[j] >= 0) most = fmaxf(most, logit(row, bf16, id[j]));
+  return most;
+}
+
 // Ids of the entries that lanes have marked (bits of their EPL), in ascending order one a lane from scratch on; how many
 // there are, of which at most 32 fit.
 template <int EPL> __device__ __forceinline__ int gather_marked(unsigned marked, uint2 *scratch) {
@@ -611,7 +623,15 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       float x = 0.f;
       if (e >= 0) {
         atomicOr(&s_bits[r >> 5][e], 1u << (r & 31));
-        x = a.sigmoid ? 1.0f / (1.0f + expf(-logit(logits + (t0 + r) * row_bytes, bf16, e))) : expf(s_val[i] - s_stat[r].x);
+        if (a.sigmoid) {
+          const uint8_t *row = logits + (t0 + r) * row_bytes;
+          const float g = logit(row, bf16, e);
+          // (where g is not low the largest is not either)
+          const float most = g < kLowLogit && !a.raw_weights ? most_selected(row, bf16, s_id + r * k, k) : 0.f;
+          x = most <= kNoScore ? 0.f : sigmoid_over(g, most);
+        } else {
+          x = expf(s_val[i] - s_stat[r].x);
+        }
       }
       s_val[i] = x;
     }
