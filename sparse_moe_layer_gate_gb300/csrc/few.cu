@@ -544,7 +544,9 @@ __device__ __noinline__ void select_token(const FewParams &p, int t, uint2 *scra
       for (int j = 0; j < EPL; ++j) den += lo + j < E ? expf(v[j] - top) : 0.f;
     }
   } else {
-    if (mine) num = 1.f / (1.f + expf(-__ldcg(row + sel)));
+    const float g = mine ? __ldcg(row + sel) : -INFINITY;
+    const float most = key_value(__reduce_max_sync(kAll, order_key(g)));
+    if (mine) num = sigmoid_over(g, d.raw_weights ? 0.f : most);
   }
   if (!d.raw_weights) den = num;
 #pragma unroll

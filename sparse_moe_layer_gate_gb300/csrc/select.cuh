@@ -146,7 +146,8 @@ __device__ __noinline__ void select_sigmoid_group(const Dims &d, const float *v_
     const float o = __shfl_sync(0xffffffffu, v[c], owner);
     if (c == idx) z = o;
   }
-  const float sg = lane < k ? 1.f / (1.f + expf(-z)) : 0.f;
+  const float most = key_value(__reduce_max_sync(0xffffffffu, lane < k ? order_key(z) : 0u));
+  const float sg = lane < k ? sigmoid_over(z, d.raw_weights ? 0.f : most) : 0.f;
   float denom = 0.f;
   for (int j = 0; j < k; ++j) denom += __shfl_sync(0xffffffffu, sg, j);
   *sel_out = sel;
