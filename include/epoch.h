@@ -618,9 +618,9 @@ epoch_status epoch_combine(const epoch_combine_args *args, epoch_stream stream);
  *    s = e4m3(min(max|v'| / 6, 448)), at least 2^-9;  q = e2m1(v' / s)
  *  EPOCH_FP4_MXFP4: blocks of 32, s = 2^(floor(log2 max|v|) - 2), at least 2^-127, as e8m0
  *    (the exponent plus 127); q = e2m1(v / s); tensor_scale must be 1
- * Both roundings are to nearest even of the exact quotients; beyond 6, q is 6. The value
- * that a code stands for is q * s (* tensor_scale). A block that holds a NaN or an
- * infinity has a NaN scale (0x7F, 0xFF), and so does every block of a row whose index
+ * Both roundings are to nearest even of the exact quotients; beyond 6, q is 6 (of a v' that
+ * is beyond fp32 as well). The value that a code stands for is q * s (* tensor_scale). A
+ * block of v that holds a NaN or an infinity has a NaN scale (0x7F, 0xFF), and so does every block of a row whose index
  * is not in [0, n_src), which is not read; products with them are NaN.
  *  x_dev, rows_dev, n_src, swiglu as for epoch_fp8_quantize.
  *  q_dev [n_rows][cols / 2] bytes; scales_dev [ceil(cols / 256)][n_rows][16 or 8] bytes: the

@@ -15,6 +15,7 @@
 // One pass: a thread keeps its columns (32, or 8 of them where few blocks leave places on the device empty) in registers, and lanes
 // that share a block exchange its maximum. Bound by the instructions of the exact rounding (70 % of the issue slots), the
 // way back by latency: 8192 rows of 2048 gathered from bf16 to nvfp4 and back take 14.4 us, their bytes 5.8.
+#include <cfloat>
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -209,14 +210,10 @@ __global__ void __launch_bounds__(kThreads) k_fp4_quant(const Fp4QuantArgs a, un
   } else {
     open_words<T>(w, v);
   }
-  if constexpr (NV && EXACT) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] *= inv;
-  }
-  unsigned m[kB];
+  unsigned m[kB];  // of v: a maximum times 1 / t is the maximum of the v'
 #pragma unroll
   for (int b = 0; b < kB; ++b) {
-    if constexpr (sizeof(T) == 2 && !SWIGLU && !(NV && EXACT)) {
+    if constexpr (sizeof(T) == 2 && !SWIGLU) {
       uint32_t big = 0;  // largest magnitudes of the low and of the high halves
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) big = __vmaxu2(big, w[b * kPer / 2 + i] & 0x7FFF7FFFu);
@@ -237,9 +234,16 @@ __global__ void __launch_bounds__(kThreads) k_fp4_quant(const Fp4QuantArgs a, un
     const bool spoilt = m[b] >= 0x7F800000u || bad;
     float *y = v + b * kPer;
     if constexpr (NV) {
-      const float f = EXACT ? 1.0f : inv;
-      const uint32_t c = nv_scale(spoilt ? 0.f : __uint_as_float(m[b]) * f);
-      const float s = open_e4m3(c), r = reciprocal_near(s) * f;
+      const float most = __uint_as_float(m[b]) * inv;
+      const uint32_t c = nv_scale(spoilt ? 0.f : fminf(most, FLT_MAX));
+      const float s = open_e4m3(c), r = reciprocal_near(s) * (EXACT ? 1.0f : inv);
+      if constexpr (EXACT) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) y[i] *= inv;
+        if (most > FLT_MAX)  // beyond fp32: the largest codes, as beyond e4m3
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) y[i] = fminf(fmaxf(y[i], -FLT_MAX), FLT_MAX);
+      }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const uint32_t t = to_twelve(y[i] * r);

@@ -1,9 +1,11 @@
 """Edges of the experts' operators that their own sizes pass over, against forms in 64 bits."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from test_experts import BF16, F32, I32, _gen, _rnd, check_route, ops, route64  # noqa: F401
+from test_experts import BF16, E4M3, F32, I32, U8, _gen, _rnd, check_codes, check_route, ops, route64  # noqa: F401
 
 
 # ------------------------------------------------------------------------------------------- router
@@ -55,3 +57,65 @@ def test_route_sigmoids_below_the_range(ops, T):
                 want = route64(logits, k, True, raw=raw, **kw)
                 assert np.isfinite(want[1]).all()
                 check_route(ops.route(logits, k, router="sigmoid_group", raw_weights=raw, **kw), want)
+
+
+# ------------------------------------------------------------------------------------ 4-bit quantiser
+def _borders(s):
+    """Rows [scales, 32] of two blocks whose scale is s: every border between two codes times s, and a step to both sides."""
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    at = (s.unsqueeze(1) * mids).unsqueeze(2).view(torch.int32) + torch.tensor([-1, 0, 1], device="cuda", dtype=I32)
+    at = at.view(F32).reshape(-1, 21)
+    x = torch.zeros(s.numel(), 32, device="cuda")
+    x[:, :11], x[:, 16:26] = at[:, :11], at[:, 11:]
+    x[:, 15] = x[:, 31] = 6 * s
+    return x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 200])  # rows of every scale: few blocks, and many
+def test_fp4_quotients_on_both_sides_of_every_border(ops, n):
+    s = torch.arange(1, 127, device="cuda", dtype=U8).view(E4M3).float()
+    x = _borders(s).repeat(n, 1)
+    for y in (x, -x, torch.where(torch.arange(32, device="cuda") % 2 == 0, x, -x)):
+        q, sc = ops.fp4_quantize(y)
+        assert torch.equal(sc.view(U8)[0, :, :2], torch.arange(1, 127, device="cuda", dtype=U8).repeat(n)[:, None].expand(-1, 2))
+        check_codes(q, sc, y, "nvfp4")
+        q, sc = ops.fp4_quantize(y, tensor_scale=0.25)
+        check_codes(q, sc, y, "nvfp4", 0.25)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("n", [5, 3000])
+def test_fp4_quantize_by_any_tensor_scale(ops, dt, n):
+    """v' = v * (1 / tensor_scale), each rounded to fp32; the codes are those of v'."""
+    x = _rnd(_gen(n), n, 288, std=3.0, dtype=dt)
+    for t in (0.3, 1.7, 1e-5, 12345.0):
+        v = x.float() * (torch.ones((), device="cuda") / torch.tensor(t, device="cuda"))
+        q, s = ops.fp4_quantize(x, tensor_scale=t)
+        check_codes(q, s, v, "nvfp4")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("n", [2, 3000])
+@pytest.mark.parametrize("t", [2.0 ** -20, 2.0 ** -110, 3e-7])
+def test_fp4_quantize_beyond_the_largest_quotient(ops, dt, n, t):
+    """Finite values whose quotient by the tensor scale is beyond fp32's range saturate, as those beyond e4m3's do; only a
+    NaN or an infinity of x makes a block NaN."""
+    x = torch.zeros(n, 64, device="cuda")
+    x[:, :8] = torch.tensor([3e38, -3e38, 1e37, -1e30, 2e33, 1.0, -1e-30, 0.0], device="cuda")
+    x[:, 16:20] = torch.tensor([-3.3e38, 3.3e38, 0.0, 1e38], device="cuda")
+    x[:, 33] = math.inf
+    x[:, 50] = math.nan
+    x = x.to(dt)
+    q, s = ops.fp4_quantize(x, tensor_scale=t)
+    byte = s.view(U8)[0, :, :4]
+    assert torch.equal(byte, torch.tensor([0x7E, 0x7E, 0x7F, 0x7F], device="cuda", dtype=U8).expand(n, -1))
+    fine = x[:, :32].contiguous()
+    q, s = ops.fp4_quantize(fine, tensor_scale=t)
+    check_codes(q, s, fine, "nvfp4", t)
+    # silu(30) is 30 in fp32, and so the product with u is what is quantised
+    both = torch.cat([torch.full_like(fine, 30.0), fine / 32], 1)
+    q, s = ops.fp4_quantize(both, tensor_scale=t, swiglu=True)
+    check_codes(q, s, fine.float() / 32 * 30, "nvfp4", t)
