@@ -641,10 +641,10 @@ epoch_status epoch_fp4_quantize_weight(const void *w_dev, int32_t dtype, int32_t
                                        int32_t format, void *q_dev, void *scales_dev, float *tensor_scales_dev,
                                        epoch_stream stream);
 
-/* The values that codes stand for, times scale and, where it is given, group_scale_dev [n_mats]:
- * out_dev [n_mats * n] rows of k values of out_dtype, out_stride apart, from q_dev [n_mats][n][k / 2]
+/* The values q * s that codes stand for, times f = scale * group_scale[i] in fp32 (group_scale_dev
+ * [n_mats] NULL: f = scale): out_dev [n_mats * n] rows of k values of out_dtype, out_stride apart, from q_dev [n_mats][n][k / 2]
  * and scales_dev [n_mats][ceil(k / 256)][n][16 or 8] (rows as epoch_fp4_quantize gives them: n_mats 1).
- * Rounded once. EPOCH_EINVAL as above. */
+ * q * s * f is rounded to fp32, and from there to bf16. EPOCH_EINVAL as above. */
 epoch_status epoch_fp4_dequantize(const void *q_dev, const void *scales_dev, int32_t format, int32_t n_mats, int32_t n,
                                   int32_t k, float scale, const float *group_scale_dev, void *out_dev,
                                   int64_t out_stride, int32_t out_dtype, epoch_stream stream);

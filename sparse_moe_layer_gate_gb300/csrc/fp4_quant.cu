@@ -297,7 +297,8 @@ __global__ void k_fp4_tensor_scales(uint32_t *amax, int n, int nv) {
   if (i < n) reinterpret_cast<float *>(amax)[i] = nv ? fp4_tensor_scale(amax[i]) : 1.0f;
 }
 
-// In the order of k_fp4_quant.
+// In the order of k_fp4_quant. A code's value times its scale is exact in fp32 (mxfp4: an eighth of it, so that the largest
+// are finite), and only then multiplied by the factor: zeros stay zeros whatever the scale and factor.
 template <typename T, bool NV, int C>
 __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a, unsigned kb_n) {
   constexpr int kCodes = C / 8, kWords = C * static_cast<int>(sizeof(T)) / 4;
@@ -315,13 +316,17 @@ __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a
     q[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
     code = __ldg(a.scales + block * (NV ? 16 : 8) + (p.part >> (NV ? 1 : 2)));
   }
-  const float f = a.group_scale ? a.scale * __ldg(a.group_scale + mat) : a.scale;
+  float f = a.group_scale ? a.scale * __ldg(a.group_scale + mat) : a.scale;
   float s[2];
   if constexpr (NV) {
-    s[0] = open_e4m3(code) * f;
-    s[1] = open_e4m3(code >> 8) * f;
+    s[0] = open_e4m3(code);
+    s[1] = open_e4m3(code >> 8);
   } else {
-    s[0] = s[1] = (code == 0xFFu ? __uint_as_float(0x7FC00000u) : code ? __uint_as_float(code << 23) : 0x1p-127f) * f;
+    s[0] = s[1] = code == 0xFFu ? __uint_as_float(0x7FC00000u) : code ? __uint_as_float(code << 23) : 0x1p-127f;
+    if (fabsf(f) < 0x1p120f) {  // (beyond it a value of 2^128 has an infinite product either way)
+      f *= 8.f;
+      s[0] = s[1] *= 0.125f;
+    }
   }
   uint32_t o[kWords];
 #pragma unroll
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) k_fp4_dequant(const Fp4DequantArgs a
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&d[j]));
-      const float y0 = x.x * s[h / 2], y1 = x.y * s[h / 2];
+      const float y0 = x.x * s[h / 2] * f, y1 = x.y * s[h / 2] * f;
       if constexpr (sizeof(T) == 2) {
         const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
         o[4 * h + j] = *reinterpret_cast<const uint32_t *>(&t);

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_experts import BF16, E4M3, F32, I32, U8, _gen, _rnd, check_codes, check_route, ops, route64  # noqa: F401
+from test_experts import BF16, E4M3, F32, F64, FORMS, GRID, I32, U8, _gen, _rnd, check_codes, check_route, ops, route64  # noqa: F401
 
 
 # ------------------------------------------------------------------------------------------- router
@@ -119,3 +119,29 @@ def test_fp4_quantize_beyond_the_largest_quotient(ops, dt, n, t):
     both = torch.cat([torch.full_like(fine, 30.0), fine / 32], 1)
     q, s = ops.fp4_quantize(both, tensor_scale=t, swiglu=True)
     check_codes(q, s, fine.float() / 32 * 30, "nvfp4", t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n", [3, 3000])
+@pytest.mark.parametrize("ot", [F32, BF16])
+def test_fp4_dequantize_by_any_factor(ops, form, n, ot):
+    """Every code with every finite scale, times factors that are no powers of two and such as meet the ends of fp32's
+    range: the bits of the exact product (q * s has six bits and a factor 24, so 64 bits hold it) rounded to fp32 and from
+    there to the result; a zero stays zero."""
+    block, dtype = FORMS[form]
+    g = _gen(n)
+    top = 127 if form == "nvfp4" else 255
+    code = (torch.arange(256, device="cuda") + torch.arange(n, device="cuda")[:, None]) % 16
+    byte = torch.randint(0, top, (n, 256 // block), generator=g, device="cuda").to(U8)
+    byte[0, 0], byte[0, 1], byte[1, 0] = top - 1, 0, top - 2
+    q = (code[:, 0::2] | code[:, 1::2] << 4).to(U8)
+    s = byte.view(1, n, -1).view(dtype)
+    wide = byte.view(E4M3).double() if form == "nvfp4" else torch.exp2(byte.double() - 127)
+    v = torch.tensor(GRID + [-x for x in GRID], device="cuda", dtype=F64)[code] * wide.repeat_interleave(block, 1)
+    for f in (0.1, 1 / 3, -1.1, 0.875, 2.0, 8.0, 1e5, 1e30, 1e36, 3e38, 1e-5, 1e-30, 1e-40, 0.0):
+        f32 = torch.tensor([f], device="cuda")
+        want = (v * f32.double()).float().to(ot)
+        for factor in (f, f32):
+            got = ops.fp4_dequantize(q, s, tensor_scale=factor, out_dtype=ot)
+            assert got.dtype == ot and torch.equal(got, want) and torch.equal(torch.signbit(got), torch.signbit(want)), f
