@@ -4,8 +4,9 @@
 //   y[i, n] = s_e * sum_k a[i, k] * w[e, n, k],   offsets[e] <= i < offsets[e + 1]
 //
 // and, with swiglu, z[i, n] = silu(y[i, n]) * y[i, N / 2 + n]. Row i of a bf16 product may be row
-// rows[i] of x (a worklist's positions). Sums are the tensor cores' fp32 accumulators; the factors
-// s_e and the SwiGLU are applied to them in fp32 and the result is rounded once.
+// rows[i] of x (a worklist's positions). Sums are the tensor cores' fp32 accumulators of some blocks of K, added up in
+// fp32; the factors s_e and the SwiGLU are applied to them in fp32 (for bf16 results the SwiGLU with the fast exponential
+// and quotient, off by less than 2^-17 up to |y| = 80: a 500th of the rounding that follows) and the result is rounded once.
 //
 // Tiles of 128 rows x 256, 128, 64 or 32 columns, or of 256 x 256 by two CTAs whose tensor cores
 // read both halves of the weights. A producer warp streams 128-byte-wide operand tiles (64 bf16 or
@@ -53,7 +54,7 @@ struct ExpertParams {
   int align;         // bytes on which output rows start: 32, 16 or less
   int bulk;          // the output has a tensor map: its rows start and end on 16-byte boundaries
   int reuse;         // weights are read by several row tiles
-  int acc_kb;        // K blocks that an accumulator sums before it is added to the fp32 sums in registers
+  int acc_kb;        // K blocks (an even number) that an accumulator sums before it is added to the fp32 sums in registers
   uint32_t *err;
   int64_t timeout_ns;
   uint32_t hold;  // bytes that a stage waits for beyond its copies': 0, but for the test of waits that run out
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
     const bool swiglu = p.g.swiglu != 0, bf16 = p.g.out_bf16 != 0;
     const int c0 = swiglu ? half * Q : half * 2 * Q, c1 = swiglu ? BN / 2 + half * Q : c0 + Q;
     const size_t size = bf16 ? 2 : 4;
-    constexpr int kPiece = Q < 32 ? Q : 32;
+    constexpr int kPiece = FP4 ? 8 : Q < 32 ? Q : 32;  // (what registers are left beside the scales' code)
     uint32_t seq = 0, turn = 0;
     uint8_t *const places = ring_ptr + G::stages * G::stage + warp * 8192;
     bool ok = true;
@@ -667,38 +668,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_gemm(const __grid_consta
       }
       float v0[Q], v1[Q];
       const bool any = quarter * 32 < rows && n0 < p.out_n;  // this warp holds an element of the tile
-      for (int kb = 0; kb < p.kb_n; kb += p.acc_kb, ++seq) {
+      uint32_t src = 0;
+      auto begin = [&]() {  // the next accumulator is whole
         const uint32_t buf = seq % G::bufs;
         ok = __all_sync(0xffffffffu, wait_for(tfull + 8 * buf, (seq / G::bufs) & 1u, abort, p.err, p.timeout_ns));
-        if (!ok) break;
         tc_fence_after();
-        if (any) {
-          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-          if (FP4 != 0 || kb == 0) {
-            load_cols<Q>(src + c0, v0);
-            load_cols<Q>(src + c1, v1);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int j = 0; j < Q; j += kPiece) {
-              float w[kPiece];
-              load_cols<kPiece>(src + c0 + j, w);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < kPiece; ++i) v0[j + i] += w[i];
-              load_cols<kPiece>(src + c1 + j, w);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < kPiece; ++i) v1[j + i] += w[i];
-            }
-          }
-        }
+        src = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+      };
+      auto end = [&]() {  // and has been read
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (PAIR) arrive_cluster(read + 8 * buf);
-          else mbar_arrive(read + 8 * buf);
+          if constexpr (PAIR) arrive_cluster(read + 8 * (seq % G::bufs));
+          else mbar_arrive(read + 8 * (seq % G::bufs));
         }
+        ++seq;
+      };
+      begin();
+      if (!ok) break;
+      if (any) {
+        load_cols<Q>(src + c0, v0);
+        load_cols<Q>(src + c1, v1);
+        tmem_ld_wait();
+      }
+      end();
+      for (int kb = p.acc_kb; kb < p.kb_n; kb += p.acc_kb) {
+        begin();
+        if (!ok) break;
+        if (any) {
+#pragma unroll
+          for (int j = 0; j < Q; j += kPiece) {
+            float w[kPiece];
+            load_cols<kPiece>(src + c0 + j, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) v0[j + i] += w[i];
+            load_cols<kPiece>(src + c1 + j, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) v1[j + i] += w[i];
+          }
+        }
+        end();
       }
       if (!ok) break;
       if (!any) continue;
@@ -853,9 +864,13 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t 
   p.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
   const int64_t E = a.offsets ? a.n_groups : 1;
   p.reuse = a.m > kBm * E;
-  // The tensor core's sums drift by their truncation: over 1024 columns to 1e-6 of an fp32 result, four times what sums
-  // in fp32 are off by. So fp32 results of bf16 products add up accumulators of 256 columns.
-  p.acc_kb = fp4 || a.out_bf16 ? p.kb_n : 4;
+  // The tensor core's sums are truncated, by 0.8 of a step of fp32 a product on the average, and so drift where terms have
+  // one sign: over 65536 bf16 columns (4096 products) by 4e-4 of the result. So fp32 results add up accumulators of four
+  // blocks (16 products: 4e-7), with 4-bit operands of eight (32: 8e-7 at most, and 1e-7 where scales are alike, since the
+  // terms have few bits; 8192 x 4096 x 4096 nvfp4 64 us, in one accumulator 61, by four blocks 71). bf16 results add up
+  // accumulators of 64 blocks (256 products: 1.4e-5, less than a hundredth of half a step of bf16; four blocks would cost a
+  // prompt's bf16 product a tenth of its time).
+  p.acc_kb = a.out_bf16 ? 64 : fp4 ? 8 : 4;
   p.err = ops_error_word();
   p.timeout_ns = timeout_ns;
   p.hold = hold;

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_experts import BF16, E4M3, F32, F64, FORMS, GRID, I32, U8, _gen, _rnd, check_codes, check_route, ops, route64  # noqa: F401
+from test_experts import BF16, E4M3, F32, F64, FORMS, GRID, I32, U, U8, _gen, _half, _rnd, _within, check_codes, check_route, ops, route64  # noqa: F401
 
 
 # ------------------------------------------------------------------------------------------- router
@@ -145,3 +145,40 @@ def test_fp4_dequantize_by_any_factor(ops, form, n, ot):
         for factor in (f, f32):
             got = ops.fp4_dequantize(q, s, tensor_scale=factor, out_dtype=ot)
             assert got.dtype == ot and torch.equal(got, want) and torch.equal(torch.signbit(got), torch.signbit(want)), f
+
+
+# ---------------------------------------------------------------------------------- products of long K
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m", [16, 17, 300, 1100])
+def test_fp4_matmul_sums_of_many_columns(ops, form, m):
+    """fp32 results over K = 65536 columns of one sign, where sums that truncate drift: an accumulator of the tensor core
+    holds 32 products at most, each off by at most a step (two roundings) of what it holds, and K / 2048 of them are
+    summed in fp32. With few rows and with tiles alike."""
+    k, n = 65536, 512
+    g = _gen(m)
+    a, sa = ops.fp4_quantize(_rnd(g, m, k).abs(), form=form)
+    b, sb, t = ops.fp4_quantize_weight(_rnd(g, n, k).abs(), form=form)
+    y = ops.fp4_dequantize(a, sa, out_dtype=F32).double() @ ops.fp4_dequantize(b, sb, out_dtype=F32).double().T
+    got = ops.fp4_matmul(a, sa, b, sb, out_dtype=F32)
+    _within(got, y, y * (2 * 32 + k / 2048 + 4) * U)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(512, 256), (17, 5120), (3000, 512)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_bf16_results_of_many_columns_do_not_drift(ops, m, n, gather):
+    """bf16 results over K = 65536 columns of one sign: accumulators of 256 products at most, a step each, so that beside the
+    result's own rounding, which averages out, the sums stay within 512 roundings of fp32 and those of K / 4096 fp32 sums."""
+    k = 65536
+    g = _gen(m)
+    x, w = _rnd(g, m, k).abs().to(BF16), _rnd(g, n, k).abs().to(BF16)
+    rows = torch.arange(m, device="cuda", dtype=I32).flip(0).contiguous() if gather else None
+    y = x.double() @ w.double().T
+    y = y.flip(0) if gather else y
+    got = ops.grouped_matmul(x, w, None, rows=rows)
+    off = (got.double() - y) / y
+    drift = (512 + k / 4096 + 4) * U
+    assert float(off.abs().max()) <= _half(BF16) * (1 + 2 ** -7) + drift
+    # the mean of m n roundings, each spread over +-2^-8 at most: five standard deviations
+    assert abs(float(off.mean())) <= drift + 5 * _half(BF16) / math.sqrt(3 * m * n)
