@@ -256,16 +256,26 @@ __device__ __forceinline__ bool apart(float a, float b) { return fabsf(a - b) > 
 // not the sum's, which is small where the biases cancel.
 __device__ __forceinline__ float group_reach(float a, float b) { return 1.2e-6f + 2.5e-7f * (fabsf(a) + fabsf(b)); }
 
-// Logits up to here have a score of 0 in 64 bits too (exp(-g) overflows): their order is that of the ids, and the weights of
-// a position that selects no other are 0 / 0.
-constexpr float kNoScore = -709.7827f;
-
-// The largest of a position's selected logits.
-__device__ __noinline__ float most_selected(const void *row, bool bf16, const int16_t *id, int k) {
-  float most = -INFINITY;
-  for (int j = 0; j < k; ++j)
-    if (id[j] >= 0) most = fmaxf(most, logit(row, bf16, id[j]));
-  return most;
+// Weights where every selected sigmoid lies below exp(kLowLogit), which their sum then shows, over this thread's edges (of
+// rows from row0 on): quotients of the sigmoids over the largest (see sigmoid_over). Logits up to kNoScore have a score of 0 in
+// 64 bits too (exp(-g) overflows): their order is that of the ids, and the weights of a position that selects no other are
+// 0 / 0. Out of the loop over the edges, which a call in it would slow down (16384 positions, softmax: 20.1 us, 20.8 with it).
+constexpr float kLowSum = 4e-8f, kNoScore = -709.7827f;
+__device__ __noinline__ void low_weights(const RouteArgs &a, const uint8_t *rows, int64_t row_bytes, const int16_t *ids, const float2 *stat,
+                                         float *weights, int edges) {
+  const int k = a.top_k;
+  for (int i = threadIdx.x; i < edges; i += blockDim.x) {
+    const int r = i / k;
+    const int16_t *id = ids + r * k;
+    const uint8_t *row = rows + r * row_bytes;
+    if (ids[i] < 0) continue;
+    float most = -INFINITY, sum = stat[r].y;
+    for (int j = 0; j < k; ++j)
+      if (id[j] >= 0) most = fmaxf(most, logit(row, a.bf16 != 0, id[j]));
+    for (int j = 0; j < k; ++j)
+      if (id[j] >= 0) sum += sigmoid_over(logit(row, a.bf16 != 0, id[j]), most);
+    if (most < kLowLogit) weights[i] = most <= kNoScore ? __uint_as_float(0x7FC00000u) : sigmoid_over(logit(row, a.bf16 != 0, ids[i]), most) / sum;
+  }
 }
 
 // Ids of the entries that lanes have marked (bits of their EPL), in ascending order one a lane from scratch on; how many
@@ -623,15 +633,7 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       float x = 0.f;
       if (e >= 0) {
         atomicOr(&s_bits[r >> 5][e], 1u << (r & 31));
-        if (a.sigmoid) {
-          const uint8_t *row = logits + (t0 + r) * row_bytes;
-          const float g = logit(row, bf16, e);
-          // (where g is not low the largest is not either)
-          const float most = g < kLowLogit && !a.raw_weights ? most_selected(row, bf16, s_id + r * k, k) : 0.f;
-          x = most <= kNoScore ? 0.f : sigmoid_over(g, most);
-        } else {
-          x = expf(s_val[i] - s_stat[r].x);
-        }
+        x = a.sigmoid ? sigmoid_over(logit(logits + (t0 + r) * row_bytes, bf16, e), 0.f) : expf(s_val[i] - s_stat[r].x);
       }
       s_val[i] = x;
     }
@@ -648,6 +650,7 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       for (int64_t i = s_off[E] + tid; i < static_cast<int64_t>(a.n_tok) * k; i += threads) a.positions[i] = -1;
     }
     const int *base = one ? s_off : s_count;
+    bool low = false;
     for (int i = tid; i < edges; i += threads) {
       const int r = static_cast<int>(i * by_k >> 16), e = s_id[i];
       const int64_t at = t0 * k + i;
@@ -657,7 +660,8 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
         float sum = s_stat[r].y;
         if (!a.raw_weights)
           for (int j = 0; j < k; ++j) sum += s_val[r * k + j];
-        w = a.raw_weights && a.sigmoid ? s_val[i] + sum : s_val[i] / sum;
+        if (a.raw_weights && a.sigmoid) w = s_val[i] + sum;
+        else w = s_val[i] / sum, low = low || sum < kLowSum;  // (softmax's are 1 or more)
         place = base[e];
         for (int q = 0; q < (r >> 5); ++q) place += __popc(s_bits[q][e]);
         place += __popc(s_bits[r >> 5][e] & ((1u << (r & 31)) - 1u));
@@ -667,6 +671,7 @@ __global__ void __launch_bounds__(THREADS) k_router_select(const RouteArgs a, in
       a.weights[at] = w;
       a.slots[at] = place;
     }
+    if (low) low_weights(a, logits + t0 * row_bytes, row_bytes, s_id, s_stat, a.weights + t0 * k, edges);
     if (one) return;
     __syncthreads();
     for (int i = tid; i < E; i += threads) {
