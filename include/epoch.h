@@ -556,9 +556,11 @@ epoch_status epoch_test_fp8_timeout(const void *a_dev, const float *a_scales_dev
  *    the logits), equal ones by lower id; weights are a softmax over them, or with
  *    raw_weights their probabilities among all n_experts.
  *  EPOCH_ROUTER_SIGMOID_GROUP: the top_k largest sigmoid(logit) + bias (NULL: 0)
- *    under the group rule of epoch_layer_config, in exact arithmetic; weights are the
- *    selected sigmoids over their sum (NaN where every selected logit is below -709.78,
- *    whose 1 / (1 + exp(-logit)) is 0 in 64 bits too), or with raw_weights the sigmoids.
+ *    under the group rule of epoch_layer_config, by their order in 64 bits and equal ones by
+ *    lower id (1 / (1 + exp(-logit)) is 1 there from 37 on, and a large bias absorbs small
+ *    differences); weights are the selected sigmoids over their sum (NaN where every
+ *    selected logit is below -709.78, whose sigmoid is 0 in 64 bits), or with raw_weights
+ *    the sigmoids.
  *  live [n_tok] (NULL: all): a position with 0 is routed to no expert.
  *  eligible [n_experts] (NULL: all): an expert with 0 is never selected; nor is one
  *    whose logit is -inf. A NaN ranks below every number and makes all of its

@@ -5,8 +5,10 @@
 //
 // and, with swiglu, z[i, n] = silu(y[i, n]) * y[i, N / 2 + n]. Row i of a bf16 product may be row
 // rows[i] of x (a worklist's positions). Sums are the tensor cores' fp32 accumulators of some blocks of K, added up in
-// fp32; the factors s_e and the SwiGLU are applied to them in fp32 (for bf16 results the SwiGLU with the fast exponential
-// and quotient, off by less than 2^-17 up to |y| = 80: a 500th of the rounding that follows) and the result is rounded once.
+// fp32; the factors s_e and the SwiGLU are applied to them in fp32 and the result is rounded once. For bf16 results the
+// SwiGLU has the fast exponential and quotient: off by less than 2^-16 for gates down to -80, a 256th of the rounding that
+// follows, and 0 for gates below -87, where silu is less than 2^-119 (the precise ones make an epilogue longer than the
+// products of K = 512: 8192 rows over 8 experts of 4096 x 512 43 us, with these 30).
 //
 // Tiles of 128 rows x 256, 128, 64 or 32 columns, or of 256 x 256 by two CTAs whose tensor cores
 // read both halves of the weights. A producer warp streams 128-byte-wide operand tiles (64 bf16 or
@@ -23,8 +25,12 @@
 //
 // What bounds it: with few rows an expert the weights' bytes (256 rows over 256 experts of 1024 x 2048, bf16 with swiglu: 94 us,
 // 6.3 TB/s; 8192 rows, mxfp4: 53 us, 5.7 TB/s). With many, bf16: what an SM takes in from L2 for a tile of 128 rows, and the
-// power limit (65536 gathered rows over 64 experts of 2048 x 2048: 405 us, 1.36 PFLOP/s); 4-bit: the scales leave room for one
-// accumulator of 256 columns, so products wait while it is read (8192 x 4096 x 4096: 55 us, 5.0 PFLOP/s).
+// power limit (65536 gathered rows over 64 experts of 2048 x 2048: 405 us in a graph, 1.36 PFLOP/s; 450 called back to back);
+// 4-bit: the scales leave room for one
+// accumulator of 256 columns, so products wait while it is read (8192 x 4096 x 4096: 55 us, 5.0 PFLOP/s), and products are 64
+// deep, at four times the bf16 rate; the form 96 deep, at six times, is not used. Registers: a thread of the epilogue holds 128
+// sums of a tile of 256 columns, so there the compiler spills some (bytes stored: bf16 single 84 and pairs 292, nvfp4 96 and 52,
+// mxfp4 112 and 68).
 #include <cstring>
 #include <mutex>
 
