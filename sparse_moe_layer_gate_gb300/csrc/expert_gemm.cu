@@ -872,10 +872,10 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t s, int64_t 
   p.reuse = a.m > kBm * E;
   // The tensor core's sums are truncated, by 0.8 of a step of fp32 a product on the average, and so drift where terms have
   // one sign: over 65536 bf16 columns (4096 products) by 4e-4 of the result. So fp32 results add up accumulators of four
-  // blocks (16 products: 4e-7), with 4-bit operands of eight (32: 8e-7 at most, and 1e-7 where scales are alike, since the
-  // terms have few bits; 8192 x 4096 x 4096 nvfp4 64 us, in one accumulator 61, by four blocks 71). bf16 results add up
-  // accumulators of 64 blocks (256 products: 1.4e-5, less than a hundredth of half a step of bf16; four blocks would cost a
-  // prompt's bf16 product a tenth of its time).
+  // blocks (16 products: 4e-7, or 1.1e-6 where the terms range over many octaves), with 4-bit operands of eight (32: 1e-7 and
+  // 6.5e-7, since the terms have few bits; 8192 x 4096 x 4096 nvfp4 64 us, in one accumulator 61, by four blocks 71). bf16
+  // results add up accumulators of 64 blocks (256 products: 1.5e-5 and 2.4e-5, an 80th of half a step of bf16 at most; four
+  // blocks would cost a prompt's bf16 product a tenth of its time).
   p.acc_kb = a.out_bf16 ? 64 : fp4 ? 8 : 4;
   p.err = ops_error_word();
   p.timeout_ns = timeout_ns;
